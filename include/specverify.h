@@ -268,6 +268,119 @@ sv_status spec_verify_attn_tree(const void *q, sv_dtype q_dtype,
                                 int32_t *dev_status, sv_stream_t stream);
 
 /* ------------------------------------------------------------------------ *
+ * spec_verify_attn_window
+ *   spec_verify_attn through a sliding window with sinks (walkerchi "KV
+ *   Cache", section 3.6, StreamingLLM): the query at position p sees key
+ *   t <= p iff t > p - window or t < sinks, i.e. the window's last `window`
+ *   keys (its own among them) and the first `sinks` keys of the sequence.
+ *   Positions are absolute: keys are not renumbered. window = 0 means no
+ *   window (every key t <= p; sinks then has no effect). window, sinks >= 0.
+ *   Blocks that no query of the call sees are not read: their table entries
+ *   may be anything (-1 once the caller has released the page). Keys of a
+ *   block that is read but that no query sees do not reach the output
+ *   whatever their values. Other arguments, layouts and support as for
+ *   spec_verify_attn; the workspace is
+ *   spec_verify_attn_window_workspace_size(...) bytes.
+ * ------------------------------------------------------------------------ */
+size_t spec_verify_attn_window_workspace_size(int B, int n_new, int H_q, int H_kv, int d_head,
+                                              int max_blocks_per_seq, int block_size,
+                                              int window, int sinks);
+
+sv_status spec_verify_attn_window(const void *q, sv_dtype q_dtype,
+                                  const void *k_cache, const void *v_cache, sv_dtype kv_dtype,
+                                  const sv_kv_layout *layout,
+                                  const float *k_scale, const float *v_scale,
+                                  const int32_t *block_table, int max_blocks_per_seq,
+                                  const int32_t *seq_lens,
+                                  int B, int n_new, int H_q, int H_kv, int d_head, int block_size,
+                                  int num_blocks, float softmax_scale, int window, int sinks,
+                                  void *out, sv_dtype out_dtype,
+                                  void *workspace, size_t workspace_bytes,
+                                  int32_t *dev_status, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * 4-bit paged cache ("KV Cache + Speculative Decoding", section 4.5 and Q9:
+ * KV quantisation below 8 bits)
+ *
+ * Pools. K and V pools are bytes, [num_blocks][H_kv][record]: the record of
+ * one (block, kv head) holds the 4-bit codes of its block_size slots and then
+ * one (scale, minimum) pair of f16 per slot; sv_q4_record_bytes(d_head,
+ * block_size) = block_size * (d_head / 2 + 4) bytes. A value is
+ * code * scale + minimum, code in 0..15.
+ *   K record: slot-major, d_head / 2 code bytes a slot; byte i holds head dim
+ *     2i in its low and 2i + 1 in its high four bits. With d_head a multiple
+ *     of 128 the 16-byte chunk c of slot s is stored at chunk
+ *     c ^ ((s >> 1) & 3) of the slot.
+ *   V record: dim-major, block_size / 2 code bytes a head dim; byte i holds
+ *     slot 2i in its low and 2i + 1 in its high four bits.
+ * d_head: a multiple of 32, <= 256; block_size: a multiple of 8, <= 64
+ * (SV_ERR_UNSUPPORTED otherwise; the size query returns 0). Pools are 16-byte
+ * aligned. A non-NULL layout gives the strides between records in BYTES
+ * (block_stride, head_stride: multiples of 16, at least a record; slot_stride
+ * 0), e.g. a per-layer slice of a larger pool. sv_copy_blocks copies such
+ * pages like any others.
+ *
+ * kv_block_append_q4
+ *   kv_block_append into 4-bit pools. A row x (one token, one kv head, all of
+ *   d_head) is quantised in fp32 with IEEE rounding: m = f16(min x),
+ *   s = f16((max x - m) / 15), raised to 2^-24 if it rounds to zero; both are
+ *   kept within +-65504; code = (x - m) / s rounded to the nearest even
+ *   integer and kept within 0..15. NaN elements take no part in the minimum
+ *   and maximum and get code 0; a row of nothing but NaN becomes zeros.
+ *   k_new, v_new: [B][n_new][H_kv][d_head], SV_F32 or SV_BF16. Slots of a
+ *   block that the call does not write keep their codes and pairs. No two
+ *   sequences of a call may write the same block (copy-on-write is the
+ *   caller's job, as for kv_block_append).
+ *
+ * kv_block_gather_q4
+ *   Reads cached rows back: k_out[b][i][g][:], v_out[b][i][g][:] = the values
+ *   of position start[b] + i of sequence b, i < n_rows, as SV_BF16 (rounded
+ *   to nearest even) or SV_F32; positions outside [0, seq_lens[b]) give zero
+ *   rows. start: device int32 [B]. k_out, v_out: [B][n_rows][H_kv][d_head].
+ *   For chunked prefill over a quantised prefix, or to move a sequence to
+ *   another cache. A length outside [0, max_blocks_per_seq * block_size] or a
+ *   bad block sets SV_DEV_* and gives zero rows.
+ *
+ * spec_verify_attn_q4
+ *   spec_verify_attn over 4-bit pools, with the window and sinks of
+ *   spec_verify_attn_window (window = 0: every key). q, out: SV_BF16 or
+ *   SV_F32. bf16 queries with d_head 128, block_size 16 and
+ *   (H_q/H_kv) * n_new <= 128 run on the tensor cores (q must then be 16-byte
+ *   aligned, else SV_ERR_INVALID_ARG); every other supported shape runs on a
+ *   CUDA-core kernel with fp32 arithmetic. The workspace is
+ *   spec_verify_attn_q4_workspace_size(...) bytes, 256-byte aligned; its
+ *   contents need no initialisation.
+ * ------------------------------------------------------------------------ */
+size_t sv_q4_record_bytes(int d_head, int block_size);
+
+sv_status kv_block_append_q4(const void *k_new, const void *v_new, sv_dtype new_dtype,
+                             void *k_cache, void *v_cache, const sv_kv_layout *layout,
+                             const int32_t *block_table, int max_blocks_per_seq,
+                             const int32_t *seq_lens, int B, int n_new, int H_kv, int d_head,
+                             int block_size, int num_blocks, int32_t *dev_status,
+                             sv_stream_t stream);
+
+sv_status kv_block_gather_q4(const void *k_cache, const void *v_cache, const sv_kv_layout *layout,
+                             const int32_t *block_table, int max_blocks_per_seq,
+                             const int32_t *seq_lens, const int32_t *start, int B, int n_rows,
+                             int H_kv, int d_head, int block_size, int num_blocks,
+                             void *k_out, void *v_out, sv_dtype out_dtype,
+                             int32_t *dev_status, sv_stream_t stream);
+
+size_t spec_verify_attn_q4_workspace_size(int B, int n_new, int H_q, int H_kv, int d_head,
+                                          int max_blocks_per_seq, int block_size, int window,
+                                          int sinks);
+
+sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const void *k_cache,
+                              const void *v_cache, const sv_kv_layout *layout,
+                              const int32_t *block_table, int max_blocks_per_seq,
+                              const int32_t *seq_lens, int B, int n_new, int H_q, int H_kv,
+                              int d_head, int block_size, int num_blocks, float softmax_scale,
+                              int window, int sinks, void *out, sv_dtype out_dtype,
+                              void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                              sv_stream_t stream);
+
+/* ------------------------------------------------------------------------ *
  * spec_verify_sample
  *   p_i = softmax(target_logits[b][i][:] / T), i = 0..K (row K is p_{K+1}).
  *   q_i = softmax(draft[b][i][:] / T) (draft_is_probs == 0, draft logits of

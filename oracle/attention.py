@@ -71,18 +71,35 @@ def tree_visibility(parent, L):
     return vis
 
 
-def dense_attention(q, Kd, Vd, n_new, softmax_scale, parent=None):
+def window_visibility(n_new, L, window, sinks):
+    """[n_new, L] bool: key t visible to query j at p = L - n_new + j through a
+    sliding window with sinks (walkerchi "KV Cache", section 3.6): t <= p and
+    (t > p - window or t < sinks)."""
+    vis = np.zeros((n_new, L), dtype=bool)
+    for j in range(n_new):
+        p = L - n_new + j
+        for t in range(p + 1):
+            vis[j, t] = t > p - window or t < sinks
+    return vis
+
+
+def dense_attention(q, Kd, Vd, n_new, softmax_scale, parent=None, visible=None):
     """Textbook GQA attention of the n_new queries of one sequence.
 
     q: [n_new, H_q, d]; Kd, Vd: [L, H_kv, d] (fp64). Returns [n_new, H_q, d].
     parent: the draft tree's parent indices (None: the causal chain).
+    visible: a mask [n_new, L] in place of either. Keys that no query sees
+    are left out, whatever their values.
     """
     q = np.asarray(q, dtype=np.float64)
     L = Kd.shape[0]
     H_q, H_kv = q.shape[1], Kd.shape[1]
     G = H_q // H_kv
     out = np.empty_like(q)
-    if parent is None:
+    if visible is not None:
+        seen = visible.any(axis=0)
+        Kd, Vd, visible = Kd[seen], Vd[seen], visible[:, seen]
+    elif parent is None:
         visible = np.tril(np.ones((n_new, L), dtype=bool), k=L - n_new)
     else:
         visible = tree_visibility(parent, L)

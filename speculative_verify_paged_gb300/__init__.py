@@ -9,6 +9,11 @@ CPU fallback: if the library is missing or CUDA is unavailable, calls raise.
 Entry points (names follow the C ABI in include/specverify.h):
   kv_block_append     paged write of the K+1 new K/V rows
   spec_verify_attn    paged GQA verify attention over the K+1 queries
+  spec_verify_attn_window
+                      the same through a sliding window with sinks
+  alloc_q4_pools, kv_block_append_q4, kv_block_gather_q4, spec_verify_attn_q4
+                      a 4-bit paged cache: its pools, its append, its read-back
+                      and the verify attention over it (window and sinks too)
   spec_verify_sample  fused rejection sampling (accept / residual / bonus)
   verify_step         the three in stream order (one verify round of one layer)
   tree_verify_step    the same for a draft tree, with the commit of the accepted path
@@ -87,6 +92,20 @@ def load_library(path: str = LIB_PATH):
     lib.spec_verify_attn.argtypes = attn_args + [P]
     lib.spec_verify_attn_ex.restype = I
     lib.spec_verify_attn_ex.argtypes = attn_args + [I, P]
+    lib.spec_verify_attn_window_workspace_size.restype = Z
+    lib.spec_verify_attn_window_workspace_size.argtypes = [I] * 9
+    lib.spec_verify_attn_window.restype = I
+    lib.spec_verify_attn_window.argtypes = attn_args[:19] + [I, I] + attn_args[19:] + [P]
+    lib.sv_q4_record_bytes.restype = Z
+    lib.sv_q4_record_bytes.argtypes = [I, I]
+    lib.kv_block_append_q4.restype = I
+    lib.kv_block_append_q4.argtypes = [P, P, I, P, P, LP, P, I, P, I, I, I, I, I, I, P, P]
+    lib.kv_block_gather_q4.restype = I
+    lib.kv_block_gather_q4.argtypes = [P, P, LP, P, I, P, P, I, I, I, I, I, I, P, P, I, P, P]
+    lib.spec_verify_attn_q4_workspace_size.restype = Z
+    lib.spec_verify_attn_q4_workspace_size.argtypes = [I] * 9
+    lib.spec_verify_attn_q4.restype = I
+    lib.spec_verify_attn_q4.argtypes = [P, I, P, P, LP, P, I, P, I, I, I, I, I, I, I, F, I, I, P, I, P, Z, P, P]
     lib.spec_verify_attn_tree_workspace_size.restype = Z
     lib.spec_verify_attn_tree_workspace_size.argtypes = [I, I, I, I, I, I, I]
     lib.spec_verify_attn_tree.restype = I
@@ -313,6 +332,241 @@ def spec_verify_attn(q, k_cache, v_cache, block_table, seq_lens, softmax_scale=N
     return out
 
 
+# --------------------------------------- window, sinks and 4-bit pools ---
+
+def _on_current_device(what, first, *rest):
+    """Kernels run on the current stream of the current device."""
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError("%s: tensors on different devices (%s and %s)" % (what, first.device, t.device))
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError("%s: the tensors are on %s, the current device is cuda:%d"
+                         % (what, first.device, torch.cuda.current_device()))
+
+
+def _check_batch(what, B, block_table, seq_lens, **per_seq):
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("%s: block_table must be [%d, max_blocks_per_seq], got %s"
+                         % (what, B, tuple(block_table.shape)))
+    for name, t in dict(seq_lens=seq_lens, **per_seq).items():
+        if t.shape != (B,):
+            raise ValueError("%s: %s must be [%d], got %s" % (what, name, B, tuple(t.shape)))
+
+
+def _check_like(what, name, t, shape, dtype):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError("%s: %s must be %s %s, got %s %s"
+                         % (what, name, tuple(shape), dtype, tuple(t.shape), t.dtype))
+
+
+def _check_status(what, status):
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("%s: status must hold an int32" % what)
+
+
+def q4_record_bytes(d_head, block_size=16):
+    """Bytes of one (block, kv head) of a 4-bit pool: block_size * (d_head / 2 + 4)."""
+    n = int(load_library().sv_q4_record_bytes(int(d_head), int(block_size)))
+    if n == 0:
+        raise ValueError("4-bit pools take d_head a multiple of 32 up to 256 and block_size a multiple of 8 up "
+                         "to 64, got d_head %d, block_size %d" % (d_head, block_size))
+    return n
+
+
+def alloc_q4_pools(num_blocks, H_kv, d_head, block_size=16, device="cuda"):
+    """A zeroed pair (k_cache, v_cache) of 4-bit pools, uint8 [num_blocks, H_kv, record]."""
+    shape = (int(num_blocks), int(H_kv), q4_record_bytes(d_head, block_size))
+    return tuple(torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2))
+
+
+def _is_q4(k_cache):
+    """4-bit pools are uint8 [num_blocks, H_kv, record]; fp8 pools have four dimensions."""
+    return k_cache.dtype == torch.uint8 and k_cache.dim() == 3
+
+
+def _q4_pools(what, k_cache, v_cache, d, block_size, layout, num_blocks, H_kv):
+    """(num_blocks, H_kv) of a pair of 4-bit pools, after checking that the
+    records the call reads lie within them."""
+    rec = q4_record_bytes(d, block_size)
+    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8:
+        raise ValueError("%s: 4-bit pools are uint8" % what)
+    if layout is None:
+        if k_cache.dim() != 3 or k_cache.shape != v_cache.shape or k_cache.shape[2] != rec:
+            raise ValueError("%s: 4-bit pools must be [num_blocks, H_kv, %d] (d_head %d, block_size %d), got %s and %s"
+                             % (what, rec, d, block_size, tuple(k_cache.shape), tuple(v_cache.shape)))
+        if H_kv is not None and k_cache.shape[1] != H_kv:
+            raise ValueError("%s: the pools hold %d kv heads, the new rows %d" % (what, k_cache.shape[1], H_kv))
+        return k_cache.shape[0], k_cache.shape[1]
+    if num_blocks is None or H_kv is None:
+        raise ValueError("with an explicit layout pass num_blocks and H_kv")
+    end = (num_blocks - 1) * layout[0] + (H_kv - 1) * layout[1] + rec
+    if end > k_cache.numel() or end > v_cache.numel():
+        raise ValueError("%s: the layout reaches byte %d of pools of %d and %d bytes"
+                         % (what, end, k_cache.numel(), v_cache.numel()))
+    return num_blocks, H_kv
+
+
+def kv_block_append_q4(k_new, v_new, k_cache, v_cache, block_table, seq_lens, block_size=16, layout=None,
+                       num_blocks=None, status=None):
+    """Quantise k_new/v_new [B, n_new, H_kv, d] (f32 or bf16) into the 4-bit pools at positions
+    seq_lens - n_new .. seq_lens - 1. Pools uint8 [num_blocks, H_kv, q4_record_bytes(d, bs)], or, with
+    `layout` = (block, head, 0) record strides in bytes, flat views plus num_blocks."""
+    what = "kv_block_append_q4"
+    _int32(block_table=block_table, seq_lens=seq_lens)
+    if k_new.dim() != 4 or k_new.shape != v_new.shape or k_new.dtype != v_new.dtype:
+        raise ValueError("%s: k_new and v_new must both be [B, n_new, H_kv, d] of one dtype" % what)
+    B, n_new, H_kv, d = k_new.shape
+    nb, _ = _q4_pools(what, k_cache, v_cache, d, block_size, layout, num_blocks, H_kv)
+    _check_batch(what, B, block_table, seq_lens)
+    _check_status(what, status)
+    _cuda(k_new, v_new, k_cache, v_cache, block_table, seq_lens, status)
+    _on_current_device(what, k_new, v_new, k_cache, v_cache, block_table, seq_lens, status)
+    _check(load_library().kv_block_append_q4(_ptr(k_new), _ptr(v_new), _dtype_code(k_new), _ptr(k_cache),
+                                             _ptr(v_cache), _layout_arg(layout), _ptr(block_table),
+                                             block_table.shape[1], _ptr(seq_lens), B, n_new, H_kv, d, block_size,
+                                             nb, _ptr(status), _stream()))
+
+
+def kv_block_gather_q4(k_cache, v_cache, block_table, seq_lens, start, n_rows, d_head, block_size=16, layout=None,
+                       num_blocks=None, H_kv=None, k_out=None, v_out=None, out_dtype=torch.bfloat16, status=None):
+    """Read cached rows of 4-bit pools back: (k, v), each [B, n_rows, H_kv, d_head], row i of sequence b the
+    values of position start[b] + i (zeros outside [0, seq_lens[b])). start: int32 [B]."""
+    what = "kv_block_gather_q4"
+    _int32(block_table=block_table, seq_lens=seq_lens, start=start)
+    nb, H = _q4_pools(what, k_cache, v_cache, d_head, block_size, layout, num_blocks, H_kv)
+    B = start.shape[0] if start.dim() == 1 else -1
+    _check_batch(what, B, block_table, seq_lens, start=start)
+    if n_rows < 0:
+        raise ValueError("%s: n_rows must be >= 0" % what)
+    shape = (B, int(n_rows), H, int(d_head))
+    if k_out is not None:
+        out_dtype = k_out.dtype
+    _check_like(what, "k_out", k_out, shape, out_dtype)
+    _check_like(what, "v_out", v_out, shape, out_dtype)
+    _check_status(what, status)
+    _cuda(k_cache, v_cache, block_table, seq_lens, start, k_out, v_out, status)
+    _on_current_device(what, k_cache, v_cache, block_table, seq_lens, start, k_out, v_out, status)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
+    if k_out.numel():
+        _check(load_library().kv_block_gather_q4(_ptr(k_cache), _ptr(v_cache), _layout_arg(layout), _ptr(block_table),
+                                                 block_table.shape[1], _ptr(seq_lens), _ptr(start), B, int(n_rows), H,
+                                                 int(d_head), block_size, nb, _ptr(k_out), _ptr(v_out),
+                                                 _dtype_code(k_out), _ptr(status), _stream()))
+    return k_out, v_out
+
+
+def attn_window_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size=16, window=0, sinks=0):
+    return load_library().spec_verify_attn_window_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq,
+                                                                 block_size, int(window), int(sinks))
+
+
+def attn_q4_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size=16, window=0, sinks=0):
+    return load_library().spec_verify_attn_q4_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq,
+                                                             block_size, int(window), int(sinks))
+
+
+def _attn_outputs(what, q, block_table, seq_lens, out, workspace, status):
+    if q.dim() != 4:
+        raise ValueError("%s: q must be [B, n_new, H_q, d]" % what)
+    _check_batch(what, q.shape[0], block_table, seq_lens)
+    _check_like(what, "out", out, q.shape, q.dtype)
+    _check_status(what, status)
+
+
+def spec_verify_attn_window(q, k_cache, v_cache, block_table, seq_lens, window, sinks=0, softmax_scale=None,
+                            k_scale=None, v_scale=None, block_size=16, out=None, workspace=None, status=None,
+                            layout=None, num_blocks=None, H_kv=None):
+    """Paged GQA verify attention through a sliding window: the query at position p sees key t <= p iff
+    t > p - window or t < sinks (window = 0: every key). Pools and layout as for spec_verify_attn."""
+    what = "spec_verify_attn_window"
+    _int32(block_table=block_table, seq_lens=seq_lens)
+    _attn_outputs(what, q, block_table, seq_lens, out, workspace, status)
+    B, n_new, H_q, d = q.shape
+    if layout is None:
+        if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or tuple(k_cache.shape[2:]) != (block_size, d):
+            raise ValueError("%s: pools must be [num_blocks, H_kv, %d, %d], got %s and %s"
+                             % (what, block_size, d, tuple(k_cache.shape), tuple(v_cache.shape)))
+        num_blocks, H_kv = k_cache.shape[0], k_cache.shape[1]
+    elif H_kv is None or num_blocks is None:
+        raise ValueError("with an explicit layout pass num_blocks and H_kv")
+    if k_cache.dtype != v_cache.dtype:
+        raise ValueError("%s: k_cache and v_cache must have one dtype" % what)
+    if _dtype_code(k_cache) == SV_FP8_E4M3:
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is None or t.dtype != torch.float32 or t.numel() < H_kv:
+                raise ValueError("%s: fp8 pools need %s, float32 [H_kv]" % (what, name))
+    _cuda(q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out, workspace, status)
+    _on_current_device(what, q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out, workspace, status)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    max_blocks = block_table.shape[1]
+    if workspace is None:
+        workspace = alloc_workspace(attn_window_workspace_size(B, n_new, H_q, H_kv, d, max_blocks, block_size,
+                                                               max(window, 0), max(sinks, 0)), q.device)
+    _check(load_library().spec_verify_attn_window(
+        _ptr(q), _dtype_code(q), _ptr(k_cache), _ptr(v_cache), _dtype_code(k_cache), _layout_arg(layout),
+        _ptr(k_scale), _ptr(v_scale), _ptr(block_table), max_blocks, _ptr(seq_lens), B, n_new, H_q, H_kv, d,
+        block_size, num_blocks, float(softmax_scale), int(window), int(sinks), _ptr(out), _dtype_code(out),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status), _stream()))
+    return out
+
+
+def spec_verify_attn_q4(q, k_cache, v_cache, block_table, seq_lens, softmax_scale=None, window=0, sinks=0,
+                        block_size=16, out=None, workspace=None, status=None, layout=None, num_blocks=None,
+                        H_kv=None):
+    """Paged GQA verify attention over 4-bit pools (kv_block_append_q4), q [B, n_new, H_q, d] bf16 or f32; with
+    window > 0 the query at position p sees key t <= p iff t > p - window or t < sinks."""
+    what = "spec_verify_attn_q4"
+    _int32(block_table=block_table, seq_lens=seq_lens)
+    _attn_outputs(what, q, block_table, seq_lens, out, workspace, status)
+    B, n_new, H_q, d = q.shape
+    nb, H = _q4_pools(what, k_cache, v_cache, d, block_size, layout, num_blocks, H_kv)
+    _cuda(q, k_cache, v_cache, block_table, seq_lens, out, workspace, status)
+    _on_current_device(what, q, k_cache, v_cache, block_table, seq_lens, out, workspace, status)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    max_blocks = block_table.shape[1]
+    if workspace is None:
+        workspace = alloc_workspace(attn_q4_workspace_size(B, n_new, H_q, H, d, max_blocks, block_size,
+                                                           max(window, 0), max(sinks, 0)), q.device)
+    _check(load_library().spec_verify_attn_q4(
+        _ptr(q), _dtype_code(q), _ptr(k_cache), _ptr(v_cache), _layout_arg(layout), _ptr(block_table), max_blocks,
+        _ptr(seq_lens), B, n_new, H_q, H, d, block_size, nb, float(softmax_scale), int(window), int(sinks),
+        _ptr(out), _dtype_code(out), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+        _stream()))
+    return out
+
+
+def _append_any(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, block_size, status):
+    """The append that the pools call for."""
+    if _is_q4(k_cache):
+        kv_block_append_q4(k_new, v_new, k_cache, v_cache, block_table, seq_lens, block_size=block_size, status=status)
+    else:
+        kv_block_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale,
+                        block_size=block_size, status=status)
+
+
+def _attn_any(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, k_scale, v_scale, window, sinks, block_size,
+              out, workspace, status):
+    """The verify attention that the pools and the window call for."""
+    if _is_q4(k_cache):
+        return spec_verify_attn_q4(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, window, sinks,
+                                   block_size=block_size, out=out, workspace=workspace, status=status)
+    if window:
+        return spec_verify_attn_window(q, k_cache, v_cache, block_table, seq_lens, window, sinks, softmax_scale,
+                                       k_scale, v_scale, block_size=block_size, out=out, workspace=workspace,
+                                       status=status)
+    return spec_verify_attn(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, k_scale, v_scale,
+                            block_size=block_size, out=out, workspace=workspace, status=status)
+
+
 # ------------------------------------------------------------------ MLA ---
 
 def kv_block_append_latent(c_new, cache, block_table, seq_lens, block_size=16, status=None):
@@ -491,16 +745,18 @@ def spec_verify_sample_tree(target_logits, draft, tree_parent, tree_tokens, unif
 def verify_step(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, target_logits, draft,
                 draft_tokens, uniforms, k_scale=None, v_scale=None, draft_is_probs=False,
                 temperature=1.0, softmax_scale=None, attn_out=None, attn_workspace=None,
-                sample_workspace=None, status=None):
+                sample_workspace=None, status=None, window=0, sinks=0):
     """One verify round of one layer: append the K+1 new K/V rows, attend, sample.
+
+    The pools may be 4-bit ones (alloc_q4_pools); window > 0 attends through a
+    sliding window with sinks (spec_verify_attn_window).
 
     Returns (attn_out, out_tokens, num_accepted). Rolling the cache back is the
     caller's job: next round's length is seq_lens - (K+1) + num_accepted + 1.
     """
-    kv_block_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale,
-                    status=status)
-    out = spec_verify_attn(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, k_scale,
-                           v_scale, out=attn_out, workspace=attn_workspace, status=status)
+    _append_any(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, 16, status)
+    out = _attn_any(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, k_scale, v_scale, window, sinks, 16,
+                    attn_out, attn_workspace, status)
     toks, nacc, _, _ = spec_verify_sample(target_logits, draft, draft_tokens, uniforms,
                                           draft_is_probs, temperature, workspace=sample_workspace,
                                           status=status, want_probs=False)
@@ -663,6 +919,8 @@ class MultiLayerVerify:
     layers: list of dicts with device tensors q, k_new, v_new, k_cache, v_cache
     (and optionally k_scale, v_scale), all layers sharing block_table and
     seq_lens (one page table for the whole model, one pool pair per layer).
+    A layer's pools may be 4-bit ones (alloc_q4_pools), and a layer with
+    "window" (and "sinks") attends through a sliding window.
     Inputs and outputs stay in these static buffers, so the round can be
     captured once as a CUDA graph (capture()) and replayed (replay()); run()
     launches it directly. Attention outputs: self.outs[layer]; sampling:
@@ -681,8 +939,13 @@ class MultiLayerVerify:
         H_kv = layers[0]["k_cache"].shape[1]
         dev = q0.device
         self.outs = [torch.empty_like(l["q"]) for l in layers]
-        self.attn_ws = alloc_workspace(attn_workspace_size(B, n_new, H_q, H_kv, d, block_table.shape[1],
-                                                           block_size), dev)
+        shape = (B, n_new, H_q, H_kv, d, block_table.shape[1], block_size)
+        need = 0
+        for l in layers:
+            span = (l.get("window", 0), l.get("sinks", 0))
+            need = max(need, attn_q4_workspace_size(*shape, *span) if _is_q4(l["k_cache"])
+                       else attn_window_workspace_size(*shape, *span) if span[0] else attn_workspace_size(*shape))
+        self.attn_ws = alloc_workspace(need, dev)
         Bs, K1, V = target_logits.shape
         self.samp_ws = alloc_workspace(sample_workspace_size(Bs, K1 - 1, V), dev)
         self.out_tokens = torch.empty((Bs, K1), dtype=torch.int32, device=dev)
@@ -692,11 +955,11 @@ class MultiLayerVerify:
 
     def run(self):
         for l, out in zip(self.layers, self.outs):
-            kv_block_append(l["k_new"], l["v_new"], l["k_cache"], l["v_cache"], self.block_table, self.seq_lens,
-                            l.get("k_scale"), l.get("v_scale"), block_size=self.block_size, status=self.status)
-            spec_verify_attn(l["q"], l["k_cache"], l["v_cache"], self.block_table, self.seq_lens, None,
-                             l.get("k_scale"), l.get("v_scale"), block_size=self.block_size, out=out,
-                             workspace=self.attn_ws, status=self.status)
+            _append_any(l["k_new"], l["v_new"], l["k_cache"], l["v_cache"], self.block_table, self.seq_lens,
+                        l.get("k_scale"), l.get("v_scale"), self.block_size, self.status)
+            _attn_any(l["q"], l["k_cache"], l["v_cache"], self.block_table, self.seq_lens, None, l.get("k_scale"),
+                      l.get("v_scale"), l.get("window", 0), l.get("sinks", 0), self.block_size, out, self.attn_ws,
+                      self.status)
         spec_verify_sample(self.target_logits, self.draft, self.draft_tokens, self.uniforms, self.draft_is_probs,
                            self.temperature, out_tokens=self.out_tokens, num_accepted=self.num_accepted,
                            workspace=self.samp_ws, status=self.status, want_probs=False)

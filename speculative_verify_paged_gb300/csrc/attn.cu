@@ -39,7 +39,7 @@
 #include <mutex>
 #include <type_traits>
 
-#include "sv_common.cuh"
+#include "q4.cuh"
 
 namespace sv {
 namespace {
@@ -1684,9 +1684,13 @@ struct GenParams {
   const uint64_t *anc;    // [B][n_new] ancestor masks of a draft tree (NULL: a chain)
   int32_t *status;
   int B, n_new, H_q, H_kv, G, R, d, bs, max_blocks, num_blocks, bps, S;
-  int64_t block_stride, head_stride, slot_stride;
+  int64_t block_stride, head_stride, slot_stride;   // elements; 4-bit pools: bytes of the records
   float scale_log2;
+  int window, sinks;      // window 0: every key
 };
+
+// A 4-bit pool's element type (q4.cuh) in the kernels below.
+struct Q4 {};
 
 template <typename T>
 __device__ __forceinline__ float kv_value(const void *pool, int64_t off, float scale);
@@ -1722,12 +1726,14 @@ __global__ void __launch_bounds__(kGenThreads) attn_generic_kernel(const __grid_
   float *l_s = m_s + R;                   // [R]
   float *c_s = l_s + R;                   // [R]
 
-  const int L = P.seq_lens[b];
-  if (L < P.n_new || L > P.max_blocks * P.bs) {
+  const int L_seq = P.seq_lens[b];
+  if (L_seq < P.n_new || L_seq > P.max_blocks * P.bs) {
     if (tid == 0 && g == 0 && s == 0) atomic_or_status(P.status, SV_DEV_BAD_SEQ_LEN);
     return;
   }
-  const int nblk = (L + P.bs - 1) / P.bs;
+  // from here on keys are counted in the span the call reads (key_span)
+  const KeySpan span = key_span(L_seq, P.n_new, P.window, P.sinks, P.bs);
+  const int L = span.L, nblk = span.nblk;
   const int blk0 = s * P.bps;
   if (blk0 >= nblk) return;
   const int t_begin = blk0 * P.bs, t_end = min(L, min(nblk, blk0 + P.bps) * P.bs);
@@ -1750,10 +1756,23 @@ __global__ void __launch_bounds__(kGenThreads) attn_generic_kernel(const __grid_
       const int kk = idx / d, c = idx % d;
       const int t = t0 + kk;
       float kv = 0.f, vv = 0.f;
-      if (t < t_end) {
-        int phys = table[t / P.bs];
+      // (a key that no query's window reaches counts as zeros, whatever is there)
+      if (t < t_end && (P.window <= 0 || t < P.sinks || t > L - P.n_new - P.window)) {
+        const int blk = t / P.bs;
+        const int phys = table[blk < span.nsb ? blk : blk + span.skip];
         if (phys < 0 || phys >= P.num_blocks) {
           atomic_or_status(P.status, SV_DEV_BAD_BLOCK);
+        } else if constexpr (std::is_same<TKV, Q4>::value) {
+          const int slot = t % P.bs;
+          const int64_t off = (int64_t)phys * P.block_stride + (int64_t)g * P.head_stride;
+          const uint8_t *kr = static_cast<const uint8_t *>(P.k_cache) + off;
+          const uint8_t *vr = static_cast<const uint8_t *>(P.v_cache) + off;
+          const __half *kp = reinterpret_cast<const __half *>(kr + q4_code_bytes(d, P.bs)) + 2 * slot;
+          const __half *vp = reinterpret_cast<const __half *>(vr + q4_code_bytes(d, P.bs)) + 2 * slot;
+          const int kc = (kr[q4_k_byte(slot, c, d)] >> (4 * (c & 1))) & 15;
+          const int vc = (vr[q4_v_byte(slot, c, P.bs)] >> (4 * (slot & 1))) & 15;
+          kv = fmaf((float)kc, __half2float(kp[0]), __half2float(kp[1]));
+          vv = fmaf((float)vc, __half2float(vp[0]), __half2float(vp[1]));
         } else {
           const int64_t off = (int64_t)phys * P.block_stride + (int64_t)g * P.head_stride +
                               (int64_t)(t % P.bs) * P.slot_stride + c;
@@ -1771,7 +1790,8 @@ __global__ void __launch_bounds__(kGenThreads) attn_generic_kernel(const __grid_
       const int rel = t - (L - P.n_new);
       const bool in_tree = !P.anc || rel < 0 || ((P.anc[(int64_t)b * P.n_new + r / P.G] >> (rel & 63)) & 1ull);
       float sc = -INFINITY;
-      if (t < t_end && t <= lim && in_tree) {
+      const bool in_window = P.window <= 0 || t < P.sinks || t > lim - P.window;
+      if (t < t_end && t <= lim && in_tree && in_window) {
         float acc = 0.f;
         for (int c = 0; c < d; ++c) acc = fmaf(q_s[r * d + c], k_s[lane * d + c], acc);
         sc = acc * P.scale_log2;
@@ -1805,7 +1825,7 @@ __global__ void __launch_bounds__(kGenThreads) attn_generic_kernel(const __grid_
       const int r = idx / d, cc = idx % d;
       const int j = r / P.G, hh = r % P.G;
       const int64_t off = (((int64_t)b * P.n_new + j) * P.H_q + (int64_t)g * P.G + hh) * d + cc;
-      const float v = l_s[r] > 0.f ? o_s[idx] / l_s[r] : 0.f;
+      const float v = l_s[r] > 0.f ? o_s[idx] / l_s[r] : o_s[idx] * 0.f;   // (a NaN stays one, as in the merge)
       if (std::is_same<TQ, float>::value) static_cast<float *>(P.out)[off] = v;
       else static_cast<__nv_bfloat16 *>(P.out)[off] = __float2bfloat16_rn(v);
     }
@@ -1829,6 +1849,7 @@ struct MergeParams {
   void *out;
   int B, n_new, H_q, H_kv, G, R, d, bs, max_blocks, bps, S, per_split;
   int C;                    // balanced mode: CTAs of the tcgen05 kernel (0: split mode)
+  int window, sinks;        // the span the splits cover (key_span; window 0: every key)
 };
 
 // Split merge: WPR warps per output row (sequence, kv head, packed query row),
@@ -1858,7 +1879,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
     b = (int)(bg / P.H_kv);
     const int L = P.seq_lens[b];
     if (L >= P.n_new && L <= P.max_blocks * P.bs) {
-      const int nblk = (L + P.bs - 1) / P.bs;
+      const int nblk = key_span(L, P.n_new, P.window, P.sinks, P.bs).nblk;
       nsplit = (nblk + P.bps - 1) / P.bps;
     }
   }
@@ -1973,7 +1994,7 @@ __global__ void __launch_bounds__(1024) attn_merge_pair_kernel(const __grid_cons
   const int g = (int)(bg % P.H_kv), b = (int)(bg / P.H_kv);
   const int L = P.seq_lens[b];
   if (L < P.n_new || L > P.max_blocks * P.bs) return;
-  const int nsplit = ((L + P.bs - 1) / P.bs + P.bps - 1) / P.bps;
+  const int nsplit = (key_span(L, P.n_new, P.window, P.sinks, P.bs).nblk + P.bps - 1) / P.bps;
   if (nsplit <= 1) return;
   const int R = P.R, nc = P.d >> 2;
   for (int r = warp; r < R; r += (int)(blockDim.x >> 5)) {
@@ -2381,7 +2402,7 @@ static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache,
                            const int32_t *seq_lens, int B, int n_new, int H_q, int H_kv, int d_head,
                            int block_size, int num_blocks, float softmax_scale, void *out, sv_dtype out_dtype,
                            void *workspace, size_t workspace_bytes, int32_t *dev_status, int bps_req,
-                           const int32_t *tree_parent, sv_stream_t stream) {
+                           const int32_t *tree_parent, int window, int sinks, sv_stream_t stream) {
   if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out)
     return fail(SV_ERR_INVALID_ARG, "spec_verify_attn: null pointer argument");
   if (tree_parent && n_new > 64)
@@ -2393,6 +2414,8 @@ static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache,
   if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
     return fail(SV_ERR_INVALID_ARG, "spec_verify_attn: softmax_scale must be finite and > 0");
   if (q_dtype != out_dtype) return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: q and out dtypes must match");
+  if (kv_dtype == kQ4 && q_dtype != SV_F32 && q_dtype != SV_BF16)
+    return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn_q4: queries must be f32 or bf16");
   if (kv_dtype == SV_F32 && q_dtype != SV_F32)
     return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: fp32 caches take fp32 queries");
   if ((kv_dtype == SV_BF16 || kv_dtype == SV_FP8_E4M3) && q_dtype != SV_BF16)
@@ -2402,10 +2425,13 @@ static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache,
     return fail(SV_ERR_INVALID_ARG, "spec_verify_attn: fp8 caches need k_scale and v_scale");
   if (d_head > 256 || d_head % 4) return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: d_head must be a multiple of 4 and <= 256");
   if (B > 65535 || H_kv > 65535) return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: B or H_kv too large");
-  if (layout && (layout->slot_stride < d_head || layout->head_stride < d_head || layout->block_stride < d_head))
+  if (kv_dtype != kQ4 && layout && (layout->slot_stride < d_head || layout->head_stride < d_head || layout->block_stride < d_head))
     return fail(SV_ERR_INVALID_ARG, "spec_verify_attn: layout strides smaller than d_head");
-  const Plan plan = make_plan(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size, kv_dtype, q_dtype,
-                              layout, bps_req);
+  if (window < 0 || sinks < 0) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_window: negative window or sinks");
+  if ((int64_t)window >= (int64_t)max_blocks_per_seq * block_size) window = sinks = 0;   // reaches every key
+  const int span_blocks = span_blocks_max(max_blocks_per_seq, n_new, window, sinks, block_size);
+  Plan plan = make_plan(B, n_new, H_q, H_kv, d_head, span_blocks, block_size, kv_dtype, q_dtype, layout, bps_req);
+  if (window > 0 && plan.tc) plan = make_plan(B, n_new, H_q, H_kv, d_head, span_blocks, block_size, SV_F32, SV_F32, layout, bps_req);
   if (plan.R > 65535) return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: too many query rows per kv head");
   const size_t base_need = ws_bytes(plan, B, H_kv);
   const size_t need = base_need + (tree_parent ? align_up((size_t)B * n_new * sizeof(uint64_t), 256) : 0);
@@ -2425,6 +2451,11 @@ static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache,
     slot_stride = layout->slot_stride;
     head_stride = layout->head_stride;
     block_stride = layout->block_stride;
+  }
+  if (kv_dtype == kQ4) {
+    const sv_status qrc = q4_check("spec_verify_attn_q4", k_cache, v_cache, layout, H_kv, d_head, block_size,
+                                   &block_stride, &head_stride);
+    if (qrc != SV_OK) return qrc;
   }
   const float scale_log2 = (float)((double)softmax_scale * 1.4426950408889634074);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -2498,7 +2529,9 @@ static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache,
     P.max_blocks = max_blocks_per_seq; P.num_blocks = num_blocks; P.bps = plan.bps; P.S = plan.S;
     P.block_stride = block_stride; P.head_stride = head_stride; P.slot_stride = slot_stride;
     P.scale_log2 = scale_log2;
-    if (kv_dtype == SV_F32) rc = launch_gen<float, float>(P, st);
+    P.window = window; P.sinks = sinks;
+    if (kv_dtype == kQ4) rc = q_dtype == SV_F32 ? launch_gen<Q4, float>(P, st) : launch_gen<Q4, __nv_bfloat16>(P, st);
+    else if (kv_dtype == SV_F32) rc = launch_gen<float, float>(P, st);
     else if (kv_dtype == SV_BF16) rc = launch_gen<__nv_bfloat16, __nv_bfloat16>(P, st);
     else rc = launch_gen<uint8_t, __nv_bfloat16>(P, st);
   }
@@ -2518,6 +2551,7 @@ static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache,
   M.ws_acc = ws_acc; M.ws_ml = ws_ml; M.seq_lens = seq_lens; M.out = out;
   M.B = B; M.n_new = n_new; M.H_q = H_q; M.H_kv = H_kv; M.G = G; M.R = plan.R; M.d = d_head; M.bs = block_size;
   M.max_blocks = max_blocks_per_seq; M.bps = plan.bps; M.S = plan.S; M.per_split = plan.per_split;
+  M.window = window; M.sinks = sinks;
   const int64_t rows = (int64_t)B * H_kv * plan.R;
   if (out_dtype == SV_F32) launch_merge<float>(M, rows, st);
   else launch_merge<__nv_bfloat16>(M, rows, st);
@@ -2563,7 +2597,7 @@ extern "C" sv_status spec_verify_attn(const void *q, sv_dtype q_dtype, const voi
                                       int32_t *dev_status, sv_stream_t stream) {
   return attn_impl(q, q_dtype, k_cache, v_cache, kv_dtype, layout, k_scale, v_scale, block_table,
                    max_blocks_per_seq, seq_lens, B, n_new, H_q, H_kv, d_head, block_size, num_blocks,
-                   softmax_scale, out, out_dtype, workspace, workspace_bytes, dev_status, 0, nullptr, stream);
+                   softmax_scale, out, out_dtype, workspace, workspace_bytes, dev_status, 0, nullptr, 0, 0, stream);
 }
 
 extern "C" sv_status spec_verify_attn_ex(const void *q, sv_dtype q_dtype, const void *k_cache,
@@ -2578,7 +2612,7 @@ extern "C" sv_status spec_verify_attn_ex(const void *q, sv_dtype q_dtype, const 
   return attn_impl(q, q_dtype, k_cache, v_cache, kv_dtype, layout, k_scale, v_scale, block_table,
                    max_blocks_per_seq, seq_lens, B, n_new, H_q, H_kv, d_head, block_size, num_blocks,
                    softmax_scale, out, out_dtype, workspace, workspace_bytes, dev_status,
-                   blocks_per_split == 0 ? -1 : blocks_per_split, nullptr, stream);
+                   blocks_per_split == 0 ? -1 : blocks_per_split, nullptr, 0, 0, stream);
 }
 
 extern "C" size_t spec_verify_attn_tree_workspace_size(int B, int n_new, int H_q, int H_kv, int d_head,
@@ -2599,5 +2633,51 @@ extern "C" sv_status spec_verify_attn_tree(const void *q, sv_dtype q_dtype, cons
   if (!tree_parent) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_tree: tree_parent is NULL");
   return attn_impl(q, q_dtype, k_cache, v_cache, kv_dtype, layout, k_scale, v_scale, block_table,
                    max_blocks_per_seq, seq_lens, B, n_new, H_q, H_kv, d_head, block_size, num_blocks,
-                   softmax_scale, out, out_dtype, workspace, workspace_bytes, dev_status, 0, tree_parent, stream);
+                   softmax_scale, out, out_dtype, workspace, workspace_bytes, dev_status, 0, tree_parent, 0, 0, stream);
+}
+
+extern "C" size_t spec_verify_attn_window_workspace_size(int B, int n_new, int H_q, int H_kv, int d_head,
+                                                         int max_blocks_per_seq, int block_size, int window,
+                                                         int sinks) {
+  if (B < 0 || n_new < 1 || H_q < 1 || H_kv < 1 || H_q % H_kv || d_head < 1 || max_blocks_per_seq < 1 ||
+      block_size < 1 || window < 0 || sinks < 0)
+    return 0;
+  if ((int64_t)window >= (int64_t)max_blocks_per_seq * block_size) window = sinks = 0;
+  return ws_bytes_any(B, n_new, H_q, H_kv, d_head, span_blocks_max(max_blocks_per_seq, n_new, window, sinks, block_size),
+                      block_size, 0);
+}
+
+extern "C" sv_status spec_verify_attn_window(const void *q, sv_dtype q_dtype, const void *k_cache, const void *v_cache,
+                                             sv_dtype kv_dtype, const sv_kv_layout *layout, const float *k_scale,
+                                             const float *v_scale, const int32_t *block_table,
+                                             int max_blocks_per_seq, const int32_t *seq_lens, int B, int n_new,
+                                             int H_q, int H_kv, int d_head, int block_size, int num_blocks,
+                                             float softmax_scale, int window, int sinks, void *out,
+                                             sv_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                                             int32_t *dev_status, sv_stream_t stream) {
+  if (window < 0 || sinks < 0) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_window: negative window or sinks");
+  if (kv_dtype != SV_F32 && kv_dtype != SV_BF16 && kv_dtype != SV_FP8_E4M3)
+    return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn_window: caches must be f32, bf16 or fp8");
+  return attn_impl(q, q_dtype, k_cache, v_cache, kv_dtype, layout, k_scale, v_scale, block_table,
+                   max_blocks_per_seq, seq_lens, B, n_new, H_q, H_kv, d_head, block_size, num_blocks,
+                   softmax_scale, out, out_dtype, workspace, workspace_bytes, dev_status, 0, nullptr, window, sinks,
+                   stream);
+}
+
+extern "C" size_t spec_verify_attn_q4_workspace_size(int B, int n_new, int H_q, int H_kv, int d_head,
+                                                     int max_blocks_per_seq, int block_size, int window, int sinks) {
+  return spec_verify_attn_window_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size, window,
+                                                sinks);
+}
+
+extern "C" sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const void *k_cache, const void *v_cache,
+                                         const sv_kv_layout *layout, const int32_t *block_table,
+                                         int max_blocks_per_seq, const int32_t *seq_lens, int B, int n_new, int H_q,
+                                         int H_kv, int d_head, int block_size, int num_blocks, float softmax_scale,
+                                         int window, int sinks, void *out, sv_dtype out_dtype, void *workspace,
+                                         size_t workspace_bytes, int32_t *dev_status, sv_stream_t stream) {
+  if (window < 0 || sinks < 0) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_q4: negative window or sinks");
+  return attn_impl(q, q_dtype, k_cache, v_cache, kQ4, layout, nullptr, nullptr, block_table, max_blocks_per_seq,
+                   seq_lens, B, n_new, H_q, H_kv, d_head, block_size, num_blocks, softmax_scale, out, out_dtype,
+                   workspace, workspace_bytes, dev_status, 0, nullptr, window, sinks, stream);
 }
