@@ -140,6 +140,7 @@ struct TcParams {   // 64-byte aligned through its CUtensorMap members
   float scale_log2;   // softmax_scale * log2(e)
   uint64_t wait_ns;   // limit of each wait on another warp's signal
   unsigned withhold;  // test hook: SV_TEST_WITHHOLD_COPIES issues no K/V copies
+  int window, sinks;  // WIN kernels: key t <= p is visible iff t > p - window or t < sinks
 };
 
 // TMA coordinates {d, dim1, dim2, dim3} of tile (kv head g, physical block)
@@ -366,7 +367,8 @@ constexpr int kOrdThreads = 1024;
 constexpr int kOrdMaxTiles = 1023;   // buckets 0..kOrdMaxTiles
 constexpr int kOrdPairs = 4;         // (s, b) pairs a thread keeps in registers
 __global__ void __launch_bounds__(kOrdThreads) attn_order_kernel(const int32_t *seq_lens, int B, int S, int H_kv,
-                                                                 int bps, int n_new, int max_blocks, int32_t *order) {
+                                                                 int bps, int n_new, int max_blocks, int window,
+                                                                 int sinks, int32_t *order) {
   pdl_trigger();
   __shared__ int cur[kOrdMaxTiles + 1];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(kOrdThreads) attn_order_kernel(const int32_t *
     const int sp = p % S, bp = p / S;
     const int L = seq_lens[bp];
     if (L < n_new || L > max_blocks * kBS) return 0;
-    const int blk = min(bps, (L + kBS - 1) / kBS - sp * bps);
+    const int blk = min(bps, key_span(L, n_new, window, sinks, kBS).nblk - sp * bps);
     return blk > 0 ? min(T, (blk + kT5Blk - 1) / kT5Blk) : 0;
   };
   for (int w = tid; w <= T; w += kOrdThreads) cur[w] = 0;
@@ -598,7 +600,10 @@ __device__ __forceinline__ float t5_store_q(uint32_t q_smem, int row, const uint
   }
 }
 
-template <int QR, bool FP8>
+// WIN: a sliding window with sinks. Keys and blocks are counted in the span the
+// call reads (key_span in q4.cuh), so only the table lookup knows of the gap,
+// and tiles that hold a key some row's window has left get one more compare.
+template <int QR, bool FP8, bool WIN>
 __global__ void __launch_bounds__(T5Cfg<QR, FP8>::kThreads, 2) attn_tc5_kernel(const __grid_constant__ TcParams P) {
   using Cfg = T5Cfg<QR, FP8>;
   constexpr int KS = Cfg::kKS, VS = Cfg::kVS;
@@ -664,7 +669,7 @@ __global__ void __launch_bounds__(T5Cfg<QR, FP8>::kThreads, 2) attn_tc5_kernel(c
   // the sequence length (the row is max_blocks entries long; entries past
   // the sequence are read but never used)
   int tab_cur = 0, tab_nxt = 0;
-  if (warp == 4 || warp == 5) {
+  if (!WIN && (warp == 4 || warp == 5)) {   // (WIN: the entries depend on the length)
     const int avail = P.max_blocks - s * P.bps;
     const int32_t *row0 = P.block_table + (int64_t)b * P.max_blocks + (int64_t)s * P.bps;
     tab_cur = lane < avail ? __ldg(row0 + lane) : 0;
@@ -677,12 +682,13 @@ __global__ void __launch_bounds__(T5Cfg<QR, FP8>::kThreads, 2) attn_tc5_kernel(c
   // the V ring the MMAs read: the widened one for FP8, else the TMA ring
   const uint32_t vc_ring = FP8 ? v_ring + VS * Cfg::kVRaw : v_ring;
 
-  const int L = P.seq_lens[b];
-  if (L < P.n_new || L > P.max_blocks * kBS) {
+  const int L_seq = P.seq_lens[b];
+  if (L_seq < P.n_new || L_seq > P.max_blocks * kBS) {
     if (tid == 0 && g == 0 && s == 0) atomic_or_status(P.status, SV_DEV_BAD_SEQ_LEN);
     return;
   }
-  const int nblk = (L + kBS - 1) / kBS;
+  const KeySpan span = key_span(L_seq, P.n_new, WIN ? P.window : 0, WIN ? P.sinks : 0, kBS);
+  const int L = span.L, nblk = span.nblk;
   const int blk0 = s * P.bps;
   if (blk0 >= nblk) return;   // the merge never reads this split
   const int blk1 = min(nblk, blk0 + P.bps);
@@ -711,6 +717,14 @@ __global__ void __launch_bounds__(T5Cfg<QR, FP8>::kThreads, 2) attn_tc5_kernel(c
       const uint32_t ring = isv ? v_ring : k_ring;
       const CUtensorMap *map = isv ? &P.tmv : &P.tmk;
       const int32_t *table = P.block_table + (int64_t)b * P.max_blocks + blk0;
+      // table entry of the split's block rel
+      auto entry = [&](int rel) {
+        return table[WIN && blk0 + rel >= span.nsb ? rel + span.skip : rel];
+      };
+      if (WIN) {
+        tab_cur = lane < nblocks ? entry(lane) : 0;
+        tab_nxt = 32 + lane < nblocks ? entry(32 + lane) : 0;
+      }
       int cur = tab_cur;
       int nxt = tab_nxt;
       int chunk = 0;
@@ -724,7 +738,7 @@ __global__ void __launch_bounds__(T5Cfg<QR, FP8>::kThreads, 2) attn_tc5_kernel(c
           chunk = first >> 5;
           cur = nxt;
           const int rel = (chunk + 1) * 32 + lane;
-          nxt = rel < nblocks ? table[rel] : 0;
+          nxt = rel < nblocks ? entry(rel) : 0;
         }
         int phys[TB];
 #pragma unroll
@@ -910,10 +924,13 @@ __global__ void __launch_bounds__(T5Cfg<QR, FP8>::kThreads, 2) attn_tc5_kernel(c
 #pragma unroll
             for (int k = 0; k < TN; ++k) x[k] = __uint_as_float(r[k]);   // unscaled scores
           }
-          if (key0 + TN > end_key || key0 + TN - 1 > L - P.n_new) {   // reaches the diagonal or the end
+          if (key0 + TN > end_key || key0 + TN - 1 > L - P.n_new ||    // reaches the diagonal or the end
+              (WIN && key0 < L - P.window)) {                          // or holds keys the last row's window has left
 #pragma unroll
             for (int k = 0; k < TN; ++k)
-              if (key0 + k > lim || key0 + k >= end_key) x[k] = -INFINITY;
+              if (key0 + k > lim || key0 + k >= end_key ||
+                  (WIN && key0 + k >= P.sinks && key0 + k <= lim - P.window))
+                x[k] = -INFINITY;
             if (P.anc) {   // draft tree: new keys off the row's ancestor path go too
 #pragma unroll
               for (int k = 0; k < TN; ++k) {
@@ -992,6 +1009,26 @@ __global__ void __launch_bounds__(T5Cfg<QR, FP8>::kThreads, 2) attn_tc5_kernel(c
                 for (int c = 0; c < 8; ++c)
                   asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vb + hh * Cfg::kVHalf + off + c * 16),
                                "r"(0u)
+                               : "memory");
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if (WIN && !FP8 && warp == 0 && key0 <= L - P.n_new - P.window && key0 + TN > P.sinks) {
+          // keys that no row sees: their V rows are zeroed in the same way
+          for (int h = 0; h < VPT; ++h) {
+            const int vi = t * VPT + h, k0 = key0 + 16 * kT5Blk * h;
+            if (k0 >= end_key) continue;   // (that stage was not copied)
+            if (!t5_wait(&v_full[vi % VS], (vi / VS) & 1, abf, P.wait_ns)) ok = false;
+            const uint32_t vb = v_ring + (vi % VS) * Cfg::kVRaw;
+            for (int k = lane; k < 16 * kT5Blk; k += 32) {
+              if (k0 + k < P.sinks || k0 + k > L - P.n_new - P.window) continue;
+              const uint32_t off = (uint32_t)((k >> 4) * 2048 + (k & 15) * 128);
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vb + hh * Cfg::kVHalf + off + c * 16), "r"(0u)
                                : "memory");
             }
           }
@@ -1090,7 +1127,9 @@ __global__ void __launch_bounds__(T5Cfg<QR, FP8>::kThreads, 2) attn_tc5_kernel(c
                        : "=r"(v0), "=r"(v1), "=r"(v2), "=r"(v3)
                        : "r"(src + blk * 2048 + r16 * 128 + ((ch ^ (r16 & 7)) << 4)));
           uint32_t h[8];
-          if (key0 + row < end_key) {
+          // (WIN: zeros for the keys that no row sees, too)
+          if (key0 + row < end_key &&
+              !(WIN && key0 + row >= P.sinks && key0 + row <= L - P.n_new - P.window)) {
             const uint32_t w[4] = {v0, v1, v2, v3};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -2339,7 +2378,7 @@ __global__ void __launch_bounds__(64) attn_tree_kernel(const int32_t *parent, in
   anc[(int64_t)b * n_new + j] = m;
 }
 
-template <int QR, bool FP8>
+template <int QR, bool FP8, bool WIN>
 sv_status launch_tc5(const TcParams &P0, cudaStream_t st) {
   using Cfg = T5Cfg<QR, FP8>;
   TcParams P = P0;
@@ -2347,8 +2386,8 @@ sv_status launch_tc5(const TcParams &P0, cudaStream_t st) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(attn_tc5_kernel<QR, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
-    if (attr_err == cudaSuccess)
+    attr_err = cudaFuncSetAttribute(attn_tc5_kernel<QR, FP8, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    if (!WIN && attr_err == cudaSuccess)
       attr_err = cudaFuncSetAttribute(attn_tc5_bal_kernel<QR, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       Cfg::kSmem);
   });
@@ -2369,13 +2408,13 @@ sv_status launch_tc5(const TcParams &P0, cudaStream_t st) {
       P.order = nullptr;
     } else {
       launch_k(attn_order_kernel, dim3(1), dim3(kOrdThreads), 0, st, 1, P.seq_lens, P.B, P.S, P.H_kv, P.bps, P.n_new,
-               P.max_blocks, const_cast<int32_t *>(P.order));
+               P.max_blocks, P.window, P.sinks, const_cast<int32_t *>(P.order));
     }
   }
   sv_status rc = check_launch("spec_verify_attn order launch");
   if (rc != SV_OK) return rc;
   if (P.balanced) launch_k(attn_tc5_bal_kernel<QR, FP8>, dim3(grid), dim3(Cfg::kThreads), Cfg::kSmem, st, 1, P);
-  else launch_k(attn_tc5_kernel<QR, FP8>, dim3(grid), dim3(Cfg::kThreads), Cfg::kSmem, st, 1, P);
+  else launch_k(attn_tc5_kernel<QR, FP8, WIN>, dim3(grid), dim3(Cfg::kThreads), Cfg::kSmem, st, 1, P);
   return check_launch("spec_verify_attn tcgen05 launch");
 }
 
@@ -2430,8 +2469,8 @@ static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache,
   if (window < 0 || sinks < 0) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_window: negative window or sinks");
   if ((int64_t)window >= (int64_t)max_blocks_per_seq * block_size) window = sinks = 0;   // reaches every key
   const int span_blocks = span_blocks_max(max_blocks_per_seq, n_new, window, sinks, block_size);
-  Plan plan = make_plan(B, n_new, H_q, H_kv, d_head, span_blocks, block_size, kv_dtype, q_dtype, layout, bps_req);
-  if (window > 0 && plan.tc) plan = make_plan(B, n_new, H_q, H_kv, d_head, span_blocks, block_size, SV_F32, SV_F32, layout, bps_req);
+  const Plan plan =
+      make_plan(B, n_new, H_q, H_kv, d_head, span_blocks, block_size, kv_dtype, q_dtype, layout, bps_req);
   if (plan.R > 65535) return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: too many query rows per kv head");
   const size_t base_need = ws_bytes(plan, B, H_kv);
   const size_t need = base_need + (tree_parent ? align_up((size_t)B * n_new * sizeof(uint64_t), 256) : 0);
@@ -2518,8 +2557,15 @@ static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache,
     P.scale_log2 = scale_log2;
     P.wait_ns = wait_limit_ns();
     P.withhold = test_withhold();
-    if (!fp8) rc = plan.R <= 64 ? launch_tc5<64, false>(P, st) : launch_tc5<128, false>(P, st);
-    else rc = plan.R <= 64 ? launch_tc5<64, true>(P, st) : launch_tc5<128, true>(P, st);
+    P.window = window;
+    P.sinks = sinks;
+    if (window > 0) {
+      if (!fp8) rc = plan.R <= 64 ? launch_tc5<64, false, true>(P, st) : launch_tc5<128, false, true>(P, st);
+      else rc = plan.R <= 64 ? launch_tc5<64, true, true>(P, st) : launch_tc5<128, true, true>(P, st);
+    } else {
+      if (!fp8) rc = plan.R <= 64 ? launch_tc5<64, false, false>(P, st) : launch_tc5<128, false, false>(P, st);
+      else rc = plan.R <= 64 ? launch_tc5<64, true, false>(P, st) : launch_tc5<128, true, false>(P, st);
+    }
   } else {
     GenParams P;
     P.q = q; P.out = out; P.k_cache = k_cache; P.v_cache = v_cache; P.k_scale = k_scale; P.v_scale = v_scale;
