@@ -40,6 +40,7 @@
 #include <type_traits>
 
 #include "q4.cuh"
+#include "tc5.cuh"
 
 namespace sv {
 namespace {
@@ -49,70 +50,6 @@ constexpr int kD = 128;           // head dim of the tensor-core path
 constexpr int kBS = 16;           // block size of the tensor-core path
 constexpr int kGenThreads = 128;
 constexpr int kGenKeys = 32;
-
-// ------------------------------------------------------ PTX: tensor core ---
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (F16) {
-    __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t *>(&h);
-  } else {
-    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t *>(&h);
-  }
-}
-
-// maximum of a tile's N scores per row as a tree of depth log2 N (a chain
-// of N - 1 dependent maxima otherwise sits on every tile's critical path)
-template <int N>
-__device__ __forceinline__ float t5_tile_max(const float (&x)[N]) {
-  static_assert(N >= 2 && (N & (N - 1)) == 0, "power of two");
-  float m[N / 2];
-#pragma unroll
-  for (int k = 0; k < N / 2; ++k) m[k] = fmaxf(x[k], x[k + N / 2]);
-#pragma unroll
-  for (int w = N / 4; w >= 1; w >>= 1)
-#pragma unroll
-    for (int k = 0; k < w; ++k) m[k] = fmaxf(m[k], m[k + w]);
-  return m[0];
-}
-
-// 2^x on the SFU (results below 2^-126 flush to zero)
-__device__ __forceinline__ float ex2f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// two fp32 values -> two e4m3 codes (x0 in the low byte), rounded to
-// nearest even, saturating at +-448
-__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float x0, float x1) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
-  return r;
-}
-
-// two e4m3 codes (low byte first) -> f16x2
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
-  uint32_t out;
-  asm volatile("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(out) : "h"(v));
-  return out;
-}
-
-// 4-D TMA tile copy into shared memory, completion on `bar`.
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
-                                            int c3, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-      "%3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ void named_bar_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 
 // ------------------------------------------------- tensor-core kernel -----
 struct TcParams {   // 64-byte aligned through its CUtensorMap members
@@ -225,84 +162,6 @@ template <int QR, bool FP8> struct T5Cfg {
   static_assert(kSmem <= 1024 + 106496, "two CTAs per SM");
 };
 constexpr uint32_t kT5Cols = 256;              // TMEM columns: S/P buffers, O
-
-__device__ __forceinline__ uint64_t t5_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFF) << 32;
-  d |= (uint64_t)1 << 46;   // descriptor version of the sm_100 family
-  d |= (uint64_t)2 << 61;   // 128-byte swizzle
-  return d;
-}
-
-__device__ __forceinline__ void t5_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-               "r"(a), "l"(b), "r"(idesc), "r"(acc));
-}
-
-// A from shared memory (descriptor)
-__device__ __forceinline__ void t5_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-               "l"(a), "l"(b), "r"(idesc), "r"(acc));
-}
-
-// kind::f8f6f4 (e4m3 A and B, 32 elements of K per MMA), A from shared memory
-__device__ __forceinline__ void t5_mma_ss_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-               "l"(a), "l"(b), "r"(idesc), "r"(acc));
-}
-
-__device__ __forceinline__ void t5_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
-
-__device__ __forceinline__ void t5_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void t5_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-__device__ __forceinline__ void t5_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-
-__device__ __forceinline__ void t5_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
-__device__ __forceinline__ void t5_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void t5_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Non-blocking probe of a barrier phase.
-__device__ __forceinline__ bool t5_test(uint64_t *bar, uint32_t phase) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(phase)
-      : "memory");
-  return done != 0;
-}
-
-// Bounded wait (limit_ns) that gives up at once after any earlier wait of the
-// CTA gave up.
-__device__ __forceinline__ bool t5_wait(uint64_t *bar, uint32_t phase, volatile int *abort_flag, uint64_t limit_ns) {
-  if (*abort_flag) return false;
-  if (mbar_wait(bar, phase, limit_ns)) return true;
-  *abort_flag = 1;
-  return false;
-}
 
 // The work items of a CTA of the balanced-mode kernel: blocks [blk0, blk1)
 // of kv head g of sequence b. The sequence of tiles (P.tblk blocks each) of
@@ -2710,20 +2569,16 @@ extern "C" sv_status spec_verify_attn_window(const void *q, sv_dtype q_dtype, co
                    stream);
 }
 
-extern "C" size_t spec_verify_attn_q4_workspace_size(int B, int n_new, int H_q, int H_kv, int d_head,
-                                                     int max_blocks_per_seq, int block_size, int window, int sinks) {
-  return spec_verify_attn_window_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size, window,
-                                                sinks);
-}
+namespace sv {
 
-extern "C" sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const void *k_cache, const void *v_cache,
-                                         const sv_kv_layout *layout, const int32_t *block_table,
-                                         int max_blocks_per_seq, const int32_t *seq_lens, int B, int n_new, int H_q,
-                                         int H_kv, int d_head, int block_size, int num_blocks, float softmax_scale,
-                                         int window, int sinks, void *out, sv_dtype out_dtype, void *workspace,
-                                         size_t workspace_bytes, int32_t *dev_status, sv_stream_t stream) {
-  if (window < 0 || sinks < 0) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_q4: negative window or sinks");
+sv_status attn_cuda_core_q4(const void *q, sv_dtype q_dtype, const void *k_cache, const void *v_cache,
+                            const sv_kv_layout *layout, const int32_t *block_table, int max_blocks_per_seq,
+                            const int32_t *seq_lens, int B, int n_new, int H_q, int H_kv, int d_head, int block_size,
+                            int num_blocks, float softmax_scale, int window, int sinks, void *out, sv_dtype out_dtype,
+                            void *workspace, size_t workspace_bytes, int32_t *dev_status, sv_stream_t stream) {
   return attn_impl(q, q_dtype, k_cache, v_cache, kQ4, layout, nullptr, nullptr, block_table, max_blocks_per_seq,
                    seq_lens, B, n_new, H_q, H_kv, d_head, block_size, num_blocks, softmax_scale, out, out_dtype,
                    workspace, workspace_bytes, dev_status, 0, nullptr, window, sinks, stream);
 }
+
+}  // namespace sv

@@ -1,0 +1,1012 @@
+// spec_verify_attn_q4 on the tensor cores: paged GQA verify attention over a
+// 4-bit cache (record layout: q4.cuh), d_head 128, 16-token blocks, bf16
+// queries.
+//
+// Mathematics. With K_t = s_t c_t + m_t and V_t = s'_t c'_t + m'_t (c, c' codes
+// in 0..15, one scale and minimum per key), for query row r
+//   x_rt = scale (s_t (q_r . c_t) + m_t sum(q_r)),
+//   p'_rt = s'_t 2^(x_rt - ref_r)            (log2 domain, ref_r a running reference)
+//   out_r = [sum_t p'_rt (c'_t - 8) + sum_t p'_rt (m'_t / s'_t + 8)] / sum_t p'_rt / s'_t
+// so both products run on the bare codes and the scales enter per key. (The
+// tensor cores' accumulation rounds towards zero: with codes of one sign the
+// first sum grows to some 8 sum p', and at 128K keys, where the outputs are
+// averages near zero, its rounding errors reached 1 % of the outputs.)
+//
+// Codes as operands. The low four bits of an f16 are the code times 2^-24, a
+// subnormal that the tensor cores multiply exactly; a word of eight K codes
+// becomes four f16 pairs with `(w >> 4k) & 0x000F000F`, seven instructions for
+// eight values and no conversion. V codes are put below the exponent of 1024
+// in the same instruction, and 1032 is taken off the pair. A pair holds codes
+// k and k + 4 of the word, so the other operand of each product is stored in
+// that order.
+//
+// Keys on the lanes. The M = 128 side of both products is the cache: S^T = C Q^T
+// has a key per lane, O^T = C'^T P'^T a head dim per lane, and N is the number
+// of query rows (16 to 64), so no tensor-core work is padding whatever the
+// GQA group. The A operand is written by the thread that owns its lane, from
+// its own 64 bytes of codes, straight into tensor memory; shared memory holds
+// only the raw records, Q and P'. A K record is slot-major and a V record
+// dim-major for this reason.
+//
+// What bounds it: 136 bytes per key and kv head leave about 820 SM cycles per
+// 128-key tile at the measured HBM bandwidth, for 2 x 128 x 128 codes to unpack
+// and 128 R exponentials.
+//
+// Work: the tiles of all sequences end to end are cut into equal ranges, one
+// per SM and kv head; each CTA (one per SM) computes its own range from the
+// lengths and streams through its sequences without draining the pipeline. A
+// range that ends inside a sequence leaves fp32 partials for the merge.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+#include <type_traits>
+
+#include "q4.cuh"
+#include "tc5.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kD = 128;                    // head dim
+constexpr int kBS = 16;                    // block size
+constexpr int kTP = 8;                     // blocks per tile
+constexpr int kTK = kTP * kBS;             // keys per tile
+constexpr int kRec = kBS * (kD / 2 + 4);   // record bytes
+constexpr int kCodes = kBS * kD / 2;
+constexpr int kStage = 2 * kTP * kRec;     // K records, then V records
+constexpr int kNS = 8;                     // stages of the record ring
+constexpr int kPBytes = kTK * 128;         // a P' buffer: 128 bytes (64 columns of f16) a key
+constexpr int kWarps = 20;
+constexpr int kKWarp = 8, kVWarp = 12, kLoadWarp = 16, kMmaWarp = 17, kQWarp = 18;
+// Registers: launched at 96 a thread; the K, V and service warps hand over 32
+// each so that the softmax warps hold a tile's scores and two sums per column
+// (256 x 144 + 384 x 64 = 640 x 96).
+constexpr int kRegsSoftmax = 144, kRegsOther = 64;
+constexpr float kUnset = 1e30f;            // minus the reference of a row that has met no key
+
+struct Q4Params {
+  const void *q;
+  void *out;
+  const uint8_t *k_cache, *v_cache;
+  const int32_t *block_table, *seq_lens;
+  float *ws_acc;      // [2 CTAs][Rg][kD] partials (entry 2c: CTA c's first sequence, 2c + 1: its last)
+  float *ws_ml;       // [2 CTAs][Rg][2]
+  int4 *ws_split;     // per range: the sequence whose first cut is the range's start (b, first tile, tiles), or b = -1
+  int32_t *status;
+  int64_t block_stride, head_stride;
+  int B, n_new, H_q, H_kv, G, R;
+  int Rg, RG;         // query rows of a CTA, and row groups per kv head
+  int NR;             // ranges
+  int max_blocks, num_blocks, window, sinks;
+  float scale_log2;   // softmax_scale * log2(e)
+  uint64_t wait_ns;
+  unsigned withhold;
+};
+
+template <int NC> struct Q4Cfg {   // NC columns per softmax warpgroup
+  static constexpr int kN = 2 * NC;
+  static constexpr int kQ = kN * 256;   // two head-dim halves of 128-byte rows
+  static constexpr uint32_t kKCol = 0, kVCol = 128, kSCol = 256, kOCol = 256 + 2 * kN;
+  static constexpr int kSmem = 1024 + 2 * kQ + 2 * kPBytes + kNS * kStage;
+  static_assert(kOCol + kN <= 512, "TMEM columns");
+  static_assert(kSmem + 6144 <= 227 * 1024, "shared memory");
+};
+
+// A sequence's part of a CTA's range.
+struct Q4Item {
+  int b, L, tile0, ntiles;
+  KeySpan span;
+  bool whole;      // the whole sequence: written directly
+  bool first;      // the CTA's first item
+};
+// Walks the range; the next sequence's length is loaded one item ahead.
+struct Q4Walk {
+  int b, off, left, L;
+  bool first;
+};
+
+__device__ __forceinline__ int q4_tiles(const Q4Params &P, int L) {
+  if (L < P.n_new || L > P.max_blocks * kBS) return 0;
+  return (key_span(L, P.n_new, P.window, P.sinks, kBS).nblk + kTP - 1) / kTP;
+}
+
+__device__ __forceinline__ Q4Walk q4_walk(const Q4Params &P, const int4 &w) {
+  Q4Walk k = {w.x, w.y, w.z, 0, true};
+  if (k.left > 0 && k.b < P.B) k.L = P.seq_lens[k.b];
+  return k;
+}
+
+__device__ __forceinline__ bool q4_next(const Q4Params &P, Q4Walk &w, Q4Item &it) {
+  if (w.left <= 0) return false;
+  int nt;
+  for (;;) {   // sequences with invalid lengths hold no tiles
+    if (w.b >= P.B) return false;
+    nt = q4_tiles(P, w.L);
+    if (nt > 0) break;
+    ++w.b;
+    w.L = w.b < P.B ? P.seq_lens[w.b] : 0;
+  }
+  const int take = min(nt - w.off, w.left);
+  it.b = w.b;
+  it.L = w.L;
+  it.tile0 = w.off;
+  it.ntiles = take;
+  it.span = key_span(w.L, P.n_new, P.window, P.sinks, kBS);
+  it.whole = w.off == 0 && take == nt;
+  it.first = w.first;
+  w.first = false;
+  w.left -= take;
+  w.off = 0;
+  ++w.b;
+  w.L = w.left > 0 && w.b < P.B ? P.seq_lens[w.b] : 0;
+  return true;
+}
+
+// One warp: range r of the tile sequence as (b, first tile within b, tiles),
+// and the split record of the range's start.
+__device__ __forceinline__ int4 q4_range(const Q4Params &P, int r, bool report, int4 &split) {
+  const int lane = threadIdx.x & 31;
+  int64_t T = 0;
+  for (int b0 = 0; b0 < P.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int L = b < P.B ? P.seq_lens[b] : P.n_new;
+    int nt = b < P.B ? q4_tiles(P, L) : 0;
+    if (report && (L < P.n_new || L > P.max_blocks * kBS)) atomic_or_status(P.status, SV_DEV_BAD_SEQ_LEN);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) nt += __shfl_xor_sync(0xffffffffu, nt, o);
+    T += nt;
+  }
+  const int64_t t0 = r * T / P.NR, t1 = (r + 1) * T / P.NR;
+  int4 w = make_int4(0, 0, 0, 0);
+  split = make_int4(-1, 0, 0, 0);
+  if (t1 <= t0) return w;
+  int64_t A = 0;
+  for (int b0 = 0; b0 < P.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int nt = b < P.B ? q4_tiles(P, P.seq_lens[b]) : 0;
+    int incl = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, A + incl > t0);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const int off = (int)(t0 - (A + __shfl_sync(0xffffffffu, incl - nt, src)));
+      w = make_int4(b0 + src, off, (int)(t1 - t0), 0);
+      // a range that starts inside a sequence is its first cut if one range
+      // holds all its tiles before (tile x lies in range ((x + 1) NR - 1) / T)
+      const int64_t first = t0 - off;
+      if (off > 0 && (t0 * P.NR - 1) / T == ((first + 1) * P.NR - 1) / T)
+        split = make_int4(b0 + src, (int)first, __shfl_sync(0xffffffffu, nt, src), (int)T);
+      return w;
+    }
+    A += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return w;
+}
+
+__device__ __forceinline__ bool bar_or(int id, int threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+// Bounded wait; a wait that has to sleep gives up at once after any earlier
+// one of the CTA gave up.
+__device__ __forceinline__ bool q4_wait(uint64_t *bar, uint32_t phase, volatile int *abort_flag, uint64_t limit_ns) {
+  if (mbar_try_wait(bar, phase)) return true;
+  return t5_wait(bar, phase, abort_flag, limit_ns);
+}
+
+template <int R> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// eight codes of a word -> four f16 pairs (codes k and k + 4): K codes times
+// 2^-24, V codes minus 8
+template <bool V>
+__device__ __forceinline__ void spread(uint32_t w, uint32_t *o) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t c = (w >> (4 * k)) & 0x000F000Fu;
+    if constexpr (V) {
+      const uint32_t y = c | 0x64006400u;
+      const __half2 z = __hsub2(*reinterpret_cast<const __half2 *>(&y), __half2half2(__ushort_as_half(0x6408)));
+      o[k] = *reinterpret_cast<const uint32_t *>(&z);
+    } else {
+      o[k] = c;
+    }
+  }
+}
+
+// Sums of v[0..NV) over the warp's lanes: lane l returns the sum of column
+// l * NV / 32 (NV a power of two up to 32): each step exchanges the half of the
+// columns that the other lane keeps.
+template <int NV>
+__device__ __forceinline__ float warp_columns(float (&v)[NV], int lane) {
+#pragma unroll
+  for (int n = NV / 2, o = 16; o >= 1; n >>= 1, o >>= 1) {
+    if (n >= 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int k = 0; k < (n > 0 ? n : 1); ++k) {
+        const float send = up ? v[k] : v[k + n], keep = up ? v[k + n] : v[k];
+        v[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
+  }
+  return v[0];
+}
+
+// N columns of this warp's lanes, N a multiple of 8
+__device__ __forceinline__ void t5_ld8(uint32_t taddr, uint32_t *r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+template <int N>
+__device__ __forceinline__ void t5_ldn(uint32_t taddr, uint32_t (&r)[N]) {
+#pragma unroll
+  for (int k = 0; k + 16 <= N; k += 16) t5_ld16(taddr + k, *reinterpret_cast<uint32_t(*)[16]>(r + k));
+  if constexpr (N % 16 == 8) t5_ld8(taddr + N - 8, r + N - 8);
+}
+
+// Warps 0-3 and 4-7: softmax (a key per thread; each warpgroup half of the
+// query rows), later the epilogue (a head dim per thread). 8-11: K codes to
+// tensor memory. 12-15: V codes. 16: record copies. 17: MMA issue, owner of
+// the 512 TMEM columns (two K, two V, two S buffers and O). 18: Q of the next
+// sequence. 19: none (it completes the warpgroup).
+template <int NC>
+__global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_constant__ Q4Params P) {
+  using Cfg = Q4Cfg<NC>;
+  constexpr int N = Cfg::kN;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t raw_full[kNS], raw_empty[kNS];
+  __shared__ __align__(8) uint64_t kop_full[2], kop_empty[2], vop_full[2], vop_empty[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2], o_free, drain;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  __shared__ int4 s_work;
+  // per row of the two items in flight: sum(q), position (0 .. n_new - 1),
+  // row of q and out; per item the power of two that undoes Q's scaling
+  __shared__ __align__(16) float s_qs[2][N];
+  __shared__ int s_pos[2][N], s_row[2][N];
+  __shared__ float s_fold[2];
+  __shared__ __align__(16) float s_nb[N], s_a[N];   // minus the reference; the last factor of a rescale
+  __shared__ float s_max[8][NC], s_red[8][NC][2];
+  __shared__ __align__(8) float2 s_fin[N];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int Hp = P.H_kv * P.RG;
+  const int range = blockIdx.x / Hp, gp = blockIdx.x % Hp;
+  const int g = gp / P.RG, row0 = (gp % P.RG) * P.Rg;
+  const int rows = min(P.Rg, P.R - row0);       // live rows of this CTA
+  const int live0 = (rows + 1) / 2;             // of the first softmax warpgroup
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t q_smem = smem_u32(smem);
+  const uint32_t p_smem = q_smem + 2 * Cfg::kQ;
+  const uint32_t ring = p_smem + 2 * kPBytes;
+
+  if (warp == 0) {
+    // (the lengths are the caller's: read before the wait on the previous kernel)
+    int4 split;
+    const int4 w = q4_range(P, range, blockIdx.x == 0, split);
+    if (lane == 0) s_work = w;
+    pdl_wait();   // the previous kernel may be a merge that still reads this workspace
+    if (lane == 0 && gp == 0) P.ws_split[range] = split;
+  } else if (tid == 32) {
+    for (int k = 0; k < kNS; ++k) {
+      mbar_init(&raw_full[k], 1);
+      mbar_init(&raw_empty[k], 16);   // the K, V and softmax warps
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&kop_full[k], 4);
+      mbar_init(&kop_empty[k], 1);
+      mbar_init(&vop_full[k], 4);
+      mbar_init(&vop_empty[k], 1);
+      mbar_init(&s_full[k], 1);
+      mbar_init(&p_full[k], 8);
+      mbar_init(&o_done[k], 1);
+      mbar_init(&q_full[k], 1);
+      mbar_init(&q_empty[k], 9);   // the softmax warps, and the last Q K^T
+    }
+    mbar_init(&o_free, 8);
+    mbar_init(&drain, 1);
+    abort_flag = 0;
+    fence_mbarrier_init();
+  } else if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  pdl_wait();
+  pdl_trigger();
+  t5_fence_before();
+  __syncthreads();
+  t5_fence_after();
+  const uint32_t tb = tmem_base;
+  const int4 work = s_work;
+  const int total = work.z;   // tiles of this CTA
+  volatile int *abf = &abort_flag;
+  // every stage, buffer and phase below follows the CTA's running tile count u
+
+  if (warp >= kLoadWarp) regs_dec<kRegsOther>();
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------- records --
+    // Lane l copies block l / 2 of a tile, K (even) or V. The block table is
+    // read 32 entries at a time, one window and one sequence ahead.
+    Q4Walk wk = q4_walk(P, work);
+    Q4Item it, nx;
+    const int page = lane >> 1;
+    const bool mine = lane < 2 * kTP;
+    const uint8_t *pool = ((lane & 1) ? P.v_cache : P.k_cache) + (int64_t)g * P.head_stride;
+    const uint32_t dst0 = (lane & 1) * (kTP * kRec) + page * kRec;
+    auto entry = [&](const Q4Item &i, int v) {   // table entry of block v of the span
+      return v < min(i.span.nblk, (i.tile0 + i.ntiles) * kTP)
+                 ? P.block_table[(int64_t)i.b * P.max_blocks + (v < i.span.nsb ? v : v + i.span.skip)]
+                 : 0;
+    };
+    int u = 0, st = 0, round = 0;
+    bool go = !(P.withhold & SV_TEST_WITHHOLD_COPIES);
+    bool have = q4_next(P, wk, it);
+    int cur = have ? entry(it, it.tile0 * kTP + lane) : 0;
+    while (go && have) {
+      const bool more = q4_next(P, wk, nx);
+      const int v0 = it.tile0 * kTP;
+      int ahead = entry(it, v0 + 32 + lane);
+      const int cur_nx = more ? entry(nx, nx.tile0 * kTP + lane) : 0;
+      for (int ti = 0; ti < it.ntiles; ++ti, ++u) {
+        if (ti > 0 && (ti & 3) == 0) {
+          cur = ahead;
+          ahead = entry(it, v0 + ti * kTP + 32 + lane);
+        }
+        int phys = __shfl_sync(0xffffffffu, cur, ((ti & 3) * kTP + page) & 31);
+        if (round > 0) go = __all_sync(0xffffffffu, q4_wait(&raw_empty[st], (round & 1) ^ 1, abf, P.wait_ns));
+        if (!go) break;
+        const int nv = min(kTP, it.span.nblk - (it.tile0 + ti) * kTP);
+        if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], (uint32_t)(nv * 2 * kRec));
+        __syncwarp();
+        if (mine && page < nv) {
+          if (phys < 0 || phys >= P.num_blocks) {
+            atomic_or_status(P.status, SV_DEV_BAD_BLOCK);
+            phys = 0;   // stay in bounds; the output of this sequence is flagged
+          }
+          bulk_g2s(smem + (ring - q_smem) + st * kStage + dst0, pool + (int64_t)phys * P.block_stride, kRec, &raw_full[st]);
+        }
+        if (++st == kNS) {
+          st = 0;
+          ++round;
+        }
+      }
+      it = nx;
+      cur = cur_nx;
+      have = more;
+    }
+    // the copies in flight land before the CTA may exit
+    if (lane == 0)
+      for (int t = max(0, u - kNS); t < u; ++t)
+        if (!mbar_wait(&raw_full[t % kNS], (t / kNS) & 1)) atomic_or_status(P.status, SV_DEV_TIMEOUT);
+  } else if (warp == kQWarp) {
+    // ------------------------------------------------------------------- Q --
+    // Row by row to f16, scaled by one power of two that brings the largest
+    // finite element of the CTA's rows to [2^14, 2^15): bf16 values are then
+    // exact down to 2^-28 of it.
+    Q4Walk wk = q4_walk(P, work);
+    Q4Item it;
+    int i = 0;
+    while (q4_next(P, wk, it)) {
+      const int buf = i & 1;
+      if (i >= 2 && !__all_sync(0xffffffffu, q4_wait(&q_empty[buf], ((i >> 1) & 1) ^ 1, abf, P.wait_ns))) break;
+      const int c8 = lane & 15;
+      auto row_of = [&](int col) {   // query row of a column, -1 for padding
+        const int w = col / NC, c = col - w * NC;
+        const int r = w * live0 + c;
+        return c < (w ? rows - live0 : live0) ? row0 + r : -1;
+      };
+      auto q_row = [&](int r) {   // its row in q and out
+        const int j = r / P.G;
+        return (it.b * P.n_new + j) * P.H_q + g * P.G + (r - j * P.G);
+      };
+      const uint4 *q = static_cast<const uint4 *>(P.q);
+      uint32_t top = 0;
+#pragma unroll 4
+      for (int c0 = 0; c0 < N; c0 += 2) {
+        const int r = row_of(c0 + (lane >> 4));
+        const uint4 v = r >= 0 ? q[(int64_t)q_row(r) * 16 + c8] : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t lo = (w[e] << 16) & 0x7fffffffu, hi = w[e] & 0x7fff0000u;
+          if (lo < 0x7f800000u) top = max(top, lo);
+          if (hi < 0x7f800000u) top = max(top, hi);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int ex = min(117, max(-113, (int)(top >> 23) - 127));   // (both powers stay normal)
+      const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+#pragma unroll 2
+      for (int c0 = 0; c0 < N; c0 += 2) {
+        const int col = c0 + (lane >> 4);
+        const int r = row_of(col);
+        const uint4 v = r >= 0 ? q[(int64_t)q_row(r) * 16 + c8] : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float x[8], sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[2 * e] = __uint_as_float(w[e] << 16);
+          x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += x[e];
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        uint32_t h[4];   // in the order of the codes: dims k and k + 4
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = pack2<true>(x[e] * up, x[e + 4] * up);
+        const uint32_t dst = q_smem + buf * Cfg::kQ + (c8 >> 3) * (N * 128) + col * 128 + (((c8 & 7) ^ (col & 7)) << 4);
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                     : "memory");
+        if (c8 == 0) {
+          s_qs[buf][col] = sum;
+          s_pos[buf][col] = r >= 0 ? r / P.G : 0;
+          s_row[buf][col] = r >= 0 ? q_row(r) : 0;
+        }
+      }
+      // 2^-24 of the codes and 2^(14 - ex) of Q
+      if (lane == 0) s_fold[buf] = __uint_as_float((uint32_t)(127 + 10 + ex) << 23);
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[buf]);
+      ++i;
+    }
+  } else if (warp == kMmaWarp) {
+    // ----------------------------------------------------------------- MMA --
+    if (lane == 0 && total > 0) {
+      // f16 A and B, f32 accumulators, M = 128
+      constexpr uint32_t idesc_qk = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+      constexpr uint32_t idesc_pv = idesc_qk | (1u << 16);   // B = P'^T with the rows contiguous
+      Q4Walk wq = q4_walk(P, work), wp = wq;
+      Q4Item iq, ip;
+      int nq = 0, np = 0;          // items started
+      int lq = 0, lp = 0, tp = 0;  // tiles left in the current item; its next P V tile
+      auto qk = [&](int u) {
+        const int bf = u & 1;
+        if (lq == 0) {
+          q4_next(P, wq, iq);
+          lq = iq.ntiles;
+          if (!q4_wait(&q_full[nq & 1], (nq >> 1) & 1, abf, P.wait_ns)) return false;
+          ++nq;
+        }
+        if (!q4_wait(&kop_full[bf], (u >> 1) & 1, abf, P.wait_ns)) return false;
+        t5_fence_after();
+        const uint32_t qb = q_smem + ((nq - 1) & 1) * Cfg::kQ;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)   // 16 head dims per MMA
+          t5_mma_ts(tb + Cfg::kSCol + bf * N, tb + Cfg::kKCol + bf * 64 + 8 * kk,
+                    t5_desc(qb + (kk >> 2) * (N * 128) + (kk & 3) * 32, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
+        t5_commit(&s_full[bf]);
+        t5_commit(&kop_empty[bf]);
+        if (--lq == 0) t5_commit(&q_empty[(nq - 1) & 1]);
+        return true;
+      };
+      bool okm = qk(0);
+      for (int u = 0; okm && u < total; ++u) {
+        if (u + 1 < total && !qk(u + 1)) break;
+        const int bf = u & 1;
+        const bool fresh = lp == 0;
+        if (fresh) {
+          q4_next(P, wp, ip);
+          lp = ip.ntiles;
+          tp = ip.tile0;
+          // the previous item's O has been read
+          if (np > 0 && !q4_wait(&o_free, (np - 1) & 1, abf, P.wait_ns)) break;
+          ++np;
+        }
+        if (!q4_wait(&vop_full[bf], (u >> 1) & 1, abf, P.wait_ns)) break;
+        if (!q4_wait(&p_full[bf], (u >> 1) & 1, abf, P.wait_ns)) break;
+        t5_fence_after();
+        const int nv = min(kTP, ip.span.nblk - tp * kTP);   // blocks past the end have no weight
+#pragma unroll
+        for (int kk = 0; kk < kTP; ++kk)   // a block's 16 keys per MMA
+          if (kk < nv)
+            t5_mma_ts(tb + Cfg::kOCol, tb + Cfg::kVCol + bf * 64 + 8 * kk, t5_desc(p_smem + bf * kPBytes + kk * 2048, 16, 1024),
+                      idesc_pv, (!fresh || kk > 0) ? 1u : 0u);
+        t5_commit(&vop_empty[bf]);
+        t5_commit(&o_done[bf]);
+        --lp;
+        ++tp;
+      }
+      // every MMA issued has completed before TMEM can be released
+      t5_commit(&drain);
+      if (!mbar_wait(&drain, 0)) atomic_or_status(P.status, SV_DEV_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (warp >= kKWarp && warp < kLoadWarp) {
+    // ------------------------------------------------------ codes to TMEM --
+    regs_dec<kRegsOther>();
+    const int t = tid & 127;   // a key (K) or a head dim (V)
+    const uint32_t lanes = tb + ((uint32_t)((warp & 3) * 32) << 16);
+    auto role = [&](auto is_v) {
+      constexpr bool V = decltype(is_v)::value;
+      uint64_t *full = V ? vop_full : kop_full, *empty = V ? vop_empty : kop_empty;
+      const uint32_t col = lanes + (V ? Cfg::kVCol : Cfg::kKCol);
+      const int slot = t & 15, sw = (slot >> 1) & 3;
+      const uint32_t src0 = V ? ring + kTP * kRec + t * 8 : ring + (t >> 4) * kRec + slot * 64;
+      int st = 0, round = 0;
+      for (int u = 0; u < total; ++u) {
+        const int bf = u & 1;
+        bool ok = q4_wait(&raw_full[st], round & 1, abf, P.wait_ns);
+        uint32_t w[16];
+        const uint32_t src = src0 + st * kStage;
+        if constexpr (V) {
+#pragma unroll
+          for (int p = 0; p < kTP; ++p)
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[2 * p]), "=r"(w[2 * p + 1]) : "r"(src + p * kRec));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
+                         : "r"(src + ((c ^ sw) << 4)));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&raw_empty[st]);
+        if (ok && u >= 2) ok = q4_wait(&empty[bf], ((u >> 1) & 1) ^ 1, abf, P.wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        t5_fence_after();
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t o[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) spread<V>(w[4 * h + k], o + 4 * k);
+          t5_st16(col + bf * 64 + 16 * h, o);
+        }
+        t5_wait_st();
+        t5_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[bf]);
+        if (++st == kNS) {
+          st = 0;
+          ++round;
+        }
+      }
+    };
+    if (warp >= kVWarp) role(std::true_type{});
+    else role(std::false_type{});
+  } else if (warp < kKWarp) {
+    // ------------------------------------------------------------- softmax --
+    regs_inc<kRegsSoftmax>();
+    const int w = warp >> 2, t = tid & 127;
+    const int c_first = w * NC;                 // this warpgroup's columns
+    const int live = w ? rows - live0 : live0;
+    const int bar = 1 + w;
+    const uint32_t lanes = tb + ((uint32_t)((warp & 3) * 32) << 16);
+    // row of P' that this thread's key takes (the order of the codes)
+    const int prow = (t & ~7) | ((t & 3) << 1) | ((t >> 2) & 1);
+    const uint32_t pair_src = ring + (t >> 4) * kRec + kCodes + (t & 15) * 4;
+    Q4Walk wk = q4_walk(P, work);
+    Q4Item it;
+    int u = 0, i = 0, st = 0, round = 0;
+    // A wait that gave up (ok false) only shows at the warpgroup's next vote, so
+    // that its four warps leave together.
+    bool ok = true;
+    while (q4_next(P, wk, it)) {
+      const int buf = i & 1;
+      ok = __all_sync(0xffffffffu, q4_wait(&q_full[buf], (i >> 1) & 1, abf, P.wait_ns)) && ok;
+      const float sl2 = P.scale_log2, fold = sl2 * s_fold[buf];
+      const int L = it.span.L;
+      const int hid1 = P.window > 0 ? L - P.n_new - P.window : -1;   // keys in [sinks, hid1] are seen by no row
+      if (t < NC) s_nb[c_first + t] = t < live ? kUnset : -kUnset;   // (padding never moves)
+      float2 l2[NC / 2], b2[NC / 2];
+#pragma unroll
+      for (int k = 0; k < NC / 2; ++k) l2[k] = b2[k] = make_float2(0.f, 0.f);
+      if (bar_or(bar, 128, !ok)) break;
+      bool gone = false;
+      for (int ti = 0; ti < it.ntiles; ++ti, ++u) {
+        const int bf = u & 1;
+        const int key0 = (it.tile0 + ti) * kTK, key = key0 + t;
+        // this key's scales
+        ok = q4_wait(&raw_full[st], round & 1, abf, P.wait_ns) && ok;
+        uint32_t kp, vp;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kp) : "r"(pair_src + st * kStage));
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vp) : "r"(pair_src + st * kStage + kTP * kRec));
+        float ka = 0.f, kb = 0.f, vc = -INFINITY, vi = 0.f, vz = 0.f;
+        if (key < L && !(key >= P.sinks && key <= hid1)) {
+          const float2 k2 = __half22float2(*reinterpret_cast<const __half2 *>(&kp));
+          const float2 v2 = __half22float2(*reinterpret_cast<const __half2 *>(&vp));
+          const float vs = fmaxf(v2.x, 5.9604645e-8f);   // pages never written hold zeros
+          ka = k2.x * fold;
+          kb = k2.y * sl2;
+          vc = __log2f(vs);
+          vi = __fdividef(1.f, vs);
+          vz = fmaf(v2.y, vi, 8.f);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&raw_empty[st]);
+        if (++st == kNS) {
+          st = 0;
+          ++round;
+        }
+        // S of this tile, and the P' buffer that the last but one P V read
+        ok = q4_wait(&s_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
+        if (u >= 2) ok = q4_wait(&o_done[bf], ((u >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        t5_fence_after();
+        const bool edge = key0 + kTK - 1 > L - P.n_new || (P.window > 0 && key0 < L - P.window);
+        const float2 ka2 = make_float2(ka, ka), kb2 = make_float2(kb, kb), vc2 = make_float2(vc, vc);
+        const uint32_t s_col = lanes + Cfg::kSCol + bf * N + c_first;
+        float2 y[NC / 2];
+        auto scores = [&](bool with_ref) {   // log2 weights, minus the reference
+          uint32_t x[NC];
+          t5_ldn(s_col, x);
+          t5_wait_ld();
+#pragma unroll
+          for (int k = 0; k < NC; k += 4) {
+            const float4 qs = *reinterpret_cast<const float4 *>(&s_qs[buf][c_first + k]);
+            const float4 nb = with_ref ? *reinterpret_cast<const float4 *>(&s_nb[c_first + k]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float2 z0 = __ffma2_rn(make_float2(qs.x, qs.y), kb2, __fadd2_rn(vc2, make_float2(nb.x, nb.y)));
+            const float2 z1 = __ffma2_rn(make_float2(qs.z, qs.w), kb2, __fadd2_rn(vc2, make_float2(nb.z, nb.w)));
+            y[k / 2] = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), ka2, z0);
+            y[k / 2 + 1] = __ffma2_rn(make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), ka2, z1);
+          }
+          if (edge) {
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+              const int p = L - P.n_new + s_pos[buf][c_first + k];
+              if (key > p || (P.window > 0 && key >= P.sinks && key <= p - P.window)) {
+                if (k & 1) y[k / 2].y = -INFINITY;
+                else y[k / 2].x = -INFINITY;
+              }
+            }
+          }
+        };
+        scores(true);
+        // the reference moves when a weight exceeds it by more than 2^8 (f16
+        // holds 2^16); all four warps decide together, as they share O
+        float top = fmaxf(y[0].x, y[0].y);
+#pragma unroll
+        for (int k = 1; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[k].x), y[k].y);
+        if (bar_or(bar, 128, top > 8.f || !ok)) {
+          if (bar_or(bar, 128, !ok)) {
+            gone = true;
+            break;
+          }
+          scores(false);
+#pragma unroll
+          for (int k = 0; k < NC; ++k) {
+            const float m = warp_max((k & 1) ? y[k / 2].y : y[k / 2].x);
+            if (lane == 0) s_max[warp][k] = m;
+          }
+          named_bar_sync(bar, 128);
+          if (t < live) {
+            float m = s_max[4 * w][t];
+#pragma unroll
+            for (int k = 1; k < 4; ++k) m = fmaxf(m, s_max[4 * w + k][t]);
+            const float nb = s_nb[c_first + t];
+            const bool move = m + nb > 8.f;
+            s_a[c_first + t] = move ? ex2f(-nb - m) : 1.f;
+            if (move) s_nb[c_first + t] = -m;
+          } else if (t < NC) {
+            s_a[c_first + t] = 1.f;
+          }
+          named_bar_sync(bar, 128);
+#pragma unroll
+          for (int k = 0; k < NC / 2; ++k) {
+            const float2 a = *reinterpret_cast<const float2 *>(&s_a[c_first + 2 * k]);
+            l2[k] = __fmul2_rn(l2[k], a);
+            b2[k] = __fmul2_rn(b2[k], a);
+          }
+          if (ti > 0) {   // O too, once the previous P V has landed
+            ok = __all_sync(0xffffffffu, q4_wait(&o_done[bf ^ 1], ((u - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
+            t5_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < NC; k += 4) {
+              uint32_t o[4];
+              asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+                           : "r"(lanes + Cfg::kOCol + c_first + k));
+              t5_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s_a[c_first + k + e]);
+              asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(lanes + Cfg::kOCol + c_first + k),
+                           "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                           : "memory");
+            }
+            t5_wait_st();
+          }
+          scores(true);
+        }
+        const float2 vi2 = make_float2(vi, vi), vz2 = make_float2(vz, vz);
+        const uint32_t p_row = p_smem + bf * kPBytes + prow * 128;
+#pragma unroll
+        for (int c = 0; c < NC; c += 8) {
+          uint32_t ph[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int e = c / 2 + k;
+            const float2 p = make_float2(ex2f(y[e].x), ex2f(y[e].y));
+            l2[e] = __ffma2_rn(p, vi2, l2[e]);
+            b2[e] = __ffma2_rn(p, vz2, b2[e]);
+            ph[k] = pack2<true>(p.x, p.y);
+          }
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p_row + ((((c_first + c) >> 3) ^ (prow & 7)) << 4)),
+                       "r"(ph[0]), "r"(ph[1]), "r"(ph[2]), "r"(ph[3])
+                       : "memory");
+        }
+        if (gone) break;
+        fence_proxy_async_shared();
+        t5_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[bf]);
+      }
+      if (gone) break;
+      // ---- epilogue: sums over the keys, then a head dim per thread ---------
+      {
+        constexpr int NV = NC <= 8 ? 8 : (NC <= 16 ? 16 : 32);
+        float v[NV];
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+          for (int k = 0; k < NV; ++k) {
+            const float2 x = pass ? b2[(k < NC ? k : 0) / 2] : l2[(k < NC ? k : 0) / 2];
+            v[k] = k < NC ? ((k & 1) ? x.y : x.x) : 0.f;
+          }
+          const float s = warp_columns<NV>(v, lane);
+          const int c = lane / (32 / NV);
+          if (lane % (32 / NV) == 0 && c < NC) s_red[warp][c][pass] = s;
+        }
+      }
+      named_bar_sync(bar, 128);
+      const int64_t ent = 2 * (int64_t)blockIdx.x + (it.first ? 0 : 1);
+      if (t < live) {
+        float l = 0.f, b = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          l += s_red[4 * w + k][t][0];
+          b += s_red[4 * w + k][t][1];
+        }
+        // (a row of NaN stays NaN; l is 0 only for a row without keys, which a query that sees itself never is)
+        s_fin[c_first + t] = make_float2(it.whole ? 1.f / l : 1.f, b);
+        if (!it.whole) {
+          const int64_t e = ent * P.Rg + w * live0 + t;
+          P.ws_ml[2 * e] = -s_nb[c_first + t];
+          P.ws_ml[2 * e + 1] = l;
+        }
+      }
+      named_bar_sync(bar, 128);
+      ok = __all_sync(0xffffffffu, q4_wait(&o_done[(u - 1) & 1], ((u - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
+      t5_fence_after();
+#pragma unroll
+      for (int c0 = 0; c0 < NC; c0 += 8) {
+        uint32_t o[8];
+        t5_ld8(lanes + Cfg::kOCol + c_first + c0, o);
+        t5_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (c0 + k >= live || !ok) break;
+          const float2 f = s_fin[c_first + c0 + k];
+          const float x = (__uint_as_float(o[k]) + f.y) * f.x;
+          if (it.whole) {
+            static_cast<__nv_bfloat16 *>(P.out)[(int64_t)s_row[buf][c_first + c0 + k] * kD + t] = __float2bfloat16_rn(x);
+          } else {
+            P.ws_acc[(ent * P.Rg + w * live0 + c0 + k) * kD + t] = x;
+          }
+        }
+      }
+      t5_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&o_free);
+        mbar_arrive(&q_empty[buf]);
+      }
+      ++i;
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && *abf) atomic_or_status(P.status, SV_DEV_TIMEOUT);
+  t5_fence_after();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tb), "r"(512));
+}
+
+// Merge of the sequences that more than one range holds: CTA (range r, kv head
+// and row group, eight rows) leaves at once unless r's start is the first cut
+// of a sequence. Its pieces come from ranges r - 1 (the last item of its CTA,
+// or the first if that range starts with the sequence), r, r + 1, ... (first
+// items); a warp takes a row, lane l the head dims 4l .. 4l + 3, and loads
+// eight pieces at once.
+constexpr int kMergeWarps = 8;
+__global__ void __launch_bounds__(32 * kMergeWarps) attn_q4_merge_kernel(const __grid_constant__ Q4Params P) {
+  pdl_wait();
+  pdl_trigger();
+  const int Hp = P.H_kv * P.RG;
+  const int r = 1 + blockIdx.x / Hp, gp = blockIdx.x % Hp;
+  const int4 sp = P.ws_split[r];
+  if (sp.x < 0) return;
+  const int lane = threadIdx.x & 31;
+  const int g = gp / P.RG, row0 = (gp % P.RG) * P.Rg;
+  const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  if (row >= min(P.Rg, P.R - row0)) return;
+  const int64_t T = sp.w, A = sp.y, end = A + sp.z;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kMB = 8;
+  const int last = (int)((end * P.NR - 1) / T);   // the range that holds the last tile
+  // empty ranges before r hold nothing: the piece before the cut is that of the range with tile A
+  const int first = (int)(((A + 1) * P.NR - 1) / T);
+  for (int e0 = first; e0 <= last; e0 += kMB) {
+    float me[kMB], le[kMB];
+    float4 va[kMB];
+#pragma unroll
+    for (int k = 0; k < kMB; ++k) {
+      const int e = e0 + k;
+      const int64_t t0 = (int64_t)e * T / P.NR, t1 = (int64_t)(e + 1) * T / P.NR;
+      me[k] = -INFINITY;
+      le[k] = 0.f;
+      va[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (e <= last && t1 > t0) {
+        const int64_t at = (2 * ((int64_t)e * Hp + gp) + (t0 < A ? 1 : 0)) * P.Rg + row;
+        me[k] = P.ws_ml[2 * at];
+        le[k] = P.ws_ml[2 * at + 1];
+        va[k] = reinterpret_cast<const float4 *>(P.ws_acc + at * kD)[lane];
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < kMB; ++k) mn = fmaxf(mn, me[k]);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const float a = ex2f(m - base);
+    l *= a;
+    acc.x *= a; acc.y *= a; acc.z *= a; acc.w *= a;
+#pragma unroll
+    for (int k = 0; k < kMB; ++k) {
+      const float x = ex2f(me[k] - base);
+      l = fmaf(le[k], x, l);
+      acc.x = fmaf(va[k].x, x, acc.x);
+      acc.y = fmaf(va[k].y, x, acc.y);
+      acc.z = fmaf(va[k].z, x, acc.z);
+      acc.w = fmaf(va[k].w, x, acc.w);
+    }
+    m = mn;
+  }
+  const float inv = 1.f / l;
+  const int rr = row0 + row, j = rr / P.G;
+  const int64_t o = ((int64_t)sp.x * P.n_new + j) * P.H_q + g * P.G + (rr - j * P.G);
+  uint2 w;
+  w.x = pack2<false>(acc.x * inv, acc.y * inv);
+  w.y = pack2<false>(acc.z * inv, acc.w * inv);
+  reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(P.out) + o * kD)[lane] = w;
+}
+
+int q4_sms() {
+  static int n = 0;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 148;
+  });
+  return n;
+}
+
+struct Q4Plan {
+  bool tc;
+  int R, RG, Rg, NR, C;
+};
+
+Q4Plan q4_plan(int B, int n_new, int H_q, int H_kv, int d, int max_blocks, int bs, sv_dtype qd, int window, int sinks) {
+  Q4Plan p = {};
+  const int span = span_blocks_max(max_blocks, n_new, window, sinks, bs);
+  const int64_t tiles = (int64_t)std::max(B, 1) * ((span + kTP - 1) / kTP);
+  const int64_t R = (int64_t)n_new * (H_q / H_kv);
+  p.tc = qd == SV_BF16 && d == kD && bs == kBS && R <= 128 && tiles < (1ll << 30) &&
+         (int64_t)B * n_new * H_q < (1ll << 31);
+  if (!p.tc) return p;
+  p.R = (int)R;
+  p.RG = p.R > 64 ? 2 : 1;               // at most 64 query rows a CTA
+  p.Rg = (p.R + p.RG - 1) / p.RG;
+  const int64_t Hp = (int64_t)H_kv * p.RG;
+  p.NR = (int)std::max<int64_t>(1, std::min<int64_t>(q4_sms() / Hp, tiles));
+  p.C = (int)(p.NR * Hp);
+  return p;
+}
+
+size_t q4_ws_bytes(const Q4Plan &p) {
+  const size_t ent = (size_t)2 * p.C * p.Rg;
+  return align_up(ent * kD * sizeof(float), 256) + align_up(ent * 2 * sizeof(float), 256) +
+         align_up((size_t)p.NR * sizeof(int4), 256);
+}
+
+template <int NC>
+sv_status launch_q4(const Q4Params &P, int C, cudaStream_t st) {
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [] {
+    err = cudaFuncSetAttribute(attn_q4_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4Cfg<NC>::kSmem);
+  });
+  if (err != cudaSuccess) return fail(SV_ERR_CUDA, "spec_verify_attn_q4: cudaFuncSetAttribute: %s", cudaGetErrorString(err));
+  launch_k(attn_q4_kernel<NC>, dim3(C), dim3(32 * kWarps), Q4Cfg<NC>::kSmem, st, 1, P);
+  return check_launch("spec_verify_attn_q4 launch");
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" size_t spec_verify_attn_q4_workspace_size(int B, int n_new, int H_q, int H_kv, int d_head,
+                                                     int max_blocks_per_seq, int block_size, int window, int sinks) {
+  const size_t other = spec_verify_attn_window_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq,
+                                                              block_size, window, sinks);
+  if (other == 0) return 0;
+  if ((int64_t)window >= (int64_t)max_blocks_per_seq * block_size) window = sinks = 0;
+  const Q4Plan p = q4_plan(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size, SV_BF16, window, sinks);
+  // (queries in f32 run on the CUDA-core kernel whatever the shape)
+  return p.tc ? std::max(other, q4_ws_bytes(p)) : other;
+}
+
+extern "C" sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const void *k_cache, const void *v_cache,
+                                         const sv_kv_layout *layout, const int32_t *block_table,
+                                         int max_blocks_per_seq, const int32_t *seq_lens, int B, int n_new, int H_q,
+                                         int H_kv, int d_head, int block_size, int num_blocks, float softmax_scale,
+                                         int window, int sinks, void *out, sv_dtype out_dtype, void *workspace,
+                                         size_t workspace_bytes, int32_t *dev_status, sv_stream_t stream) {
+  if (window < 0 || sinks < 0) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_q4: negative window or sinks");
+  Q4Plan p = {};
+  const bool sizes_ok = B >= 0 && n_new >= 1 && H_q >= 1 && H_kv >= 1 && H_q % H_kv == 0 && num_blocks >= 1 &&
+                        max_blocks_per_seq >= 1 && H_kv <= 65535 && block_size >= 1;
+  int win = window, snk = sinks;
+  if ((int64_t)win >= (int64_t)max_blocks_per_seq * block_size) win = snk = 0;   // reaches every key
+  if (sizes_ok) p = q4_plan(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size, q_dtype, win, snk);
+  if (!p.tc || q_dtype != out_dtype)
+    return attn_cuda_core_q4(q, q_dtype, k_cache, v_cache, layout, block_table, max_blocks_per_seq, seq_lens, B, n_new,
+                             H_q, H_kv, d_head, block_size, num_blocks, softmax_scale, window, sinks, out, out_dtype,
+                             workspace, workspace_bytes, dev_status, stream);
+  if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out)
+    return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_q4: null pointer argument");
+  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
+    return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_q4: softmax_scale must be finite and > 0");
+  Q4Params P;
+  memset(&P, 0, sizeof(P));
+  const sv_status rc = q4_check("spec_verify_attn_q4", k_cache, v_cache, layout, H_kv, d_head, block_size,
+                                &P.block_stride, &P.head_stride);
+  if (rc != SV_OK) return rc;
+  const size_t need = q4_ws_bytes(p);
+  if (!workspace || workspace_bytes < need)
+    return fail(SV_ERR_WORKSPACE, "spec_verify_attn_q4: workspace needs %zu bytes", need);
+  if (!aligned(workspace, 256)) return fail(SV_ERR_WORKSPACE, "spec_verify_attn_q4: workspace not 256-byte aligned");
+  if (!aligned(q, 16) || !aligned(out, 16))
+    return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_q4: q and out must be 16-byte aligned");
+  if (B == 0) return ok();
+  const size_t ent = (size_t)2 * p.C * p.Rg;
+  P.q = q; P.out = out;
+  P.k_cache = static_cast<const uint8_t *>(k_cache); P.v_cache = static_cast<const uint8_t *>(v_cache);
+  P.block_table = block_table; P.seq_lens = seq_lens;
+  P.ws_acc = static_cast<float *>(workspace);
+  P.ws_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + align_up(ent * kD * sizeof(float), 256));
+  P.ws_split = reinterpret_cast<int4 *>(reinterpret_cast<uint8_t *>(P.ws_ml) + align_up(ent * 2 * sizeof(float), 256));
+  P.status = dev_status;
+  P.B = B; P.n_new = n_new; P.H_q = H_q; P.H_kv = H_kv; P.G = H_q / H_kv; P.R = p.R; P.Rg = p.Rg; P.RG = p.RG;
+  P.NR = p.NR; P.max_blocks = max_blocks_per_seq; P.num_blocks = num_blocks; P.window = win; P.sinks = snk;
+  P.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634074);
+  P.wait_ns = wait_limit_ns();
+  P.withhold = test_withhold();
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int half = (p.Rg + 1) / 2;   // rows of a softmax warpgroup
+  sv_status r2 = half <= 8 ? launch_q4<8>(P, p.C, st)
+                 : half <= 16 ? launch_q4<16>(P, p.C, st)
+                 : half <= 24 ? launch_q4<24>(P, p.C, st) : launch_q4<32>(P, p.C, st);
+  if (r2 != SV_OK || p.NR == 1) return r2;
+  launch_k(attn_q4_merge_kernel, dim3((p.NR - 1) * H_kv * p.RG, (p.Rg + kMergeWarps - 1) / kMergeWarps),
+           dim3(32 * kMergeWarps), 0, st, 1, P);
+  return check_launch("spec_verify_attn_q4 merge launch");
+}

@@ -80,4 +80,12 @@ constexpr sv_dtype kQ4 = static_cast<sv_dtype>(4);
 sv_status q4_check(const char *what, const void *k_cache, const void *v_cache, const sv_kv_layout *layout, int H_kv,
                    int d_head, int block_size, int64_t *block_stride, int64_t *head_stride);
 
+// spec_verify_attn_q4 on the CUDA-core kernel (attn.cu), for every shape and
+// type, with all its argument checks.
+sv_status attn_cuda_core_q4(const void *q, sv_dtype q_dtype, const void *k_cache, const void *v_cache,
+                            const sv_kv_layout *layout, const int32_t *block_table, int max_blocks_per_seq,
+                            const int32_t *seq_lens, int B, int n_new, int H_q, int H_kv, int d_head, int block_size,
+                            int num_blocks, float softmax_scale, int window, int sinks, void *out, sv_dtype out_dtype,
+                            void *workspace, size_t workspace_bytes, int32_t *dev_status, sv_stream_t stream);
+
 }  // namespace sv
