@@ -52,13 +52,14 @@ constexpr int kD = 128;                    // head dim
 constexpr int kBS = 16;                    // block size
 constexpr int kTP = 8;                     // blocks per tile
 constexpr int kTK = kTP * kBS;             // keys per tile
-constexpr int kRec = kBS * (kD / 2 + 4);   // record bytes
-constexpr int kCodes = kBS * kD / 2;
-constexpr int kStage = 2 * kTP * kRec;     // K records, then V records
-constexpr int kNS = 8;                     // stages of the record ring
+constexpr int kCodes = kBS * kD / 2;       // code bytes of a record
+constexpr int kStage = 2 * kTP * kCodes;   // codes of a tile: K, then V, 2 KB a warp that unpacks them
+constexpr int kNS = 8;                     // stages of the code ring
+constexpr int kPairs = 4;                  // stages of the softmax threads' own rings of (scale, minimum) pairs
+constexpr int kChunk = 8, kChunks = 4;     // tiles of a chunk of block numbers, and chunks in shared memory
 constexpr int kPBytes = kTK * 128;         // a P' buffer: 128 bytes (64 columns of f16) a key
 constexpr int kWarps = 20;
-constexpr int kKWarp = 8, kVWarp = 12, kLoadWarp = 16, kMmaWarp = 17, kQWarp = 18;
+constexpr int kKWarp = 8, kVWarp = 12, kPageWarp = 16, kMmaWarp = 17, kQWarp = 18;
 // Registers: launched at 96 a thread; the K, V and service warps hand over 32
 // each so that the softmax warps hold a tile's scores and two sums per column
 // (256 x 144 + 384 x 64 = 640 x 96).
@@ -88,9 +89,9 @@ template <int NC> struct Q4Cfg {   // NC columns per softmax warpgroup
   static constexpr int kN = 2 * NC;
   static constexpr int kQ = kN * 256;   // two head-dim halves of 128-byte rows
   static constexpr uint32_t kKCol = 0, kVCol = 128, kSCol = 256, kOCol = 256 + 2 * kN;
-  static constexpr int kSmem = 1024 + 2 * kQ + 2 * kPBytes + kNS * kStage;
+  static constexpr int kSmem = 1024 + 2 * kQ + 2 * kPBytes + kNS * kStage + kPairs * 2 * 256 * 4;
   static_assert(kOCol + kN <= 512, "TMEM columns");
-  static_assert(kSmem + 6144 <= 227 * 1024, "shared memory");
+  static_assert(kSmem + 7168 <= 227 * 1024, "shared memory");
 };
 
 // A sequence's part of a CTA's range.
@@ -199,11 +200,40 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool v) {
 }
 
 // Bounded wait; a wait that has to sleep gives up at once after any earlier
-// one of the CTA gave up.
+// one of the CTA gave up. Small on purpose, like everything in the tile loops
+// below: the five roles' code shares each scheduler's instruction cache, and
+// with unrolled unpacking and masking a fifth of the warps' time went into
+// fetching it.
 __device__ __forceinline__ bool q4_wait(uint64_t *bar, uint32_t phase, volatile int *abort_flag, uint64_t limit_ns) {
-  if (mbar_try_wait(bar, phase)) return true;
-  return t5_wait(bar, phase, abort_flag, limit_ns);
+  uint64_t t0 = 0;
+  while (!mbar_try_wait_sleep(bar, phase)) {
+    const uint64_t now = global_ns();
+    if (t0 == 0) t0 = now;
+    if (*abort_flag || now - t0 > limit_ns) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
 }
+
+// true in one lane of a converged warp, in a form that keeps the code around it
+// uniform for the compiler
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// n bytes (0: none, zeros are written) of a 16- or 4-byte asynchronous copy
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <int R> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
@@ -261,15 +291,21 @@ __device__ __forceinline__ void t5_ldn(uint32_t taddr, uint32_t (&r)[N]) {
 
 // Warps 0-3 and 4-7: softmax (a key per thread; each warpgroup half of the
 // query rows), later the epilogue (a head dim per thread). 8-11: K codes to
-// tensor memory. 12-15: V codes. 16: record copies. 17: MMA issue, owner of
-// the 512 TMEM columns (two K, two V, two S buffers and O). 18: Q of the next
-// sequence. 19: none (it completes the warpgroup).
+// tensor memory, 12-15: V codes. 16: block numbers of the tiles ahead. 17: MMA
+// issue, owner of the 512 TMEM columns (two K, two V, two S buffers and O).
+// 18, 19: Q of the next sequence.
+// Every warp copies what it reads: a K warp the two blocks that its keys lie
+// in, a V warp its 32 head dims of the tile's eight blocks, a softmax thread
+// the pairs of its key; so a copy is waited for by its own warp alone. (Bulk
+// copies of whole records were limited by their issue: 1088 bytes each, they
+// reached 2.9 TB/s from one warp and 4.8 TB/s from sixteen.)
 template <int NC>
 __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_constant__ Q4Params P) {
   using Cfg = Q4Cfg<NC>;
   constexpr int N = Cfg::kN;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t raw_full[kNS], raw_empty[kNS];
+  __shared__ __align__(8) uint64_t page_full[kChunks], page_empty[kChunks];
+  __shared__ int s_page[kChunks][kChunk][kTP];   // blocks of the tiles ahead; -1 past a sequence's end
   __shared__ __align__(8) uint64_t kop_full[2], kop_empty[2], vop_full[2], vop_empty[2];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2], o_free, drain;
   __shared__ uint32_t tmem_base;
@@ -278,7 +314,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   // per row of the two items in flight: sum(q), position (0 .. n_new - 1),
   // row of q and out; per item the power of two that undoes Q's scaling
   __shared__ __align__(16) float s_qs[2][N];
-  __shared__ int s_pos[2][N], s_row[2][N];
+  __shared__ __align__(16) int s_pos[2][N];
+  __shared__ int s_row[2][N];
   __shared__ float s_fold[2];
   __shared__ __align__(16) float s_nb[N], s_a[N];   // minus the reference; the last factor of a rescale
   __shared__ float s_max[8][NC], s_red[8][NC][2];
@@ -294,6 +331,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   const uint32_t q_smem = smem_u32(smem);
   const uint32_t p_smem = q_smem + 2 * Cfg::kQ;
   const uint32_t ring = p_smem + 2 * kPBytes;
+  const uint32_t pairs = ring + kNS * kStage;
 
   if (warp == 0) {
     // (the lengths are the caller's: read before the wait on the previous kernel)
@@ -303,9 +341,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     pdl_wait();   // the previous kernel may be a merge that still reads this workspace
     if (lane == 0 && gp == 0) P.ws_split[range] = split;
   } else if (tid == 32) {
-    for (int k = 0; k < kNS; ++k) {
-      mbar_init(&raw_full[k], 1);
-      mbar_init(&raw_empty[k], 16);   // the K, V and softmax warps
+    for (int k = 0; k < kChunks; ++k) {
+      mbar_init(&page_full[k], 1);
+      mbar_init(&page_empty[k], 16);   // the K, V and softmax warps
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(&kop_full[k], 4);
@@ -315,7 +353,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       mbar_init(&s_full[k], 1);
       mbar_init(&p_full[k], 8);
       mbar_init(&o_done[k], 1);
-      mbar_init(&q_full[k], 1);
+      mbar_init(&q_full[k], 2);
       mbar_init(&q_empty[k], 9);   // the softmax warps, and the last Q K^T
     }
     mbar_init(&o_free, 8);
@@ -338,81 +376,86 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   volatile int *abf = &abort_flag;
   // every stage, buffer and phase below follows the CTA's running tile count u
 
-  if (warp >= kLoadWarp) regs_dec<kRegsOther>();
-  if (warp == kLoadWarp) {
-    // ------------------------------------------------------------- records --
-    // Lane l copies block l / 2 of a tile, K (even) or V. The block table is
-    // read 32 entries at a time, one window and one sequence ahead.
+  // The blocks of tile u (u < total) for the copies of this warp; done with a
+  // chunk's last tile the warp hands the chunk back.
+  auto pages_of = [&](int u, bool &ok) -> const int * {
+    const int c = (u / kChunk) % kChunks;
+    if (u % kChunk == 0) ok = q4_wait(&page_full[c], (u / (kChunk * kChunks)) & 1, abf, P.wait_ns) && ok;
+    return s_page[c][u % kChunk];
+  };
+  auto pages_done = [&](int u) {
+    if (u % kChunk == kChunk - 1) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&page_empty[(u / kChunk) % kChunks]);
+    }
+  };
+
+  if (warp >= kPageWarp) regs_dec<kRegsOther>();
+  if (warp == kPageWarp) {
+    // ------------------------------------------------------- block numbers --
     Q4Walk wk = q4_walk(P, work);
-    Q4Item it, nx;
-    const int page = lane >> 1;
-    const bool mine = lane < 2 * kTP;
-    const uint8_t *pool = ((lane & 1) ? P.v_cache : P.k_cache) + (int64_t)g * P.head_stride;
-    const uint32_t dst0 = (lane & 1) * (kTP * kRec) + page * kRec;
-    auto entry = [&](const Q4Item &i, int v) {   // table entry of block v of the span
-      return v < min(i.span.nblk, (i.tile0 + i.ntiles) * kTP)
-                 ? P.block_table[(int64_t)i.b * P.max_blocks + (v < i.span.nsb ? v : v + i.span.skip)]
-                 : 0;
-    };
-    int u = 0, st = 0, round = 0;
-    bool go = !(P.withhold & SV_TEST_WITHHOLD_COPIES);
+    Q4Item it;
     bool have = q4_next(P, wk, it);
-    int cur = have ? entry(it, it.tile0 * kTP + lane) : 0;
-    while (go && have) {
-      const bool more = q4_next(P, wk, nx);
-      const int v0 = it.tile0 * kTP;
-      int ahead = entry(it, v0 + 32 + lane);
-      const int cur_nx = more ? entry(nx, nx.tile0 * kTP + lane) : 0;
-      for (int ti = 0; ti < it.ntiles; ++ti, ++u) {
-        if (ti > 0 && (ti & 3) == 0) {
-          cur = ahead;
-          ahead = entry(it, v0 + ti * kTP + 32 + lane);
+    int ti = 0;   // next tile of the item
+    for (int c = 0; c * kChunk < total; ++c) {
+      if (c >= kChunks &&
+          !__all_sync(0xffffffffu, q4_wait(&page_empty[c % kChunks], ((c / kChunks) & 1) ^ 1, abf, P.wait_ns)))
+        break;
+      for (int filled = 0; filled < kChunk && have;) {
+        const int n = min(kChunk - filled, it.ntiles - ti);
+        const int32_t *table = P.block_table + (int64_t)it.b * P.max_blocks;
+        int phys[kChunk * kTP / 32];
+#pragma unroll
+        for (int k = 0; k < kChunk * kTP / 32; ++k) {
+          const int e = lane + 32 * k, v = (it.tile0 + ti) * kTP + e;
+          phys[k] = e < n * kTP && v < it.span.nblk ? table[v < it.span.nsb ? v : v + it.span.skip] : -2;
         }
-        int phys = __shfl_sync(0xffffffffu, cur, ((ti & 3) * kTP + page) & 31);
-        if (round > 0) go = __all_sync(0xffffffffu, q4_wait(&raw_empty[st], (round & 1) ^ 1, abf, P.wait_ns));
-        if (!go) break;
-        const int nv = min(kTP, it.span.nblk - (it.tile0 + ti) * kTP);
-        if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], (uint32_t)(nv * 2 * kRec));
-        __syncwarp();
-        if (mine && page < nv) {
-          if (phys < 0 || phys >= P.num_blocks) {
+#pragma unroll
+        for (int k = 0; k < kChunk * kTP / 32; ++k) {
+          const int e = lane + 32 * k;
+          if (e >= n * kTP) continue;
+          int ph = phys[k];
+          if (ph == -2 && (it.tile0 + ti) * kTP + e >= it.span.nblk) {
+            ph = -1;
+          } else if (ph < 0 || ph >= P.num_blocks) {
             atomic_or_status(P.status, SV_DEV_BAD_BLOCK);
-            phys = 0;   // stay in bounds; the output of this sequence is flagged
+            ph = 0;   // stay in bounds; the output of this sequence is flagged
           }
-          bulk_g2s(smem + (ring - q_smem) + st * kStage + dst0, pool + (int64_t)phys * P.block_stride, kRec, &raw_full[st]);
+          s_page[c % kChunks][filled + e / kTP][e % kTP] = ph;
         }
-        if (++st == kNS) {
-          st = 0;
-          ++round;
+        filled += n;
+        ti += n;
+        if (ti == it.ntiles) {
+          have = q4_next(P, wk, it);
+          ti = 0;
         }
       }
-      it = nx;
-      cur = cur_nx;
-      have = more;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&page_full[c % kChunks]);
     }
-    // the copies in flight land before the CTA may exit
-    if (lane == 0)
-      for (int t = max(0, u - kNS); t < u; ++t)
-        if (!mbar_wait(&raw_full[t % kNS], (t / kNS) & 1)) atomic_or_status(P.status, SV_DEV_TIMEOUT);
-  } else if (warp == kQWarp) {
+  } else if (warp >= kQWarp) {
     // ------------------------------------------------------------------- Q --
     // Row by row to f16, scaled by one power of two that brings the largest
     // finite element of the CTA's rows to [2^14, 2^15): bf16 values are then
-    // exact down to 2^-28 of it.
+    // exact down to 2^-28 of it. Both warps look for the largest element; each
+    // converts half of the rows.
     Q4Walk wk = q4_walk(P, work);
     Q4Item it;
     int i = 0;
+    const uint32_t inv_g = (65536u + P.G - 1) / P.G;
     while (q4_next(P, wk, it)) {
       const int buf = i & 1;
       if (i >= 2 && !__all_sync(0xffffffffu, q4_wait(&q_empty[buf], ((i >> 1) & 1) ^ 1, abf, P.wait_ns))) break;
       const int c8 = lane & 15;
+      // r / G without a division: exact for r < 128, G <= 128
+      auto pos_of = [&](int r) { return (int)(((uint32_t)r * inv_g) >> 16); };
       auto row_of = [&](int col) {   // query row of a column, -1 for padding
         const int w = col / NC, c = col - w * NC;
         const int r = w * live0 + c;
         return c < (w ? rows - live0 : live0) ? row0 + r : -1;
       };
       auto q_row = [&](int r) {   // its row in q and out
-        const int j = r / P.G;
+        const int j = pos_of(r);
         return (it.b * P.n_new + j) * P.H_q + g * P.G + (r - j * P.G);
       };
       const uint4 *q = static_cast<const uint4 *>(P.q);
@@ -434,7 +477,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       const int ex = min(117, max(-113, (int)(top >> 23) - 127));   // (both powers stay normal)
       const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
 #pragma unroll 2
-      for (int c0 = 0; c0 < N; c0 += 2) {
+      for (int c0 = 2 * (warp - kQWarp); c0 < N; c0 += 4) {
         const int col = c0 + (lane >> 4);
         const int r = row_of(col);
         const uint4 v = r >= 0 ? q[(int64_t)q_row(r) * 16 + c8] : make_uint4(0u, 0u, 0u, 0u);
@@ -457,12 +500,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
                      : "memory");
         if (c8 == 0) {
           s_qs[buf][col] = sum;
-          s_pos[buf][col] = r >= 0 ? r / P.G : 0;
+          s_pos[buf][col] = r >= 0 ? pos_of(r) : 0;
           s_row[buf][col] = r >= 0 ? q_row(r) : 0;
         }
       }
       // 2^-24 of the codes and 2^(14 - ex) of Q
-      if (lane == 0) s_fold[buf] = __uint_as_float((uint32_t)(127 + 10 + ex) << 23);
+      if (lane == 0 && warp == kQWarp) s_fold[buf] = __uint_as_float((uint32_t)(127 + 10 + ex) << 23);
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[buf]);
@@ -470,115 +513,139 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     }
   } else if (warp == kMmaWarp) {
     // ----------------------------------------------------------------- MMA --
-    if (lane == 0 && total > 0) {
-      // f16 A and B, f32 accumulators, M = 128
-      constexpr uint32_t idesc_qk = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
-      constexpr uint32_t idesc_pv = idesc_qk | (1u << 16);   // B = P'^T with the rows contiguous
-      Q4Walk wq = q4_walk(P, work), wp = wq;
-      Q4Item iq, ip;
-      int nq = 0, np = 0;          // items started
-      int lq = 0, lp = 0, tp = 0;  // tiles left in the current item; its next P V tile
-      auto qk = [&](int u) {
-        const int bf = u & 1;
+    // The whole warp walks the tiles, one lane issues. Q K^T of tile u + 1 goes
+    // ahead of P V of tile u; as a commit covers everything issued before it,
+    // S of tile u being there also means that P V of tile u - 2 is done.
+    // f16 A and B, f32 accumulators, M = 128
+    constexpr uint32_t idesc_qk = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+    constexpr uint32_t idesc_pv = idesc_qk | (1u << 16);   // B = P'^T with the rows contiguous
+    Q4Walk wq = q4_walk(P, work), wp = wq;
+    Q4Item iq, ip;
+    int nq = 0, np = 0;          // items started
+    int lq = 0, lp = 0, tp = 0;  // tiles left in the current item; its next P V tile
+    for (int u = -1; u < total; ++u) {
+      if (u + 1 < total) {
+        const int bf = (u + 1) & 1;
+        bool ok = true;
         if (lq == 0) {
           q4_next(P, wq, iq);
           lq = iq.ntiles;
-          if (!q4_wait(&q_full[nq & 1], (nq >> 1) & 1, abf, P.wait_ns)) return false;
+          ok = q4_wait(&q_full[nq & 1], (nq >> 1) & 1, abf, P.wait_ns);
           ++nq;
         }
-        if (!q4_wait(&kop_full[bf], (u >> 1) & 1, abf, P.wait_ns)) return false;
+        ok = q4_wait(&kop_full[bf], ((u + 1) >> 1) & 1, abf, P.wait_ns) && ok;
+        if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
-        const uint32_t qb = q_smem + ((nq - 1) & 1) * Cfg::kQ;
+        --lq;
+        if (elect_one()) {
+          const uint64_t qd = t5_desc(q_smem + ((nq - 1) & 1) * Cfg::kQ, 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)   // 16 head dims per MMA
-          t5_mma_ts(tb + Cfg::kSCol + bf * N, tb + Cfg::kKCol + bf * 64 + 8 * kk,
-                    t5_desc(qb + (kk >> 2) * (N * 128) + (kk & 3) * 32, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
-        t5_commit(&s_full[bf]);
-        t5_commit(&kop_empty[bf]);
-        if (--lq == 0) t5_commit(&q_empty[(nq - 1) & 1]);
-        return true;
-      };
-      bool okm = qk(0);
-      for (int u = 0; okm && u < total; ++u) {
-        if (u + 1 < total && !qk(u + 1)) break;
-        const int bf = u & 1;
-        const bool fresh = lp == 0;
-        if (fresh) {
-          q4_next(P, wp, ip);
-          lp = ip.ntiles;
-          tp = ip.tile0;
-          // the previous item's O has been read
-          if (np > 0 && !q4_wait(&o_free, (np - 1) & 1, abf, P.wait_ns)) break;
-          ++np;
+          for (int kk = 0; kk < 8; ++kk)   // 16 head dims per MMA, two halves of four
+            t5_mma_ts(tb + Cfg::kSCol + bf * N, tb + Cfg::kKCol + bf * 64 + 8 * kk,
+                      qd + (kk >> 2) * (N * 128 / 16) + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
+          t5_commit(&s_full[bf]);
+          t5_commit(&kop_empty[bf]);
+          if (lq == 0) t5_commit(&q_empty[(nq - 1) & 1]);
         }
-        if (!q4_wait(&vop_full[bf], (u >> 1) & 1, abf, P.wait_ns)) break;
-        if (!q4_wait(&p_full[bf], (u >> 1) & 1, abf, P.wait_ns)) break;
-        t5_fence_after();
+        __syncwarp();
+      }
+      if (u < 0) continue;
+      const int bf = u & 1;
+      const bool fresh = lp == 0;
+      bool ok = true;
+      if (fresh) {
+        q4_next(P, wp, ip);
+        lp = ip.ntiles;
+        tp = ip.tile0;
+        // the previous item's O has been read
+        if (np > 0) ok = q4_wait(&o_free, (np - 1) & 1, abf, P.wait_ns);
+        ++np;
+      }
+      ok = q4_wait(&vop_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
+      ok = q4_wait(&p_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
+      if (!__all_sync(0xffffffffu, ok)) break;
+      t5_fence_after();
+      if (elect_one()) {
         const int nv = min(kTP, ip.span.nblk - tp * kTP);   // blocks past the end have no weight
+        const uint64_t pd = t5_desc(p_smem + bf * kPBytes, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < kTP; ++kk)   // a block's 16 keys per MMA
           if (kk < nv)
-            t5_mma_ts(tb + Cfg::kOCol, tb + Cfg::kVCol + bf * 64 + 8 * kk, t5_desc(p_smem + bf * kPBytes + kk * 2048, 16, 1024),
-                      idesc_pv, (!fresh || kk > 0) ? 1u : 0u);
+            t5_mma_ts(tb + Cfg::kOCol, tb + Cfg::kVCol + bf * 64 + 8 * kk, pd + kk * (2048 / 16), idesc_pv,
+                      (!fresh || kk > 0) ? 1u : 0u);
         t5_commit(&vop_empty[bf]);
         t5_commit(&o_done[bf]);
-        --lp;
-        ++tp;
       }
-      // every MMA issued has completed before TMEM can be released
-      t5_commit(&drain);
-      if (!mbar_wait(&drain, 0)) atomic_or_status(P.status, SV_DEV_TIMEOUT);
+      __syncwarp();
+      --lp;
+      ++tp;
     }
-    __syncwarp();
-  } else if (warp >= kKWarp && warp < kLoadWarp) {
+    // every MMA issued has completed before TMEM can be released
+    if (total > 0) {
+      if (elect_one()) t5_commit(&drain);
+      __syncwarp();
+      if (!mbar_wait(&drain, 0) && lane == 0) atomic_or_status(P.status, SV_DEV_TIMEOUT);
+    }
+  } else if (warp >= kKWarp && warp < kPageWarp) {
     // ------------------------------------------------------ codes to TMEM --
     regs_dec<kRegsOther>();
-    const int t = tid & 127;   // a key (K) or a head dim (V)
     const uint32_t lanes = tb + ((uint32_t)((warp & 3) * 32) << 16);
     auto role = [&](auto is_v) {
       constexpr bool V = decltype(is_v)::value;
       uint64_t *full = V ? vop_full : kop_full, *empty = V ? vop_empty : kop_empty;
       const uint32_t col = lanes + (V ? Cfg::kVCol : Cfg::kKCol);
-      const int slot = t & 15, sw = (slot >> 1) & 3;
-      const uint32_t src0 = V ? ring + kTP * kRec + t * 8 : ring + (t >> 4) * kRec + slot * 64;
-      int st = 0, round = 0;
-      for (int u = 0; u < total; ++u) {
-        const int bf = u & 1;
-        bool ok = q4_wait(&raw_full[st], round & 1, abf, P.wait_ns);
-        uint32_t w[16];
-        const uint32_t src = src0 + st * kStage;
-        if constexpr (V) {
+      const int slot = lane & 15, sw = (slot >> 1) & 3;
+      const uint8_t *pool = (V ? P.v_cache : P.k_cache) + (int64_t)g * P.head_stride;
+      const uint32_t mine = ring + (warp - kKWarp) * 2048;   // this warp's part of a stage
+      bool ok = true;
+      auto issue = [&](int u) {
+        if (u < total) {
+          const int *pg = pages_of(u, ok);
+          const uint32_t dst = mine + (u % kNS) * kStage + lane * 16;
 #pragma unroll
-          for (int p = 0; p < kTP; ++p)
-            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[2 * p]), "=r"(w[2 * p + 1]) : "r"(src + p * kRec));
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
-                         : "r"(src + ((c ^ sw) << 4)));
+          for (int j = 0; j < 4; ++j) {
+            // K: half a block of keys per copy; V: 32 head dims of two blocks
+            // (block numbers that never came are not read)
+            const int ph = ok ? pg[V ? 2 * j + (lane >> 4) : 2 * (warp & 3) + (j >> 1)] : -1;
+            const int off = V ? (warp & 3) * 256 + (lane & 15) * 16 : (j & 1) * 512 + lane * 16;
+            copy16(dst + j * 512, pool + (int64_t)max(ph, 0) * P.block_stride + off, ph >= 0 ? 16 : 0);
+          }
+          pages_done(u);
         }
+        copies_commit();
+      };
+      const bool run = !(P.withhold & SV_TEST_WITHHOLD_COPIES);
+      for (int u = 1 - kNS; run && u < total; ++u) {
+        issue(u + kNS - 1);
+        if (u < 0) continue;
+        const int bf = u & 1;
+        copies_wait<kNS - 1>();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&raw_empty[st]);
         if (ok && u >= 2) ok = q4_wait(&empty[bf], ((u >> 1) & 1) ^ 1, abf, P.wait_ns);
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
+        const uint32_t src = mine + (u % kNS) * kStage + (V ? lane * 8 : lane * 64);
+#pragma unroll 1
+        for (int h = 0; h < 4; ++h) {   // K: 32 head dims of a key; V: 32 keys of a head dim
+          uint32_t w[4], o[16];
+          if constexpr (V) {
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src + h * 512));
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[2]), "=r"(w[3]) : "r"(src + h * 512 + 256));
+          } else {
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(src + ((h ^ sw) << 4)));
+          }
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t o[16];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) spread<V>(w[4 * h + k], o + 4 * k);
+          for (int k = 0; k < 4; ++k) spread<V>(w[k], o + 4 * k);
           t5_st16(col + bf * 64 + 16 * h, o);
         }
         t5_wait_st();
         t5_fence_before();
-        __syncwarp();
+        __syncwarp();   // (every lane has read its codes: the stage is refilled next)
         if (lane == 0) mbar_arrive(&full[bf]);
-        if (++st == kNS) {
-          st = 0;
-          ++round;
-        }
       }
+      copies_wait<0>();
     };
     if (warp >= kVWarp) role(std::true_type{});
     else role(std::false_type{});
@@ -592,19 +659,33 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     const uint32_t lanes = tb + ((uint32_t)((warp & 3) * 32) << 16);
     // row of P' that this thread's key takes (the order of the codes)
     const int prow = (t & ~7) | ((t & 3) << 1) | ((t >> 2) & 1);
-    const uint32_t pair_src = ring + (t >> 4) * kRec + kCodes + (t & 15) * 4;
+    // this thread's ring of pairs: (K, V) of its key in the tiles ahead
+    const uint32_t my_pairs = pairs + tid * 4;
+    const int64_t pair_off = (int64_t)g * P.head_stride + kCodes + (t & 15) * 4;
     Q4Walk wk = q4_walk(P, work);
     Q4Item it;
-    int u = 0, i = 0, st = 0, round = 0;
+    int u = 0, i = 0;
     // A wait that gave up (ok false) only shows at the warpgroup's next vote, so
     // that its four warps leave together.
     bool ok = true;
+    auto issue = [&](int v) {
+      if (v < total) {
+        const int *pg = pages_of(v, ok);
+        const int ph = ok ? pg[t >> 4] : -1;
+        const int64_t off = (int64_t)max(ph, 0) * P.block_stride + pair_off;
+        const uint32_t dst = my_pairs + (v % kPairs) * 2048;
+        copy4(dst, P.k_cache + off, ph >= 0 ? 4 : 0);
+        copy4(dst + 1024, P.v_cache + off, ph >= 0 ? 4 : 0);
+        pages_done(v);
+      }
+      copies_commit();
+    };
+    for (int v = 0; v < kPairs - 1; ++v) issue(v);
     while (q4_next(P, wk, it)) {
       const int buf = i & 1;
       ok = __all_sync(0xffffffffu, q4_wait(&q_full[buf], (i >> 1) & 1, abf, P.wait_ns)) && ok;
       const float sl2 = P.scale_log2, fold = sl2 * s_fold[buf];
       const int L = it.span.L;
-      const int hid1 = P.window > 0 ? L - P.n_new - P.window : -1;   // keys in [sinks, hid1] are seen by no row
       if (t < NC) s_nb[c_first + t] = t < live ? kUnset : -kUnset;   // (padding never moves)
       float2 l2[NC / 2], b2[NC / 2];
 #pragma unroll
@@ -615,44 +696,39 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         const int bf = u & 1;
         const int key0 = (it.tile0 + ti) * kTK, key = key0 + t;
         // this key's scales
-        ok = q4_wait(&raw_full[st], round & 1, abf, P.wait_ns) && ok;
+        issue(u + kPairs - 1);
+        copies_wait<kPairs - 1>();
         uint32_t kp, vp;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kp) : "r"(pair_src + st * kStage));
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vp) : "r"(pair_src + st * kStage + kTP * kRec));
-        float ka = 0.f, kb = 0.f, vc = -INFINITY, vi = 0.f, vz = 0.f;
-        if (key < L && !(key >= P.sinks && key <= hid1)) {
-          const float2 k2 = __half22float2(*reinterpret_cast<const __half2 *>(&kp));
-          const float2 v2 = __half22float2(*reinterpret_cast<const __half2 *>(&vp));
-          const float vs = fmaxf(v2.x, 5.9604645e-8f);   // pages never written hold zeros
-          ka = k2.x * fold;
-          kb = k2.y * sl2;
-          vc = __log2f(vs);
-          vi = __fdividef(1.f, vs);
-          vz = fmaf(v2.y, vi, 8.f);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&raw_empty[st]);
-        if (++st == kNS) {
-          st = 0;
-          ++round;
-        }
-        // S of this tile, and the P' buffer that the last but one P V read
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kp) : "r"(my_pairs + (u % kPairs) * 2048));
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vp) : "r"(my_pairs + (u % kPairs) * 2048 + 1024));
+        const float2 k2 = __half22float2(*reinterpret_cast<const __half2 *>(&kp));
+        const float2 v2 = __half22float2(*reinterpret_cast<const __half2 *>(&vp));
+        const float vs = fmaxf(v2.x, 5.9604645e-8f);   // (pages never written hold zeros)
+        const float ka = k2.x * fold, kb = k2.y * sl2, vc = __log2f(vs);
+        float vi = __fdividef(1.f, vs), vz = fmaf(v2.y, vi, 8.f);
+        // A tile that ends past the oldest query or holds keys that a window
+        // has left: position j sees the key iff 0 <= j - j0 < reach. A key that
+        // no position sees (past the end, or between sinks and window) may hold
+        // anything.
+        const bool edge = key0 + kTK - 1 > L - P.n_new || (P.window > 0 && key0 < L - P.window);
+        const int j0 = key - (L - P.n_new);
+        const uint32_t reach = P.window > 0 && key >= P.sinks ? (uint32_t)P.window : 0x80000000u;
+        if (edge && (key >= L || (uint32_t)(P.n_new - 1 - j0) >= reach + (uint32_t)(P.n_new - 1))) vi = vz = 0.f;
+        // S of this tile (and with it the P' buffer, read by the last but one P V)
         ok = q4_wait(&s_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
-        if (u >= 2) ok = q4_wait(&o_done[bf], ((u >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
         ok = __all_sync(0xffffffffu, ok);
         t5_fence_after();
-        const bool edge = key0 + kTK - 1 > L - P.n_new || (P.window > 0 && key0 < L - P.window);
         const float2 ka2 = make_float2(ka, ka), kb2 = make_float2(kb, kb), vc2 = make_float2(vc, vc);
         const uint32_t s_col = lanes + Cfg::kSCol + bf * N + c_first;
-        float2 y[NC / 2];
-        auto scores = [&](bool with_ref) {   // log2 weights, minus the reference
+        float2 y[NC / 2];   // log2 weights, minus the reference
+        for (int again = 0;; ++again) {
           uint32_t x[NC];
           t5_ldn(s_col, x);
           t5_wait_ld();
 #pragma unroll
           for (int k = 0; k < NC; k += 4) {
             const float4 qs = *reinterpret_cast<const float4 *>(&s_qs[buf][c_first + k]);
-            const float4 nb = with_ref ? *reinterpret_cast<const float4 *>(&s_nb[c_first + k]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 nb = *reinterpret_cast<const float4 *>(&s_nb[c_first + k]);
             const float2 z0 = __ffma2_rn(make_float2(qs.x, qs.y), kb2, __fadd2_rn(vc2, make_float2(nb.x, nb.y)));
             const float2 z1 = __ffma2_rn(make_float2(qs.z, qs.w), kb2, __fadd2_rn(vc2, make_float2(nb.z, nb.w)));
             y[k / 2] = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), ka2, z0);
@@ -660,71 +736,74 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           }
           if (edge) {
 #pragma unroll
-            for (int k = 0; k < NC; ++k) {
-              const int p = L - P.n_new + s_pos[buf][c_first + k];
-              if (key > p || (P.window > 0 && key >= P.sinks && key <= p - P.window)) {
-                if (k & 1) y[k / 2].y = -INFINITY;
-                else y[k / 2].x = -INFINITY;
-              }
+            for (int k = 0; k < NC; k += 4) {
+              const int4 j = *reinterpret_cast<const int4 *>(&s_pos[buf][c_first + k]);
+              if ((uint32_t)(j.x - j0) >= reach) y[k / 2].x = -INFINITY;
+              if ((uint32_t)(j.y - j0) >= reach) y[k / 2].y = -INFINITY;
+              if ((uint32_t)(j.z - j0) >= reach) y[k / 2 + 1].x = -INFINITY;
+              if ((uint32_t)(j.w - j0) >= reach) y[k / 2 + 1].y = -INFINITY;
             }
           }
-        };
-        scores(true);
-        // the reference moves when a weight exceeds it by more than 2^8 (f16
-        // holds 2^16); all four warps decide together, as they share O
-        float top = fmaxf(y[0].x, y[0].y);
+          if (again) break;
+          // the reference moves when a weight exceeds it by more than 2^8 (f16
+          // holds 2^16); all four warps decide together, as they share O
+          float top = fmaxf(y[0].x, y[0].y);
 #pragma unroll
-        for (int k = 1; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[k].x), y[k].y);
-        if (bar_or(bar, 128, top > 8.f || !ok)) {
+          for (int k = 1; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[k].x), y[k].y);
+          if (!bar_or(bar, 128, top > 8.f || !ok)) break;
           if (bar_or(bar, 128, !ok)) {
             gone = true;
             break;
           }
-          scores(false);
-#pragma unroll
-          for (int k = 0; k < NC; ++k) {
-            const float m = warp_max((k & 1) ? y[k / 2].y : y[k / 2].x);
-            if (lane == 0) s_max[warp][k] = m;
+          // each column's largest weight, without the reference
+#pragma unroll 1
+          for (int k = 0; k < live; ++k) {
+            uint32_t xs;
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(xs) : "r"(s_col + k));
+            t5_wait_ld();
+            float z = fmaf(__uint_as_float(xs), ka, fmaf(s_qs[buf][c_first + k], kb, vc));
+            if (edge && (uint32_t)(s_pos[buf][c_first + k] - j0) >= reach) z = -INFINITY;
+            z = warp_max(z);
+            if (lane == 0) s_max[warp][k] = z;
           }
           named_bar_sync(bar, 128);
-          if (t < live) {
-            float m = s_max[4 * w][t];
-#pragma unroll
-            for (int k = 1; k < 4; ++k) m = fmaxf(m, s_max[4 * w + k][t]);
-            const float nb = s_nb[c_first + t];
-            const bool move = m + nb > 8.f;
-            s_a[c_first + t] = move ? ex2f(-nb - m) : 1.f;
-            if (move) s_nb[c_first + t] = -m;
-          } else if (t < NC) {
-            s_a[c_first + t] = 1.f;
+          if (t < NC) {
+            float a = 1.f;
+            if (t < live) {
+              const float m = fmaxf(fmaxf(s_max[4 * w][t], s_max[4 * w + 1][t]), fmaxf(s_max[4 * w + 2][t], s_max[4 * w + 3][t]));
+              const float nb = s_nb[c_first + t];
+              if (m + nb > 8.f) {
+                a = ex2f(-nb - m);
+                s_nb[c_first + t] = -m;
+              }
+            }
+            s_a[c_first + t] = a;
           }
           named_bar_sync(bar, 128);
 #pragma unroll
-          for (int k = 0; k < NC / 2; ++k) {
-            const float2 a = *reinterpret_cast<const float2 *>(&s_a[c_first + 2 * k]);
-            l2[k] = __fmul2_rn(l2[k], a);
-            b2[k] = __fmul2_rn(b2[k], a);
+          for (int k = 0; k < NC; k += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(&s_a[c_first + k]);
+            l2[k / 2] = __fmul2_rn(l2[k / 2], make_float2(a.x, a.y));
+            b2[k / 2] = __fmul2_rn(b2[k / 2], make_float2(a.x, a.y));
+            l2[k / 2 + 1] = __fmul2_rn(l2[k / 2 + 1], make_float2(a.z, a.w));
+            b2[k / 2 + 1] = __fmul2_rn(b2[k / 2 + 1], make_float2(a.z, a.w));
           }
           if (ti > 0) {   // O too, once the previous P V has landed
             ok = __all_sync(0xffffffffu, q4_wait(&o_done[bf ^ 1], ((u - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
             t5_fence_after();
 #pragma unroll 1
-            for (int k = 0; k < NC; k += 4) {
-              uint32_t o[4];
-              asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-                           : "r"(lanes + Cfg::kOCol + c_first + k));
+            for (int k = 0; k < live; ++k) {
+              uint32_t o;
+              const uint32_t at = lanes + Cfg::kOCol + c_first + k;
+              asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o) : "r"(at));
               t5_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s_a[c_first + k + e]);
-              asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(lanes + Cfg::kOCol + c_first + k),
-                           "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                           : "memory");
+              o = __float_as_uint(__uint_as_float(o) * s_a[c_first + k]);
+              asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(at), "r"(o) : "memory");
             }
             t5_wait_st();
           }
-          scores(true);
         }
+        if (gone) break;
         const float2 vi2 = make_float2(vi, vi), vz2 = make_float2(vz, vz);
         const uint32_t p_row = p_smem + bf * kPBytes + prow * 128;
 #pragma unroll
@@ -742,7 +821,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
                        "r"(ph[0]), "r"(ph[1]), "r"(ph[2]), "r"(ph[3])
                        : "memory");
         }
-        if (gone) break;
         fence_proxy_async_shared();
         t5_fence_before();
         __syncwarp();
