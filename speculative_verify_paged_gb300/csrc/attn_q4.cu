@@ -64,6 +64,7 @@ constexpr int kKWarp = 8, kVWarp = 12, kPageWarp = 16, kMmaWarp = 17, kQWarp = 1
 // each so that the softmax warps hold a tile's scores and two sums per column
 // (256 x 144 + 384 x 64 = 640 x 96).
 constexpr int kRegsSoftmax = 144, kRegsOther = 64;
+constexpr int kNapShort = 20, kNap = 60, kNapLong = 400;   // between the tries of a wait (ns)
 constexpr float kUnset = 1e30f;            // minus the reference of a row that has met no key
 
 struct Q4Params {
@@ -200,21 +201,30 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool v) {
 }
 
 // Bounded wait; a wait that has to sleep gives up at once after any earlier
-// one of the CTA gave up. Small on purpose, like everything in the tile loops
-// below: the five roles' code shares each scheduler's instruction cache, and
-// with unrolled unpacking and masking a fifth of the warps' time went into
-// fetching it.
+// one of the CTA gave up. It sleeps NS nanoseconds between its tries: try_wait
+// comes back after some hundred cycles whatever its time hint, and trying
+// again at once, the warps that wait take issue slots from those that work.
+template <int NS>
 __device__ __forceinline__ bool q4_wait(uint64_t *bar, uint32_t phase, volatile int *abort_flag, uint64_t limit_ns) {
-  uint64_t t0 = 0;
-  while (!mbar_try_wait_sleep(bar, phase)) {
-    const uint64_t now = global_ns();
-    if (t0 == 0) t0 = now;
-    if (*abort_flag || now - t0 > limit_ns) {
-      *abort_flag = 1;
-      return false;
-    }
-  }
-  return true;
+  if (mbar_try_wait(bar, phase)) return true;
+  const uint64_t t0 = global_ns();
+  do {
+    __nanosleep(NS);
+    if (mbar_try_wait(bar, phase)) return true;
+  } while (!*abort_flag && global_ns() - t0 <= limit_ns);
+  *abort_flag = 1;
+  return false;
+}
+
+__device__ __forceinline__ float lg2f(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcpf(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // true in one lane of a converged warp, in a form that keeps the code around it
@@ -225,12 +235,12 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// n bytes (0: none, zeros are written) of a 16- or 4-byte asynchronous copy
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int n) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// 16- or 4-byte asynchronous copies
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src, int n) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -305,7 +315,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   constexpr int N = Cfg::kN;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t page_full[kChunks], page_empty[kChunks];
-  __shared__ int s_page[kChunks][kChunk][kTP];   // blocks of the tiles ahead; -1 past a sequence's end
+  __shared__ __align__(16) int64_t s_off[kChunks * kChunk * kTP];   // byte offsets of the blocks of the tiles ahead
   __shared__ __align__(8) uint64_t kop_full[2], kop_empty[2], vop_full[2], vop_empty[2];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2], o_free, drain;
   __shared__ uint32_t tmem_base;
@@ -376,17 +386,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   volatile int *abf = &abort_flag;
   // every stage, buffer and phase below follows the CTA's running tile count u
 
-  // The blocks of tile u (u < total) for the copies of this warp; done with a
+  // Block offsets of tile u (u < total) for the copies of this warp; done with a
   // chunk's last tile the warp hands the chunk back.
-  auto pages_of = [&](int u, bool &ok) -> const int * {
-    const int c = (u / kChunk) % kChunks;
-    if (u % kChunk == 0) ok = q4_wait(&page_full[c], (u / (kChunk * kChunks)) & 1, abf, P.wait_ns) && ok;
-    return s_page[c][u % kChunk];
+  auto pages_of = [&](uint32_t u, bool &ok) -> const int64_t * {
+    if (u % kChunk == 0)
+      ok = q4_wait<kNapShort>(&page_full[u / kChunk % kChunks], (u / (kChunk * kChunks)) & 1, abf, P.wait_ns) && ok;
+    return s_off + u % (kChunk * kChunks) * kTP;
   };
-  auto pages_done = [&](int u) {
+  auto pages_done = [&](uint32_t u) {
     if (u % kChunk == kChunk - 1) {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&page_empty[(u / kChunk) % kChunks]);
+      if (lane == 0) mbar_arrive(&page_empty[u / kChunk % kChunks]);
     }
   };
 
@@ -399,7 +409,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     int ti = 0;   // next tile of the item
     for (int c = 0; c * kChunk < total; ++c) {
       if (c >= kChunks &&
-          !__all_sync(0xffffffffu, q4_wait(&page_empty[c % kChunks], ((c / kChunks) & 1) ^ 1, abf, P.wait_ns)))
+          !__all_sync(0xffffffffu, q4_wait<kNapLong>(&page_empty[c % kChunks], ((c / kChunks) & 1) ^ 1, abf, P.wait_ns)))
         break;
       for (int filled = 0; filled < kChunk && have;) {
         const int n = min(kChunk - filled, it.ntiles - ti);
@@ -408,20 +418,20 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
 #pragma unroll
         for (int k = 0; k < kChunk * kTP / 32; ++k) {
           const int e = lane + 32 * k, v = (it.tile0 + ti) * kTP + e;
-          phys[k] = e < n * kTP && v < it.span.nblk ? table[v < it.span.nsb ? v : v + it.span.skip] : -2;
+          // (past the end: the last block once more)
+          const int vb = min(v, it.span.nblk - 1);
+          phys[k] = e < n * kTP ? table[vb < it.span.nsb ? vb : vb + it.span.skip] : 0;
         }
 #pragma unroll
         for (int k = 0; k < kChunk * kTP / 32; ++k) {
           const int e = lane + 32 * k;
           if (e >= n * kTP) continue;
           int ph = phys[k];
-          if (ph == -2 && (it.tile0 + ti) * kTP + e >= it.span.nblk) {
-            ph = -1;
-          } else if (ph < 0 || ph >= P.num_blocks) {
+          if (ph < 0 || ph >= P.num_blocks) {   // stay in bounds; the output of this sequence is flagged
             atomic_or_status(P.status, SV_DEV_BAD_BLOCK);
-            ph = 0;   // stay in bounds; the output of this sequence is flagged
+            ph = 0;
           }
-          s_page[c % kChunks][filled + e / kTP][e % kTP] = ph;
+          s_off[(c % kChunks * kChunk + filled) * kTP + e] = (int64_t)ph * P.block_stride;
         }
         filled += n;
         ti += n;
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     const uint32_t inv_g = (65536u + P.G - 1) / P.G;
     while (q4_next(P, wk, it)) {
       const int buf = i & 1;
-      if (i >= 2 && !__all_sync(0xffffffffu, q4_wait(&q_empty[buf], ((i >> 1) & 1) ^ 1, abf, P.wait_ns))) break;
+      if (i >= 2 && !__all_sync(0xffffffffu, q4_wait<kNapLong>(&q_empty[buf], ((i >> 1) & 1) ^ 1, abf, P.wait_ns))) break;
       const int c8 = lane & 15;
       // r / G without a division: exact for r < 128, G <= 128
       auto pos_of = [&](int r) { return (int)(((uint32_t)r * inv_g) >> 16); };
@@ -530,10 +540,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         if (lq == 0) {
           q4_next(P, wq, iq);
           lq = iq.ntiles;
-          ok = q4_wait(&q_full[nq & 1], (nq >> 1) & 1, abf, P.wait_ns);
+          ok = q4_wait<kNapShort>(&q_full[nq & 1], (nq >> 1) & 1, abf, P.wait_ns);
           ++nq;
         }
-        ok = q4_wait(&kop_full[bf], ((u + 1) >> 1) & 1, abf, P.wait_ns) && ok;
+        ok = q4_wait<kNapShort>(&kop_full[bf], ((u + 1) >> 1) & 1, abf, P.wait_ns) && ok;
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
         --lq;
@@ -558,11 +568,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         lp = ip.ntiles;
         tp = ip.tile0;
         // the previous item's O has been read
-        if (np > 0) ok = q4_wait(&o_free, (np - 1) & 1, abf, P.wait_ns);
+        if (np > 0) ok = q4_wait<kNapShort>(&o_free, (np - 1) & 1, abf, P.wait_ns);
         ++np;
       }
-      ok = q4_wait(&vop_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
-      ok = q4_wait(&p_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
+      ok = q4_wait<kNapShort>(&vop_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
+      ok = q4_wait<kNapShort>(&p_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
       if (!__all_sync(0xffffffffu, ok)) break;
       t5_fence_after();
       if (elect_one()) {
@@ -595,25 +605,26 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       uint64_t *full = V ? vop_full : kop_full, *empty = V ? vop_empty : kop_empty;
       const uint32_t col = lanes + (V ? Cfg::kVCol : Cfg::kKCol);
       const int slot = lane & 15, sw = (slot >> 1) & 3;
-      const uint8_t *pool = (V ? P.v_cache : P.k_cache) + (int64_t)g * P.head_stride;
-      const uint32_t mine = ring + (warp - kKWarp) * 2048;   // this warp's part of a stage
+      // this warp's part of a stage, and of a record
+      const uint32_t mine = ring + (warp - kKWarp) * 2048;
+      const uint8_t *pool = (V ? P.v_cache : P.k_cache) + (int64_t)g * P.head_stride +
+                            (V ? (warp & 3) * 256 + (lane & 15) * 16 : lane * 16);
       bool ok = true;
-      auto issue = [&](int u) {
-        if (u < total) {
-          const int *pg = pages_of(u, ok);
-          const uint32_t dst = mine + (u % kNS) * kStage + lane * 16;
+      uint32_t fill = mine + lane * 16;   // the next stage to copy to
+      auto issue = [&](uint32_t u) {
+        if (u < (uint32_t)total) {
+          const int64_t *pg = pages_of(u, ok) + (V ? lane >> 4 : 2 * (warp & 3));
+          if (ok) {   // (offsets that never came are not read)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // K: half a block of keys per copy; V: 32 head dims of two blocks
-            // (block numbers that never came are not read)
-            const int ph = ok ? pg[V ? 2 * j + (lane >> 4) : 2 * (warp & 3) + (j >> 1)] : -1;
-            const int off = V ? (warp & 3) * 256 + (lane & 15) * 16 : (j & 1) * 512 + lane * 16;
-            copy16(dst + j * 512, pool + (int64_t)max(ph, 0) * P.block_stride + off, ph >= 0 ? 16 : 0);
+            for (int j = 0; j < 4; ++j)   // K: half a block of keys per copy; V: 32 head dims of two blocks
+              copy16(fill + j * 512, pool + pg[V ? 2 * j : j >> 1] + (V ? 0 : (j & 1) * 512));
           }
           pages_done(u);
+          fill = fill == mine + lane * 16 + (kNS - 1) * kStage ? mine + lane * 16 : fill + kStage;
         }
         copies_commit();
       };
+      uint32_t src = mine + (V ? lane * 8 : lane * 64);   // the stage to read
       const bool run = !(P.withhold & SV_TEST_WITHHOLD_COPIES);
       for (int u = 1 - kNS; run && u < total; ++u) {
         issue(u + kNS - 1);
@@ -621,10 +632,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         const int bf = u & 1;
         copies_wait<kNS - 1>();
         __syncwarp();
-        if (ok && u >= 2) ok = q4_wait(&empty[bf], ((u >> 1) & 1) ^ 1, abf, P.wait_ns);
+        if (ok && u >= 2) ok = q4_wait<kNap>(&empty[bf], ((u >> 1) & 1) ^ 1, abf, P.wait_ns);
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
-        const uint32_t src = mine + (u % kNS) * kStage + (V ? lane * 8 : lane * 64);
 #pragma unroll 1
         for (int h = 0; h < 4; ++h) {   // K: 32 head dims of a key; V: 32 keys of a head dim
           uint32_t w[4], o[16];
@@ -642,6 +652,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         }
         t5_wait_st();
         t5_fence_before();
+        src = src >= mine + (kNS - 1) * kStage ? src - (kNS - 1) * kStage : src + kStage;
         __syncwarp();   // (every lane has read its codes: the stage is refilled next)
         if (lane == 0) mbar_arrive(&full[bf]);
       }
@@ -661,21 +672,23 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     const int prow = (t & ~7) | ((t & 3) << 1) | ((t >> 2) & 1);
     // this thread's ring of pairs: (K, V) of its key in the tiles ahead
     const uint32_t my_pairs = pairs + tid * 4;
-    const int64_t pair_off = (int64_t)g * P.head_stride + kCodes + (t & 15) * 4;
+    const uint8_t *k_pair = P.k_cache + (int64_t)g * P.head_stride + kCodes + (t & 15) * 4;
+    const uint8_t *v_pair = P.v_cache + (int64_t)g * P.head_stride + kCodes + (t & 15) * 4;
     Q4Walk wk = q4_walk(P, work);
     Q4Item it;
     int u = 0, i = 0;
     // A wait that gave up (ok false) only shows at the warpgroup's next vote, so
     // that its four warps leave together.
     bool ok = true;
-    auto issue = [&](int v) {
-      if (v < total) {
-        const int *pg = pages_of(v, ok);
-        const int ph = ok ? pg[t >> 4] : -1;
-        const int64_t off = (int64_t)max(ph, 0) * P.block_stride + pair_off;
-        const uint32_t dst = my_pairs + (v % kPairs) * 2048;
-        copy4(dst, P.k_cache + off, ph >= 0 ? 4 : 0);
-        copy4(dst + 1024, P.v_cache + off, ph >= 0 ? 4 : 0);
+    auto issue = [&](uint32_t v) {
+      if (v < (uint32_t)total) {
+        const int64_t *pg = pages_of(v, ok);
+        if (ok) {
+          const int64_t off = pg[t >> 4];
+          const uint32_t dst = my_pairs + v % kPairs * 2048;
+          copy4(dst, k_pair + off);
+          copy4(dst + 1024, v_pair + off);
+        }
         pages_done(v);
       }
       copies_commit();
@@ -683,9 +696,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     for (int v = 0; v < kPairs - 1; ++v) issue(v);
     while (q4_next(P, wk, it)) {
       const int buf = i & 1;
-      ok = __all_sync(0xffffffffu, q4_wait(&q_full[buf], (i >> 1) & 1, abf, P.wait_ns)) && ok;
+      ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&q_full[buf], (i >> 1) & 1, abf, P.wait_ns)) && ok;
       const float sl2 = P.scale_log2, fold = sl2 * s_fold[buf];
       const int L = it.span.L;
+      const int edge0 = L - P.n_new - kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
       if (t < NC) s_nb[c_first + t] = t < live ? kUnset : -kUnset;   // (padding never moves)
       float2 l2[NC / 2], b2[NC / 2];
 #pragma unroll
@@ -699,23 +713,27 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         issue(u + kPairs - 1);
         copies_wait<kPairs - 1>();
         uint32_t kp, vp;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kp) : "r"(my_pairs + (u % kPairs) * 2048));
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vp) : "r"(my_pairs + (u % kPairs) * 2048 + 1024));
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kp) : "r"(my_pairs + (uint32_t)u % kPairs * 2048));
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vp) : "r"(my_pairs + (uint32_t)u % kPairs * 2048 + 1024));
         const float2 k2 = __half22float2(*reinterpret_cast<const __half2 *>(&kp));
         const float2 v2 = __half22float2(*reinterpret_cast<const __half2 *>(&vp));
         const float vs = fmaxf(v2.x, 5.9604645e-8f);   // (pages never written hold zeros)
-        const float ka = k2.x * fold, kb = k2.y * sl2, vc = __log2f(vs);
-        float vi = __fdividef(1.f, vs), vz = fmaf(v2.y, vi, 8.f);
+        const float ka = k2.x * fold, kb = k2.y * sl2, vc = lg2f(vs);
+        float vi = rcpf(vs), vz = fmaf(v2.y, vi, 8.f);
         // A tile that ends past the oldest query or holds keys that a window
         // has left: position j sees the key iff 0 <= j - j0 < reach. A key that
         // no position sees (past the end, or between sinks and window) may hold
         // anything.
-        const bool edge = key0 + kTK - 1 > L - P.n_new || (P.window > 0 && key0 < L - P.window);
-        const int j0 = key - (L - P.n_new);
-        const uint32_t reach = P.window > 0 && key >= P.sinks ? (uint32_t)P.window : 0x80000000u;
-        if (edge && (key >= L || (uint32_t)(P.n_new - 1 - j0) >= reach + (uint32_t)(P.n_new - 1))) vi = vz = 0.f;
+        const bool edge = key0 >= edge0 || key0 < edge1;
+        int j0 = 0;
+        uint32_t reach = 0;
+        if (edge) {
+          j0 = key - (L - P.n_new);
+          reach = P.window > 0 && key >= P.sinks ? (uint32_t)P.window : 0x80000000u;
+          if (key >= L || (uint32_t)(P.n_new - 1 - j0) >= reach + (uint32_t)(P.n_new - 1)) vi = vz = 0.f;
+        }
         // S of this tile (and with it the P' buffer, read by the last but one P V)
-        ok = q4_wait(&s_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
+        ok = q4_wait<kNapShort>(&s_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
         ok = __all_sync(0xffffffffu, ok);
         t5_fence_after();
         const float2 ka2 = make_float2(ka, ka), kb2 = make_float2(kb, kb), vc2 = make_float2(vc, vc);
@@ -789,7 +807,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             b2[k / 2 + 1] = __fmul2_rn(b2[k / 2 + 1], make_float2(a.z, a.w));
           }
           if (ti > 0) {   // O too, once the previous P V has landed
-            ok = __all_sync(0xffffffffu, q4_wait(&o_done[bf ^ 1], ((u - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
+            ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&o_done[bf ^ 1], ((u - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
             t5_fence_after();
 #pragma unroll 1
             for (int k = 0; k < live; ++k) {
@@ -861,7 +879,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         }
       }
       named_bar_sync(bar, 128);
-      ok = __all_sync(0xffffffffu, q4_wait(&o_done[(u - 1) & 1], ((u - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
+      ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&o_done[(u - 1) & 1], ((u - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
       t5_fence_after();
 #pragma unroll
       for (int c0 = 0; c0 < NC; c0 += 8) {
