@@ -12,14 +12,16 @@
 // first sum grows to some 8 sum p', and at 128K keys, where the outputs are
 // averages near zero, its rounding errors reached 1 % of the outputs.)
 //
-// Codes as operands. The low four bits of an f16 are the code times 2^-24, a
-// subnormal that the tensor cores multiply exactly; a word of eight K codes
-// becomes four f16 pairs with `(w >> 4k) & 0x000F000F`, seven instructions for
-// eight values and no conversion. V codes are put below the exponent of 1024
-// in the same instruction, and 1032 is taken off the pair. A pair holds codes
-// k and k + 4 of the word, so the other operand of each product is stored in
-// that order.
-//
+// Codes as operands. A K code in the low four bits of a byte is, read as e4m3,
+// the code times 2^-9 exactly (0 to 7 are subnormals, 8 to 15 the first normal
+// binade), so a word of eight codes becomes two words of e4m3 with three
+// instructions: Q K^T runs in kind::f8f6f4 with each query row as two e4m3 terms
+// (hi + lo: 8 bits down to 2^-9 of the largest element, an error of 2^-17 of it
+// below). V codes become f16 integers: put below the exponent of 1024 (bits 0-3
+// of a half, or 4-7: then 16 times the code) and 1032 (1152) taken off, so P V
+// runs in kind::f16; the keys that come out 16 times too large have weights 16
+// times smaller. Both spread the codes of a word over several registers, so the
+// other operand of each product is stored in that order.
 // Keys on the lanes. The M = 128 side of both products is the cache: S^T = C Q^T
 // has a key per lane, O^T = C'^T P'^T a head dim per lane, and N is the number
 // of query rows (16 to 64), so no tensor-core work is padding whatever the
@@ -54,17 +56,19 @@ constexpr int kTP = 8;                     // blocks per tile
 constexpr int kTK = kTP * kBS;             // keys per tile
 constexpr int kCodes = kBS * kD / 2;       // code bytes of a record
 constexpr int kStage = 2 * kTP * kCodes;   // codes of a tile: K, then V, 2 KB a warp that unpacks them
-constexpr int kNS = 8;                     // stages of the code ring
+constexpr int kNS = 7;                     // stages of the code ring
 constexpr int kPairs = 4;                  // stages of the softmax threads' own rings of (scale, minimum) pairs
 constexpr int kChunk = 8, kChunks = 4;     // tiles of a chunk of block numbers, and chunks in shared memory
 constexpr int kPBytes = kTK * 128;         // a P' buffer: 128 bytes (64 columns of f16) a key
-constexpr int kWarps = 20;
-constexpr int kKWarp = 8, kVWarp = 12, kPageWarp = 16, kMmaWarp = 17, kQWarp = 18;
-// Registers: launched at 96 a thread; the K, V and service warps hand over 32
+constexpr int kSB = 3;                     // S and P' buffers
+constexpr int kWarps = 28;
+constexpr int kKWarp = 16, kVWarp = 20, kPageWarp = 24, kQkWarp = 25, kPvWarp = 26, kQWarp = 27;
+// Registers: launched at 72 a thread; the K, V and service warps hand over 32
 // each so that the softmax warps hold a tile's scores and two sums per column
-// (256 x 144 + 384 x 64 = 640 x 96).
-constexpr int kRegsSoftmax = 144, kRegsOther = 64;
+// (512 x 96 + 384 x 40 = 896 x 72).
+constexpr int kRegsSoftmax = 96, kRegsOther = 40;
 constexpr int kNapShort = 20, kNap = 60, kNapLong = 400;   // between the tries of a wait (ns)
+constexpr int kFirst = 1, kLast = 2, kFresh = 4;   // of a tile: the sequence's first or last here, its set's first
 constexpr float kUnset = 1e30f;            // minus the reference of a row that has met no key
 
 struct Q4Params {
@@ -86,13 +90,13 @@ struct Q4Params {
   unsigned withhold;
 };
 
-template <int NC> struct Q4Cfg {   // NC columns per softmax warpgroup
-  static constexpr int kN = 2 * NC;
-  static constexpr int kQ = kN * 256;   // two head-dim halves of 128-byte rows
-  static constexpr uint32_t kKCol = 0, kVCol = 128, kSCol = 256, kOCol = 256 + 2 * kN;
-  static constexpr int kSmem = 1024 + 2 * kQ + 2 * kPBytes + kNS * kStage + kPairs * 2 * 256 * 4;
-  static_assert(kOCol + kN <= 512, "TMEM columns");
-  static_assert(kSmem + 7168 <= 227 * 1024, "shared memory");
+template <int NC> struct Q4Cfg {   // NC query rows per softmax warpgroup
+  static constexpr int kCols = (NC + 7) / 8 * 8, kN = 2 * kCols;   // columns of S and O
+  static constexpr int kQ = kN * 256;   // the two e4m3 terms of a row, 128 bytes each
+  static constexpr uint32_t kKCol = 0, kVCol = 64, kSCol = 192, kOCol = 192 + kSB * kN;
+  static constexpr int kSmem = 1024 + 2 * kQ + kSB * kPBytes + kNS * kStage + kPairs * 2 * 512 * 4;
+  static_assert(kOCol + 2 * kN <= 512, "TMEM columns");
+  static_assert(kSmem + 8192 <= 227 * 1024, "shared memory");
 };
 
 // A sequence's part of a CTA's range.
@@ -203,7 +207,8 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool v) {
 // Bounded wait; a wait that has to sleep gives up at once after any earlier
 // one of the CTA gave up. It sleeps NS nanoseconds between its tries: try_wait
 // comes back after some hundred cycles whatever its time hint, and trying
-// again at once, the warps that wait take issue slots from those that work.
+// again at once, the warps that wait issued as many instructions as those that
+// work.
 template <int NS>
 __device__ __forceinline__ bool q4_wait(uint64_t *bar, uint32_t phase, volatile int *abort_flag, uint64_t limit_ns) {
   if (mbar_try_wait(bar, phase)) return true;
@@ -214,17 +219,6 @@ __device__ __forceinline__ bool q4_wait(uint64_t *bar, uint32_t phase, volatile 
   } while (!*abort_flag && global_ns() - t0 <= limit_ns);
   *abort_flag = 1;
   return false;
-}
-
-__device__ __forceinline__ float lg2f(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcpf(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // true in one lane of a converged warp, in a form that keeps the code around it
@@ -248,28 +242,47 @@ template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("c
 template <int R> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-// eight codes of a word -> four f16 pairs (codes k and k + 4): K codes times
-// 2^-24, V codes minus 8
-template <bool V>
-__device__ __forceinline__ void spread(uint32_t w, uint32_t *o) {
+// eight K codes of a word -> two words of e4m3 (codes 0 2 4 6, then 1 3 5 7),
+// each the code times 2^-9
+__device__ __forceinline__ void spread_k(uint32_t w, uint32_t *o) {
+  o[0] = w & 0x0F0F0F0Fu;
+  o[1] = (w >> 4) & 0x0F0F0F0Fu;
+}
+// eight V codes of a word -> four f16 pairs (codes k and k + 4), each the code
+// minus 8, times 16 for odd k
+__device__ __forceinline__ void spread_v(uint32_t w, uint32_t *o) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t c = (w >> (4 * k)) & 0x000F000Fu;
-    if constexpr (V) {
-      const uint32_t y = c | 0x64006400u;
-      const __half2 z = __hsub2(*reinterpret_cast<const __half2 *>(&y), __half2half2(__ushort_as_half(0x6408)));
-      o[k] = *reinterpret_cast<const uint32_t *>(&z);
-    } else {
-      o[k] = c;
-    }
+    const uint32_t y = ((k < 2 ? w : w >> 8) & (k & 1 ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+    const __half2 z = __hsub2(*reinterpret_cast<const __half2 *>(&y), __half2half2(__ushort_as_half(k & 1 ? 0x6480 : 0x6408)));
+    o[k] = *reinterpret_cast<const uint32_t *>(&z);
   }
 }
 
-// Sums of v[0..NV) over the warp's lanes: lane l returns the sum of column
-// l * NV / 32 (NV a power of two up to 32): each step exchanges the half of the
-// columns that the other lane keeps.
-template <int NV>
+__device__ __forceinline__ float lg2f(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcpf(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// kind::f8f6f4 (e4m3 A and B, 32 elements of K per MMA), A from tensor memory
+__device__ __forceinline__ void t5_mma_ts_f8(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+               "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+
+// Sums (or maxima) of v[0..NV) over the warp's lanes: lane l returns that of
+// column l * NV / 32 (NV a power of two up to 32): each step exchanges the half
+// of the columns that the other lane keeps.
+template <int NV, bool MAX>
 __device__ __forceinline__ float warp_columns(float (&v)[NV], int lane) {
+  auto join = [](float x, float y) { return MAX ? fmaxf(x, y) : x + y; };
 #pragma unroll
   for (int n = NV / 2, o = 16; o >= 1; n >>= 1, o >>= 1) {
     if (n >= 1) {
@@ -277,33 +290,46 @@ __device__ __forceinline__ float warp_columns(float (&v)[NV], int lane) {
 #pragma unroll
       for (int k = 0; k < (n > 0 ? n : 1); ++k) {
         const float send = up ? v[k] : v[k + n], keep = up ? v[k + n] : v[k];
-        v[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        v[k] = join(keep, __shfl_xor_sync(0xffffffffu, send, o));
       }
     } else {
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+      v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
     }
   }
   return v[0];
 }
 
-// N columns of this warp's lanes, N a multiple of 8
+// N columns of this warp's lanes, N a multiple of 4
 __device__ __forceinline__ void t5_ld8(uint32_t taddr, uint32_t *r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
+__device__ __forceinline__ void t5_ld4(uint32_t taddr, uint32_t *r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
 template <int N>
 __device__ __forceinline__ void t5_ldn(uint32_t taddr, uint32_t (&r)[N]) {
+  constexpr int a = N / 16 * 16, b = a + (N - a) / 8 * 8;
 #pragma unroll
-  for (int k = 0; k + 16 <= N; k += 16) t5_ld16(taddr + k, *reinterpret_cast<uint32_t(*)[16]>(r + k));
-  if constexpr (N % 16 == 8) t5_ld8(taddr + N - 8, r + N - 8);
+  for (int k = 0; k < a; k += 16) t5_ld16(taddr + k, *reinterpret_cast<uint32_t(*)[16]>(r + k));
+  if constexpr (b > a) t5_ld8(taddr + a, r + a);
+  if constexpr (N > b) t5_ld4(taddr + b, r + b);
+}
+__device__ __forceinline__ void t5_st8(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
-// Warps 0-3 and 4-7: softmax (a key per thread; each warpgroup half of the
-// query rows), later the epilogue (a head dim per thread). 8-11: K codes to
-// tensor memory, 12-15: V codes. 16: block numbers of the tiles ahead. 17: MMA
-// issue, owner of the 512 TMEM columns (two K, two V, two S buffers and O).
-// 18, 19: Q of the next sequence.
+// Warps 0-15: softmax (a key per thread), later the epilogue (a head dim per
+// thread). 16-19: K codes to tensor memory, 20-23: V codes. 24: block offsets
+// and flags of the tiles ahead. 25: issues Q K^T, owns the 512 TMEM columns (two
+// K, two V, three S buffers and two O). 26: issues P V (one warp for both
+// products took 1400 cycles a tile for its waits and commits alone). 27: Q of
+// the next sequence.
 // Every warp copies what it reads: a K warp the two blocks that its keys lie
 // in, a V warp its 32 head dims of the tile's eight blocks, a softmax thread
 // the pairs of its key; so a copy is waited for by its own warp alone. (Bulk
@@ -312,12 +338,14 @@ __device__ __forceinline__ void t5_ldn(uint32_t taddr, uint32_t (&r)[N]) {
 template <int NC>
 __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_constant__ Q4Params P) {
   using Cfg = Q4Cfg<NC>;
-  constexpr int N = Cfg::kN;
+  constexpr int N = Cfg::kN, CP = Cfg::kCols;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t page_full[kChunks], page_empty[kChunks];
-  __shared__ __align__(16) int64_t s_off[kChunks * kChunk * kTP];   // byte offsets of the blocks of the tiles ahead
+  // offsets of the blocks of the tiles ahead in 16-byte units, even blocks of a tile first
+  __shared__ __align__(16) uint32_t s_off[kChunks * kChunk * kTP];
+  __shared__ int s_flag[kChunks * kChunk];   // kFirst, kLast, kFresh, blocks of the tile << 8
   __shared__ __align__(8) uint64_t kop_full[2], kop_empty[2], vop_full[2], vop_empty[2];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2], o_free, drain;
+  __shared__ __align__(8) uint64_t s_full[kSB], p_full[kSB], pv_done[kSB], q_full[2], q_empty[2], o_free, drain[2];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ int4 s_work;
@@ -327,9 +355,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   __shared__ __align__(16) int s_pos[2][N];
   __shared__ int s_row[2][N];
   __shared__ float s_fold[2];
-  __shared__ __align__(16) float s_nb[N], s_a[N];   // minus the reference; the last factor of a rescale
-  __shared__ float s_max[8][NC], s_red[8][NC][2];
-  __shared__ __align__(8) float2 s_fin[N];
+  __shared__ __align__(16) float s_nb[2][N], s_a[2][N];   // per set: minus the reference; the last factor of a rescale
+  __shared__ float s_max[16][NC], s_red[16][NC][2];
+  __shared__ __align__(16) float4 s_fin[N];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Hp = P.H_kv * P.RG;
@@ -340,7 +368,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t q_smem = smem_u32(smem);
   const uint32_t p_smem = q_smem + 2 * Cfg::kQ;
-  const uint32_t ring = p_smem + 2 * kPBytes;
+  const uint32_t ring = p_smem + kSB * kPBytes;
   const uint32_t pairs = ring + kNS * kStage;
 
   if (warp == 0) {
@@ -353,24 +381,26 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   } else if (tid == 32) {
     for (int k = 0; k < kChunks; ++k) {
       mbar_init(&page_full[k], 1);
-      mbar_init(&page_empty[k], 16);   // the K, V and softmax warps
+      mbar_init(&page_empty[k], 26);   // the K, V, softmax and MMA warps
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(&kop_full[k], 4);
       mbar_init(&kop_empty[k], 1);
       mbar_init(&vop_full[k], 4);
       mbar_init(&vop_empty[k], 1);
+      mbar_init(&drain[k], 1);
+      mbar_init(&q_full[k], 1);
+      mbar_init(&q_empty[k], 17);   // the softmax warps, and the last Q K^T
+    }
+    for (int k = 0; k < kSB; ++k) {
       mbar_init(&s_full[k], 1);
       mbar_init(&p_full[k], 8);
-      mbar_init(&o_done[k], 1);
-      mbar_init(&q_full[k], 2);
-      mbar_init(&q_empty[k], 9);   // the softmax warps, and the last Q K^T
+      mbar_init(&pv_done[k], 1);
     }
-    mbar_init(&o_free, 8);
-    mbar_init(&drain, 1);
+    mbar_init(&o_free, 16);
     abort_flag = 0;
     fence_mbarrier_init();
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kQkWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
                  "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -386,15 +416,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   volatile int *abf = &abort_flag;
   // every stage, buffer and phase below follows the CTA's running tile count u
 
-  // Block offsets of tile u (u < total) for the copies of this warp; done with a
-  // chunk's last tile the warp hands the chunk back.
-  auto pages_of = [&](uint32_t u, bool &ok) -> const int64_t * {
-    if (u % kChunk == 0)
+  // The blocks of tile u (u < total) for the copies of this warp, which takes
+  // every step-th tile; done with a chunk's last tile it hands the chunk back.
+  auto pages_of = [&](uint32_t u, uint32_t step, bool &ok) -> const uint32_t * {
+    if (u % kChunk < step)
       ok = q4_wait<kNapShort>(&page_full[u / kChunk % kChunks], (u / (kChunk * kChunks)) & 1, abf, P.wait_ns) && ok;
     return s_off + u % (kChunk * kChunks) * kTP;
   };
-  auto pages_done = [&](uint32_t u) {
-    if (u % kChunk == kChunk - 1) {
+  auto pages_done = [&](uint32_t u, uint32_t step) {
+    if (u % kChunk >= kChunk - step) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&page_empty[u / kChunk % kChunks]);
     }
@@ -407,6 +437,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     Q4Item it;
     bool have = q4_next(P, wk, it);
     int ti = 0;   // next tile of the item
+    const uint32_t unit = (uint32_t)(P.block_stride >> 4);
     for (int c = 0; c * kChunk < total; ++c) {
       if (c >= kChunks &&
           !__all_sync(0xffffffffu, q4_wait<kNapLong>(&page_empty[c % kChunks], ((c / kChunks) & 1) ^ 1, abf, P.wait_ns)))
@@ -431,7 +462,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             atomic_or_status(P.status, SV_DEV_BAD_BLOCK);
             ph = 0;
           }
-          s_off[(c % kChunks * kChunk + filled) * kTP + e] = (int64_t)ph * P.block_stride;
+          const int page = e % kTP;
+          s_off[(c % kChunks * kChunk + filled) * kTP + e - page + (page >> 1) + 4 * (page & 1)] = (uint32_t)ph * unit;
+        }
+        if (lane < n) {
+          const int tt = ti + lane;
+          s_flag[c % kChunks * kChunk + filled + lane] =
+              (tt == 0 ? kFirst : 0) | (tt == it.ntiles - 1 ? kLast : 0) | (tt < 2 ? kFresh : 0) |
+              min(kTP, it.span.nblk - (it.tile0 + tt) * kTP) << 8;
         }
         filled += n;
         ti += n;
@@ -443,12 +481,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(&page_full[c % kChunks]);
     }
-  } else if (warp >= kQWarp) {
+  } else if (warp == kQWarp) {
     // ------------------------------------------------------------------- Q --
-    // Row by row to f16, scaled by one power of two that brings the largest
-    // finite element of the CTA's rows to [2^14, 2^15): bf16 values are then
-    // exact down to 2^-28 of it. Both warps look for the largest element; each
-    // converts half of the rows.
+    // Row by row to two e4m3 terms, scaled by one power of two that brings the
+    // largest finite element of the CTA's rows to [2^7, 2^8).
     Q4Walk wk = q4_walk(P, work);
     Q4Item it;
     int i = 0;
@@ -460,7 +496,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       // r / G without a division: exact for r < 128, G <= 128
       auto pos_of = [&](int r) { return (int)(((uint32_t)r * inv_g) >> 16); };
       auto row_of = [&](int col) {   // query row of a column, -1 for padding
-        const int w = col / NC, c = col - w * NC;
+        const int w = col / CP, c = col - w * CP;
         const int r = w * live0 + c;
         return c < (w ? rows - live0 : live0) ? row0 + r : -1;
       };
@@ -485,9 +521,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int ex = min(117, max(-113, (int)(top >> 23) - 127));   // (both powers stay normal)
-      const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+      const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
 #pragma unroll 2
-      for (int c0 = 2 * (warp - kQWarp); c0 < N; c0 += 4) {
+      for (int c0 = 0; c0 < N; c0 += 2) {
         const int col = c0 + (lane >> 4);
         const int r = row_of(col);
         const uint4 v = r >= 0 ? q[(int64_t)q_row(r) * 16 + c8] : make_uint4(0u, 0u, 0u, 0u);
@@ -502,99 +538,114 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         for (int e = 0; e < 8; ++e) sum += x[e];
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        uint32_t h[4];   // in the order of the codes: dims k and k + 4
+        uint32_t hi[2], lo[2];   // in the order of the codes: dims 0 2 4 6, then 1 3 5 7
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = pack2<true>(x[e] * up, x[e + 4] * up);
-        const uint32_t dst = q_smem + buf * Cfg::kQ + (c8 >> 3) * (N * 128) + col * 128 + (((c8 & 7) ^ (col & 7)) << 4);
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
-                     : "memory");
+        for (int e = 0; e < 2; ++e) {
+          hi[e] = lo[e] = 0;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float y0 = x[4 * k + e] * up, y1 = x[4 * k + 2 + e] * up;
+            const uint32_t c = f32x2_to_e4m3x2(y0, y1);
+            const uint32_t f = e4m3x2_to_f16x2((uint16_t)c);
+            const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&f));
+            hi[e] |= c << (16 * k);
+            lo[e] |= f32x2_to_e4m3x2(y0 - hv.x, y1 - hv.y) << (16 * k);
+          }
+        }
+        const uint32_t dst = q_smem + buf * Cfg::kQ + col * 128 + (((c8 >> 1) ^ (col & 7)) << 4) + (c8 & 1) * 8;
+        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(dst), "r"(hi[0]), "r"(hi[1]) : "memory");
+        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(dst + N * 128), "r"(lo[0]), "r"(lo[1]) : "memory");
         if (c8 == 0) {
           s_qs[buf][col] = sum;
           s_pos[buf][col] = r >= 0 ? pos_of(r) : 0;
           s_row[buf][col] = r >= 0 ? q_row(r) : 0;
         }
       }
-      // 2^-24 of the codes and 2^(14 - ex) of Q
-      if (lane == 0 && warp == kQWarp) s_fold[buf] = __uint_as_float((uint32_t)(127 + 10 + ex) << 23);
+      // 2^-9 of the codes and 2^(7 - ex) of Q
+      if (lane == 0) s_fold[buf] = __uint_as_float((uint32_t)(127 + 2 + ex) << 23);
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[buf]);
       ++i;
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kQkWarp || warp == kPvWarp) {
     // ----------------------------------------------------------------- MMA --
-    // The whole warp walks the tiles, one lane issues. Q K^T of tile u + 1 goes
-    // ahead of P V of tile u; as a commit covers everything issued before it,
-    // S of tile u being there also means that P V of tile u - 2 is done.
-    // f16 A and B, f32 accumulators, M = 128
+    // One warp per product; all its lanes wait, one issues. Formats 0 (e4m3 for
+    // Q K^T, f16 for P V), f32 accumulators, M = 128.
     constexpr uint32_t idesc_qk = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
     constexpr uint32_t idesc_pv = idesc_qk | (1u << 16);   // B = P'^T with the rows contiguous
-    Q4Walk wq = q4_walk(P, work), wp = wq;
-    Q4Item iq, ip;
-    int nq = 0, np = 0;          // items started
-    int lq = 0, lp = 0, tp = 0;  // tiles left in the current item; its next P V tile
-    for (int u = -1; u < total; ++u) {
-      if (u + 1 < total) {
-        const int bf = (u + 1) & 1;
-        bool ok = true;
-        if (lq == 0) {
-          q4_next(P, wq, iq);
-          lq = iq.ntiles;
-          ok = q4_wait<kNapShort>(&q_full[nq & 1], (nq >> 1) & 1, abf, P.wait_ns);
-          ++nq;
+    uint32_t items = 0, sb = 0, sph = 0;   // items started; S and P' buffer of the tile, and its phase
+    bool ok = true;
+    if (warp == kQkWarp) {
+      for (uint32_t u = 0; u < (uint32_t)total; ++u) {
+        const uint32_t bf = u & 1;
+        pages_of(u, 1, ok);
+        const int flag = s_flag[u % (kChunks * kChunk)];
+        pages_done(u, 1);
+        if (flag & kFirst) {
+          ok = q4_wait<kNapShort>(&q_full[items & 1], (items >> 1) & 1, abf, P.wait_ns) && ok;
+          ++items;
         }
-        ok = q4_wait<kNapShort>(&kop_full[bf], ((u + 1) >> 1) & 1, abf, P.wait_ns) && ok;
+        // the S buffer has been read, and its P' buffer too, once P V of tile
+        // u - 3 is done: so S being there tells the softmax that P' is free
+        if (u >= kSB) ok = q4_wait<kNapShort>(&pv_done[sb], sph ^ 1, abf, P.wait_ns) && ok;
+        ok = q4_wait<kNapShort>(&kop_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
-        --lq;
         if (elect_one()) {
-          const uint64_t qd = t5_desc(q_smem + ((nq - 1) & 1) * Cfg::kQ, 16, 1024);
+          const uint64_t qd = t5_desc(q_smem + ((items - 1) & 1) * Cfg::kQ, 16, 1024);
+          const uint32_t d = tb + Cfg::kSCol + sb * N, a = tb + Cfg::kKCol + bf * 32;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)   // 16 head dims per MMA, two halves of four
-            t5_mma_ts(tb + Cfg::kSCol + bf * N, tb + Cfg::kKCol + bf * 64 + 8 * kk,
-                      qd + (kk >> 2) * (N * 128 / 16) + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
-          t5_commit(&s_full[bf]);
+          for (int kk = 0; kk < 8; ++kk)   // 32 head dims per MMA, the hi terms of Q and then the lo terms
+            t5_mma_ts_f8(d, a + 8 * (kk & 3), qd + (kk >> 2) * (N * 128 / 16) + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
+          t5_commit(&s_full[sb]);
           t5_commit(&kop_empty[bf]);
-          if (lq == 0) t5_commit(&q_empty[(nq - 1) & 1]);
+          if (flag & kLast) t5_commit(&q_empty[(items - 1) & 1]);
         }
         __syncwarp();
+        if (++sb == kSB) {
+          sb = 0;
+          sph ^= 1;
+        }
       }
-      if (u < 0) continue;
-      const int bf = u & 1;
-      const bool fresh = lp == 0;
-      bool ok = true;
-      if (fresh) {
-        q4_next(P, wp, ip);
-        lp = ip.ntiles;
-        tp = ip.tile0;
-        // the previous item's O has been read
-        if (np > 0) ok = q4_wait<kNapShort>(&o_free, (np - 1) & 1, abf, P.wait_ns);
-        ++np;
-      }
-      ok = q4_wait<kNapShort>(&vop_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
-      ok = q4_wait<kNapShort>(&p_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
-      if (!__all_sync(0xffffffffu, ok)) break;
-      t5_fence_after();
-      if (elect_one()) {
-        const int nv = min(kTP, ip.span.nblk - tp * kTP);   // blocks past the end have no weight
-        const uint64_t pd = t5_desc(p_smem + bf * kPBytes, 16, 1024);
+    } else {
+      for (uint32_t u = 0; u < (uint32_t)total; ++u) {
+        const uint32_t bf = u & 1;
+        pages_of(u, 1, ok);
+        const int flag = s_flag[u % (kChunks * kChunk)];
+        pages_done(u, 1);
+        if (flag & kFirst) {
+          // the previous item's O have been read
+          if (items > 0) ok = q4_wait<kNapShort>(&o_free, (items - 1) & 1, abf, P.wait_ns) && ok;
+          ++items;
+        }
+        ok = q4_wait<kNapShort>(&vop_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
+        ok = q4_wait<kNapShort>(&p_full[sb], sph, abf, P.wait_ns) && ok;
+        if (!__all_sync(0xffffffffu, ok)) break;
+        t5_fence_after();
+        if (elect_one()) {
+          const uint64_t pd = t5_desc(p_smem + sb * kPBytes, 16, 1024);
+          const uint32_t d = tb + Cfg::kOCol + bf * N, a = tb + Cfg::kVCol + bf * 64;
+          const int nv = flag >> 8;   // blocks past the end have no weight
 #pragma unroll
-        for (int kk = 0; kk < kTP; ++kk)   // a block's 16 keys per MMA
-          if (kk < nv)
-            t5_mma_ts(tb + Cfg::kOCol, tb + Cfg::kVCol + bf * 64 + 8 * kk, pd + kk * (2048 / 16), idesc_pv,
-                      (!fresh || kk > 0) ? 1u : 0u);
-        t5_commit(&vop_empty[bf]);
-        t5_commit(&o_done[bf]);
+          for (int kk = 0; kk < kTP; ++kk)   // a block's 16 keys per MMA; each set's first tile starts its O afresh
+            if (kk < nv) t5_mma_ts(d, a + 8 * kk, pd + kk * (2048 / 16), idesc_pv, !(flag & kFresh) || kk > 0 ? 1u : 0u);
+          t5_commit(&pv_done[sb]);
+          t5_commit(&vop_empty[bf]);
+        }
+        __syncwarp();
+        if (++sb == kSB) {
+          sb = 0;
+          sph ^= 1;
+        }
       }
-      __syncwarp();
-      --lp;
-      ++tp;
     }
     // every MMA issued has completed before TMEM can be released
     if (total > 0) {
-      if (elect_one()) t5_commit(&drain);
+      uint64_t *dr = &drain[warp - kQkWarp];
+      if (elect_one()) t5_commit(dr);
       __syncwarp();
-      if (!mbar_wait(&drain, 0) && lane == 0) atomic_or_status(P.status, SV_DEV_TIMEOUT);
+      if (!mbar_wait(dr, 0) && lane == 0) atomic_or_status(P.status, SV_DEV_TIMEOUT);
     }
   } else if (warp >= kKWarp && warp < kPageWarp) {
     // ------------------------------------------------------ codes to TMEM --
@@ -606,25 +657,34 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       const uint32_t col = lanes + (V ? Cfg::kVCol : Cfg::kKCol);
       const int slot = lane & 15, sw = (slot >> 1) & 3;
       // this warp's part of a stage, and of a record
-      const uint32_t mine = ring + (warp - kKWarp) * 2048;
+      const uint32_t mine = ring + (warp - kKWarp) * 2048, mine_end = mine + kNS * kStage;
       const uint8_t *pool = (V ? P.v_cache : P.k_cache) + (int64_t)g * P.head_stride +
                             (V ? (warp & 3) * 256 + (lane & 15) * 16 : lane * 16);
       bool ok = true;
-      uint32_t fill = mine + lane * 16;   // the next stage to copy to
+      uint32_t fill = mine;   // the next stage to copy to
       auto issue = [&](uint32_t u) {
         if (u < (uint32_t)total) {
-          const int64_t *pg = pages_of(u, ok) + (V ? lane >> 4 : 2 * (warp & 3));
+          const uint32_t *pg = pages_of(u, 1, ok);
           if (ok) {   // (offsets that never came are not read)
+            uint32_t at[4];
+            if constexpr (V) {   // 32 head dims of two blocks per copy
+              const uint4 a = *reinterpret_cast<const uint4 *>(pg + (lane >> 4) * 4);
+              at[0] = a.x; at[1] = a.y; at[2] = a.z; at[3] = a.w;
+            } else {             // half a block of keys per copy
+              at[0] = at[1] = pg[warp & 3];
+              at[2] = at[3] = pg[4 + (warp & 3)];
+            }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)   // K: half a block of keys per copy; V: 32 head dims of two blocks
-              copy16(fill + j * 512, pool + pg[V ? 2 * j : j >> 1] + (V ? 0 : (j & 1) * 512));
+            for (int j = 0; j < 4; ++j)
+              copy16(fill + lane * 16 + j * 512, pool + (uint64_t)at[j] * 16 + (V ? 0 : (j & 1) * 512));
           }
-          pages_done(u);
-          fill = fill == mine + lane * 16 + (kNS - 1) * kStage ? mine + lane * 16 : fill + kStage;
+          pages_done(u, 1);
+          fill += kStage;
+          if (fill == mine_end) fill = mine;
         }
         copies_commit();
       };
-      uint32_t src = mine + (V ? lane * 8 : lane * 64);   // the stage to read
+      uint32_t src = mine;   // the stage to read
       const bool run = !(P.withhold & SV_TEST_WITHHOLD_COPIES);
       for (int u = 1 - kNS; run && u < total; ++u) {
         issue(u + kNS - 1);
@@ -635,24 +695,30 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         if (ok && u >= 2) ok = q4_wait<kNap>(&empty[bf], ((u >> 1) & 1) ^ 1, abf, P.wait_ns);
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
-#pragma unroll 1
+#pragma unroll 2
         for (int h = 0; h < 4; ++h) {   // K: 32 head dims of a key; V: 32 keys of a head dim
-          uint32_t w[4], o[16];
+          uint32_t w[4];
           if constexpr (V) {
-            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src + h * 512));
-            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[2]), "=r"(w[3]) : "r"(src + h * 512 + 256));
+            uint32_t o[16];
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src + lane * 8 + h * 512));
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[2]), "=r"(w[3]) : "r"(src + lane * 8 + h * 512 + 256));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) spread_v(w[k], o + 4 * k);
+            t5_st16(col + bf * 64 + 16 * h, o);
           } else {
+            uint32_t o[8];
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(src + ((h ^ sw) << 4)));
-          }
+                         : "r"(src + lane * 64 + ((h ^ sw) << 4)));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) spread<V>(w[k], o + 4 * k);
-          t5_st16(col + bf * 64 + 16 * h, o);
+            for (int k = 0; k < 4; ++k) spread_k(w[k], o + 2 * k);
+            t5_st8(col + bf * 32 + 8 * h, o);
+          }
         }
         t5_wait_st();
         t5_fence_before();
-        src = src >= mine + (kNS - 1) * kStage ? src - (kNS - 1) * kStage : src + kStage;
+        src += kStage;
+        if (src == mine_end) src = mine;
         __syncwarp();   // (every lane has read its codes: the stage is refilled next)
         if (lane == 0) mbar_arrive(&full[bf]);
       }
@@ -663,63 +729,71 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   } else if (warp < kKWarp) {
     // ------------------------------------------------------------- softmax --
     regs_inc<kRegsSoftmax>();
-    const int w = warp >> 2, t = tid & 127;
-    const int c_first = w * NC;                 // this warpgroup's columns
+    // Two sets of two warpgroups: set `set` takes the tiles of its parity with an
+    // O, references and sums of its own, as if the keys were split in two, so
+    // that one set's waits lie under the other's arithmetic; the epilogue joins
+    // them. The warpgroups of a set take half of the query rows each.
+    const int set = warp >> 3, w = (warp >> 2) & 1, t = tid & 127;
+    const int c_first = w * CP;                 // this warpgroup's columns
     const int live = w ? rows - live0 : live0;
-    const int bar = 1 + w;
+    const int bar = 1 + (warp >> 2), both = 5 + w;   // barriers of the warpgroup, and with its other set's twin
     const uint32_t lanes = tb + ((uint32_t)((warp & 3) * 32) << 16);
-    // row of P' that this thread's key takes (the order of the codes)
+    const uint32_t o_col = lanes + Cfg::kOCol + set * N + c_first;
+    // row of P' that this thread's key takes (the order of the codes); a key whose
+    // codes come out 16 times too large has a 16 times smaller weight
     const int prow = (t & ~7) | ((t & 3) << 1) | ((t >> 2) & 1);
     // this thread's ring of pairs: (K, V) of its key in the tiles ahead
     const uint32_t my_pairs = pairs + tid * 4;
+    const float shrink = t & 1 ? 0.0625f : 1.f, eight = t & 1 ? 128.f : 8.f;
     const uint8_t *k_pair = P.k_cache + (int64_t)g * P.head_stride + kCodes + (t & 15) * 4;
     const uint8_t *v_pair = P.v_cache + (int64_t)g * P.head_stride + kCodes + (t & 15) * 4;
     Q4Walk wk = q4_walk(P, work);
     Q4Item it;
-    int u = 0, i = 0;
-    // A wait that gave up (ok false) only shows at the warpgroup's next vote, so
-    // that its four warps leave together.
+    int u0 = 0, i = 0;                  // the item's first tile
+    int n = 0;                          // tiles this set has done: tile 2 n + set is next
+    int sb = set, sph = 0;              // its S and P' buffer, and their phase
+    // A wait that gave up (ok false) only shows at the next vote, so that the
+    // warps that share a barrier leave together.
     bool ok = true;
-    auto issue = [&](uint32_t v) {
-      if (v < (uint32_t)total) {
-        const int64_t *pg = pages_of(v, ok);
+    auto issue = [&](int m) {
+      const int v = 2 * m + set;
+      if (v < total) {
+        const uint32_t *pg = pages_of(v, 2, ok);
         if (ok) {
-          const int64_t off = pg[t >> 4];
-          const uint32_t dst = my_pairs + v % kPairs * 2048;
+          const uint64_t off = (uint64_t)pg[(t >> 5) + 4 * ((t >> 4) & 1)] * 16;
+          const uint32_t dst = my_pairs + (uint32_t)m % kPairs * 4096;
           copy4(dst, k_pair + off);
-          copy4(dst + 1024, v_pair + off);
+          copy4(dst + 2048, v_pair + off);
         }
-        pages_done(v);
+        pages_done(v, 2);
       }
       copies_commit();
     };
-    for (int v = 0; v < kPairs - 1; ++v) issue(v);
+    for (int m = 0; m < kPairs - 1; ++m) issue(m);
     while (q4_next(P, wk, it)) {
       const int buf = i & 1;
       ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&q_full[buf], (i >> 1) & 1, abf, P.wait_ns)) && ok;
       const float sl2 = P.scale_log2, fold = sl2 * s_fold[buf];
       const int L = it.span.L;
       const int edge0 = L - P.n_new - kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
-      if (t < NC) s_nb[c_first + t] = t < live ? kUnset : -kUnset;   // (padding never moves)
+      if (t < NC) s_nb[set][c_first + t] = 0.f;
       float2 l2[NC / 2], b2[NC / 2];
 #pragma unroll
       for (int k = 0; k < NC / 2; ++k) l2[k] = b2[k] = make_float2(0.f, 0.f);
-      if (bar_or(bar, 128, !ok)) break;
-      bool gone = false;
-      for (int ti = 0; ti < it.ntiles; ++ti, ++u) {
-        const int bf = u & 1;
+      bool gone = bar_or(bar, 128, !ok);
+      for (int ti = 2 * n + set - u0; !gone && ti < it.ntiles; ti += 2, ++n) {
         const int key0 = (it.tile0 + ti) * kTK, key = key0 + t;
         // this key's scales
-        issue(u + kPairs - 1);
+        issue(n + kPairs - 1);
         copies_wait<kPairs - 1>();
         uint32_t kp, vp;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kp) : "r"(my_pairs + (uint32_t)u % kPairs * 2048));
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vp) : "r"(my_pairs + (uint32_t)u % kPairs * 2048 + 1024));
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kp) : "r"(my_pairs + (uint32_t)n % kPairs * 4096));
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vp) : "r"(my_pairs + (uint32_t)n % kPairs * 4096 + 2048));
         const float2 k2 = __half22float2(*reinterpret_cast<const __half2 *>(&kp));
         const float2 v2 = __half22float2(*reinterpret_cast<const __half2 *>(&vp));
-        const float vs = fmaxf(v2.x, 5.9604645e-8f);   // (pages never written hold zeros)
+        const float vs = fmaxf(v2.x, 5.9604645e-8f) * shrink;   // (pages never written hold zeros)
         const float ka = k2.x * fold, kb = k2.y * sl2, vc = lg2f(vs);
-        float vi = rcpf(vs), vz = fmaf(v2.y, vi, 8.f);
+        float vi = rcpf(vs), vz = fmaf(v2.y, vi, eight);
         // A tile that ends past the oldest query or holds keys that a window
         // has left: position j sees the key iff 0 <= j - j0 < reach. A key that
         // no position sees (past the end, or between sinks and window) may hold
@@ -732,13 +806,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           reach = P.window > 0 && key >= P.sinks ? (uint32_t)P.window : 0x80000000u;
           if (key >= L || (uint32_t)(P.n_new - 1 - j0) >= reach + (uint32_t)(P.n_new - 1)) vi = vz = 0.f;
         }
-        // S of this tile (and with it the P' buffer, read by the last but one P V)
-        ok = q4_wait<kNapShort>(&s_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
+        // S of this tile (and with it the P' buffer, read by P V three tiles ago)
+        ok = q4_wait<kNapShort>(&s_full[sb], sph, abf, P.wait_ns) && ok;
         ok = __all_sync(0xffffffffu, ok);
         t5_fence_after();
         const float2 ka2 = make_float2(ka, ka), kb2 = make_float2(kb, kb), vc2 = make_float2(vc, vc);
-        const uint32_t s_col = lanes + Cfg::kSCol + bf * N + c_first;
+        const uint32_t s_col = lanes + Cfg::kSCol + sb * N + c_first;
         float2 y[NC / 2];   // log2 weights, minus the reference
+        const bool first = ti < 2;
         for (int again = 0;; ++again) {
           uint32_t x[NC];
           t5_ldn(s_col, x);
@@ -746,7 +821,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
 #pragma unroll
           for (int k = 0; k < NC; k += 4) {
             const float4 qs = *reinterpret_cast<const float4 *>(&s_qs[buf][c_first + k]);
-            const float4 nb = *reinterpret_cast<const float4 *>(&s_nb[c_first + k]);
+            const float4 nb = *reinterpret_cast<const float4 *>(&s_nb[set][c_first + k]);
             const float2 z0 = __ffma2_rn(make_float2(qs.x, qs.y), kb2, __fadd2_rn(vc2, make_float2(nb.x, nb.y)));
             const float2 z1 = __ffma2_rn(make_float2(qs.z, qs.w), kb2, __fadd2_rn(vc2, make_float2(nb.z, nb.w)));
             y[k / 2] = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), ka2, z0);
@@ -763,91 +838,113 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             }
           }
           if (again) break;
-          // the reference moves when a weight exceeds it by more than 2^8 (f16
-          // holds 2^16); all four warps decide together, as they share O
+          // The set's first tile of a sequence sets the references (they are 0
+          // so far); later ones move when a weight exceeds them by more than
+          // 2^8 (f16 holds 2^16). All four warps decide together, as they share O.
           float top = fmaxf(y[0].x, y[0].y);
 #pragma unroll
           for (int k = 1; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[k].x), y[k].y);
-          if (!bar_or(bar, 128, top > 8.f || !ok)) break;
+          if (!bar_or(bar, 128, first || top > 8.f || !ok)) break;
           if (bar_or(bar, 128, !ok)) {
             gone = true;
             break;
           }
           // each column's largest weight, without the reference
+          if (first) {
+            constexpr int NV = NC <= 4 ? 4 : (NC <= 8 ? 8 : (NC <= 16 ? 16 : 32));
+            float v[NV];
+#pragma unroll
+            for (int k = 0; k < NV; ++k) v[k] = k < NC ? ((k & 1) ? y[(k < NC ? k : 0) / 2].y : y[(k < NC ? k : 0) / 2].x) : -INFINITY;
+            const float m = warp_columns<NV, true>(v, lane);
+            const int c = lane / (32 / NV);
+            if (lane % (32 / NV) == 0 && c < NC) s_max[warp][c] = m;
+          } else {
 #pragma unroll 1
-          for (int k = 0; k < live; ++k) {
-            uint32_t xs;
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(xs) : "r"(s_col + k));
-            t5_wait_ld();
-            float z = fmaf(__uint_as_float(xs), ka, fmaf(s_qs[buf][c_first + k], kb, vc));
-            if (edge && (uint32_t)(s_pos[buf][c_first + k] - j0) >= reach) z = -INFINITY;
-            z = warp_max(z);
-            if (lane == 0) s_max[warp][k] = z;
+            for (int k = 0; k < live; ++k) {
+              uint32_t xs;
+              asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(xs) : "r"(s_col + k));
+              t5_wait_ld();
+              float z = fmaf(__uint_as_float(xs), ka, fmaf(s_qs[buf][c_first + k], kb, vc));
+              if (edge && (uint32_t)(s_pos[buf][c_first + k] - j0) >= reach) z = -INFINITY;
+              z = warp_max(z);
+              if (lane == 0) s_max[warp][k] = z;
+            }
           }
           named_bar_sync(bar, 128);
           if (t < NC) {
-            float a = 1.f;
+            float a = 1.f, nb = first ? kUnset : s_nb[set][c_first + t];
             if (t < live) {
-              const float m = fmaxf(fmaxf(s_max[4 * w][t], s_max[4 * w + 1][t]), fmaxf(s_max[4 * w + 2][t], s_max[4 * w + 3][t]));
-              const float nb = s_nb[c_first + t];
-              if (m + nb > 8.f) {
+              const int w0 = warp & ~3;
+              const float m = fmaxf(fmaxf(s_max[w0][t], s_max[w0 + 1][t]), fmaxf(s_max[w0 + 2][t], s_max[w0 + 3][t]));
+              if (m + nb > 8.f) {   // (a row that has met no key keeps kUnset)
                 a = ex2f(-nb - m);
-                s_nb[c_first + t] = -m;
+                nb = -m;
               }
+            } else {
+              nb = -kUnset;   // padding never moves
             }
-            s_a[c_first + t] = a;
+            s_nb[set][c_first + t] = nb;
+            s_a[set][c_first + t] = a;
           }
           named_bar_sync(bar, 128);
+          if (!first) {
 #pragma unroll
-          for (int k = 0; k < NC; k += 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(&s_a[c_first + k]);
-            l2[k / 2] = __fmul2_rn(l2[k / 2], make_float2(a.x, a.y));
-            b2[k / 2] = __fmul2_rn(b2[k / 2], make_float2(a.x, a.y));
-            l2[k / 2 + 1] = __fmul2_rn(l2[k / 2 + 1], make_float2(a.z, a.w));
-            b2[k / 2 + 1] = __fmul2_rn(b2[k / 2 + 1], make_float2(a.z, a.w));
-          }
-          if (ti > 0) {   // O too, once the previous P V has landed
-            ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&o_done[bf ^ 1], ((u - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
+            for (int k = 0; k < NC; k += 4) {
+              const float4 a = *reinterpret_cast<const float4 *>(&s_a[set][c_first + k]);
+              l2[k / 2] = __fmul2_rn(l2[k / 2], make_float2(a.x, a.y));
+              b2[k / 2] = __fmul2_rn(b2[k / 2], make_float2(a.x, a.y));
+              l2[k / 2 + 1] = __fmul2_rn(l2[k / 2 + 1], make_float2(a.z, a.w));
+              b2[k / 2 + 1] = __fmul2_rn(b2[k / 2 + 1], make_float2(a.z, a.w));
+            }
+            // O too, once the set's previous P V has landed
+            const int pb = sb >= 2 ? sb - 2 : sb + 1;   // its buffer, two of three back
+            ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&pv_done[pb], sb >= 2 ? sph : sph ^ 1, abf, P.wait_ns)) && ok;
             t5_fence_after();
 #pragma unroll 1
             for (int k = 0; k < live; ++k) {
               uint32_t o;
-              const uint32_t at = lanes + Cfg::kOCol + c_first + k;
-              asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o) : "r"(at));
+              asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o) : "r"(o_col + k));
               t5_wait_ld();
-              o = __float_as_uint(__uint_as_float(o) * s_a[c_first + k]);
-              asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(at), "r"(o) : "memory");
+              o = __float_as_uint(__uint_as_float(o) * s_a[set][c_first + k]);
+              asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(o_col + k), "r"(o) : "memory");
             }
             t5_wait_st();
           }
         }
         if (gone) break;
         const float2 vi2 = make_float2(vi, vi), vz2 = make_float2(vz, vz);
-        const uint32_t p_row = p_smem + bf * kPBytes + prow * 128;
+        const uint32_t p_row = p_smem + sb * kPBytes + prow * 128;
 #pragma unroll
         for (int c = 0; c < NC; c += 8) {
           uint32_t ph[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < (NC - c < 8 ? 2 : 4); ++k) {
             const int e = c / 2 + k;
             const float2 p = make_float2(ex2f(y[e].x), ex2f(y[e].y));
             l2[e] = __ffma2_rn(p, vi2, l2[e]);
             b2[e] = __ffma2_rn(p, vz2, b2[e]);
             ph[k] = pack2<true>(p.x, p.y);
           }
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p_row + ((((c_first + c) >> 3) ^ (prow & 7)) << 4)),
-                       "r"(ph[0]), "r"(ph[1]), "r"(ph[2]), "r"(ph[3])
-                       : "memory");
+          const uint32_t dst = p_row + ((((c_first + c) >> 3) ^ (prow & 7)) << 4);
+          if (NC - c < 8)   // (what the columns of padding hold does not matter)
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(dst), "r"(ph[0]), "r"(ph[1]) : "memory");
+          else
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(ph[0]), "r"(ph[1]), "r"(ph[2]), "r"(ph[3])
+                         : "memory");
         }
         fence_proxy_async_shared();
         t5_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[bf]);
+        if (lane == 0) mbar_arrive(&p_full[sb]);
+        sb += 2;   // tile + 2 of three buffers
+        if (sb >= kSB) {
+          sb -= kSB;
+          sph ^= 1;
+        }
       }
-      if (gone) break;
       // ---- epilogue: sums over the keys, then a head dim per thread ---------
       {
-        constexpr int NV = NC <= 8 ? 8 : (NC <= 16 ? 16 : 32);
+        constexpr int NV = NC <= 4 ? 4 : (NC <= 8 ? 8 : (NC <= 16 ? 16 : 32));
         float v[NV];
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
@@ -856,41 +953,61 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             const float2 x = pass ? b2[(k < NC ? k : 0) / 2] : l2[(k < NC ? k : 0) / 2];
             v[k] = k < NC ? ((k & 1) ? x.y : x.x) : 0.f;
           }
-          const float s = warp_columns<NV>(v, lane);
+          const float s = warp_columns<NV, false>(v, lane);
           const int c = lane / (32 / NV);
           if (lane % (32 / NV) == 0 && c < NC) s_red[warp][c][pass] = s;
         }
       }
-      named_bar_sync(bar, 128);
+      if (bar_or(both, 256, !ok || gone)) break;
       const int64_t ent = 2 * (int64_t)blockIdx.x + (it.first ? 0 : 1);
-      if (t < live) {
-        float l = 0.f, b = 0.f;
+      if (set == 0 && t < live) {
+        float l[2], b[2], x[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          l += s_red[4 * w + k][t][0];
-          b += s_red[4 * w + k][t][1];
+        for (int e = 0; e < 2; ++e) {
+          l[e] = b[e] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            l[e] += s_red[8 * e + 4 * w + k][t][0];
+            b[e] += s_red[8 * e + 4 * w + k][t][1];
+          }
+          // (a set with no tile of this sequence, as one with no key of it)
+          x[e] = ((e - u0) & 1) < it.ntiles ? -s_nb[e][c_first + t] : -kUnset;
         }
-        // (a row of NaN stays NaN; l is 0 only for a row without keys, which a query that sees itself never is)
-        s_fin[c_first + t] = make_float2(it.whole ? 1.f / l : 1.f, b);
+        // a set without keys has the lowest reference and no O
+        const float m = fmaxf(x[0], x[1]);
+        const float f0 = x[0] == -kUnset ? 0.f : ex2f(x[0] - m), f1 = x[1] == -kUnset ? 0.f : ex2f(x[1] - m);
+        const float ls = l[0] * f0 + l[1] * f1, bs = b[0] * f0 + b[1] * f1;
+        // (a row of NaN stays NaN; ls is 0 only for a row without keys, which a query that sees itself never is)
+        s_fin[c_first + t] = make_float4(f0, f1, bs, it.whole ? 1.f / ls : 1.f);
         if (!it.whole) {
           const int64_t e = ent * P.Rg + w * live0 + t;
-          P.ws_ml[2 * e] = -s_nb[c_first + t];
-          P.ws_ml[2 * e + 1] = l;
+          P.ws_ml[2 * e] = m;
+          P.ws_ml[2 * e + 1] = ls;
         }
       }
-      named_bar_sync(bar, 128);
-      ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&o_done[(u - 1) & 1], ((u - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
+      named_bar_sync(both, 256);
+      const int last = u0 + it.ntiles - 1;
+      for (int e = max(last - 1, u0); e <= last; ++e)   // each set's last tile
+        ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&pv_done[e % kSB], (e / kSB) & 1, abf, P.wait_ns)) && ok;
       t5_fence_after();
+      // the sets take columns in turn
+#pragma unroll 1
+      for (int c0 = 4 * set; c0 < live && ok; c0 += 8) {
+        uint32_t o[2][4];
 #pragma unroll
-      for (int c0 = 0; c0 < NC; c0 += 8) {
-        uint32_t o[8];
-        t5_ld8(lanes + Cfg::kOCol + c_first + c0, o);
+        for (int e = 0; e < 2; ++e)
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(o[e][0]), "=r"(o[e][1]), "=r"(o[e][2]), "=r"(o[e][3])
+                       : "r"(lanes + Cfg::kOCol + e * N + c_first + c0));
         t5_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (c0 + k >= live || !ok) break;
-          const float2 f = s_fin[c_first + c0 + k];
-          const float x = (__uint_as_float(o[k]) + f.y) * f.x;
+        for (int k = 0; k < 4; ++k) {
+          if (c0 + k >= live) break;
+          const float4 f = s_fin[c_first + c0 + k];
+          float x = f.z;
+          if (f.x != 0.f) x = fmaf(__uint_as_float(o[0][k]), f.x, x);
+          if (f.y != 0.f) x = fmaf(__uint_as_float(o[1][k]), f.y, x);
+          x *= f.w;
           if (it.whole) {
             static_cast<__nv_bfloat16 *>(P.out)[(int64_t)s_row[buf][c_first + c0 + k] * kD + t] = __float2bfloat16_rn(x);
           } else {
@@ -904,13 +1021,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         mbar_arrive(&o_free);
         mbar_arrive(&q_empty[buf]);
       }
+      u0 += it.ntiles;
       ++i;
     }
   }
   __syncthreads();
   if (tid == 0 && *abf) atomic_or_status(P.status, SV_DEV_TIMEOUT);
   t5_fence_after();
-  if (warp == kMmaWarp)
+  if (warp == kQkWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tb), "r"(512));
 }
 
@@ -1008,7 +1126,7 @@ Q4Plan q4_plan(int B, int n_new, int H_q, int H_kv, int d, int max_blocks, int b
          (int64_t)B * n_new * H_q < (1ll << 31);
   if (!p.tc) return p;
   p.R = (int)R;
-  p.RG = p.R > 64 ? 2 : 1;               // at most 64 query rows a CTA
+  p.RG = (p.R + 47) / 48;                // at most 48 query rows a CTA (the registers of the softmax warps)
   p.Rg = (p.R + p.RG - 1) / p.RG;
   const int64_t Hp = (int64_t)H_kv * p.RG;
   p.NR = (int)std::max<int64_t>(1, std::min<int64_t>(q4_sms() / Hp, tiles));
@@ -1062,7 +1180,9 @@ extern "C" sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const 
                         max_blocks_per_seq >= 1 && H_kv <= 65535 && block_size >= 1;
   int win = window, snk = sinks;
   if ((int64_t)win >= (int64_t)max_blocks_per_seq * block_size) win = snk = 0;   // reaches every key
-  if (sizes_ok) p = q4_plan(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size, q_dtype, win, snk);
+  // (block offsets are held in 32 bits, in 16-byte units)
+  const int64_t bstride = layout ? layout->block_stride : (int64_t)q4_record_bytes(kD, kBS) * H_kv;
+  if (sizes_ok && (int64_t)num_blocks * (bstride / 16) < (1ll << 32)) p = q4_plan(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size, q_dtype, win, snk);
   if (!p.tc || q_dtype != out_dtype)
     return attn_cuda_core_q4(q, q_dtype, k_cache, v_cache, layout, block_table, max_blocks_per_seq, seq_lens, B, n_new,
                              H_q, H_kv, d_head, block_size, num_blocks, softmax_scale, window, sinks, out, out_dtype,
@@ -1098,9 +1218,12 @@ extern "C" sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const 
   P.withhold = test_withhold();
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int half = (p.Rg + 1) / 2;   // rows of a softmax warpgroup
-  sv_status r2 = half <= 8 ? launch_q4<8>(P, p.C, st)
-                 : half <= 16 ? launch_q4<16>(P, p.C, st)
-                 : half <= 24 ? launch_q4<24>(P, p.C, st) : launch_q4<32>(P, p.C, st);
+  const sv_status r2 = half <= 4    ? launch_q4<4>(P, p.C, st)
+                       : half <= 8  ? launch_q4<8>(P, p.C, st)
+                       : half <= 12 ? launch_q4<12>(P, p.C, st)
+                       : half <= 16 ? launch_q4<16>(P, p.C, st)
+                       : half <= 20 ? launch_q4<20>(P, p.C, st)
+                                    : launch_q4<24>(P, p.C, st);
   if (r2 != SV_OK || p.NR == 1) return r2;
   launch_k(attn_q4_merge_kernel, dim3((p.NR - 1) * H_kv * p.RG, (p.Rg + kMergeWarps - 1) / kMergeWarps),
            dim3(32 * kMergeWarps), 0, st, 1, P);
