@@ -35,9 +35,9 @@
 // and 128 R exponentials.
 //
 // Work: the tiles of all sequences end to end are cut into equal ranges, one
-// per SM and kv head; each CTA (one per SM) computes its own range from the
-// lengths and streams through its sequences without draining the pipeline. A
-// range that ends inside a sequence leaves fp32 partials for the merge.
+// per SM and kv head; each CTA (one per SM) streams through the sequences of its
+// range without draining the pipeline. A range that ends inside a sequence
+// leaves fp32 partials for the merge.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -55,20 +55,22 @@ constexpr int kBS = 16;                    // block size
 constexpr int kTP = 8;                     // blocks per tile
 constexpr int kTK = kTP * kBS;             // keys per tile
 constexpr int kCodes = kBS * kD / 2;       // code bytes of a record
-constexpr int kStage = 2 * kTP * kCodes;   // codes of a tile: K, then V, 2 KB a warp that unpacks them
-constexpr int kNS = 7;                     // stages of the code ring
-constexpr int kPairs = 4;                  // stages of the softmax threads' own rings of (scale, minimum) pairs
-constexpr int kChunk = 8, kChunks = 4;     // tiles of a chunk of block numbers, and chunks in shared memory
+constexpr int kNS = 3;                     // stages of a K or V warp's ring of codes (2 KB each)
+// The keys' scales, unpacked: a K warp writes those of tile u before it hands
+// over the codes, after Q K^T of tile u - 2; that waited for P V of the pair
+// before the last, so the softmax has read every tile up to u - 6.
+constexpr int kScales = 8;
+constexpr int kScaleBytes = kTK * 20;      // a float4 and a float a key
+constexpr int kChunk = 8, kChunks = 4;     // tiles of a chunk of block offsets, and chunks in shared memory
 constexpr int kPBytes = kTK * 128;         // a P' buffer: 128 bytes (64 columns of f16) a key
-constexpr int kSB = 3;                     // S and P' buffers
 constexpr int kWarps = 28;
-constexpr int kKWarp = 16, kVWarp = 20, kPageWarp = 24, kQkWarp = 25, kPvWarp = 26, kQWarp = 27;
+constexpr int kKWarp = 8, kVWarp = 16, kPageWarp = 24, kQkWarp = 25, kPvWarp = 26, kQWarp = 27;
 // Registers: launched at 72 a thread; the K, V and service warps hand over 32
-// each so that the softmax warps hold a tile's scores and two sums per column
-// (512 x 96 + 384 x 40 = 896 x 72).
-constexpr int kRegsSoftmax = 96, kRegsOther = 40;
+// each so that the softmax warps hold two tiles' scores and two sums per
+// column (256 x 144 + 640 x 40 <= 896 x 72).
+constexpr int kRegsSoftmax = 144, kRegsOther = 40;
 constexpr int kNapShort = 20, kNap = 60, kNapLong = 400;   // between the tries of a wait (ns)
-constexpr int kFirst = 1, kLast = 2, kFresh = 4;   // of a tile: the sequence's first or last here, its set's first
+constexpr int kFirst = 1, kLast = 2, kEnd = 4, kSecond = 8;   // of a tile: the sequence's first or last here, its pair's last, its pair's second
 constexpr float kUnset = 1e30f;            // minus the reference of a row that has met no key
 
 struct Q4Params {
@@ -78,7 +80,10 @@ struct Q4Params {
   const int32_t *block_table, *seq_lens;
   float *ws_acc;      // [2 CTAs][Rg][kD] partials (entry 2c: CTA c's first sequence, 2c + 1: its last)
   float *ws_ml;       // [2 CTAs][Rg][2]
-  int4 *ws_split;     // per range: the sequence whose first cut is the range's start (b, first tile, tiles), or b = -1
+  int4 *ws_work;      // per range: (first sequence, first tile within it, tiles)
+  int4 *ws_split;     // per range: the sequence whose first cut is the range's start (b, first tile, tiles, T), or b = -1
+  uint8_t *ws_q;      // per (sequence, kv head and row group): its Q as the kernel's shared memory holds it
+  float *ws_qs;       // [kN + 4] per entry: the rows' sums, then the power of two that undoes the scaling
   int32_t *status;
   int64_t block_stride, head_stride;
   int B, n_new, H_q, H_kv, G, R;
@@ -93,9 +98,9 @@ struct Q4Params {
 template <int NC> struct Q4Cfg {   // NC query rows per softmax warpgroup
   static constexpr int kCols = (NC + 7) / 8 * 8, kN = 2 * kCols;   // columns of S and O
   static constexpr int kQ = kN * 256;   // the two e4m3 terms of a row, 128 bytes each
-  static constexpr uint32_t kKCol = 0, kVCol = 64, kSCol = 192, kOCol = 192 + kSB * kN;
-  static constexpr int kSmem = 1024 + 2 * kQ + kSB * kPBytes + kNS * kStage + kPairs * 2 * 512 * 4;
-  static_assert(kOCol + 2 * kN <= 512, "TMEM columns");
+  static constexpr uint32_t kKCol = 0, kVCol = 64, kSCol = 192, kOCol = 192 + 4 * kN;
+  static constexpr int kSmem = 1024 + 2 * kQ + 4 * kPBytes + 16 * kNS * 2048 + 8 * kNS * 256 + kScales * kScaleBytes;
+  static_assert(kOCol + kN <= 512, "TMEM columns");
   static_assert(kSmem + 8192 <= 227 * 1024, "shared memory");
 };
 
@@ -150,19 +155,9 @@ __device__ __forceinline__ bool q4_next(const Q4Params &P, Q4Walk &w, Q4Item &it
 }
 
 // One warp: range r of the tile sequence as (b, first tile within b, tiles),
-// and the split record of the range's start.
-__device__ __forceinline__ int4 q4_range(const Q4Params &P, int r, bool report, int4 &split) {
+// and the split record of the range's start; T is the number of tiles.
+__device__ int4 q4_range(const Q4Params &P, int r, int64_t T, int4 &split) {
   const int lane = threadIdx.x & 31;
-  int64_t T = 0;
-  for (int b0 = 0; b0 < P.B; b0 += 32) {
-    const int b = b0 + lane;
-    const int L = b < P.B ? P.seq_lens[b] : P.n_new;
-    int nt = b < P.B ? q4_tiles(P, L) : 0;
-    if (report && (L < P.n_new || L > P.max_blocks * kBS)) atomic_or_status(P.status, SV_DEV_BAD_SEQ_LEN);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) nt += __shfl_xor_sync(0xffffffffu, nt, o);
-    T += nt;
-  }
   const int64_t t0 = r * T / P.NR, t1 = (r + 1) * T / P.NR;
   int4 w = make_int4(0, 0, 0, 0);
   split = make_int4(-1, 0, 0, 0);
@@ -192,6 +187,120 @@ __device__ __forceinline__ int4 q4_range(const Q4Params &P, int r, bool report, 
     A += __shfl_sync(0xffffffffu, incl, 31);
   }
   return w;
+}
+
+// Before the attention: the ranges (the first CTAs, a warp each), and the query
+// rows of every (sequence, kv head and row group) as two e4m3 terms in the
+// layout of the K-major 128-byte-swizzled operand, scaled by one power of two
+// that brings the largest finite element of the entry to [2^7, 2^8). The kernel
+// then takes a sequence's Q with one bulk copy: converted there, by one warp,
+// it took 20,000 cycles a sequence.
+constexpr int kPrepWarps = 4;
+template <int NC>
+__global__ void __launch_bounds__(32 * kPrepWarps) attn_q4_prep_kernel(const __grid_constant__ Q4Params P) {
+  using Cfg = Q4Cfg<NC>;
+  constexpr int N = Cfg::kN, CP = Cfg::kCols;
+  constexpr int kPass = N / (2 * kPrepWarps);   // half a warp a row and pass
+  __shared__ uint32_t s_top[kPrepWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nrange = (P.NR + kPrepWarps - 1) / kPrepWarps;
+  pdl_trigger();
+  if ((int)blockIdx.x < nrange) {
+    // (the lengths are the caller's: read before the wait on the previous kernel)
+    int64_t T = 0;
+    for (int b0 = 0; b0 < P.B; b0 += 32) {
+      const int b = b0 + lane;
+      const int L = b < P.B ? P.seq_lens[b] : P.n_new;
+      int nt = b < P.B ? q4_tiles(P, L) : 0;
+      if (blockIdx.x == 0 && warp == 0 && (L < P.n_new || L > P.max_blocks * kBS)) atomic_or_status(P.status, SV_DEV_BAD_SEQ_LEN);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) nt += __shfl_xor_sync(0xffffffffu, nt, o);
+      T += nt;
+    }
+    const int r = blockIdx.x * kPrepWarps + warp;
+    int4 split = make_int4(-1, 0, 0, 0), w = split;
+    if (r < P.NR) w = q4_range(P, r, T, split);
+    pdl_wait();   // the previous kernel may still read this workspace
+    if (r < P.NR && lane == 0) {
+      P.ws_work[r] = w;
+      P.ws_split[r] = split;
+    }
+    return;
+  }
+  pdl_wait();
+  const int64_t ent = (int64_t)blockIdx.x - nrange;
+  const int Hp = P.H_kv * P.RG;
+  const int gp = (int)(ent % Hp), b = (int)(ent / Hp);
+  const int g = gp / P.RG, row0 = (gp % P.RG) * P.Rg;
+  const int rows = min(P.Rg, P.R - row0), live0 = (rows + 1) / 2;
+  const int c8 = lane & 15;
+  uint4 v[kPass];
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < kPass; ++k) {
+    const int col = (k * kPrepWarps + warp) * 2 + (lane >> 4);
+    const int w = col / CP, c = col - w * CP;
+    v[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (c < (w ? rows - live0 : live0)) {
+      const int r = row0 + w * live0 + c, j = r / P.G;
+      const int64_t at = ((int64_t)b * P.n_new + j) * P.H_q + g * P.G + (r - j * P.G);
+      v[k] = static_cast<const uint4 *>(P.q)[at * 16 + c8];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kPass; ++k) {
+    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t lo = (w[e] << 16) & 0x7fffffffu, hi = w[e] & 0x7fff0000u;
+      if (lo < 0x7f800000u) top = max(top, lo);
+      if (hi < 0x7f800000u) top = max(top, hi);
+    }
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kPrepWarps; ++k) top = max(top, s_top[k]);
+  const int ex = min(117, max(-113, (int)(top >> 23) - 127));   // (both powers stay normal)
+  const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
+  uint8_t *img = P.ws_q + ent * Cfg::kQ;
+  float *qs = P.ws_qs + ent * (N + 4);
+#pragma unroll
+  for (int k = 0; k < kPass; ++k) {
+    const int col = (k * kPrepWarps + warp) * 2 + (lane >> 4);
+    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    float x[8], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = __uint_as_float(w[e] << 16);
+      x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += x[e];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    uint32_t hi[2], lo[2];   // in the order of the codes: dims 0 2 4 6, then 1 3 5 7
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      hi[e] = lo[e] = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float y0 = x[4 * h + e] * up, y1 = x[4 * h + 2 + e] * up;
+        const uint32_t c = f32x2_to_e4m3x2(y0, y1);
+        const uint32_t f = e4m3x2_to_f16x2((uint16_t)c);
+        const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&f));
+        hi[e] |= c << (16 * h);
+        lo[e] |= f32x2_to_e4m3x2(y0 - hv.x, y1 - hv.y) << (16 * h);
+      }
+    }
+    uint8_t *dst = img + col * 128 + (((c8 >> 1) ^ (col & 7)) << 4) + (c8 & 1) * 8;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2 *>(dst + N * 128) = make_uint2(lo[0], lo[1]);
+    if (c8 == 0) qs[col] = sum;
+  }
+  // 2^-9 of the codes and 2^(7 - ex) of Q
+  if (threadIdx.x == 0) qs[N] = __uint_as_float((uint32_t)(127 + 2 + ex) << 23);
 }
 
 __device__ __forceinline__ bool bar_or(int id, int threads, bool v) {
@@ -229,12 +338,9 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// 16- or 4-byte asynchronous copies
+// 16-byte asynchronous copy
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -324,15 +430,19 @@ __device__ __forceinline__ void t5_st8(uint32_t taddr, const uint32_t *r) {
                : "memory");
 }
 
-// Warps 0-15: softmax (a key per thread), later the epilogue (a head dim per
-// thread). 16-19: K codes to tensor memory, 20-23: V codes. 24: block offsets
-// and flags of the tiles ahead. 25: issues Q K^T, owns the 512 TMEM columns (two
-// K, two V, three S buffers and two O). 26: issues P V (one warp for both
-// products took 1400 cycles a tile for its waits and commits alone). 27: Q of
-// the next sequence.
+// Warps 0-3 and 4-7: softmax (a key per thread and tile; each warpgroup half
+// of the query rows), later the epilogue (a head dim per thread). 8-15: K codes
+// to tensor memory, 16-23: V codes (four warps per tile parity). 24: block
+// offsets and flags of the tiles ahead. 25: issues Q K^T, owns the 512 TMEM
+// columns (two K, two V, four S buffers and O). 26: issues P V (one warp for
+// both products took 1400 cycles a tile for its waits and commits alone). 27: Q
+// of the next sequence.
+// The softmax takes two tiles at a time: its waits, its vote and its fences
+// cost as much as the arithmetic of a tile.
 // Every warp copies what it reads: a K warp the two blocks that its keys lie
-// in, a V warp its 32 head dims of the tile's eight blocks, a softmax thread
-// the pairs of its key; so a copy is waited for by its own warp alone. (Bulk
+// in (and the keys' pairs of K and V, which it unpacks for the softmax), a V
+// warp its 32 head dims of the tile's eight blocks; so a copy is waited for by
+// its own warp alone. (Bulk
 // copies of whole records were limited by their issue: 1088 bytes each, they
 // reached 2.9 TB/s from one warp and 4.8 TB/s from sixteen.)
 template <int NC>
@@ -343,9 +453,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   __shared__ __align__(8) uint64_t page_full[kChunks], page_empty[kChunks];
   // offsets of the blocks of the tiles ahead in 16-byte units, even blocks of a tile first
   __shared__ __align__(16) uint32_t s_off[kChunks * kChunk * kTP];
-  __shared__ int s_flag[kChunks * kChunk];   // kFirst, kLast, kFresh, blocks of the tile << 8
+  __shared__ int s_flag[kChunks * kChunk];   // kFirst, kLast, kEnd, kSecond, blocks of the tile << 8
   __shared__ __align__(8) uint64_t kop_full[2], kop_empty[2], vop_full[2], vop_empty[2];
-  __shared__ __align__(8) uint64_t s_full[kSB], p_full[kSB], pv_done[kSB], q_full[2], q_empty[2], o_free, drain[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], q_empty[2], o_free, drain[2];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ int4 s_work;
@@ -355,9 +465,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   __shared__ __align__(16) int s_pos[2][N];
   __shared__ int s_row[2][N];
   __shared__ float s_fold[2];
-  __shared__ __align__(16) float s_nb[2][N], s_a[2][N];   // per set: minus the reference; the last factor of a rescale
-  __shared__ float s_max[16][NC], s_red[16][NC][2];
-  __shared__ __align__(16) float4 s_fin[N];
+  __shared__ __align__(16) float s_nb[N], s_a[N];   // minus the reference; the last factor of a rescale
+  __shared__ float s_max[8][NC], s_red[8][NC][2];
+  __shared__ __align__(8) float2 s_fin[N];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Hp = P.H_kv * P.RG;
@@ -368,20 +478,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t q_smem = smem_u32(smem);
   const uint32_t p_smem = q_smem + 2 * Cfg::kQ;
-  const uint32_t ring = p_smem + kSB * kPBytes;
-  const uint32_t pairs = ring + kNS * kStage;
+  const uint32_t ring = p_smem + 4 * kPBytes;
+  const uint32_t pairs = ring + 16 * kNS * 2048;      // the K warps' rings of (scale, minimum) pairs
+  const uint32_t scales = pairs + 8 * kNS * 256;
 
   if (warp == 0) {
-    // (the lengths are the caller's: read before the wait on the previous kernel)
-    int4 split;
-    const int4 w = q4_range(P, range, blockIdx.x == 0, split);
-    if (lane == 0) s_work = w;
-    pdl_wait();   // the previous kernel may be a merge that still reads this workspace
-    if (lane == 0 && gp == 0) P.ws_split[range] = split;
+    pdl_wait();
+    if (lane == 0) s_work = P.ws_work[range];
   } else if (tid == 32) {
     for (int k = 0; k < kChunks; ++k) {
       mbar_init(&page_full[k], 1);
-      mbar_init(&page_empty[k], 26);   // the K, V, softmax and MMA warps
+      mbar_init(&page_empty[k], 18);   // the K, V and MMA warps
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(&kop_full[k], 4);
@@ -390,14 +497,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       mbar_init(&vop_empty[k], 1);
       mbar_init(&drain[k], 1);
       mbar_init(&q_full[k], 1);
-      mbar_init(&q_empty[k], 17);   // the softmax warps, and the last Q K^T
-    }
-    for (int k = 0; k < kSB; ++k) {
-      mbar_init(&s_full[k], 1);
+      mbar_init(&q_empty[k], 9);   // the softmax warps, and the last Q K^T
+      mbar_init(&s_full[k], 2);   // the commit, and the issuing lane itself, which has seen the K warps' scales
       mbar_init(&p_full[k], 8);
       mbar_init(&pv_done[k], 1);
     }
-    mbar_init(&o_free, 16);
+    mbar_init(&o_free, 8);
     abort_flag = 0;
     fence_mbarrier_init();
   } else if (warp == kQkWarp) {
@@ -468,7 +573,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         if (lane < n) {
           const int tt = ti + lane;
           s_flag[c % kChunks * kChunk + filled + lane] =
-              (tt == 0 ? kFirst : 0) | (tt == it.ntiles - 1 ? kLast : 0) | (tt < 2 ? kFresh : 0) |
+              (tt == 0 ? kFirst : 0) | (tt == it.ntiles - 1 ? kLast | kEnd : 0) | (tt & 1 ? kEnd | kSecond : 0) |
               min(kTP, it.span.nblk - (it.tile0 + tt) * kTP) << 8;
         }
         filled += n;
@@ -483,102 +588,46 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     }
   } else if (warp == kQWarp) {
     // ------------------------------------------------------------------- Q --
-    // Row by row to two e4m3 terms, scaled by one power of two that brings the
-    // largest finite element of the CTA's rows to [2^7, 2^8).
     Q4Walk wk = q4_walk(P, work);
     Q4Item it;
     int i = 0;
-    const uint32_t inv_g = (65536u + P.G - 1) / P.G;
     while (q4_next(P, wk, it)) {
       const int buf = i & 1;
       if (i >= 2 && !__all_sync(0xffffffffu, q4_wait<kNapLong>(&q_empty[buf], ((i >> 1) & 1) ^ 1, abf, P.wait_ns))) break;
-      const int c8 = lane & 15;
-      // r / G without a division: exact for r < 128, G <= 128
-      auto pos_of = [&](int r) { return (int)(((uint32_t)r * inv_g) >> 16); };
-      auto row_of = [&](int col) {   // query row of a column, -1 for padding
+      const int64_t ent = (int64_t)it.b * Hp + gp;
+      const float *qs = P.ws_qs + ent * (N + 4);
+      for (int col = lane; col < N; col += 32) {
         const int w = col / CP, c = col - w * CP;
-        const int r = w * live0 + c;
-        return c < (w ? rows - live0 : live0) ? row0 + r : -1;
-      };
-      auto q_row = [&](int r) {   // its row in q and out
-        const int j = pos_of(r);
-        return (it.b * P.n_new + j) * P.H_q + g * P.G + (r - j * P.G);
-      };
-      const uint4 *q = static_cast<const uint4 *>(P.q);
-      uint32_t top = 0;
-#pragma unroll 4
-      for (int c0 = 0; c0 < N; c0 += 2) {
-        const int r = row_of(c0 + (lane >> 4));
-        const uint4 v = r >= 0 ? q[(int64_t)q_row(r) * 16 + c8] : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t lo = (w[e] << 16) & 0x7fffffffu, hi = w[e] & 0x7fff0000u;
-          if (lo < 0x7f800000u) top = max(top, lo);
-          if (hi < 0x7f800000u) top = max(top, hi);
-        }
+        const int r = row0 + (c < (w ? rows - live0 : live0) ? w * live0 + c : 0);   // (padding: any)
+        const int j = r / P.G;
+        s_qs[buf][col] = qs[col];
+        s_pos[buf][col] = j;
+        s_row[buf][col] = (it.b * P.n_new + j) * P.H_q + g * P.G + (r - j * P.G);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int ex = min(117, max(-113, (int)(top >> 23) - 127));   // (both powers stay normal)
-      const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
-#pragma unroll 2
-      for (int c0 = 0; c0 < N; c0 += 2) {
-        const int col = c0 + (lane >> 4);
-        const int r = row_of(col);
-        const uint4 v = r >= 0 ? q[(int64_t)q_row(r) * 16 + c8] : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        float x[8], sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[2 * e] = __uint_as_float(w[e] << 16);
-          x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += x[e];
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        uint32_t hi[2], lo[2];   // in the order of the codes: dims 0 2 4 6, then 1 3 5 7
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          hi[e] = lo[e] = 0;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float y0 = x[4 * k + e] * up, y1 = x[4 * k + 2 + e] * up;
-            const uint32_t c = f32x2_to_e4m3x2(y0, y1);
-            const uint32_t f = e4m3x2_to_f16x2((uint16_t)c);
-            const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&f));
-            hi[e] |= c << (16 * k);
-            lo[e] |= f32x2_to_e4m3x2(y0 - hv.x, y1 - hv.y) << (16 * k);
-          }
-        }
-        const uint32_t dst = q_smem + buf * Cfg::kQ + col * 128 + (((c8 >> 1) ^ (col & 7)) << 4) + (c8 & 1) * 8;
-        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(dst), "r"(hi[0]), "r"(hi[1]) : "memory");
-        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(dst + N * 128), "r"(lo[0]), "r"(lo[1]) : "memory");
-        if (c8 == 0) {
-          s_qs[buf][col] = sum;
-          s_pos[buf][col] = r >= 0 ? pos_of(r) : 0;
-          s_row[buf][col] = r >= 0 ? q_row(r) : 0;
-        }
-      }
-      // 2^-9 of the codes and 2^(7 - ex) of Q
-      if (lane == 0) s_fold[buf] = __uint_as_float((uint32_t)(127 + 2 + ex) << 23);
-      fence_proxy_async_shared();
+      if (lane == 0) s_fold[buf] = qs[N];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[buf]);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full[buf], Cfg::kQ);
+        bulk_g2s(smem + buf * Cfg::kQ, P.ws_q + ent * Cfg::kQ, Cfg::kQ, &q_full[buf]);
+      }
+      __syncwarp();
       ++i;
     }
+    // the copies in flight land before the CTA may exit
+    if (lane == 0)
+      for (int k = max(0, i - 2); k < i; ++k)
+        if (!mbar_wait(&q_full[k & 1], (k >> 1) & 1)) atomic_or_status(P.status, SV_DEV_TIMEOUT);
   } else if (warp == kQkWarp || warp == kPvWarp) {
     // ----------------------------------------------------------------- MMA --
     // One warp per product; all its lanes wait, one issues. Formats 0 (e4m3 for
     // Q K^T, f16 for P V), f32 accumulators, M = 128.
     constexpr uint32_t idesc_qk = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
     constexpr uint32_t idesc_pv = idesc_qk | (1u << 16);   // B = P'^T with the rows contiguous
-    uint32_t items = 0, sb = 0, sph = 0;   // items started; S and P' buffer of the tile, and its phase
+    uint32_t items = 0, pair = 0;   // items started, pairs done
     bool ok = true;
     if (warp == kQkWarp) {
       for (uint32_t u = 0; u < (uint32_t)total; ++u) {
-        const uint32_t bf = u & 1;
+        const uint32_t bf = u & 1, pb = pair & 1;
         pages_of(u, 1, ok);
         const int flag = s_flag[u % (kChunks * kChunk)];
         pages_done(u, 1);
@@ -586,58 +635,57 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           ok = q4_wait<kNapShort>(&q_full[items & 1], (items >> 1) & 1, abf, P.wait_ns) && ok;
           ++items;
         }
-        // the S buffer has been read, and its P' buffer too, once P V of tile
-        // u - 3 is done: so S being there tells the softmax that P' is free
-        if (u >= kSB) ok = q4_wait<kNapShort>(&pv_done[sb], sph ^ 1, abf, P.wait_ns) && ok;
+        // the S buffers have been read, and their P' buffers too, once P V of the
+        // pair before the last is done: so S being there tells the softmax that
+        // P' is free
+        if (!(flag & kSecond) && pair >= 2) ok = q4_wait<kNapShort>(&pv_done[pb], ((pair >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
         ok = q4_wait<kNapShort>(&kop_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
         if (elect_one()) {
           const uint64_t qd = t5_desc(q_smem + ((items - 1) & 1) * Cfg::kQ, 16, 1024);
-          const uint32_t d = tb + Cfg::kSCol + sb * N, a = tb + Cfg::kKCol + bf * 32;
+          const uint32_t d = tb + Cfg::kSCol + (2 * pb + (flag & kSecond ? 1 : 0)) * N, a = tb + Cfg::kKCol + bf * 32;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)   // 32 head dims per MMA, the hi terms of Q and then the lo terms
             t5_mma_ts_f8(d, a + 8 * (kk & 3), qd + (kk >> 2) * (N * 128 / 16) + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
-          t5_commit(&s_full[sb]);
           t5_commit(&kop_empty[bf]);
+          if (flag & kEnd) {
+            t5_commit(&s_full[pb]);
+            mbar_arrive(&s_full[pb]);
+          }
           if (flag & kLast) t5_commit(&q_empty[(items - 1) & 1]);
         }
         __syncwarp();
-        if (++sb == kSB) {
-          sb = 0;
-          sph ^= 1;
-        }
+        if (flag & kEnd) ++pair;
       }
     } else {
       for (uint32_t u = 0; u < (uint32_t)total; ++u) {
-        const uint32_t bf = u & 1;
+        const uint32_t bf = u & 1, pb = pair & 1;
         pages_of(u, 1, ok);
         const int flag = s_flag[u % (kChunks * kChunk)];
         pages_done(u, 1);
         if (flag & kFirst) {
-          // the previous item's O have been read
+          // the previous item's O has been read
           if (items > 0) ok = q4_wait<kNapShort>(&o_free, (items - 1) & 1, abf, P.wait_ns) && ok;
           ++items;
         }
         ok = q4_wait<kNapShort>(&vop_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
-        ok = q4_wait<kNapShort>(&p_full[sb], sph, abf, P.wait_ns) && ok;
+        if (!(flag & kSecond)) ok = q4_wait<kNapShort>(&p_full[pb], (pair >> 1) & 1, abf, P.wait_ns) && ok;
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
         if (elect_one()) {
-          const uint64_t pd = t5_desc(p_smem + sb * kPBytes, 16, 1024);
-          const uint32_t d = tb + Cfg::kOCol + bf * N, a = tb + Cfg::kVCol + bf * 64;
+          const uint64_t pd = t5_desc(p_smem + (2 * pb + (flag & kSecond ? 1 : 0)) * kPBytes, 16, 1024);
+          const uint32_t a = tb + Cfg::kVCol + bf * 64;
           const int nv = flag >> 8;   // blocks past the end have no weight
 #pragma unroll
-          for (int kk = 0; kk < kTP; ++kk)   // a block's 16 keys per MMA; each set's first tile starts its O afresh
-            if (kk < nv) t5_mma_ts(d, a + 8 * kk, pd + kk * (2048 / 16), idesc_pv, !(flag & kFresh) || kk > 0 ? 1u : 0u);
-          t5_commit(&pv_done[sb]);
+          for (int kk = 0; kk < kTP; ++kk)   // a block's 16 keys per MMA
+            if (kk < nv)
+              t5_mma_ts(tb + Cfg::kOCol, a + 8 * kk, pd + kk * (2048 / 16), idesc_pv, !(flag & kFirst) || kk > 0 ? 1u : 0u);
           t5_commit(&vop_empty[bf]);
+          if (flag & kEnd) t5_commit(&pv_done[pb]);
         }
         __syncwarp();
-        if (++sb == kSB) {
-          sb = 0;
-          sph ^= 1;
-        }
+        if (flag & kEnd) ++pair;
       }
     }
     // every MMA issued has completed before TMEM can be released
@@ -653,18 +701,21 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     const uint32_t lanes = tb + ((uint32_t)((warp & 3) * 32) << 16);
     auto role = [&](auto is_v) {
       constexpr bool V = decltype(is_v)::value;
-      uint64_t *full = V ? vop_full : kop_full, *empty = V ? vop_empty : kop_empty;
-      const uint32_t col = lanes + (V ? Cfg::kVCol : Cfg::kKCol);
+      // these four warps take the tiles of one parity, that is, one TMEM buffer
+      const uint32_t bf = (warp >> 2) & 1;
+      uint64_t *full = (V ? vop_full : kop_full) + bf, *empty = (V ? vop_empty : kop_empty) + bf;
+      const uint32_t col = lanes + (V ? Cfg::kVCol + bf * 64 : Cfg::kKCol + bf * 32);
       const int slot = lane & 15, sw = (slot >> 1) & 3;
       // this warp's part of a stage, and of a record
-      const uint32_t mine = ring + (warp - kKWarp) * 2048, mine_end = mine + kNS * kStage;
+      const uint32_t mine = ring + (warp - kKWarp) * (kNS * 2048), mine_end = mine + kNS * 2048;
       const uint8_t *pool = (V ? P.v_cache : P.k_cache) + (int64_t)g * P.head_stride +
                             (V ? (warp & 3) * 256 + (lane & 15) * 16 : lane * 16);
       bool ok = true;
-      uint32_t fill = mine;   // the next stage to copy to
+      const uint32_t my_pairs = V ? 0u : pairs + (warp - kKWarp) * (kNS * 256);
+      uint32_t fill = mine, fill_pairs = my_pairs;   // the next stage to copy to
       auto issue = [&](uint32_t u) {
         if (u < (uint32_t)total) {
-          const uint32_t *pg = pages_of(u, 1, ok);
+          const uint32_t *pg = pages_of(u, 2, ok);
           if (ok) {   // (offsets that never came are not read)
             uint32_t at[4];
             if constexpr (V) {   // 32 head dims of two blocks per copy
@@ -677,22 +728,34 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               copy16(fill + lane * 16 + j * 512, pool + (uint64_t)at[j] * 16 + (V ? 0 : (j & 1) * 512));
+            if constexpr (!V) {   // the pairs: lanes 0-7 those of the two K blocks, 8-15 of the V blocks
+              if (lane < 16)
+                copy16(fill_pairs + lane * 16, (lane < 8 ? P.k_cache : P.v_cache) + (int64_t)g * P.head_stride + kCodes +
+                                                   (uint64_t)(lane & 4 ? at[2] : at[0]) * 16 + (lane & 3) * 16);
+            }
           }
-          pages_done(u, 1);
-          fill += kStage;
-          if (fill == mine_end) fill = mine;
+          pages_done(u, 2);
+          fill += 2048;
+          fill_pairs += 256;
+          if (fill == mine_end) {
+            fill = mine;
+            fill_pairs = my_pairs;
+          }
         }
         copies_commit();
       };
-      uint32_t src = mine;   // the stage to read
+      uint32_t src = mine, src_pairs = my_pairs;   // the stage to read
+      // K: this lane's key in its tile; a key whose V codes come out 16 times too
+      // large has a 16 times smaller weight
+      const int key = 32 * (warp & 3) + lane;
+      const float shrink = key & 1 ? 0.0625f : 1.f, eight = key & 1 ? 128.f : 8.f;
       const bool run = !(P.withhold & SV_TEST_WITHHOLD_COPIES);
-      for (int u = 1 - kNS; run && u < total; ++u) {
-        issue(u + kNS - 1);
-        if (u < 0) continue;
-        const int bf = u & 1;
+      for (int k = 1 - kNS; run && 2 * k + (int)bf < total; ++k) {   // tile 2 k + bf
+        issue(2 * (k + kNS - 1) + bf);
+        if (k < 0) continue;
         copies_wait<kNS - 1>();
         __syncwarp();
-        if (ok && u >= 2) ok = q4_wait<kNap>(&empty[bf], ((u >> 1) & 1) ^ 1, abf, P.wait_ns);
+        if (ok && k > 0) ok = q4_wait<kNap>(empty, (k & 1) ^ 1, abf, P.wait_ns);
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
 #pragma unroll 2
@@ -704,7 +767,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[2]), "=r"(w[3]) : "r"(src + lane * 8 + h * 512 + 256));
 #pragma unroll
             for (int k = 0; k < 4; ++k) spread_v(w[k], o + 4 * k);
-            t5_st16(col + bf * 64 + 16 * h, o);
+            t5_st16(col + 16 * h, o);
           } else {
             uint32_t o[8];
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -712,15 +775,33 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
                          : "r"(src + lane * 64 + ((h ^ sw) << 4)));
 #pragma unroll
             for (int k = 0; k < 4; ++k) spread_k(w[k], o + 2 * k);
-            t5_st8(col + bf * 32 + 8 * h, o);
+            t5_st8(col + 8 * h, o);
           }
+        }
+        if constexpr (!V) {
+          uint32_t kp, vp;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kp) : "r"(src_pairs + lane * 4));
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vp) : "r"(src_pairs + lane * 4 + 128));
+          const float2 k2 = __half22float2(*reinterpret_cast<const __half2 *>(&kp));
+          const float2 v2 = __half22float2(*reinterpret_cast<const __half2 *>(&vp));
+          const float vs = fmaxf(v2.x, 5.9604645e-8f) * shrink;   // (pages never written hold zeros)
+          const float vi = rcpf(vs), vz = fmaf(v2.y, vi, eight);
+          const uint32_t dst = scales + (uint32_t)(2 * k + bf) % kScales * kScaleBytes;
+          asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(dst + key * 16), "f"(k2.x), "f"(k2.y * P.scale_log2),
+                       "f"(lg2f(vs)), "f"(vi)
+                       : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + kTK * 16 + key * 4), "f"(vz) : "memory");
         }
         t5_wait_st();
         t5_fence_before();
-        src += kStage;
-        if (src == mine_end) src = mine;
+        src += 2048;
+        src_pairs += 256;
+        if (src == mine_end) {
+          src = mine;
+          src_pairs = my_pairs;
+        }
         __syncwarp();   // (every lane has read its codes: the stage is refilled next)
-        if (lane == 0) mbar_arrive(&full[bf]);
+        if (lane == 0) mbar_arrive(full);
       }
       copies_wait<0>();
     };
@@ -729,121 +810,108 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   } else if (warp < kKWarp) {
     // ------------------------------------------------------------- softmax --
     regs_inc<kRegsSoftmax>();
-    // Two sets of two warpgroups: set `set` takes the tiles of its parity with an
-    // O, references and sums of its own, as if the keys were split in two, so
-    // that one set's waits lie under the other's arithmetic; the epilogue joins
-    // them. The warpgroups of a set take half of the query rows each.
-    const int set = warp >> 3, w = (warp >> 2) & 1, t = tid & 127;
+    const int w = warp >> 2, t = tid & 127;
     const int c_first = w * CP;                 // this warpgroup's columns
     const int live = w ? rows - live0 : live0;
-    const int bar = 1 + (warp >> 2), both = 5 + w;   // barriers of the warpgroup, and with its other set's twin
+    const int bar = 1 + w;
     const uint32_t lanes = tb + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t o_col = lanes + Cfg::kOCol + set * N + c_first;
-    // row of P' that this thread's key takes (the order of the codes); a key whose
-    // codes come out 16 times too large has a 16 times smaller weight
+    // row of P' that this thread's key takes (the order of the codes)
     const int prow = (t & ~7) | ((t & 3) << 1) | ((t >> 2) & 1);
-    // this thread's ring of pairs: (K, V) of its key in the tiles ahead
-    const uint32_t my_pairs = pairs + tid * 4;
-    const float shrink = t & 1 ? 0.0625f : 1.f, eight = t & 1 ? 128.f : 8.f;
-    const uint8_t *k_pair = P.k_cache + (int64_t)g * P.head_stride + kCodes + (t & 15) * 4;
-    const uint8_t *v_pair = P.v_cache + (int64_t)g * P.head_stride + kCodes + (t & 15) * 4;
     Q4Walk wk = q4_walk(P, work);
     Q4Item it;
-    int u0 = 0, i = 0;                  // the item's first tile
-    int n = 0;                          // tiles this set has done: tile 2 n + set is next
-    int sb = set, sph = 0;              // its S and P' buffer, and their phase
-    // A wait that gave up (ok false) only shows at the next vote, so that the
-    // warps that share a barrier leave together.
+    int u = 0, i = 0;            // tiles and items done
+    uint32_t pair = 0;
+    // A wait that gave up (ok false) only shows at the warpgroup's next vote, so
+    // that its four warps leave together.
     bool ok = true;
-    auto issue = [&](int m) {
-      const int v = 2 * m + set;
-      if (v < total) {
-        const uint32_t *pg = pages_of(v, 2, ok);
-        if (ok) {
-          const uint64_t off = (uint64_t)pg[(t >> 5) + 4 * ((t >> 4) & 1)] * 16;
-          const uint32_t dst = my_pairs + (uint32_t)m % kPairs * 4096;
-          copy4(dst, k_pair + off);
-          copy4(dst + 2048, v_pair + off);
-        }
-        pages_done(v, 2);
-      }
-      copies_commit();
-    };
-    for (int m = 0; m < kPairs - 1; ++m) issue(m);
     while (q4_next(P, wk, it)) {
       const int buf = i & 1;
       ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&q_full[buf], (i >> 1) & 1, abf, P.wait_ns)) && ok;
-      const float sl2 = P.scale_log2, fold = sl2 * s_fold[buf];
+      const float fold = P.scale_log2 * s_fold[buf];
       const int L = it.span.L;
       const int edge0 = L - P.n_new - kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
-      if (t < NC) s_nb[set][c_first + t] = 0.f;
+      if (t < NC) s_nb[c_first + t] = 0.f;
       float2 l2[NC / 2], b2[NC / 2];
 #pragma unroll
       for (int k = 0; k < NC / 2; ++k) l2[k] = b2[k] = make_float2(0.f, 0.f);
       bool gone = bar_or(bar, 128, !ok);
-      for (int ti = 2 * n + set - u0; !gone && ti < it.ntiles; ti += 2, ++n) {
-        const int key0 = (it.tile0 + ti) * kTK, key = key0 + t;
-        // this key's scales
-        issue(n + kPairs - 1);
-        copies_wait<kPairs - 1>();
-        uint32_t kp, vp;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kp) : "r"(my_pairs + (uint32_t)n % kPairs * 4096));
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vp) : "r"(my_pairs + (uint32_t)n % kPairs * 4096 + 2048));
-        const float2 k2 = __half22float2(*reinterpret_cast<const __half2 *>(&kp));
-        const float2 v2 = __half22float2(*reinterpret_cast<const __half2 *>(&vp));
-        const float vs = fmaxf(v2.x, 5.9604645e-8f) * shrink;   // (pages never written hold zeros)
-        const float ka = k2.x * fold, kb = k2.y * sl2, vc = lg2f(vs);
-        float vi = rcpf(vs), vz = fmaf(v2.y, vi, eight);
-        // A tile that ends past the oldest query or holds keys that a window
-        // has left: position j sees the key iff 0 <= j - j0 < reach. A key that
-        // no position sees (past the end, or between sinks and window) may hold
-        // anything.
-        const bool edge = key0 >= edge0 || key0 < edge1;
-        int j0 = 0;
-        uint32_t reach = 0;
-        if (edge) {
-          j0 = key - (L - P.n_new);
-          reach = P.window > 0 && key >= P.sinks ? (uint32_t)P.window : 0x80000000u;
-          if (key >= L || (uint32_t)(P.n_new - 1 - j0) >= reach + (uint32_t)(P.n_new - 1)) vi = vz = 0.f;
+      for (int ti = 0; ti < it.ntiles && !gone; ++pair) {
+        const int nt = min(it.ntiles - ti, 2);
+        // S of this pair, and with it the keys' scales and P' buffers that P V two
+        // pairs ago has read
+        const int pb = pair & 1;
+        ok = q4_wait<kNapShort>(&s_full[pb], (pair >> 1) & 1, abf, P.wait_ns) && ok;
+        float ka[2], kb[2], vc[2], vi[2], vz[2];
+        bool edge[2];
+        int j0[2];
+        uint32_t reach[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // this thread's two keys
+          const int key0 = (it.tile0 + ti + h) * kTK, key = key0 + t;
+          const uint32_t src = scales + (uint32_t)(u + h) % kScales * kScaleBytes;
+          asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(ka[h]), "=f"(kb[h]), "=f"(vc[h]), "=f"(vi[h]) : "r"(src + t * 16));
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vz[h]) : "r"(src + kTK * 16 + t * 4));
+          ka[h] *= fold;
+          // A tile that ends past the oldest query or holds keys that a window
+          // has left: position j sees the key iff 0 <= j - j0 < reach. A key
+          // that no position sees (past the end, or between sinks and window)
+          // may hold anything.
+          edge[h] = key0 >= edge0 || key0 < edge1;
+          j0[h] = 0;
+          reach[h] = 0;
+          if (edge[h]) {
+            j0[h] = key - (L - P.n_new);
+            reach[h] = P.window > 0 && key >= P.sinks ? (uint32_t)P.window : 0x80000000u;
+            if (key >= L || (uint32_t)(P.n_new - 1 - j0[h]) >= reach[h] + (uint32_t)(P.n_new - 1)) vi[h] = vz[h] = 0.f;
+          }
         }
-        // S of this tile (and with it the P' buffer, read by P V three tiles ago)
-        ok = q4_wait<kNapShort>(&s_full[sb], sph, abf, P.wait_ns) && ok;
         ok = __all_sync(0xffffffffu, ok);
         t5_fence_after();
-        const float2 ka2 = make_float2(ka, ka), kb2 = make_float2(kb, kb), vc2 = make_float2(vc, vc);
-        const uint32_t s_col = lanes + Cfg::kSCol + sb * N + c_first;
-        float2 y[NC / 2];   // log2 weights, minus the reference
-        const bool first = ti < 2;
-        for (int again = 0;; ++again) {
+        const uint32_t s_col = lanes + Cfg::kSCol + 2 * pb * N + c_first;
+        float2 y[2][NC / 2];   // log2 weights, minus the reference
+        auto scores = [&](int h) {
+          const float2 ka2 = make_float2(ka[h], ka[h]), kb2 = make_float2(kb[h], kb[h]), vc2 = make_float2(vc[h], vc[h]);
           uint32_t x[NC];
-          t5_ldn(s_col, x);
+          t5_ldn(s_col + h * N, x);
           t5_wait_ld();
 #pragma unroll
           for (int k = 0; k < NC; k += 4) {
             const float4 qs = *reinterpret_cast<const float4 *>(&s_qs[buf][c_first + k]);
-            const float4 nb = *reinterpret_cast<const float4 *>(&s_nb[set][c_first + k]);
+            const float4 nb = *reinterpret_cast<const float4 *>(&s_nb[c_first + k]);
             const float2 z0 = __ffma2_rn(make_float2(qs.x, qs.y), kb2, __fadd2_rn(vc2, make_float2(nb.x, nb.y)));
             const float2 z1 = __ffma2_rn(make_float2(qs.z, qs.w), kb2, __fadd2_rn(vc2, make_float2(nb.z, nb.w)));
-            y[k / 2] = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), ka2, z0);
-            y[k / 2 + 1] = __ffma2_rn(make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), ka2, z1);
+            y[h][k / 2] = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), ka2, z0);
+            y[h][k / 2 + 1] = __ffma2_rn(make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), ka2, z1);
           }
-          if (edge) {
+          if (edge[h]) {
 #pragma unroll
             for (int k = 0; k < NC; k += 4) {
               const int4 j = *reinterpret_cast<const int4 *>(&s_pos[buf][c_first + k]);
-              if ((uint32_t)(j.x - j0) >= reach) y[k / 2].x = -INFINITY;
-              if ((uint32_t)(j.y - j0) >= reach) y[k / 2].y = -INFINITY;
-              if ((uint32_t)(j.z - j0) >= reach) y[k / 2 + 1].x = -INFINITY;
-              if ((uint32_t)(j.w - j0) >= reach) y[k / 2 + 1].y = -INFINITY;
+              if ((uint32_t)(j.x - j0[h]) >= reach[h]) y[h][k / 2].x = -INFINITY;
+              if ((uint32_t)(j.y - j0[h]) >= reach[h]) y[h][k / 2].y = -INFINITY;
+              if ((uint32_t)(j.z - j0[h]) >= reach[h]) y[h][k / 2 + 1].x = -INFINITY;
+              if ((uint32_t)(j.w - j0[h]) >= reach[h]) y[h][k / 2 + 1].y = -INFINITY;
             }
           }
-          if (again) break;
-          // The set's first tile of a sequence sets the references (they are 0
-          // so far); later ones move when a weight exceeds them by more than
-          // 2^8 (f16 holds 2^16). All four warps decide together, as they share O.
-          float top = fmaxf(y[0].x, y[0].y);
+        };
+        bool first = ti == 0;
+        for (int again = 0;; ++again) {
+          scores(0);
+          if (nt > 1) {
+            scores(1);
+          } else {
 #pragma unroll
-          for (int k = 1; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[k].x), y[k].y);
+            for (int k = 0; k < NC / 2; ++k) y[1][k] = make_float2(-INFINITY, -INFINITY);
+          }
+          if (again) break;
+          // The first pair of a sequence sets the references (they are 0 so
+          // far); later ones move when a weight exceeds them by more than 2^8
+          // (f16 holds 2^16). All four warps decide together, as they share O.
+          float top = fmaxf(y[0][0].x, y[0][0].y);
+#pragma unroll
+          for (int k = 1; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[0][k].x), y[0][k].y);
+#pragma unroll
+          for (int k = 0; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[1][k].x), y[1][k].y);
           if (!bar_or(bar, 128, first || top > 8.f || !ok)) break;
           if (bar_or(bar, 128, !ok)) {
             gone = true;
@@ -854,28 +922,35 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             constexpr int NV = NC <= 4 ? 4 : (NC <= 8 ? 8 : (NC <= 16 ? 16 : 32));
             float v[NV];
 #pragma unroll
-            for (int k = 0; k < NV; ++k) v[k] = k < NC ? ((k & 1) ? y[(k < NC ? k : 0) / 2].y : y[(k < NC ? k : 0) / 2].x) : -INFINITY;
+            for (int k = 0; k < NV; ++k)
+              v[k] = k < NC ? ((k & 1) ? fmaxf(y[0][(k < NC ? k : 0) / 2].y, y[1][(k < NC ? k : 0) / 2].y)
+                                       : fmaxf(y[0][(k < NC ? k : 0) / 2].x, y[1][(k < NC ? k : 0) / 2].x))
+                            : -INFINITY;
             const float m = warp_columns<NV, true>(v, lane);
             const int c = lane / (32 / NV);
             if (lane % (32 / NV) == 0 && c < NC) s_max[warp][c] = m;
           } else {
 #pragma unroll 1
             for (int k = 0; k < live; ++k) {
-              uint32_t xs;
-              asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(xs) : "r"(s_col + k));
-              t5_wait_ld();
-              float z = fmaf(__uint_as_float(xs), ka, fmaf(s_qs[buf][c_first + k], kb, vc));
-              if (edge && (uint32_t)(s_pos[buf][c_first + k] - j0) >= reach) z = -INFINITY;
-              z = warp_max(z);
-              if (lane == 0) s_max[warp][k] = z;
+              float m = -INFINITY;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (h >= nt) break;
+                uint32_t xs;
+                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(xs) : "r"(s_col + h * N + k));
+                t5_wait_ld();
+                const float z = fmaf(__uint_as_float(xs), ka[h], fmaf(s_qs[buf][c_first + k], kb[h], vc[h]));
+                if (!edge[h] || (uint32_t)(s_pos[buf][c_first + k] - j0[h]) < reach[h]) m = fmaxf(m, z);
+              }
+              m = warp_max(m);
+              if (lane == 0) s_max[warp][k] = m;
             }
           }
           named_bar_sync(bar, 128);
           if (t < NC) {
-            float a = 1.f, nb = first ? kUnset : s_nb[set][c_first + t];
+            float a = 1.f, nb = first ? kUnset : s_nb[c_first + t];
             if (t < live) {
-              const int w0 = warp & ~3;
-              const float m = fmaxf(fmaxf(s_max[w0][t], s_max[w0 + 1][t]), fmaxf(s_max[w0 + 2][t], s_max[w0 + 3][t]));
+              const float m = fmaxf(fmaxf(s_max[4 * w][t], s_max[4 * w + 1][t]), fmaxf(s_max[4 * w + 2][t], s_max[4 * w + 3][t]));
               if (m + nb > 8.f) {   // (a row that has met no key keeps kUnset)
                 a = ex2f(-nb - m);
                 nb = -m;
@@ -883,65 +958,67 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             } else {
               nb = -kUnset;   // padding never moves
             }
-            s_nb[set][c_first + t] = nb;
-            s_a[set][c_first + t] = a;
+            s_nb[c_first + t] = nb;
+            s_a[c_first + t] = a;
           }
           named_bar_sync(bar, 128);
           if (!first) {
 #pragma unroll
             for (int k = 0; k < NC; k += 4) {
-              const float4 a = *reinterpret_cast<const float4 *>(&s_a[set][c_first + k]);
+              const float4 a = *reinterpret_cast<const float4 *>(&s_a[c_first + k]);
               l2[k / 2] = __fmul2_rn(l2[k / 2], make_float2(a.x, a.y));
               b2[k / 2] = __fmul2_rn(b2[k / 2], make_float2(a.x, a.y));
               l2[k / 2 + 1] = __fmul2_rn(l2[k / 2 + 1], make_float2(a.z, a.w));
               b2[k / 2 + 1] = __fmul2_rn(b2[k / 2 + 1], make_float2(a.z, a.w));
             }
-            // O too, once the set's previous P V has landed
-            const int pb = sb >= 2 ? sb - 2 : sb + 1;   // its buffer, two of three back
-            ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&pv_done[pb], sb >= 2 ? sph : sph ^ 1, abf, P.wait_ns)) && ok;
+            // O too, once the previous P V has landed
+            ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&pv_done[pb ^ 1], ((pair - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
             t5_fence_after();
 #pragma unroll 1
             for (int k = 0; k < live; ++k) {
               uint32_t o;
-              asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o) : "r"(o_col + k));
+              const uint32_t at = lanes + Cfg::kOCol + c_first + k;
+              asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o) : "r"(at));
               t5_wait_ld();
-              o = __float_as_uint(__uint_as_float(o) * s_a[set][c_first + k]);
-              asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(o_col + k), "r"(o) : "memory");
+              o = __float_as_uint(__uint_as_float(o) * s_a[c_first + k]);
+              asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(at), "r"(o) : "memory");
             }
             t5_wait_st();
           }
         }
         if (gone) break;
-        const float2 vi2 = make_float2(vi, vi), vz2 = make_float2(vz, vz);
-        const uint32_t p_row = p_smem + sb * kPBytes + prow * 128;
+        const uint32_t p_row = p_smem + 2 * pb * kPBytes + prow * 128;
 #pragma unroll
-        for (int c = 0; c < NC; c += 8) {
-          uint32_t ph[4];
+        for (int h = 0; h < 2; ++h) {
+          if (h >= nt) break;
+          const float2 vi2 = make_float2(vi[h], vi[h]), vz2 = make_float2(vz[h], vz[h]);
 #pragma unroll
-          for (int k = 0; k < (NC - c < 8 ? 2 : 4); ++k) {
-            const int e = c / 2 + k;
-            const float2 p = make_float2(ex2f(y[e].x), ex2f(y[e].y));
-            l2[e] = __ffma2_rn(p, vi2, l2[e]);
-            b2[e] = __ffma2_rn(p, vz2, b2[e]);
-            ph[k] = pack2<true>(p.x, p.y);
+          for (int c = 0; c < NC; c += 8) {
+            uint32_t ph[4];
+#pragma unroll
+            for (int k = 0; k < (NC - c < 8 ? 2 : 4); ++k) {
+              const int e = c / 2 + k;
+              const float2 p = make_float2(ex2f(y[h][e].x), ex2f(y[h][e].y));
+              l2[e] = __ffma2_rn(p, vi2, l2[e]);
+              b2[e] = __ffma2_rn(p, vz2, b2[e]);
+              ph[k] = pack2<true>(p.x, p.y);
+            }
+            const uint32_t dst = p_row + h * kPBytes + ((((c_first + c) >> 3) ^ (prow & 7)) << 4);
+            if (NC - c < 8)   // (what the columns of padding hold does not matter)
+              asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(dst), "r"(ph[0]), "r"(ph[1]) : "memory");
+            else
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(ph[0]), "r"(ph[1]), "r"(ph[2]), "r"(ph[3])
+                           : "memory");
           }
-          const uint32_t dst = p_row + ((((c_first + c) >> 3) ^ (prow & 7)) << 4);
-          if (NC - c < 8)   // (what the columns of padding hold does not matter)
-            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(dst), "r"(ph[0]), "r"(ph[1]) : "memory");
-          else
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(ph[0]), "r"(ph[1]), "r"(ph[2]), "r"(ph[3])
-                         : "memory");
         }
         fence_proxy_async_shared();
         t5_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[sb]);
-        sb += 2;   // tile + 2 of three buffers
-        if (sb >= kSB) {
-          sb -= kSB;
-          sph ^= 1;
-        }
+        if (lane == 0) mbar_arrive(&p_full[pb]);
+        ti += nt;
+        u += nt;
       }
+      if (gone) break;
       // ---- epilogue: sums over the keys, then a head dim per thread ---------
       {
         constexpr int NV = NC <= 4 ? 4 : (NC <= 8 ? 8 : (NC <= 16 ? 16 : 32));
@@ -958,56 +1035,36 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           if (lane % (32 / NV) == 0 && c < NC) s_red[warp][c][pass] = s;
         }
       }
-      if (bar_or(both, 256, !ok || gone)) break;
+      named_bar_sync(bar, 128);
       const int64_t ent = 2 * (int64_t)blockIdx.x + (it.first ? 0 : 1);
-      if (set == 0 && t < live) {
-        float l[2], b[2], x[2];
+      if (t < live) {
+        float l = 0.f, b = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          l[e] = b[e] = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            l[e] += s_red[8 * e + 4 * w + k][t][0];
-            b[e] += s_red[8 * e + 4 * w + k][t][1];
-          }
-          // (a set with no tile of this sequence, as one with no key of it)
-          x[e] = ((e - u0) & 1) < it.ntiles ? -s_nb[e][c_first + t] : -kUnset;
+        for (int k = 0; k < 4; ++k) {
+          l += s_red[4 * w + k][t][0];
+          b += s_red[4 * w + k][t][1];
         }
-        // a set without keys has the lowest reference and no O
-        const float m = fmaxf(x[0], x[1]);
-        const float f0 = x[0] == -kUnset ? 0.f : ex2f(x[0] - m), f1 = x[1] == -kUnset ? 0.f : ex2f(x[1] - m);
-        const float ls = l[0] * f0 + l[1] * f1, bs = b[0] * f0 + b[1] * f1;
-        // (a row of NaN stays NaN; ls is 0 only for a row without keys, which a query that sees itself never is)
-        s_fin[c_first + t] = make_float4(f0, f1, bs, it.whole ? 1.f / ls : 1.f);
+        // (a row of NaN stays NaN; l is 0 only for a row without keys, which a query that sees itself never is)
+        s_fin[c_first + t] = make_float2(it.whole ? 1.f / l : 1.f, b);
         if (!it.whole) {
           const int64_t e = ent * P.Rg + w * live0 + t;
-          P.ws_ml[2 * e] = m;
-          P.ws_ml[2 * e + 1] = ls;
+          P.ws_ml[2 * e] = -s_nb[c_first + t];
+          P.ws_ml[2 * e + 1] = l;
         }
       }
-      named_bar_sync(both, 256);
-      const int last = u0 + it.ntiles - 1;
-      for (int e = max(last - 1, u0); e <= last; ++e)   // each set's last tile
-        ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&pv_done[e % kSB], (e / kSB) & 1, abf, P.wait_ns)) && ok;
+      named_bar_sync(bar, 128);
+      ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&pv_done[(pair - 1) & 1], ((pair - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
       t5_fence_after();
-      // the sets take columns in turn
 #pragma unroll 1
-      for (int c0 = 4 * set; c0 < live && ok; c0 += 8) {
-        uint32_t o[2][4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(o[e][0]), "=r"(o[e][1]), "=r"(o[e][2]), "=r"(o[e][3])
-                       : "r"(lanes + Cfg::kOCol + e * N + c_first + c0));
+      for (int c0 = 0; c0 < live && ok; c0 += 4) {
+        uint32_t o[4];
+        t5_ld4(lanes + Cfg::kOCol + c_first + c0, o);
         t5_wait_ld();
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (c0 + k >= live) break;
-          const float4 f = s_fin[c_first + c0 + k];
-          float x = f.z;
-          if (f.x != 0.f) x = fmaf(__uint_as_float(o[0][k]), f.x, x);
-          if (f.y != 0.f) x = fmaf(__uint_as_float(o[1][k]), f.y, x);
-          x *= f.w;
+          const float2 f = s_fin[c_first + c0 + k];
+          const float x = (__uint_as_float(o[k]) + f.y) * f.x;
           if (it.whole) {
             static_cast<__nv_bfloat16 *>(P.out)[(int64_t)s_row[buf][c_first + c0 + k] * kD + t] = __float2bfloat16_rn(x);
           } else {
@@ -1021,7 +1078,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         mbar_arrive(&o_free);
         mbar_arrive(&q_empty[buf]);
       }
-      u0 += it.ntiles;
       ++i;
     }
   }
@@ -1123,7 +1179,7 @@ Q4Plan q4_plan(int B, int n_new, int H_q, int H_kv, int d, int max_blocks, int b
   const int64_t tiles = (int64_t)std::max(B, 1) * ((span + kTP - 1) / kTP);
   const int64_t R = (int64_t)n_new * (H_q / H_kv);
   p.tc = qd == SV_BF16 && d == kD && bs == kBS && R <= 128 && tiles < (1ll << 30) &&
-         (int64_t)B * n_new * H_q < (1ll << 31);
+         (int64_t)B * n_new * H_q < (1ll << 30);
   if (!p.tc) return p;
   p.R = (int)R;
   p.RG = (p.R + 47) / 48;                // at most 48 query rows a CTA (the registers of the softmax warps)
@@ -1134,10 +1190,14 @@ Q4Plan q4_plan(int B, int n_new, int H_q, int H_kv, int d, int max_blocks, int b
   return p;
 }
 
-size_t q4_ws_bytes(const Q4Plan &p) {
-  const size_t ent = (size_t)2 * p.C * p.Rg;
+// Columns of S and O, a softmax warpgroup's rows in steps of 4 (of 8 for the layout)
+int q4_cols(const Q4Plan &p) { return 2 * (((p.Rg + 1) / 2 + 7) / 8 * 8); }
+
+size_t q4_ws_bytes(const Q4Plan &p, int B, int H_kv) {
+  const size_t ent = (size_t)2 * p.C * p.Rg, qent = (size_t)B * H_kv * p.RG, n = q4_cols(p);
   return align_up(ent * kD * sizeof(float), 256) + align_up(ent * 2 * sizeof(float), 256) +
-         align_up((size_t)p.NR * sizeof(int4), 256);
+         2 * align_up((size_t)p.NR * sizeof(int4), 256) + align_up(qent * n * 256, 256) +
+         align_up(qent * (n + 4) * sizeof(float), 256);
 }
 
 template <int NC>
@@ -1148,6 +1208,8 @@ sv_status launch_q4(const Q4Params &P, int C, cudaStream_t st) {
     err = cudaFuncSetAttribute(attn_q4_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4Cfg<NC>::kSmem);
   });
   if (err != cudaSuccess) return fail(SV_ERR_CUDA, "spec_verify_attn_q4: cudaFuncSetAttribute: %s", cudaGetErrorString(err));
+  const int64_t prep = (P.NR + kPrepWarps - 1) / kPrepWarps + (int64_t)P.B * P.H_kv * P.RG;
+  launch_k(attn_q4_prep_kernel<NC>, dim3((unsigned)prep), dim3(32 * kPrepWarps), 0, st, 1, P);
   launch_k(attn_q4_kernel<NC>, dim3(C), dim3(32 * kWarps), Q4Cfg<NC>::kSmem, st, 1, P);
   return check_launch("spec_verify_attn_q4 launch");
 }
@@ -1165,7 +1227,7 @@ extern "C" size_t spec_verify_attn_q4_workspace_size(int B, int n_new, int H_q, 
   if ((int64_t)window >= (int64_t)max_blocks_per_seq * block_size) window = sinks = 0;
   const Q4Plan p = q4_plan(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size, SV_BF16, window, sinks);
   // (queries in f32 run on the CUDA-core kernel whatever the shape)
-  return p.tc ? std::max(other, q4_ws_bytes(p)) : other;
+  return p.tc ? std::max(other, q4_ws_bytes(p, B, H_kv)) : other;
 }
 
 extern "C" sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const void *k_cache, const void *v_cache,
@@ -1196,7 +1258,7 @@ extern "C" sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const 
   const sv_status rc = q4_check("spec_verify_attn_q4", k_cache, v_cache, layout, H_kv, d_head, block_size,
                                 &P.block_stride, &P.head_stride);
   if (rc != SV_OK) return rc;
-  const size_t need = q4_ws_bytes(p);
+  const size_t need = q4_ws_bytes(p, B, H_kv);
   if (!workspace || workspace_bytes < need)
     return fail(SV_ERR_WORKSPACE, "spec_verify_attn_q4: workspace needs %zu bytes", need);
   if (!aligned(workspace, 256)) return fail(SV_ERR_WORKSPACE, "spec_verify_attn_q4: workspace not 256-byte aligned");
@@ -1209,7 +1271,14 @@ extern "C" sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const 
   P.block_table = block_table; P.seq_lens = seq_lens;
   P.ws_acc = static_cast<float *>(workspace);
   P.ws_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + align_up(ent * kD * sizeof(float), 256));
-  P.ws_split = reinterpret_cast<int4 *>(reinterpret_cast<uint8_t *>(P.ws_ml) + align_up(ent * 2 * sizeof(float), 256));
+  uint8_t *at = reinterpret_cast<uint8_t *>(P.ws_ml) + align_up(ent * 2 * sizeof(float), 256);
+  P.ws_split = reinterpret_cast<int4 *>(at);
+  at += align_up((size_t)p.NR * sizeof(int4), 256);
+  P.ws_work = reinterpret_cast<int4 *>(at);
+  at += align_up((size_t)p.NR * sizeof(int4), 256);
+  P.ws_q = at;
+  at += align_up((size_t)B * H_kv * p.RG * q4_cols(p) * 256, 256);
+  P.ws_qs = reinterpret_cast<float *>(at);
   P.status = dev_status;
   P.B = B; P.n_new = n_new; P.H_q = H_q; P.H_kv = H_kv; P.G = H_q / H_kv; P.R = p.R; P.Rg = p.Rg; P.RG = p.RG;
   P.NR = p.NR; P.max_blocks = max_blocks_per_seq; P.num_blocks = num_blocks; P.window = win; P.sinks = snk;
