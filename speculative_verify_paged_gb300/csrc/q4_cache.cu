@@ -9,6 +9,7 @@
 // s never reaches zero, so readers may divide by it or take its logarithm;
 // a constant row has every code 0 and the value m.
 #include <algorithm>
+#include <cstring>
 
 #include "q4.cuh"
 
@@ -24,41 +25,63 @@ struct Q4AppendArgs {
   int32_t *status;
 };
 
-constexpr int kQaWarps = 8;
+constexpr int kQaWarps = 4;
+constexpr int kQaRows = 4;   // rows a group of lanes loads before it works on the first
 
-// NE consecutive elements of a row as floats; `vec`: the address is a multiple
-// of the group's size.
-template <typename T, int NE>
-__device__ __forceinline__ void load_row(const T *p, bool vec, float (&x)[NE]) {
-  if constexpr (sizeof(T) * NE % 8 == 0) {
-    if (vec) {
-      constexpr int NW = sizeof(T) * NE / 8;
-      uint2 w[NW];
+// Eight consecutive elements of a row as floats; `vec`: 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, bool vec, T (&x)[8]) {
+  if (vec) {
 #pragma unroll
-      for (int k = 0; k < NW; ++k) w[k] = __ldg(reinterpret_cast<const uint2 *>(p) + k);
-      const T *e = reinterpret_cast<const T *>(w);
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+      reinterpret_cast<uint4 *>(x)[k] = __ldg(reinterpret_cast<const uint4 *>(p) + k);
+  } else {
 #pragma unroll
-      for (int k = 0; k < NE; ++k) x[k] = to_f32(e[k]);
-      return;
-    }
+    for (int k = 0; k < 8; ++k) x[k] = __ldg(p + k);
   }
-#pragma unroll
-  for (int k = 0; k < NE; ++k) x[k] = to_f32(__ldg(p + k));
 }
 
-// One CTA per (block that new rows land in, kv head, sequence). A warp takes a
-// row, NE = d / 32 elements a lane: minimum, maximum and codes, which go to
-// shared memory a byte each; the CTA then packs them, K along the head dim and
-// V along the slots, four bytes (eight codes) a thread. Words of a V record
-// that also hold codes of other slots are read and merged; no other CTA of the
-// call touches the record.
+// x: eight words of eight 4-bit values, word j nibble i. Afterwards nibbles of
+// equal place lie in equal bytes: bits 0-3 of byte k of x[i] and x[i + 1] (i
+// even) are nibble i of words 2k and 2k + 1, bits 4-7 their nibble i + 1.
+__device__ __forceinline__ void transpose8(uint32_t (&x)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {   // halves, across a distance of four words
+    const uint32_t a = x[k], b = x[k + 4];
+    x[k] = __byte_perm(a, b, 0x5410);
+    x[k + 4] = __byte_perm(a, b, 0x7632);
+  }
+#pragma unroll
+  for (int h = 0; h < 8; h += 4)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {   // bytes, across two
+      const uint32_t a = x[h + k], b = x[h + k + 2];
+      x[h + k] = __byte_perm(a, b, 0x6240);
+      x[h + k + 2] = __byte_perm(a, b, 0x7351);
+    }
+}
+
+// One CTA per (block that new rows land in, kv head, sequence). A group of
+// lanes takes a row, eight elements a lane: minimum, maximum and a word of
+// eight codes, which for K is a word of the record and for V goes to shared
+// memory, where the CTA turns words along the head dim into words along the
+// slots. Words of a V record that also hold codes of other slots are read and
+// merged; no other CTA of the call touches the record.
+// The quotient (x - m) / s is first taken as (x - m) times 1 / s, within 3 ulp
+// of the IEEE quotient; only where that lies within 2^-16 of the middle between
+// two codes (3 ulp are at most 3 x 2^-20 below 16) is the division done.
 template <typename TIn, int NE>
 __global__ void __launch_bounds__(32 * kQaWarps) q4_append_kernel(const __grid_constant__ Q4AppendArgs a, bool vec) {
-  constexpr int d = 32 * NE;
-  extern __shared__ __align__(16) uint8_t qa_codes[];   // [2][bs][d]
+  constexpr int d = 32 * NE, W = d / 8;                              // words of a row
+  constexpr int LPR = NE == 1 ? 4 : NE == 2 ? 8 : NE <= 4 ? 16 : 32;  // lanes of a row (those past W idle)
+  constexpr int kGroups = 32 * kQaWarps / LPR;
+  constexpr float kMagic = 12582912.f;                               // 1.5 x 2^23: adding it rounds to an integer
+  extern __shared__ __align__(16) uint32_t qa_smem[];
+  uint32_t *words = qa_smem;                // [bs][W] of V, eight head dims each
+  uint32_t *image = qa_smem + a.bs * W;     // the V record's codes
   pdl_trigger();
   const int g = blockIdx.y, b = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = threadIdx.x / LPR, li = threadIdx.x % LPR;
   const int bs = a.bs;
   const int L = a.seq_lens[b];
   if (L < a.n_new || L > a.max_blocks * bs) {
@@ -70,76 +93,110 @@ __global__ void __launch_bounds__(32 * kQaWarps) q4_append_kernel(const __grid_c
   const int s0 = max(first - page * bs, 0), s1 = min(L - page * bs, bs);   // slots written
   if (s0 >= s1) return;
   const int phys = a.block_table[(int64_t)b * a.max_blocks + page];
-  if (phys < 0 || phys >= a.num_blocks) {
-    if (threadIdx.x == 0) atomic_or_status(a.status, SV_DEV_BAD_BLOCK);
-    return;
-  }
-  const int64_t rec = (int64_t)phys * a.block_stride + (int64_t)g * a.head_stride;
   const int nr = s1 - s0;
+  const int64_t row_stride = (int64_t)a.H_kv * d;
+  const int64_t src0 = (((int64_t)b * a.n_new + (page * bs + s0 - first)) * a.H_kv + g) * d + li * 8;
+  const bool on = li < W;
   bool waited = false;
-  for (int i = warp; i < 2 * nr; i += kQaWarps) {
-    const int kv = i >= nr ? 1 : 0, slot = s0 + i - kv * nr;
-    const int j = page * bs + slot - first;
-    const TIn *src = static_cast<const TIn *>(a.src[kv]) + (((int64_t)b * a.n_new + j) * a.H_kv + g) * d + lane * NE;
-    float x[NE];
-    load_row<TIn, NE>(src, vec, x);
-    float mn = x[0], mx = x[0];   // (fminf and fmaxf leave NaN out)
+  for (int i0 = 0; i0 < 2 * nr; i0 += kQaRows * kGroups) {
+    alignas(16) TIn xr[kQaRows][8];
 #pragma unroll
-    for (int k = 1; k < NE; ++k) {
-      mn = fminf(mn, x[k]);
-      mx = fmaxf(mx, x[k]);
+    for (int u = 0; u < kQaRows; ++u) {
+      const int i = i0 + u * kGroups + group;
+      if (i < 2 * nr && on) load8(static_cast<const TIn *>(a.src[i >= nr]) + src0 + (i >= nr ? i - nr : i) * row_stride, vec, xr[u]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    }
-    if (!(mn <= mx)) mn = mx = 0.f;   // nothing but NaN
-    const __half mh = __float2half_rn(fminf(fmaxf(mn, -65504.f), 65504.f));
-    const float m = __half2float(mh);
-    const __half sh = __hmax(__float2half_rn(fminf(__fdiv_rn(__fsub_rn(mx, m), 15.f), 65504.f)), __ushort_as_half(1));
-    const float s = __half2float(sh);
-    uint8_t *dst = qa_codes + (kv * bs + slot) * d + lane * NE;
-#pragma unroll
-    for (int k = 0; k < NE; ++k)
-      dst[k] = (uint8_t)(int)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[k], m), s)), 0.f), 15.f);
     // everything read so far is the caller's; the pools may still be read by
     // the previous kernel of the stream
     if (!waited) {
       pdl_wait();
       waited = true;
+      if (phys < 0 || phys >= a.num_blocks) {
+        if (threadIdx.x == 0) atomic_or_status(a.status, SV_DEV_BAD_BLOCK);
+        return;
+      }
     }
-    if (lane == 0) {
-      const uint32_t pair = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(mh) << 16);
-      *reinterpret_cast<uint32_t *>(a.cache[kv] + rec + q4_code_bytes(d, bs) + 4 * slot) = pair;
+    uint8_t *rec[2];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) rec[kv] = a.cache[kv] + (int64_t)phys * a.block_stride + (int64_t)g * a.head_stride;
+#pragma unroll
+    for (int u = 0; u < kQaRows; ++u) {
+      if (i0 + u * kGroups >= 2 * nr) break;   // (the same for the whole CTA)
+      const int i = i0 + u * kGroups + group;
+      const bool live = i < 2 * nr;
+      const int kv = i >= nr ? 1 : 0, slot = s0 + i - kv * nr;
+      float x[8], mn = INFINITY, mx = -INFINITY;   // (fminf and fmaxf leave NaN out)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[k] = live && on ? to_f32(xr[u][k]) : NAN;
+        mn = fminf(mn, x[k]);
+        mx = fmaxf(mx, x[k]);
+      }
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) {
+        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      }
+      if (!(mn <= mx)) mn = mx = 0.f;   // nothing but NaN
+      const __half mh = __float2half_rn(fminf(fmaxf(mn, -65504.f), 65504.f));
+      const float m = __half2float(mh);
+      const __half sh = __hmax(__float2half_rn(fminf(__fdiv_rn(__fsub_rn(mx, m), 15.f), 65504.f)), __ushort_as_half(1));
+      const float s = __half2float(sh), inv = __fdiv_rn(1.f, s);
+      uint32_t w = 0;
+      float near = 0.f;   // distance from a code, the largest of the eight
+#pragma unroll
+      for (int k = 7; k >= 0; --k) {
+        const float t = fminf(fmaxf(__fmul_rn(__fsub_rn(x[k], m), inv), 0.f), 15.f);   // (NaN: 0)
+        const float r = __fadd_rn(t, kMagic);
+        near = fmaxf(near, fabsf(__fsub_rn(t, __fsub_rn(r, kMagic))));
+        w = (w << 4) + __float_as_uint(r);   // (the bits of kMagic come off below)
+      }
+      w -= 0x4B400000u * 0x11111111u;
+      if (near > 0.5f - 0x1p-16f) {
+        w = 0;
+#pragma unroll
+        for (int k = 7; k >= 0; --k)
+          w = (w << 4) + (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[k], m), s)), 0.f), 15.f);
+      }
+      if (!live) continue;
+      if (on) {
+        if (kv) words[slot * W + li] = w;
+        else *reinterpret_cast<uint32_t *>(rec[0] + q4_k_byte(slot, 8 * li, d)) = w;
+      }
+      if (li == 0) {
+        const uint32_t pair = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(mh) << 16);
+        *reinterpret_cast<uint32_t *>(rec[kv] + q4_code_bytes(d, bs) + 4 * slot) = pair;
+      }
     }
   }
-  if (!waited) pdl_wait();
   __syncthreads();
-  // K: eight head dims of a slot per word
-  for (int i = threadIdx.x; i < nr * (d / 8); i += 32 * kQaWarps) {
-    const int slot = s0 + i / (d / 8), c = 8 * (i % (d / 8));
-    const uint8_t *p = qa_codes + slot * d + c;
-    uint32_t w = 0;
+  // V: eight head dims by eight slots a thread
+  const int wpd = bs / 8;   // words of a head dim
+  for (int i = threadIdx.x; i < W * wpd; i += 32 * kQaWarps) {
+    const int o = i % W, t0 = 8 * (i / W);
+    uint32_t x[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w |= (uint32_t)p[k] << (4 * k);
-    *reinterpret_cast<uint32_t *>(a.cache[0] + rec + q4_k_byte(slot, c, d)) = w;
-  }
-  // V: eight slots of a head dim per word
-  const int wpd = bs / 8;
-  for (int i = threadIdx.x; i < d * wpd; i += 32 * kQaWarps) {
-    const int c = i / wpd, t0 = 8 * (i % wpd);
-    if (t0 + 8 <= s0 || t0 >= s1) continue;
-    uint32_t w = 0, keep = 0;
+    for (int k = 0; k < 8; ++k) x[k] = t0 + k >= s0 && t0 + k < s1 ? words[(t0 + k) * W + o] : 0;
+    transpose8(x);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int slot = t0 + k;
-      if (slot >= s0 && slot < s1) w |= (uint32_t)qa_codes[(bs + slot) * d + c] << (4 * k);
-      else keep |= 0xFu << (4 * k);
+    for (int k = 0; k < 8; k += 2) {
+      image[(8 * o + k) * wpd + i / W] = (x[k] & 0x0F0F0F0Fu) | ((x[k + 1] & 0x0F0F0F0Fu) << 4);
+      image[(8 * o + k + 1) * wpd + i / W] = ((x[k] >> 4) & 0x0F0F0F0Fu) | (x[k + 1] & 0xF0F0F0F0u);
     }
-    uint32_t *p = reinterpret_cast<uint32_t *>(a.cache[1] + rec + q4_v_byte(t0, c, bs));
-    if (keep) w |= *p & keep;
-    *p = w;
+  }
+  __syncthreads();
+  uint8_t *rec = a.cache[1] + (int64_t)phys * a.block_stride + (int64_t)g * a.head_stride;
+  if (nr == bs) {
+    for (int i = threadIdx.x; i < d * bs / 32; i += 32 * kQaWarps)
+      reinterpret_cast<uint4 *>(rec)[i] = reinterpret_cast<const uint4 *>(image)[i];
+    return;
+  }
+  for (int i = threadIdx.x; i < d * wpd; i += 32 * kQaWarps) {
+    const int t0 = 8 * (i % wpd);
+    if (t0 + 8 <= s0 || t0 >= s1) continue;
+    const int lo = max(s0 - t0, 0), hi = min(s1 - t0, 8);
+    const uint32_t mask = (0xFFFFFFFFu << (4 * lo)) & (0xFFFFFFFFu >> (32 - 4 * hi));
+    uint32_t *p = reinterpret_cast<uint32_t *>(rec) + i;
+    *p = mask == 0xFFFFFFFFu ? image[i] : (image[i] & mask) | (*p & ~mask);
   }
 }
 
@@ -147,53 +204,128 @@ struct Q4GatherArgs {
   const uint8_t *cache[2];
   void *out[2];   // [B][n_rows][H_kv][d]
   const int32_t *block_table, *seq_lens, *start;
-  int max_blocks, n_rows, H_kv, d, bs, num_blocks;
+  int max_blocks, n_rows, H_kv, bs, num_blocks, pages;   // pages: blocks that n_rows rows can touch
   int64_t block_stride, head_stride;   // bytes
   int32_t *status;
 };
 
-// Any head dim and block size: a thread per value.
+// Eight codes (even elements in the bytes of e, odd ones in those of o) as
+// code * scale + minimum to eight consecutive elements of a row.
 template <typename TO>
-__global__ void __launch_bounds__(256) q4_gather_kernel(const __grid_constant__ Q4GatherArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  const int i = blockIdx.x, b = blockIdx.y;
-  const int L = a.seq_lens[b];
-  const bool len_ok = L >= 0 && L <= a.max_blocks * a.bs;
-  if (!len_ok && threadIdx.x == 0 && i == 0) atomic_or_status(a.status, SV_DEV_BAD_SEQ_LEN);
-  const int64_t pos = (int64_t)a.start[b] + i;
-  int phys = -1;
-  if (len_ok && pos >= 0 && pos < L) {
-    phys = a.block_table[(int64_t)b * a.max_blocks + pos / a.bs];
-    if (phys < 0 || phys >= a.num_blocks) {
-      if (threadIdx.x == 0) atomic_or_status(a.status, SV_DEV_BAD_BLOCK);
-      phys = -1;
+__device__ __forceinline__ void write8(TO *dst, bool vec, uint32_t e, uint32_t o, float s, float m) {
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {   // (a byte under the exponent of 2^23 is 2^23 + the byte)
+    v[2 * k] = fmaf(__uint_as_float(__byte_perm(e, 0x4B000000u, 0x7540 + k)) - 8388608.f, s, m);
+    v[2 * k + 1] = fmaf(__uint_as_float(__byte_perm(o, 0x4B000000u, 0x7540 + k)) - 8388608.f, s, m);
+  }
+  if (vec) {
+    uint4 w[sizeof(TO) / 2];
+    if constexpr (sizeof(TO) == 4) {
+      memcpy(w, v, sizeof(w));
+    } else {
+      __nv_bfloat162 h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[k] = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+      memcpy(w, h, sizeof(w));
+    }
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(TO) / 2; ++k) reinterpret_cast<uint4 *>(dst)[k] = w[k];
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if constexpr (sizeof(TO) == 4) dst[k] = v[k];
+      else dst[k] = __float2bfloat16_rn(v[k]);
     }
   }
-  const int slot = (int)(pos % a.bs);
-  const int64_t row = ((int64_t)b * a.n_rows + i) * a.H_kv;
-  for (int e = threadIdx.x; e < 2 * a.H_kv * a.d; e += blockDim.x) {
-    const int kv = e / (a.H_kv * a.d), r = e - kv * a.H_kv * a.d;
-    const int g = r / a.d, c = r - g * a.d;
-    float v = 0.f;
-    if (phys >= 0) {
-      const uint8_t *rec = a.cache[kv] + (int64_t)phys * a.block_stride + (int64_t)g * a.head_stride;
-      const int code = kv ? (rec[q4_v_byte(slot, c, a.bs)] >> (4 * (slot & 1))) & 15
-                          : (rec[q4_k_byte(slot, c, a.d)] >> (4 * (c & 1))) & 15;
-      const __half *pr = reinterpret_cast<const __half *>(rec + q4_code_bytes(a.d, a.bs)) + 2 * slot;
-      v = fmaf((float)code, __half2float(pr[0]), __half2float(pr[1]));
+}
+
+// A warp takes one block of one kv head: first the K record, a word (eight head
+// dims of a slot) a lane and step, then the V record, eight head dims by eight
+// slots a lane, turned in registers. Rows are written eight elements at a time,
+// a row's lanes side by side. Rows outside the sequence, and those of a block
+// with a number out of range, are written as zeros.
+constexpr int kQgWarps = 8;
+template <typename TO, int NE>
+__global__ void __launch_bounds__(32 * kQgWarps) q4_gather_kernel(const __grid_constant__ Q4GatherArgs a, bool vec) {
+  constexpr int d = 32 * NE, W = d / 8, kStep = 4;
+  pdl_trigger();
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int64_t unit = (int64_t)blockIdx.x * kQgWarps + (threadIdx.x >> 5);
+  const int g = (int)(unit % a.H_kv);
+  const int64_t p = unit / a.H_kv;
+  const int bs = a.bs;
+  const int L = a.seq_lens[b], start = a.start[b];
+  pdl_wait();
+  if (p >= a.pages) return;
+  const bool len_ok = L >= 0 && L <= a.max_blocks * bs;
+  if (!len_ok && lane == 0 && unit == 0) atomic_or_status(a.status, SV_DEV_BAD_SEQ_LEN);
+  const int64_t page = (start >= 0 ? start / bs : -((bs - 1 - (int64_t)start) / bs)) + p;
+  const int64_t i0 = page * bs - start;   // output row of slot 0
+  const int r0 = (int)max((int64_t)0, -i0), r1 = (int)min((int64_t)bs, a.n_rows - i0);   // slots to write
+  if (r0 >= r1) return;
+  int held = len_ok && page >= 0 ? (int)min((int64_t)bs, max((int64_t)0, L - page * bs)) : 0;   // slots that hold rows
+  int phys = 0;
+  if (held > 0) {
+    phys = a.block_table[(int64_t)b * a.max_blocks + page];
+    if (phys < 0 || phys >= a.num_blocks) {
+      if (lane == 0) atomic_or_status(a.status, SV_DEV_BAD_BLOCK);
+      phys = held = 0;
     }
-    TO *o = static_cast<TO *>(a.out[kv]) + (row + g) * a.d + c;
-    if constexpr (sizeof(TO) == 4) *o = v;
-    else *o = __float2bfloat16_rn(v);
+  }
+  const int64_t rec = (int64_t)phys * a.block_stride + (int64_t)g * a.head_stride;
+  const int64_t stride = (int64_t)a.H_kv * d;
+  const int64_t at = ((int64_t)b * a.n_rows + i0) * stride + (int64_t)g * d;   // of slot 0
+  const int code_bytes = q4_code_bytes(d, bs);
+  const uint8_t *kr = a.cache[0] + rec, *vr = a.cache[1] + rec;
+  const int steps = bs * NE / 8;
+  for (int k0 = 0; k0 < steps; k0 += kStep) {
+    uint32_t w[kStep], pr[kStep];
+#pragma unroll
+    for (int u = 0; u < kStep; ++u) {
+      const int i = (k0 + u) * 32 + lane, slot = i / W;
+      w[u] = pr[u] = 0;
+      if (k0 + u < steps && slot < held) {
+        w[u] = *reinterpret_cast<const uint32_t *>(kr + q4_k_byte(slot, 8 * (i % W), d));
+        pr[u] = *reinterpret_cast<const uint32_t *>(kr + code_bytes + 4 * slot);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kStep; ++u) {
+      const int i = (k0 + u) * 32 + lane, slot = i / W;
+      if (k0 + u >= steps || slot < r0 || slot >= r1) continue;
+      const float2 sm = __half22float2(*reinterpret_cast<const __half2 *>(&pr[u]));
+      write8(static_cast<TO *>(a.out[0]) + at + slot * stride + 8 * (i % W), vec, w[u] & 0x0F0F0F0Fu,
+             (w[u] >> 4) & 0x0F0F0F0Fu, sm.x, sm.y);
+    }
+  }
+  const int wpd = bs / 8;
+  for (int i = lane; i < W * wpd; i += 32) {
+    const int o = i % W, t = i / W;
+    uint32_t x[8], pr[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[k] = pr[k] = 0;
+      if (8 * t < held) x[k] = reinterpret_cast<const uint32_t *>(vr)[(8 * o + k) * wpd + t];
+      if (8 * t + k < held) pr[k] = reinterpret_cast<const uint32_t *>(vr + code_bytes)[8 * t + k];
+    }
+    transpose8(x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int slot = 8 * t + k;
+      if (slot < r0 || slot >= r1) continue;
+      const float2 sm = __half22float2(*reinterpret_cast<const __half2 *>(&pr[k]));
+      const uint32_t e = k & 1 ? x[k - 1] >> 4 : x[k], od = k & 1 ? x[k] >> 4 : x[k + 1];
+      write8(static_cast<TO *>(a.out[1]) + at + slot * stride + 8 * o, vec, e & 0x0F0F0F0Fu, od & 0x0F0F0F0Fu, sm.x, sm.y);
+    }
   }
 }
 
 template <typename TIn, int NE>
 sv_status launch_append_q4(const Q4AppendArgs &a, int B, cudaStream_t s) {
   const int pages = (a.n_new + a.bs - 2) / a.bs + 1;
-  const bool vec = aligned(a.src[0], 8) && aligned(a.src[1], 8);
-  launch_k(q4_append_kernel<TIn, NE>, dim3(pages, a.H_kv, B), dim3(32 * kQaWarps), (size_t)2 * a.bs * 32 * NE, s, 1, a,
+  const bool vec = aligned(a.src[0], 16) && aligned(a.src[1], 16);
+  launch_k(q4_append_kernel<TIn, NE>, dim3(pages, a.H_kv, B), dim3(32 * kQaWarps), (size_t)a.bs * 32 * NE, s, 1, a,
            vec);
   return check_launch("kv_block_append_q4 launch");
 }
@@ -209,6 +341,29 @@ sv_status launch_append_q4_d(const Q4AppendArgs &a, int d, int B, cudaStream_t s
     case 6: return launch_append_q4<TIn, 6>(a, B, s);
     case 7: return launch_append_q4<TIn, 7>(a, B, s);
     default: return launch_append_q4<TIn, 8>(a, B, s);
+  }
+}
+
+template <typename TO, int NE>
+sv_status launch_gather_q4(const Q4GatherArgs &a, int B, cudaStream_t s) {
+  const bool vec = aligned(a.out[0], 16) && aligned(a.out[1], 16);
+  const int64_t ctas = ((int64_t)a.pages * a.H_kv + kQgWarps - 1) / kQgWarps;
+  if (ctas >= (1ll << 31)) return fail(SV_ERR_UNSUPPORTED, "kv_block_gather_q4: too many rows");
+  launch_k(q4_gather_kernel<TO, NE>, dim3((unsigned)ctas, B), dim3(32 * kQgWarps), 0, s, 1, a, vec);
+  return check_launch("kv_block_gather_q4 launch");
+}
+
+template <typename TO>
+sv_status launch_gather_q4_d(const Q4GatherArgs &a, int d, int B, cudaStream_t s) {
+  switch (d / 32) {
+    case 1: return launch_gather_q4<TO, 1>(a, B, s);
+    case 2: return launch_gather_q4<TO, 2>(a, B, s);
+    case 3: return launch_gather_q4<TO, 3>(a, B, s);
+    case 4: return launch_gather_q4<TO, 4>(a, B, s);
+    case 5: return launch_gather_q4<TO, 5>(a, B, s);
+    case 6: return launch_gather_q4<TO, 6>(a, B, s);
+    case 7: return launch_gather_q4<TO, 7>(a, B, s);
+    default: return launch_gather_q4<TO, 8>(a, B, s);
   }
 }
 
@@ -292,11 +447,10 @@ extern "C" sv_status kv_block_gather_q4(const void *k_cache, const void *v_cache
   if (B == 0 || n_rows == 0) return ok();
   a.cache[0] = static_cast<const uint8_t *>(k_cache); a.cache[1] = static_cast<const uint8_t *>(v_cache);
   a.out[0] = k_out; a.out[1] = v_out; a.block_table = block_table; a.seq_lens = seq_lens; a.start = start;
-  a.max_blocks = max_blocks_per_seq; a.n_rows = n_rows; a.H_kv = H_kv; a.d = d_head; a.bs = block_size;
+  a.max_blocks = max_blocks_per_seq; a.n_rows = n_rows; a.H_kv = H_kv; a.bs = block_size;
   a.num_blocks = num_blocks; a.status = dev_status;
+  a.pages = (int)(((int64_t)n_rows + block_size - 2) / block_size + 1);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid(n_rows, B);
-  if (out_dtype == SV_F32) launch_k(q4_gather_kernel<float>, grid, dim3(256), 0, s, 1, a);
-  else launch_k(q4_gather_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, 1, a);
-  return check_launch("kv_block_gather_q4 launch");
+  if (out_dtype == SV_F32) return launch_gather_q4_d<float>(a, d_head, B, s);
+  return launch_gather_q4_d<__nv_bfloat16>(a, d_head, B, s);
 }
