@@ -6,9 +6,10 @@
 // in 0..15, one scale and minimum per key), for query row r
 //   x_rt = scale (s_t (q_r . c_t) + m_t sum(q_r)),
 //   p'_rt = s'_t 2^(x_rt - ref_r)            (log2 domain, ref_r a running reference)
-//   out_r = [sum_t p'_rt (c'_t - 8) + sum_t p'_rt (m'_t / s'_t + 8)] / sum_t p'_rt / s'_t
-// so both products run on the bare codes and the scales enter per key. (The
-// tensor cores' accumulation rounds towards zero: with codes of one sign the
+//   out_r = [sum_t p'_rt (c'_t - z_t) + sum_t p'_rt (m'_t / s'_t + z_t)] / sum_t p'_rt / s'_t
+// so both products run on the bare codes and the scales enter per key. z_t is 0
+// for even keys and 15 for odd ones, whose terms are taken as -p' (15 - c'). (The
+// tensor cores' accumulation rounds towards zero: with terms of one sign the
 // first sum grows to some 8 sum p', and at 128K keys, where the outputs are
 // averages near zero, its rounding errors reached 1 % of the outputs.)
 //
@@ -17,10 +18,10 @@
 // binade), so a word of eight codes becomes two words of e4m3 with three
 // instructions: Q K^T runs in kind::f8f6f4 with each query row as two e4m3 terms
 // (hi + lo: 8 bits down to 2^-9 of the largest element, an error of 2^-17 of it
-// below). V codes become f16 integers: put below the exponent of 1024 (bits 0-3
-// of a half, or 4-7: then 16 times the code) and 1032 (1152) taken off, so P V
-// runs in kind::f16; the keys that come out 16 times too large have weights 16
-// times smaller. Both spread the codes of a word over several registers, so the
+// below). V codes are subnormals of f16 in bits 0-3 of a half, or 4-7: then 16
+// times as large, and those keys have weights 16 times smaller; a word becomes
+// four with five instructions (15 - c' is the complement). P V runs in
+// kind::f16. Both spread the codes of a word over several registers, so the
 // other operand of each product is stored in that order.
 // Keys on the lanes. The M = 128 side of both products is the cache: S^T = C Q^T
 // has a key per lane, O^T = C'^T P'^T a head dim per lane, and N is the number
@@ -57,8 +58,8 @@ constexpr int kTK = kTP * kBS;             // keys per tile
 constexpr int kCodes = kBS * kD / 2;       // code bytes of a record
 constexpr int kNS = 3;                     // stages of a K or V warp's ring of codes (2 KB each)
 // The keys' scales, unpacked: a K warp writes those of tile u before it hands
-// over the codes, after Q K^T of tile u - 2; that waited for P V of the pair
-// before the last, so the softmax has read every tile up to u - 6.
+// over the codes, after Q K^T of tile u - 2; that waited for the softmax of the
+// pair before the last, so every tile up to u - 6 has been read.
 constexpr int kScales = 8;
 constexpr int kScaleBytes = kTK * 20;      // a float4 and a float a key
 constexpr int kChunk = 8, kChunks = 4;     // tiles of a chunk of block offsets, and chunks in shared memory
@@ -354,15 +355,14 @@ __device__ __forceinline__ void spread_k(uint32_t w, uint32_t *o) {
   o[0] = w & 0x0F0F0F0Fu;
   o[1] = (w >> 4) & 0x0F0F0F0Fu;
 }
-// eight V codes of a word -> four f16 pairs (codes k and k + 4), each the code
-// minus 8, times 16 for odd k
+// eight V codes of a word -> four f16 pairs (codes k and k + 4): a code times
+// 2^-24 for even k, 15 minus the code times 2^-20 for odd k
 __device__ __forceinline__ void spread_v(uint32_t w, uint32_t *o) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t y = ((k < 2 ? w : w >> 8) & (k & 1 ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
-    const __half2 z = __hsub2(*reinterpret_cast<const __half2 *>(&y), __half2half2(__ushort_as_half(k & 1 ? 0x6480 : 0x6408)));
-    o[k] = *reinterpret_cast<const uint32_t *>(&z);
-  }
+  o[0] = w & 0x000F000Fu;
+  o[1] = ~w & 0x00F000F0u;
+  w >>= 8;
+  o[2] = w & 0x000F000Fu;
+  o[3] = ~w & 0x00F000F0u;
 }
 
 __device__ __forceinline__ float lg2f(float x) {
@@ -383,26 +383,35 @@ __device__ __forceinline__ void t5_mma_ts_f8(uint32_t d, uint32_t a, uint64_t b,
                "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 
-// Sums (or maxima) of v[0..NV) over the warp's lanes: lane l returns that of
-// column l * NV / 32 (NV a power of two up to 32): each step exchanges the half
-// of the columns that the other lane keeps.
-template <int NV, bool MAX>
-__device__ __forceinline__ float warp_columns(float (&v)[NV], int lane) {
-  auto join = [](float x, float y) { return MAX ? fmaxf(x, y) : x + y; };
+// Sums of v[0..NV) over the warp's lanes. While their number is even, each step
+// exchanges the half of the values that the other lane keeps; lane l is left
+// with the sums of n values from `at` on.
+template <int NV, int O = 16>
+__device__ __forceinline__ void warp_sums(float *v, int lane, int &at, int &n) {
+  if constexpr (O == 0) {
+    n = NV;
+  } else if constexpr (NV % 2 == 0) {
+    constexpr int H = NV / 2;
+    const bool up = lane & O;
 #pragma unroll
-  for (int n = NV / 2, o = 16; o >= 1; n >>= 1, o >>= 1) {
-    if (n >= 1) {
-      const bool up = lane & o;
-#pragma unroll
-      for (int k = 0; k < (n > 0 ? n : 1); ++k) {
-        const float send = up ? v[k] : v[k + n], keep = up ? v[k + n] : v[k];
-        v[k] = join(keep, __shfl_xor_sync(0xffffffffu, send, o));
-      }
-    } else {
-      v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    for (int k = 0; k < H; ++k) {
+      const float send = up ? v[k] : v[k + H], keep = up ? v[k + H] : v[k];
+      v[k] = keep + __shfl_xor_sync(0xffffffffu, send, O);
     }
+    if (up) at += H;
+    warp_sums<H, O / 2>(v, lane, at, n);
+  } else {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], O);
+    warp_sums<NV, O / 2>(v, lane, at, n);
   }
-  return v[0];
+}
+
+// Largest of the warp's values (NaN left out)
+__device__ __forceinline__ float warp_top(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
 }
 
 // N columns of this warp's lanes, N a multiple of 4
@@ -423,6 +432,12 @@ __device__ __forceinline__ void t5_ldn(uint32_t taddr, uint32_t (&r)[N]) {
   for (int k = 0; k < a; k += 16) t5_ld16(taddr + k, *reinterpret_cast<uint32_t(*)[16]>(r + k));
   if constexpr (b > a) t5_ld8(taddr + a, r + a);
   if constexpr (N > b) t5_ld4(taddr + b, r + b);
+}
+// Keeps the compiler from using loaded columns ahead of the wait before this.
+template <int N>
+__device__ __forceinline__ void keep_after(float (&r)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; k += 4) asm volatile("" : "+f"(r[k]), "+f"(r[k + 1]), "+f"(r[k + 2]), "+f"(r[k + 3]));
 }
 __device__ __forceinline__ void t5_st8(uint32_t taddr, const uint32_t *r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
@@ -466,7 +481,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   __shared__ int s_row[2][N];
   __shared__ float s_fold[2];
   __shared__ __align__(16) float s_nb[N], s_a[N];   // minus the reference; the last factor of a rescale
-  __shared__ float s_max[8][NC], s_red[8][NC][2];
+  __shared__ float s_max[8][NC], s_red[8][2 * NC];
   __shared__ __align__(8) float2 s_fin[N];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -498,7 +513,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       mbar_init(&drain[k], 1);
       mbar_init(&q_full[k], 1);
       mbar_init(&q_empty[k], 9);   // the softmax warps, and the last Q K^T
-      mbar_init(&s_full[k], 2);   // the commit, and the issuing lane itself, which has seen the K warps' scales
+      // Q K^T of the pair (its commit, and the issuing lane itself, which has seen
+      // the K warps' scales), and P V of the pair before the last
+      mbar_init(&s_full[k], 3);
       mbar_init(&p_full[k], 8);
       mbar_init(&pv_done[k], 1);
     }
@@ -635,10 +652,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           ok = q4_wait<kNapShort>(&q_full[items & 1], (items >> 1) & 1, abf, P.wait_ns) && ok;
           ++items;
         }
-        // the S buffers have been read, and their P' buffers too, once P V of the
-        // pair before the last is done: so S being there tells the softmax that
-        // P' is free
-        if (!(flag & kSecond) && pair >= 2) ok = q4_wait<kNapShort>(&pv_done[pb], ((pair >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
+        // the softmax of the pair before the last has read the S buffers
+        if (!(flag & kSecond) && pair >= 2) ok = q4_wait<kNapShort>(&p_full[pb], ((pair >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
         ok = q4_wait<kNapShort>(&kop_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
@@ -659,6 +674,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         if (flag & kEnd) ++pair;
       }
     } else {
+      if (lane < 2) mbar_arrive(&s_full[lane]);   // (no P V before the first pairs)
       for (uint32_t u = 0; u < (uint32_t)total; ++u) {
         const uint32_t bf = u & 1, pb = pair & 1;
         pages_of(u, 1, ok);
@@ -682,7 +698,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             if (kk < nv)
               t5_mma_ts(tb + Cfg::kOCol, a + 8 * kk, pd + kk * (2048 / 16), idesc_pv, !(flag & kFirst) || kk > 0 ? 1u : 0u);
           t5_commit(&vop_empty[bf]);
-          if (flag & kEnd) t5_commit(&pv_done[pb]);
+          if (flag & kEnd) {
+            t5_commit(&pv_done[pb]);
+            t5_commit(&s_full[pb]);   // the P' buffers are free: part of what the softmax of the pair after next waits for
+          }
         }
         __syncwarp();
         if (flag & kEnd) ++pair;
@@ -745,10 +764,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         copies_commit();
       };
       uint32_t src = mine, src_pairs = my_pairs;   // the stage to read
-      // K: this lane's key in its tile; a key whose V codes come out 16 times too
-      // large has a 16 times smaller weight
+      // K: this lane's key in its tile; an odd key, whose V codes come out 16 times
+      // too large, has a 16 times smaller weight, and a part 15 that was taken off
       const int key = 32 * (warp & 3) + lane;
-      const float shrink = key & 1 ? 0.0625f : 1.f, eight = key & 1 ? 128.f : 8.f;
+      const float shrink = key & 1 ? 0.0625f : 1.f, taken = key & 1 ? 240.f : 0.f;
       const bool run = !(P.withhold & SV_TEST_WITHHOLD_COPIES);
       for (int k = 1 - kNS; run && 2 * k + (int)bf < total; ++k) {   // tile 2 k + bf
         issue(2 * (k + kNS - 1) + bf);
@@ -785,7 +804,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           const float2 k2 = __half22float2(*reinterpret_cast<const __half2 *>(&kp));
           const float2 v2 = __half22float2(*reinterpret_cast<const __half2 *>(&vp));
           const float vs = fmaxf(v2.x, 5.9604645e-8f) * shrink;   // (pages never written hold zeros)
-          const float vi = rcpf(vs), vz = fmaf(v2.y, vi, eight);
+          const float vi = rcpf(vs), vz = fmaf(v2.y, vi, taken);
           const uint32_t dst = scales + (uint32_t)(2 * k + bf) % kScales * kScaleBytes;
           asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(dst + key * 16), "f"(k2.x), "f"(k2.y * P.scale_log2),
                        "f"(lg2f(vs)), "f"(vi)
@@ -817,6 +836,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     const uint32_t lanes = tb + ((uint32_t)((warp & 3) * 32) << 16);
     // row of P' that this thread's key takes (the order of the codes)
     const int prow = (t & ~7) | ((t & 3) << 1) | ((t >> 2) & 1);
+    const uint32_t sign = t & 1 ? 0x80008000u : 0u;   // odd keys' weights are negative
     Q4Walk wk = q4_walk(P, work);
     Q4Item it;
     int u = 0, i = 0;            // tiles and items done
@@ -919,16 +939,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           }
           // each column's largest weight, without the reference
           if (first) {
-            constexpr int NV = NC <= 4 ? 4 : (NC <= 8 ? 8 : (NC <= 16 ? 16 : 32));
-            float v[NV];
+            float mine = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-              v[k] = k < NC ? ((k & 1) ? fmaxf(y[0][(k < NC ? k : 0) / 2].y, y[1][(k < NC ? k : 0) / 2].y)
-                                       : fmaxf(y[0][(k < NC ? k : 0) / 2].x, y[1][(k < NC ? k : 0) / 2].x))
-                            : -INFINITY;
-            const float m = warp_columns<NV, true>(v, lane);
-            const int c = lane / (32 / NV);
-            if (lane % (32 / NV) == 0 && c < NC) s_max[warp][c] = m;
+            for (int k = 0; k < NC; ++k) {
+              const float m = warp_top(k & 1 ? fmaxf(y[0][k / 2].y, y[1][k / 2].y) : fmaxf(y[0][k / 2].x, y[1][k / 2].x));
+              if (lane == k) mine = m;
+            }
+            if (lane < NC) s_max[warp][lane] = mine;
           } else {
 #pragma unroll 1
             for (int k = 0; k < live; ++k) {
@@ -1001,7 +1018,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
               const float2 p = make_float2(ex2f(y[h][e].x), ex2f(y[h][e].y));
               l2[e] = __ffma2_rn(p, vi2, l2[e]);
               b2[e] = __ffma2_rn(p, vz2, b2[e]);
-              ph[k] = pack2<true>(p.x, p.y);
+              ph[k] = pack2<true>(p.x, p.y) ^ sign;
             }
             const uint32_t dst = p_row + h * kPBytes + ((((c_first + c) >> 3) ^ (prow & 7)) << 4);
             if (NC - c < 8)   // (what the columns of padding hold does not matter)
@@ -1021,19 +1038,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       if (gone) break;
       // ---- epilogue: sums over the keys, then a head dim per thread ---------
       {
-        constexpr int NV = NC <= 4 ? 4 : (NC <= 8 ? 8 : (NC <= 16 ? 16 : 32));
-        float v[NV];
+        float v[2 * NC];
 #pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll
-          for (int k = 0; k < NV; ++k) {
-            const float2 x = pass ? b2[(k < NC ? k : 0) / 2] : l2[(k < NC ? k : 0) / 2];
-            v[k] = k < NC ? ((k & 1) ? x.y : x.x) : 0.f;
-          }
-          const float s = warp_columns<NV, false>(v, lane);
-          const int c = lane / (32 / NV);
-          if (lane % (32 / NV) == 0 && c < NC) s_red[warp][c][pass] = s;
+        for (int k = 0; k < NC; ++k) {
+          v[k] = k & 1 ? l2[k / 2].y : l2[k / 2].x;
+          v[NC + k] = k & 1 ? b2[k / 2].y : b2[k / 2].x;
         }
+        int at = 0, n = 0;
+        warp_sums<2 * NC>(v, lane, at, n);
+#pragma unroll
+        for (int k = 0; k < 5; ++k)   // (lanes with the same sums write the same words)
+          if (k < n) s_red[warp][at + k] = v[k];
       }
       named_bar_sync(bar, 128);
       const int64_t ent = 2 * (int64_t)blockIdx.x + (it.first ? 0 : 1);
@@ -1041,8 +1056,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         float l = 0.f, b = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          l += s_red[4 * w + k][t][0];
-          b += s_red[4 * w + k][t][1];
+          l += s_red[4 * w + k][t];
+          b += s_red[4 * w + k][NC + t];
         }
         // (a row of NaN stays NaN; l is 0 only for a row without keys, which a query that sees itself never is)
         s_fin[c_first + t] = make_float2(it.whole ? 1.f / l : 1.f, b);
@@ -1055,20 +1070,20 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       named_bar_sync(bar, 128);
       ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&pv_done[(pair - 1) & 1], ((pair - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
       t5_fence_after();
-#pragma unroll 1
-      for (int c0 = 0; c0 < live && ok; c0 += 4) {
-        uint32_t o[4];
-        t5_ld4(lanes + Cfg::kOCol + c_first + c0, o);
+      if (ok) {
+        float o[NC];
+        t5_ldn(lanes + Cfg::kOCol + c_first, reinterpret_cast<uint32_t(&)[NC]>(o));
         t5_wait_ld();
+        keep_after<NC>(o);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (c0 + k >= live) break;
-          const float2 f = s_fin[c_first + c0 + k];
-          const float x = (__uint_as_float(o[k]) + f.y) * f.x;
+        for (int k = 0; k < NC; ++k) {
+          if (k >= live) break;
+          const float2 f = s_fin[c_first + k];
+          const float x = fmaf(o[k], 0x1p24f, f.y) * f.x;
           if (it.whole) {
-            static_cast<__nv_bfloat16 *>(P.out)[(int64_t)s_row[buf][c_first + c0 + k] * kD + t] = __float2bfloat16_rn(x);
+            static_cast<__nv_bfloat16 *>(P.out)[(int64_t)s_row[buf][c_first + k] * kD + t] = __float2bfloat16_rn(x);
           } else {
-            P.ws_acc[(ent * P.Rg + w * live0 + c0 + k) * kD + t] = x;
+            P.ws_acc[(ent * P.Rg + w * live0 + k) * kD + t] = x;
           }
         }
       }
