@@ -72,6 +72,7 @@ constexpr int kKWarp = 8, kVWarp = 16, kPageWarp = 24, kQkWarp = 25, kPvWarp = 2
 constexpr int kRegsSoftmax = 144, kRegsOther = 40;
 constexpr int kNapShort = 20, kNap = 60, kNapLong = 400;   // between the tries of a wait (ns)
 constexpr int kFirst = 1, kLast = 2, kEnd = 4, kSecond = 8;   // of a tile: the sequence's first or last here, its pair's last, its pair's second
+constexpr int kWhole = 1, kOpening = 2;     // of an item: the whole sequence, the first of its CTA
 constexpr float kUnset = 1e30f;            // minus the reference of a row that has met no key
 
 struct Q4Params {
@@ -81,7 +82,6 @@ struct Q4Params {
   const int32_t *block_table, *seq_lens;
   float *ws_acc;      // [2 CTAs][Rg][kD] partials (entry 2c: CTA c's first sequence, 2c + 1: its last)
   float *ws_ml;       // [2 CTAs][Rg][2]
-  int4 *ws_work;      // per range: (first sequence, first tile within it, tiles)
   int4 *ws_split;     // per range: the sequence whose first cut is the range's start (b, first tile, tiles, T), or b = -1
   uint8_t *ws_q;      // per (sequence, kv head and row group): its Q as the kernel's shared memory holds it
   float *ws_qs;       // [kN + 4] per entry: the rows' sums, then the power of two that undoes the scaling
@@ -99,9 +99,9 @@ struct Q4Params {
 template <int NC> struct Q4Cfg {   // NC query rows per softmax warpgroup
   static constexpr int kCols = (NC + 7) / 8 * 8, kN = 2 * kCols;   // columns of S and O
   static constexpr int kQ = kN * 256;   // the two e4m3 terms of a row, 128 bytes each
-  static constexpr uint32_t kKCol = 0, kVCol = 64, kSCol = 192, kOCol = 192 + 4 * kN;
+  static constexpr uint32_t kKCol = 0, kVCol = 64, kSCol = 192, kOCol = 192 + 4 * kN;   // (two O buffers)
   static constexpr int kSmem = 1024 + 2 * kQ + 4 * kPBytes + 16 * kNS * 2048 + 8 * kNS * 256 + kScales * kScaleBytes;
-  static_assert(kOCol + kN <= 512, "TMEM columns");
+  static_assert(kOCol + 2 * kN <= 512, "TMEM columns");
   static_assert(kSmem + 8192 <= 227 * 1024, "shared memory");
 };
 
@@ -190,7 +190,24 @@ __device__ int4 q4_range(const Q4Params &P, int r, int64_t T, int4 &split) {
   return w;
 }
 
-// Before the attention: the ranges (the first CTAs, a warp each), and the query
+// One warp: the tiles of all sequences, and whether a length is out of range.
+__device__ int64_t q4_all_tiles(const Q4Params &P, bool &bad) {
+  const int lane = threadIdx.x & 31;
+  int64_t T = 0;
+  bad = false;
+  for (int b0 = 0; b0 < P.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int L = b < P.B ? P.seq_lens[b] : P.n_new;
+    int nt = b < P.B ? q4_tiles(P, L) : 0;
+    bad = bad || L < P.n_new || L > P.max_blocks * kBS;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) nt += __shfl_xor_sync(0xffffffffu, nt, o);
+    T += nt;
+  }
+  return T;
+}
+
+// Before the attention: where the ranges cut sequences (the first CTAs, a warp a range), and the query
 // rows of every (sequence, kv head and row group) as two e4m3 terms in the
 // layout of the K-major 128-byte-swizzled operand, scaled by one power of two
 // that brings the largest finite element of the entry to [2^7, 2^8). The kernel
@@ -208,24 +225,14 @@ __global__ void __launch_bounds__(32 * kPrepWarps) attn_q4_prep_kernel(const __g
   pdl_trigger();
   if ((int)blockIdx.x < nrange) {
     // (the lengths are the caller's: read before the wait on the previous kernel)
-    int64_t T = 0;
-    for (int b0 = 0; b0 < P.B; b0 += 32) {
-      const int b = b0 + lane;
-      const int L = b < P.B ? P.seq_lens[b] : P.n_new;
-      int nt = b < P.B ? q4_tiles(P, L) : 0;
-      if (blockIdx.x == 0 && warp == 0 && (L < P.n_new || L > P.max_blocks * kBS)) atomic_or_status(P.status, SV_DEV_BAD_SEQ_LEN);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) nt += __shfl_xor_sync(0xffffffffu, nt, o);
-      T += nt;
-    }
+    bool bad;
+    const int64_t T = q4_all_tiles(P, bad);
     const int r = blockIdx.x * kPrepWarps + warp;
-    int4 split = make_int4(-1, 0, 0, 0), w = split;
-    if (r < P.NR) w = q4_range(P, r, T, split);
+    int4 split = make_int4(-1, 0, 0, 0);
+    if (r < P.NR) q4_range(P, r, T, split);
     pdl_wait();   // the previous kernel may still read this workspace
-    if (r < P.NR && lane == 0) {
-      P.ws_work[r] = w;
-      P.ws_split[r] = split;
-    }
+    if (blockIdx.x == 0 && warp == 0 && bad) atomic_or_status(P.status, SV_DEV_BAD_SEQ_LEN);
+    if (r < P.NR && lane == 0) P.ws_split[r] = split;
     return;
   }
   pdl_wait();
@@ -449,7 +456,7 @@ __device__ __forceinline__ void t5_st8(uint32_t taddr, const uint32_t *r) {
 // of the query rows), later the epilogue (a head dim per thread). 8-15: K codes
 // to tensor memory, 16-23: V codes (four warps per tile parity). 24: block
 // offsets and flags of the tiles ahead. 25: issues Q K^T, owns the 512 TMEM
-// columns (two K, two V, four S buffers and O). 26: issues P V (one warp for
+// columns (two K, two V, four S and two O buffers). 26: issues P V (one warp for
 // both products took 1400 cycles a tile for its waits and commits alone). 27: Q
 // of the next sequence.
 // The softmax takes two tiles at a time: its waits, its vote and its fences
@@ -470,19 +477,20 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   __shared__ __align__(16) uint32_t s_off[kChunks * kChunk * kTP];
   __shared__ int s_flag[kChunks * kChunk];   // kFirst, kLast, kEnd, kSecond, blocks of the tile << 8
   __shared__ __align__(8) uint64_t kop_full[2], kop_empty[2], vop_full[2], vop_empty[2];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], q_empty[2], o_free, drain[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], q_empty[2], o_free[2], drain[2];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ int4 s_work;
-  // per row of the two items in flight: sum(q), position (0 .. n_new - 1),
+  // per row of the items in flight: sum(q), position (0 .. n_new - 1),
   // row of q and out; per item the power of two that undoes Q's scaling
-  __shared__ __align__(16) float s_qs[2][N];
-  __shared__ __align__(16) int s_pos[2][N];
-  __shared__ int s_row[2][N];
-  __shared__ float s_fold[2];
+  __shared__ __align__(16) float s_qs[3][N];
+  __shared__ __align__(16) int s_pos[3][N];
+  __shared__ int s_row[3][N];
+  __shared__ float s_fold[3];
+  __shared__ __align__(16) int4 s_item[3];   // first tile, tiles, length in span coordinates, kWhole | kOpening
   __shared__ __align__(16) float s_nb[N], s_a[N];   // minus the reference; the last factor of a rescale
   __shared__ float s_max[8][NC], s_red[8][2 * NC];
-  __shared__ __align__(8) float2 s_fin[N];
+  __shared__ __align__(8) float2 s_fin[2][N];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Hp = P.H_kv * P.RG;
@@ -497,9 +505,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   const uint32_t pairs = ring + 16 * kNS * 2048;      // the K warps' rings of (scale, minimum) pairs
   const uint32_t scales = pairs + 8 * kNS * 256;
 
+  // Lengths and block numbers are the caller's: the ranges and the first block
+  // offsets are worked out while the kernel before this one runs.
   if (warp == 0) {
-    pdl_wait();
-    if (lane == 0) s_work = P.ws_work[range];
+    bool bad;
+    int4 split;
+    const int64_t T = q4_all_tiles(P, bad);
+    const int4 w = q4_range(P, range, T, split);
+    if (lane == 0) s_work = w;
   } else if (tid == 32) {
     for (int k = 0; k < kChunks; ++k) {
       mbar_init(&page_full[k], 1);
@@ -512,14 +525,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       mbar_init(&vop_empty[k], 1);
       mbar_init(&drain[k], 1);
       mbar_init(&q_full[k], 1);
-      mbar_init(&q_empty[k], 9);   // the softmax warps, and the last Q K^T
+      mbar_init(&q_empty[k], 1);
+      mbar_init(&o_free[k], 8);
       // Q K^T of the pair (its commit, and the issuing lane itself, which has seen
       // the K warps' scales), and P V of the pair before the last
       mbar_init(&s_full[k], 3);
       mbar_init(&p_full[k], 8);
       mbar_init(&pv_done[k], 1);
     }
-    mbar_init(&o_free, 8);
     abort_flag = 0;
     fence_mbarrier_init();
   } else if (warp == kQkWarp) {
@@ -527,8 +540,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
                  "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  pdl_wait();
-  pdl_trigger();
   t5_fence_before();
   __syncthreads();
   t5_fence_after();
@@ -553,14 +564,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   };
 
   if (warp >= kPageWarp) regs_dec<kRegsOther>();
+  if (warp != kPageWarp) pdl_wait();
+  pdl_trigger();
   if (warp == kPageWarp) {
     // ------------------------------------------------------- block numbers --
     Q4Walk wk = q4_walk(P, work);
     Q4Item it;
     bool have = q4_next(P, wk, it);
     int ti = 0;   // next tile of the item
+    bool bad = false;
     const uint32_t unit = (uint32_t)(P.block_stride >> 4);
     for (int c = 0; c * kChunk < total; ++c) {
+      if (c == kChunks) pdl_wait();   // (from here on it waits for warps that wait there)
       if (c >= kChunks &&
           !__all_sync(0xffffffffu, q4_wait<kNapLong>(&page_empty[c % kChunks], ((c / kChunks) & 1) ^ 1, abf, P.wait_ns)))
         break;
@@ -581,7 +596,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           if (e >= n * kTP) continue;
           int ph = phys[k];
           if (ph < 0 || ph >= P.num_blocks) {   // stay in bounds; the output of this sequence is flagged
-            atomic_or_status(P.status, SV_DEV_BAD_BLOCK);
+            bad = true;
             ph = 0;
           }
           const int page = e % kTP;
@@ -603,25 +618,34 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(&page_full[c % kChunks]);
     }
+    pdl_wait();
+    if (bad) atomic_or_status(P.status, SV_DEV_BAD_BLOCK);
   } else if (warp == kQWarp) {
     // ------------------------------------------------------------------- Q --
     Q4Walk wk = q4_walk(P, work);
     Q4Item it;
     int i = 0;
     while (q4_next(P, wk, it)) {
-      const int buf = i & 1;
-      if (i >= 2 && !__all_sync(0xffffffffu, q4_wait<kNapLong>(&q_empty[buf], ((i >> 1) & 1) ^ 1, abf, P.wait_ns))) break;
+      const int buf = i & 1, row = i % 3;
+      // the buffer after Q K^T of the item before the last, the rows after the
+      // epilogue of the one before that
+      bool ok = i < 2 || q4_wait<kNapLong>(&q_empty[buf], ((i >> 1) & 1) ^ 1, abf, P.wait_ns);
+      if (i >= 3) ok = q4_wait<kNapLong>(&o_free[buf ^ 1], ((i - 3) >> 1) & 1, abf, P.wait_ns) && ok;
+      if (!__all_sync(0xffffffffu, ok)) break;
       const int64_t ent = (int64_t)it.b * Hp + gp;
       const float *qs = P.ws_qs + ent * (N + 4);
       for (int col = lane; col < N; col += 32) {
         const int w = col / CP, c = col - w * CP;
         const int r = row0 + (c < (w ? rows - live0 : live0) ? w * live0 + c : 0);   // (padding: any)
         const int j = r / P.G;
-        s_qs[buf][col] = qs[col];
-        s_pos[buf][col] = j;
-        s_row[buf][col] = (it.b * P.n_new + j) * P.H_q + g * P.G + (r - j * P.G);
+        s_qs[row][col] = qs[col];
+        s_pos[row][col] = j;
+        s_row[row][col] = (it.b * P.n_new + j) * P.H_q + g * P.G + (r - j * P.G);
       }
-      if (lane == 0) s_fold[buf] = qs[N];
+      if (lane == 0) {
+        s_fold[row] = qs[N];
+        s_item[row] = make_int4(it.tile0, it.ntiles, it.span.L, (it.whole ? kWhole : 0) | (it.first ? kOpening : 0));
+      }
       __syncwarp();
       if (lane == 0) {
         mbar_arrive_expect_tx(&q_full[buf], Cfg::kQ);
@@ -681,8 +705,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         const int flag = s_flag[u % (kChunks * kChunk)];
         pages_done(u, 1);
         if (flag & kFirst) {
-          // the previous item's O has been read
-          if (items > 0) ok = q4_wait<kNapShort>(&o_free, (items - 1) & 1, abf, P.wait_ns) && ok;
+          // O of the item before the last has been read
+          if (items >= 2) ok = q4_wait<kNapShort>(&o_free[items & 1], ((items >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
           ++items;
         }
         ok = q4_wait<kNapShort>(&vop_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
@@ -696,7 +720,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
 #pragma unroll
           for (int kk = 0; kk < kTP; ++kk)   // a block's 16 keys per MMA
             if (kk < nv)
-              t5_mma_ts(tb + Cfg::kOCol, a + 8 * kk, pd + kk * (2048 / 16), idesc_pv, !(flag & kFirst) || kk > 0 ? 1u : 0u);
+              t5_mma_ts(tb + Cfg::kOCol + ((items - 1) & 1) * N, a + 8 * kk, pd + kk * (2048 / 16), idesc_pv, !(flag & kFirst) || kk > 0 ? 1u : 0u);
           t5_commit(&vop_empty[bf]);
           if (flag & kEnd) {
             t5_commit(&pv_done[pb]);
@@ -837,26 +861,53 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     // row of P' that this thread's key takes (the order of the codes)
     const int prow = (t & ~7) | ((t & 3) << 1) | ((t >> 2) & 1);
     const uint32_t sign = t & 1 ? 0x80008000u : 0u;   // odd keys' weights are negative
-    Q4Walk wk = q4_walk(P, work);
-    Q4Item it;
     int u = 0, i = 0;            // tiles and items done
     uint32_t pair = 0;
     // A wait that gave up (ok false) only shows at the warpgroup's next vote, so
     // that its four warps leave together.
     bool ok = true;
-    while (q4_next(P, wk, it)) {
-      const int buf = i & 1;
-      ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&q_full[buf], (i >> 1) & 1, abf, P.wait_ns)) && ok;
+    // The epilogue's second part, a head dim per thread: O of an item, once its
+    // last P V is done; it is taken after the next item's first pair, which hides
+    // that P V.
+    struct { bool pending, whole; uint32_t pair; int i; int64_t ent; } done = {false, false, 0, 0, 0};
+    auto finish = [&] {
+      done.pending = false;
+      ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&pv_done[done.pair & 1], (done.pair >> 1) & 1, abf, P.wait_ns)) && ok;
+      if (!ok) return;
+      t5_fence_after();
+      float o[NC];
+      t5_ldn(lanes + Cfg::kOCol + (done.i & 1) * N + c_first, reinterpret_cast<uint32_t(&)[NC]>(o));
+      t5_wait_ld();
+      keep_after<NC>(o);
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        if (k >= live) break;
+        const float2 f = s_fin[done.i & 1][c_first + k];
+        const float x = fmaf(o[k], 0x1p24f, f.y) * f.x;
+        if (done.whole)
+          static_cast<__nv_bfloat16 *>(P.out)[(int64_t)s_row[done.i % 3][c_first + k] * kD + t] = __float2bfloat16_rn(x);
+        else
+          P.ws_acc[(done.ent * P.Rg + w * live0 + k) * kD + t] = x;
+      }
+      t5_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free[done.i & 1]);
+    };
+    while (u < total) {
+      const int buf = i % 3;
+      const uint32_t o_col = lanes + Cfg::kOCol + (i & 1) * N + c_first;
+      ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&q_full[i & 1], (i >> 1) & 1, abf, P.wait_ns)) && ok;
       const float fold = P.scale_log2 * s_fold[buf];
-      const int L = it.span.L;
+      const int4 it = s_item[buf];
+      const int tile0 = it.x, ntiles = it.y, L = it.z;
       const int edge0 = L - P.n_new - kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
       if (t < NC) s_nb[c_first + t] = 0.f;
       float2 l2[NC / 2], b2[NC / 2];
 #pragma unroll
       for (int k = 0; k < NC / 2; ++k) l2[k] = b2[k] = make_float2(0.f, 0.f);
       bool gone = bar_or(bar, 128, !ok);
-      for (int ti = 0; ti < it.ntiles && !gone; ++pair) {
-        const int nt = min(it.ntiles - ti, 2);
+      for (int ti = 0; ti < ntiles && !gone; ++pair) {
+        const int nt = min(ntiles - ti, 2);
         // S of this pair, and with it the keys' scales and P' buffers that P V two
         // pairs ago has read
         const int pb = pair & 1;
@@ -867,7 +918,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         uint32_t reach[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {   // this thread's two keys
-          const int key0 = (it.tile0 + ti + h) * kTK, key = key0 + t;
+          const int key0 = (tile0 + ti + h) * kTK, key = key0 + t;
           const uint32_t src = scales + (uint32_t)(u + h) % kScales * kScaleBytes;
           asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(ka[h]), "=f"(kb[h]), "=f"(vc[h]), "=f"(vi[h]) : "r"(src + t * 16));
           asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vz[h]) : "r"(src + kTK * 16 + t * 4));
@@ -914,7 +965,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             }
           }
         };
-        bool first = ti == 0;
+        const bool first = ti == 0;
         for (int again = 0;; ++again) {
           scores(0);
           if (nt > 1) {
@@ -979,7 +1030,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             s_a[c_first + t] = a;
           }
           named_bar_sync(bar, 128);
-          if (!first) {
+          if (first) {
+#pragma unroll
+            for (int k = 0; k < NC; k += 4) {
+              const float4 nb = *reinterpret_cast<const float4 *>(&s_nb[c_first + k]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                y[h][k / 2] = __fadd2_rn(y[h][k / 2], make_float2(nb.x, nb.y));
+                y[h][k / 2 + 1] = __fadd2_rn(y[h][k / 2 + 1], make_float2(nb.z, nb.w));
+              }
+            }
+            break;
+          } else {
 #pragma unroll
             for (int k = 0; k < NC; k += 4) {
               const float4 a = *reinterpret_cast<const float4 *>(&s_a[c_first + k]);
@@ -994,7 +1056,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
 #pragma unroll 1
             for (int k = 0; k < live; ++k) {
               uint32_t o;
-              const uint32_t at = lanes + Cfg::kOCol + c_first + k;
+              const uint32_t at = o_col + k;
               asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o) : "r"(at));
               t5_wait_ld();
               o = __float_as_uint(__uint_as_float(o) * s_a[c_first + k]);
@@ -1034,9 +1096,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         if (lane == 0) mbar_arrive(&p_full[pb]);
         ti += nt;
         u += nt;
+        if (done.pending) finish();
       }
       if (gone) break;
-      // ---- epilogue: sums over the keys, then a head dim per thread ---------
+      // ---- epilogue, first part: sums over the keys -------------------------
       {
         float v[2 * NC];
 #pragma unroll
@@ -1051,7 +1114,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           if (k < n) s_red[warp][at + k] = v[k];
       }
       named_bar_sync(bar, 128);
-      const int64_t ent = 2 * (int64_t)blockIdx.x + (it.first ? 0 : 1);
+      const int64_t ent = 2 * (int64_t)blockIdx.x + (it.w & kOpening ? 0 : 1);
       if (t < live) {
         float l = 0.f, b = 0.f;
 #pragma unroll
@@ -1060,41 +1123,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           b += s_red[4 * w + k][NC + t];
         }
         // (a row of NaN stays NaN; l is 0 only for a row without keys, which a query that sees itself never is)
-        s_fin[c_first + t] = make_float2(it.whole ? 1.f / l : 1.f, b);
-        if (!it.whole) {
+        s_fin[i & 1][c_first + t] = make_float2(it.w & kWhole ? 1.f / l : 1.f, b);
+        if (!(it.w & kWhole)) {
           const int64_t e = ent * P.Rg + w * live0 + t;
           P.ws_ml[2 * e] = -s_nb[c_first + t];
           P.ws_ml[2 * e + 1] = l;
         }
       }
-      named_bar_sync(bar, 128);
-      ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&pv_done[(pair - 1) & 1], ((pair - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
-      t5_fence_after();
-      if (ok) {
-        float o[NC];
-        t5_ldn(lanes + Cfg::kOCol + c_first, reinterpret_cast<uint32_t(&)[NC]>(o));
-        t5_wait_ld();
-        keep_after<NC>(o);
-#pragma unroll
-        for (int k = 0; k < NC; ++k) {
-          if (k >= live) break;
-          const float2 f = s_fin[c_first + k];
-          const float x = fmaf(o[k], 0x1p24f, f.y) * f.x;
-          if (it.whole) {
-            static_cast<__nv_bfloat16 *>(P.out)[(int64_t)s_row[buf][c_first + k] * kD + t] = __float2bfloat16_rn(x);
-          } else {
-            P.ws_acc[(ent * P.Rg + w * live0 + k) * kD + t] = x;
-          }
-        }
-      }
-      t5_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&o_free);
-        mbar_arrive(&q_empty[buf]);
-      }
+      done = {true, (it.w & kWhole) != 0, pair - 1, i, ent};
       ++i;
     }
+    named_bar_sync(bar, 128);
+    if (done.pending) finish();
   }
   __syncthreads();
   if (tid == 0 && *abf) atomic_or_status(P.status, SV_DEV_TIMEOUT);
@@ -1211,7 +1251,7 @@ int q4_cols(const Q4Plan &p) { return 2 * (((p.Rg + 1) / 2 + 7) / 8 * 8); }
 size_t q4_ws_bytes(const Q4Plan &p, int B, int H_kv) {
   const size_t ent = (size_t)2 * p.C * p.Rg, qent = (size_t)B * H_kv * p.RG, n = q4_cols(p);
   return align_up(ent * kD * sizeof(float), 256) + align_up(ent * 2 * sizeof(float), 256) +
-         2 * align_up((size_t)p.NR * sizeof(int4), 256) + align_up(qent * n * 256, 256) +
+         align_up((size_t)p.NR * sizeof(int4), 256) + align_up(qent * n * 256, 256) +
          align_up(qent * (n + 4) * sizeof(float), 256);
 }
 
@@ -1288,8 +1328,6 @@ extern "C" sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const 
   P.ws_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + align_up(ent * kD * sizeof(float), 256));
   uint8_t *at = reinterpret_cast<uint8_t *>(P.ws_ml) + align_up(ent * 2 * sizeof(float), 256);
   P.ws_split = reinterpret_cast<int4 *>(at);
-  at += align_up((size_t)p.NR * sizeof(int4), 256);
-  P.ws_work = reinterpret_cast<int4 *>(at);
   at += align_up((size_t)p.NR * sizeof(int4), 256);
   P.ws_q = at;
   at += align_up((size_t)B * H_kv * p.RG * q4_cols(p) * 256, 256);
