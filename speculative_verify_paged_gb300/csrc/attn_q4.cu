@@ -900,7 +900,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       const float fold = P.scale_log2 * s_fold[buf];
       const int4 it = s_item[buf];
       const int tile0 = it.x, ntiles = it.y, L = it.z;
-      const int edge0 = L - P.n_new - kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
+      const int edge0 = L - P.n_new - 2 * kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
       if (t < NC) s_nb[c_first + t] = 0.f;
       float2 l2[NC / 2], b2[NC / 2];
 #pragma unroll
@@ -913,24 +913,25 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         const int pb = pair & 1;
         ok = q4_wait<kNapShort>(&s_full[pb], (pair >> 1) & 1, abf, P.wait_ns) && ok;
         float ka[2], kb[2], vc[2], vi[2], vz[2];
-        bool edge[2];
-        int j0[2];
-        uint32_t reach[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {   // this thread's two keys
-          const int key0 = (tile0 + ti + h) * kTK, key = key0 + t;
           const uint32_t src = scales + (uint32_t)(u + h) % kScales * kScaleBytes;
           asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(ka[h]), "=f"(kb[h]), "=f"(vc[h]), "=f"(vi[h]) : "r"(src + t * 16));
           asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vz[h]) : "r"(src + kTK * 16 + t * 4));
           ka[h] *= fold;
-          // A tile that ends past the oldest query or holds keys that a window
-          // has left: position j sees the key iff 0 <= j - j0 < reach. A key
-          // that no position sees (past the end, or between sinks and window)
-          // may hold anything.
-          edge[h] = key0 >= edge0 || key0 < edge1;
-          j0[h] = 0;
-          reach[h] = 0;
-          if (edge[h]) {
+        }
+        // A pair that ends past the oldest query or holds keys that a window has
+        // left: position j sees a key iff 0 <= j - j0 < reach. A key that no
+        // position sees (past the end, or between sinks and window) may hold
+        // anything.
+        const int key0 = (tile0 + ti) * kTK;
+        const bool edge = key0 >= edge0 || key0 < edge1;
+        int j0[2] = {0, 0};
+        uint32_t reach[2] = {0, 0};
+        if (edge) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int key = key0 + h * kTK + t;
             j0[h] = key - (L - P.n_new);
             reach[h] = P.window > 0 && key >= P.sinks ? (uint32_t)P.window : 0x80000000u;
             if (key >= L || (uint32_t)(P.n_new - 1 - j0[h]) >= reach[h] + (uint32_t)(P.n_new - 1)) vi[h] = vz[h] = 0.f;
@@ -954,7 +955,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             y[h][k / 2] = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), ka2, z0);
             y[h][k / 2 + 1] = __ffma2_rn(make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), ka2, z1);
           }
-          if (edge[h]) {
+          if (edge) {
 #pragma unroll
             for (int k = 0; k < NC; k += 4) {
               const int4 j = *reinterpret_cast<const int4 *>(&s_pos[buf][c_first + k]);
@@ -1008,7 +1009,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
                 asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(xs) : "r"(s_col + h * N + k));
                 t5_wait_ld();
                 const float z = fmaf(__uint_as_float(xs), ka[h], fmaf(s_qs[buf][c_first + k], kb[h], vc[h]));
-                if (!edge[h] || (uint32_t)(s_pos[buf][c_first + k] - j0[h]) < reach[h]) m = fmaxf(m, z);
+                if (!edge || (uint32_t)(s_pos[buf][c_first + k] - j0[h]) < reach[h]) m = fmaxf(m, z);
               }
               m = warp_max(m);
               if (lane == 0) s_max[warp][k] = m;
