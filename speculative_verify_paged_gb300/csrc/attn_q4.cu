@@ -716,11 +716,16 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         if (elect_one()) {
           const uint64_t pd = t5_desc(p_smem + (2 * pb + (flag & kSecond ? 1 : 0)) * kPBytes, 16, 1024);
           const uint32_t a = tb + Cfg::kVCol + bf * 64;
+          const uint32_t d = tb + Cfg::kOCol + ((items - 1) & 1) * N;
+          t5_mma_ts(d, a, pd, idesc_pv, flag & kFirst ? 0u : 1u);   // a block's 16 keys per MMA
           const int nv = flag >> 8;   // blocks past the end have no weight
+          if (nv == kTP) {
 #pragma unroll
-          for (int kk = 0; kk < kTP; ++kk)   // a block's 16 keys per MMA
-            if (kk < nv)
-              t5_mma_ts(tb + Cfg::kOCol + ((items - 1) & 1) * N, a + 8 * kk, pd + kk * (2048 / 16), idesc_pv, !(flag & kFirst) || kk > 0 ? 1u : 0u);
+            for (int kk = 1; kk < kTP; ++kk) t5_mma_ts(d, a + 8 * kk, pd + kk * (2048 / 16), idesc_pv, 1u);
+          } else {
+#pragma unroll 1
+            for (int kk = 1; kk < nv; ++kk) t5_mma_ts(d, a + 8 * kk, pd + kk * (2048 / 16), idesc_pv, 1u);
+          }
           t5_commit(&vop_empty[bf]);
           if (flag & kEnd) {
             t5_commit(&pv_done[pb]);
