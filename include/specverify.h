@@ -280,7 +280,8 @@ sv_status spec_verify_attn_tree(const void *q, sv_dtype q_dtype,
  *   block that is read but that no query sees do not reach the output
  *   whatever their values. Other arguments, layouts and support as for
  *   spec_verify_attn; the workspace is
- *   spec_verify_attn_window_workspace_size(...) bytes.
+ *   spec_verify_attn_window_workspace_size(...) bytes. max_blocks_per_seq *
+ *   block_size must be below 2^30 (SV_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------ */
 size_t spec_verify_attn_window_workspace_size(int B, int n_new, int H_q, int H_kv, int d_head,
                                               int max_blocks_per_seq, int block_size,
@@ -318,7 +319,8 @@ sv_status spec_verify_attn_window(const void *q, sv_dtype q_dtype,
  * aligned. A non-NULL layout gives the strides between records in BYTES
  * (block_stride, head_stride: multiples of 16, at least a record; slot_stride
  * 0), e.g. a per-layer slice of a larger pool. sv_copy_blocks copies such
- * pages like any others.
+ * pages like any others. max_blocks_per_seq * block_size must be below 2^30
+ * (SV_ERR_UNSUPPORTED).
  *
  * kv_block_append_q4
  *   kv_block_append into 4-bit pools. A row x (one token, one kv head, all of
@@ -345,11 +347,14 @@ sv_status spec_verify_attn_window(const void *q, sv_dtype q_dtype,
  *   spec_verify_attn over 4-bit pools, with the window and sinks of
  *   spec_verify_attn_window (window = 0: every key). q, out: SV_BF16 or
  *   SV_F32. bf16 queries with d_head 128, block_size 16 and
- *   (H_q/H_kv) * n_new <= 128 run on the tensor cores (q must then be 16-byte
- *   aligned, else SV_ERR_INVALID_ARG); every other supported shape runs on a
- *   CUDA-core kernel with fp32 arithmetic. The workspace is
- *   spec_verify_attn_q4_workspace_size(...) bytes, 256-byte aligned; its
- *   contents need no initialisation.
+ *   (H_q/H_kv) * n_new <= 128 run on the tensor cores (q and out must then be
+ *   16-byte aligned, else SV_ERR_INVALID_ARG; beyond 48 query rows per kv head
+ *   the cache is read once for every 48); every other supported shape, and
+ *   pools of more than 64 GB, run on a CUDA-core kernel with fp32 arithmetic.
+ *   The workspace is spec_verify_attn_q4_workspace_size(...) bytes, 256-byte
+ *   aligned; its contents need no initialisation. It holds the converted
+ *   queries and partial results of one call: calls that may run at the same
+ *   time need one each.
  * ------------------------------------------------------------------------ */
 size_t sv_q4_record_bytes(int d_head, int block_size);
 

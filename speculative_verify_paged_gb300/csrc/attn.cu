@@ -2561,6 +2561,8 @@ extern "C" sv_status spec_verify_attn_window(const void *q, sv_dtype q_dtype, co
                                              sv_dtype out_dtype, void *workspace, size_t workspace_bytes,
                                              int32_t *dev_status, sv_stream_t stream) {
   if (window < 0 || sinks < 0) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_window: negative window or sinks");
+  if (max_blocks_per_seq > 0 && block_size > 0 && !capacity_ok(max_blocks_per_seq, block_size))
+    return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn_window: max_blocks_per_seq * block_size must be below 2^30");
   if (kv_dtype != SV_F32 && kv_dtype != SV_BF16 && kv_dtype != SV_FP8_E4M3)
     return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn_window: caches must be f32, bf16 or fp8");
   return attn_impl(q, q_dtype, k_cache, v_cache, kv_dtype, layout, k_scale, v_scale, block_table,

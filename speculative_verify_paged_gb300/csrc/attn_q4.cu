@@ -1298,6 +1298,8 @@ extern "C" sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const 
                                          int window, int sinks, void *out, sv_dtype out_dtype, void *workspace,
                                          size_t workspace_bytes, int32_t *dev_status, sv_stream_t stream) {
   if (window < 0 || sinks < 0) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_q4: negative window or sinks");
+  if (max_blocks_per_seq > 0 && block_size > 0 && !capacity_ok(max_blocks_per_seq, block_size))
+    return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn_q4: max_blocks_per_seq * block_size must be below 2^30");
   Q4Plan p = {};
   const bool sizes_ok = B >= 0 && n_new >= 1 && H_q >= 1 && H_kv >= 1 && H_q % H_kv == 0 && num_blocks >= 1 &&
                         max_blocks_per_seq >= 1 && H_kv <= 65535 && block_size >= 1;

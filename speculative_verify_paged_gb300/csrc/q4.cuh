@@ -71,6 +71,10 @@ inline int span_blocks_max(int max_blocks, int n_new, int window, int sinks, int
   return (int)(n < max_blocks ? n : max_blocks);
 }
 
+// Positions and lengths are 32-bit integers and tiles run past the end: the
+// entry points here take tables of less than 2^30 tokens a sequence.
+inline bool capacity_ok(int max_blocks, int bs) { return (int64_t)max_blocks * bs < (1ll << 30); }
+
 // Marks a 4-bit pool inside the library (the pools carry their own scales, so
 // no entry point takes it as an element type).
 constexpr sv_dtype kQ4 = static_cast<sv_dtype>(4);

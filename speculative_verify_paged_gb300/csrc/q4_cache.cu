@@ -84,14 +84,19 @@ __global__ void __launch_bounds__(32 * kQaWarps) q4_append_kernel(const __grid_c
   const int group = threadIdx.x / LPR, li = threadIdx.x % LPR;
   const int bs = a.bs;
   const int L = a.seq_lens[b];
+  // (every CTA waits, so that this grid ends after the one before it)
   if (L < a.n_new || L > a.max_blocks * bs) {
+    pdl_wait();
     if (threadIdx.x == 0 && g == 0 && blockIdx.x == 0) atomic_or_status(a.status, SV_DEV_BAD_SEQ_LEN);
     return;
   }
   const int first = L - a.n_new;
   const int page = first / bs + (int)blockIdx.x;
   const int s0 = max(first - page * bs, 0), s1 = min(L - page * bs, bs);   // slots written
-  if (s0 >= s1) return;
+  if (s0 >= s1) {
+    pdl_wait();
+    return;
+  }
   const int phys = a.block_table[(int64_t)b * a.max_blocks + page];
   const int nr = s1 - s0;
   const int64_t row_stride = (int64_t)a.H_kv * d;
@@ -413,6 +418,8 @@ extern "C" sv_status kv_block_append_q4(const void *k_new, const void *v_new, sv
   if (new_dtype != SV_F32 && new_dtype != SV_BF16)
     return fail(SV_ERR_UNSUPPORTED, "kv_block_append_q4: new rows must be f32 or bf16");
   if (B > 65535 || H_kv > 65535) return fail(SV_ERR_UNSUPPORTED, "kv_block_append_q4: B or H_kv too large");
+  if (!capacity_ok(max_blocks_per_seq, block_size))
+    return fail(SV_ERR_UNSUPPORTED, "kv_block_append_q4: max_blocks_per_seq * block_size must be below 2^30");
   Q4AppendArgs a = {};
   const sv_status rc = q4_check("kv_block_append_q4", k_cache, v_cache, layout, H_kv, d_head, block_size,
                                 &a.block_stride, &a.head_stride);
@@ -440,6 +447,8 @@ extern "C" sv_status kv_block_gather_q4(const void *k_cache, const void *v_cache
   if (out_dtype != SV_F32 && out_dtype != SV_BF16)
     return fail(SV_ERR_UNSUPPORTED, "kv_block_gather_q4: rows are read back as f32 or bf16");
   if (B > 65535 || H_kv > 65535) return fail(SV_ERR_UNSUPPORTED, "kv_block_gather_q4: B or H_kv too large");
+  if (!capacity_ok(max_blocks_per_seq, block_size))
+    return fail(SV_ERR_UNSUPPORTED, "kv_block_gather_q4: max_blocks_per_seq * block_size must be below 2^30");
   Q4GatherArgs a = {};
   const sv_status rc = q4_check("kv_block_gather_q4", k_cache, v_cache, layout, H_kv, d_head, block_size,
                                 &a.block_stride, &a.head_stride);

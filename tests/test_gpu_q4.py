@@ -69,6 +69,48 @@ def test_append_special_values(lib):
     assert torch.isfinite(back).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_append_ties(lib, dtype):
+    # values on and next to the middle between two codes, for scales of every kind of mantissa
+    g = torch.Generator().manual_seed(2)
+    s = torch.rand((64, 1), generator=g) * 3 + 0.01
+    half = torch.arange(128) % 31 / 2.0
+    x = half[None, :] * s
+    x[:32] = half[None, :] * torch.tensor([1.0, 0.5, 3.0, 7.0]).repeat(8)[:, None]
+    x[32:48] = torch.nextafter(x[32:48], torch.full((), 100.0))
+    x += torch.tensor([0.0, 1.0, -2.5, 0.125]).repeat(16)[:, None]
+    x[:, 0], x[:, 30] = x.min(-1).values, x.max(-1).values
+    x = x[None, :, None].contiguous().to(dtype)
+    table, lens = torch.tensor([[3, 0, 2, 1]], dtype=torch.int32), [64]
+    kc, vc = q4_pools(4, 1, 128, 16, seed=3)
+    kd, vd = kc.to(DEV), vc.to(DEV)
+    lib.kv_block_append_q4(x.to(DEV), (-x).to(DEV), kd, vd, table.to(DEV), i32(lens))
+    want = oq4.append(kc.numpy(), vc.numpy(), x.float().numpy(), -x.float().numpy(), table.numpy(), lens)
+    assert np.array_equal(kd.cpu().numpy(), want[0]) and np.array_equal(vd.cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_at_any_element(lib, dtype):
+    # new rows and read-back buffers that start at an odd element of their storage
+    H, n, lens = 3, 21, [40, 21]
+    table, total = table_for(lens, 16, seed=5)
+    kc, vc = (p.to(DEV) for p in q4_pools(total, H, 128, 16, seed=5))
+    k2, v2 = kc.clone(), vc.clone()
+    size = 2 * n * H * 128
+    flat = torch.randn(2 * size + 8, generator=torch.Generator().manual_seed(5)).to(dtype).to(DEV)
+    k, v = (flat[o:o + size].view(2, n, H, 128) for o in (1, size + 3))
+    lib.kv_block_append_q4(k, v, kc, vc, table.to(DEV), i32(lens))
+    lib.kv_block_append_q4(k.clone(), v.clone(), k2, v2, table.to(DEV), i32(lens))
+    assert torch.equal(kc, k2) and torch.equal(vc, v2)
+    dst = torch.full((2 * size + 8,), 7.0, dtype=dtype, device=DEV)
+    out = [dst[o:o + size].view(2, n, H, 128) for o in (1, size + 3)]
+    start = i32([25, -4])
+    lib.kv_block_gather_q4(kc, vc, table.to(DEV), i32(lens), start, n, 128, k_out=out[0], v_out=out[1])
+    want = lib.kv_block_gather_q4(kc, vc, table.to(DEV), i32(lens), start, n, 128, out_dtype=dtype)
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    assert (dst[[0, size + 1, size + 2] + list(range(2 * size + 3, 2 * size + 8))] == 7).all()
+
+
 def test_append_bad_lengths_and_blocks_leave_the_pools(lib):
     table = torch.tensor([[0, 1], [99, 99], [2, 3], [4, -1]], dtype=torch.int32, device=DEV)
     kc, vc = (p.to(DEV) for p in q4_pools(6, 2, 128, 16, seed=5))
@@ -202,6 +244,47 @@ def test_attention_large(lib, B, H_q, H_kv, n, lo, hi, window, sinks):
     assert int(st) == 0 and torch.isfinite(out).all()
     rows = sorted({0, B // 2, B - 1, int(np.argmax(lens)), int(np.argmin(lens))})[:4]
     check_q4_attention(out, *q4_reference(q, kc, vc, table, lens, 16, window, sinks, rows), rows=rows)
+
+
+@pytest.mark.parametrize("H_q,H_kv,n", [(32, 8, 1), (64, 8, 5), (16, 1, 2), (64, 8, 8)])
+def test_attention_many_short_sequences(lib, H_q, H_kv, n):
+    # far more sequences than CTAs, most of them a part of one tile, some empty or with a bad length
+    B = 500
+    lens = torch.randint(n, 200, (B,), generator=torch.Generator().manual_seed(n)).tolist()
+    lens[7::50] = [2000] * 10
+    table, total = table_for(lens, 16, seed=2)
+    bad = {3: 0, 4: -5, 100: n - 1, 499: 16 * table.shape[1] + 1}
+    kc, vc = q4_pools(total, H_kv, 128, 16, seed=3)
+    q = torch.randn((B, n, H_q, 128), generator=torch.Generator().manual_seed(9)).bfloat16()
+    given = [bad.get(b, L) for b, L in enumerate(lens)]
+    st = status0()
+    out = torch.full_like(q, 7.0, device=DEV)
+    lib.spec_verify_attn_q4(q.to(DEV), kc.to(DEV), vc.to(DEV), table.to(DEV), i32(given), out=out, status=st)
+    assert int(st) == 1
+    assert (out[list(bad)] == 7).all()
+    rows = [b for b in range(B) if b not in bad]
+    check_q4_attention(out, *q4_reference(q, kc, vc, table, lens, 16, rows=rows), rows=rows)
+
+
+def test_attention_wait_runs_out_then_next_call_is_correct(lib):
+    # the code copies are withheld, so every wait on them can only end by its limit (2 ms)
+    lens = [700, 5, 3000]
+    table, total = table_for(lens, 16, seed=2)
+    kc, vc = q4_pools(total, 2, 128, 16, seed=3)
+    q = torch.randn((3, 4, 16, 128), generator=torch.Generator().manual_seed(9)).bfloat16()
+    args = (q.to(DEV), kc.to(DEV), vc.to(DEV), table.to(DEV), i32(lens))
+    st = status0()
+    try:
+        lib.test_hooks(2_000_000, lib.SV_TEST_WITHHOLD_COPIES)
+        lib.spec_verify_attn_q4(*args, status=st)
+        torch.cuda.synchronize()
+    finally:
+        lib.test_hooks(0, 0)
+    assert int(st) & lib.SV_DEV_TIMEOUT
+    st.zero_()
+    out = lib.spec_verify_attn_q4(*args, status=st)
+    assert int(st) == 0
+    check_q4_attention(out, *q4_reference(q, kc, vc, table, lens, 16))
 
 
 def test_attention_rising_scores_and_extreme_rows(lib):

@@ -107,6 +107,19 @@ def test_workspace_sizes(lib):
         assert lib.spec_verify_attn_q4_workspace_size(*bad) == 0
 
 
+def test_capacity_limit(lib):
+    # positions are 32-bit: 2^30 tokens of table a sequence and more are refused, whatever the lengths
+    big = 1 << 26
+    assert attn_q4(lib, mb=big) == 2 and b"2^30" in lib.sv_last_error_string()
+    assert attn_q4(lib, mb=2 ** 31 - 1, qdt=0, odt=0) == 2
+    assert lib.kv_block_append_q4(FAKE, FAKE, 1, FAKE, FAKE, None, FAKE, big, FAKE, 2, 5, 2, 128, 16, 10, NULL, NULL) == 2
+    assert lib.kv_block_gather_q4(FAKE, FAKE, None, FAKE, big, FAKE, FAKE, 2, 5, 2, 128, 16, 10, FAKE, FAKE, 1, NULL,
+                                  NULL) == 2
+    assert lib.spec_verify_attn_window(FAKE, 1, FAKE, FAKE, 1, None, NULL, NULL, FAKE, big, FAKE, 2, 5, 8, 2, 128, 16, 10,
+                                       0.1, 4, 0, FAKE, 1, FAKE, 1 << 40, NULL, NULL) == 2
+    assert b"2^30" in lib.sv_last_error_string()
+
+
 # ---------------------------------------------------------------- binding ---
 
 REC = 16 * 68
