@@ -41,6 +41,57 @@ __device__ __forceinline__ void load8(const T *p, bool vec, T (&x)[8]) {
   }
 }
 
+// Eight elements of no row: NaN, which takes no part in anything.
+template <typename T>
+__device__ __forceinline__ void no_row(T (&x)[8]) {
+#pragma unroll
+  for (int k = 0; k < (int)sizeof(T) * 2; ++k)
+    reinterpret_cast<uint32_t *>(x)[k] = sizeof(T) == 2 ? 0x7FC07FC0u : 0x7FC00000u;
+}
+
+// Smallest and largest of the 8 LPR elements of a group of lanes, NaN left out
+// (no more than NaN: NaN or mn > mx).
+template <int LPR>
+__device__ __forceinline__ void extremes(const __nv_bfloat16 (&x)[8], float &mn, float &mx) {
+  // exact in bf16; (min, -max) travel together
+  const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(x);
+  const __nv_bfloat162 lo = __hmin2(__hmin2(p[0], p[1]), __hmin2(p[2], p[3]));
+  const __nv_bfloat162 hi = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+  uint32_t a, b;
+  memcpy(&a, &lo, 4);
+  memcpy(&b, &hi, 4);
+  b ^= 0x80008000u;
+  const uint32_t c = __byte_perm(a, b, 0x5410), d = __byte_perm(a, b, 0x7632);
+  __nv_bfloat162 v, o;
+  memcpy(&v, &c, 4);
+  memcpy(&o, &d, 4);
+  v = __hmin2(v, o);
+#pragma unroll
+  for (int k = LPR / 2; k > 0; k >>= 1) {
+    memcpy(&a, &v, 4);
+    a = __shfl_xor_sync(0xffffffffu, a, k);
+    memcpy(&o, &a, 4);
+    v = __hmin2(v, o);
+  }
+  mn = __low2float(v);
+  mx = -__high2float(v);
+}
+template <int LPR>
+__device__ __forceinline__ void extremes(const float (&x)[8], float &mn, float &mx) {
+  mn = INFINITY;   // (fminf and fmaxf leave NaN out)
+  mx = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    mn = fminf(mn, x[k]);
+    mx = fmaxf(mx, x[k]);
+  }
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) {
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  }
+}
+
 // x: eight words of eight 4-bit values, word j nibble i. Afterwards nibbles of
 // equal place lie in equal bytes: bits 0-3 of byte k of x[i] and x[i + 1] (i
 // even) are nibble i of words 2k and 2k + 1, bits 4-7 their nibble i + 1.
@@ -67,9 +118,11 @@ __device__ __forceinline__ void transpose8(uint32_t (&x)[8]) {
 // memory, where the CTA turns words along the head dim into words along the
 // slots. Words of a V record that also hold codes of other slots are read and
 // merged; no other CTA of the call touches the record.
-// The quotient (x - m) / s is first taken as (x - m) times 1 / s, within 3 ulp
-// of the IEEE quotient; only where that lies within 2^-16 of the middle between
-// two codes (3 ulp are at most 3 x 2^-20 below 16) is the division done.
+// The quotient (x - m) / s is first taken as 15 times ((x - m) times 1 / (15 s),
+// kept within 0..1). The reciprocal's error is 2^-23, the product's 2^-24 and the
+// IEEE quotient's 2^-24 relative, so the two differ by less than 15 x 2^-22; only
+// where a value lies within 2^-16 of the middle between two codes is the division
+// done.
 template <typename TIn, int NE>
 __global__ void __launch_bounds__(32 * kQaWarps) q4_append_kernel(const __grid_constant__ Q4AppendArgs a, bool vec) {
   constexpr int d = 32 * NE, W = d / 8;                              // words of a row
@@ -108,6 +161,7 @@ __global__ void __launch_bounds__(32 * kQaWarps) q4_append_kernel(const __grid_c
 #pragma unroll
     for (int u = 0; u < kQaRows; ++u) {
       const int i = i0 + u * kGroups + group;
+      no_row(xr[u]);
       if (i < 2 * nr && on) load8(static_cast<const TIn *>(a.src[i >= nr]) + src0 + (i >= nr ? i - nr : i) * row_stride, vec, xr[u]);
     }
     // everything read so far is the caller's; the pools may still be read by
@@ -129,38 +183,35 @@ __global__ void __launch_bounds__(32 * kQaWarps) q4_append_kernel(const __grid_c
       const int i = i0 + u * kGroups + group;
       const bool live = i < 2 * nr;
       const int kv = i >= nr ? 1 : 0, slot = s0 + i - kv * nr;
-      float x[8], mn = INFINITY, mx = -INFINITY;   // (fminf and fmaxf leave NaN out)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        x[k] = live && on ? to_f32(xr[u][k]) : NAN;
-        mn = fminf(mn, x[k]);
-        mx = fmaxf(mx, x[k]);
-      }
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) {
-        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      }
+      float mn, mx;
+      extremes<LPR>(xr[u], mn, mx);
       if (!(mn <= mx)) mn = mx = 0.f;   // nothing but NaN
       const __half mh = __float2half_rn(fminf(fmaxf(mn, -65504.f), 65504.f));
       const float m = __half2float(mh);
       const __half sh = __hmax(__float2half_rn(fminf(__fdiv_rn(__fsub_rn(mx, m), 15.f), 65504.f)), __ushort_as_half(1));
-      const float s = __half2float(sh), inv = __fdiv_rn(1.f, s);
+      const float s = __half2float(sh);
+      float inv;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(15.f * s));
       uint32_t w = 0;
       float near = 0.f;   // distance from a code, the largest of the eight
+      const float2 m2 = make_float2(-m, -m), magic2 = make_float2(kMagic, kMagic), less2 = make_float2(-kMagic, -kMagic);
 #pragma unroll
-      for (int k = 7; k >= 0; --k) {
-        const float t = fminf(fmaxf(__fmul_rn(__fsub_rn(x[k], m), inv), 0.f), 15.f);   // (NaN: 0)
-        const float r = __fadd_rn(t, kMagic);
-        near = fmaxf(near, fabsf(__fsub_rn(t, __fsub_rn(r, kMagic))));
-        w = (w << 4) + __float_as_uint(r);   // (the bits of kMagic come off below)
+      for (int k = 6; k >= 0; k -= 2) {
+        const float2 y = __fadd2_rn(make_float2(to_f32(xr[u][k]), to_f32(xr[u][k + 1])), m2);
+        const float2 t = make_float2(__saturatef(y.x * inv), __saturatef(y.y * inv));   // (NaN: 0)
+        const float2 r = __ffma2_rn(t, make_float2(15.f, 15.f), magic2);
+        const float2 c = __fadd2_rn(r, less2);
+        const float2 e = __ffma2_rn(t, make_float2(-15.f, -15.f), c);
+        near = fmaxf(fmaxf(near, fabsf(e.x)), fabsf(e.y));
+        w = (w << 4) + __float_as_uint(r.y);   // (the bits of kMagic come off below)
+        w = (w << 4) + __float_as_uint(r.x);
       }
       w -= 0x4B400000u * 0x11111111u;
       if (near > 0.5f - 0x1p-16f) {
         w = 0;
 #pragma unroll
         for (int k = 7; k >= 0; --k)
-          w = (w << 4) + (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[k], m), s)), 0.f), 15.f);
+          w = (w << 4) + (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(to_f32(xr[u][k]), m), s)), 0.f), 15.f);
       }
       if (!live) continue;
       if (on) {
