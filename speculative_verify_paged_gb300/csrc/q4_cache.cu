@@ -26,7 +26,7 @@ struct Q4AppendArgs {
 };
 
 constexpr int kQaWarps = 4;
-constexpr int kQaRows = 4;   // rows a group of lanes loads before it works on the first
+constexpr int kQaRows = 2;   // rows of K, and of V, that a group of lanes takes at a time
 
 // Eight consecutive elements of a row as floats; `vec`: 16-byte aligned.
 template <typename T>
@@ -124,7 +124,7 @@ __device__ __forceinline__ void transpose8(uint32_t (&x)[8]) {
 // where a value lies within 2^-16 of the middle between two codes is the division
 // done.
 template <typename TIn, int NE>
-__global__ void __launch_bounds__(32 * kQaWarps) q4_append_kernel(const __grid_constant__ Q4AppendArgs a, bool vec) {
+__global__ void __launch_bounds__(32 * kQaWarps, sizeof(TIn) == 2 ? 12 : 8) q4_append_kernel(const __grid_constant__ Q4AppendArgs a, bool vec) {
   constexpr int d = 32 * NE, W = d / 8;                              // words of a row
   constexpr int LPR = NE == 1 ? 4 : NE == 2 ? 8 : NE <= 4 ? 16 : 32;  // lanes of a row (those past W idle)
   constexpr int kGroups = 32 * kQaWarps / LPR;
@@ -154,44 +154,55 @@ __global__ void __launch_bounds__(32 * kQaWarps) q4_append_kernel(const __grid_c
   const int nr = s1 - s0;
   const int64_t row_stride = (int64_t)a.H_kv * d;
   const int64_t src0 = (((int64_t)b * a.n_new + (page * bs + s0 - first)) * a.H_kv + g) * d + li * 8;
+  const int64_t rec0 = (int64_t)phys * a.block_stride + (int64_t)g * a.head_stride;
   const bool on = li < W;
-  bool waited = false;
-  for (int i0 = 0; i0 < 2 * nr; i0 += kQaRows * kGroups) {
-    alignas(16) TIn xr[kQaRows][8];
+  for (int i0 = 0; i0 < nr; i0 += kQaRows * kGroups) {
+    // (rows 0 .. kQaRows - 1 are of K, the others of V)
+    alignas(16) TIn xr[2 * kQaRows][8];
 #pragma unroll
-    for (int u = 0; u < kQaRows; ++u) {
-      const int i = i0 + u * kGroups + group;
+    for (int u = 0; u < 2 * kQaRows; ++u) {
+      const int i = i0 + u % kQaRows * kGroups + group;
       no_row(xr[u]);
-      if (i < 2 * nr && on) load8(static_cast<const TIn *>(a.src[i >= nr]) + src0 + (i >= nr ? i - nr : i) * row_stride, vec, xr[u]);
+      if (i < nr && on) load8(static_cast<const TIn *>(a.src[u / kQaRows]) + src0 + i * row_stride, vec, xr[u]);
     }
     // everything read so far is the caller's; the pools may still be read by
     // the previous kernel of the stream
-    if (!waited) {
+    if (i0 == 0) {
       pdl_wait();
-      waited = true;
       if (phys < 0 || phys >= a.num_blocks) {
         if (threadIdx.x == 0) atomic_or_status(a.status, SV_DEV_BAD_BLOCK);
         return;
       }
     }
-    uint8_t *rec[2];
+    // lane u of the group works out row u's pair
+    float mn = 0.f, mx = 0.f;
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) rec[kv] = a.cache[kv] + (int64_t)phys * a.block_stride + (int64_t)g * a.head_stride;
+    for (int u = 0; u < 2 * kQaRows; ++u) {
+      float lo, hi;
+      extremes<LPR>(xr[u], lo, hi);
+      if (li == u) {
+        mn = lo;
+        mx = hi;
+      }
+    }
+    if (!(mn <= mx)) mn = mx = 0.f;   // nothing but NaN
+    const __half mh = __float2half_rn(fminf(fmaxf(mn, -65504.f), 65504.f));
+    const __half sh = __hmax(__float2half_rn(fminf(__fdiv_rn(__fsub_rn(mx, __half2float(mh)), 15.f), 65504.f)),
+                             __ushort_as_half(1));
+    const uint32_t own = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(mh) << 16);
+    float own_inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(own_inv) : "f"(15.f * __half2float(sh)));
+    if (li < 2 * kQaRows) {
+      const int i = i0 + li % kQaRows * kGroups + group;
+      if (i < nr)
+        *reinterpret_cast<uint32_t *>((li < kQaRows ? a.cache[0] : a.cache[1]) + rec0 + q4_code_bytes(d, bs) + 4 * (s0 + i)) = own;
+    }
 #pragma unroll
-    for (int u = 0; u < kQaRows; ++u) {
-      if (i0 + u * kGroups >= 2 * nr) break;   // (the same for the whole CTA)
-      const int i = i0 + u * kGroups + group;
-      const bool live = i < 2 * nr;
-      const int kv = i >= nr ? 1 : 0, slot = s0 + i - kv * nr;
-      float mn, mx;
-      extremes<LPR>(xr[u], mn, mx);
-      if (!(mn <= mx)) mn = mx = 0.f;   // nothing but NaN
-      const __half mh = __float2half_rn(fminf(fmaxf(mn, -65504.f), 65504.f));
-      const float m = __half2float(mh);
-      const __half sh = __hmax(__float2half_rn(fminf(__fdiv_rn(__fsub_rn(mx, m), 15.f), 65504.f)), __ushort_as_half(1));
-      const float s = __half2float(sh);
-      float inv;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(15.f * s));
+    for (int u = 0; u < 2 * kQaRows; ++u) {
+      const int i = i0 + u % kQaRows * kGroups + group, slot = s0 + i;
+      const uint32_t pair = __shfl_sync(0xffffffffu, own, u, LPR);
+      const float inv = __shfl_sync(0xffffffffu, own_inv, u, LPR);
+      const float m = __half2float(__ushort_as_half((unsigned short)(pair >> 16)));
       uint32_t w = 0;
       float near = 0.f;   // distance from a code, the largest of the eight
       const float2 m2 = make_float2(-m, -m), magic2 = make_float2(kMagic, kMagic), less2 = make_float2(-kMagic, -kMagic);
@@ -208,19 +219,15 @@ __global__ void __launch_bounds__(32 * kQaWarps) q4_append_kernel(const __grid_c
       }
       w -= 0x4B400000u * 0x11111111u;
       if (near > 0.5f - 0x1p-16f) {
+        const float s = __half2float(__ushort_as_half((unsigned short)pair));
         w = 0;
 #pragma unroll
         for (int k = 7; k >= 0; --k)
           w = (w << 4) + (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(to_f32(xr[u][k]), m), s)), 0.f), 15.f);
       }
-      if (!live) continue;
-      if (on) {
-        if (kv) words[slot * W + li] = w;
-        else *reinterpret_cast<uint32_t *>(rec[0] + q4_k_byte(slot, 8 * li, d)) = w;
-      }
-      if (li == 0) {
-        const uint32_t pair = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(mh) << 16);
-        *reinterpret_cast<uint32_t *>(rec[kv] + q4_code_bytes(d, bs) + 4 * slot) = pair;
+      if (i < nr && on) {
+        if (u >= kQaRows) words[slot * W + li] = w;
+        else *reinterpret_cast<uint32_t *>(a.cache[0] + rec0 + q4_k_byte(slot, 8 * li, d)) = w;
       }
     }
   }
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(32 * kQaWarps) q4_append_kernel(const __grid_c
     }
   }
   __syncthreads();
-  uint8_t *rec = a.cache[1] + (int64_t)phys * a.block_stride + (int64_t)g * a.head_stride;
+  uint8_t *rec = a.cache[1] + rec0;
   if (nr == bs) {
     for (int i = threadIdx.x; i < d * bs / 32; i += 32 * kQaWarps)
       reinterpret_cast<uint4 *>(rec)[i] = reinterpret_cast<const uint4 *>(image)[i];
