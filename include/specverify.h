@@ -348,8 +348,8 @@ sv_status spec_verify_attn_window(const void *q, sv_dtype q_dtype,
  *   spec_verify_attn_window (window = 0: every key). q, out: SV_BF16 or
  *   SV_F32. bf16 queries with d_head 128, block_size 16 and
  *   (H_q/H_kv) * n_new <= 128 run on the tensor cores (q and out must then be
- *   16-byte aligned, else SV_ERR_INVALID_ARG; beyond 48 query rows per kv head
- *   the cache is read once for every 48); every other supported shape, and
+ *   16-byte aligned, else SV_ERR_INVALID_ARG; beyond 64 query rows per kv head
+ *   the cache is read once for every 64); every other supported shape, and
  *   pools of more than 64 GB, run on a CUDA-core kernel with fp32 arithmetic.
  *   The workspace is spec_verify_attn_q4_workspace_size(...) bytes, 256-byte
  *   aligned; its contents need no initialisation. It holds the converted

@@ -33,7 +33,13 @@
 //
 // What bounds it: 136 bytes per key and kv head leave about 820 SM cycles per
 // 128-key tile at the measured HBM bandwidth, for 2 x 128 x 128 codes to unpack
-// and 128 R exponentials.
+// and 128 R exponentials. Measured: 64 sequences of 1024-8192 keys, 5 positions,
+// 64/8 heads take 128 us (330 MB, 2.6 TB/s; 49 us at the bandwidth), 128K keys
+// with 8 positions 86 us, about 1700 cycles a tile of 40 rows. A tile takes 4270
+// warp instructions (V 485, K 361, the exponentials and P' 625, the scores 700,
+// the rest copies, waits and bookkeeping) at 62 % of the issue slots; the softmax
+// warps are the ones the others wait for, and each part that is taken out for a
+// test gains 3 to 9 %.
 //
 // Work: the tiles of all sequences end to end are cut into equal ranges, one
 // per SM and kv head; each CTA (one per SM) streams through the sequences of its
@@ -59,7 +65,7 @@ constexpr int kCodes = kBS * kD / 2;       // code bytes of a record
 constexpr int kNS = 3;                     // stages of a K or V warp's ring of codes (2 KB each)
 // The keys' scales, unpacked: a K warp writes those of tile u before it hands
 // over the codes, after Q K^T of tile u - 2; that waited for the softmax of the
-// pair before the last, so every tile up to u - 6 has been read.
+// step before the last, so every tile up to u - 6 has been read.
 constexpr int kScales = 8;
 constexpr int kScaleBytes = kTK * 20;      // a float4 and a float a key
 constexpr int kChunk = 8, kChunks = 4;     // tiles of a chunk of block offsets, and chunks in shared memory
@@ -67,11 +73,10 @@ constexpr int kPBytes = kTK * 128;         // a P' buffer: 128 bytes (64 columns
 constexpr int kWarps = 28;
 constexpr int kKWarp = 8, kVWarp = 16, kPageWarp = 24, kQkWarp = 25, kPvWarp = 26, kQWarp = 27;
 // Registers: launched at 72 a thread; the K, V and service warps hand over 32
-// each so that the softmax warps hold two tiles' scores and two sums per
-// column (256 x 144 + 640 x 40 <= 896 x 72).
+// each so that the softmax warps hold a step's scores and two sums per column
+// (256 x 144 + 640 x 40 <= 896 x 72).
 constexpr int kRegsSoftmax = 144, kRegsOther = 40;
-constexpr int kNapShort = 20, kNap = 60, kNapLong = 400;   // between the tries of a wait (ns)
-constexpr int kFirst = 1, kLast = 2, kEnd = 4, kSecond = 8;   // of a tile: the sequence's first or last here, its pair's last, its pair's second
+constexpr int kFirst = 1, kLast = 2, kEnd = 4, kSecond = 8;   // of a tile: the sequence's first or last here, its step's last or second
 constexpr int kWhole = 1, kOpening = 2;     // of an item: the whole sequence, the first of its CTA
 constexpr float kUnset = 1e30f;            // minus the reference of a row that has met no key
 
@@ -98,9 +103,10 @@ struct Q4Params {
 
 template <int NC> struct Q4Cfg {   // NC query rows per softmax warpgroup
   static constexpr int kCols = (NC + 7) / 8 * 8, kN = 2 * kCols;   // columns of S and O
+  static constexpr int kT = NC > 24 ? 1 : 2;   // tiles of a softmax step (their scores stay in registers)
   static constexpr int kQ = kN * 256;   // the two e4m3 terms of a row, 128 bytes each
-  static constexpr uint32_t kKCol = 0, kVCol = 64, kSCol = 192, kOCol = 192 + 4 * kN;   // (two O buffers)
-  static constexpr int kSmem = 1024 + 2 * kQ + 4 * kPBytes + 16 * kNS * 2048 + 8 * kNS * 256 + kScales * kScaleBytes;
+  static constexpr uint32_t kKCol = 0, kVCol = 64, kSCol = 192, kOCol = 192 + 2 * kT * kN;   // (two O buffers)
+  static constexpr int kSmem = 1024 + 2 * kQ + 2 * kT * kPBytes + 16 * kNS * 2048 + 8 * kNS * 256 + kScales * kScaleBytes;
   static_assert(kOCol + 2 * kN <= 512, "TMEM columns");
   static_assert(kSmem + 8192 <= 227 * 1024, "shared memory");
 };
@@ -321,17 +327,13 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool v) {
   return r != 0;
 }
 
-// Bounded wait; a wait that has to sleep gives up at once after any earlier
-// one of the CTA gave up. It sleeps NS nanoseconds between its tries: try_wait
-// comes back after some hundred cycles whatever its time hint, and trying
-// again at once, the warps that wait issued as many instructions as those that
-// work.
-template <int NS>
+// Bounded wait; gives up at once after any earlier one of the CTA gave up. (Naps
+// of 20 to 800 ns between the tries change neither the time nor the number of
+// instructions: try_wait itself sleeps.)
 __device__ __forceinline__ bool q4_wait(uint64_t *bar, uint32_t phase, volatile int *abort_flag, uint64_t limit_ns) {
   if (mbar_try_wait(bar, phase)) return true;
   const uint64_t t0 = global_ns();
   do {
-    __nanosleep(NS);
     if (mbar_try_wait(bar, phase)) return true;
   } while (!*abort_flag && global_ns() - t0 <= limit_ns);
   *abort_flag = 1;
@@ -459,8 +461,10 @@ __device__ __forceinline__ void t5_st8(uint32_t taddr, const uint32_t *r) {
 // columns (two K, two V, four S and two O buffers). 26: issues P V (one warp for
 // both products took 1400 cycles a tile for its waits and commits alone). 27: Q
 // of the next sequence.
-// The softmax takes two tiles at a time: its waits, its vote and its fences
-// cost as much as the arithmetic of a tile.
+// The softmax takes two tiles at a time (one with more than 48 rows, whose
+// scores would not fit in registers): its waits, its vote and its fences cost as
+// much as the arithmetic of a tile. More than two gain nothing, as V has two
+// buffers.
 // Every warp copies what it reads: a K warp the two blocks that its keys lie
 // in (and the keys' pairs of K and V, which it unpacks for the softmax), a V
 // warp its 32 head dims of the tile's eight blocks; so a copy is waited for by
@@ -470,7 +474,7 @@ __device__ __forceinline__ void t5_st8(uint32_t taddr, const uint32_t *r) {
 template <int NC>
 __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_constant__ Q4Params P) {
   using Cfg = Q4Cfg<NC>;
-  constexpr int N = Cfg::kN, CP = Cfg::kCols;
+  constexpr int N = Cfg::kN, CP = Cfg::kCols, T = Cfg::kT;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t page_full[kChunks], page_empty[kChunks];
   // offsets of the blocks of the tiles ahead in 16-byte units, even blocks of a tile first
@@ -501,7 +505,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t q_smem = smem_u32(smem);
   const uint32_t p_smem = q_smem + 2 * Cfg::kQ;
-  const uint32_t ring = p_smem + 4 * kPBytes;
+  const uint32_t ring = p_smem + 2 * T * kPBytes;
   const uint32_t pairs = ring + 16 * kNS * 2048;      // the K warps' rings of (scale, minimum) pairs
   const uint32_t scales = pairs + 8 * kNS * 256;
 
@@ -510,8 +514,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   if (warp == 0) {
     bool bad;
     int4 split;
-    const int64_t T = q4_all_tiles(P, bad);
-    const int4 w = q4_range(P, range, T, split);
+    const int64_t all = q4_all_tiles(P, bad);
+    const int4 w = q4_range(P, range, all, split);
     if (lane == 0) s_work = w;
   } else if (tid == 32) {
     for (int k = 0; k < kChunks; ++k) {
@@ -527,8 +531,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       mbar_init(&q_full[k], 1);
       mbar_init(&q_empty[k], 1);
       mbar_init(&o_free[k], 8);
-      // Q K^T of the pair (its commit, and the issuing lane itself, which has seen
-      // the K warps' scales), and P V of the pair before the last
+      // Q K^T of the step (its commit, and the issuing lane itself, which has seen
+      // the K warps' scales), and P V of the step before the last
       mbar_init(&s_full[k], 3);
       mbar_init(&p_full[k], 8);
       mbar_init(&pv_done[k], 1);
@@ -553,7 +557,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   // every step-th tile; done with a chunk's last tile it hands the chunk back.
   auto pages_of = [&](uint32_t u, uint32_t step, bool &ok) -> const uint32_t * {
     if (u % kChunk < step)
-      ok = q4_wait<kNapShort>(&page_full[u / kChunk % kChunks], (u / (kChunk * kChunks)) & 1, abf, P.wait_ns) && ok;
+      ok = q4_wait(&page_full[u / kChunk % kChunks], (u / (kChunk * kChunks)) & 1, abf, P.wait_ns) && ok;
     return s_off + u % (kChunk * kChunks) * kTP;
   };
   auto pages_done = [&](uint32_t u, uint32_t step) {
@@ -577,7 +581,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     for (int c = 0; c * kChunk < total; ++c) {
       if (c == kChunks) pdl_wait();   // (from here on it waits for warps that wait there)
       if (c >= kChunks &&
-          !__all_sync(0xffffffffu, q4_wait<kNapLong>(&page_empty[c % kChunks], ((c / kChunks) & 1) ^ 1, abf, P.wait_ns)))
+          !__all_sync(0xffffffffu, q4_wait(&page_empty[c % kChunks], ((c / kChunks) & 1) ^ 1, abf, P.wait_ns)))
         break;
       for (int filled = 0; filled < kChunk && have;) {
         const int n = min(kChunk - filled, it.ntiles - ti);
@@ -605,7 +609,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         if (lane < n) {
           const int tt = ti + lane;
           s_flag[c % kChunks * kChunk + filled + lane] =
-              (tt == 0 ? kFirst : 0) | (tt == it.ntiles - 1 ? kLast | kEnd : 0) | (tt & 1 ? kEnd | kSecond : 0) |
+              (tt == 0 ? kFirst : 0) | (tt == it.ntiles - 1 ? kLast | kEnd : 0) | (tt % T == T - 1 ? kEnd : 0) | (tt % T ? kSecond : 0) |
               min(kTP, it.span.nblk - (it.tile0 + tt) * kTP) << 8;
         }
         filled += n;
@@ -629,8 +633,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       const int buf = i & 1, row = i % 3;
       // the buffer after Q K^T of the item before the last, the rows after the
       // epilogue of the one before that
-      bool ok = i < 2 || q4_wait<kNapLong>(&q_empty[buf], ((i >> 1) & 1) ^ 1, abf, P.wait_ns);
-      if (i >= 3) ok = q4_wait<kNapLong>(&o_free[buf ^ 1], ((i - 3) >> 1) & 1, abf, P.wait_ns) && ok;
+      bool ok = i < 2 || q4_wait(&q_empty[buf], ((i >> 1) & 1) ^ 1, abf, P.wait_ns);
+      if (i >= 3) ok = q4_wait(&o_free[buf ^ 1], ((i - 3) >> 1) & 1, abf, P.wait_ns) && ok;
       if (!__all_sync(0xffffffffu, ok)) break;
       const int64_t ent = (int64_t)it.b * Hp + gp;
       const float *qs = P.ws_qs + ent * (N + 4);
@@ -664,26 +668,26 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     // Q K^T, f16 for P V), f32 accumulators, M = 128.
     constexpr uint32_t idesc_qk = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
     constexpr uint32_t idesc_pv = idesc_qk | (1u << 16);   // B = P'^T with the rows contiguous
-    uint32_t items = 0, pair = 0;   // items started, pairs done
+    uint32_t items = 0, step = 0;   // items started, steps done
     bool ok = true;
     if (warp == kQkWarp) {
       for (uint32_t u = 0; u < (uint32_t)total; ++u) {
-        const uint32_t bf = u & 1, pb = pair & 1;
+        const uint32_t bf = u & 1, pb = step & 1;
         pages_of(u, 1, ok);
         const int flag = s_flag[u % (kChunks * kChunk)];
         pages_done(u, 1);
         if (flag & kFirst) {
-          ok = q4_wait<kNapShort>(&q_full[items & 1], (items >> 1) & 1, abf, P.wait_ns) && ok;
+          ok = q4_wait(&q_full[items & 1], (items >> 1) & 1, abf, P.wait_ns) && ok;
           ++items;
         }
-        // the softmax of the pair before the last has read the S buffers
-        if (!(flag & kSecond) && pair >= 2) ok = q4_wait<kNapShort>(&p_full[pb], ((pair >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
-        ok = q4_wait<kNapShort>(&kop_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
+        // the softmax of the step before the last has read the S buffers
+        if (!(flag & kSecond) && step >= 2) ok = q4_wait(&p_full[pb], ((step >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
+        ok = q4_wait(&kop_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
         if (elect_one()) {
           const uint64_t qd = t5_desc(q_smem + ((items - 1) & 1) * Cfg::kQ, 16, 1024);
-          const uint32_t d = tb + Cfg::kSCol + (2 * pb + (flag & kSecond ? 1 : 0)) * N, a = tb + Cfg::kKCol + bf * 32;
+          const uint32_t d = tb + Cfg::kSCol + (T * pb + (flag & kSecond ? 1 : 0)) * N, a = tb + Cfg::kKCol + bf * 32;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)   // 32 head dims per MMA, the hi terms of Q and then the lo terms
             t5_mma_ts_f8(d, a + 8 * (kk & 3), qd + (kk >> 2) * (N * 128 / 16) + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
@@ -695,26 +699,26 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           if (flag & kLast) t5_commit(&q_empty[(items - 1) & 1]);
         }
         __syncwarp();
-        if (flag & kEnd) ++pair;
+        if (flag & kEnd) ++step;
       }
     } else {
-      if (lane < 2) mbar_arrive(&s_full[lane]);   // (no P V before the first pairs)
+      if (lane < 2) mbar_arrive(&s_full[lane]);   // (no P V before the first steps)
       for (uint32_t u = 0; u < (uint32_t)total; ++u) {
-        const uint32_t bf = u & 1, pb = pair & 1;
+        const uint32_t bf = u & 1, pb = step & 1;
         pages_of(u, 1, ok);
         const int flag = s_flag[u % (kChunks * kChunk)];
         pages_done(u, 1);
         if (flag & kFirst) {
           // O of the item before the last has been read
-          if (items >= 2) ok = q4_wait<kNapShort>(&o_free[items & 1], ((items >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
+          if (items >= 2) ok = q4_wait(&o_free[items & 1], ((items >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
           ++items;
         }
-        ok = q4_wait<kNapShort>(&vop_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
-        if (!(flag & kSecond)) ok = q4_wait<kNapShort>(&p_full[pb], (pair >> 1) & 1, abf, P.wait_ns) && ok;
+        ok = q4_wait(&vop_full[bf], (u >> 1) & 1, abf, P.wait_ns) && ok;
+        if (!(flag & kSecond)) ok = q4_wait(&p_full[pb], (step >> 1) & 1, abf, P.wait_ns) && ok;
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
         if (elect_one()) {
-          const uint64_t pd = t5_desc(p_smem + (2 * pb + (flag & kSecond ? 1 : 0)) * kPBytes, 16, 1024);
+          const uint64_t pd = t5_desc(p_smem + (T * pb + (flag & kSecond ? 1 : 0)) * kPBytes, 16, 1024);
           const uint32_t a = tb + Cfg::kVCol + bf * 64;
           const uint32_t d = tb + Cfg::kOCol + ((items - 1) & 1) * N;
           t5_mma_ts(d, a, pd, idesc_pv, flag & kFirst ? 0u : 1u);   // a block's 16 keys per MMA
@@ -729,11 +733,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           t5_commit(&vop_empty[bf]);
           if (flag & kEnd) {
             t5_commit(&pv_done[pb]);
-            t5_commit(&s_full[pb]);   // the P' buffers are free: part of what the softmax of the pair after next waits for
+            t5_commit(&s_full[pb]);   // the P' buffers are free: part of what the softmax of the step after next waits for
           }
         }
         __syncwarp();
-        if (flag & kEnd) ++pair;
+        if (flag & kEnd) ++step;
       }
     }
     // every MMA issued has completed before TMEM can be released
@@ -803,7 +807,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         if (k < 0) continue;
         copies_wait<kNS - 1>();
         __syncwarp();
-        if (ok && k > 0) ok = q4_wait<kNap>(empty, (k & 1) ^ 1, abf, P.wait_ns);
+        if (ok && k > 0) ok = q4_wait(empty, (k & 1) ^ 1, abf, P.wait_ns);
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
 #pragma unroll 2
@@ -867,17 +871,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     const int prow = (t & ~7) | ((t & 3) << 1) | ((t >> 2) & 1);
     const uint32_t sign = t & 1 ? 0x80008000u : 0u;   // odd keys' weights are negative
     int u = 0, i = 0;            // tiles and items done
-    uint32_t pair = 0;
+    uint32_t step = 0;
     // A wait that gave up (ok false) only shows at the warpgroup's next vote, so
     // that its four warps leave together.
     bool ok = true;
     // The epilogue's second part, a head dim per thread: O of an item, once its
-    // last P V is done; it is taken after the next item's first pair, which hides
+    // last P V is done; it is taken after the next item's first step, which hides
     // that P V.
-    struct { bool pending, whole; uint32_t pair; int i; int64_t ent; } done = {false, false, 0, 0, 0};
+    struct { bool pending, whole; uint32_t step; int i; int64_t ent; } done = {false, false, 0, 0, 0};
     auto finish = [&] {
       done.pending = false;
-      ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&pv_done[done.pair & 1], (done.pair >> 1) & 1, abf, P.wait_ns)) && ok;
+      ok = __all_sync(0xffffffffu, q4_wait(&pv_done[done.step & 1], (done.step >> 1) & 1, abf, P.wait_ns)) && ok;
       if (!ok) return;
       t5_fence_after();
       float o[NC];
@@ -901,41 +905,41 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     while (u < total) {
       const int buf = i % 3;
       const uint32_t o_col = lanes + Cfg::kOCol + (i & 1) * N + c_first;
-      ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&q_full[i & 1], (i >> 1) & 1, abf, P.wait_ns)) && ok;
+      ok = __all_sync(0xffffffffu, q4_wait(&q_full[i & 1], (i >> 1) & 1, abf, P.wait_ns)) && ok;
       const float fold = P.scale_log2 * s_fold[buf];
       const int4 it = s_item[buf];
       const int tile0 = it.x, ntiles = it.y, L = it.z;
-      const int edge0 = L - P.n_new - 2 * kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
+      const int edge0 = L - P.n_new - T * kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
       if (t < NC) s_nb[c_first + t] = 0.f;
       float2 l2[NC / 2], b2[NC / 2];
 #pragma unroll
       for (int k = 0; k < NC / 2; ++k) l2[k] = b2[k] = make_float2(0.f, 0.f);
       bool gone = bar_or(bar, 128, !ok);
-      for (int ti = 0; ti < ntiles && !gone; ++pair) {
-        const int nt = min(ntiles - ti, 2);
-        // S of this pair, and with it the keys' scales and P' buffers that P V two
-        // pairs ago has read
-        const int pb = pair & 1;
-        ok = q4_wait<kNapShort>(&s_full[pb], (pair >> 1) & 1, abf, P.wait_ns) && ok;
-        float ka[2], kb[2], vc[2], vi[2], vz[2];
+      for (int ti = 0; ti < ntiles && !gone; ++step) {
+        const int nt = min(ntiles - ti, T);
+        // S of this step, and with it the keys' scales and P' buffers that P V two
+        // steps ago has read
+        const int pb = step & 1;
+        ok = q4_wait(&s_full[pb], (step >> 1) & 1, abf, P.wait_ns) && ok;
+        float ka[T], kb[T], vc[T], vi[T], vz[T];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {   // this thread's two keys
+        for (int h = 0; h < T; ++h) {   // this thread's keys
           const uint32_t src = scales + (uint32_t)(u + h) % kScales * kScaleBytes;
           asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(ka[h]), "=f"(kb[h]), "=f"(vc[h]), "=f"(vi[h]) : "r"(src + t * 16));
           asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vz[h]) : "r"(src + kTK * 16 + t * 4));
           ka[h] *= fold;
         }
-        // A pair that ends past the oldest query or holds keys that a window has
+        // A step that ends past the oldest query or holds keys that a window has
         // left: position j sees a key iff 0 <= j - j0 < reach. A key that no
         // position sees (past the end, or between sinks and window) may hold
         // anything.
         const int key0 = (tile0 + ti) * kTK;
         const bool edge = key0 >= edge0 || key0 < edge1;
-        int j0[2] = {0, 0};
-        uint32_t reach[2] = {0, 0};
+        int j0[T] = {};
+        uint32_t reach[T] = {};
         if (edge) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < T; ++h) {
             const int key = key0 + h * kTK + t;
             j0[h] = key - (L - P.n_new);
             reach[h] = P.window > 0 && key >= P.sinks ? (uint32_t)P.window : 0x80000000u;
@@ -944,8 +948,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         }
         ok = __all_sync(0xffffffffu, ok);
         t5_fence_after();
-        const uint32_t s_col = lanes + Cfg::kSCol + 2 * pb * N + c_first;
-        float2 y[2][NC / 2];   // log2 weights, minus the reference
+        const uint32_t s_col = lanes + Cfg::kSCol + T * pb * N + c_first;
+        float2 y[T][NC / 2];   // log2 weights, minus the reference
         auto scores = [&](int h) {
           const float2 ka2 = make_float2(ka[h], ka[h]), kb2 = make_float2(kb[h], kb[h]), vc2 = make_float2(vc[h], vc[h]);
           uint32_t x[NC];
@@ -974,21 +978,25 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         const bool first = ti == 0;
         for (int again = 0;; ++again) {
           scores(0);
-          if (nt > 1) {
-            scores(1);
-          } else {
+          if constexpr (T > 1) {
+            if (nt > 1) {
+              scores(1);
+            } else {
 #pragma unroll
-            for (int k = 0; k < NC / 2; ++k) y[1][k] = make_float2(-INFINITY, -INFINITY);
+              for (int k = 0; k < NC / 2; ++k) y[1][k] = make_float2(-INFINITY, -INFINITY);
+            }
           }
           if (again) break;
-          // The first pair of a sequence sets the references (they are 0 so
+          // The first step of a sequence sets the references (they are 0 so
           // far); later ones move when a weight exceeds them by more than 2^8
           // (f16 holds 2^16). All four warps decide together, as they share O.
           float top = fmaxf(y[0][0].x, y[0][0].y);
 #pragma unroll
           for (int k = 1; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[0][k].x), y[0][k].y);
+          if constexpr (T > 1) {
 #pragma unroll
-          for (int k = 0; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[1][k].x), y[1][k].y);
+            for (int k = 0; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[1][k].x), y[1][k].y);
+          }
           if (!bar_or(bar, 128, first || top > 8.f || !ok)) break;
           if (bar_or(bar, 128, !ok)) {
             gone = true;
@@ -999,7 +1007,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             float mine = -INFINITY;
 #pragma unroll
             for (int k = 0; k < NC; ++k) {
-              const float m = warp_top(k & 1 ? fmaxf(y[0][k / 2].y, y[1][k / 2].y) : fmaxf(y[0][k / 2].x, y[1][k / 2].x));
+              const float m = warp_top(k & 1 ? fmaxf(y[0][k / 2].y, y[T - 1][k / 2].y) : fmaxf(y[0][k / 2].x, y[T - 1][k / 2].x));
               if (lane == k) mine = m;
             }
             if (lane < NC) s_max[warp][lane] = mine;
@@ -1008,7 +1016,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             for (int k = 0; k < live; ++k) {
               float m = -INFINITY;
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
+              for (int h = 0; h < T; ++h) {
                 if (h >= nt) break;
                 uint32_t xs;
                 asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(xs) : "r"(s_col + h * N + k));
@@ -1041,7 +1049,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             for (int k = 0; k < NC; k += 4) {
               const float4 nb = *reinterpret_cast<const float4 *>(&s_nb[c_first + k]);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
+              for (int h = 0; h < T; ++h) {
                 y[h][k / 2] = __fadd2_rn(y[h][k / 2], make_float2(nb.x, nb.y));
                 y[h][k / 2 + 1] = __fadd2_rn(y[h][k / 2 + 1], make_float2(nb.z, nb.w));
               }
@@ -1057,7 +1065,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
               b2[k / 2 + 1] = __fmul2_rn(b2[k / 2 + 1], make_float2(a.z, a.w));
             }
             // O too, once the previous P V has landed
-            ok = __all_sync(0xffffffffu, q4_wait<kNapShort>(&pv_done[pb ^ 1], ((pair - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
+            ok = __all_sync(0xffffffffu, q4_wait(&pv_done[pb ^ 1], ((step - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
             t5_fence_after();
 #pragma unroll 1
             for (int k = 0; k < live; ++k) {
@@ -1072,9 +1080,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           }
         }
         if (gone) break;
-        const uint32_t p_row = p_smem + 2 * pb * kPBytes + prow * 128;
+        const uint32_t p_row = p_smem + T * pb * kPBytes + prow * 128;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < T; ++h) {
           if (h >= nt) break;
           const float2 vi2 = make_float2(vi[h], vi[h]), vz2 = make_float2(vz[h], vz[h]);
 #pragma unroll
@@ -1136,7 +1144,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           P.ws_ml[2 * e + 1] = l;
         }
       }
-      done = {true, (it.w & kWhole) != 0, pair - 1, i, ent};
+      done = {true, (it.w & kWhole) != 0, step - 1, i, ent};
       ++i;
     }
     named_bar_sync(bar, 128);
@@ -1243,7 +1251,7 @@ Q4Plan q4_plan(int B, int n_new, int H_q, int H_kv, int d, int max_blocks, int b
          (int64_t)B * n_new * H_q < (1ll << 30);
   if (!p.tc) return p;
   p.R = (int)R;
-  p.RG = (p.R + 47) / 48;                // at most 48 query rows a CTA (the registers of the softmax warps)
+  p.RG = (p.R + 63) / 64;                // at most 64 query rows a CTA (the registers of the softmax warps)
   p.Rg = (p.R + p.RG - 1) / p.RG;
   const int64_t Hp = (int64_t)H_kv * p.RG;
   p.NR = (int)std::max<int64_t>(1, std::min<int64_t>(q4_sms() / Hp, tiles));
@@ -1353,7 +1361,8 @@ extern "C" sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const 
                        : half <= 12 ? launch_q4<12>(P, p.C, st)
                        : half <= 16 ? launch_q4<16>(P, p.C, st)
                        : half <= 20 ? launch_q4<20>(P, p.C, st)
-                                    : launch_q4<24>(P, p.C, st);
+                       : half <= 24 ? launch_q4<24>(P, p.C, st)
+                                    : launch_q4<32>(P, p.C, st);
   if (r2 != SV_OK || p.NR == 1) return r2;
   launch_k(attn_q4_merge_kernel, dim3((p.NR - 1) * H_kv * p.RG, (p.Rg + kMergeWarps - 1) / kMergeWarps),
            dim3(32 * kMergeWarps), 0, st, 1, P);

@@ -212,6 +212,21 @@ def test_attention(lib, H_q, H_kv, n, lens, window, sinks):
     check_q4_attention(out, *q4_reference(q, kc, vc, table, lens, 16, window, sinks))
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (33, 5), (200, 40)])
+@pytest.mark.parametrize("H_q,H_kv,n", [(2, 2, r) for r in (47, 49, 57, 65, 97, 101, 128)] + [(24, 2, 5), (20, 1, 5)])
+def test_attention_query_rows(lib, H_q, H_kv, n, window, sinks):
+    # every way the query rows of a kv head are dealt to row groups and warpgroups
+    lens = [n, n + 1, 300, 129 + n, 1025]
+    table, total = table_for(lens, 16, seed=n)
+    kc, vc = q4_pools(total, H_kv, 128, 16, seed=n + H_q)
+    q = torch.randn((len(lens), n, H_q, 128), generator=torch.Generator().manual_seed(9)).bfloat16()
+    st = status0()
+    out = lib.spec_verify_attn_q4(q.to(DEV), kc.to(DEV), vc.to(DEV), table.to(DEV), i32(lens), window=window,
+                                  sinks=sinks, status=st)
+    assert int(st) == 0
+    check_q4_attention(out, *q4_reference(q, kc, vc, table, lens, 16, window, sinks))
+
+
 @pytest.mark.parametrize("window,sinks", [(0, 0), (7, 3), (40, 20)])
 @pytest.mark.parametrize("d,bs,H_q,H_kv,n,lens,qd", [
     (64, 16, 8, 2, 5, (70, 5), torch.bfloat16), (96, 8, 4, 4, 2, (33, 2), torch.bfloat16),
