@@ -24,6 +24,7 @@ Entry points (names follow the C ABI in include/specverify.h):
   copy_blocks         device page copies for copy-on-write (sv_copy_blocks)
 """
 import ctypes
+import functools
 import math
 import os
 
@@ -177,12 +178,12 @@ def _check(rc):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
     # (the raw handle: a Stream object costs 3 us, a fifth of a small call)
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dtype_code(t: torch.Tensor, fp8: bool = False) -> int:
@@ -335,6 +336,19 @@ def spec_verify_attn(q, k_cache, v_cache, block_table, seq_lens, softmax_scale=N
 
 # --------------------------------------- window, sinks and 4-bit pools ---
 
+def _ready(what, first, *rest):
+    """Tensors (or None) on the current device, contiguous: one pass, and the checks one by one, which say what is
+    wrong, only if something is."""
+    dev = first.get_device()
+    ok = dev >= 0 and first.is_contiguous()
+    for t in rest:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            ok = False
+    if not ok or dev != torch.cuda.current_device():
+        _cuda(first, *rest)
+        _on_current_device(what, first, *rest)
+
+
 def _on_current_device(what, first, *rest):
     """Kernels run on the current stream of the current device."""
     for t in rest:
@@ -349,7 +363,8 @@ def _check_batch(what, B, block_table, seq_lens, **per_seq):
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("%s: block_table must be [%d, max_blocks_per_seq], got %s"
                          % (what, B, tuple(block_table.shape)))
-    for name, t in dict(seq_lens=seq_lens, **per_seq).items():
+    per_seq["seq_lens"] = seq_lens
+    for name, t in per_seq.items():
         if t.shape != (B,):
             raise ValueError("%s: %s must be [%d], got %s" % (what, name, B, tuple(t.shape)))
 
@@ -365,6 +380,7 @@ def _check_status(what, status):
         raise ValueError("%s: status must hold an int32" % what)
 
 
+@functools.lru_cache(maxsize=256)
 def q4_record_bytes(d_head, block_size=16):
     """Bytes of one (block, kv head) of a 4-bit pool: block_size * (d_head / 2 + 4)."""
     n = int(load_library().sv_q4_record_bytes(int(d_head), int(block_size)))
@@ -413,15 +429,15 @@ def kv_block_append_q4(k_new, v_new, k_cache, v_cache, block_table, seq_lens, bl
     seq_lens - n_new .. seq_lens - 1. Pools uint8 [num_blocks, H_kv, q4_record_bytes(d, bs)], or, with
     `layout` = (block, head, 0) record strides in bytes, flat views plus num_blocks."""
     what = "kv_block_append_q4"
-    _int32(block_table=block_table, seq_lens=seq_lens)
+    if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        _int32(block_table=block_table, seq_lens=seq_lens)
     if k_new.dim() != 4 or k_new.shape != v_new.shape or k_new.dtype != v_new.dtype:
         raise ValueError("%s: k_new and v_new must both be [B, n_new, H_kv, d] of one dtype" % what)
     B, n_new, H_kv, d = k_new.shape
     nb, _ = _q4_pools(what, k_cache, v_cache, d, block_size, layout, num_blocks, H_kv)
     _check_batch(what, B, block_table, seq_lens)
     _check_status(what, status)
-    _cuda(k_new, v_new, k_cache, v_cache, block_table, seq_lens, status)
-    _on_current_device(what, k_new, v_new, k_cache, v_cache, block_table, seq_lens, status)
+    _ready(what, k_new, v_new, k_cache, v_cache, block_table, seq_lens, status)
     _check(load_library().kv_block_append_q4(_ptr(k_new), _ptr(v_new), _dtype_code(k_new), _ptr(k_cache),
                                              _ptr(v_cache), _layout_arg(layout), _ptr(block_table),
                                              block_table.shape[1], _ptr(seq_lens), B, n_new, H_kv, d, block_size,
@@ -445,8 +461,7 @@ def kv_block_gather_q4(k_cache, v_cache, block_table, seq_lens, start, n_rows, d
     _check_like(what, "k_out", k_out, shape, out_dtype)
     _check_like(what, "v_out", v_out, shape, out_dtype)
     _check_status(what, status)
-    _cuda(k_cache, v_cache, block_table, seq_lens, start, k_out, v_out, status)
-    _on_current_device(what, k_cache, v_cache, block_table, seq_lens, start, k_out, v_out, status)
+    _ready(what, k_cache, v_cache, block_table, seq_lens, start, k_out, v_out, status)
     if k_out is None:
         k_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
     if v_out is None:
@@ -459,11 +474,13 @@ def kv_block_gather_q4(k_cache, v_cache, block_table, seq_lens, start, n_rows, d
     return k_out, v_out
 
 
+@functools.lru_cache(maxsize=1024)
 def attn_window_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size=16, window=0, sinks=0):
     return load_library().spec_verify_attn_window_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq,
                                                                  block_size, int(window), int(sinks))
 
 
+@functools.lru_cache(maxsize=1024)
 def attn_q4_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size=16, window=0, sinks=0):
     return load_library().spec_verify_attn_q4_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq,
                                                              block_size, int(window), int(sinks))
@@ -483,7 +500,8 @@ def spec_verify_attn_window(q, k_cache, v_cache, block_table, seq_lens, window, 
     """Paged GQA verify attention through a sliding window: the query at position p sees key t <= p iff
     t > p - window or t < sinks (window = 0: every key). Pools and layout as for spec_verify_attn."""
     what = "spec_verify_attn_window"
-    _int32(block_table=block_table, seq_lens=seq_lens)
+    if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        _int32(block_table=block_table, seq_lens=seq_lens)
     _attn_outputs(what, q, block_table, seq_lens, out, workspace, status)
     B, n_new, H_q, d = q.shape
     if layout is None:
@@ -499,8 +517,7 @@ def spec_verify_attn_window(q, k_cache, v_cache, block_table, seq_lens, window, 
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is None or t.dtype != torch.float32 or t.numel() < H_kv:
                 raise ValueError("%s: fp8 pools need %s, float32 [H_kv]" % (what, name))
-    _cuda(q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out, workspace, status)
-    _on_current_device(what, q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out, workspace, status)
+    _ready(what, q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out, workspace, status)
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
     if out is None:
@@ -523,12 +540,12 @@ def spec_verify_attn_q4(q, k_cache, v_cache, block_table, seq_lens, softmax_scal
     """Paged GQA verify attention over 4-bit pools (kv_block_append_q4), q [B, n_new, H_q, d] bf16 or f32; with
     window > 0 the query at position p sees key t <= p iff t > p - window or t < sinks."""
     what = "spec_verify_attn_q4"
-    _int32(block_table=block_table, seq_lens=seq_lens)
+    if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        _int32(block_table=block_table, seq_lens=seq_lens)
     _attn_outputs(what, q, block_table, seq_lens, out, workspace, status)
     B, n_new, H_q, d = q.shape
     nb, H = _q4_pools(what, k_cache, v_cache, d, block_size, layout, num_blocks, H_kv)
-    _cuda(q, k_cache, v_cache, block_table, seq_lens, out, workspace, status)
-    _on_current_device(what, q, k_cache, v_cache, block_table, seq_lens, out, workspace, status)
+    _ready(what, q, k_cache, v_cache, block_table, seq_lens, out, workspace, status)
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
     if out is None:
