@@ -73,10 +73,7 @@ constexpr int kChunk = 8, kChunks = 4;     // tiles of a chunk of block offsets,
 constexpr int kPBytes = kTK * 128;         // a P' buffer: 128 bytes (64 columns of f16) a key
 constexpr int kWarps = 28;
 constexpr int kKWarp = 8, kVWarp = 16, kPageWarp = 24, kQkWarp = 25, kPvWarp = 26, kQWarp = 27;
-// Registers: launched at 72 a thread; the K, V and service warps hand over 32
-// each so that the softmax warps hold a step's scores and two sums per column
-// (256 x 144 + 640 x 40 <= 896 x 72).
-constexpr int kRegsSoftmax = 144, kRegsOther = 40;
+constexpr int kRegs = 72;                  // a thread at the launch
 constexpr int kFirst = 1, kLast = 2, kEnd = 4, kSecond = 8;   // of a tile: the sequence's first or last here, its step's last or second
 constexpr int kWhole = 1, kOpening = 2;     // of an item: the whole sequence, the first of its CTA
 constexpr float kUnset = 1e30f;            // minus the reference of a row that has met no key
@@ -105,6 +102,12 @@ struct Q4Params {
 template <int NC> struct Q4Cfg {   // NC query rows per softmax warpgroup
   static constexpr int kCols = (NC + 7) / 8 * 8, kN = 2 * kCols;   // columns of S and O
   static constexpr int kT = NC > 24 ? 1 : 2;   // tiles of a softmax step (their scores stay in registers)
+  // Registers: the K, V and service warps hand over theirs so that the softmax
+  // warps hold a step's scores and two sums per column. 128 / 48 against 144 / 40:
+  // 63.4 and 64.3 us with 4 columns, 132.3 and 128.4 with 20; 152 / 40 against 144
+  // / 40: 85.0 and 86.0 with 32, 130.4 and 128.4 with 20.
+  static constexpr int kRegsSoftmax = NC <= 16 ? 128 : NC <= 20 ? 144 : 152, kRegsOther = NC <= 16 ? 48 : 40;
+  static_assert(256 * kRegsSoftmax + 32 * (kWarps - 8) * kRegsOther <= 32 * kWarps * kRegs, "registers");
   static constexpr int kQ = kN * 256;   // the two e4m3 terms of a row, 128 bytes each
   static constexpr uint32_t kKCol = 0, kVCol = 64, kSCol = 192, kOCol = 192 + 2 * kT * kN;   // (two O buffers)
   static constexpr int kSmem = 1024 + 2 * kQ + 2 * kT * kPBytes + 16 * kNS * 2048 + 8 * kNS * 256 + kScales * kScaleBytes;
@@ -568,7 +571,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     }
   };
 
-  if (warp >= kPageWarp) regs_dec<kRegsOther>();
+  if (warp >= kPageWarp) regs_dec<Cfg::kRegsOther>();
   if (warp != kPageWarp) pdl_wait();
   pdl_trigger();
   if (warp == kPageWarp) {
@@ -750,7 +753,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     }
   } else if (warp >= kKWarp && warp < kPageWarp) {
     // ------------------------------------------------------ codes to TMEM --
-    regs_dec<kRegsOther>();
+    regs_dec<Cfg::kRegsOther>();
     const uint32_t lanes = tb + ((uint32_t)((warp & 3) * 32) << 16);
     auto role = [&](auto is_v) {
       constexpr bool V = decltype(is_v)::value;
@@ -862,7 +865,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     else role(std::false_type{});
   } else if (warp < kKWarp) {
     // ------------------------------------------------------------- softmax --
-    regs_inc<kRegsSoftmax>();
+    regs_inc<Cfg::kRegsSoftmax>();
     const int w = warp >> 2, t = tid & 127;
     const int c_first = w * CP;                 // this warpgroup's columns
     const int live = w ? rows - live0 : live0;
