@@ -103,10 +103,10 @@ template <int NC> struct Q4Cfg {   // NC query rows per softmax warpgroup
   static constexpr int kCols = (NC + 7) / 8 * 8, kN = 2 * kCols;   // columns of S and O
   static constexpr int kT = NC > 24 ? 1 : 2;   // tiles of a softmax step (their scores stay in registers)
   // Registers: the K, V and service warps hand over theirs so that the softmax
-  // warps hold a step's scores and two sums per column. 128 / 48 against 144 / 40:
-  // 63.4 and 64.3 us with 4 columns, 132.3 and 128.4 with 20; 152 / 40 against 144
-  // / 40: 85.0 and 86.0 with 32, 130.4 and 128.4 with 20.
-  static constexpr int kRegsSoftmax = NC <= 16 ? 128 : NC <= 20 ? 144 : 152, kRegsOther = NC <= 16 ? 48 : 40;
+  // warps hold a step's scores and two sums per column. 144 / 40 against 168 / 32:
+  // 62.7 and 64.5 us with 4 columns, 121.9 and 127.9 with 20, 150.2 and 143.0 with
+  // 24, 84.4 and 80.5 with 32 (spills on one side or the other).
+  static constexpr int kRegsSoftmax = NC <= 20 ? 144 : 168, kRegsOther = NC <= 20 ? 40 : 32;
   static_assert(256 * kRegsSoftmax + 32 * (kWarps - 8) * kRegsOther <= 32 * kWarps * kRegs, "registers");
   static constexpr int kQ = kN * 256;   // the two e4m3 terms of a row, 128 bytes each
   static constexpr uint32_t kKCol = 0, kVCol = 64, kSCol = 192, kOCol = 192 + 2 * kT * kN;   // (two O buffers)
@@ -763,12 +763,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       const uint32_t col = lanes + (V ? Cfg::kVCol + bf * 64 : Cfg::kKCol + bf * 32);
       const int slot = lane & 15, sw = (slot >> 1) & 3;
       // this warp's part of a stage, and of a record
-      const uint32_t mine = ring + (warp - kKWarp) * (kNS * 2048), mine_end = mine + kNS * 2048;
+      const uint32_t mine = ring + (warp - kKWarp) * (kNS * 2048);
       const uint8_t *pool = (V ? P.v_cache : P.k_cache) + (int64_t)g * P.head_stride +
                             (V ? (warp & 3) * 256 + (lane & 15) * 16 : lane * 16);
       bool ok = true;
       const uint32_t my_pairs = V ? 0u : pairs + (warp - kKWarp) * (kNS * 256);
-      uint32_t fill = mine, fill_pairs = my_pairs;   // the next stage to copy to
+      uint32_t fill = 0;   // offset of the next stage to copy to
       auto issue = [&](uint32_t u) {
         if (u < (uint32_t)total) {
           const uint32_t *pg = pages_of(u, 2, ok);
@@ -783,24 +783,19 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              copy16(fill + lane * 16 + j * 512, pool + (uint64_t)at[j] * 16 + (V ? 0 : (j & 1) * 512));
+              copy16(mine + fill + lane * 16 + j * 512, pool + (uint64_t)at[j] * 16 + (V ? 0 : (j & 1) * 512));
             if constexpr (!V) {   // the pairs: lanes 0-7 those of the two K blocks, 8-15 of the V blocks
               if (lane < 16)
-                copy16(fill_pairs + lane * 16, (lane < 8 ? P.k_cache : P.v_cache) + (int64_t)g * P.head_stride + kCodes +
+                copy16(my_pairs + fill / 8 + lane * 16, (lane < 8 ? P.k_cache : P.v_cache) + (int64_t)g * P.head_stride + kCodes +
                                                    (uint64_t)(lane & 4 ? at[2] : at[0]) * 16 + (lane & 3) * 16);
             }
           }
           pages_done(u, 2);
-          fill += 2048;
-          fill_pairs += 256;
-          if (fill == mine_end) {
-            fill = mine;
-            fill_pairs = my_pairs;
-          }
+          fill = fill == (kNS - 1) * 2048 ? 0 : fill + 2048;
         }
         copies_commit();
       };
-      uint32_t src = mine, src_pairs = my_pairs;   // the stage to read
+      uint32_t stage = 0;   // offset of the stage to read
       // K: this lane's key in its tile; an odd key, whose V codes come out 16 times
       // too large, has a 16 times smaller weight, and a part 15 that was taken off
       const int key = 32 * (warp & 3) + lane;
@@ -814,7 +809,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         if (ok && k > 0) ok = q4_wait(empty, (k & 1) ^ 1, abf, P.wait_ns);
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
-#pragma unroll 2
+        const uint32_t src = mine + stage;
+        // (V unrolled by two spills: 127.7 against 122.4 us for 64 sequences)
+#pragma unroll (V ? 1 : 2)
         for (int h = 0; h < 4; ++h) {   // K: 32 head dims of a key; V: 32 keys of a head dim
           uint32_t w[4];
           if constexpr (V) {
@@ -836,8 +833,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         }
         if constexpr (!V) {
           uint32_t kp, vp;
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kp) : "r"(src_pairs + lane * 4));
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vp) : "r"(src_pairs + lane * 4 + 128));
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kp) : "r"(my_pairs + stage / 8 + lane * 4));
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vp) : "r"(my_pairs + stage / 8 + lane * 4 + 128));
           const float2 k2 = __half22float2(*reinterpret_cast<const __half2 *>(&kp));
           const float2 v2 = __half22float2(*reinterpret_cast<const __half2 *>(&vp));
           const float vs = fmaxf(v2.x, 5.9604645e-8f) * shrink;   // (pages never written hold zeros)
@@ -850,12 +847,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         }
         t5_wait_st();
         t5_fence_before();
-        src += 2048;
-        src_pairs += 256;
-        if (src == mine_end) {
-          src = mine;
-          src_pairs = my_pairs;
-        }
+        stage = stage == (kNS - 1) * 2048 ? 0 : stage + 2048;
         __syncwarp();   // (every lane has read its codes: the stage is refilled next)
         if (lane == 0) mbar_arrive(full);
       }
