@@ -34,10 +34,10 @@
 // What bounds it: 136 bytes per key and kv head leave about 820 SM cycles per
 // 128-key tile at the measured HBM bandwidth, for 2 x 128 x 128 codes to unpack
 // and 128 R exponentials. Measured: 64 sequences of 1024-8192 keys, 5 positions,
-// 64/8 heads take 128 us (330 MB, 2.6 TB/s; 49 us at the bandwidth), 128K keys
-// with 8 positions 86 us, about 1700 cycles a tile of 40 rows. A tile takes 4270
+// 64/8 heads take 122.5 us (330 MB, 2.7 TB/s; 49 us at the bandwidth), 128K keys
+// with 8 positions 80.5 us, about 1650 cycles a tile of 40 rows. A tile takes 4130
 // warp instructions (V 485, K 361, the exponentials and P' 625, the scores 700,
-// the rest copies, waits and bookkeeping) at 62 % of the issue slots; the softmax
+// the rest copies, waits and bookkeeping) at 61 % of the issue slots; the softmax
 // warps are the ones the others wait for, and each part that is taken out for a
 // test gains 3 to 9 %.
 //
