@@ -78,6 +78,10 @@ constexpr int kFirst = 1, kLast = 2, kEnd = 4, kSecond = 8;   // of a tile: the 
 constexpr int kWhole = 1, kOpening = 2;     // of an item: the whole sequence, the first of its CTA
 constexpr float kUnset = 1e30f;            // minus the reference of a row that has met no key
 
+// Query rows of a CTA that the first softmax warpgroup takes.
+constexpr int kAlone = 8;
+__host__ __device__ inline int q4_first(int rows) { return rows <= kAlone ? rows : (rows + 1) / 2; }
+
 struct Q4Params {
   const void *q;
   void *out;
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps) attn_q4_prep_kernel(const __g
   const int Hp = P.H_kv * P.RG;
   const int gp = (int)(ent % Hp), b = (int)(ent / Hp);
   const int g = gp / P.RG, row0 = (gp % P.RG) * P.Rg;
-  const int rows = min(P.Rg, P.R - row0), live0 = (rows + 1) / 2;
+  const int rows = min(P.Rg, P.R - row0), live0 = q4_first(rows);
   const int c8 = lane & 15;
   uint4 v[kPass];
   uint32_t top = 0;
@@ -505,7 +509,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   const int range = blockIdx.x / Hp, gp = blockIdx.x % Hp;
   const int g = gp / P.RG, row0 = (gp % P.RG) * P.Rg;
   const int rows = min(P.Rg, P.R - row0);       // live rows of this CTA
-  const int live0 = (rows + 1) / 2;             // of the first softmax warpgroup
+  const int live0 = q4_first(rows);             // of the first softmax warpgroup
+  const int softmax_warps = live0 < rows ? 8 : 4;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t q_smem = smem_u32(smem);
   const uint32_t p_smem = q_smem + 2 * Cfg::kQ;
@@ -534,11 +539,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       mbar_init(&drain[k], 1);
       mbar_init(&q_full[k], 1);
       mbar_init(&q_empty[k], 1);
-      mbar_init(&o_free[k], 8);
+      mbar_init(&o_free[k], softmax_warps);
       // Q K^T of the step (its commit, and the issuing lane itself, which has seen
       // the K warps' scales), and P V of the step before the last
       mbar_init(&s_full[k], 3);
-      mbar_init(&p_full[k], 8);
+      mbar_init(&p_full[k], softmax_warps);
       mbar_init(&pv_done[k], 1);
     }
     abort_flag = 0;
@@ -855,7 +860,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
     };
     if (warp >= kVWarp) role(std::true_type{});
     else role(std::false_type{});
-  } else if (warp < kKWarp) {
+  } else if (warp < softmax_warps) {
     // ------------------------------------------------------------- softmax --
     regs_inc<Cfg::kRegsSoftmax>();
     const int w = warp >> 2, t = tid & 127;
@@ -1259,7 +1264,7 @@ Q4Plan q4_plan(int B, int n_new, int H_q, int H_kv, int d, int max_blocks, int b
 }
 
 // Columns of S and O, a softmax warpgroup's rows in steps of 4 (of 8 for the layout)
-int q4_cols(const Q4Plan &p) { return 2 * (((p.Rg + 1) / 2 + 7) / 8 * 8); }
+int q4_cols(const Q4Plan &p) { return 2 * ((q4_first(p.Rg) + 7) / 8 * 8); }
 
 size_t q4_ws_bytes(const Q4Plan &p, int B, int H_kv) {
   const size_t ent = (size_t)2 * p.C * p.Rg, qent = (size_t)B * H_kv * p.RG, n = q4_cols(p);
@@ -1358,7 +1363,7 @@ extern "C" sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const 
   P.wait_ns = wait_limit_ns();
   P.withhold = test_withhold();
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int half = (p.Rg + 1) / 2;   // rows of a softmax warpgroup
+  const int half = q4_first(p.Rg);   // rows of a softmax warpgroup
   const sv_status r2 = half <= 4    ? launch_q4<4>(P, p.C, st)
                        : half <= 8  ? launch_q4<8>(P, p.C, st)
                        : half <= 12 ? launch_q4<12>(P, p.C, st)
