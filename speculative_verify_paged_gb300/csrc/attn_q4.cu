@@ -78,7 +78,9 @@ constexpr int kFirst = 1, kLast = 2, kEnd = 4, kSecond = 8;   // of a tile: the 
 constexpr int kWhole = 1, kOpening = 2;     // of an item: the whole sequence, the first of its CTA
 constexpr float kUnset = 1e30f;            // minus the reference of a row that has met no key
 
-// Query rows of a CTA that the first softmax warpgroup takes.
+// Query rows of a CTA that the first softmax warpgroup takes: up to 8 it takes
+// all, so that a step's fixed work is done once (64 sequences of 1024-8192 keys, 8
+// rows: 91.8 against 94.9 us; up to 16 it would be 106 against 99 with 16 rows).
 constexpr int kAlone = 8;
 __host__ __device__ inline int q4_first(int rows) { return rows <= kAlone ? rows : (rows + 1) / 2; }
 
