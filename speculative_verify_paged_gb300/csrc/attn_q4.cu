@@ -180,10 +180,15 @@ __device__ int4 q4_range(const Q4Params &P, int r, int64_t T, int4 &split) {
   split = make_int4(-1, 0, 0, 0);
   if (t1 <= t0) return w;
   int64_t A = 0;
-  for (int b0 = 0; b0 < P.B; b0 += 32) {
-    const int b = b0 + lane;
-    const int nt = b < P.B ? q4_tiles(P, P.seq_lens[b]) : 0;
-    int incl = nt;
+  for (int b0 = 0; b0 < P.B; b0 += 128) {   // four sequences a lane
+    int nt[4], own = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int b = b0 + 4 * lane + k;
+      nt[k] = b < P.B ? q4_tiles(P, P.seq_lens[b]) : 0;
+      own += nt[k];
+    }
+    int incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -192,13 +197,23 @@ __device__ int4 q4_range(const Q4Params &P, int r, int64_t T, int4 &split) {
     const unsigned hit = __ballot_sync(0xffffffffu, A + incl > t0);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      const int off = (int)(t0 - (A + __shfl_sync(0xffffffffu, incl - nt, src)));
-      w = make_int4(b0 + src, off, (int)(t1 - t0), 0);
+      int off = (int)(t0 - (A + __shfl_sync(0xffffffffu, incl - own, src))), k = 0, n = nt[0];
+#pragma unroll
+      for (int e = 1; e < 4; ++e) {   // (lane src: the sequence among its four)
+        if (k == e - 1 && off >= n) {
+          off -= n;
+          n = nt[e];
+          k = e;
+        }
+      }
+      off = __shfl_sync(0xffffffffu, off, src);
+      n = __shfl_sync(0xffffffffu, n, src);
+      const int b = b0 + 4 * src + __shfl_sync(0xffffffffu, k, src);
+      w = make_int4(b, off, (int)(t1 - t0), 0);
       // a range that starts inside a sequence is its first cut if one range
       // holds all its tiles before (tile x lies in range ((x + 1) NR - 1) / T)
       const int64_t first = t0 - off;
-      if (off > 0 && (t0 * P.NR - 1) / T == ((first + 1) * P.NR - 1) / T)
-        split = make_int4(b0 + src, (int)first, __shfl_sync(0xffffffffu, nt, src), (int)T);
+      if (off > 0 && (t0 * P.NR - 1) / T == ((first + 1) * P.NR - 1) / T) split = make_int4(b, (int)first, n, (int)T);
       return w;
     }
     A += __shfl_sync(0xffffffffu, incl, 31);
@@ -209,17 +224,17 @@ __device__ int4 q4_range(const Q4Params &P, int r, int64_t T, int4 &split) {
 // One warp: the tiles of all sequences, and whether a length is out of range.
 __device__ int64_t q4_all_tiles(const Q4Params &P, bool &bad) {
   const int lane = threadIdx.x & 31;
-  int64_t T = 0;
+  int own = 0;   // (all tiles together are below 2^30)
   bad = false;
-  for (int b0 = 0; b0 < P.B; b0 += 32) {
-    const int b = b0 + lane;
-    const int L = b < P.B ? P.seq_lens[b] : P.n_new;
-    int nt = b < P.B ? q4_tiles(P, L) : 0;
+#pragma unroll 4
+  for (int b = lane; b < P.B; b += 32) {
+    const int L = P.seq_lens[b];
+    own += q4_tiles(P, L);
     bad = bad || L < P.n_new || L > P.max_blocks * kBS;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) nt += __shfl_xor_sync(0xffffffffu, nt, o);
-    T += nt;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
+  const int64_t T = own;
   return T;
 }
 
