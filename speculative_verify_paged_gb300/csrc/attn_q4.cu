@@ -25,8 +25,8 @@
 // other operand of each product is stored in that order.
 // Keys on the lanes. The M = 128 side of both products is the cache: S^T = C Q^T
 // has a key per lane, O^T = C'^T P'^T a head dim per lane, and N is the number
-// of query rows (16 to 64), so no tensor-core work is padding whatever the
-// GQA group. The A operand is written by the thread that owns its lane, from
+// of query rows in steps of 16 (up to 64), so little tensor-core work is padding
+// whatever the GQA group. The A operand is written by the thread that owns its lane, from
 // its own 64 bytes of codes, straight into tensor memory; shared memory holds
 // only the raw records, Q and P'. A K record is slot-major and a V record
 // dim-major for this reason.
@@ -480,7 +480,7 @@ __device__ __forceinline__ void t5_st8(uint32_t taddr, const uint32_t *r) {
 }
 
 // Warps 0-3 and 4-7: softmax (a key per thread and tile; each warpgroup half
-// of the query rows), later the epilogue (a head dim per thread). 8-15: K codes
+// of the query rows, or the first all of them), later the epilogue (a head dim per thread). 8-15: K codes
 // to tensor memory, 16-23: V codes (four warps per tile parity). 24: block
 // offsets and flags of the tiles ahead. 25: issues Q K^T, owns the 512 TMEM
 // columns (two K, two V, four S and two O buffers). 26: issues P V (one warp for
@@ -488,14 +488,13 @@ __device__ __forceinline__ void t5_st8(uint32_t taddr, const uint32_t *r) {
 // of the next sequence.
 // The softmax takes two tiles at a time (one with more than 48 rows, whose
 // scores would not fit in registers): its waits, its vote and its fences cost as
-// much as the arithmetic of a tile. More than two gain nothing, as V has two
-// buffers.
+// much as the arithmetic of a tile. (Four for up to 16 rows, with two or four V
+// buffers, gained nothing.)
 // Every warp copies what it reads: a K warp the two blocks that its keys lie
 // in (and the keys' pairs of K and V, which it unpacks for the softmax), a V
 // warp its 32 head dims of the tile's eight blocks; so a copy is waited for by
-// its own warp alone. (Bulk
-// copies of whole records were limited by their issue: 1088 bytes each, they
-// reached 2.9 TB/s from one warp and 4.8 TB/s from sixteen.)
+// its own warp alone. (Bulk copies of whole records were limited by their issue:
+// 1088 bytes each, they reached 2.9 TB/s from one warp and 4.8 TB/s from sixteen.)
 template <int NC>
 __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_constant__ Q4Params P) {
   using Cfg = Q4Cfg<NC>;
