@@ -340,7 +340,8 @@ sv_status spec_verify_attn_window(const void *q, sv_dtype q_dtype,
  *   to nearest even) or SV_F32; positions outside [0, seq_lens[b]) give zero
  *   rows. start: device int32 [B]. k_out, v_out: [B][n_rows][H_kv][d_head].
  *   For chunked prefill over a quantised prefix, or to move a sequence to
- *   another cache. A length outside [0, max_blocks_per_seq * block_size] or a
+ *   another cache (the rows may go to an append on the same stream as they
+ *   stand). A length outside [0, max_blocks_per_seq * block_size] or a
  *   bad block sets SV_DEV_* and gives zero rows.
  *
  * spec_verify_attn_q4

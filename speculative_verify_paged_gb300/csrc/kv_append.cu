@@ -44,14 +44,14 @@ template <typename TIn>
 __device__ __forceinline__ void load8_in(const TIn *src, bool vec, float (&x)[8]) {
   if constexpr (std::is_same<TIn, float>::value) {
     if (vec) {
-      const float4 a = __ldg(reinterpret_cast<const float4 *>(src));
-      const float4 b = __ldg(reinterpret_cast<const float4 *>(src) + 1);
+      const float4 a = reinterpret_cast<const float4 *>(src)[0];
+      const float4 b = reinterpret_cast<const float4 *>(src)[1];
       x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
       return;
     }
   } else {
     if (vec) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src));
+      const uint4 w = *reinterpret_cast<const uint4 *>(src);
       const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -110,10 +110,10 @@ __device__ __forceinline__ void store8_out(void *cache, int64_t off, const float
 
 // One CTA per (new position j, sequence b); a thread takes groups of eight
 // consecutive elements of one head row (d % 8 == 0; element by element
-// otherwise). Everything it reads (lengths, block table, the new rows) is
-// loaded before the wait on the previous kernel (the library's kernels
-// never write them); only the stores into the pools wait, since a previous
-// kernel may still be reading the pools.
+// otherwise). Lengths and block table are loaded before the wait on the
+// previous kernel (the library's kernels never write them). The new rows are
+// read after it, with plain loads: they may be what kv_block_gather_q4, the
+// kernel before, reads back from a 4-bit cache.
 template <typename TIn, int KV>
 __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
   pdl_trigger();
@@ -126,26 +126,19 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
   const int64_t src0 = ((int64_t)b * a.n_new + j) * a.H_kv * a.d;
   const TIn *kn = static_cast<const TIn *>(a.k_new) + src0;
   const TIn *vn = static_cast<const TIn *>(a.v_new) + src0;
+  pdl_wait();
+  if (!len_ok || !blk_ok) {
+    if (threadIdx.x == 0) atomic_or_status(a.status, len_ok ? SV_DEV_BAD_BLOCK : SV_DEV_BAD_SEQ_LEN);
+    return;
+  }
+  const int64_t base = (int64_t)blk * a.block_stride + (int64_t)(pos % a.bs) * a.slot_stride;
   if (a.d % 8 == 0) {
     const int groups = a.H_kv * a.d / 8;
-    float kx[8], vx[8];
-    const int e0 = threadIdx.x * 8;
-    if ((int)threadIdx.x < groups) {
-      load8_in<TIn>(kn + e0, a.vec_in, kx);
-      load8_in<TIn>(vn + e0, a.vec_in, vx);
-    }
-    pdl_wait();
-    if (!len_ok || !blk_ok) {
-      if (threadIdx.x == 0) atomic_or_status(a.status, len_ok ? SV_DEV_BAD_BLOCK : SV_DEV_BAD_SEQ_LEN);
-      return;
-    }
-    const int64_t base = (int64_t)blk * a.block_stride + (int64_t)(pos % a.bs) * a.slot_stride;
     for (int gi = threadIdx.x; gi < groups; gi += blockDim.x) {
       const int e = gi * 8;
-      if (gi != (int)threadIdx.x) {   // more groups than threads
-        load8_in<TIn>(kn + e, a.vec_in, kx);
-        load8_in<TIn>(vn + e, a.vec_in, vx);
-      }
+      float kx[8], vx[8];
+      load8_in<TIn>(kn + e, a.vec_in, kx);
+      load8_in<TIn>(vn + e, a.vec_in, vx);
       const int g = e / a.d, c = e - g * a.d;
       const int64_t off = base + (int64_t)g * a.head_stride + c;
       float ks = 1.f, vs = 1.f;
@@ -158,12 +151,6 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
     }
     return;
   }
-  pdl_wait();
-  if (!len_ok || !blk_ok) {
-    if (threadIdx.x == 0) atomic_or_status(a.status, len_ok ? SV_DEV_BAD_BLOCK : SV_DEV_BAD_SEQ_LEN);
-    return;
-  }
-  const int64_t base = (int64_t)blk * a.block_stride + (int64_t)(pos % a.bs) * a.slot_stride;
   const int total = a.H_kv * a.d;
   for (int e = threadIdx.x; e < total; e += blockDim.x) {
     const int g = e / a.d, c = e - g * a.d;

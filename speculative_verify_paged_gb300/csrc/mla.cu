@@ -604,14 +604,14 @@ __global__ void __launch_bounds__(96) latent_append_kernel(const uint4 *c_new, u
   const int pos = L - n_new + j;
   const int blk = len_ok ? table[(int64_t)b * max_blocks + pos / kLBS] : -1;
   const bool blk_ok = blk >= 0 && blk < num_blocks;
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if ((int)threadIdx.x < kRowVec) v = __ldg(c_new + ((int64_t)b * n_new + j) * kRowVec + threadIdx.x);
   pdl_wait();
   if (!len_ok || !blk_ok) {
     if (threadIdx.x == 0) atomic_or_status(status, len_ok ? SV_DEV_BAD_BLOCK : SV_DEV_BAD_SEQ_LEN);
     return;
   }
-  if ((int)threadIdx.x < kRowVec) cache[((int64_t)blk * kLBS + pos % kLBS) * kRowVec + threadIdx.x] = v;
+  if ((int)threadIdx.x < kRowVec)   // (read after the wait: a kernel of the library may have written the rows)
+    cache[((int64_t)blk * kLBS + pos % kLBS) * kRowVec + threadIdx.x] =
+        c_new[((int64_t)b * n_new + j) * kRowVec + threadIdx.x];
 }
 
 struct MlaPlan {

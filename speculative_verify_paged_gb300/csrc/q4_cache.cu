@@ -34,10 +34,10 @@ __device__ __forceinline__ void load8(const T *p, bool vec, T (&x)[8]) {
   if (vec) {
 #pragma unroll
     for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-      reinterpret_cast<uint4 *>(x)[k] = __ldg(reinterpret_cast<const uint4 *>(p) + k);
+      reinterpret_cast<uint4 *>(x)[k] = reinterpret_cast<const uint4 *>(p)[k];
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = __ldg(p + k);
+    for (int k = 0; k < 8; ++k) x[k] = p[k];
   }
 }
 
@@ -161,6 +161,13 @@ __global__ void __launch_bounds__(32 * kQaWarps, sizeof(TIn) == 2 ? 12 : 8) q4_a
   const int64_t src0 = (((int64_t)b * a.n_new + (page * bs + s0 - first)) * a.H_kv + g) * d + li * 8;
   const int64_t rec0 = (int64_t)phys * a.block_stride + (int64_t)g * a.head_stride;
   const bool on = li < W;
+  // the new rows may be what the kernel before reads back (q4_gather_kernel),
+  // and the pools may still be read by it
+  pdl_wait();
+  if (phys < 0 || phys >= a.num_blocks) {
+    if (threadIdx.x == 0) atomic_or_status(a.status, SV_DEV_BAD_BLOCK);
+    return;
+  }
   for (int i0 = 0; i0 < nr; i0 += kQaRows * kGroups) {
     // (rows 0 .. kQaRows - 1 are of K, the others of V)
     alignas(16) TIn xr[2 * kQaRows][8];
@@ -169,15 +176,6 @@ __global__ void __launch_bounds__(32 * kQaWarps, sizeof(TIn) == 2 ? 12 : 8) q4_a
       const int i = i0 + u % kQaRows * kGroups + group;
       no_row(xr[u]);
       if (i < nr && on) load8(static_cast<const TIn *>(a.src[u / kQaRows]) + src0 + i * row_stride, vec, xr[u]);
-    }
-    // everything read so far is the caller's; the pools may still be read by
-    // the previous kernel of the stream
-    if (i0 == 0) {
-      pdl_wait();
-      if (phys < 0 || phys >= a.num_blocks) {
-        if (threadIdx.x == 0) atomic_or_status(a.status, SV_DEV_BAD_BLOCK);
-        return;
-      }
     }
     // lane u of the group works out row u's pair
     float mn = 0.f, mx = 0.f;

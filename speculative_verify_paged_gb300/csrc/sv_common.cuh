@@ -207,9 +207,10 @@ __device__ __forceinline__ int ld_dsmem_s32(uint32_t addr) {
 // their memory is visible. pdl_trigger(): the next launch of the stream may
 // be scheduled while this grid drains. Kernels call both first, except where
 // a kernel reads only inputs no kernel of the library writes (lengths, block
-// table, new K/V rows, logits): those loads may come before the wait, and
-// every write still comes after it. Data that the previous kernel writes
-// (a work order, a partition, ancestor masks, accepted counts) is read after
+// table): those loads may come before the wait, and every write still comes
+// after it. Data that the previous kernel writes
+// (a work order, a partition, ancestor masks, accepted counts, the K/V rows
+// that kv_block_gather_q4 reads back for the next append) is read after
 // the wait with plain loads, never __ldg: that kernel may still have been
 // writing it when this grid started, so it is not read-only data for this
 // grid, and a read-only load may be scheduled as if it were.
