@@ -214,14 +214,13 @@ __device__ __forceinline__ bool t5_item(const TcParams &P, T5Walk &w, T5Item &it
 // innermost; empty splits, and sequences with invalid lengths, last). The
 // order within a bucket is that of the atomics: each item is still computed
 // once, and its result does not depend on when.
-// It reads only seq_lens and writes only its own part of the workspace, so
-// it runs while the previous kernel of the stream is still running (that
-// kernel passed its own wait, so everything before it has completed; the
-// library's kernels never write seq_lens; an attention kernel of the
-// previous call lets the next kernel start only once each of its CTAs has
-// read its item from this order). It waits for that kernel at its end, so
-// the attention kernel's wait on this one still covers, for example, the
-// K/V rows the append kernel writes.
+// It reads only seq_lens (which the library's kernels never write) before its
+// wait, so that it counts and ranks while the previous kernel of the stream is
+// still running. It writes the order after the wait: the workspace may be
+// shared with a call of another layout (a layer with other pools or a window),
+// whose attention or merge may be running yet, behind an append that let this
+// kernel start before its own wait. The wait also makes the attention kernel's
+// wait on this one cover, for example, the K/V rows the append kernel writes.
 constexpr int kOrdThreads = 1024;
 constexpr int kOrdMaxTiles = 1023;   // buckets 0..kOrdMaxTiles
 constexpr int kOrdPairs = 4;         // (s, b) pairs a thread keeps in registers
@@ -275,16 +274,19 @@ __global__ void __launch_bounds__(kOrdThreads) attn_order_kernel(const int32_t *
     }
   }
   __syncthreads();
-  auto place = [&](int p, int w) {
-    const int pos = atomicAdd(&cur[w], 1);
+  auto place = [&](int p, int pos) {
     const int sp = p % S, bp = p / S;
     for (int gg = 0; gg < H_kv; ++gg) order[(int64_t)pos * H_kv + gg] = sp + S * (gg + H_kv * bp);
   };
+  int pos[kOrdPairs] = {};
 #pragma unroll
   for (int k = 0; k < kOrdPairs; ++k)
-    if (tid + k * kOrdThreads < npairs) place(tid + k * kOrdThreads, wk[k]);
-  for (int p = tid + kOrdPairs * kOrdThreads; p < npairs; p += kOrdThreads) place(p, work(p));
+    if (tid + k * kOrdThreads < npairs) pos[k] = atomicAdd(&cur[wk[k]], 1);
   pdl_wait();
+#pragma unroll
+  for (int k = 0; k < kOrdPairs; ++k)
+    if (tid + k * kOrdThreads < npairs) place(tid + k * kOrdThreads, pos[k]);
+  for (int p = tid + kOrdPairs * kOrdThreads; p < npairs; p += kOrdThreads) place(p, atomicAdd(&cur[work(p)], 1));
 }
 
 // Balanced partition for the tcgen05 kernel: one CTA. The global tile

@@ -82,3 +82,59 @@ def test_rows_read_back_move_to_another_cache(lib, dtype, target, captured, B, H
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(bits(a[0]), bits(b[0])) and torch.equal(bits(a[1]), bits(b[1]))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_layers_of_all_kinds_share_a_workspace(lib, captured):
+    # plain, windowed and 4-bit layers in turn over one workspace: grids of several waves (ordered work), contexts in
+    # several splits (partials and a merge) and in one; bit-equal to a workspace each
+    import workloads
+    cfg = workloads.CONFIGS["tiny"].with_(kv_dtype="bf16", q_dtype="bf16", logit_dtype="bf16", B=64, H_q=16, H_kv=8,
+                                          d_head=128, K=4, V=512, ctx=("uniform", (5, 3000)))
+    a = {k: (t.to(DEV) if isinstance(t, torch.Tensor) else t) for k, t in
+         {**workloads.make_attention_inputs(cfg, 0), **workloads.make_append_inputs(cfg, 0),
+          **workloads.make_sampling_inputs(cfg, 0)}.items()}
+    table = torch.full((64, 2048), -1, dtype=torch.int32, device=DEV)   # 32K tokens a sequence
+    table[:, :a["block_table"].shape[1]] = a["block_table"]
+    total = a["k_cache"].shape[0]
+    g = torch.Generator(device=DEV).manual_seed(5)
+
+    def bf16():
+        return {n + "_cache": torch.randn(a[n + "_cache"].shape, generator=g, device=DEV).bfloat16() for n in "kv"}
+
+    def fp8():
+        return dict({n + "_cache": torch.randint(0, 120, a[n + "_cache"].shape, generator=g, device=DEV,
+                                                 dtype=torch.uint8) for n in "kv"},
+                    k_scale=torch.full((8,), 0.01, device=DEV), v_scale=torch.full((8,), 0.01, device=DEV))
+
+    def q4():
+        k, v = (p.to(DEV) for p in q4_pools(total, 8, 128, BS, seed=8, spread=False))
+        return dict(k_cache=k, v_cache=v)
+
+    kinds = [(bf16, 0, 0), (bf16, 1024, 4), (fp8, 0, 0), (q4, 0, 0), (bf16, 0, 0), (fp8, 500, 17), (bf16, 0, 0),
+             (q4, 1024, 4), (bf16, 100, 0)]
+    layers = []
+    for k, (make, W, S) in enumerate(kinds):
+        q = torch.randn(a["q"].shape, generator=g, device=DEV).bfloat16()
+        layers.append(dict(make(), q=q, k_new=a["k_new"], v_new=a["v_new"], window=W, sinks=S))
+    assert lib.attn_workspace_size(64, 5, 16, 8, 128, 2048) != lib.attn_window_workspace_size(64, 5, 16, 8, 128, 2048, 16,
+                                                                                              1024, 4)
+    sample = (a["target_logits"], a["draft_logits"], a["draft_tokens"], a["uniforms"])
+    want = []
+    for l in layers:
+        m = lib.MultiLayerVerify([l], table, a["seq_lens"], *sample)
+        m.run()
+        torch.cuda.synchronize()
+        assert int(m.status) == 0
+        want.append(m.outs[0].clone())
+    m = lib.MultiLayerVerify(layers, table, a["seq_lens"], *sample)
+    if captured:
+        m.capture()
+    for _ in range(4):
+        for o in m.outs:
+            o.fill_(float("nan"))
+        m.replay() if captured else m.run()
+        torch.cuda.synchronize()
+        assert int(m.status) == 0
+        for o, w in zip(m.outs, want):
+            assert torch.equal(o, w)

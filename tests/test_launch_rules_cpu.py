@@ -45,3 +45,13 @@ def test_appends_read_the_new_rows_after_the_wait(name, kernel, rows):
 def test_appends_read_the_new_rows_with_plain_loads(name, helper):
     assert "__ldg" not in body(name, helper)
     assert "__ldg" not in body("mla.cu", "latent_append_kernel")
+
+
+@pytest.mark.parametrize("name,kernel,stores", [
+    ("attn.cu", "attn_order_kernel", r"(?<!auto )\bplace\("),
+])
+def test_orders_are_written_after_the_wait(name, kernel, stores):
+    # (the workspace may be shared with a call of another layout that still reads it)
+    b = body(name, kernel)
+    at = [m.start() for m in re.finditer(stores, b)]
+    assert at and b.index("pdl_wait()") < min(at)
