@@ -540,22 +540,31 @@ __global__ void __launch_bounds__(kLThreads, 1) attn_mla_kernel(const __grid_con
 
 // Longest-first order of the sequences (ties by batch index): the CTAs of
 // the longest contexts start first, so the last wave holds short ones. Rank
-// of b = number of sequences that come before it; order[rank] = b. It reads
-// only seq_lens (which no kernel of the library writes), so it runs while the
-// previous kernel of the stream finishes, and waits for it at its end.
+// of b = number of sequences that come before it; order[rank] = b. Before its
+// wait it reads only seq_lens (which no kernel of the library writes), so the
+// ranks are worked out while the previous kernel of the stream finishes; they
+// are stored after it, since that kernel may still read this workspace.
 constexpr int kLMaxOrder = 4096;
 __global__ void __launch_bounds__(1024) mla_order_kernel(const int32_t *seq_lens, int B, int32_t *order) {
   pdl_trigger();
   __shared__ int lens[kLMaxOrder];
   for (int b = threadIdx.x; b < B; b += blockDim.x) lens[b] = seq_lens[b];
   __syncthreads();
-  for (int b = threadIdx.x; b < B; b += blockDim.x) {
+  constexpr int kPer = kLMaxOrder / 1024;   // sequences of a thread
+  int rank[kPer] = {};
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int b = threadIdx.x + k * 1024;
+    if (b >= B) break;
     const int L = lens[b];
-    int rank = 0;
-    for (int c = 0; c < B; ++c) rank += (lens[c] > L) || (lens[c] == L && c < b);
-    order[rank] = b;
+    for (int c = 0; c < B; ++c) rank[k] += (lens[c] > L) || (lens[c] == L && c < b);
   }
   pdl_wait();
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int b = threadIdx.x + k * 1024;
+    if (b < B) order[rank[k]] = b;
+  }
 }
 
 // Merge of the splits of one query row: weights 2^(m_s - M) on the partial

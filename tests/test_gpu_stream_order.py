@@ -138,3 +138,41 @@ def test_layers_of_all_kinds_share_a_workspace(lib, captured):
         assert int(m.status) == 0
         for o, w in zip(m.outs, want):
             assert torch.equal(o, w)
+
+
+@pytest.mark.parametrize("B,n_new,H", [(96, 1, 16), (5, 4, 64), (1500, 1, 1)])
+def test_latent_calls_of_other_lengths_share_a_workspace(lib, B, n_new, H):
+    # one workspace, lengths that sort the other way round from call to call: bit-equal to a workspace each
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(n_new, 400 if B < 1000 else 40, (B,), generator=g).to(torch.int32)
+    other = lens.max() + n_new - lens
+    table, total = table_for([int(lens.max()) + n_new] * B, BS, seed=1)
+    cache = torch.randn((total, BS, 576), generator=g).to(torch.bfloat16).to(DEV)
+    q = torch.randn((B, n_new, H, 576), generator=g).to(torch.bfloat16).to(DEV)
+    table, both = table.to(DEV), [lens.to(DEV), other.to(DEV)]
+    want = []
+    for L in both:
+        want.append(lib.spec_verify_attn_mla(q, cache, table, L, 0.07))
+        torch.cuda.synchronize()
+    ws = lib.alloc_workspace(lib.mla_workspace_size(B, n_new, H, table.shape[1]), DEV)
+    outs = [torch.empty_like(w) for w in want]
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def run():
+        for _ in range(3):
+            for L, o in zip(both, outs):
+                lib.spec_verify_attn_mla(q, cache, table, L, 0.07, out=o, workspace=ws, status=st)
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for go in (run, graph.replay):
+        for o in outs:
+            o.fill_(float("nan"))
+        go()
+        torch.cuda.synchronize()
+        assert int(st) == 0
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)

@@ -49,6 +49,7 @@ def test_appends_read_the_new_rows_with_plain_loads(name, helper):
 
 @pytest.mark.parametrize("name,kernel,stores", [
     ("attn.cu", "attn_order_kernel", r"(?<!auto )\bplace\("),
+    ("mla.cu", "mla_order_kernel", r"\border\["),
 ])
 def test_orders_are_written_after_the_wait(name, kernel, stores):
     # (the workspace may be shared with a call of another layout that still reads it)
