@@ -77,6 +77,15 @@ constexpr int kRegs = 72;                  // a thread at the launch
 constexpr int kFirst = 1, kLast = 2, kEnd = 4, kSecond = 8;   // of a tile: the sequence's first or last here, its step's last or second
 constexpr int kWhole = 1, kOpening = 2;     // of an item: the whole sequence, the first of its CTA
 constexpr float kUnset = 1e30f;            // minus the reference of a row that has met no key
+// P' is f16. A row's reference puts its largest weight at 2^kTop and moves once
+// one exceeds 2^kMove (f16 ends at 65504), so weights keep f16's 11 bits down to
+// 2^-21 of the largest (odd keys, stored 16 times smaller: 2^-17) and an absolute
+// error of 2^-32 (2^-28) of it below. A key whose weight f16 loses counts as an
+// end of its row's range 15 s', since the sums below take the fp32 weight: n such
+// keys move an output by at most n 2^-28 of that range. With the largest weight at
+// 1 and 128K keys beside one that holds 97 % of the weight, that was 4 % of the
+// output; it is 4e-6 now.
+constexpr float kTop = 7.f, kMove = 15.f;
 
 // Query rows of a CTA that the first softmax warpgroup takes: up to 8 it takes
 // all, so that a step's fixed work is done once (64 sequences of 1024-8192 keys, 8
@@ -1005,8 +1014,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           }
           if (again) break;
           // The first step of a sequence sets the references (they are 0 so
-          // far); later ones move when a weight exceeds them by more than 2^8
-          // (f16 holds 2^16). All four warps decide together, as they share O.
+          // far); later ones move when a weight exceeds 2^kMove. All four warps
+          // decide together, as they share O.
           float top = fmaxf(y[0][0].x, y[0][0].y);
 #pragma unroll
           for (int k = 1; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[0][k].x), y[0][k].y);
@@ -1014,7 +1023,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
 #pragma unroll
             for (int k = 0; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[1][k].x), y[1][k].y);
           }
-          if (!bar_or(bar, 128, first || top > 8.f || !ok)) break;
+          if (!bar_or(bar, 128, first || top > kMove || !ok)) break;
           if (bar_or(bar, 128, !ok)) {
             gone = true;
             break;
@@ -1050,9 +1059,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             float a = 1.f, nb = first ? kUnset : s_nb[c_first + t];
             if (t < live) {
               const float m = fmaxf(fmaxf(s_max[4 * w][t], s_max[4 * w + 1][t]), fmaxf(s_max[4 * w + 2][t], s_max[4 * w + 3][t]));
-              if (m + nb > 8.f) {   // (a row that has met no key keeps kUnset)
-                a = ex2f(-nb - m);
-                nb = -m;
+              if (m + nb > kMove) {   // (a row that has met no key keeps kUnset)
+                a = ex2f(kTop - m - nb);
+                nb = kTop - m;
               }
             } else {
               nb = -kUnset;   // padding never moves
