@@ -17,11 +17,11 @@
 // the code times 2^-9 exactly (0 to 7 are subnormals, 8 to 15 the first normal
 // binade), so a word of eight codes becomes two words of e4m3 with three
 // instructions: Q K^T runs in kind::f8f6f4 with each query row as two e4m3 terms
-// (hi + lo: 8 bits down to 2^-9 of the largest element, an error of 2^-17 of it
-// below). V codes are subnormals of f16 in bits 0-3 of a half, or 4-7: then 16
-// times as large, and those keys have weights 16 times smaller; a word becomes
-// four with five instructions (15 - c' is the complement). P V runs in
-// kind::f16. Both spread the codes of a word over several registers, so the
+// (hi + lo: 8 bits down to 2^-9 of the largest element scaled with it, an error
+// of 2^-17 of that one below). V codes are subnormals of f16 in bits 0-3 of a
+// half, or 4-7: then 16 times as large, and those keys have weights 16 times
+// smaller; a word becomes four with five instructions (15 - c' is the
+// complement). P V runs in kind::f16. Both spread the codes of a word over several registers, so the
 // other operand of each product is stored in that order.
 // Keys on the lanes. The M = 128 side of both products is the cache: S^T = C Q^T
 // has a key per lane, O^T = C'^T P'^T a head dim per lane, and N is the number
@@ -47,6 +47,7 @@
 // leaves fp32 partials for the merge.
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -102,7 +103,8 @@ struct Q4Params {
   float *ws_ml;       // [2 CTAs][Rg][2]
   int4 *ws_split;     // per range: the sequence whose first cut is the range's start (b, first tile, tiles, T), or b = -1
   uint8_t *ws_q;      // per (sequence, kv head and row group): its Q as the kernel's shared memory holds it
-  float *ws_qs;       // [kN + 4] per entry: the rows' sums, then the power of two that undoes the scaling
+  float *ws_qs;       // [2 kN + 4] per entry: the rows' sums, the power of two that undoes the scaling (or -1: every row
+                      // has its own), and from kN + 4 on the rows' own
   int32_t *status;
   int64_t block_stride, head_stride;
   int B, n_new, H_q, H_kv, G, R;
@@ -250,16 +252,20 @@ __device__ int64_t q4_all_tiles(const Q4Params &P, bool &bad) {
 // Before the attention: where the ranges cut sequences (the first CTAs, a warp a range), and the query
 // rows of every (sequence, kv head and row group) as two e4m3 terms in the
 // layout of the K-major 128-byte-swizzled operand, scaled by one power of two
-// that brings the largest finite element of the entry to [2^7, 2^8). The kernel
-// then takes a sequence's Q with one bulk copy: converted there, by one warp,
-// it took 20,000 cycles a sequence.
+// that brings the largest finite element of the entry to [2^7, 2^8). Where a
+// row's own largest element lies more than 2^kNear below that (rows of padding may
+// hold anything), every row has a power of its own, so that each keeps 2^-10 of its
+// largest element whatever lies beside it. The kernel then takes a sequence's Q
+// with one bulk copy: converted there, by one warp, it took 20,000 cycles a
+// sequence.
 constexpr int kPrepWarps = 4;
+constexpr int kNear = 6;
 template <int NC>
 __global__ void __launch_bounds__(32 * kPrepWarps) attn_q4_prep_kernel(const __grid_constant__ Q4Params P) {
   using Cfg = Q4Cfg<NC>;
   constexpr int N = Cfg::kN, CP = Cfg::kCols;
   constexpr int kPass = N / (2 * kPrepWarps);   // half a warp a row and pass
-  __shared__ uint32_t s_top[kPrepWarps];
+  __shared__ uint32_t s_top[kPrepWarps], s_low[kPrepWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nrange = (P.NR + kPrepWarps - 1) / kPrepWarps;
   pdl_trigger();
@@ -283,7 +289,8 @@ __global__ void __launch_bounds__(32 * kPrepWarps) attn_q4_prep_kernel(const __g
   const int rows = min(P.Rg, P.R - row0), live0 = q4_first(rows);
   const int c8 = lane & 15;
   uint4 v[kPass];
-  uint32_t top = 0;
+  // largest finite elements (their bits): of each row, of the entry, and of its smallest row but those of zeros
+  uint32_t rtop[kPass], top = 0, low = 0x7f800000u;
 #pragma unroll
   for (int k = 0; k < kPass; ++k) {
     const int col = (k * kPrepWarps + warp) * 2 + (lane >> 4);
@@ -298,27 +305,48 @@ __global__ void __launch_bounds__(32 * kPrepWarps) attn_q4_prep_kernel(const __g
 #pragma unroll
   for (int k = 0; k < kPass; ++k) {
     const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    rtop[k] = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t lo = (w[e] << 16) & 0x7fffffffu, hi = w[e] & 0x7fff0000u;
-      if (lo < 0x7f800000u) top = max(top, lo);
-      if (hi < 0x7f800000u) top = max(top, hi);
+      if (lo < 0x7f800000u) rtop[k] = max(rtop[k], lo);
+      if (hi < 0x7f800000u) rtop[k] = max(rtop[k], hi);
     }
   }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)   // (half a warp a row)
+#pragma unroll
+    for (int k = 0; k < kPass; ++k) rtop[k] = max(rtop[k], __shfl_xor_sync(0xffffffffu, rtop[k], o));
+#pragma unroll
+  for (int k = 0; k < kPass; ++k) {
+    top = max(top, rtop[k]);
+    if (rtop[k] != 0) low = min(low, rtop[k]);
+  }
   top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) s_top[warp] = top;
+  low = __reduce_min_sync(0xffffffffu, low);
+  if (lane == 0) {
+    s_top[warp] = top;
+    s_low[warp] = low;
+  }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kPrepWarps; ++k) top = max(top, s_top[k]);
-  const int ex = min(117, max(-113, (int)(top >> 23) - 127));   // (both powers stay normal)
-  const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
+  for (int k = 0; k < kPrepWarps; ++k) {
+    top = max(top, s_top[k]);
+    low = min(low, s_low[k]);
+  }
+  const bool own = (int)(top >> 23) - (int)(low >> 23) > kNear;
+  auto power = [](uint32_t t) { return min(117, max(-113, (int)(t >> 23) - 127)); };   // (all powers stay normal)
+  // 2^-9 of the codes and 2^(7 - power) of Q
+  auto undo = [](int ex) { return __uint_as_float((uint32_t)(127 + 2 + ex) << 23); };
   uint8_t *img = P.ws_q + ent * Cfg::kQ;
-  float *qs = P.ws_qs + ent * (N + 4);
+  float *qs = P.ws_qs + ent * (2 * N + 4);
 #pragma unroll
   for (int k = 0; k < kPass; ++k) {
     const int col = (k * kPrepWarps + warp) * 2 + (lane >> 4);
     const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
     float x[8], sum = 0.f;
+    const int ex = power(own ? rtop[k] : top);
+    const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       x[2 * e] = __uint_as_float(w[e] << 16);
@@ -345,10 +373,12 @@ __global__ void __launch_bounds__(32 * kPrepWarps) attn_q4_prep_kernel(const __g
     uint8_t *dst = img + col * 128 + (((c8 >> 1) ^ (col & 7)) << 4) + (c8 & 1) * 8;
     *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
     *reinterpret_cast<uint2 *>(dst + N * 128) = make_uint2(lo[0], lo[1]);
-    if (c8 == 0) qs[col] = sum;
+    if (c8 == 0) {
+      qs[col] = sum;
+      if (own) qs[N + 4 + col] = undo(ex);
+    }
   }
-  // 2^-9 of the codes and 2^(7 - ex) of Q
-  if (threadIdx.x == 0) qs[N] = __uint_as_float((uint32_t)(127 + 2 + ex) << 23);
+  if (threadIdx.x == 0) qs[N] = own ? -1.f : undo(power(top));
 }
 
 __device__ __forceinline__ bool bar_or(int id, int threads, bool v) {
@@ -482,10 +512,34 @@ __device__ __forceinline__ void keep_after(float (&r)[N]) {
 #pragma unroll
   for (int k = 0; k < N; k += 4) asm volatile("" : "+f"(r[k]), "+f"(r[k + 1]), "+f"(r[k + 2]), "+f"(r[k + 3]));
 }
+__device__ __forceinline__ void t5_st4(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
+               : "memory");
+}
 __device__ __forceinline__ void t5_st8(uint32_t taddr, const uint32_t *r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+// Columns of S times their rows' powers of two, where they lie (nt tiles)
+template <int NC, int N>
+__device__ __noinline__ void q4_scale_rows(uint32_t s_col, int nt, const float *qf) {
+  t5_fence_after();
+#pragma unroll 1
+  for (int h = 0; h < nt; ++h)
+#pragma unroll 1
+    for (int c = 0; c < NC; c += 4) {
+      const float4 f = *reinterpret_cast<const float4 *>(qf + c);
+      float x[4];
+      t5_ld4(s_col + h * N + c, reinterpret_cast<uint32_t *>(x));
+      t5_wait_ld();
+      keep_after<4>(x);
+      x[0] *= f.x; x[1] *= f.y; x[2] *= f.z; x[3] *= f.w;
+      t5_st4(s_col + h * N + c, reinterpret_cast<const uint32_t *>(x));
+    }
+  t5_wait_st();
 }
 
 // Warps 0-3 and 4-7: softmax (a key per thread and tile; each warpgroup half
@@ -519,8 +573,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
   __shared__ int abort_flag;
   __shared__ int4 s_work;
   // per row of the items in flight: sum(q), position (0 .. n_new - 1),
-  // row of q and out; per item the power of two that undoes Q's scaling
-  __shared__ __align__(16) float s_qs[3][N];
+  // row of q and out, its own power of two; per item the power of two that undoes Q's scaling (-1: the rows have their own)
+  __shared__ __align__(16) float s_qs[3][N], s_qf[3][N];
   __shared__ __align__(16) int s_pos[3][N];
   __shared__ int s_row[3][N];
   __shared__ float s_fold[3];
@@ -671,7 +725,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       if (i >= 3) ok = q4_wait(&o_free[buf ^ 1], ((i - 3) >> 1) & 1, abf, P.wait_ns) && ok;
       if (!__all_sync(0xffffffffu, ok)) break;
       const int64_t ent = (int64_t)it.b * Hp + gp;
-      const float *qs = P.ws_qs + ent * (N + 4);
+      const float *qs = P.ws_qs + ent * (2 * N + 4);
+      const float fold = qs[N];
       for (int col = lane; col < N; col += 32) {
         const int w = col / CP, c = col - w * CP;
         const int r = row0 + (c < (w ? rows - live0 : live0) ? w * live0 + c : 0);   // (padding: any)
@@ -680,8 +735,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
         s_pos[row][col] = j;
         s_row[row][col] = (it.b * P.n_new + j) * P.H_q + g * P.G + (r - j * P.G);
       }
+      if (fold < 0.f)
+        for (int col = lane; col < N; col += 32) s_qf[row][col] = qs[N + 4 + col];
       if (lane == 0) {
-        s_fold[row] = qs[N];
+        s_fold[row] = fold;
         s_item[row] = make_int4(it.tile0, it.ntiles, it.span.L, (it.whole ? kWhole : 0) | (it.first ? kOpening : 0));
       }
       __syncwarp();
@@ -935,7 +992,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
       const float fold = P.scale_log2 * s_fold[buf];
       const int4 it = s_item[buf];
       const int tile0 = it.x, ntiles = it.y, L = it.z;
-      const int edge0 = L - P.n_new - T * kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
+      const int edge0 = fold < 0.f ? INT_MIN : L - P.n_new - T * kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
       if (t < NC) s_nb[c_first + t] = 0.f;
       float2 l2[NC / 2], b2[NC / 2];
 #pragma unroll
@@ -953,8 +1010,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
           const uint32_t src = scales + (uint32_t)(u + h) % kScales * kScaleBytes;
           asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(ka[h]), "=f"(kb[h]), "=f"(vc[h]), "=f"(vi[h]) : "r"(src + t * 16));
           asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vz[h]) : "r"(src + kTK * 16 + t * 4));
-          ka[h] *= fold;
+          ka[h] *= fabsf(fold);
         }
+        const uint32_t s_col = lanes + Cfg::kSCol + T * pb * N + c_first;
         // A step that ends past the oldest query or holds keys that a window has
         // left: position j sees a key iff 0 <= j - j0 < reach. A key that no
         // position sees (past the end, or between sinks and window) may hold
@@ -971,10 +1029,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q4_kernel(const __grid_co
             reach[h] = P.window > 0 && key >= P.sinks ? (uint32_t)P.window : 0x80000000u;
             if (key >= L || (uint32_t)(P.n_new - 1 - j0[h]) >= reach[h] + (uint32_t)(P.n_new - 1)) vi[h] = vz[h] = 0.f;
           }
+          // Rows with powers of their own (every step of such an item counts as
+          // an edge: a test apart, a second copy of the steps or a factor a score
+          // cost every call 3 to 7 %; this way it is 64 sequences 126.9 against
+          // 123.5 us, and 180 us where rows do have them).
+          ok = __all_sync(0xffffffffu, ok);
+          if (fold < 0.f && ok) q4_scale_rows<NC, N>(s_col, nt, &s_qf[buf][c_first]);
         }
         ok = __all_sync(0xffffffffu, ok);
         t5_fence_after();
-        const uint32_t s_col = lanes + Cfg::kSCol + T * pb * N + c_first;
         float2 y[T][NC / 2];   // log2 weights, minus the reference
         auto scores = [&](int h) {
           const float2 ka2 = make_float2(ka[h], ka[h]), kb2 = make_float2(kb[h], kb[h]), vc2 = make_float2(vc[h], vc[h]);
@@ -1295,7 +1358,7 @@ size_t q4_ws_bytes(const Q4Plan &p, int B, int H_kv) {
   const size_t ent = (size_t)2 * p.C * p.Rg, qent = (size_t)B * H_kv * p.RG, n = q4_cols(p);
   return align_up(ent * kD * sizeof(float), 256) + align_up(ent * 2 * sizeof(float), 256) +
          align_up((size_t)p.NR * sizeof(int4), 256) + align_up(qent * n * 256, 256) +
-         align_up(qent * (n + 4) * sizeof(float), 256);
+         align_up(qent * (2 * n + 4) * sizeof(float), 256);
 }
 
 template <int NC>
