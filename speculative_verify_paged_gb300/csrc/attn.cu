@@ -2300,6 +2300,13 @@ sv_status launch_gen(const GenParams &P, cudaStream_t st) {
 
 using namespace sv;
 
+// The element types of the pools that the entry points here take (4-bit pools,
+// which attn_impl serves too, come through spec_verify_attn_q4 alone).
+static sv_status check_pool_type(const char *what, sv_dtype kv_dtype) {
+  if (kv_dtype == SV_F32 || kv_dtype == SV_BF16 || kv_dtype == SV_FP8_E4M3) return SV_OK;
+  return fail(SV_ERR_UNSUPPORTED, "%s: caches must be f32, bf16 or fp8 (kv_dtype %d)", what, (int)kv_dtype);
+}
+
 static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache, const void *v_cache,
                            sv_dtype kv_dtype, const sv_kv_layout *layout, const float *k_scale,
                            const float *v_scale, const int32_t *block_table, int max_blocks_per_seq,
@@ -2324,7 +2331,6 @@ static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache,
     return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: fp32 caches take fp32 queries");
   if ((kv_dtype == SV_BF16 || kv_dtype == SV_FP8_E4M3) && q_dtype != SV_BF16)
     return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: bf16 / fp8 caches take bf16 queries");
-  if (kv_dtype == SV_F16) return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: f16 caches are not supported");
   if (kv_dtype == SV_FP8_E4M3 && (!k_scale || !v_scale))
     return fail(SV_ERR_INVALID_ARG, "spec_verify_attn: fp8 caches need k_scale and v_scale");
   if (d_head > 256 || d_head % 4) return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: d_head must be a multiple of 4 and <= 256");
@@ -2506,6 +2512,7 @@ extern "C" sv_status spec_verify_attn(const void *q, sv_dtype q_dtype, const voi
                                       int block_size, int num_blocks, float softmax_scale, void *out,
                                       sv_dtype out_dtype, void *workspace, size_t workspace_bytes,
                                       int32_t *dev_status, sv_stream_t stream) {
+  if (const sv_status rc = check_pool_type("spec_verify_attn", kv_dtype)) return rc;
   return attn_impl(q, q_dtype, k_cache, v_cache, kv_dtype, layout, k_scale, v_scale, block_table,
                    max_blocks_per_seq, seq_lens, B, n_new, H_q, H_kv, d_head, block_size, num_blocks,
                    softmax_scale, out, out_dtype, workspace, workspace_bytes, dev_status, 0, nullptr, 0, 0, stream);
@@ -2520,6 +2527,7 @@ extern "C" sv_status spec_verify_attn_ex(const void *q, sv_dtype q_dtype, const 
                                          size_t workspace_bytes, int32_t *dev_status, int blocks_per_split,
                                          sv_stream_t stream) {
   if (blocks_per_split < 0) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_ex: blocks_per_split < 0");
+  if (const sv_status rc = check_pool_type("spec_verify_attn_ex", kv_dtype)) return rc;
   return attn_impl(q, q_dtype, k_cache, v_cache, kv_dtype, layout, k_scale, v_scale, block_table,
                    max_blocks_per_seq, seq_lens, B, n_new, H_q, H_kv, d_head, block_size, num_blocks,
                    softmax_scale, out, out_dtype, workspace, workspace_bytes, dev_status,
@@ -2542,6 +2550,7 @@ extern "C" sv_status spec_verify_attn_tree(const void *q, sv_dtype q_dtype, cons
                                            void *out, sv_dtype out_dtype, void *workspace,
                                            size_t workspace_bytes, int32_t *dev_status, sv_stream_t stream) {
   if (!tree_parent) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_tree: tree_parent is NULL");
+  if (const sv_status rc = check_pool_type("spec_verify_attn_tree", kv_dtype)) return rc;
   return attn_impl(q, q_dtype, k_cache, v_cache, kv_dtype, layout, k_scale, v_scale, block_table,
                    max_blocks_per_seq, seq_lens, B, n_new, H_q, H_kv, d_head, block_size, num_blocks,
                    softmax_scale, out, out_dtype, workspace, workspace_bytes, dev_status, 0, tree_parent, 0, 0, stream);
@@ -2569,8 +2578,7 @@ extern "C" sv_status spec_verify_attn_window(const void *q, sv_dtype q_dtype, co
   if (window < 0 || sinks < 0) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_window: negative window or sinks");
   if (max_blocks_per_seq > 0 && block_size > 0 && !capacity_ok(max_blocks_per_seq, block_size))
     return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn_window: max_blocks_per_seq * block_size must be below 2^30");
-  if (kv_dtype != SV_F32 && kv_dtype != SV_BF16 && kv_dtype != SV_FP8_E4M3)
-    return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn_window: caches must be f32, bf16 or fp8");
+  if (const sv_status rc = check_pool_type("spec_verify_attn_window", kv_dtype)) return rc;
   return attn_impl(q, q_dtype, k_cache, v_cache, kv_dtype, layout, k_scale, v_scale, block_table,
                    max_blocks_per_seq, seq_lens, B, n_new, H_q, H_kv, d_head, block_size, num_blocks,
                    softmax_scale, out, out_dtype, workspace, workspace_bytes, dev_status, 0, nullptr, window, sinks,
