@@ -229,6 +229,20 @@ def _check_latent_pool(cache, d_total, block_size, what):
                          % (what, cache.shape[2], d_total))
 
 
+def _is_q4(k_cache):
+    """4-bit pools are uint8 [num_blocks, H_kv, record]; fp8 pools have four dimensions."""
+    return k_cache.dtype == torch.uint8 and k_cache.dim() == 3
+
+
+def _not_q4(what, row, *pools):
+    """Refuses 4-bit pools where pools of whole elements are read: taken for e4m3 ones of `row` bytes a block and
+    head they would be read and written past their end."""
+    for p in pools:
+        if _is_q4(p) and p.shape[2] != row:
+            raise ValueError("%s does not take 4-bit pools; e4m3 pools are [num_blocks, H_kv, block_size, d], got %s"
+                             % (what, tuple(p.shape)))
+
+
 def _layout_arg(layout):
     if layout is None:
         return None
@@ -241,6 +255,8 @@ def kv_block_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_sca
                     v_scale=None, block_size=16, layout=None, status=None):
     """Write k_new/v_new [B, n_new, H_kv, d] at positions seq_lens-n_new .. seq_lens-1."""
     _int32(block_table=block_table, seq_lens=seq_lens)
+    if layout is None:
+        _not_q4("kv_block_append", block_size * k_new.shape[-1], k_cache, v_cache)
     lib = load_library()
     _cuda(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, status)
     B, n_new, H_kv, d = k_new.shape
@@ -257,6 +273,8 @@ def kv_tree_commit(k_cache, v_cache, block_table, seq_lens, path_nodes, num_acce
     """Move each sequence's accepted tree path (path_nodes [B, n_new], num_accepted [B])
     next to the root in the paged pools; pools [num_blocks, H_kv, bs, d] unless layout."""
     _int32(block_table=block_table, seq_lens=seq_lens, path_nodes=path_nodes, num_accepted=num_accepted)
+    if layout is None:
+        _not_q4("kv_tree_commit", -1, k_cache, v_cache)
     lib = load_library()
     _cuda(k_cache, v_cache, block_table, seq_lens, path_nodes, num_accepted, status)
     B, n_new = path_nodes.shape
@@ -297,6 +315,8 @@ def spec_verify_attn(q, k_cache, v_cache, block_table, seq_lens, softmax_scale=N
     tree_parent (int32 [B, n_new], optional): the new positions are a draft tree in BFS
     order and each query sees only its ancestors among them."""
     _int32(block_table=block_table, seq_lens=seq_lens, tree_parent=tree_parent)
+    if layout is None:
+        _not_q4("spec_verify_attn", block_size * q.shape[-1], k_cache, v_cache)
     lib = load_library()
     _cuda(q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out, workspace, status,
           tree_parent)
@@ -394,11 +414,6 @@ def alloc_q4_pools(num_blocks, H_kv, d_head, block_size=16, device="cuda"):
     """A zeroed pair (k_cache, v_cache) of 4-bit pools, uint8 [num_blocks, H_kv, record]."""
     shape = (int(num_blocks), int(H_kv), q4_record_bytes(d_head, block_size))
     return tuple(torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2))
-
-
-def _is_q4(k_cache):
-    """4-bit pools are uint8 [num_blocks, H_kv, record]; fp8 pools have four dimensions."""
-    return k_cache.dtype == torch.uint8 and k_cache.dim() == 3
 
 
 def _q4_pools(what, k_cache, v_cache, d, block_size, layout, num_blocks, H_kv):
@@ -920,7 +935,9 @@ def tree_verify_step(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, t
     """One tree-verify round of one layer, in stream order: append the n node rows,
     tree attention, tree sampling, then move each accepted path next to its root
     (kv_tree_commit). Returns (attn_out, out_tokens, num_accepted, path_nodes); the
-    next round's length is seq_lens - n + num_accepted + 1 (BlockManager.commit_verify)."""
+    next round's length is seq_lens - n + num_accepted + 1 (BlockManager.commit_verify).
+    Pools of f32, bf16 or e4m3: a tree's rows cannot be moved inside 4-bit blocks."""
+    _not_q4("tree_verify_step", -1, k_cache, v_cache)
     kv_block_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, status=status)
     out = spec_verify_attn(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, k_scale, v_scale,
                            status=status, tree_parent=tree_parent)
