@@ -2248,13 +2248,12 @@ sv_status launch_tc5(const TcParams &P0, cudaStream_t st) {
   using Cfg = T5Cfg<QR, FP8>;
   TcParams P = P0;
   P.tblk = Cfg::kBlk;   // the partition counts this kernel's tiles
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(attn_tc5_kernel<QR, FP8, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
-    if (!WIN && attr_err == cudaSuccess)
-      attr_err = cudaFuncSetAttribute(attn_tc5_bal_kernel<QR, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      Cfg::kSmem);
+  static DeviceOnce once;
+  const cudaError_t attr_err = once_per_device(once, [] {
+    cudaError_t e = cudaFuncSetAttribute(attn_tc5_kernel<QR, FP8, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    if (!WIN && e == cudaSuccess)
+      e = cudaFuncSetAttribute(attn_tc5_bal_kernel<QR, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    return e;
   });
   if (attr_err != cudaSuccess)
     return fail(SV_ERR_CUDA, "spec_verify_attn: cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));

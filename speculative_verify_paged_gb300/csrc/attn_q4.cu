@@ -46,7 +46,6 @@
 // range without draining the pipeline. A range that ends inside a sequence
 // leaves fp32 partials for the merge.
 #include <algorithm>
-#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -1363,15 +1362,10 @@ size_t q4_ws_bytes(const Q4Plan &p, int B, int H_kv) {
 
 template <int NC>
 sv_status launch_q4(const Q4Params &P, int C, cudaStream_t st) {
-  // (the attribute belongs to the device)
-  static std::atomic<uint64_t> set{0};
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  const uint64_t bit = 1ull << (dev & 63);
-  if (err == cudaSuccess && !(set.load(std::memory_order_relaxed) & bit)) {
-    err = cudaFuncSetAttribute(attn_q4_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4Cfg<NC>::kSmem);
-    if (err == cudaSuccess) set.fetch_or(bit, std::memory_order_relaxed);
-  }
+  static DeviceOnce once;
+  const cudaError_t err = once_per_device(once, [] {
+    return cudaFuncSetAttribute(attn_q4_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4Cfg<NC>::kSmem);
+  });
   if (err != cudaSuccess) return fail(SV_ERR_CUDA, "spec_verify_attn_q4: cudaFuncSetAttribute: %s", cudaGetErrorString(err));
   const int64_t prep = (P.NR + kPrepWarps - 1) / kPrepWarps + (int64_t)P.B * P.H_kv * P.RG;
   launch_k(attn_q4_prep_kernel<NC>, dim3((unsigned)prep), dim3(32 * kPrepWarps), 0, st, 1, P);

@@ -6,8 +6,6 @@
 #include <cstring>
 #include <type_traits>
 
-#include <mutex>
-
 #include "sv_common.cuh"
 
 namespace sv {
@@ -296,11 +294,10 @@ extern "C" sv_status kv_tree_commit(void *k_cache, void *v_cache, sv_dtype kv_dt
   a.unit = (a.row_bytes % 16 == 0 && aligned(k_cache, 16) && aligned(v_cache, 16) && a.block_stride % 16 == 0 &&
             a.head_stride % 16 == 0 && a.slot_stride % 16 == 0) ? 16 : 1;
   const size_t smem = (size_t)(n_new - 1) * a.row_bytes + 16;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(kv_tree_commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    63 * kCmMaxRowBytes + 16);
+  static DeviceOnce once;
+  const cudaError_t attr_err = once_per_device(once, [] {
+    return cudaFuncSetAttribute(kv_tree_commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                63 * kCmMaxRowBytes + 16);
   });
   if (attr_err != cudaSuccess) return fail(SV_ERR_CUDA, "kv_tree_commit attributes: %s", cudaGetErrorString(attr_err));
   const cudaError_t e = launch_k(kv_tree_commit_kernel, dim3(B, 2), dim3(kCmThreads), smem,

@@ -758,11 +758,9 @@ extern "C" sv_status spec_verify_attn_mla(const void *q_lat, sv_dtype q_dtype, c
   P.max_blocks = max_blocks_per_seq; P.num_blocks = num_blocks; P.bps = plan.bps; P.S = plan.S;
   P.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634074);
 
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(attn_mla_kernel<kLNK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    MlaCfg<kLNK>::kSmem);
+  static DeviceOnce once;
+  const cudaError_t attr_err = once_per_device(once, [] {
+    return cudaFuncSetAttribute(attn_mla_kernel<kLNK>, cudaFuncAttributeMaxDynamicSharedMemorySize, MlaCfg<kLNK>::kSmem);
   });
   if (attr_err != cudaSuccess)
     return fail(SV_ERR_CUDA, "spec_verify_attn_mla: kernel attributes: %s", cudaGetErrorString(attr_err));

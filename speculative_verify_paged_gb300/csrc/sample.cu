@@ -1586,17 +1586,18 @@ void split_ff(double d, float &hi, float &lo) {
 
 template <typename TT, int DK>
 sv_status launch_sample(const SampleParams &P, int cs, cudaStream_t s) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  static int fin_blocks = 0;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(sample_draw_kernel<TT, DK>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  static DeviceOnce once;
+  static std::atomic<int> fin_grid{0};
+  const cudaError_t attr_err = once_per_device(once, [] {
+    cudaError_t e = cudaFuncSetAttribute(sample_draw_kernel<TT, DK>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     int per_sm = 0;
-    if (attr_err == cudaSuccess)
-      attr_err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, sample_finish_kernel<TT, DK>, kFinThreads, 0);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, sample_finish_kernel<TT, DK>, kFinThreads, 0);
     // one CTA per SM (the kernel is bound to one by its registers), all resident
-    fin_blocks = std::min(kMaxFinCtas, sm_count() * std::min(per_sm, 1));
+    fin_grid.store(std::min(kMaxFinCtas, sm_count() * std::min(per_sm, 1)), std::memory_order_relaxed);
+    return e;
   });
+  const int fin_blocks = fin_grid.load(std::memory_order_relaxed);
   if (attr_err != cudaSuccess)
     return fail(SV_ERR_CUDA, "spec_verify_sample: kernel attributes: %s", cudaGetErrorString(attr_err));
   if (fin_blocks < 1) return fail(SV_ERR_CUDA, "spec_verify_sample: the finish grid does not fit on the device");

@@ -15,6 +15,7 @@
 #include <utility>
 
 #include "../../include/specverify.h"
+#include "device_once.cuh"
 
 namespace sv {
 
@@ -54,6 +55,14 @@ inline sv_status check_launch(const char *what) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(SV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return ok();
+}
+
+// f() once for the current device (DeviceOnce).
+template <typename F>
+inline cudaError_t once_per_device(DeviceOnce &once, F f) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : once.run<cudaError_t>(dev, f);
 }
 
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

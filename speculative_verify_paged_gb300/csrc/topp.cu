@@ -50,7 +50,6 @@
 // compares logits with two thresholds.
 
 #include <cmath>
-#include <mutex>
 
 #include "sv_common.cuh"
 
@@ -1122,13 +1121,12 @@ sv_status launch_topp_filter(sv_dtype dtype, const void *in0, void *out0, int ro
   if (V <= kTbMaxV) {
     // exact per-bin masses: rows up to kTbMaxV logits
     for (int j = 0; j < 128; ++j) P.base[j] = (unsigned long long)std::llround(std::ldexp(std::exp2(-j / 128.0), 62));
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
+    static DeviceOnce once;
+    const cudaError_t attr = once_per_device(once, [] {
       const cudaError_t e1 = cudaFuncSetAttribute(topp_bin_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTbSmem);
       const cudaError_t e2 = cudaFuncSetAttribute(topp_bin_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTbSmem);
       const cudaError_t e3 = cudaFuncSetAttribute(topp_bin_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTbSmem);
-      attr = e1 != cudaSuccess ? e1 : (e2 != cudaSuccess ? e2 : e3);
+      return e1 != cudaSuccess ? e1 : (e2 != cudaSuccess ? e2 : e3);
     });
     if (attr != cudaSuccess) return fail(SV_ERR_CUDA, "top-p filter: cudaFuncSetAttribute: %s", cudaGetErrorString(attr));
     switch (dtype) {
