@@ -489,16 +489,22 @@ def kv_block_gather_q4(k_cache, v_cache, block_table, seq_lens, start, n_rows, d
     return k_out, v_out
 
 
+def _span(window, sinks):
+    """(window, sinks) as 32-bit integers: a table holds fewer than 2^30 tokens, so larger values mean what the largest
+    does (and any below zero is refused by the library)."""
+    return tuple(max(-1, min(int(x), 2 ** 31 - 1)) for x in (window, sinks))
+
+
 @functools.lru_cache(maxsize=1024)
 def attn_window_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size=16, window=0, sinks=0):
     return load_library().spec_verify_attn_window_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq,
-                                                                 block_size, int(window), int(sinks))
+                                                                 block_size, *_span(window, sinks))
 
 
 @functools.lru_cache(maxsize=1024)
 def attn_q4_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size=16, window=0, sinks=0):
     return load_library().spec_verify_attn_q4_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq,
-                                                             block_size, int(window), int(sinks))
+                                                             block_size, *_span(window, sinks))
 
 
 def _attn_outputs(what, q, block_table, seq_lens, out, workspace, status):
@@ -515,6 +521,7 @@ def spec_verify_attn_window(q, k_cache, v_cache, block_table, seq_lens, window, 
     """Paged GQA verify attention through a sliding window: the query at position p sees key t <= p iff
     t > p - window or t < sinks (window = 0: every key). Pools and layout as for spec_verify_attn."""
     what = "spec_verify_attn_window"
+    window, sinks = _span(window, sinks)
     if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         _int32(block_table=block_table, seq_lens=seq_lens)
     _attn_outputs(what, q, block_table, seq_lens, out, workspace, status)
@@ -540,11 +547,11 @@ def spec_verify_attn_window(q, k_cache, v_cache, block_table, seq_lens, window, 
     max_blocks = block_table.shape[1]
     if workspace is None:
         workspace = alloc_workspace(attn_window_workspace_size(B, n_new, H_q, H_kv, d, max_blocks, block_size,
-                                                               max(window, 0), max(sinks, 0)), q.device)
+                                                               window, sinks), q.device)
     _check(load_library().spec_verify_attn_window(
         _ptr(q), _dtype_code(q), _ptr(k_cache), _ptr(v_cache), _dtype_code(k_cache), _layout_arg(layout),
         _ptr(k_scale), _ptr(v_scale), _ptr(block_table), max_blocks, _ptr(seq_lens), B, n_new, H_q, H_kv, d,
-        block_size, num_blocks, float(softmax_scale), int(window), int(sinks), _ptr(out), _dtype_code(out),
+        block_size, num_blocks, float(softmax_scale), window, sinks, _ptr(out), _dtype_code(out),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status), _stream()))
     return out
 
@@ -555,6 +562,7 @@ def spec_verify_attn_q4(q, k_cache, v_cache, block_table, seq_lens, softmax_scal
     """Paged GQA verify attention over 4-bit pools (kv_block_append_q4), q [B, n_new, H_q, d] bf16 or f32; with
     window > 0 the query at position p sees key t <= p iff t > p - window or t < sinks."""
     what = "spec_verify_attn_q4"
+    window, sinks = _span(window, sinks)
     if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         _int32(block_table=block_table, seq_lens=seq_lens)
     _attn_outputs(what, q, block_table, seq_lens, out, workspace, status)
@@ -568,10 +576,10 @@ def spec_verify_attn_q4(q, k_cache, v_cache, block_table, seq_lens, softmax_scal
     max_blocks = block_table.shape[1]
     if workspace is None:
         workspace = alloc_workspace(attn_q4_workspace_size(B, n_new, H_q, H, d, max_blocks, block_size,
-                                                           max(window, 0), max(sinks, 0)), q.device)
+                                                           window, sinks), q.device)
     _check(load_library().spec_verify_attn_q4(
         _ptr(q), _dtype_code(q), _ptr(k_cache), _ptr(v_cache), _layout_arg(layout), _ptr(block_table), max_blocks,
-        _ptr(seq_lens), B, n_new, H_q, H, d, block_size, nb, float(softmax_scale), int(window), int(sinks),
+        _ptr(seq_lens), B, n_new, H_q, H, d, block_size, nb, float(softmax_scale), window, sinks,
         _ptr(out), _dtype_code(out), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
         _stream()))
     return out
