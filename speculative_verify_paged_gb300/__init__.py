@@ -533,6 +533,12 @@ def spec_verify_attn_window(q, k_cache, v_cache, block_table, seq_lens, window, 
         num_blocks, H_kv = k_cache.shape[0], k_cache.shape[1]
     elif H_kv is None or num_blocks is None:
         raise ValueError("with an explicit layout pass num_blocks and H_kv")
+    else:
+        end = (num_blocks - 1) * layout[0] + (H_kv - 1) * layout[1] + (block_size - 1) * layout[2] + d
+        for t in (k_cache, v_cache):   # (past the view, but not past the memory under it)
+            held = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+            if end > held:
+                raise ValueError("%s: the layout reaches element %d of a pool of %d" % (what, end, held))
     if k_cache.dtype != v_cache.dtype:
         raise ValueError("%s: k_cache and v_cache must have one dtype" % what)
     if _dtype_code(k_cache) == SV_FP8_E4M3:

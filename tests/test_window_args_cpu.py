@@ -50,3 +50,27 @@ def test_workspace_of_a_window_past_32_bits():
     assert sv.attn_window_workspace_size(*shape, 2 ** 32 + 5, 0) == sv.attn_workspace_size(*shape)
     assert sv.attn_q4_workspace_size(*shape, 2 ** 32 + 5, 0) == sv.attn_q4_workspace_size(*shape)
     assert sv.attn_window_workspace_size(*shape, -1, 0) == sv.attn_window_workspace_size(*shape, 2, -2 ** 32 - 1) == 0
+
+
+def test_layouts_past_the_pool():
+    # one layer of [blocks][slots][layers][H_kv][d]: the last rows of the last block are the pool's last elements
+    nb, bs, layers, H, d = 6, 16, 3, 2, 128
+    big = torch.zeros(nb, bs, layers, H, d, dtype=torch.bfloat16)
+    q = torch.zeros(2, 3, 8, d, dtype=torch.bfloat16)
+    table, lens = torch.zeros(2, 4, dtype=torch.int32), torch.full((2,), 20, dtype=torch.int32)
+    layout = (bs * layers * H * d, d, layers * H * d)
+
+    def call(layer, blocks, lay=layout, first=None):
+        v = big.view(-1)[layer * H * d:]
+        sv.spec_verify_attn_window(q, v if first is None else v[:first], v, table, lens, 4, layout=lay, num_blocks=blocks,
+                                   H_kv=H)
+
+    for layer in range(layers):   # within the pool: as far as the check for CUDA tensors
+        with pytest.raises(ValueError, match="CUDA"):
+            call(layer, nb)
+    with pytest.raises(ValueError, match="CUDA"):
+        call(0, nb, first=H * d)   # a view of the first rows only
+    with pytest.raises(ValueError, match="layout reaches"):
+        call(0, nb + 1)
+    with pytest.raises(ValueError, match="layout reaches"):
+        call(2, nb, (bs * layers * H * d, d, layers * H * d + 128))
