@@ -507,7 +507,7 @@ def attn_q4_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, bloc
                                                              block_size, *_span(window, sinks))
 
 
-def _attn_outputs(what, q, block_table, seq_lens, out, workspace, status):
+def _attn_outputs(what, q, block_table, seq_lens, out, status):
     if q.dim() != 4:
         raise ValueError("%s: q must be [B, n_new, H_q, d]" % what)
     _check_batch(what, q.shape[0], block_table, seq_lens)
@@ -524,7 +524,7 @@ def spec_verify_attn_window(q, k_cache, v_cache, block_table, seq_lens, window, 
     window, sinks = _span(window, sinks)
     if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         _int32(block_table=block_table, seq_lens=seq_lens)
-    _attn_outputs(what, q, block_table, seq_lens, out, workspace, status)
+    _attn_outputs(what, q, block_table, seq_lens, out, status)
     B, n_new, H_q, d = q.shape
     if layout is None:
         if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or tuple(k_cache.shape[2:]) != (block_size, d):
@@ -571,7 +571,7 @@ def spec_verify_attn_q4(q, k_cache, v_cache, block_table, seq_lens, softmax_scal
     window, sinks = _span(window, sinks)
     if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         _int32(block_table=block_table, seq_lens=seq_lens)
-    _attn_outputs(what, q, block_table, seq_lens, out, workspace, status)
+    _attn_outputs(what, q, block_table, seq_lens, out, status)
     B, n_new, H_q, d = q.shape
     nb, H = _q4_pools(what, k_cache, v_cache, d, block_size, layout, num_blocks, H_kv)
     _ready(what, q, k_cache, v_cache, block_table, seq_lens, out, workspace, status)
