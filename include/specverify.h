@@ -40,10 +40,10 @@
  *     Outputs that depended on the bad value are unspecified.
  *   - No C++ exception crosses this interface.
  *   - Kernels are launched with programmatic stream serialization: a call
- *     may start while the previous kernel of the stream drains, and
- *     kv_block_append reads its inputs (new rows, table, lengths) before
- *     it waits for that kernel. A kernel of the caller that produces those
- *     inputs must therefore not release its dependents early
+ *     may start while the previous kernel of the stream drains, and reads
+ *     block tables and lengths before it waits for that kernel. A kernel of
+ *     the caller that produces those must therefore not release its
+ *     dependents early
  *     (griddepcontrol.launch_dependents before its last write); kernels that
  *     never do (the default) and copies are safe.
  *
@@ -351,7 +351,17 @@ sv_status spec_verify_attn_window(const void *q, sv_dtype q_dtype,
  *   (H_q/H_kv) * n_new <= 128 run on the tensor cores (q and out must then be
  *   16-byte aligned, else SV_ERR_INVALID_ARG; beyond 64 query rows per kv head
  *   the cache is read once for every 64); every other supported shape, and
- *   pools of more than 64 GB, run on a CUDA-core kernel with fp32 arithmetic.
+ *   pools of more than 64 GB, run on a CUDA-core kernel with fp32 arithmetic,
+ *   which keeps the queries in shared memory: at d_head 128 it takes up to
+ *   147 query rows per kv head, fewer at 256 (SV_ERR_UNSUPPORTED above).
+ *   Precision on the tensor cores: a query row enters with an error of at
+ *   most 2^-10 of its largest element per element (two e4m3 terms; bf16's 8
+ *   bits are kept down to 2^-9 of the largest element of the rows of a
+ *   sequence and kv head, or of its own where rows differ by more than 2^6).
+ *   Weights, times their values' scale, are rounded to f16: 2^-11 relative
+ *   down to 2^-17 of the row's largest, and 2^-28 of that one absolutely
+ *   below. Scores, sums, scales and outputs are fp32 until the last rounding.
+ *   What other rows hold does not spoil a row: padding may be anything.
  *   The workspace is spec_verify_attn_q4_workspace_size(...) bytes, 256-byte
  *   aligned; its contents need no initialisation. It holds the converted
  *   queries and partial results of one call: calls that may run at the same

@@ -466,7 +466,7 @@ __device__ __forceinline__ float t5_store_q(uint32_t q_smem, int row, const uint
 // and tiles that hold a key some row's window has left get one more compare.
 // Measured: 64 sequences, 5 positions of 64/8 heads, window 1024 + 4 sinks over
 // bf16 pages 58 us (281 MB, 4.8 TB/s: 512 items on 304 CTA slots are two waves);
-// 128 sequences, 9 positions of 32/8 heads, window 500 + 17 over e4m3 pages 71 us
+// 128 sequences, 9 positions of 32/8 heads, window 500 + 17 over e4m3 pages 71.5 us
 // (151 MB; the V widening stage sets the tile rate, as without a window).
 template <int QR, bool FP8, bool WIN>
 __global__ void __launch_bounds__(T5Cfg<QR, FP8>::kThreads, 2) attn_tc5_kernel(const __grid_constant__ TcParams P) {

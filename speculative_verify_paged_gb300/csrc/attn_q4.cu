@@ -34,10 +34,10 @@
 // What bounds it: 136 bytes per key and kv head leave about 820 SM cycles per
 // 128-key tile at the measured HBM bandwidth, for 2 x 128 x 128 codes to unpack
 // and 128 R exponentials. Measured: 64 sequences of 1024-8192 keys, 5 positions,
-// 64/8 heads take 122.5 us (330 MB, 2.7 TB/s; 49 us at the bandwidth), 128K keys
-// with 8 positions 80.5 us, about 1650 cycles a tile of 40 rows. A tile takes 4130
+// 64/8 heads take 126.4 us (330 MB, 2.6 TB/s; 49 us at the bandwidth), 128K keys
+// with 8 positions 81.5 us, about 1700 cycles a tile of 40 rows. A tile takes 4150
 // warp instructions (V 485, K 361, the exponentials and P' 625, the scores 700,
-// the rest copies, waits and bookkeeping) at 61 % of the issue slots; the softmax
+// the rest copies, waits and bookkeeping) at 60 % of the issue slots; the softmax
 // warps are the ones the others wait for, and each part that is taken out for a
 // test gains 3 to 9 %.
 //
@@ -88,8 +88,9 @@ constexpr float kUnset = 1e30f;            // minus the reference of a row that 
 constexpr float kTop = 7.f, kMove = 15.f;
 
 // Query rows of a CTA that the first softmax warpgroup takes: up to 8 it takes
-// all, so that a step's fixed work is done once (64 sequences of 1024-8192 keys, 8
-// rows: 91.8 against 94.9 us; up to 16 it would be 106 against 99 with 16 rows).
+// all, so that a step's fixed work is done once (64 sequences of 1024-8192 keys,
+// captured: 4 rows 90.3 against 97.4 us, 8 rows 96.4 against 97.4; up to 16 it
+// would be 106.7 against 104.6 with 16 rows, 105.6 against 104.6 with 12).
 constexpr int kAlone = 8;
 __host__ __device__ inline int q4_first(int rows) { return rows <= kAlone ? rows : (rows + 1) / 2; }
 
@@ -119,9 +120,11 @@ template <int NC> struct Q4Cfg {   // NC query rows per softmax warpgroup
   static constexpr int kCols = (NC + 7) / 8 * 8, kN = 2 * kCols;   // columns of S and O
   static constexpr int kT = NC > 24 ? 1 : 2;   // tiles of a softmax step (their scores stay in registers)
   // Registers: the K, V and service warps hand over theirs so that the softmax
-  // warps hold a step's scores and two sums per column. 144 / 40 against 168 / 32:
-  // 62.7 and 64.5 us with 4 columns, 121.9 and 127.9 with 20, 150.2 and 143.0 with
-  // 24, 84.4 and 80.5 with 32 (spills on one side or the other).
+  // warps hold a step's scores and two sums per column. 144 / 40 against 168 / 32
+  // (64 sequences of 1024-8192 keys, captured, resolution 1 us): 89.2 and 91.2 us
+  // with 4 columns, 104.6 and 105.6 with 8, 113.8 and 115.8 with 12, 122.0 and
+  // 125.0 with 16, 136.3 both with 20, 152.7 and 148.6 with 24, 197.8 and 186.5
+  // with 32 (spills on one side or the other).
   static constexpr int kRegsSoftmax = NC <= 20 ? 144 : 168, kRegsOther = NC <= 20 ? 40 : 32;
   static_assert(256 * kRegsSoftmax + 32 * (kWarps - 8) * kRegsOther <= 32 * kWarps * kRegs, "registers");
   static constexpr int kQ = kN * 256;   // the two e4m3 terms of a row, 128 bytes each
@@ -1342,9 +1345,14 @@ Q4Plan q4_plan(int B, int n_new, int H_q, int H_kv, int d, int max_blocks, int b
   p.RG = (p.R + 63) / 64;                // at most 64 query rows a CTA (the registers of the softmax warps)
   p.Rg = (p.R + p.RG - 1) / p.RG;
   const int64_t Hp = (int64_t)H_kv * p.RG;
-  // Four tiles in all stay in one range, which needs no merge (captured, 8 kv
-  // heads, one position: 256 keys 6.7 against 8.6 us, 512 keys 7.9 against 8.6,
-  // 1000 keys 10.3 against 9.1).
+  // Four tiles in all stay in one range, which needs no merge (captured, with the
+  // replay's own 5 us: 256 keys, one position, 13.4 against 17.5 us with 8 kv
+  // heads and 14.4 against 16.6 with 40; 512 keys 15.5 against 16.5 and 15.5
+  // against 18.6; 8 positions of 64/8 heads 19.6 against 23.7 at 256 keys and
+  // 22.6 against 24.7 at 512. Up to eight tiles 1000 keys gain nothing.) A range
+  // per SM and kv head leaves SMs idle where the heads do not divide them: 40
+  // heads take 120 of 152, 77 and more have one range each (80 heads as long as
+  // 152: 294 and 298 us for 16 sequences of 4000).
   p.NR = tiles <= 4 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(q4_sms() / Hp, tiles));
   p.C = (int)(p.NR * Hp);
   return p;

@@ -124,10 +124,10 @@ __device__ __forceinline__ void transpose8(uint32_t (&x)[8]) {
 // where a value lies within 2^-16 of the middle between two codes is the division
 // done.
 // Measured: 2 x 16 x 2047 bf16 rows of 8 heads of 128 (170 MB to move, 25 us at
-// the measured bandwidth) take 52 us: bound by instruction issue (83 % of the
-// slots, some 210 warp instructions for two rows). One lane per row works out its
-// scale; with all lanes of a row doing so it took 60. Twelve CTAs an SM (40
-// registers) against nine: 2 us.
+// the measured bandwidth) take 57 us (f32 rows: 64): bound by instruction issue
+// (82 % of the slots, some 200 warp instructions for two rows). One lane per row
+// works out its scale; with all lanes of a row doing so it took 8 us more. Twelve
+// CTAs an SM (40 registers) against nine: 2 us.
 template <typename TIn, int NE>
 __global__ void __launch_bounds__(32 * kQaWarps, sizeof(TIn) == 2 ? 12 : 8) q4_append_kernel(const __grid_constant__ Q4AppendArgs a, bool vec) {
   constexpr int d = 32 * NE, W = d / 8;                              // words of a row
@@ -311,7 +311,8 @@ __device__ __forceinline__ void write8(TO *dst, bool vec, uint32_t e, uint32_t o
 // slots a lane, turned in registers. Rows are written eight elements at a time,
 // a row's lanes side by side. Rows outside the sequence, and those of a block
 // with a number out of range, are written as zeros. Bound by HBM: 16 x 8192 rows
-// of 8 heads of 128 (643 MB) take 99 us, 6.5 TB/s (a thread per value: 906 us).
+// of 8 heads of 128 (643 MB) take 99 us, 6.5 TB/s (a thread per value: 906 us);
+// as f32 rows (1.22 GB) 236 us.
 constexpr int kQgWarps = 8;
 template <typename TO, int NE>
 __global__ void __launch_bounds__(32 * kQgWarps) q4_gather_kernel(const __grid_constant__ Q4GatherArgs a, bool vec) {
