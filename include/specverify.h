@@ -397,6 +397,160 @@ sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const void *k_cac
                               sv_stream_t stream);
 
 /* ------------------------------------------------------------------------ *
+ * 8-bit block-scaled paged cache ("KV Cache + Speculative Decoding", section
+ * 4.5 and Q9: FP8 KV with a scale; here one for each block of tokens and kv
+ * head, set by the rows themselves, so that nothing has to be calibrated)
+ *
+ * Pools. K and V pools are bytes, [num_blocks][page]: the page of a block
+ * holds its e4m3 codes, [H_kv][block_size][d_head], then one f32 scale per kv
+ * head, and is padded to a multiple of 128 bytes: sv_q8_page_bytes(H_kv,
+ * d_head, block_size) bytes. A value is code * scale. d_head: a multiple of
+ * 16, <= 256; block_size <= 64 (SV_ERR_UNSUPPORTED otherwise; the size query
+ * returns 0). Pools are 16-byte aligned. A non-NULL layout gives the stride
+ * between pages in BYTES (block_stride: a multiple of 16, at least a page;
+ * head_stride and slot_stride 0), e.g. a per-layer slice of a larger pool.
+ * sv_copy_blocks copies such pages like any others. max_blocks_per_seq *
+ * block_size must be below 2^30 (SV_ERR_UNSUPPORTED).
+ * Scales are read within 2^-32 .. 2^32 (a page of zeros holds zeros). The
+ * code of NaN (0x7f, 0xff) is never written by the append; where a page
+ * filled otherwise holds one in a slot that some query sees, the outputs of
+ * that sequence and kv head may be NaN.
+ *
+ * kv_block_append_q8
+ *   kv_block_append into 8-bit pools. For the new rows of one (block, kv
+ *   head), with A their largest magnitude (NaN left out), e is the smallest
+ *   integer with A <= 448 * 2^e, kept within -32..32 (A = 0: -32). Rows that
+ *   start at slot 0 open the block: its scale becomes 2^e. Otherwise it
+ *   becomes the larger of 2^e and the scale it has, and where that grows,
+ *   the codes of the slots that the call does not write are moved to it:
+ *   e4m3(code * old / new), exact but for codes that become subnormal. A new
+ *   element becomes e4m3(x / scale), to nearest even, saturated at +-448; a
+ *   NaN becomes 0.
+ *   k_new, v_new: [B][n_new][H_kv][d_head], SV_F32 or SV_BF16. No two
+ *   sequences of a call may write the same block (copy-on-write is the
+ *   caller's job, as for kv_block_append). Rejected rows that a rollback
+ *   leaves behind may have raised a block's scale: it stays raised until the
+ *   block is opened again, which costs bits only where codes are subnormal.
+ *
+ * kv_block_gather_q8
+ *   Reads cached rows back, as kv_block_gather_q4 does: k_out[b][i][g][:],
+ *   v_out[b][i][g][:] = the values of position start[b] + i of sequence b,
+ *   i < n_rows, as SV_BF16 (rounded to nearest even; exact for scales that
+ *   the append wrote) or SV_F32; positions outside [0, seq_lens[b]) give
+ *   zero rows. start: device int32 [B]. A length outside [0,
+ *   max_blocks_per_seq * block_size] or a bad block sets SV_DEV_* and gives
+ *   zero rows.
+ *
+ * spec_verify_attn_q8
+ *   spec_verify_attn over 8-bit pools, with the window and sinks of
+ *   spec_verify_attn_window (window = 0: every key). q, out: SV_BF16 or
+ *   SV_F32. The workspace is spec_verify_attn_q8_workspace_size(...) bytes,
+ *   256-byte aligned; its contents need no initialisation. It holds what one
+ *   call computes on the way: calls that may run at the same time need one
+ *   each.
+ * ------------------------------------------------------------------------ */
+size_t sv_q8_page_bytes(int H_kv, int d_head, int block_size);
+
+sv_status kv_block_append_q8(const void *k_new, const void *v_new, sv_dtype new_dtype,
+                             void *k_cache, void *v_cache, const sv_kv_layout *layout,
+                             const int32_t *block_table, int max_blocks_per_seq,
+                             const int32_t *seq_lens, int B, int n_new, int H_kv, int d_head,
+                             int block_size, int num_blocks, int32_t *dev_status,
+                             sv_stream_t stream);
+
+sv_status kv_block_gather_q8(const void *k_cache, const void *v_cache, const sv_kv_layout *layout,
+                             const int32_t *block_table, int max_blocks_per_seq,
+                             const int32_t *seq_lens, const int32_t *start, int B, int n_rows,
+                             int H_kv, int d_head, int block_size, int num_blocks,
+                             void *k_out, void *v_out, sv_dtype out_dtype,
+                             int32_t *dev_status, sv_stream_t stream);
+
+size_t spec_verify_attn_q8_workspace_size(int B, int n_new, int H_q, int H_kv, int d_head,
+                                          int max_blocks_per_seq, int block_size, int window,
+                                          int sinks);
+
+sv_status spec_verify_attn_q8(const void *q, sv_dtype q_dtype, const void *k_cache,
+                              const void *v_cache, const sv_kv_layout *layout,
+                              const int32_t *block_table, int max_blocks_per_seq,
+                              const int32_t *seq_lens, int B, int n_new, int H_q, int H_kv,
+                              int d_head, int block_size, int num_blocks, float softmax_scale,
+                              int window, int sinks, void *out, sv_dtype out_dtype,
+                              void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                              sv_stream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * Rotary positions ("KV Cache + Speculative Decoding", section 6.3, _rope;
+ * section 4.4, the decoupled RoPE part of MLA)
+ *
+ * sv_rope (host) describes the rotation: dims offset .. offset + rotary_dim -
+ * 1 of a row are rotary_dim / 2 pairs, dims i and i + rotary_dim / 2 of them
+ * (interleaved 0) or 2i and 2i + 1 (interleaved 1). Pair i of a row at
+ * position p turns by p * inv_freq[i] radians, times scale:
+ *   (a, b) -> scale * (a cos - b sin, b cos + a sin).
+ *   sv_rope_init fills inv_freq[i] = theta^(-2i / rotary_dim), offset 0, half
+ *   layout, scale 1; every field may be changed afterwards. Then at most one
+ *   way to stretch the context:
+ *   sv_rope_scale_linear  every inv_freq divided by factor;
+ *   sv_rope_scale_llama3  with t = original_length * inv_freq / 2 pi turns
+ *     over the original context and s = (t - low_freq_factor) /
+ *     (high_freq_factor - low_freq_factor) kept within 0..1, inv_freq becomes
+ *     inv_freq * s + inv_freq / factor * (1 - s);
+ *   sv_rope_scale_yarn    with ramp = (i - lo) / (hi - lo) kept within 0..1,
+ *     lo and hi the pairs (rounded down and up, within 0..rotary_dim - 1) that
+ *     make beta_fast and beta_slow turns over original_length, inv_freq
+ *     becomes inv_freq / factor * ramp + inv_freq * (1 - ramp); scale is
+ *     multiplied by attention_factor, or, where that is 0, by 0.1 ln(factor)
+ *     + 1 (1 for factor <= 1).
+ *
+ * spec_rope
+ *   q_out[b][j][h] = q[b][j][h] and k_out[b][j][g] = k[b][j][g] rotated, rows
+ *   of d elements, of dtype (SV_F32, SV_BF16 or SV_F16; computed in f32 and
+ *   rounded once); dims outside the rotated ones are copied. q_out may be q,
+ *   and k_out may be k (in place; otherwise they must not overlap). H_q or
+ *   H_kv may be 0 (its pointers are then not read): latent queries
+ *   [B][n_new][H][576] and latent rows [B][n_new][1][576] rotate with offset
+ *   512. Positions: positions[b][j] (device int32 [B][n_new], any value: the
+ *   depth of a tree's node, say; a negative one turns back), or, where that
+ *   is NULL, seq_lens[b] - n_new + j, the positions the append writes
+ *   (seq_lens[b] < n_new sets SV_DEV_BAD_SEQ_LEN and leaves that sequence's
+ *   rows unwritten).
+ *   The rows of each tensor are packed [B][n_new][heads][d], or lie at the
+ *   strides (elements, not negative) of its sv_rope_rows, e.g. heads of a
+ *   packed projection. The angle is exact to 2^-31 turns at every 32-bit
+ *   position. rope is read before the call returns (a captured call keeps
+ *   it). rotary_dim <= SV_ROPE_MAX_DIM.
+ * ------------------------------------------------------------------------ */
+#define SV_ROPE_MAX_DIM 256
+
+typedef struct {
+  int rotary_dim, offset, interleaved;
+  float scale;
+  double inv_freq[SV_ROPE_MAX_DIM / 2];
+} sv_rope;
+
+/* Where the rows of a tensor lie: element (b, j, h, 0) is at
+ * b * seq_stride + j * row_stride + h * head_stride. */
+typedef struct {
+  int64_t seq_stride;
+  int64_t row_stride;
+  int64_t head_stride;
+} sv_rope_rows;
+
+sv_status sv_rope_init(sv_rope *rope, int rotary_dim, double theta);
+sv_status sv_rope_scale_linear(sv_rope *rope, double factor);
+sv_status sv_rope_scale_llama3(sv_rope *rope, double factor, double low_freq_factor,
+                               double high_freq_factor, double original_length);
+sv_status sv_rope_scale_yarn(sv_rope *rope, double theta, double factor, double beta_fast,
+                             double beta_slow, double original_length, double attention_factor);
+
+sv_status spec_rope(const void *q, void *q_out, const void *k, void *k_out, sv_dtype dtype,
+                    const sv_rope_rows *q_rows, const sv_rope_rows *q_out_rows,
+                    const sv_rope_rows *k_rows, const sv_rope_rows *k_out_rows,
+                    const sv_rope *rope, const int32_t *positions, const int32_t *seq_lens,
+                    int B, int n_new, int H_q, int H_kv, int d, int32_t *dev_status,
+                    sv_stream_t stream);
+
+/* ------------------------------------------------------------------------ *
  * spec_verify_sample
  *   p_i = softmax(target_logits[b][i][:] / T), i = 0..K (row K is p_{K+1}).
  *   q_i = softmax(draft[b][i][:] / T) (draft_is_probs == 0, draft logits of

@@ -19,10 +19,13 @@ a page or a stated reading fixes another precision:
   fp8.py        OCP FP8 E4M3 encode/decode (used for the fp8 KV pools)
   q4.py         the 4-bit pages: quantisation, record layout, append, dense
                 read-back
+  q8.py         the 8-bit block-scaled pages: quantisation, append, dense
+                read-back
+  rope.py       rotary positions and the frequencies of stretched contexts
   theory.py     closed forms: alpha, residual mass, E[tau], speedup, KV bytes
 
 Parity status: every function here is pinned by a -m "not gpu" test against
 something other than itself (exact enumeration, closed forms, library
 routines on special cases, Monte-Carlo laws, invariances). None is unpinned.
 """
-from . import attention, fp8, kv_append, q4, sampling, theory  # noqa: F401
+from . import attention, fp8, kv_append, q4, q8, rope, sampling, theory  # noqa: F401

@@ -14,6 +14,9 @@ Entry points (names follow the C ABI in include/specverify.h):
   alloc_q4_pools, kv_block_append_q4, kv_block_gather_q4, spec_verify_attn_q4
                       a 4-bit paged cache: its pools, its append, its read-back
                       and the verify attention over it (window and sinks too)
+  alloc_q8_pools, q8_views, kv_block_append_q8, kv_block_gather_q8, spec_verify_attn_q8
+                      the same for an 8-bit cache with a scale per block and kv head
+  Rope, spec_rope     rotary positions of the new queries and keys
   spec_verify_sample  fused rejection sampling (accept / residual / bonus)
   verify_step         the three in stream order (one verify round of one layer)
   tree_verify_step    the same for a draft tree, with the commit of the accepted path
@@ -65,6 +68,18 @@ class _Layout(ctypes.Structure):
                 ("slot_stride", ctypes.c_int64)]
 
 
+ROPE_MAX_DIM = 256
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("offset", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("scale", ctypes.c_float), ("inv_freq", ctypes.c_double * (ROPE_MAX_DIM // 2))]
+
+
+class _RopeRows(ctypes.Structure):
+    _fields_ = [("seq_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 def load_library(path: str = LIB_PATH):
     """Load (not build) the shared library and declare its signatures."""
     global _lib
@@ -107,6 +122,24 @@ def load_library(path: str = LIB_PATH):
     lib.spec_verify_attn_q4_workspace_size.argtypes = [I] * 9
     lib.spec_verify_attn_q4.restype = I
     lib.spec_verify_attn_q4.argtypes = [P, I, P, P, LP, P, I, P, I, I, I, I, I, I, I, F, I, I, P, I, P, Z, P, P]
+    lib.sv_q8_page_bytes.restype = Z
+    lib.sv_q8_page_bytes.argtypes = [I, I, I]
+    for name in ("kv_block_append", "kv_block_gather", "spec_verify_attn"):   # the 4-bit calls' arguments
+        f8, f4 = getattr(lib, name + "_q8"), getattr(lib, name + "_q4")
+        f8.restype, f8.argtypes = f4.restype, f4.argtypes
+    lib.spec_verify_attn_q8_workspace_size.restype = Z
+    lib.spec_verify_attn_q8_workspace_size.argtypes = [I] * 9
+    D, RP, RR = ctypes.c_double, ctypes.POINTER(_Rope), ctypes.POINTER(_RopeRows)
+    lib.sv_rope_init.restype = I
+    lib.sv_rope_init.argtypes = [RP, I, D]
+    lib.sv_rope_scale_linear.restype = I
+    lib.sv_rope_scale_linear.argtypes = [RP, D]
+    lib.sv_rope_scale_llama3.restype = I
+    lib.sv_rope_scale_llama3.argtypes = [RP, D, D, D, D]
+    lib.sv_rope_scale_yarn.restype = I
+    lib.sv_rope_scale_yarn.argtypes = [RP, D, D, D, D, D, D]
+    lib.spec_rope.restype = I
+    lib.spec_rope.argtypes = [P, P, P, P, I, RR, RR, RR, RR, RP, P, P, I, I, I, I, I, P, P]
     lib.spec_verify_attn_tree_workspace_size.restype = Z
     lib.spec_verify_attn_tree_workspace_size.argtypes = [I, I, I, I, I, I, I]
     lib.spec_verify_attn_tree.restype = I
@@ -243,6 +276,20 @@ def _not_q4(what, row, *pools):
                              % (what, tuple(p.shape)))
 
 
+def _is_q8(k_cache):
+    """8-bit block-scaled pools are uint8 [num_blocks, page]; fp8 pools have four dimensions."""
+    return k_cache.dtype == torch.uint8 and k_cache.dim() == 2
+
+
+def _not_q8(what, block, *pools):
+    """Refuses 8-bit block-scaled pools where pools of whole elements are read, but for flat pools of e4m3 codes,
+    `block` of them a block (-1: those too)."""
+    for p in pools:
+        if _is_q8(p) and p.shape[1] != block:
+            raise ValueError("%s does not take 8-bit block-scaled pools; e4m3 pools are [num_blocks, H_kv, block_size, "
+                             "d], got %s" % (what, tuple(p.shape)))
+
+
 def _layout_arg(layout):
     if layout is None:
         return None
@@ -257,6 +304,7 @@ def kv_block_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_sca
     _int32(block_table=block_table, seq_lens=seq_lens)
     if layout is None:
         _not_q4("kv_block_append", block_size * k_new.shape[-1], k_cache, v_cache)
+        _not_q8("kv_block_append", block_size * k_new.shape[-1] * k_new.shape[-2], k_cache, v_cache)
     lib = load_library()
     _cuda(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, status)
     B, n_new, H_kv, d = k_new.shape
@@ -275,6 +323,7 @@ def kv_tree_commit(k_cache, v_cache, block_table, seq_lens, path_nodes, num_acce
     _int32(block_table=block_table, seq_lens=seq_lens, path_nodes=path_nodes, num_accepted=num_accepted)
     if layout is None:
         _not_q4("kv_tree_commit", -1, k_cache, v_cache)
+        _not_q8("kv_tree_commit", -1, k_cache, v_cache)
     lib = load_library()
     _cuda(k_cache, v_cache, block_table, seq_lens, path_nodes, num_accepted, status)
     B, n_new = path_nodes.shape
@@ -317,6 +366,7 @@ def spec_verify_attn(q, k_cache, v_cache, block_table, seq_lens, softmax_scale=N
     _int32(block_table=block_table, seq_lens=seq_lens, tree_parent=tree_parent)
     if layout is None:
         _not_q4("spec_verify_attn", block_size * q.shape[-1], k_cache, v_cache)
+        _not_q8("spec_verify_attn", -1, k_cache, v_cache)
     lib = load_library()
     _cuda(q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out, workspace, status,
           tree_parent)
@@ -591,9 +641,268 @@ def spec_verify_attn_q4(q, k_cache, v_cache, block_table, seq_lens, softmax_scal
     return out
 
 
+# ------------------------------------------ 8-bit block-scaled pools ---
+
+@functools.lru_cache(maxsize=256)
+def q8_page_bytes(H_kv, d_head, block_size=16):
+    """Bytes of a block of an 8-bit block-scaled pool: its codes and a scale per kv head, padded to a multiple of 128."""
+    n = int(load_library().sv_q8_page_bytes(int(H_kv), int(d_head), int(block_size)))
+    if n == 0:
+        raise ValueError("8-bit pools take d_head a multiple of 16 up to 256 and block_size up to 64, got d_head %d, "
+                         "block_size %d, H_kv %d" % (d_head, block_size, H_kv))
+    return n
+
+
+def alloc_q8_pools(num_blocks, H_kv, d_head, block_size=16, device="cuda"):
+    """A zeroed pair (k_cache, v_cache) of 8-bit block-scaled pools, uint8 [num_blocks, page]."""
+    shape = (int(num_blocks), q8_page_bytes(H_kv, d_head, block_size))
+    return tuple(torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2))
+
+
+def q8_views(pool, H_kv, d_head, block_size=16):
+    """(codes, scales) of an 8-bit block-scaled pool as views: float8_e4m3fn [num_blocks, H_kv, block_size, d_head]
+    and float32 [num_blocks, H_kv]; a value is code * scale."""
+    _q8_pools("q8_views", pool, pool, d_head, block_size, None, None, H_kv)
+    at = H_kv * block_size * d_head
+    codes = pool[:, :at].unflatten(1, (H_kv, block_size, d_head)).view(torch.float8_e4m3fn)
+    return codes, pool[:, at:at + 4 * H_kv].view(torch.float32)
+
+
+def _q8_pools(what, k_cache, v_cache, d, block_size, layout, num_blocks, H_kv):
+    """num_blocks of a pair of 8-bit block-scaled pools, after checking that the pages the call reads lie within them."""
+    page = q8_page_bytes(H_kv, d, block_size)
+    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8:
+        raise ValueError("%s: 8-bit block-scaled pools are uint8" % what)
+    if layout is None:
+        if k_cache.dim() != 2 or k_cache.shape != v_cache.shape or k_cache.shape[1] != page:
+            raise ValueError("%s: 8-bit block-scaled pools must be [num_blocks, %d] (H_kv %d, d_head %d, block_size %d), "
+                             "got %s and %s" % (what, page, H_kv, d, block_size, tuple(k_cache.shape), tuple(v_cache.shape)))
+        return k_cache.shape[0]
+    if num_blocks is None:
+        raise ValueError("with an explicit layout pass num_blocks")
+    end = (num_blocks - 1) * layout[0] + page
+    if end > k_cache.numel() or end > v_cache.numel():
+        raise ValueError("%s: the layout reaches byte %d of pools of %d and %d bytes"
+                         % (what, end, k_cache.numel(), v_cache.numel()))
+    return num_blocks
+
+
+def _q8_heads(what, k_cache, d, block_size, layout):
+    """H_kv of a pool [num_blocks, page], where the page's padding is smaller than a head."""
+    if layout is not None or block_size * d + 4 < 128:
+        raise ValueError("%s: with an explicit layout, or heads of less than 128 bytes a block, pass H_kv" % what)
+    return max(1, k_cache.shape[-1] // (block_size * d + 4))
+
+
+def kv_block_append_q8(k_new, v_new, k_cache, v_cache, block_table, seq_lens, block_size=16, layout=None,
+                       num_blocks=None, status=None):
+    """Quantise k_new/v_new [B, n_new, H_kv, d] (f32 or bf16) into the 8-bit block-scaled pools at positions
+    seq_lens - n_new .. seq_lens - 1. Pools uint8 [num_blocks, q8_page_bytes(H_kv, d, bs)], or, with
+    `layout` = (page stride in bytes, 0, 0), flat views plus num_blocks."""
+    what = "kv_block_append_q8"
+    if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        _int32(block_table=block_table, seq_lens=seq_lens)
+    if k_new.dim() != 4 or k_new.shape != v_new.shape or k_new.dtype != v_new.dtype:
+        raise ValueError("%s: k_new and v_new must both be [B, n_new, H_kv, d] of one dtype" % what)
+    B, n_new, H_kv, d = k_new.shape
+    nb = _q8_pools(what, k_cache, v_cache, d, block_size, layout, num_blocks, H_kv)
+    _check_batch(what, B, block_table, seq_lens)
+    _check_status(what, status)
+    _ready(what, k_new, v_new, k_cache, v_cache, block_table, seq_lens, status)
+    _check(load_library().kv_block_append_q8(_ptr(k_new), _ptr(v_new), _dtype_code(k_new), _ptr(k_cache),
+                                             _ptr(v_cache), _layout_arg(layout), _ptr(block_table),
+                                             block_table.shape[1], _ptr(seq_lens), B, n_new, H_kv, d, block_size,
+                                             nb, _ptr(status), _stream()))
+
+
+def kv_block_gather_q8(k_cache, v_cache, block_table, seq_lens, start, n_rows, d_head, block_size=16, layout=None,
+                       num_blocks=None, H_kv=None, k_out=None, v_out=None, out_dtype=torch.bfloat16, status=None):
+    """Read cached rows of 8-bit block-scaled pools back: (k, v), each [B, n_rows, H_kv, d_head], row i of sequence b
+    the values of position start[b] + i (zeros outside [0, seq_lens[b])). start: int32 [B]."""
+    what = "kv_block_gather_q8"
+    _int32(block_table=block_table, seq_lens=seq_lens, start=start)
+    if H_kv is None:
+        H_kv = _q8_heads(what, k_cache, d_head, block_size, layout)
+    nb = _q8_pools(what, k_cache, v_cache, d_head, block_size, layout, num_blocks, H_kv)
+    B = start.shape[0] if start.dim() == 1 else -1
+    _check_batch(what, B, block_table, seq_lens, start=start)
+    if n_rows < 0:
+        raise ValueError("%s: n_rows must be >= 0" % what)
+    shape = (B, int(n_rows), int(H_kv), int(d_head))
+    if k_out is not None:
+        out_dtype = k_out.dtype
+    _check_like(what, "k_out", k_out, shape, out_dtype)
+    _check_like(what, "v_out", v_out, shape, out_dtype)
+    _check_status(what, status)
+    _ready(what, k_cache, v_cache, block_table, seq_lens, start, k_out, v_out, status)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
+    if k_out.numel():
+        _check(load_library().kv_block_gather_q8(_ptr(k_cache), _ptr(v_cache), _layout_arg(layout), _ptr(block_table),
+                                                 block_table.shape[1], _ptr(seq_lens), _ptr(start), B, int(n_rows),
+                                                 int(H_kv), int(d_head), block_size, nb, _ptr(k_out), _ptr(v_out),
+                                                 _dtype_code(k_out), _ptr(status), _stream()))
+    return k_out, v_out
+
+
+@functools.lru_cache(maxsize=1024)
+def attn_q8_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size=16, window=0, sinks=0):
+    return load_library().spec_verify_attn_q8_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq,
+                                                             block_size, *_span(window, sinks))
+
+
+def spec_verify_attn_q8(q, k_cache, v_cache, block_table, seq_lens, softmax_scale=None, window=0, sinks=0,
+                        block_size=16, out=None, workspace=None, status=None, layout=None, num_blocks=None,
+                        H_kv=None):
+    """Paged GQA verify attention over 8-bit block-scaled pools (kv_block_append_q8), q [B, n_new, H_q, d] bf16 or
+    f32; with window > 0 the query at position p sees key t <= p iff t > p - window or t < sinks."""
+    what = "spec_verify_attn_q8"
+    window, sinks = _span(window, sinks)
+    if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        _int32(block_table=block_table, seq_lens=seq_lens)
+    _attn_outputs(what, q, block_table, seq_lens, out, status)
+    B, n_new, H_q, d = q.shape
+    if H_kv is None:
+        H_kv = _q8_heads(what, k_cache, d, block_size, layout)
+    nb = _q8_pools(what, k_cache, v_cache, d, block_size, layout, num_blocks, H_kv)
+    _ready(what, q, k_cache, v_cache, block_table, seq_lens, out, workspace, status)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    max_blocks = block_table.shape[1]
+    if workspace is None:
+        workspace = alloc_workspace(attn_q8_workspace_size(B, n_new, H_q, H_kv, d, max_blocks, block_size,
+                                                           window, sinks), q.device)
+    _check(load_library().spec_verify_attn_q8(
+        _ptr(q), _dtype_code(q), _ptr(k_cache), _ptr(v_cache), _layout_arg(layout), _ptr(block_table), max_blocks,
+        _ptr(seq_lens), B, n_new, H_q, H_kv, d, block_size, nb, float(softmax_scale), window, sinks,
+        _ptr(out), _dtype_code(out), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+        _stream()))
+    return out
+
+
+# ------------------------------------------------------ rotary positions ---
+
+class Rope:
+    """How rows turn with their position (sv_rope): dims offset .. offset + rotary_dim - 1 are pairs, dims i and
+    i + rotary_dim / 2 of them, or 2i and 2i + 1 (interleaved); pair i turns by position * inv_freq[i], times scale.
+
+    inv_freq: theta^(-2i / rotary_dim), or the list given. scaling: None, or how the context is stretched:
+      {"kind": "linear", "factor"}
+      {"kind": "llama3", "factor", "low_freq_factor", "high_freq_factor", "original_length"}
+      {"kind": "yarn", "factor", "original_length", optional "beta_fast" (32), "beta_slow" (1), "attention_factor"}
+    """
+
+    _SCALINGS = {"linear": ({"factor"}, {}),
+                 "llama3": ({"factor", "low_freq_factor", "high_freq_factor", "original_length"}, {}),
+                 "yarn": ({"factor", "original_length"}, {"beta_fast": 32.0, "beta_slow": 1.0, "attention_factor": None})}
+
+    def __init__(self, rotary_dim, theta=10000.0, interleaved=False, offset=0, scaling=None, inv_freq=None, scale=1.0):
+        lib = load_library()
+        self._c = _Rope()
+        self._ref = ctypes.byref(self._c)
+        _check(lib.sv_rope_init(self._ref, int(rotary_dim), float(theta)))
+        if inv_freq is not None:
+            w = [float(x) for x in inv_freq]
+            if len(w) != rotary_dim // 2 or not all(math.isfinite(x) for x in w):
+                raise ValueError("Rope: inv_freq must be %d finite numbers" % (rotary_dim // 2))
+            self._c.inv_freq[:len(w)] = w
+        if offset < 0:
+            raise ValueError("Rope: offset must be >= 0")
+        if not math.isfinite(scale):
+            raise ValueError("Rope: scale must be finite")
+        self._c.offset, self._c.interleaved, self._c.scale = int(offset), int(bool(interleaved)), float(scale)
+        if scaling:
+            s = dict(scaling)
+            kind = s.pop("kind", None)
+            if kind not in self._SCALINGS:
+                raise ValueError("Rope: scaling kinds are %s, got %r" % (", ".join(sorted(self._SCALINGS)), kind))
+            needed, optional = self._SCALINGS[kind]
+            if not needed <= set(s) <= needed | set(optional):
+                raise ValueError("Rope: %s scaling takes %s, got %s"
+                                 % (kind, ", ".join(sorted(needed | set(optional))), ", ".join(sorted(s))))
+            s = {**optional, **s}
+            if kind == "linear":
+                _check(lib.sv_rope_scale_linear(self._ref, float(s["factor"])))
+            elif kind == "llama3":
+                _check(lib.sv_rope_scale_llama3(self._ref, float(s["factor"]), float(s["low_freq_factor"]),
+                                                float(s["high_freq_factor"]), float(s["original_length"])))
+            else:
+                if s["attention_factor"] is not None and not s["attention_factor"] > 0:
+                    raise ValueError("Rope: attention_factor must be > 0")
+                _check(lib.sv_rope_scale_yarn(self._ref, float(theta), float(s["factor"]), float(s["beta_fast"]),
+                                              float(s["beta_slow"]), float(s["original_length"]),
+                                              float(s["attention_factor"] or 0.0)))
+
+    rotary_dim = property(lambda self: self._c.rotary_dim)
+    offset = property(lambda self: self._c.offset)
+    interleaved = property(lambda self: bool(self._c.interleaved))
+    scale = property(lambda self: self._c.scale)
+    inv_freq = property(lambda self: list(self._c.inv_freq[:self._c.rotary_dim // 2]))
+
+
+def _rope_rows(what, name, t):
+    """The strides of rows [B, n_new, heads, d] whose elements lie side by side; None if packed."""
+    if t is None or t.is_contiguous():
+        return None
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError("%s: the elements of a row of %s must lie side by side" % (what, name))
+    return ctypes.byref(_RopeRows(*t.stride()[:3]))
+
+
+def spec_rope(q, k, rope, seq_lens=None, positions=None, q_out=None, k_out=None, status=None):
+    """Rotate the new queries q [B, n_new, H_q, d] and keys k [B, n_new, H_kv, d] (one of them may be None) of a verify
+    round: (q_out, k_out), f32, bf16 or f16. Rows may be strided (heads of a packed projection). q_out may be q and k_out
+    may be k; other overlaps are not allowed. Positions: seq_lens - n_new + j (those the append writes), or
+    positions [B, n_new] (the nodes of a tree)."""
+    what = "spec_rope"
+    if not isinstance(rope, Rope):
+        raise TypeError("%s: rope must be a Rope" % what)
+    if seq_lens is None and positions is None:
+        raise ValueError("%s: seq_lens or positions is needed" % what)
+    _int32(seq_lens=seq_lens, positions=positions)
+    x = q if q is not None else k
+    if x is None or any(t is not None and (t.dim() != 4 or t.shape[:2] != x.shape[:2] or t.shape[3] != x.shape[3] or
+                                           t.dtype != x.dtype) for t in (q, k)):
+        raise ValueError("%s: q and k must be [B, n_new, heads, d] of one dtype" % what)
+    if x.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        raise ValueError("%s: rows must be f32, bf16 or f16, not %s" % (what, x.dtype))
+    B, n_new, _, d = x.shape
+    if seq_lens is not None:
+        _check_like(what, "seq_lens", seq_lens, (B,), torch.int32)
+    if positions is not None:
+        _check_like(what, "positions", positions, (B, n_new), torch.int32)
+    _check_status(what, status)
+    for name, t, out in (("q_out", q, q_out), ("k_out", k, k_out)):
+        if t is None and out is not None:
+            raise ValueError("%s: %s without its rows" % (what, name))
+        if out is not None:
+            _check_like(what, name, out, t.shape, t.dtype)
+    _cuda(seq_lens, positions, status)
+    if not x.is_cuda:
+        raise ValueError("tensor arguments must live on a CUDA device")
+    _on_current_device(what, x, q, k, q_out, k_out, seq_lens, positions, status)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    if x.numel():
+        _check(load_library().spec_rope(
+            _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), _dtype_code(x), _rope_rows(what, "q", q),
+            _rope_rows(what, "q_out", q_out), _rope_rows(what, "k", k), _rope_rows(what, "k_out", k_out), rope._ref,
+            _ptr(positions), _ptr(seq_lens), B, n_new, 0 if q is None else q.shape[2], 0 if k is None else k.shape[2], d,
+            _ptr(status), _stream()))
+    return q_out, k_out
+
+
 def _append_any(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, block_size, status):
     """The append that the pools call for."""
-    if _is_q4(k_cache):
+    if _is_q8(k_cache):
+        kv_block_append_q8(k_new, v_new, k_cache, v_cache, block_table, seq_lens, block_size=block_size, status=status)
+    elif _is_q4(k_cache):
         kv_block_append_q4(k_new, v_new, k_cache, v_cache, block_table, seq_lens, block_size=block_size, status=status)
     else:
         kv_block_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale,
@@ -603,9 +912,10 @@ def _append_any(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_scale, 
 def _attn_any(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, k_scale, v_scale, window, sinks, block_size,
               out, workspace, status):
     """The verify attention that the pools and the window call for."""
-    if _is_q4(k_cache):
-        return spec_verify_attn_q4(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, window, sinks,
-                                   block_size=block_size, out=out, workspace=workspace, status=status)
+    if _is_q8(k_cache) or _is_q4(k_cache):
+        attn = spec_verify_attn_q8 if _is_q8(k_cache) else spec_verify_attn_q4
+        return attn(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, window, sinks, block_size=block_size,
+                    out=out, workspace=workspace, status=status)
     if window:
         return spec_verify_attn_window(q, k_cache, v_cache, block_table, seq_lens, window, sinks, softmax_scale,
                                        k_scale, v_scale, block_size=block_size, out=out, workspace=workspace,
@@ -792,15 +1102,19 @@ def spec_verify_sample_tree(target_logits, draft, tree_parent, tree_tokens, unif
 def verify_step(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, target_logits, draft,
                 draft_tokens, uniforms, k_scale=None, v_scale=None, draft_is_probs=False,
                 temperature=1.0, softmax_scale=None, attn_out=None, attn_workspace=None,
-                sample_workspace=None, status=None, window=0, sinks=0):
+                sample_workspace=None, status=None, window=0, sinks=0, rope=None):
     """One verify round of one layer: append the K+1 new K/V rows, attend, sample.
 
-    The pools may be 4-bit ones (alloc_q4_pools); window > 0 attends through a
-    sliding window with sinks (spec_verify_attn_window).
+    The pools may be 4-bit or 8-bit block-scaled ones (alloc_q4_pools,
+    alloc_q8_pools); window > 0 attends through a sliding window with sinks
+    (spec_verify_attn_window). With a rope, q and k_new come without positions
+    and are rotated first (spec_rope, out of place).
 
     Returns (attn_out, out_tokens, num_accepted). Rolling the cache back is the
     caller's job: next round's length is seq_lens - (K+1) + num_accepted + 1.
     """
+    if rope is not None:
+        q, k_new = spec_rope(q, k_new, rope, seq_lens=seq_lens, status=status)
     _append_any(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, 16, status)
     out = _attn_any(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, k_scale, v_scale, window, sinks, 16,
                     attn_out, attn_workspace, status)
@@ -945,13 +1259,19 @@ def copy_blocks(pools, pairs, num_blocks, block_bytes=None, block_stride_bytes=N
 
 def tree_verify_step(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, tree_parent, target_logits,
                      draft, tree_tokens, uniforms, k_scale=None, v_scale=None, draft_is_probs=False,
-                     temperature=1.0, softmax_scale=None, typical=None, status=None):
+                     temperature=1.0, softmax_scale=None, typical=None, status=None, rope=None, positions=None):
     """One tree-verify round of one layer, in stream order: append the n node rows,
     tree attention, tree sampling, then move each accepted path next to its root
     (kv_tree_commit). Returns (attn_out, out_tokens, num_accepted, path_nodes); the
     next round's length is seq_lens - n + num_accepted + 1 (BlockManager.commit_verify).
-    Pools of f32, bf16 or e4m3: a tree's rows cannot be moved inside 4-bit blocks."""
+    Pools of f32, bf16 or e4m3: a tree's rows cannot be moved between 4-bit or block-scaled blocks. With a rope, q and
+    k_new come without positions and are rotated first, to positions [B, n] (int32: the root's plus the node's depth)."""
     _not_q4("tree_verify_step", -1, k_cache, v_cache)
+    _not_q8("tree_verify_step", -1, k_cache, v_cache)
+    if rope is not None:
+        if positions is None:
+            raise ValueError("tree_verify_step: a rope needs the positions of the nodes")
+        q, k_new = spec_rope(q, k_new, rope, positions=positions, status=status)
     kv_block_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, status=status)
     out = spec_verify_attn(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, k_scale, v_scale,
                            status=status, tree_parent=tree_parent)
@@ -968,8 +1288,10 @@ class MultiLayerVerify:
     layers: list of dicts with device tensors q, k_new, v_new, k_cache, v_cache
     (and optionally k_scale, v_scale), all layers sharing block_table and
     seq_lens (one page table for the whole model, one pool pair per layer).
-    A layer's pools may be 4-bit ones (alloc_q4_pools), and a layer with
-    "window" (and "sinks") attends through a sliding window.
+    A layer's pools may be 4-bit or 8-bit block-scaled ones (alloc_q4_pools,
+    alloc_q8_pools), a layer with "window" (and "sinks") attends through a
+    sliding window, and one with "rope" (a Rope) rotates its q and k_new first,
+    into buffers of the round's own.
     Inputs and outputs stay in these static buffers, so the round can be
     captured once as a CUDA graph (capture()) and replayed (replay()); run()
     launches it directly. Attention outputs: self.outs[layer]; sampling:
@@ -985,15 +1307,20 @@ class MultiLayerVerify:
         self.draft_is_probs, self.temperature, self.block_size = draft_is_probs, temperature, block_size
         q0 = layers[0]["q"]
         B, n_new, H_q, d = q0.shape
-        H_kv = layers[0]["k_cache"].shape[1]
+        H_kv = layers[0]["k_new"].shape[2]
         dev = q0.device
         self.outs = [torch.empty_like(l["q"]) for l in layers]
         shape = (B, n_new, H_q, H_kv, d, block_table.shape[1], block_size)
         need = 0
         for l in layers:
             span = (l.get("window", 0), l.get("sinks", 0))
-            need = max(need, attn_q4_workspace_size(*shape, *span) if _is_q4(l["k_cache"])
+            need = max(need, attn_q8_workspace_size(*shape, *span) if _is_q8(l["k_cache"])
+                       else attn_q4_workspace_size(*shape, *span) if _is_q4(l["k_cache"])
                        else attn_window_workspace_size(*shape, *span) if span[0] else attn_workspace_size(*shape))
+        # (layers run one after the other: one pair of buffers serves all that rotate)
+        self.turned = None
+        if any(l.get("rope") is not None for l in layers):
+            self.turned = torch.empty_like(q0), torch.empty_like(layers[0]["k_new"])
         self.attn_ws = alloc_workspace(need, dev)
         Bs, K1, V = target_logits.shape
         self.samp_ws = alloc_workspace(sample_workspace_size(Bs, K1 - 1, V), dev)
@@ -1004,9 +1331,13 @@ class MultiLayerVerify:
 
     def run(self):
         for l, out in zip(self.layers, self.outs):
-            _append_any(l["k_new"], l["v_new"], l["k_cache"], l["v_cache"], self.block_table, self.seq_lens,
+            q, k_new = l["q"], l["k_new"]
+            if l.get("rope") is not None:
+                q, k_new = spec_rope(q, k_new, l["rope"], seq_lens=self.seq_lens, q_out=self.turned[0],
+                                     k_out=self.turned[1], status=self.status)
+            _append_any(k_new, l["v_new"], l["k_cache"], l["v_cache"], self.block_table, self.seq_lens,
                         l.get("k_scale"), l.get("v_scale"), self.block_size, self.status)
-            _attn_any(l["q"], l["k_cache"], l["v_cache"], self.block_table, self.seq_lens, None, l.get("k_scale"),
+            _attn_any(q, l["k_cache"], l["v_cache"], self.block_table, self.seq_lens, None, l.get("k_scale"),
                       l.get("v_scale"), l.get("window", 0), l.get("sinks", 0), self.block_size, out, self.attn_ws,
                       self.status)
         spec_verify_sample(self.target_logits, self.draft, self.draft_tokens, self.uniforms, self.draft_is_probs,

@@ -39,7 +39,7 @@
 #include <mutex>
 #include <type_traits>
 
-#include "q4.cuh"
+#include "q8.cuh"
 #include "tc5.cuh"
 
 namespace sv {
@@ -1588,13 +1588,15 @@ struct GenParams {
   const uint64_t *anc;    // [B][n_new] ancestor masks of a draft tree (NULL: a chain)
   int32_t *status;
   int B, n_new, H_q, H_kv, G, R, d, bs, max_blocks, num_blocks, bps, S;
-  int64_t block_stride, head_stride, slot_stride;   // elements; 4-bit pools: bytes of the records
+  int64_t block_stride, head_stride, slot_stride;   // elements; 4-bit and 8-bit block-scaled pools: bytes
   float scale_log2;
   int window, sinks;      // window 0: every key
 };
 
-// A 4-bit pool's element type (q4.cuh) in the kernels below.
+// A 4-bit pool's element type (q4.cuh) in the kernels below, and an 8-bit
+// block-scaled one's (q8.cuh).
 struct Q4 {};
+struct Q8 {};
 
 template <typename T>
 __device__ __forceinline__ float kv_value(const void *pool, int64_t off, float scale);
@@ -1677,6 +1679,13 @@ __global__ void __launch_bounds__(kGenThreads) attn_generic_kernel(const __grid_
           const int vc = (vr[q4_v_byte(slot, c, P.bs)] >> (4 * (slot & 1))) & 15;
           kv = fmaf((float)kc, __half2float(kp[0]), __half2float(kp[1]));
           vv = fmaf((float)vc, __half2float(vp[0]), __half2float(vp[1]));
+        } else if constexpr (std::is_same<TKV, Q8>::value) {
+          const uint8_t *kp = static_cast<const uint8_t *>(P.k_cache) + (int64_t)phys * P.block_stride;
+          const uint8_t *vp = static_cast<const uint8_t *>(P.v_cache) + (int64_t)phys * P.block_stride;
+          const int64_t off = (int64_t)g * P.head_stride + (int64_t)(t % P.bs) * P.slot_stride + c;
+          const int64_t so = q8_scale_offset(P.H_kv, d, P.bs) + 4 * g;
+          kv = kv_value<uint8_t>(kp, off, q8_scale(*reinterpret_cast<const float *>(kp + so)));
+          vv = kv_value<uint8_t>(vp, off, q8_scale(*reinterpret_cast<const float *>(vp + so)));
         } else {
           const int64_t off = (int64_t)phys * P.block_stride + (int64_t)g * P.head_stride +
                               (int64_t)(t % P.bs) * P.slot_stride + c;
@@ -2299,8 +2308,9 @@ sv_status launch_gen(const GenParams &P, cudaStream_t st) {
 
 using namespace sv;
 
-// The element types of the pools that the entry points here take (4-bit pools,
-// which attn_impl serves too, come through spec_verify_attn_q4 alone).
+// The element types of the pools that the entry points here take (4-bit and
+// 8-bit block-scaled pools, which attn_impl serves too, come through
+// spec_verify_attn_q4 and spec_verify_attn_q8 alone).
 static sv_status check_pool_type(const char *what, sv_dtype kv_dtype) {
   if (kv_dtype == SV_F32 || kv_dtype == SV_BF16 || kv_dtype == SV_FP8_E4M3) return SV_OK;
   return fail(SV_ERR_UNSUPPORTED, "%s: caches must be f32, bf16 or fp8 (kv_dtype %d)", what, (int)kv_dtype);
@@ -2324,8 +2334,8 @@ static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache,
   if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
     return fail(SV_ERR_INVALID_ARG, "spec_verify_attn: softmax_scale must be finite and > 0");
   if (q_dtype != out_dtype) return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: q and out dtypes must match");
-  if (kv_dtype == kQ4 && q_dtype != SV_F32 && q_dtype != SV_BF16)
-    return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn_q4: queries must be f32 or bf16");
+  if ((kv_dtype == kQ4 || kv_dtype == kQ8) && q_dtype != SV_F32 && q_dtype != SV_BF16)
+    return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn_q%d: queries must be f32 or bf16", kv_dtype == kQ4 ? 4 : 8);
   if (kv_dtype == SV_F32 && q_dtype != SV_F32)
     return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: fp32 caches take fp32 queries");
   if ((kv_dtype == SV_BF16 || kv_dtype == SV_FP8_E4M3) && q_dtype != SV_BF16)
@@ -2334,7 +2344,7 @@ static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache,
     return fail(SV_ERR_INVALID_ARG, "spec_verify_attn: fp8 caches need k_scale and v_scale");
   if (d_head > 256 || d_head % 4) return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: d_head must be a multiple of 4 and <= 256");
   if (B > 65535 || H_kv > 65535) return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: B or H_kv too large");
-  if (kv_dtype != kQ4 && layout && (layout->slot_stride < d_head || layout->head_stride < d_head || layout->block_stride < d_head))
+  if (kv_dtype != kQ4 && kv_dtype != kQ8 && layout && (layout->slot_stride < d_head || layout->head_stride < d_head || layout->block_stride < d_head))
     return fail(SV_ERR_INVALID_ARG, "spec_verify_attn: layout strides smaller than d_head");
   if (window < 0 || sinks < 0) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_window: negative window or sinks");
   if ((int64_t)window >= (int64_t)max_blocks_per_seq * block_size) window = sinks = 0;   // reaches every key
@@ -2365,6 +2375,12 @@ static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache,
     const sv_status qrc = q4_check("spec_verify_attn_q4", k_cache, v_cache, layout, H_kv, d_head, block_size,
                                    &block_stride, &head_stride);
     if (qrc != SV_OK) return qrc;
+  }
+  if (kv_dtype == kQ8) {
+    const sv_status qrc = q8_check("spec_verify_attn_q8", k_cache, v_cache, layout, H_kv, d_head, block_size, &block_stride);
+    if (qrc != SV_OK) return qrc;
+    slot_stride = d_head;
+    head_stride = (int64_t)block_size * d_head;
   }
   const float scale_log2 = (float)((double)softmax_scale * 1.4426950408889634074);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -2446,7 +2462,8 @@ static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache,
     P.block_stride = block_stride; P.head_stride = head_stride; P.slot_stride = slot_stride;
     P.scale_log2 = scale_log2;
     P.window = window; P.sinks = sinks;
-    if (kv_dtype == kQ4) rc = q_dtype == SV_F32 ? launch_gen<Q4, float>(P, st) : launch_gen<Q4, __nv_bfloat16>(P, st);
+    if (kv_dtype == kQ8) rc = q_dtype == SV_F32 ? launch_gen<Q8, float>(P, st) : launch_gen<Q8, __nv_bfloat16>(P, st);
+    else if (kv_dtype == kQ4) rc = q_dtype == SV_F32 ? launch_gen<Q4, float>(P, st) : launch_gen<Q4, __nv_bfloat16>(P, st);
     else if (kv_dtype == SV_F32) rc = launch_gen<float, float>(P, st);
     else if (kv_dtype == SV_BF16) rc = launch_gen<__nv_bfloat16, __nv_bfloat16>(P, st);
     else rc = launch_gen<uint8_t, __nv_bfloat16>(P, st);
@@ -2592,6 +2609,16 @@ sv_status attn_cuda_core_q4(const void *q, sv_dtype q_dtype, const void *k_cache
                             int num_blocks, float softmax_scale, int window, int sinks, void *out, sv_dtype out_dtype,
                             void *workspace, size_t workspace_bytes, int32_t *dev_status, sv_stream_t stream) {
   return attn_impl(q, q_dtype, k_cache, v_cache, kQ4, layout, nullptr, nullptr, block_table, max_blocks_per_seq,
+                   seq_lens, B, n_new, H_q, H_kv, d_head, block_size, num_blocks, softmax_scale, out, out_dtype,
+                   workspace, workspace_bytes, dev_status, 0, nullptr, window, sinks, stream);
+}
+
+sv_status attn_cuda_core_q8(const void *q, sv_dtype q_dtype, const void *k_cache, const void *v_cache,
+                            const sv_kv_layout *layout, const int32_t *block_table, int max_blocks_per_seq,
+                            const int32_t *seq_lens, int B, int n_new, int H_q, int H_kv, int d_head, int block_size,
+                            int num_blocks, float softmax_scale, int window, int sinks, void *out, sv_dtype out_dtype,
+                            void *workspace, size_t workspace_bytes, int32_t *dev_status, sv_stream_t stream) {
+  return attn_impl(q, q_dtype, k_cache, v_cache, kQ8, layout, nullptr, nullptr, block_table, max_blocks_per_seq,
                    seq_lens, B, n_new, H_q, H_kv, d_head, block_size, num_blocks, softmax_scale, out, out_dtype,
                    workspace, workspace_bytes, dev_status, 0, nullptr, window, sinks, stream);
 }
