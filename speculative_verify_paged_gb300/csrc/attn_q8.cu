@@ -1,15 +1,771 @@
 // spec_verify_attn_q8: paged GQA verify attention over an 8-bit block-scaled
-// cache (page layout: q8.cuh).
+// cache (page layout: q8.cuh), on the tensor cores for d_head 128, 16-token
+// blocks and bf16 queries.
+//
+// Mathematics. With K_t = s_t c_t and V_t = s'_t c'_t (c, c' e4m3 codes, one scale
+// per block), for query row r
+//   x_rt = scale s_t (q_r . c_t),
+//   p'_rt = s'_t 2^(x_rt - ref_r)            (log2 domain, ref_r a running reference)
+//   out_r = sum_t p'_rt c'_t / sum_t (p'_rt / s'_t)
+// so both products run on the codes as they lie in the pages, and the scales enter
+// per key.
+//
+// Operands. Codes go from the pages to shared memory by tensor copies (a block of
+// a kv head is 16 rows of 128 bytes) and from there to the tensor cores: nothing
+// is unpacked. Q K^T takes each query row as two e4m3 terms (hi + lo, kl_prep_kernel).
+// P V has e4m3 codes on one side, so the weights have to be 8-bit too, and e4m3
+// would not do: the sum over a long row needs the small weights as well. A weight
+// is rounded to f16 and cut into three e5m2 terms, which is a matter of bytes: the
+// upper byte of an f16 is an e5m2 number, what is left after taking it off is
+// exact in f16 again, and so on; the third is rounded. So weights keep 2^-10
+// relative (f16's 2^-11 first) down to 2^-6 (2^-16 of the largest), and an
+// absolute 2^-17 below: kind::f8f6f4 takes e4m3 and e5m2 side by side.
+// Keys on the lanes: S^T = C Q^T, O^T = C'^T P'^T (key_lanes.cuh). C is K-major as
+// it lies, C'^T is read across its rows (head dims contiguous), P' is written by
+// the key's thread as a row of its columns.
 #include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+#include <type_traits>
 
+#include "key_lanes.cuh"
 #include "q8.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kTile = kTK * kD;            // bytes of a tile of K or V
+constexpr int kWarps = 16;
+constexpr int kPageWarp = 8, kKWarp = 9, kVWarp = 10, kQkWarp = 11, kPvWarp = 12, kQWarp = 13;
+constexpr int kStatic = 9216;              // static shared memory, at most
+// Registers a thread: the softmax warps take what the others leave.
+constexpr int kRegs = 128, kRegsSoftmax = 192, kRegsOther = 64;
+static_assert(256 * kRegsSoftmax + 32 * (kWarps - 8) * kRegsOther <= 32 * kWarps * kRegs, "registers");
+// A row's reference puts its largest weight at 2^kTop and moves once one exceeds
+// 2^kMove (f16 ends at 65504, e5m2 at 57344).
+constexpr float kTop = 10.f, kMove = 15.f;
+
+template <int NC> struct Q8Cfg : KlCfg<NC> {
+  using KlCfg<NC>::kN;
+  using KlCfg<NC>::kQ;
+  using KlCfg<NC>::kT;
+  static constexpr int kRow = kN <= 32 ? 32 : 64;   // bytes of a key in a term of P'
+  static constexpr int kTerm = kTK * kRow, kPBytes = 3 * kTerm;
+  static constexpr int kFixed = 1024 + 2 * kQ + 2 * kT * kPBytes;
+  static constexpr int kAll = (227 * 1024 - kStatic - kFixed) / kTile;   // stages that fit
+  static constexpr int kVS = (kAll + 1) / 2 < 6 ? (kAll + 1) / 2 : 6, kKS = kAll - kVS < 5 ? kAll - kVS : 5;
+  static constexpr int kSmem = kFixed + (kKS + kVS) * kTile;
+  static constexpr uint32_t kSCol = 0, kOCol = 2 * kT * kN;   // (two O buffers)
+  static_assert(kOCol + 2 * kN <= 512, "TMEM columns");
+  static_assert(kKS >= 2 && kVS >= 2, "shared memory");
+};
+
+struct Q8Maps {
+  CUtensorMap k, v;   // {head dim, slot, kv head, block}, boxes of 128 x 16
+};
+
+template <int R> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// A shared-memory operand with rows of 64 or 32 bytes (swizzled within 64 or 32).
+__device__ __forceinline__ uint64_t t5_desc_row(uint32_t saddr, uint32_t sbo, bool row64) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)((sbo >> 4) & 0x3FFF) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)(row64 ? 4 : 6) << 61;
+  return d;
+}
+
+// Four weights (two f16 pairs) as three words of e5m2, largest part first
+__device__ __forceinline__ void cut_weights(uint32_t h0, uint32_t h1, uint32_t (&w)[3]) {
+  auto rest = [](uint32_t h) {   // minus its upper byte's value
+    const uint32_t u = h & 0xFF00FF00u;
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&u));
+    return *reinterpret_cast<const uint32_t *>(&r);
+  };
+  w[0] = __byte_perm(h0, h1, 0x7531);
+  h0 = rest(h0);
+  h1 = rest(h1);
+  w[1] = __byte_perm(h0, h1, 0x7531);
+  h0 = rest(h0) + 0x00800080u;   // (to nearest; far from carrying into the other half)
+  h1 = rest(h1) + 0x00800080u;
+  w[2] = __byte_perm(h0, h1, 0x7531);
+}
+
+// Warps 0-3 and 4-7: softmax (a key per thread and tile; each warpgroup half of
+// the query rows, or the first all of up to 8), later the epilogue (a head dim
+// per thread). 8: block numbers, flags and scales of the tiles ahead. 9, 10: copy
+// the K and V codes. 11: issues Q K^T, owns the 512 TMEM columns. 12: issues P V.
+// 13: Q of the next sequence.
+template <int NC>
+__global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_constant__ KlParams P, const __grid_constant__ Q8Maps M) {
+  using Cfg = Q8Cfg<NC>;
+  constexpr int N = Cfg::kN, CP = Cfg::kCols, T = Cfg::kT, KS = Cfg::kKS, VS = Cfg::kVS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t page_full[kChunks], page_empty[kChunks], scale_full[kChunks];
+  __shared__ int s_phys[kChunks * kChunk * kTP];   // blocks of the tiles ahead
+  __shared__ __align__(8) float2 s_scale[kChunks * kChunk * kTP];   // their scales of K and V
+  __shared__ int s_flag[kChunks * kChunk];   // kFirst, kLast, kEnd, kSecond, blocks of the tile << 8
+  // rows of V that no query sees: [z0, z1) and from z2 on, z0 | z1 << 8 | z2 << 16
+  __shared__ int s_zero[kChunks * kChunk];
+  __shared__ __align__(8) uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], q_empty[2], o_free[2], drain[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  __shared__ int4 s_work;
+  // per row of the items in flight: position (0 .. n_new - 1), row of q and out, its own power of two; per item the
+  // power of two that undoes Q's scaling (-1: the rows have their own)
+  __shared__ __align__(16) float s_qf[3][N];
+  __shared__ __align__(16) int s_pos[3][N];
+  __shared__ int s_row[3][N];
+  __shared__ float s_fold[3];
+  __shared__ __align__(16) int4 s_item[3];   // first tile, tiles, length in span coordinates, kWhole | kOpening
+  __shared__ __align__(16) float s_nb[N], s_a[N];   // minus the reference; the last factor of a rescale
+  __shared__ float s_max[8][NC], s_red[8][NC], s_fin[2][N];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int Hp = P.H_kv * P.RG;
+  const int range = blockIdx.x / Hp, gp = blockIdx.x % Hp;
+  const int g = gp / P.RG, row0 = (gp % P.RG) * P.Rg;
+  const int rows = min(P.Rg, P.R - row0);       // live rows of this CTA
+  const int live0 = kl_first(rows);             // of the first softmax warpgroup
+  const int softmax_warps = live0 < rows ? 8 : 4;
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t q_smem = smem_u32(smem);
+  const uint32_t k_ring = q_smem + 2 * Cfg::kQ, v_ring = k_ring + KS * kTile;
+  const uint32_t p_smem = v_ring + VS * kTile;
+
+  // Lengths and block numbers are the caller's: the ranges and the first block
+  // numbers are worked out while the kernel before this one runs.
+  if (warp == 0) {
+    bool bad;
+    int4 split;
+    const int64_t all = kl_all_tiles(P, bad);
+    const int4 w = kl_range(P, range, all, split);
+    if (lane == 0) s_work = w;
+  } else if (tid == 32) {
+    for (int k = 0; k < kChunks; ++k) {
+      mbar_init(&page_full[k], 1);
+      mbar_init(&scale_full[k], 1);
+      mbar_init(&page_empty[k], 4 + softmax_warps);   // the K, V and MMA warps, and those that read the scales
+    }
+    for (int k = 0; k < KS; ++k) {
+      mbar_init(&k_full[k], 1);
+      mbar_init(&k_empty[k], 1);
+    }
+    for (int k = 0; k < VS; ++k) {
+      mbar_init(&v_full[k], 1);
+      mbar_init(&v_empty[k], 1);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&drain[k], 1);
+      mbar_init(&q_full[k], 1);
+      mbar_init(&q_empty[k], 1);
+      mbar_init(&o_free[k], softmax_warps);
+      // Q K^T of the step (its commit, and the issuing lane itself, which has seen
+      // the scales), and P V of the step before the last
+      mbar_init(&s_full[k], 3);
+      mbar_init(&p_full[k], softmax_warps);
+      mbar_init(&pv_done[k], 1);
+    }
+    abort_flag = 0;
+    fence_mbarrier_init();
+  } else if (warp == kQkWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  t5_fence_before();
+  __syncthreads();
+  t5_fence_after();
+  const uint32_t tb = tmem_base;
+  const int4 work = s_work;
+  const int total = work.z;   // tiles of this CTA
+  volatile int *abf = &abort_flag;
+  // every stage, buffer and phase below follows the CTA's running tile count u
+
+  // Waits for the chunk that tile u opens; after a chunk's last tile a warp hands
+  // it back.
+  auto pages_wait = [&](uint32_t u, bool &ok) {
+    if (u % kChunk == 0) ok = kl_wait(&page_full[u / kChunk % kChunks], (u / (kChunk * kChunks)) & 1, abf, P.wait_ns) && ok;
+  };
+  auto pages_done = [&](uint32_t u) {
+    if (u % kChunk == kChunk - 1) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&page_empty[u / kChunk % kChunks]);
+    }
+  };
+
+  if (warp >= kPageWarp) regs_dec<kRegsOther>();
+  if (warp != kPageWarp) pdl_wait();
+  pdl_trigger();
+  if (warp == kPageWarp) {
+    // ------------------------------------------- block numbers and scales --
+    KlWalk wk = kl_walk(P, work);
+    KlItem it;
+    bool have = kl_next(P, wk, it);
+    int ti = 0;   // next tile of the item
+    bool bad = false;
+    const int64_t scales_at = q8_scale_offset(P.H_kv, kD, kBS) + 4 * g;
+    for (int c = 0; c * kChunk < total; ++c) {
+      if (c >= kChunks &&
+          !__all_sync(0xffffffffu, kl_wait(&page_empty[c % kChunks], ((c / kChunks) & 1) ^ 1, abf, P.wait_ns)))
+        break;
+      int filled = 0;
+      while (filled < kChunk && have) {
+        const int n = min(kChunk - filled, it.ntiles - ti);
+        const int32_t *table = P.block_table + (int64_t)it.b * P.max_blocks;
+        int phys[kChunk * kTP / 32];
+#pragma unroll
+        for (int k = 0; k < kChunk * kTP / 32; ++k) {
+          const int e = lane + 32 * k, v = (it.tile0 + ti) * kTP + e;
+          // (past the end: the last block once more)
+          const int vb = min(v, it.span.nblk - 1);
+          phys[k] = e < n * kTP ? table[vb < it.span.nsb ? vb : vb + it.span.skip] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kChunk * kTP / 32; ++k) {
+          const int e = lane + 32 * k;
+          if (e >= n * kTP) continue;
+          int ph = phys[k];
+          if (ph < 0 || ph >= P.num_blocks) {   // stay in bounds; the output of this sequence is flagged
+            bad = true;
+            ph = 0;
+          }
+          s_phys[(c % kChunks * kChunk + filled) * kTP + e] = ph;
+        }
+        if (lane < n) {
+          const int tt = ti + lane, at = c % kChunks * kChunk + filled + lane;
+          const int key0 = (it.tile0 + tt) * kTK, nv = min(kTP, it.span.nblk - (it.tile0 + tt) * kTP);
+          s_flag[at] = (tt == 0 ? kFirst : 0) | (tt == it.ntiles - 1 ? kLast | kEnd : 0) | (tt % T == T - 1 ? kEnd : 0) |
+                       (tt % T ? kSecond : 0) | nv << 8;
+          int z0 = 0, z1 = 0;
+          if (P.window > 0) {   // between the sinks and the oldest query's window
+            z0 = min(max(P.sinks - key0, 0), kTK);
+            z1 = min(max(it.span.L - P.n_new - P.window + 1 - key0, 0), kTK);
+            if (z0 >= z1) z0 = z1 = 0;
+          }
+          s_zero[at] = z0 | z1 << 8 | min(it.span.L - key0, kTK) << 16;
+        }
+        filled += n;
+        ti += n;
+        if (ti == it.ntiles) {
+          have = kl_next(P, wk, it);
+          ti = 0;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&page_full[c % kChunks]);
+      if (c == 0) pdl_wait();   // (the kernel before may write the pages)
+#pragma unroll
+      for (int k = 0; k < kChunk * kTP / 32; ++k) {
+        const int e = lane + 32 * k;
+        if (e >= filled * kTP) continue;
+        const int at = c % kChunks * kChunk * kTP + e;
+        const int64_t off = (int64_t)s_phys[at] * P.block_stride + scales_at;
+        s_scale[at] = make_float2(q8_scale(*reinterpret_cast<const float *>(P.k_cache + off)),
+                                  q8_scale(*reinterpret_cast<const float *>(P.v_cache + off)));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&scale_full[c % kChunks]);
+    }
+    pdl_wait();
+    if (bad) atomic_or_status(P.status, SV_DEV_BAD_BLOCK);
+  } else if (warp == kKWarp || warp == kVWarp) {
+    // ------------------------------------------------------ codes to smem --
+    auto role = [&](auto is_v) {
+      constexpr bool V = decltype(is_v)::value;
+      constexpr int S = V ? VS : KS;
+      uint64_t *full = V ? v_full : k_full, *empty = V ? v_empty : k_empty;
+      const uint32_t ring = V ? v_ring : k_ring;
+      const CUtensorMap *map = V ? &M.v : &M.k;
+      bool ok = true;
+      int u = 0, s = 0;
+      uint32_t phase = 1;   // of `empty`, from the second round of the ring on
+      const bool run = !(P.withhold & SV_TEST_WITHHOLD_COPIES);
+      for (; run && u < total; ++u) {
+        pages_wait(u, ok);
+        if (u >= S) ok = kl_wait(&empty[s], phase, abf, P.wait_ns) && ok;
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const int at = u % (kChunk * kChunks), nv = s_flag[at] >> 8;
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], nv * kBS * kD);
+        __syncwarp();
+        if (lane < nv) tma_load_4d(ring + s * kTile + lane * (kBS * kD), map, 0, 0, g, s_phys[at * kTP + lane], &full[s]);
+        pages_done(u);
+        if (++s == S) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+      // the copies in flight land before the CTA may exit
+      if (lane == 0)
+        for (int k = max(0, u - S); k < u; ++k)
+          if (!mbar_wait(&full[k % S], (k / S) & 1)) atomic_or_status(P.status, SV_DEV_TIMEOUT);
+    };
+    if (warp == kVWarp) role(std::true_type{});
+    else role(std::false_type{});
+  } else if (warp == kQWarp) {
+    // ------------------------------------------------------------------- Q --
+    KlWalk wk = kl_walk(P, work);
+    KlItem it;
+    int i = 0;
+    while (kl_next(P, wk, it)) {
+      const int buf = i & 1, row = i % 3;
+      // the buffer after Q K^T of the item before the last, the rows after the
+      // epilogue of the one before that
+      bool ok = i < 2 || kl_wait(&q_empty[buf], ((i >> 1) & 1) ^ 1, abf, P.wait_ns);
+      if (i >= 3) ok = kl_wait(&o_free[buf ^ 1], ((i - 3) >> 1) & 1, abf, P.wait_ns) && ok;
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int64_t ent = (int64_t)it.b * Hp + gp;
+      const float *qs = P.ws_qs + ent * (2 * N + 4);
+      const float fold = qs[N];
+      for (int col = lane; col < N; col += 32) {
+        const int w = col / CP, c = col - w * CP;
+        const int r = row0 + (c < (w ? rows - live0 : live0) ? w * live0 + c : 0);   // (padding: any)
+        const int j = r / P.G;
+        s_pos[row][col] = j;
+        s_row[row][col] = (it.b * P.n_new + j) * P.H_q + g * P.G + (r - j * P.G);
+      }
+      if (fold < 0.f)
+        for (int col = lane; col < N; col += 32) s_qf[row][col] = qs[N + 4 + col];
+      if (lane == 0) {
+        s_fold[row] = fold;
+        s_item[row] = make_int4(it.tile0, it.ntiles, it.span.L, (it.whole ? kWhole : 0) | (it.first ? kOpening : 0));
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full[buf], Cfg::kQ);
+        bulk_g2s(smem + buf * Cfg::kQ, P.ws_q + ent * Cfg::kQ, Cfg::kQ, &q_full[buf]);
+      }
+      __syncwarp();
+      ++i;
+    }
+    // the copies in flight land before the CTA may exit
+    if (lane == 0)
+      for (int k = max(0, i - 2); k < i; ++k)
+        if (!mbar_wait(&q_full[k & 1], (k >> 1) & 1)) atomic_or_status(P.status, SV_DEV_TIMEOUT);
+  } else if (warp == kQkWarp || warp == kPvWarp) {
+    // ----------------------------------------------------------------- MMA --
+    // One warp per product; all its lanes wait, one issues. f32 accumulators, M =
+    // 128; Q K^T of e4m3 codes and terms, P V of e4m3 codes and e5m2 terms, both
+    // read across their rows.
+    constexpr uint32_t idesc_qk = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+    constexpr uint32_t idesc_pv = idesc_qk | (1u << 10) | (1u << 15) | (1u << 16);
+    uint32_t items = 0, step = 0;   // items started, steps done
+    bool ok = true;
+    if (warp == kQkWarp) {
+      for (uint32_t u = 0; u < (uint32_t)total; ++u) {
+        const uint32_t pb = step & 1, s = u % KS;
+        pages_wait(u, ok);
+        const int flag = s_flag[u % (kChunks * kChunk)];
+        if (flag & kFirst) {
+          ok = kl_wait(&q_full[items & 1], (items >> 1) & 1, abf, P.wait_ns) && ok;
+          ++items;
+        }
+        if (u % kChunk == 0) ok = kl_wait(&scale_full[u / kChunk % kChunks], (u / (kChunk * kChunks)) & 1, abf, P.wait_ns) && ok;
+        // the softmax of the step before the last has read the S buffers
+        if (!(flag & kSecond) && step >= 2) ok = kl_wait(&p_full[pb], ((step >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
+        ok = kl_wait(&k_full[s], (u / KS) & 1, abf, P.wait_ns) && ok;
+        if (!__all_sync(0xffffffffu, ok)) break;
+        t5_fence_after();
+        if (elect_one()) {
+          const uint64_t qd = t5_desc(q_smem + ((items - 1) & 1) * Cfg::kQ, 16, 1024);
+          const uint64_t kd = t5_desc(k_ring + s * kTile, 16, 1024);
+          const uint32_t d = tb + Cfg::kSCol + (T * pb + (flag & kSecond ? 1 : 0)) * N;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)   // 32 head dims per MMA, the hi terms of Q and then the lo terms
+            t5_mma_ss_f8(d, kd + (kk & 3) * 2, qd + (kk >> 2) * (N * 128 / 16) + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
+          t5_commit(&k_empty[s]);
+          if (flag & kEnd) {
+            t5_commit(&s_full[pb]);
+            mbar_arrive(&s_full[pb]);
+          }
+          if (flag & kLast) t5_commit(&q_empty[(items - 1) & 1]);
+        }
+        __syncwarp();
+        pages_done(u);
+        if (flag & kEnd) ++step;
+      }
+    } else {
+      if (lane < 2) mbar_arrive(&s_full[lane]);   // (no P V before the first steps)
+      for (uint32_t u = 0; u < (uint32_t)total; ++u) {
+        const uint32_t pb = step & 1, s = u % VS;
+        pages_wait(u, ok);
+        const int at = u % (kChunks * kChunk), flag = s_flag[at], zero = s_zero[at];
+        pages_done(u);
+        if (flag & kFirst) {
+          // O of the item before the last has been read
+          if (items >= 2) ok = kl_wait(&o_free[items & 1], ((items >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
+          ++items;
+        }
+        ok = kl_wait(&v_full[s], (u / VS) & 1, abf, P.wait_ns) && ok;
+        const int groups = ((flag >> 8) + 1) >> 1;   // of 32 keys that hold any
+        const int z0 = zero & 255, z1 = (zero >> 8) & 255, z2 = zero >> 16;
+        if (__all_sync(0xffffffffu, ok) && (z1 > 0 || z2 < kTK)) {
+          // rows that no query sees become zeros: whatever they hold (NaN codes, or what an
+          // earlier tile left), 0 times it would not do
+          const int n1 = (z1 - z0) * 8, n2 = (groups * 32 - z2) * 8;
+          for (int i = lane; i < n1 + n2; i += 32)
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(v_ring + s * kTile + (i < n1 ? z0 * kD + i * 16 : z2 * kD + (i - n1) * 16)),
+                         "r"(0u)
+                         : "memory");
+          fence_proxy_async_shared();
+          __syncwarp();
+        }
+        if (!(flag & kSecond)) ok = kl_wait(&p_full[pb], (step >> 1) & 1, abf, P.wait_ns) && ok;
+        if (!__all_sync(0xffffffffu, ok)) break;
+        t5_fence_after();
+        if (elect_one()) {
+          const uint64_t pd = t5_desc_row(p_smem + (T * pb + (flag & kSecond ? 1 : 0)) * Cfg::kPBytes, 8 * Cfg::kRow, Cfg::kRow == 64);
+          const uint64_t vd = t5_desc(v_ring + s * kTile, 16, 1024);
+          const uint32_t d = tb + Cfg::kOCol + ((items - 1) & 1) * N;
+#pragma unroll 1
+          for (int kk = 0; kk < groups; ++kk)
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+              t5_mma_ss_f8(d, vd + kk * (32 * kD / 16), pd + e * (Cfg::kTerm / 16) + kk * (32 * Cfg::kRow / 16), idesc_pv,
+                           (flag & kFirst) && kk == 0 && e == 0 ? 0u : 1u);
+          t5_commit(&v_empty[s]);
+          if (flag & kEnd) {
+            t5_commit(&pv_done[pb]);
+            t5_commit(&s_full[pb]);   // the P' buffers are free: part of what the softmax of the step after next waits for
+          }
+        }
+        __syncwarp();
+        if (flag & kEnd) ++step;
+      }
+    }
+    // every MMA issued has completed before TMEM can be released
+    if (total > 0) {
+      uint64_t *dr = &drain[warp - kQkWarp];
+      if (elect_one()) t5_commit(dr);
+      __syncwarp();
+      if (!mbar_wait(dr, 0) && lane == 0) atomic_or_status(P.status, SV_DEV_TIMEOUT);
+    }
+  } else if (warp < softmax_warps) {
+    // ------------------------------------------------------------- softmax --
+    regs_inc<kRegsSoftmax>();
+    const int w = warp >> 2, t = tid & 127;
+    const int c_first = w * CP;                 // this warpgroup's columns
+    const int live = w ? rows - live0 : live0;
+    const int bar = 1 + w;
+    const uint32_t lanes = tb + ((uint32_t)((warp & 3) * 32) << 16);
+    // this key's row of P', and what its 16-byte pieces are exchanged by
+    const uint32_t p_row = p_smem + t * Cfg::kRow, swap = Cfg::kRow == 64 ? (t >> 1) & 3 : (t >> 2) & 1;
+    int u = 0, i = 0;            // tiles and items done
+    uint32_t step = 0;
+    // A wait that gave up (ok false) only shows at the warpgroup's next vote, so
+    // that its four warps leave together.
+    bool ok = true;
+    // The epilogue's second part, a head dim per thread: O of an item, once its
+    // last P V is done; it is taken after the next item's first step, which hides
+    // that P V.
+    struct { bool pending, whole; uint32_t step; int i; int64_t ent; } done = {false, false, 0, 0, 0};
+    auto finish = [&] {
+      done.pending = false;
+      ok = __all_sync(0xffffffffu, kl_wait(&pv_done[done.step & 1], (done.step >> 1) & 1, abf, P.wait_ns)) && ok;
+      if (!ok) return;
+      t5_fence_after();
+      float o[NC];
+      t5_ldn(lanes + Cfg::kOCol + (done.i & 1) * N + c_first, reinterpret_cast<uint32_t(&)[NC]>(o));
+      t5_wait_ld();
+      keep_after<NC>(o);
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        if (k >= live) break;
+        const float x = o[k] * s_fin[done.i & 1][c_first + k];
+        if (done.whole)
+          static_cast<__nv_bfloat16 *>(P.out)[(int64_t)s_row[done.i % 3][c_first + k] * kD + t] = __float2bfloat16_rn(x);
+        else
+          P.ws_acc[(done.ent * P.Rg + w * live0 + k) * kD + t] = x;
+      }
+      t5_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free[done.i & 1]);
+    };
+    while (u < total) {
+      const int buf = i % 3;
+      const uint32_t o_col = lanes + Cfg::kOCol + (i & 1) * N + c_first;
+      ok = __all_sync(0xffffffffu, kl_wait(&q_full[i & 1], (i >> 1) & 1, abf, P.wait_ns)) && ok;
+      const float fold = P.scale_log2 * s_fold[buf];
+      const int4 it = s_item[buf];
+      const int tile0 = it.x, ntiles = it.y, L = it.z;
+      const int edge0 = fold < 0.f ? INT_MIN : L - P.n_new - T * kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
+      if (t < NC) s_nb[c_first + t] = 0.f;
+      float2 l2[NC / 2];
+#pragma unroll
+      for (int k = 0; k < NC / 2; ++k) l2[k] = make_float2(0.f, 0.f);
+      bool gone = bar_or(bar, 128, !ok);
+      for (int ti = 0; ti < ntiles && !gone; ++step) {
+        const int nt = min(ntiles - ti, T);
+        // S of this step, and with it the scales and P' buffers that P V two
+        // steps ago has read
+        const int pb = step & 1;
+        ok = kl_wait(&s_full[pb], (step >> 1) & 1, abf, P.wait_ns) && ok;
+        float ka[T], vc[T], vi[T];
+#pragma unroll
+        for (int h = 0; h < T; ++h) {   // this thread's keys
+          const float2 s = s_scale[(u + h) % (kChunk * kChunks) * kTP + (t >> 4)];   // (of an absent tile: any)
+          ka[h] = s.x * fabsf(fold);
+          vc[h] = lg2f(s.y);
+          vi[h] = rcpf(s.y);
+        }
+        const uint32_t s_col = lanes + Cfg::kSCol + T * pb * N + c_first;
+        // A step that ends past the oldest query or holds keys that a window has
+        // left: position j sees a key iff 0 <= j - j0 < reach.
+        const int key0 = (tile0 + ti) * kTK;
+        const bool edge = key0 >= edge0 || key0 < edge1;
+        int j0[T] = {};
+        uint32_t reach[T] = {};
+        if (edge) {
+#pragma unroll
+          for (int h = 0; h < T; ++h) {
+            const int key = key0 + h * kTK + t;
+            j0[h] = key - (L - P.n_new);
+            reach[h] = P.window > 0 && key >= P.sinks ? (uint32_t)P.window : 0x80000000u;
+          }
+          // Rows with powers of their own: every step of such an item counts as an edge.
+          ok = __all_sync(0xffffffffu, ok);
+          if (fold < 0.f && ok) kl_scale_rows<NC, N>(s_col, nt, &s_qf[buf][c_first]);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        t5_fence_after();
+        float2 y[T][NC / 2];   // log2 weights, minus the reference
+        auto scores = [&](int h) {
+          const float2 ka2 = make_float2(ka[h], ka[h]), vc2 = make_float2(vc[h], vc[h]);
+          uint32_t x[NC];
+          t5_ldn(s_col + h * N, x);
+          t5_wait_ld();
+#pragma unroll
+          for (int k = 0; k < NC; k += 4) {
+            const float4 nb = *reinterpret_cast<const float4 *>(&s_nb[c_first + k]);
+            y[h][k / 2] = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), ka2,
+                                     __fadd2_rn(vc2, make_float2(nb.x, nb.y)));
+            y[h][k / 2 + 1] = __ffma2_rn(make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), ka2,
+                                         __fadd2_rn(vc2, make_float2(nb.z, nb.w)));
+          }
+          if (edge) {
+#pragma unroll
+            for (int k = 0; k < NC; k += 4) {
+              const int4 j = *reinterpret_cast<const int4 *>(&s_pos[buf][c_first + k]);
+              if ((uint32_t)(j.x - j0[h]) >= reach[h]) y[h][k / 2].x = -INFINITY;
+              if ((uint32_t)(j.y - j0[h]) >= reach[h]) y[h][k / 2].y = -INFINITY;
+              if ((uint32_t)(j.z - j0[h]) >= reach[h]) y[h][k / 2 + 1].x = -INFINITY;
+              if ((uint32_t)(j.w - j0[h]) >= reach[h]) y[h][k / 2 + 1].y = -INFINITY;
+            }
+          }
+        };
+        const bool first = ti == 0;
+        for (int again = 0;; ++again) {
+          scores(0);
+          if constexpr (T > 1) {
+            if (nt > 1) {
+              scores(1);
+            } else {
+#pragma unroll
+              for (int k = 0; k < NC / 2; ++k) y[1][k] = make_float2(-INFINITY, -INFINITY);
+            }
+          }
+          if (again) break;
+          // The first step of a sequence sets the references (they are 0 so
+          // far); later ones move when a weight exceeds 2^kMove. All four warps
+          // decide together, as they share O.
+          float top = fmaxf(y[0][0].x, y[0][0].y);
+#pragma unroll
+          for (int k = 1; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[0][k].x), y[0][k].y);
+          if constexpr (T > 1) {
+#pragma unroll
+            for (int k = 0; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[1][k].x), y[1][k].y);
+          }
+          if (!bar_or(bar, 128, first || top > kMove || !ok)) break;
+          if (bar_or(bar, 128, !ok)) {
+            gone = true;
+            break;
+          }
+          // each column's largest weight, without the reference
+          if (first) {
+            float mine = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+              const float m = warp_top(k & 1 ? fmaxf(y[0][k / 2].y, y[T - 1][k / 2].y) : fmaxf(y[0][k / 2].x, y[T - 1][k / 2].x));
+              if (lane == k) mine = m;
+            }
+            if (lane < NC) s_max[warp][lane] = mine;
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < live; ++k) {
+              float m = -INFINITY;
+#pragma unroll
+              for (int h = 0; h < T; ++h) {
+                if (h >= nt) break;
+                uint32_t xs;
+                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(xs) : "r"(s_col + h * N + k));
+                t5_wait_ld();
+                const float z = fmaf(__uint_as_float(xs), ka[h], vc[h]);
+                if (!edge || (uint32_t)(s_pos[buf][c_first + k] - j0[h]) < reach[h]) m = fmaxf(m, z);
+              }
+              m = warp_max(m);
+              if (lane == 0) s_max[warp][k] = m;
+            }
+          }
+          named_bar_sync(bar, 128);
+          if (t < NC) {
+            float a = 1.f, nb = first ? kUnset : s_nb[c_first + t];
+            if (t < live) {
+              const float m = fmaxf(fmaxf(s_max[4 * w][t], s_max[4 * w + 1][t]), fmaxf(s_max[4 * w + 2][t], s_max[4 * w + 3][t]));
+              if (m + nb > kMove) {   // (a row that has met no key keeps kUnset)
+                a = ex2f(kTop - m - nb);
+                nb = kTop - m;
+              }
+            } else {
+              nb = -kUnset;   // padding never moves
+            }
+            s_nb[c_first + t] = nb;
+            s_a[c_first + t] = a;
+          }
+          named_bar_sync(bar, 128);
+          if (first) {
+#pragma unroll
+            for (int k = 0; k < NC; k += 4) {
+              const float4 nb = *reinterpret_cast<const float4 *>(&s_nb[c_first + k]);
+#pragma unroll
+              for (int h = 0; h < T; ++h) {
+                y[h][k / 2] = __fadd2_rn(y[h][k / 2], make_float2(nb.x, nb.y));
+                y[h][k / 2 + 1] = __fadd2_rn(y[h][k / 2 + 1], make_float2(nb.z, nb.w));
+              }
+            }
+            break;
+          } else {
+#pragma unroll
+            for (int k = 0; k < NC; k += 4) {
+              const float4 a = *reinterpret_cast<const float4 *>(&s_a[c_first + k]);
+              l2[k / 2] = __fmul2_rn(l2[k / 2], make_float2(a.x, a.y));
+              l2[k / 2 + 1] = __fmul2_rn(l2[k / 2 + 1], make_float2(a.z, a.w));
+            }
+            // O too, once the previous P V has landed
+            ok = __all_sync(0xffffffffu, kl_wait(&pv_done[pb ^ 1], ((step - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
+            t5_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < live; ++k) {
+              uint32_t o;
+              const uint32_t at = o_col + k;
+              asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o) : "r"(at));
+              t5_wait_ld();
+              o = __float_as_uint(__uint_as_float(o) * s_a[c_first + k]);
+              asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(at), "r"(o) : "memory");
+            }
+            t5_wait_st();
+          }
+        }
+        if (gone) break;
+#pragma unroll
+        for (int h = 0; h < T; ++h) {
+          if (h >= nt) break;
+          const float2 vi2 = make_float2(vi[h], vi[h]);
+          const uint32_t dst = p_row + (T * pb + h) * Cfg::kPBytes;
+#pragma unroll
+          for (int c = 0; c < NC; c += 8) {   // eight columns: a half of a 16-byte piece
+            uint32_t ph[4], w0[3], w1[3] = {};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int e = c / 2 + k;
+              ph[k] = 0;
+              if (e >= NC / 2) continue;
+              const float2 p = make_float2(ex2f(y[h][e].x), ex2f(y[h][e].y));
+              l2[e] = __ffma2_rn(p, vi2, l2[e]);
+              ph[k] = pack2<true>(p.x, p.y);
+            }
+            cut_weights(ph[0], ph[1], w0);
+            if (NC - c >= 8) cut_weights(ph[2], ph[3], w1);   // (what the columns of padding hold does not matter)
+            const uint32_t col = c_first + c;
+            const uint32_t at = dst + (((col >> 4) ^ swap) << 4) + (col & 8);
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+              asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + e * Cfg::kTerm), "r"(w0[e]), "r"(w1[e]) : "memory");
+          }
+        }
+        fence_proxy_async_shared();
+        t5_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[pb]);
+        pages_done(u);
+        if (nt > 1) pages_done(u + 1);
+        ti += nt;
+        u += nt;
+        if (done.pending) finish();
+      }
+      if (gone) break;
+      // ---- epilogue, first part: sums over the keys -------------------------
+      {
+        float v[NC];
+#pragma unroll
+        for (int k = 0; k < NC; ++k) v[k] = k & 1 ? l2[k / 2].y : l2[k / 2].x;
+        int at = 0, n = 0;
+        warp_sums<NC>(v, lane, at, n);
+#pragma unroll
+        for (int k = 0; k < 5; ++k)   // (lanes with the same sums write the same words)
+          if (k < n) s_red[warp][at + k] = v[k];
+      }
+      named_bar_sync(bar, 128);
+      const int64_t ent = 2 * (int64_t)blockIdx.x + (it.w & kOpening ? 0 : 1);
+      if (t < live) {
+        float l = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) l += s_red[4 * w + k][t];
+        // (a row of NaN stays NaN; l is 0 only for a row without keys, which a query that sees itself never is)
+        s_fin[i & 1][c_first + t] = it.w & kWhole ? 1.f / l : 1.f;
+        if (!(it.w & kWhole)) {
+          const int64_t e = ent * P.Rg + w * live0 + t;
+          P.ws_ml[2 * e] = -s_nb[c_first + t];
+          P.ws_ml[2 * e + 1] = l;
+        }
+      }
+      done = {true, (it.w & kWhole) != 0, step - 1, i, ent};
+      ++i;
+    }
+    named_bar_sync(bar, 128);
+    if (done.pending) finish();
+  }
+  __syncthreads();
+  if (tid == 0 && *abf) atomic_or_status(P.status, SV_DEV_TIMEOUT);
+  t5_fence_after();
+  if (warp == kQkWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tb), "r"(512));
+}
+
+template <int NC>
+sv_status launch_q8(const KlParams &P, const Q8Maps &M, int C, cudaStream_t st) {
+  static DeviceOnce once;
+  const cudaError_t err = once_per_device(once, [] {
+    return cudaFuncSetAttribute(attn_q8_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q8Cfg<NC>::kSmem);
+  });
+  if (err != cudaSuccess) return fail(SV_ERR_CUDA, "spec_verify_attn_q8: cudaFuncSetAttribute: %s", cudaGetErrorString(err));
+  const int64_t prep = (P.NR + kPrepWarps - 1) / kPrepWarps + (int64_t)P.B * P.H_kv * P.RG;
+  launch_k(kl_prep_kernel<NC, false>, dim3((unsigned)prep), dim3(32 * kPrepWarps), 0, st, 1, P);
+  launch_k(attn_q8_kernel<NC>, dim3(C), dim3(32 * kWarps), Q8Cfg<NC>::kSmem, st, 1, P, M);
+  return check_launch("spec_verify_attn_q8 launch");
+}
+
+// Query rows of a kv head on the tensor cores: 64 share a pass over the cache.
+constexpr int64_t kMaxRows = 1 << 14;
+
+}  // namespace
+}  // namespace sv
 
 using namespace sv;
 
 extern "C" size_t spec_verify_attn_q8_workspace_size(int B, int n_new, int H_q, int H_kv, int d_head,
                                                      int max_blocks_per_seq, int block_size, int window, int sinks) {
-  return spec_verify_attn_window_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size, window,
-                                                sinks);
+  const size_t other = spec_verify_attn_window_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq,
+                                                              block_size, window, sinks);
+  if (other == 0) return 0;
+  if ((int64_t)window >= (int64_t)max_blocks_per_seq * block_size) window = sinks = 0;
+  const KlPlan p = kl_plan(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size, SV_BF16, window, sinks, kMaxRows);
+  // (queries in f32 run on the CUDA-core kernel whatever the shape)
+  return p.tc ? std::max(other, kl_ws_bytes(p, B, H_kv)) : other;
 }
 
 extern "C" sv_status spec_verify_attn_q8(const void *q, sv_dtype q_dtype, const void *k_cache, const void *v_cache,
@@ -21,7 +777,72 @@ extern "C" sv_status spec_verify_attn_q8(const void *q, sv_dtype q_dtype, const 
   if (window < 0 || sinks < 0) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_q8: negative window or sinks");
   if (max_blocks_per_seq > 0 && block_size > 0 && !capacity_ok(max_blocks_per_seq, block_size))
     return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn_q8: max_blocks_per_seq * block_size must be below 2^30");
-  return attn_cuda_core_q8(q, q_dtype, k_cache, v_cache, layout, block_table, max_blocks_per_seq, seq_lens, B, n_new,
-                           H_q, H_kv, d_head, block_size, num_blocks, softmax_scale, window, sinks, out, out_dtype,
-                           workspace, workspace_bytes, dev_status, stream);
+  KlPlan p = {};
+  const bool sizes_ok = B >= 0 && n_new >= 1 && H_q >= 1 && H_kv >= 1 && H_q % H_kv == 0 && num_blocks >= 1 &&
+                        max_blocks_per_seq >= 1 && H_kv <= 65535 && block_size >= 1;
+  int win = window, snk = sinks;
+  if ((int64_t)win >= (int64_t)max_blocks_per_seq * block_size) win = snk = 0;   // reaches every key
+  if (sizes_ok) p = kl_plan(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size, q_dtype, win, snk, kMaxRows);
+  if (!p.tc || q_dtype != out_dtype)
+    return attn_cuda_core_q8(q, q_dtype, k_cache, v_cache, layout, block_table, max_blocks_per_seq, seq_lens, B, n_new,
+                             H_q, H_kv, d_head, block_size, num_blocks, softmax_scale, window, sinks, out, out_dtype,
+                             workspace, workspace_bytes, dev_status, stream);
+  if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out)
+    return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_q8: null pointer argument");
+  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
+    return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_q8: softmax_scale must be finite and > 0");
+  KlParams P;
+  memset(&P, 0, sizeof(P));
+  const sv_status rc = q8_check("spec_verify_attn_q8", k_cache, v_cache, layout, H_kv, d_head, block_size, &P.block_stride);
+  if (rc != SV_OK) return rc;
+  const size_t need = kl_ws_bytes(p, B, H_kv);
+  if (!workspace || workspace_bytes < need)
+    return fail(SV_ERR_WORKSPACE, "spec_verify_attn_q8: workspace needs %zu bytes", need);
+  if (!aligned(workspace, 256)) return fail(SV_ERR_WORKSPACE, "spec_verify_attn_q8: workspace not 256-byte aligned");
+  if (!aligned(q, 16) || !aligned(out, 16))
+    return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_q8: q and out must be 16-byte aligned");
+  if (B == 0) return ok();
+  PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode();
+  if (!enc) return fail(SV_ERR_CUDA, "spec_verify_attn_q8: cuTensorMapEncodeTiled unavailable");
+  Q8Maps M;
+  const cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)kBS, (cuuint64_t)H_kv, (cuuint64_t)num_blocks};
+  const cuuint64_t strides[3] = {(cuuint64_t)kD, (cuuint64_t)kD * kBS, (cuuint64_t)P.block_stride};
+  const cuuint32_t box[4] = {(cuuint32_t)kD, (cuuint32_t)kBS, 1, 1}, ones[4] = {1, 1, 1, 1};
+  for (int w = 0; w < 2; ++w) {
+    const CUresult r = enc(w ? &M.v : &M.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(w ? v_cache : k_cache), dims,
+                           strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(SV_ERR_INVALID_ARG, "spec_verify_attn_q8: cuTensorMapEncodeTiled failed (%d)", (int)r);
+  }
+  const size_t ent = (size_t)2 * p.C * p.Rg;
+  P.q = q; P.out = out;
+  P.k_cache = static_cast<const uint8_t *>(k_cache); P.v_cache = static_cast<const uint8_t *>(v_cache);
+  P.block_table = block_table; P.seq_lens = seq_lens;
+  P.ws_acc = static_cast<float *>(workspace);
+  P.ws_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + align_up(ent * kD * sizeof(float), 256));
+  uint8_t *at = reinterpret_cast<uint8_t *>(P.ws_ml) + align_up(ent * 2 * sizeof(float), 256);
+  P.ws_split = reinterpret_cast<int4 *>(at);
+  at += align_up((size_t)p.NR * sizeof(int4), 256);
+  P.ws_q = at;
+  at += align_up((size_t)B * H_kv * p.RG * kl_cols(p) * 256, 256);
+  P.ws_qs = reinterpret_cast<float *>(at);
+  P.status = dev_status;
+  P.B = B; P.n_new = n_new; P.H_q = H_q; P.H_kv = H_kv; P.G = H_q / H_kv; P.R = p.R; P.Rg = p.Rg; P.RG = p.RG;
+  P.NR = p.NR; P.max_blocks = max_blocks_per_seq; P.num_blocks = num_blocks; P.window = win; P.sinks = snk;
+  P.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634074);
+  P.wait_ns = wait_limit_ns();
+  P.withhold = test_withhold();
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int half = kl_first(p.Rg);   // rows of a softmax warpgroup
+  const sv_status r2 = half <= 4    ? launch_q8<4>(P, M, p.C, st)
+                       : half <= 8  ? launch_q8<8>(P, M, p.C, st)
+                       : half <= 12 ? launch_q8<12>(P, M, p.C, st)
+                       : half <= 16 ? launch_q8<16>(P, M, p.C, st)
+                       : half <= 20 ? launch_q8<20>(P, M, p.C, st)
+                       : half <= 24 ? launch_q8<24>(P, M, p.C, st)
+                                    : launch_q8<32>(P, M, p.C, st);
+  if (r2 != SV_OK || p.NR == 1) return r2;
+  launch_k(kl_merge_kernel, dim3((p.NR - 1) * H_kv * p.RG, (p.Rg + kMergeWarps - 1) / kMergeWarps),
+           dim3(32 * kMergeWarps), 0, st, 1, P);
+  return check_launch("spec_verify_attn_q8 merge launch");
 }

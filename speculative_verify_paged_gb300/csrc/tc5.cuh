@@ -3,10 +3,28 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
 
 #include "sv_common.cuh"
 
 namespace sv {
+
+// The driver's tensor map encoder (NULL if there is none).
+inline PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
 
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {

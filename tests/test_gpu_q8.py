@@ -239,7 +239,7 @@ def test_attention(lib, H_q, H_kv, n, lens, window, sinks):
 
 
 @pytest.mark.parametrize("window,sinks", [(0, 0), (33, 5), (200, 40)])
-@pytest.mark.parametrize("H_q,H_kv,n", [(2, 2, r) for r in (9, 13, 24, 40, 47, 49, 57, 65, 97, 101, 128)] + [(24, 2, 5), (20, 1, 5)])
+@pytest.mark.parametrize("H_q,H_kv,n", [(2, 2, r) for r in (9, 13, 24, 40, 47, 49, 57, 65, 97, 101, 128, 200)] + [(24, 2, 5), (20, 1, 5), (48, 1, 7)])
 def test_attention_query_rows(lib, H_q, H_kv, n, window, sinks):
     # every way the query rows of a kv head are dealt to row groups and warpgroups
     lens = [n, n + 1, 300, 129 + n, 1025]
@@ -344,7 +344,7 @@ def test_attention_window_reads_no_other_pages(lib, qd):
 
 
 @pytest.mark.parametrize("L", [37, 33, 48, 128, 129, 250, 300])
-@pytest.mark.parametrize("H_q,n", [(8, 2), (16, 8)])
+@pytest.mark.parametrize("H_q,n", [(8, 2), (16, 8), (64, 8)])
 def test_attention_garbage_past_the_end(lib, H_q, n, L):
     # unwritten slots of the last page hold NaN codes
     table, total = table_for([L, 200], 16, seed=4)
