@@ -38,13 +38,13 @@ namespace {
 constexpr int kTile = kTK * kD;            // bytes of a tile of K or V
 constexpr int kWarps = 16;
 constexpr int kPageWarp = 8, kKWarp = 9, kVWarp = 10, kQkWarp = 11, kPvWarp = 12, kQWarp = 13;
-constexpr int kStatic = 9216;              // static shared memory, at most
+constexpr int kStatic = 9728;              // static shared memory, at most
 // Registers a thread: the softmax warps take what the others leave.
 constexpr int kRegs = 128, kRegsSoftmax = 192, kRegsOther = 64;
 static_assert(256 * kRegsSoftmax + 32 * (kWarps - 8) * kRegsOther <= 32 * kWarps * kRegs, "registers");
 // A row's reference puts its largest weight at 2^kTop and moves once one exceeds
 // 2^kMove (f16 ends at 65504, e5m2 at 57344).
-constexpr float kTop = 10.f, kMove = 15.f;
+constexpr float kTop = 10.f, kMove = 15.9f;
 
 template <int NC> struct Q8Cfg : KlCfg<NC> {
   using KlCfg<NC>::kN;
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
   __shared__ int s_row[3][N];
   __shared__ float s_fold[3];
   __shared__ __align__(16) int4 s_item[3];   // first tile, tiles, length in span coordinates, kWhole | kOpening
-  __shared__ __align__(16) float s_nb[N], s_a[N];   // minus the reference; the last factor of a rescale
+  __shared__ __align__(16) float s_nb[N], s_by[N], s_a[N];   // minus the reference; what it last moved by, as a power and a factor
   __shared__ float s_max[8][NC], s_red[8][NC], s_fin[2][N];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -494,7 +494,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
       const int4 it = s_item[buf];
       const int tile0 = it.x, ntiles = it.y, L = it.z;
       const int edge0 = fold < 0.f ? INT_MIN : L - P.n_new - T * kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
-      if (t < NC) s_nb[c_first + t] = 0.f;
+      if (t < NC) s_nb[c_first + t] = t < live ? 0.f : -kUnset;   // (padding has no weight)
+      bool open = true, unset = t < live;   // rows that have met no key; this thread's row among them
       float2 l2[NC / 2];
 #pragma unroll
       for (int k = 0; k < NC / 2; ++k) l2[k] = make_float2(0.f, 0.f);
@@ -558,109 +559,78 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
             }
           }
         };
-        const bool first = ti == 0;
-        for (int again = 0;; ++again) {
-          scores(0);
-          if constexpr (T > 1) {
-            if (nt > 1) {
-              scores(1);
-            } else {
+        scores(0);
+        if constexpr (T > 1) {
+          if (nt > 1) {
+            scores(1);
+          } else {
 #pragma unroll
-              for (int k = 0; k < NC / 2; ++k) y[1][k] = make_float2(-INFINITY, -INFINITY);
-            }
+            for (int k = 0; k < NC / 2; ++k) y[1][k] = make_float2(-INFINITY, -INFINITY);
           }
-          if (again) break;
-          // The first step of a sequence sets the references (they are 0 so
-          // far); later ones move when a weight exceeds 2^kMove. All four warps
-          // decide together, as they share O.
-          float top = fmaxf(y[0][0].x, y[0][0].y);
+        }
+        // Steps set the references of rows that have met no key yet (they are 0 so
+        // far), and move those of rows with a weight above 2^kMove. All four warps
+        // decide together, as they share O.
+        float top = fmaxf(y[0][0].x, y[0][0].y);
 #pragma unroll
-          for (int k = 1; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[0][k].x), y[0][k].y);
-          if constexpr (T > 1) {
+        for (int k = 1; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[0][k].x), y[0][k].y);
+        if constexpr (T > 1) {
 #pragma unroll
-            for (int k = 0; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[1][k].x), y[1][k].y);
-          }
-          if (!bar_or(bar, 128, first || top > kMove || !ok)) break;
+          for (int k = 0; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[1][k].x), y[1][k].y);
+        }
+        if (bar_or(bar, 128, open || top > kMove || !ok)) {
           if (bar_or(bar, 128, !ok)) {
             gone = true;
             break;
           }
-          // each column's largest weight, without the reference
-          if (first) {
-            float mine = -INFINITY;
+          float mine = -INFINITY;   // each column's largest weight
 #pragma unroll
-            for (int k = 0; k < NC; ++k) {
-              const float m = warp_top(k & 1 ? fmaxf(y[0][k / 2].y, y[T - 1][k / 2].y) : fmaxf(y[0][k / 2].x, y[T - 1][k / 2].x));
-              if (lane == k) mine = m;
-            }
-            if (lane < NC) s_max[warp][lane] = mine;
-          } else {
-#pragma unroll 1
-            for (int k = 0; k < live; ++k) {
-              float m = -INFINITY;
-#pragma unroll
-              for (int h = 0; h < T; ++h) {
-                if (h >= nt) break;
-                uint32_t xs;
-                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(xs) : "r"(s_col + h * N + k));
-                t5_wait_ld();
-                const float z = fmaf(__uint_as_float(xs), ka[h], vc[h]);
-                if (!edge || (uint32_t)(s_pos[buf][c_first + k] - j0[h]) < reach[h]) m = fmaxf(m, z);
-              }
-              m = warp_max(m);
-              if (lane == 0) s_max[warp][k] = m;
-            }
+          for (int k = 0; k < NC; ++k) {
+            const float m = warp_top(k & 1 ? fmaxf(y[0][k / 2].y, y[T - 1][k / 2].y) : fmaxf(y[0][k / 2].x, y[T - 1][k / 2].x));
+            if (lane == k) mine = m;
           }
+          if (lane < NC) s_max[warp][lane] = mine;
           named_bar_sync(bar, 128);
           if (t < NC) {
-            float a = 1.f, nb = first ? kUnset : s_nb[c_first + t];
+            float a = 1.f, by = 0.f;
             if (t < live) {
               const float m = fmaxf(fmaxf(s_max[4 * w][t], s_max[4 * w + 1][t]), fmaxf(s_max[4 * w + 2][t], s_max[4 * w + 3][t]));
-              if (m + nb > kMove) {   // (a row that has met no key keeps kUnset)
-                a = ex2f(kTop - m - nb);
-                nb = kTop - m;
+              if (m > (unset ? -INFINITY : kMove)) {
+                by = kTop - m;
+                a = unset ? 1.f : ex2f(by);
+                s_nb[c_first + t] += by;
+                unset = false;
               }
-            } else {
-              nb = -kUnset;   // padding never moves
             }
-            s_nb[c_first + t] = nb;
+            s_by[c_first + t] = by;
             s_a[c_first + t] = a;
           }
-          named_bar_sync(bar, 128);
-          if (first) {
+          open = bar_or(bar, 128, unset);
 #pragma unroll
-            for (int k = 0; k < NC; k += 4) {
-              const float4 nb = *reinterpret_cast<const float4 *>(&s_nb[c_first + k]);
+          for (int k = 0; k < NC; k += 4) {
+            const float4 by = *reinterpret_cast<const float4 *>(&s_by[c_first + k]);
+            const float4 a = *reinterpret_cast<const float4 *>(&s_a[c_first + k]);
 #pragma unroll
-              for (int h = 0; h < T; ++h) {
-                y[h][k / 2] = __fadd2_rn(y[h][k / 2], make_float2(nb.x, nb.y));
-                y[h][k / 2 + 1] = __fadd2_rn(y[h][k / 2 + 1], make_float2(nb.z, nb.w));
-              }
+            for (int h = 0; h < T; ++h) {
+              y[h][k / 2] = __fadd2_rn(y[h][k / 2], make_float2(by.x, by.y));
+              y[h][k / 2 + 1] = __fadd2_rn(y[h][k / 2 + 1], make_float2(by.z, by.w));
             }
-            break;
-          } else {
-#pragma unroll
-            for (int k = 0; k < NC; k += 4) {
-              const float4 a = *reinterpret_cast<const float4 *>(&s_a[c_first + k]);
-              l2[k / 2] = __fmul2_rn(l2[k / 2], make_float2(a.x, a.y));
-              l2[k / 2 + 1] = __fmul2_rn(l2[k / 2 + 1], make_float2(a.z, a.w));
-            }
-            // O too, once the previous P V has landed
+            l2[k / 2] = __fmul2_rn(l2[k / 2], make_float2(a.x, a.y));
+            l2[k / 2 + 1] = __fmul2_rn(l2[k / 2 + 1], make_float2(a.z, a.w));
+          }
+          if (ti > 0) {   // O too, once the previous P V has landed
             ok = __all_sync(0xffffffffu, kl_wait(&pv_done[pb ^ 1], ((step - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
             t5_fence_after();
-#pragma unroll 1
-            for (int k = 0; k < live; ++k) {
-              uint32_t o;
-              const uint32_t at = o_col + k;
-              asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o) : "r"(at));
-              t5_wait_ld();
-              o = __float_as_uint(__uint_as_float(o) * s_a[c_first + k]);
-              asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(at), "r"(o) : "memory");
-            }
+            float o[NC];
+            t5_ldn(o_col, reinterpret_cast<uint32_t(&)[NC]>(o));
+            t5_wait_ld();
+            keep_after<NC>(o);
+#pragma unroll
+            for (int k = 0; k < NC; ++k) o[k] *= s_a[c_first + k];
+            t5_stn(o_col, reinterpret_cast<const uint32_t(&)[NC]>(o));
             t5_wait_st();
           }
         }
-        if (gone) break;
 #pragma unroll
         for (int h = 0; h < T; ++h) {
           if (h >= nt) break;
@@ -719,7 +689,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
         s_fin[i & 1][c_first + t] = it.w & kWhole ? 1.f / l : 1.f;
         if (!(it.w & kWhole)) {
           const int64_t e = ent * P.Rg + w * live0 + t;
-          P.ws_ml[2 * e] = -s_nb[c_first + t];
+          P.ws_ml[2 * e] = unset ? -kUnset : -s_nb[c_first + t];
           P.ws_ml[2 * e + 1] = l;
         }
       }

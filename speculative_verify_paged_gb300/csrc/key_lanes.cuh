@@ -430,6 +430,15 @@ __device__ __forceinline__ void t5_st8(uint32_t taddr, const uint32_t *r) {
                : "memory");
 }
 
+template <int N>
+__device__ __forceinline__ void t5_stn(uint32_t taddr, const uint32_t (&r)[N]) {
+  constexpr int a = N / 16 * 16, b = a + (N - a) / 8 * 8;
+#pragma unroll
+  for (int k = 0; k < a; k += 16) t5_st16(taddr + k, *reinterpret_cast<const uint32_t(*)[16]>(r + k));
+  if constexpr (b > a) t5_st8(taddr + a, r + a);
+  if constexpr (N > b) t5_st4(taddr + b, r + b);
+}
+
 // Columns of S times their rows' powers of two, where they lie (nt tiles)
 template <int NC, int N>
 __device__ __noinline__ void kl_scale_rows(uint32_t s_col, int nt, const float *qf) {
