@@ -38,7 +38,7 @@ namespace {
 constexpr int kTile = kTK * kD;            // bytes of a tile of K or V
 constexpr int kLanes = 2;                  // pipelines that take the tiles in turn
 constexpr int kWarps = 24;
-constexpr int kPageWarp = 16, kKWarp = 17, kVWarp = 18, kQkWarp = 19, kPvWarp = 20, kQWarp = 21;
+constexpr int kPageWarp = 16, kKWarp = 17, kVWarp = 18, kQkWarp = 19, kPvWarp = 20, kQWarp = 21, kScaleWarp = 22;
 // Registers a thread: at the launch, of the softmax warps and of the others.
 constexpr int kRegs = 80, kRegsSoftmax = 96, kRegsOther = 48;
 static_assert(512 * kRegsSoftmax + 32 * (kWarps - 16) * kRegsOther <= 32 * kWarps * kRegs, "registers");
@@ -50,22 +50,22 @@ constexpr int kOwn = 16;   // of a tile: the first of the sequence in its pipeli
 template <int NC> struct Q8Cfg : KlCfg<NC> {
   using KlCfg<NC>::kN;
   using KlCfg<NC>::kQ;
-  // Up to 32 columns the terms of P' side by side are the columns of one product
-  // with three sums in O (an MMA of few columns costs 40 cycles and more for its
-  // other operand: 16 or 32 columns 41, 48 columns 45, 96 columns 57); beyond
-  // that tensor memory holds one sum. P' lies in atoms of 32 columns, 32 bytes a key.
-  static constexpr bool kWide = kN <= 32;
-  static constexpr int kSums = kWide ? 3 : 1, kOCols = kSums * kN;
-  static constexpr int kTerm = kWide ? kN : (kN + 31) / 32 * 32;   // columns from term to term
-  static constexpr int kAtom = kTK * 32, kPBytes = (3 * kTerm + 31) / 32 * kAtom;
+  // The terms of Q, and those of P', side by side are the columns of one product
+  // with several sums: what an MMA of few columns costs is its other operand (16
+  // or 32 columns 41 cycles, 48 45, 96 57, 144 72), 4 KB from shared memory, whose
+  // bandwidth the kernel is short of. Tensor memory has room for kSSums sums in
+  // kSB buffers of S a pipeline, and for three in kOB of O.
+  static constexpr int kSSums = kN <= 48 ? 2 : 1, kSCols = kSSums * kN, kSB = kN <= 16 ? 2 : 1;
+  static constexpr int kOCols = 3 * kN, kOB = kN <= 32 ? 2 : 1;
+  // P' lies in atoms of 32 columns, 32 bytes a key.
+  static constexpr int kAtom = kTK * 32, kPBytes = (kOCols + 31) / 32 * kAtom;
   static constexpr int kStatic = 7168 + 144 * kN;                  // static shared memory, at most
   static constexpr int kFixed = 1024 + 2 * kQ + kLanes * kPBytes;
   static constexpr int kAll = (227 * 1024 - kStatic - kFixed) / kTile;   // stages that fit
   static constexpr int kVS = (kAll + 1) / 2 < 5 ? (kAll + 1) / 2 : 5, kKS = kAll - kVS < 5 ? kAll - kVS : 5;
   static constexpr int kSmem = kFixed + (kKS + kVS) * kTile;
-  // two S buffers a pipeline, and O buffers: one for each pipeline and parity of the sequence
-  static constexpr uint32_t kSCol = 0, kOCol = 2 * kLanes * kN;
-  static_assert(kOCol + 2 * kLanes * kOCols <= 512, "TMEM columns");
+  static constexpr uint32_t kSCol = 0, kOCol = kLanes * kSB * kSCols;
+  static_assert(kOCol + kLanes * kOB * kOCols <= 512, "TMEM columns");
   static_assert(kKS >= 2 && kVS >= 2, "shared memory");
 };
 
@@ -109,13 +109,13 @@ __device__ __forceinline__ void cut_weights(uint32_t h0, uint32_t h1, uint32_t (
 // two of them in flight hide each other's. Warps 0-7 and 8-15: their softmax (a
 // key per thread; each warpgroup half of the query rows, or the first all of up
 // to 8). The pipelines join their sums at a sequence's end, in the epilogue (a
-// head dim per thread), which they do in turn. 16: block numbers, flags and
-// scales of the tiles ahead. 17, 18: copy the K and V codes. 19: issues Q K^T,
-// owns the 512 TMEM columns. 20: issues P V. 21: Q of the next sequence.
+// head dim per thread), which they do in turn. 16: block numbers and flags of the
+// tiles ahead. 17, 18: copy the K and V codes. 19: issues Q K^T, owns the 512 TMEM
+// columns. 20: issues P V. 21: Q of the next sequence. 22: the blocks' scales.
 template <int NC>
 __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_constant__ KlParams P, const __grid_constant__ Q8Maps M) {
   using Cfg = Q8Cfg<NC>;
-  constexpr int N = Cfg::kN, CP = Cfg::kCols, KS = Cfg::kKS, VS = Cfg::kVS, X = kLanes;
+  constexpr int N = Cfg::kN, CP = Cfg::kCols, KS = Cfg::kKS, VS = Cfg::kVS, X = kLanes, SB = Cfg::kSB, OB = Cfg::kOB;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t page_full[kChunks], page_empty[kChunks], scale_full[kChunks];
   __shared__ int s_phys[kChunks * kChunk * kTP];   // blocks of the tiles ahead
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
   // rows of V that no query sees: [z0, z1) and from z2 on, z0 | z1 << 8 | z2 << 16
   __shared__ int s_zero[kChunks * kChunk];
   __shared__ __align__(8) uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS];
-  __shared__ __align__(8) uint64_t s_full[X][2], s_free[X][2], p_full[X], pv_done[X];
+  __shared__ __align__(8) uint64_t s_full[X][SB], s_free[X][SB], p_full[X], pv_done[X];
   __shared__ __align__(8) uint64_t q_full[2], ml_full[2], o_done[2], o_free[2], drain[2];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
     for (int k = 0; k < kChunks; ++k) {
       mbar_init(&page_full[k], 1);
       mbar_init(&scale_full[k], 1);
-      mbar_init(&page_empty[k], 4 + 4 * X * groups);   // the K, V and MMA warps, and those that read the scales
+      mbar_init(&page_empty[k], 5 + 4 * X * groups);   // the K, V, MMA and scale warps, and those that read the scales
     }
     for (int k = 0; k < KS; ++k) {
       mbar_init(&k_full[k], 1);
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
       mbar_init(&v_empty[k], 1);
     }
     for (int x = 0; x < X; ++x) {
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < SB; ++k) {
         mbar_init(&s_full[x][k], 2);   // Q K^T (its commit), and the issuing lane itself, which has seen the scales
         mbar_init(&s_free[x][k], 4 * groups);
       }
@@ -224,19 +224,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
   if (warp != kPageWarp) pdl_wait();
   pdl_trigger();
   if (warp == kPageWarp) {
-    // ------------------------------------------- block numbers and scales --
+    // ------------------------------------------------------- block numbers --
     KlWalk wk = kl_walk(P, work);
     KlItem it;
     bool have = kl_next(P, wk, it);
     int ti = 0;   // next tile of the item
     bool bad = false;
-    const int64_t scales_at = q8_scale_offset(P.H_kv, kD, kBS) + 4 * g;
     for (int c = 0; c * kChunk < total; ++c) {
+      if (c == kChunks) pdl_wait();   // (from here on it waits for warps that wait there)
       if (c >= kChunks &&
           !__all_sync(0xffffffffu, kl_wait(&page_empty[c % kChunks], ((c / kChunks) & 1) ^ 1, abf, P.wait_ns)))
         break;
-      int filled = 0;
-      while (filled < kChunk && have) {
+      for (int filled = 0; filled < kChunk && have;) {
         const int n = min(kChunk - filled, it.ntiles - ti);
         const int32_t *table = P.block_table + (int64_t)it.b * P.max_blocks;
         int phys[kChunk * kTP / 32];
@@ -279,22 +278,39 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&page_full[c % kChunks]);
-      if (c == 0) pdl_wait();   // (the kernel before may write the pages)
-#pragma unroll
-      for (int k = 0; k < kChunk * kTP / 32; ++k) {
-        const int e = lane + 32 * k;
-        if (e >= filled * kTP) continue;
-        const int at = c % kChunks * kChunk * kTP + e;
-        const int64_t off = (int64_t)s_phys[at] * P.block_stride + scales_at;
-        const float ks = q8_scale(*reinterpret_cast<const float *>(P.k_cache + off));
-        const float vs = q8_scale(*reinterpret_cast<const float *>(P.v_cache + off));
-        s_scale[at] = make_float4(ks, lg2f(vs), rcpf(vs), 0.f);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&scale_full[c % kChunks]);
     }
     pdl_wait();
     if (bad) atomic_or_status(P.status, SV_DEV_BAD_BLOCK);
+  } else if (warp == kScaleWarp) {
+    // -------------------------------------------------------------- scales --
+    const int64_t scales_at = q8_scale_offset(P.H_kv, kD, kBS) + 4 * g;
+    bool ok = true;
+    for (int c = 0; c * kChunk < total; ++c) {
+      pages_wait(c * kChunk, ok);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      constexpr int kE = kChunk * kTP / 32;
+      const int n = min(kChunk, total - c * kChunk) * kTP, at = c % kChunks * kChunk * kTP;
+      float ks[kE], vs[kE];
+#pragma unroll
+      for (int k = 0; k < kE; ++k) {
+        ks[k] = vs[k] = 0.f;
+        if (lane + 32 * k < n) {
+          const int64_t off = (int64_t)s_phys[at + lane + 32 * k] * P.block_stride + scales_at;
+          ks[k] = *reinterpret_cast<const float *>(P.k_cache + off);
+          vs[k] = *reinterpret_cast<const float *>(P.v_cache + off);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kE; ++k) {
+        const float v = q8_scale(vs[k]);
+        if (lane + 32 * k < n) s_scale[at + lane + 32 * k] = make_float4(q8_scale(ks[k]), lg2f(v), rcpf(v), 0.f);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&scale_full[c % kChunks]);
+        if ((c + 1) * kChunk <= total) mbar_arrive(&page_empty[c % kChunks]);
+      }
+    }
   } else if (warp == kKWarp || warp == kVWarp) {
     // ------------------------------------------------------ codes to smem --
     auto role = [&](auto is_v) {
@@ -371,14 +387,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
     // One warp per product; all its lanes wait, one issues. f32 accumulators, M =
     // 128; Q K^T of e4m3 codes and terms, P V of e4m3 codes and e5m2 terms, both
     // read across their rows.
-    constexpr uint32_t idesc_qk = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+    constexpr uint32_t idesc_qk = (1u << 4) | ((uint32_t)(Cfg::kSCols >> 3) << 17) | (8u << 24);
     constexpr uint32_t idesc_pv = (1u << 4) | (1u << 10) | (1u << 15) | (1u << 16) | ((uint32_t)(Cfg::kOCols >> 3) << 17) | (8u << 24);
     uint32_t items = 0;   // started
     bool ok = true;
     if (warp == kQkWarp) {
       uint32_t s = 0, round = 0;   // stage, and rounds of the ring
       for (uint32_t u = 0; u < (uint32_t)total; ++u) {
-        const uint32_t x = u & 1, n = u >> 1, pb = n & 1;
+        const uint32_t x = u & 1, n = u >> 1, pb = n % SB;
         pages_wait(u, ok);
         const int flag = s_flag[u % (kChunks * kChunk)];
         if (flag & kFirst) {
@@ -386,17 +402,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
           ++items;
         }
         if (u % kChunk == 0) ok = kl_wait(&scale_full[u / kChunk % kChunks], (u / (kChunk * kChunks)) & 1, abf, P.wait_ns) && ok;
-        // the pipeline's softmax has read the scores of its tile before the last
-        if (n >= 2) ok = kl_wait(&s_free[x][pb], ((n >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
+        // the pipeline's softmax has read the scores that were there
+        if (n >= SB) ok = kl_wait(&s_free[x][pb], ((n / SB) & 1) ^ 1, abf, P.wait_ns) && ok;
         ok = kl_wait(&k_full[s], round & 1, abf, P.wait_ns) && ok;
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
         if (elect_one()) {
           const uint64_t qd = t5_desc(q_smem + ((items - 1) & 1) * Cfg::kQ, 16, 1024);
           const uint64_t kd = t5_desc(k_ring + s * kTile, 16, 1024);
-          const uint32_t d = tb + Cfg::kSCol + (2 * x + pb) * N;
+          const uint32_t d = tb + Cfg::kSCol + (SB * x + pb) * Cfg::kSCols;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)   // 32 head dims per MMA, the hi terms of Q and then the lo terms
+          for (int kk = 0; kk < 8 / Cfg::kSSums; ++kk)   // 32 head dims per MMA, the hi terms of Q and the lo terms
             t5_mma_ss_f8(d, kd + (kk & 3) * 2, qd + (kk >> 2) * (N * 128 / 16) + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
           t5_commit(&k_empty[s]);
           t5_commit(&s_full[x][pb]);
@@ -417,8 +433,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
         const int at = u % (kChunks * kChunk), flag = s_flag[at], zero = s_zero[at];
         pages_done(u);
         if (flag & kFirst) {
-          // O of the item before the last has been read
-          if (items >= 2) ok = kl_wait(&o_free[items & 1], ((items >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
+          // O of the last item in this buffer has been read
+          if (items >= OB) {
+            const uint32_t i = items - OB;
+            ok = kl_wait(&o_free[i & 1], (i >> 1) & 1, abf, P.wait_ns) && ok;
+          }
           ++items;
         }
         ok = kl_wait(&v_full[s], round & 1, abf, P.wait_ns) && ok;
@@ -441,13 +460,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
         if (elect_one()) {
           const uint64_t pd = t5_desc32(p_smem + x * Cfg::kPBytes, Cfg::kAtom, 256);
           const uint64_t vd = t5_desc(v_ring + s * kTile, 16, 1024);
-          const uint32_t d = tb + Cfg::kOCol + (2 * x + ((items - 1) & 1)) * Cfg::kOCols;
+          const uint32_t d = tb + Cfg::kOCol + (OB * x + (items - 1) % OB) * Cfg::kOCols;
           const uint32_t acc = flag & kOwn ? 0u : 1u;
           auto part = [&](int kk) {   // 32 keys
-#pragma unroll
-            for (int e = 0; e < 3 / Cfg::kSums; ++e)
-              t5_mma_ss_f8(d, vd + kk * (32 * kD / 16), pd + e * (Cfg::kTerm / 32 * Cfg::kAtom / 16) + kk * (32 * 32 / 16), idesc_pv,
-                           kk > 0 || e > 0 ? 1u : acc);
+            t5_mma_ss_f8(d, vd + kk * (32 * kD / 16), pd + kk * (32 * 32 / 16), idesc_pv, kk > 0 ? 1u : acc);
           };
           if (parts == kTP / 2) {
 #pragma unroll
@@ -524,9 +540,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
       for (int y = 0; y < X; ++y) {
         if (!done.both && y != done.only) continue;
 #pragma unroll 1
-        for (int e = 0; e < Cfg::kSums; ++e) {
+        for (int e = 0; e < 3; ++e) {
           float v[NC];
-          t5_ldn(lanes + Cfg::kOCol + (2 * y + p) * Cfg::kOCols + e * N + c_first, reinterpret_cast<uint32_t(&)[NC]>(v));
+          t5_ldn(lanes + Cfg::kOCol + (OB * y + done.i % OB) * Cfg::kOCols + e * N + c_first, reinterpret_cast<uint32_t(&)[NC]>(v));
           t5_wait_ld();
           keep_after<NC>(v);
 #pragma unroll
@@ -547,7 +563,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
     };
     for (int u0 = 0; u0 < total && !gone; ++i) {   // u0: the item's first tile
       const int buf = i & 1;
-      const uint32_t o_col = lanes + Cfg::kOCol + (2 * x + (i & 1)) * Cfg::kOCols + c_first;
+      const uint32_t o_col = lanes + Cfg::kOCol + (OB * x + i % OB) * Cfg::kOCols + c_first;
       ok = kl_wait(&q_full[i & 1], (i >> 1) & 1, abf, P.wait_ns) && ok;
       gone = bar_or(bar, 128, !ok);
       if (gone) break;
@@ -563,23 +579,24 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
       named_bar_sync(bar, 128);
       bool opening = true;
       for (int ti = (u0 ^ x) & 1; ti < ntiles; ti += 2, ++n) {
-        const int u = u0 + ti, pb = n & 1;
-        ok = kl_wait(&s_full[x][pb], (n >> 1) & 1, abf, P.wait_ns) && ok;
+        const int u = u0 + ti, pb = n % SB;
+        ok = kl_wait(&s_full[x][pb], (n / SB) & 1, abf, P.wait_ns) && ok;
         const float4 sc = s_scale[u % (kChunk * kChunks) * kTP + (t >> 4)];
         const float ka = sc.x * fabsf(fold);
-        const uint32_t s_col = lanes + Cfg::kSCol + (2 * x + pb) * N + c_first;
+        const uint32_t s_col = lanes + Cfg::kSCol + (SB * x + pb) * Cfg::kSCols + c_first;
         // A tile that ends past the oldest query or holds keys that a window has
         // left: position j sees a key iff 0 <= j - j0 < reach.
         const int key0 = (tile0 + ti) * kTK;
         const bool edge = key0 >= edge0 || key0 < edge1;
         ok = __all_sync(0xffffffffu, ok);
         // (rows with powers of their own: every tile of such an item counts as an edge)
-        if (edge && fold < 0.f && ok) kl_scale_rows<NC, N>(s_col, 1, &s_qf[buf][c_first]);
+        if (edge && fold < 0.f && ok) kl_scale_rows<NC, N>(s_col, Cfg::kSSums, &s_qf[buf][c_first]);
         t5_fence_after();
         float2 y[NC / 2];   // log2 weights, minus the reference
         {
-          uint32_t v[NC];
+          uint32_t v[NC], v1[NC];
           t5_ldn(s_col, v);
+          if constexpr (Cfg::kSSums > 1) t5_ldn(s_col + N, v1);
           const float2 ka2 = make_float2(ka, ka), vc2 = make_float2(sc.y, sc.y);
 #pragma unroll
           for (int k = 0; k < NC; k += 4) {
@@ -589,11 +606,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
           }
           t5_wait_ld();
           keep_after<NC>(reinterpret_cast<float(&)[NC]>(v));
+          if constexpr (Cfg::kSSums > 1) keep_after<NC>(reinterpret_cast<float(&)[NC]>(v1));
           t5_fence_before();
           if (lane == 0) mbar_arrive(&s_free[x][pb]);
 #pragma unroll
-          for (int k = 0; k < NC / 2; ++k)
-            y[k] = __ffma2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), ka2, y[k]);
+          for (int k = 0; k < NC / 2; ++k) {
+            float2 q = make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+            if constexpr (Cfg::kSSums > 1) q = __fadd2_rn(q, make_float2(__uint_as_float(v1[2 * k]), __uint_as_float(v1[2 * k + 1])));
+            y[k] = __ffma2_rn(q, ka2, y[k]);
+          }
         }
         if (edge) {
           const int key = key0 + t, j0 = key - (L - P.n_new);
@@ -653,7 +674,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
             ok = __all_sync(0xffffffffu, kl_wait(&pv_done[x], (n - 1) & 1, abf, P.wait_ns)) && ok;
             t5_fence_after();
 #pragma unroll 1
-            for (int e = 0; e < Cfg::kSums; ++e) {
+            for (int e = 0; e < 3; ++e) {
               float o[NC];
               t5_ldn(o_col + e * N, reinterpret_cast<uint32_t(&)[NC]>(o));
               t5_wait_ld();
@@ -666,15 +687,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
           }
         }
         opening = false;
-        // P V of the pipeline's tile before has read P'
-        if (n >= 1) ok = kl_wait(&pv_done[x], (n - 1) & 1, abf, P.wait_ns) && ok;
         const float2 vi2 = make_float2(sc.z, sc.z);
+        constexpr int kEights = (NC + 7) / 8;   // pieces of eight columns, a half of 16 bytes
+        uint2 piece[kEights][3];
 #pragma unroll
-        for (int c = 0; c < NC; c += 8) {   // eight columns: a half of a 16-byte piece
+        for (int c = 0; c < kEights; ++c) {
           uint32_t ph[4], w0[3], w1[3] = {};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int e = c / 2 + k;
+            const int e = 4 * c + k;
             ph[k] = 0;
             if (e >= NC / 2) continue;
             const float2 p = make_float2(ex2f(y[e].x), ex2f(y[e].y));
@@ -682,12 +703,39 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
             ph[k] = pack2<true>(p.x, p.y);
           }
           cut_weights(ph[0], ph[1], w0);
-          if (NC - c >= 8) cut_weights(ph[2], ph[3], w1);   // (what the columns of padding hold does not matter)
+          if (NC - 8 * c >= 8) cut_weights(ph[2], ph[3], w1);   // (what the columns of padding hold does not matter)
 #pragma unroll
-          for (int e = 0; e < 3; ++e) {
-            const uint32_t col = e * Cfg::kTerm + c_first + c;
-            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(p_row + (col >> 5) * Cfg::kAtom + ((col & 24) ^ swap)), "r"(w0[e]), "r"(w1[e])
-                         : "memory");
+          for (int e = 0; e < 3; ++e) piece[c][e] = make_uint2(w0[e], w1[e]);
+        }
+        auto store = [&](int c, int e) {
+          const uint32_t col = e * N + c_first + 8 * c;
+          asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(p_row + (col >> 5) * Cfg::kAtom + ((col & 24) ^ swap)), "r"(piece[c][e].x),
+                       "r"(piece[c][e].y)
+                       : "memory");
+        };
+        auto store2 = [&](int c, int e) {
+          const uint32_t col = e * N + c_first + 8 * c;
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p_row + (col >> 5) * Cfg::kAtom + ((col & 16) ^ swap)), "r"(piece[c][e].x),
+                       "r"(piece[c][e].y), "r"(piece[c + 1][e].x), "r"(piece[c + 1][e].y)
+                       : "memory");
+        };
+        // P V of the pipeline's tile before has read P'
+        if (n >= 1) ok = kl_wait(&pv_done[x], (n - 1) & 1, abf, P.wait_ns) && ok;
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+          if constexpr (kEights == 1) {
+            store(0, e);
+          } else if constexpr (kEights == 3) {   // (the second warpgroup starts in the middle of 16 bytes)
+            if (w == 0) {
+              store2(0, e);
+              store(2, e);
+            } else {
+              store(0, e);
+              store2(1, e);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kEights; c += 2) store2(c, e);
           }
         }
         fence_proxy_async_shared();
