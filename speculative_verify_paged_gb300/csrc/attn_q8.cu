@@ -44,7 +44,7 @@ constexpr int kRegs = 80, kRegsSoftmax = 96, kRegsOther = 48;
 static_assert(512 * kRegsSoftmax + 32 * (kWarps - 16) * kRegsOther <= 32 * kWarps * kRegs, "registers");
 // A row's reference puts its largest weight at 2^kTop and moves once one exceeds
 // 2^kMove (f16 ends at 65504, which e5m2 takes for 57344 and two smaller terms).
-constexpr float kTop = 10.f, kMove = 15.9f;
+constexpr float kTop = 5.f, kMove = 15.9f;
 constexpr int kOwn = 16;   // of a tile: the first of the sequence in its pipeline here
 
 template <int NC> struct Q8Cfg : KlCfg<NC> {
@@ -88,19 +88,22 @@ __device__ __forceinline__ uint64_t t5_desc32(uint32_t saddr, uint32_t lbo, uint
   return d;
 }
 
-// Four weights (two f16 pairs) as three words of e5m2, largest part first
+// Four weights (two f16 pairs) as three words of e5m2: the upper bytes; 4 times
+// what they leave, cut likewise; 32 times what is left then, rounded. (With a
+// weight below 2^16 the first leaves less than 2^13, the second less than 2^10.)
+constexpr float kCut1 = 0.25f, kCut2 = 0.03125f;
 __device__ __forceinline__ void cut_weights(uint32_t h0, uint32_t h1, uint32_t (&w)[3]) {
-  auto rest = [](uint32_t h) {   // minus its upper byte's value
+  auto rest = [](uint32_t h, float f) {   // minus its upper byte's value, times f
     const uint32_t u = h & 0xFF00FF00u;
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&u));
+    const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&u)), __float2half2_rn(f));
     return *reinterpret_cast<const uint32_t *>(&r);
   };
   w[0] = __byte_perm(h0, h1, 0x7531);
-  h0 = rest(h0);
-  h1 = rest(h1);
+  h0 = rest(h0, 4.f);
+  h1 = rest(h1, 4.f);
   w[1] = __byte_perm(h0, h1, 0x7531);
-  h0 = rest(h0) + 0x00800080u;   // (to nearest; far from carrying into the other half)
-  h1 = rest(h1) + 0x00800080u;
+  h0 = rest(h0, 8.f) + 0x00800080u;   // (to nearest; far from carrying into the other half)
+  h1 = rest(h1, 8.f) + 0x00800080u;
   w[2] = __byte_perm(h0, h1, 0x7531);
 }
 
@@ -403,8 +406,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
         }
         if (u % kChunk == 0) ok = kl_wait(&scale_full[u / kChunk % kChunks], (u / (kChunk * kChunks)) & 1, abf, P.wait_ns) && ok;
         // the pipeline's softmax has read the scores that were there
-        if (n >= SB) ok = kl_wait(&s_free[x][pb], ((n / SB) & 1) ^ 1, abf, P.wait_ns) && ok;
-        ok = kl_wait(&k_full[s], round & 1, abf, P.wait_ns) && ok;
+        // (before there are any, the phase that counts as done)
+        ok = kl_wait2(&k_full[s], round & 1, &s_free[x][pb], ((n / SB) & 1) ^ 1, abf, P.wait_ns) && ok;
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
         if (elect_one()) {
@@ -542,11 +545,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
 #pragma unroll 1
         for (int e = 0; e < 3; ++e) {
           float v[NC];
+          const float cut = e == 0 ? 1.f : e == 1 ? kCut1 : kCut2;
           t5_ldn(lanes + Cfg::kOCol + (OB * y + done.i % OB) * Cfg::kOCols + e * N + c_first, reinterpret_cast<uint32_t(&)[NC]>(v));
           t5_wait_ld();
           keep_after<NC>(v);
 #pragma unroll
-          for (int k = 0; k < NC; ++k) o[k] = fmaf(v[k], s_fin[x][y][c_first + k], o[k]);
+          for (int k = 0; k < NC; ++k) o[k] = fmaf(v[k] * cut, s_fin[x][y][c_first + k], o[k]);
         }
       }
 #pragma unroll
@@ -560,6 +564,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
       t5_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[p]);
+      __syncwarp();
     };
     for (int u0 = 0; u0 < total && !gone; ++i) {   // u0: the item's first tile
       const int buf = i & 1;
@@ -609,6 +614,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
           if constexpr (Cfg::kSSums > 1) keep_after<NC>(reinterpret_cast<float(&)[NC]>(v1));
           t5_fence_before();
           if (lane == 0) mbar_arrive(&s_free[x][pb]);
+          __syncwarp();   // (what follows takes whole warps)
 #pragma unroll
           for (int k = 0; k < NC / 2; ++k) {
             float2 q = make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
@@ -745,6 +751,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
           mbar_arrive(&p_full[x]);
           if (u % kChunk >= kChunk - 2) mbar_arrive(&page_empty[u / kChunk % kChunks]);
         }
+        __syncwarp();
         if (done.pending) finish();
       }
       if (gone) break;
@@ -769,6 +776,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
         __syncwarp();
         if (lane == 0) mbar_arrive(&ml_full[i & 1]);
       }
+      __syncwarp();
       if (x == (i & 1))
         done = {true, (it.w & kWhole) != 0, ntiles > 1, u0 & 1, i, 2 * (int64_t)blockIdx.x + (it.w & kOpening ? 0 : 1)};
       u0 += ntiles;

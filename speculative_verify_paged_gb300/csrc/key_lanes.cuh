@@ -337,6 +337,14 @@ __device__ __forceinline__ bool kl_wait(uint64_t *bar, uint32_t phase, volatile 
   return false;
 }
 
+// Both at once: the first tries overlap.
+__device__ __forceinline__ bool kl_wait2(uint64_t *a, uint32_t phase_a, uint64_t *b, uint32_t phase_b, volatile int *abort_flag,
+                                         uint64_t limit_ns) {
+  const bool da = mbar_try_wait(a, phase_a), db = mbar_try_wait(b, phase_b);
+  if (da && db) return true;
+  return (da || kl_wait(a, phase_a, abort_flag, limit_ns)) && (db || kl_wait(b, phase_b, abort_flag, limit_ns));
+}
+
 // true in one lane of a converged warp, in a form that keeps the code around it
 // uniform for the compiler
 __device__ __forceinline__ bool elect_one() {
