@@ -36,36 +36,33 @@ namespace sv {
 namespace {
 
 constexpr int kTile = kTK * kD;            // bytes of a tile of K or V
-constexpr int kLanes = 2;                  // pipelines that take the tiles in turn
-constexpr int kWarps = 24;
-constexpr int kPageWarp = 16, kKWarp = 17, kVWarp = 18, kQkWarp = 19, kPvWarp = 20, kQWarp = 21, kScaleWarp = 22;
-// Registers a thread: at the launch, of the softmax warps and of the others.
-constexpr int kRegs = 80, kRegsSoftmax = 96, kRegsOther = 48;
-static_assert(512 * kRegsSoftmax + 32 * (kWarps - 16) * kRegsOther <= 32 * kWarps * kRegs, "registers");
+constexpr int kWarps = 16;
+constexpr int kPageWarp = 8, kKWarp = 9, kVWarp = 10, kQkWarp = 11, kPvWarp = 12, kQWarp = 13, kScaleWarp = 14;
+// Registers a thread: the softmax warps take what the others leave.
+constexpr int kRegs = 128, kRegsSoftmax = 192, kRegsOther = 64;
+static_assert(256 * kRegsSoftmax + 32 * (kWarps - 8) * kRegsOther <= 32 * kWarps * kRegs, "registers");
 // A row's reference puts its largest weight at 2^kTop and moves once one exceeds
 // 2^kMove (f16 ends at 65504, which e5m2 takes for 57344 and two smaller terms).
 constexpr float kTop = 5.f, kMove = 15.9f;
-constexpr int kOwn = 16;   // of a tile: the first of the sequence in its pipeline here
 
 template <int NC> struct Q8Cfg : KlCfg<NC> {
   using KlCfg<NC>::kN;
   using KlCfg<NC>::kQ;
-  // The terms of Q, and those of P', side by side are the columns of one product
-  // with several sums: what an MMA of few columns costs is its other operand (16
-  // or 32 columns 41 cycles, 48 45, 96 57, 144 72), 4 KB from shared memory, whose
-  // bandwidth the kernel is short of. Tensor memory has room for kSSums sums in
-  // kSB buffers of S a pipeline, and for three in kOB of O.
-  static constexpr int kSSums = kN <= 48 ? 2 : 1, kSCols = kSSums * kN, kSB = kN <= 16 ? 2 : 1;
-  static constexpr int kOCols = 3 * kN, kOB = kN <= 32 ? 2 : 1;
+  using KlCfg<NC>::kT;
+  // The terms of P', and where tensor memory has room those of Q, side by side are
+  // the columns of one product with several sums: what an MMA of few columns costs
+  // is its other operand (16 or 32 columns 41 cycles, 48 45, 96 57, 144 72), 4 KB
+  // from shared memory, whose bandwidth the kernel is short of.
+  static constexpr int kSSums = kN <= 32 ? 2 : 1, kSCols = kSSums * kN, kOCols = 3 * kN;
   // P' lies in atoms of 32 columns, 32 bytes a key.
   static constexpr int kAtom = kTK * 32, kPBytes = (kOCols + 31) / 32 * kAtom;
-  static constexpr int kStatic = 7168 + 144 * kN;                  // static shared memory, at most
-  static constexpr int kFixed = 1024 + 2 * kQ + kLanes * kPBytes;
+  static constexpr int kStatic = 7680 + 80 * kN;                   // static shared memory, at most
+  static constexpr int kFixed = 1024 + 2 * kQ + 2 * kT * kPBytes;
   static constexpr int kAll = (227 * 1024 - kStatic - kFixed) / kTile;   // stages that fit
   static constexpr int kVS = (kAll + 1) / 2 < 5 ? (kAll + 1) / 2 : 5, kKS = kAll - kVS < 5 ? kAll - kVS : 5;
   static constexpr int kSmem = kFixed + (kKS + kVS) * kTile;
-  static constexpr uint32_t kSCol = 0, kOCol = kLanes * kSB * kSCols;
-  static_assert(kOCol + kLanes * kOB * kOCols <= 512, "TMEM columns");
+  static constexpr uint32_t kSCol = 0, kOCol = 2 * kT * kSCols;   // (two buffers each)
+  static_assert(kOCol + 2 * kOCols <= 512, "TMEM columns");
   static_assert(kKS >= 2 && kVS >= 2, "shared memory");
 };
 
@@ -88,62 +85,57 @@ __device__ __forceinline__ uint64_t t5_desc32(uint32_t saddr, uint32_t lbo, uint
   return d;
 }
 
-// Four weights (two f16 pairs) as three words of e5m2: the upper bytes; 4 times
-// what they leave, cut likewise; 32 times what is left then, rounded. (With a
-// weight below 2^16 the first leaves less than 2^13, the second less than 2^10.)
-constexpr float kCut1 = 0.25f, kCut2 = 0.03125f;
+// Four weights (two f16 pairs) as three words of e5m2: the upper bytes, those of
+// what they leave, and 32 times what is left then, rounded. (With a weight below
+// 2^16 the first leaves less than 2^13, the second less than 2^10.)
+constexpr float kCut = 0.03125f;
 __device__ __forceinline__ void cut_weights(uint32_t h0, uint32_t h1, uint32_t (&w)[3]) {
-  auto rest = [](uint32_t h, float f) {   // minus its upper byte's value, times f
+  auto rest = [](uint32_t h) {   // minus its upper byte's value
     const uint32_t u = h & 0xFF00FF00u;
-    const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&u)), __float2half2_rn(f));
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&u));
     return *reinterpret_cast<const uint32_t *>(&r);
   };
+  auto last = [](uint32_t h) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&h), __float2half2_rn(32.f));
+    return *reinterpret_cast<const uint32_t *>(&r) + 0x00800080u;   // (to nearest; far from carrying into the other half)
+  };
   w[0] = __byte_perm(h0, h1, 0x7531);
-  h0 = rest(h0, 4.f);
-  h1 = rest(h1, 4.f);
+  h0 = rest(h0);
+  h1 = rest(h1);
   w[1] = __byte_perm(h0, h1, 0x7531);
-  h0 = rest(h0, 8.f) + 0x00800080u;   // (to nearest; far from carrying into the other half)
-  h1 = rest(h1, 8.f) + 0x00800080u;
-  w[2] = __byte_perm(h0, h1, 0x7531);
+  w[2] = __byte_perm(last(rest(h0)), last(rest(h1)), 0x7531);
 }
 
-// Two pipelines take the tiles in turn, each with its own scores, weights,
-// references and sums: a tile's way through the softmax is a chain of waits, and
-// two of them in flight hide each other's. Warps 0-7 and 8-15: their softmax (a
-// key per thread; each warpgroup half of the query rows, or the first all of up
-// to 8). The pipelines join their sums at a sequence's end, in the epilogue (a
-// head dim per thread), which they do in turn. 16: block numbers and flags of the
-// tiles ahead. 17, 18: copy the K and V codes. 19: issues Q K^T, owns the 512 TMEM
-// columns. 20: issues P V. 21: Q of the next sequence. 22: the blocks' scales.
+// Warps 0-3 and 4-7: softmax (a key per thread and tile; each warpgroup half of
+// the query rows, or the first all of up to 8), later the epilogue (a head dim
+// per thread). 8: block numbers and flags of the tiles ahead. 9, 10: copy the K
+// and V codes. 11: issues Q K^T, owns the 512 TMEM columns. 12: issues P V. 13: Q
+// of the next sequence. 14: the blocks' scales.
 template <int NC>
 __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_constant__ KlParams P, const __grid_constant__ Q8Maps M) {
   using Cfg = Q8Cfg<NC>;
-  constexpr int N = Cfg::kN, CP = Cfg::kCols, KS = Cfg::kKS, VS = Cfg::kVS, X = kLanes, SB = Cfg::kSB, OB = Cfg::kOB;
+  constexpr int N = Cfg::kN, CP = Cfg::kCols, T = Cfg::kT, KS = Cfg::kKS, VS = Cfg::kVS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t page_full[kChunks], page_empty[kChunks], scale_full[kChunks];
   __shared__ int s_phys[kChunks * kChunk * kTP];   // blocks of the tiles ahead
   __shared__ __align__(16) float4 s_scale[kChunks * kChunk * kTP];   // their scales: of K, log2 of V's, 1 / V's
-  __shared__ int s_flag[kChunks * kChunk];   // kFirst, kLast, kOwn, blocks of the tile << 8
+  __shared__ int s_flag[kChunks * kChunk];   // kFirst, kLast, kEnd, kSecond, blocks of the tile << 8
   // rows of V that no query sees: [z0, z1) and from z2 on, z0 | z1 << 8 | z2 << 16
   __shared__ int s_zero[kChunks * kChunk];
   __shared__ __align__(8) uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS];
-  __shared__ __align__(8) uint64_t s_full[X][SB], s_free[X][SB], p_full[X], pv_done[X];
-  __shared__ __align__(8) uint64_t q_full[2], ml_full[2], o_done[2], o_free[2], drain[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], q_empty[2], o_free[2], drain[2];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ int4 s_work;
   // per row of the items in flight: position (0 .. n_new - 1), row of q and out, its own power of two; per item the
   // power of two that undoes Q's scaling (-1: the rows have their own)
-  __shared__ __align__(16) float s_qf[2][N];
-  __shared__ __align__(16) int s_pos[2][N];
-  __shared__ int s_row[2][N];
-  __shared__ float s_fold[2];
-  __shared__ __align__(16) int4 s_item[2];   // first tile, tiles, length in span coordinates, kWhole | kOpening
-  // per pipeline: minus the reference; what it last moved by, as a power and a factor
-  __shared__ __align__(16) float s_nb[X][N], s_by[X][N], s_a[X][N];
-  __shared__ float s_max[16][NC];
-  __shared__ __align__(8) float2 s_ml[2][X][N];   // per item (its parity) and pipeline: reference and sum of weights
-  __shared__ float s_fin[X][X][N];                // of a pipeline's epilogue: the pipelines' factors
+  __shared__ __align__(16) float s_qf[3][N];
+  __shared__ __align__(16) int s_pos[3][N];
+  __shared__ int s_row[3][N];
+  __shared__ float s_fold[3];
+  __shared__ __align__(16) int4 s_item[3];   // first tile, tiles, length in span coordinates, kWhole | kOpening
+  __shared__ __align__(16) float s_nb[N], s_by[N], s_a[N];   // minus the reference; what it last moved by, as a power and a factor
+  __shared__ float s_max[8][NC], s_red[8][NC], s_fin[2][N];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Hp = P.H_kv * P.RG;
@@ -151,7 +143,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
   const int g = gp / P.RG, row0 = (gp % P.RG) * P.Rg;
   const int rows = min(P.Rg, P.R - row0);       // live rows of this CTA
   const int live0 = kl_first(rows);             // of the first softmax warpgroup
-  const int groups = live0 < rows ? 2 : 1;      // warpgroups of a pipeline
+  const int softmax_warps = live0 < rows ? 8 : 4;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t q_smem = smem_u32(smem);
   const uint32_t k_ring = q_smem + 2 * Cfg::kQ, v_ring = k_ring + KS * kTile;
@@ -169,7 +161,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
     for (int k = 0; k < kChunks; ++k) {
       mbar_init(&page_full[k], 1);
       mbar_init(&scale_full[k], 1);
-      mbar_init(&page_empty[k], 5 + 4 * X * groups);   // the K, V, MMA and scale warps, and those that read the scales
+      mbar_init(&page_empty[k], 5 + softmax_warps);   // the K, V, MMA and scale warps, and those that read the scales
     }
     for (int k = 0; k < KS; ++k) {
       mbar_init(&k_full[k], 1);
@@ -179,20 +171,16 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
       mbar_init(&v_full[k], 1);
       mbar_init(&v_empty[k], 1);
     }
-    for (int x = 0; x < X; ++x) {
-      for (int k = 0; k < SB; ++k) {
-        mbar_init(&s_full[x][k], 2);   // Q K^T (its commit), and the issuing lane itself, which has seen the scales
-        mbar_init(&s_free[x][k], 4 * groups);
-      }
-      mbar_init(&p_full[x], 4 * groups);
-      mbar_init(&pv_done[x], 1);
-    }
     for (int k = 0; k < 2; ++k) {
       mbar_init(&drain[k], 1);
       mbar_init(&q_full[k], 1);
-      mbar_init(&ml_full[k], X * groups);
-      mbar_init(&o_done[k], 1);
-      mbar_init(&o_free[k], 4 * groups);
+      mbar_init(&q_empty[k], 1);
+      mbar_init(&o_free[k], softmax_warps);
+      // Q K^T of the step (its commit, and the issuing lane itself, which has seen
+      // the scales), and P V of the step before the last
+      mbar_init(&s_full[k], 3);
+      mbar_init(&p_full[k], softmax_warps);
+      mbar_init(&pv_done[k], 1);
     }
     abort_flag = 0;
     fence_mbarrier_init();
@@ -208,8 +196,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
   const int4 work = s_work;
   const int total = work.z;   // tiles of this CTA
   volatile int *abf = &abort_flag;
-  // every stage, buffer and phase below follows the CTA's running tile count u: tile u
-  // is the (u / 2)-th of pipeline u % 2
+  // every stage, buffer and phase below follows the CTA's running tile count u
 
   // Waits for the chunk that tile u opens; after a chunk's last tile a warp hands
   // it back.
@@ -263,7 +250,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
         if (lane < n) {
           const int tt = ti + lane, at = c % kChunks * kChunk + filled + lane;
           const int key0 = (it.tile0 + tt) * kTK, nv = min(kTP, it.span.nblk - (it.tile0 + tt) * kTP);
-          s_flag[at] = (tt == 0 ? kFirst : 0) | (tt < X ? kOwn : 0) | (tt == it.ntiles - 1 ? kLast : 0) | nv << 8;
+          s_flag[at] = (tt == 0 ? kFirst : 0) | (tt == it.ntiles - 1 ? kLast | kEnd : 0) | (tt % T == T - 1 ? kEnd : 0) |
+                       (tt % T ? kSecond : 0) | nv << 8;
           int z0 = 0, z1 = 0;
           if (P.window > 0) {   // between the sinks and the oldest query's window
             z0 = min(max(P.sinks - key0, 0), kTK);
@@ -353,9 +341,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
     KlItem it;
     int i = 0;
     while (kl_next(P, wk, it)) {
-      const int buf = i & 1;
-      // the epilogue of the item before the last: both pipelines are past it
-      const bool ok = i < 2 || kl_wait(&o_free[buf], ((i >> 1) & 1) ^ 1, abf, P.wait_ns);
+      const int buf = i & 1, row = i % 3;
+      // the buffer after Q K^T of the item before the last, the rows after the
+      // epilogue of the one before that
+      bool ok = i < 2 || kl_wait(&q_empty[buf], ((i >> 1) & 1) ^ 1, abf, P.wait_ns);
+      if (i >= 3) ok = kl_wait(&o_free[buf ^ 1], ((i - 3) >> 1) & 1, abf, P.wait_ns) && ok;
       if (!__all_sync(0xffffffffu, ok)) break;
       const int64_t ent = (int64_t)it.b * Hp + gp;
       const float *qs = P.ws_qs + ent * (2 * N + 4);
@@ -364,14 +354,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
         const int w = col / CP, c = col - w * CP;
         const int r = row0 + (c < (w ? rows - live0 : live0) ? w * live0 + c : 0);   // (padding: any)
         const int j = r / P.G;
-        s_pos[buf][col] = j;
-        s_row[buf][col] = (it.b * P.n_new + j) * P.H_q + g * P.G + (r - j * P.G);
+        s_pos[row][col] = j;
+        s_row[row][col] = (it.b * P.n_new + j) * P.H_q + g * P.G + (r - j * P.G);
       }
       if (fold < 0.f)
-        for (int col = lane; col < N; col += 32) s_qf[buf][col] = qs[N + 4 + col];
+        for (int col = lane; col < N; col += 32) s_qf[row][col] = qs[N + 4 + col];
       if (lane == 0) {
-        s_fold[buf] = fold;
-        s_item[buf] = make_int4(it.tile0, it.ntiles, it.span.L, (it.whole ? kWhole : 0) | (it.first ? kOpening : 0));
+        s_fold[row] = fold;
+        s_item[row] = make_int4(it.tile0, it.ntiles, it.span.L, (it.whole ? kWhole : 0) | (it.first ? kOpening : 0));
       }
       __syncwarp();
       if (lane == 0) {
@@ -392,12 +382,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
     // read across their rows.
     constexpr uint32_t idesc_qk = (1u << 4) | ((uint32_t)(Cfg::kSCols >> 3) << 17) | (8u << 24);
     constexpr uint32_t idesc_pv = (1u << 4) | (1u << 10) | (1u << 15) | (1u << 16) | ((uint32_t)(Cfg::kOCols >> 3) << 17) | (8u << 24);
-    uint32_t items = 0;   // started
+    uint32_t items = 0, step = 0;   // items started, steps done
     bool ok = true;
+    uint32_t s = 0, round = 0;      // stage, and rounds of the ring
     if (warp == kQkWarp) {
-      uint32_t s = 0, round = 0;   // stage, and rounds of the ring
       for (uint32_t u = 0; u < (uint32_t)total; ++u) {
-        const uint32_t x = u & 1, n = u >> 1, pb = n % SB;
+        const uint32_t pb = step & 1;
         pages_wait(u, ok);
         const int flag = s_flag[u % (kChunks * kChunk)];
         if (flag & kFirst) {
@@ -405,66 +395,69 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
           ++items;
         }
         if (u % kChunk == 0) ok = kl_wait(&scale_full[u / kChunk % kChunks], (u / (kChunk * kChunks)) & 1, abf, P.wait_ns) && ok;
-        // the pipeline's softmax has read the scores that were there
-        // (before there are any, the phase that counts as done)
-        ok = kl_wait2(&k_full[s], round & 1, &s_free[x][pb], ((n / SB) & 1) ^ 1, abf, P.wait_ns) && ok;
+        // the softmax of the step before the last has read the S buffers
+        // (before there is one, the phase that counts as done)
+        if (!(flag & kSecond)) ok = kl_wait2(&k_full[s], round & 1, &p_full[pb], ((step >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
+        else ok = kl_wait(&k_full[s], round & 1, abf, P.wait_ns) && ok;
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
         if (elect_one()) {
           const uint64_t qd = t5_desc(q_smem + ((items - 1) & 1) * Cfg::kQ, 16, 1024);
           const uint64_t kd = t5_desc(k_ring + s * kTile, 16, 1024);
-          const uint32_t d = tb + Cfg::kSCol + (SB * x + pb) * Cfg::kSCols;
+          const uint32_t d = tb + Cfg::kSCol + (T * pb + (flag & kSecond ? 1 : 0)) * Cfg::kSCols;
 #pragma unroll
           for (int kk = 0; kk < 8 / Cfg::kSSums; ++kk)   // 32 head dims per MMA, the hi terms of Q and the lo terms
             t5_mma_ss_f8(d, kd + (kk & 3) * 2, qd + (kk >> 2) * (N * 128 / 16) + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
           t5_commit(&k_empty[s]);
-          t5_commit(&s_full[x][pb]);
-          mbar_arrive(&s_full[x][pb]);
+          if (flag & kEnd) {
+            t5_commit(&s_full[pb]);
+            mbar_arrive(&s_full[pb]);
+          }
+          if (flag & kLast) t5_commit(&q_empty[(items - 1) & 1]);
         }
         __syncwarp();
         pages_done(u);
+        if (flag & kEnd) ++step;
         if (++s == KS) {
           s = 0;
           ++round;
         }
       }
     } else {
-      uint32_t s = 0, round = 0;
+      if (lane < 2) mbar_arrive(&s_full[lane]);   // (no P V before the first steps)
       for (uint32_t u = 0; u < (uint32_t)total; ++u) {
-        const uint32_t x = u & 1, n = u >> 1;
+        const uint32_t pb = step & 1;
         pages_wait(u, ok);
         const int at = u % (kChunks * kChunk), flag = s_flag[at], zero = s_zero[at];
         pages_done(u);
         if (flag & kFirst) {
-          // O of the last item in this buffer has been read
-          if (items >= OB) {
-            const uint32_t i = items - OB;
-            ok = kl_wait(&o_free[i & 1], (i >> 1) & 1, abf, P.wait_ns) && ok;
-          }
+          // O of the item before the last has been read
+          if (items >= 2) ok = kl_wait(&o_free[items & 1], ((items >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
           ++items;
         }
-        ok = kl_wait(&v_full[s], round & 1, abf, P.wait_ns) && ok;
         const int parts = ((flag >> 8) + 1) >> 1;   // of 32 keys that hold any
         const int z0 = zero & 255, z1 = (zero >> 8) & 255, z2 = zero >> 16;
-        if (__all_sync(0xffffffffu, ok) && (z1 > 0 || z2 < kTK)) {
+        if (z1 > 0 || z2 < kTK) {
           // rows that no query sees become zeros: whatever they hold (NaN codes, or what an
           // earlier tile left), 0 times it would not do
+          ok = __all_sync(0xffffffffu, kl_wait(&v_full[s], round & 1, abf, P.wait_ns)) && ok;
           const int n1 = (z1 - z0) * 8, n2 = (parts * 32 - z2) * 8;
-          for (int i = lane; i < n1 + n2; i += 32)
+          for (int i = lane; ok && i < n1 + n2; i += 32)
             asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(v_ring + s * kTile + (i < n1 ? z0 * kD + i * 16 : z2 * kD + (i - n1) * 16)),
                          "r"(0u)
                          : "memory");
           fence_proxy_async_shared();
           __syncwarp();
         }
-        ok = kl_wait(&p_full[x], n & 1, abf, P.wait_ns) && ok;
+        if (!(flag & kSecond)) ok = kl_wait2(&v_full[s], round & 1, &p_full[pb], (step >> 1) & 1, abf, P.wait_ns) && ok;
+        else ok = kl_wait(&v_full[s], round & 1, abf, P.wait_ns) && ok;
         if (!__all_sync(0xffffffffu, ok)) break;
         t5_fence_after();
         if (elect_one()) {
-          const uint64_t pd = t5_desc32(p_smem + x * Cfg::kPBytes, Cfg::kAtom, 256);
+          const uint64_t pd = t5_desc32(p_smem + (T * pb + (flag & kSecond ? 1 : 0)) * Cfg::kPBytes, Cfg::kAtom, 256);
           const uint64_t vd = t5_desc(v_ring + s * kTile, 16, 1024);
-          const uint32_t d = tb + Cfg::kOCol + (OB * x + (items - 1) % OB) * Cfg::kOCols;
-          const uint32_t acc = flag & kOwn ? 0u : 1u;
+          const uint32_t d = tb + Cfg::kOCol + ((items - 1) & 1) * Cfg::kOCols;
+          const uint32_t acc = flag & kFirst ? 0u : 1u;
           auto part = [&](int kk) {   // 32 keys
             t5_mma_ss_f8(d, vd + kk * (32 * kD / 16), pd + kk * (32 * 32 / 16), idesc_pv, kk > 0 ? 1u : acc);
           };
@@ -476,10 +469,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
             for (int kk = 0; kk < parts; ++kk) part(kk);
           }
           t5_commit(&v_empty[s]);
-          t5_commit(&pv_done[x]);
-          if (flag & kLast) t5_commit(&o_done[(items - 1) & 1]);   // (both pipelines': they are issued in order)
+          if (flag & kEnd) {
+            t5_commit(&pv_done[pb]);
+            t5_commit(&s_full[pb]);   // the P' buffers are free: part of what the softmax of the step after next waits for
+          }
         }
         __syncwarp();
+        if (flag & kEnd) ++step;
         if (++s == VS) {
           s = 0;
           ++round;
@@ -493,160 +489,167 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
       __syncwarp();
       if (!mbar_wait(dr, 0) && lane == 0) atomic_or_status(P.status, SV_DEV_TIMEOUT);
     }
-  } else if (warp < 16 && ((warp >> 2) & 1) < groups) {
+  } else if (warp < softmax_warps) {
     // ------------------------------------------------------------- softmax --
     regs_inc<kRegsSoftmax>();
-    const int x = warp >> 3, w = (warp >> 2) & 1, t = tid & 127;
+    const int w = warp >> 2, t = tid & 127;
     const int c_first = w * CP;                 // this warpgroup's columns
     const int live = w ? rows - live0 : live0;
-    const int bar = 1 + (warp >> 2);
+    const int bar = 1 + w;
     const uint32_t lanes = tb + ((uint32_t)((warp & 3) * 32) << 16);
     // this key's row of P', and what its two 16-byte pieces are exchanged by
-    const uint32_t p_row = p_smem + x * Cfg::kPBytes + t * 32, swap = (t << 2) & 16;
-    float *const nbs = s_nb[x] + c_first, *const bys = s_by[x] + c_first, *const as = s_a[x] + c_first;
-    int i = 0;                   // items done
-    uint32_t n = 0;              // tiles of this pipeline done
+    const uint32_t p_row = p_smem + t * 32, swap = (t << 2) & 16;
+    int u = 0, i = 0;            // tiles and items done
+    uint32_t step = 0;
     // A wait that gave up (ok false) only shows at the warpgroup's next vote, so
     // that its four warps leave together.
-    bool ok = true, gone = false;
-    // The epilogue of an item, a head dim per thread, once the other pipeline's sums
-    // and the last P V are there; it is taken after the next item's first tile, which
-    // hides that P V.
-    struct { bool pending, whole, both; int only, i; int64_t ent; } done = {false, false, false, 0, 0, 0};
+    bool ok = true;
+    // The epilogue's second part, a head dim per thread: O of an item, once its
+    // last P V is done; it is taken after the next item's first step, which hides
+    // that P V.
+    struct { bool pending, whole; uint32_t step; int i; int64_t ent; } done = {false, false, 0, 0, 0};
     auto finish = [&] {
       done.pending = false;
-      const int p = done.i & 1;
-      ok = kl_wait(&ml_full[p], (done.i >> 1) & 1, abf, P.wait_ns) && ok;
-      ok = kl_wait(&o_done[p], (done.i >> 1) & 1, abf, P.wait_ns) && ok;
-      if (t < live) {
-        const float2 a = s_ml[p][0][c_first + t], b = s_ml[p][1][c_first + t];
-        const float m = fmaxf(a.x, b.x), fa = ex2f(a.x - m), fb = ex2f(b.x - m), l = fmaf(a.y, fa, b.y * fb);
-        // (a row of NaN stays NaN; l is 0 only for a row without keys, which a query that sees itself never is)
-        const float inv = done.whole ? 1.f / l : 1.f;
-        s_fin[x][0][c_first + t] = fa * inv;
-        s_fin[x][1][c_first + t] = fb * inv;
-        if (!done.whole) {
-          const int64_t e = done.ent * P.Rg + w * live0 + t;
-          P.ws_ml[2 * e] = m;
-          P.ws_ml[2 * e + 1] = l;
-        }
-      }
-      if (bar_or(bar, 128, !ok)) {
-        ok = false;
-        return;
-      }
+      ok = __all_sync(0xffffffffu, kl_wait(&pv_done[done.step & 1], (done.step >> 1) & 1, abf, P.wait_ns)) && ok;
+      if (!ok) return;
       t5_fence_after();
-      float o[NC];
-#pragma unroll
-      for (int k = 0; k < NC; ++k) o[k] = 0.f;
-#pragma unroll 1
-      for (int y = 0; y < X; ++y) {
-        if (!done.both && y != done.only) continue;
-#pragma unroll 1
-        for (int e = 0; e < 3; ++e) {
-          float v[NC];
-          const float cut = e == 0 ? 1.f : e == 1 ? kCut1 : kCut2;
-          t5_ldn(lanes + Cfg::kOCol + (OB * y + done.i % OB) * Cfg::kOCols + e * N + c_first, reinterpret_cast<uint32_t(&)[NC]>(v));
-          t5_wait_ld();
-          keep_after<NC>(v);
-#pragma unroll
-          for (int k = 0; k < NC; ++k) o[k] = fmaf(v[k] * cut, s_fin[x][y][c_first + k], o[k]);
-        }
-      }
+      float o[NC], o1[NC], o2[NC];
+      const uint32_t at = lanes + Cfg::kOCol + (done.i & 1) * Cfg::kOCols + c_first;
+      t5_ldn(at, reinterpret_cast<uint32_t(&)[NC]>(o));
+      t5_ldn(at + N, reinterpret_cast<uint32_t(&)[NC]>(o1));
+      t5_ldn(at + 2 * N, reinterpret_cast<uint32_t(&)[NC]>(o2));
+      t5_wait_ld();
+      keep_after<NC>(o);
+      keep_after<NC>(o1);
+      keep_after<NC>(o2);
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
         if (k >= live) break;
+        const float x = fmaf(o2[k], kCut, o[k] + o1[k]) * s_fin[done.i & 1][c_first + k];
         if (done.whole)
-          static_cast<__nv_bfloat16 *>(P.out)[(int64_t)s_row[p][c_first + k] * kD + t] = __float2bfloat16_rn(o[k]);
+          static_cast<__nv_bfloat16 *>(P.out)[(int64_t)s_row[done.i % 3][c_first + k] * kD + t] = __float2bfloat16_rn(x);
         else
-          P.ws_acc[(done.ent * P.Rg + w * live0 + k) * kD + t] = o[k];
+          P.ws_acc[(done.ent * P.Rg + w * live0 + k) * kD + t] = x;
       }
       t5_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&o_free[p]);
-      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free[done.i & 1]);
     };
-    for (int u0 = 0; u0 < total && !gone; ++i) {   // u0: the item's first tile
-      const int buf = i & 1;
-      const uint32_t o_col = lanes + Cfg::kOCol + (OB * x + i % OB) * Cfg::kOCols + c_first;
-      ok = kl_wait(&q_full[i & 1], (i >> 1) & 1, abf, P.wait_ns) && ok;
-      gone = bar_or(bar, 128, !ok);
-      if (gone) break;
+    while (u < total) {
+      const int buf = i % 3;
+      const uint32_t o_col = lanes + Cfg::kOCol + (i & 1) * Cfg::kOCols + c_first;
+      ok = __all_sync(0xffffffffu, kl_wait(&q_full[i & 1], (i >> 1) & 1, abf, P.wait_ns)) && ok;
       const float fold = P.scale_log2 * s_fold[buf];
       const int4 it = s_item[buf];
       const int tile0 = it.x, ntiles = it.y, L = it.z;
-      const int edge0 = fold < 0.f ? INT_MIN : L - P.n_new - kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
-      if (t < NC) nbs[t] = t < live ? 0.f : -kUnset;   // (padding has no weight)
+      const int edge0 = fold < 0.f ? INT_MIN : L - P.n_new - T * kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
+      if (t < NC) s_nb[c_first + t] = t < live ? 0.f : -kUnset;   // (padding has no weight)
       bool open = true, unset = t < live;   // rows that have met no key; this thread's row among them
       float2 l2[NC / 2];
 #pragma unroll
       for (int k = 0; k < NC / 2; ++k) l2[k] = make_float2(0.f, 0.f);
-      named_bar_sync(bar, 128);
-      bool opening = true;
-      for (int ti = (u0 ^ x) & 1; ti < ntiles; ti += 2, ++n) {
-        const int u = u0 + ti, pb = n % SB;
-        ok = kl_wait(&s_full[x][pb], (n / SB) & 1, abf, P.wait_ns) && ok;
-        const float4 sc = s_scale[u % (kChunk * kChunks) * kTP + (t >> 4)];
-        const float ka = sc.x * fabsf(fold);
-        const uint32_t s_col = lanes + Cfg::kSCol + (SB * x + pb) * Cfg::kSCols + c_first;
-        // A tile that ends past the oldest query or holds keys that a window has
+      bool gone = bar_or(bar, 128, !ok);
+      for (int ti = 0; ti < ntiles && !gone; ++step) {
+        const int nt = min(ntiles - ti, T);
+        // S of this step, and with it the scales and P' buffers that P V two
+        // steps ago has read
+        const int pb = step & 1;
+        ok = kl_wait(&s_full[pb], (step >> 1) & 1, abf, P.wait_ns) && ok;
+        float ka[T], vc[T], vi[T];
+#pragma unroll
+        for (int h = 0; h < T; ++h) {   // this thread's keys
+          const float4 s = s_scale[(u + h) % (kChunk * kChunks) * kTP + (t >> 4)];   // (of an absent tile: any)
+          ka[h] = s.x * fabsf(fold);
+          vc[h] = s.y;
+          vi[h] = s.z;
+        }
+        const uint32_t s_col = lanes + Cfg::kSCol + T * pb * Cfg::kSCols + c_first;
+        // A step that ends past the oldest query or holds keys that a window has
         // left: position j sees a key iff 0 <= j - j0 < reach.
         const int key0 = (tile0 + ti) * kTK;
         const bool edge = key0 >= edge0 || key0 < edge1;
+        int j0[T] = {};
+        uint32_t reach[T] = {};
+        if (edge) {
+#pragma unroll
+          for (int h = 0; h < T; ++h) {
+            const int key = key0 + h * kTK + t;
+            j0[h] = key - (L - P.n_new);
+            reach[h] = P.window > 0 && key >= P.sinks ? (uint32_t)P.window : 0x80000000u;
+          }
+          // Rows with powers of their own: every step of such an item counts as an edge.
+          ok = __all_sync(0xffffffffu, ok);
+          if (fold < 0.f && ok) kl_scale_rows<NC, N>(s_col, nt * Cfg::kSSums, &s_qf[buf][c_first]);
+        }
         ok = __all_sync(0xffffffffu, ok);
-        // (rows with powers of their own: every tile of such an item counts as an edge)
-        if (edge && fold < 0.f && ok) kl_scale_rows<NC, N>(s_col, Cfg::kSSums, &s_qf[buf][c_first]);
         t5_fence_after();
-        float2 y[NC / 2];   // log2 weights, minus the reference
+        float2 y[T][NC / 2];   // log2 weights, minus the reference
         {
-          uint32_t v[NC], v1[NC];
-          t5_ldn(s_col, v);
-          if constexpr (Cfg::kSSums > 1) t5_ldn(s_col + N, v1);
-          const float2 ka2 = make_float2(ka, ka), vc2 = make_float2(sc.y, sc.y);
+          uint32_t v[T][Cfg::kSSums][NC];
+          auto load = [&](int h) {
+#pragma unroll
+            for (int e = 0; e < Cfg::kSSums; ++e) t5_ldn(s_col + h * Cfg::kSCols + e * N, v[h][e]);
+          };
+          load(0);
+          if (T > 1 && nt > 1) load(T - 1);
+          float2 nb[NC / 2];
 #pragma unroll
           for (int k = 0; k < NC; k += 4) {
-            const float4 nb = *reinterpret_cast<const float4 *>(nbs + k);
-            y[k / 2] = __fadd2_rn(vc2, make_float2(nb.x, nb.y));
-            y[k / 2 + 1] = __fadd2_rn(vc2, make_float2(nb.z, nb.w));
+            const float4 b = *reinterpret_cast<const float4 *>(&s_nb[c_first + k]);
+            nb[k / 2] = make_float2(b.x, b.y);
+            nb[k / 2 + 1] = make_float2(b.z, b.w);
           }
           t5_wait_ld();
-          keep_after<NC>(reinterpret_cast<float(&)[NC]>(v));
-          if constexpr (Cfg::kSSums > 1) keep_after<NC>(reinterpret_cast<float(&)[NC]>(v1));
-          t5_fence_before();
-          if (lane == 0) mbar_arrive(&s_free[x][pb]);
-          __syncwarp();   // (what follows takes whole warps)
+          auto scores = [&](int h) {
 #pragma unroll
-          for (int k = 0; k < NC / 2; ++k) {
-            float2 q = make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
-            if constexpr (Cfg::kSSums > 1) q = __fadd2_rn(q, make_float2(__uint_as_float(v1[2 * k]), __uint_as_float(v1[2 * k + 1])));
-            y[k] = __ffma2_rn(q, ka2, y[k]);
+            for (int e = 0; e < Cfg::kSSums; ++e) keep_after<NC>(reinterpret_cast<float(&)[NC]>(v[h][e]));
+            const float2 ka2 = make_float2(ka[h], ka[h]), vc2 = make_float2(vc[h], vc[h]);
+#pragma unroll
+            for (int k = 0; k < NC / 2; ++k) {
+              float2 q = make_float2(__uint_as_float(v[h][0][2 * k]), __uint_as_float(v[h][0][2 * k + 1]));
+              if constexpr (Cfg::kSSums > 1) q = __fadd2_rn(q, make_float2(__uint_as_float(v[h][1][2 * k]), __uint_as_float(v[h][1][2 * k + 1])));
+              y[h][k] = __ffma2_rn(q, ka2, __fadd2_rn(vc2, nb[k]));
+            }
+            if (edge) {
+#pragma unroll
+              for (int k = 0; k < NC; k += 4) {
+                const int4 j = *reinterpret_cast<const int4 *>(&s_pos[buf][c_first + k]);
+                if ((uint32_t)(j.x - j0[h]) >= reach[h]) y[h][k / 2].x = -INFINITY;
+                if ((uint32_t)(j.y - j0[h]) >= reach[h]) y[h][k / 2].y = -INFINITY;
+                if ((uint32_t)(j.z - j0[h]) >= reach[h]) y[h][k / 2 + 1].x = -INFINITY;
+                if ((uint32_t)(j.w - j0[h]) >= reach[h]) y[h][k / 2 + 1].y = -INFINITY;
+              }
+            }
+          };
+          scores(0);
+          if constexpr (T > 1) {
+            if (nt > 1) {
+              scores(T - 1);
+            } else {
+#pragma unroll
+              for (int k = 0; k < NC / 2; ++k) y[T - 1][k] = make_float2(-INFINITY, -INFINITY);
+            }
           }
         }
-        if (edge) {
-          const int key = key0 + t, j0 = key - (L - P.n_new);
-          const uint32_t reach = P.window > 0 && key >= P.sinks ? (uint32_t)P.window : 0x80000000u;
-#pragma unroll
-          for (int k = 0; k < NC; k += 4) {
-            const int4 j = *reinterpret_cast<const int4 *>(&s_pos[buf][c_first + k]);
-            if ((uint32_t)(j.x - j0) >= reach) y[k / 2].x = -INFINITY;
-            if ((uint32_t)(j.y - j0) >= reach) y[k / 2].y = -INFINITY;
-            if ((uint32_t)(j.z - j0) >= reach) y[k / 2 + 1].x = -INFINITY;
-            if ((uint32_t)(j.w - j0) >= reach) y[k / 2 + 1].y = -INFINITY;
-          }
-        }
-        // Tiles set the references of rows that have met no key yet (they are 0 so
+        // Steps set the references of rows that have met no key yet (they are 0 so
         // far), and move those of rows with a weight above 2^kMove. All four warps
         // decide together, as they share O.
-        float top = fmaxf(y[0].x, y[0].y);
+        float top = fmaxf(y[0][0].x, y[0][0].y);
 #pragma unroll
-        for (int k = 1; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[k].x), y[k].y);
+        for (int k = 1; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[0][k].x), y[0][k].y);
+        if constexpr (T > 1) {
+#pragma unroll
+          for (int k = 0; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[1][k].x), y[1][k].y);
+        }
         if (bar_or(bar, 128, open || top > kMove || !ok)) {
-          gone = bar_or(bar, 128, !ok);
-          if (gone) break;
+          if (bar_or(bar, 128, !ok)) {
+            gone = true;
+            break;
+          }
           float mine = -INFINITY;   // each column's largest weight
 #pragma unroll
           for (int k = 0; k < NC; ++k) {
-            const float m = warp_top(k & 1 ? y[k / 2].y : y[k / 2].x);
+            const float m = warp_top(k & 1 ? fmaxf(y[0][k / 2].y, y[T - 1][k / 2].y) : fmaxf(y[0][k / 2].x, y[T - 1][k / 2].x));
             if (lane == k) mine = m;
           }
           if (lane < NC) s_max[warp][lane] = mine;
@@ -654,30 +657,32 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
           if (t < NC) {
             float a = 1.f, by = 0.f;
             if (t < live) {
-              const float(*mx)[NC] = s_max + (warp & ~3);
-              const float m = fmaxf(fmaxf(mx[0][t], mx[1][t]), fmaxf(mx[2][t], mx[3][t]));
+              const float m = fmaxf(fmaxf(s_max[4 * w][t], s_max[4 * w + 1][t]), fmaxf(s_max[4 * w + 2][t], s_max[4 * w + 3][t]));
               if (m > (unset ? -INFINITY : kMove)) {
                 by = kTop - m;
                 a = unset ? 1.f : ex2f(by);
-                nbs[t] += by;
+                s_nb[c_first + t] += by;
                 unset = false;
               }
             }
-            bys[t] = by;
-            as[t] = a;
+            s_by[c_first + t] = by;
+            s_a[c_first + t] = a;
           }
           open = bar_or(bar, 128, unset);
 #pragma unroll
           for (int k = 0; k < NC; k += 4) {
-            const float4 by = *reinterpret_cast<const float4 *>(bys + k);
-            const float4 a = *reinterpret_cast<const float4 *>(as + k);
-            y[k / 2] = __fadd2_rn(y[k / 2], make_float2(by.x, by.y));
-            y[k / 2 + 1] = __fadd2_rn(y[k / 2 + 1], make_float2(by.z, by.w));
+            const float4 by = *reinterpret_cast<const float4 *>(&s_by[c_first + k]);
+            const float4 a = *reinterpret_cast<const float4 *>(&s_a[c_first + k]);
+#pragma unroll
+            for (int h = 0; h < T; ++h) {
+              y[h][k / 2] = __fadd2_rn(y[h][k / 2], make_float2(by.x, by.y));
+              y[h][k / 2 + 1] = __fadd2_rn(y[h][k / 2 + 1], make_float2(by.z, by.w));
+            }
             l2[k / 2] = __fmul2_rn(l2[k / 2], make_float2(a.x, a.y));
             l2[k / 2 + 1] = __fmul2_rn(l2[k / 2 + 1], make_float2(a.z, a.w));
           }
-          if (!opening) {   // O too, once the previous P V has landed
-            ok = __all_sync(0xffffffffu, kl_wait(&pv_done[x], (n - 1) & 1, abf, P.wait_ns)) && ok;
+          if (ti > 0) {   // O too, once the previous P V has landed
+            ok = __all_sync(0xffffffffu, kl_wait(&pv_done[pb ^ 1], ((step - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
             t5_fence_after();
 #pragma unroll 1
             for (int e = 0; e < 3; ++e) {
@@ -686,102 +691,114 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
               t5_wait_ld();
               keep_after<NC>(o);
 #pragma unroll
-              for (int k = 0; k < NC; ++k) o[k] *= as[k];
+              for (int k = 0; k < NC; k += 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(&s_a[c_first + k]);
+                o[k] *= a.x;
+                o[k + 1] *= a.y;
+                o[k + 2] *= a.z;
+                o[k + 3] *= a.w;
+              }
               t5_stn(o_col + e * N, reinterpret_cast<const uint32_t(&)[NC]>(o));
             }
             t5_wait_st();
           }
         }
-        opening = false;
-        const float2 vi2 = make_float2(sc.z, sc.z);
-        constexpr int kEights = (NC + 7) / 8;   // pieces of eight columns, a half of 16 bytes
-        uint2 piece[kEights][3];
+        auto weights = [&](int h) {
+          const float2 vi2 = make_float2(vi[h], vi[h]);
+          const uint32_t dst = p_row + (T * pb + h) * Cfg::kPBytes;
+          constexpr int kEights = (NC + 7) / 8;   // pieces of eight columns, a half of 16 bytes
+          uint2 piece[kEights][3];
 #pragma unroll
-        for (int c = 0; c < kEights; ++c) {
-          uint32_t ph[4], w0[3], w1[3] = {};
+          for (int c = 0; c < kEights; ++c) {
+            uint32_t ph[4], w0[3], w1[3] = {};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int e = 4 * c + k;
-            ph[k] = 0;
-            if (e >= NC / 2) continue;
-            const float2 p = make_float2(ex2f(y[e].x), ex2f(y[e].y));
-            l2[e] = __ffma2_rn(p, vi2, l2[e]);
-            ph[k] = pack2<true>(p.x, p.y);
-          }
-          cut_weights(ph[0], ph[1], w0);
-          if (NC - 8 * c >= 8) cut_weights(ph[2], ph[3], w1);   // (what the columns of padding hold does not matter)
-#pragma unroll
-          for (int e = 0; e < 3; ++e) piece[c][e] = make_uint2(w0[e], w1[e]);
-        }
-        auto store = [&](int c, int e) {
-          const uint32_t col = e * N + c_first + 8 * c;
-          asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(p_row + (col >> 5) * Cfg::kAtom + ((col & 24) ^ swap)), "r"(piece[c][e].x),
-                       "r"(piece[c][e].y)
-                       : "memory");
-        };
-        auto store2 = [&](int c, int e) {
-          const uint32_t col = e * N + c_first + 8 * c;
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p_row + (col >> 5) * Cfg::kAtom + ((col & 16) ^ swap)), "r"(piece[c][e].x),
-                       "r"(piece[c][e].y), "r"(piece[c + 1][e].x), "r"(piece[c + 1][e].y)
-                       : "memory");
-        };
-        // P V of the pipeline's tile before has read P'
-        if (n >= 1) ok = kl_wait(&pv_done[x], (n - 1) & 1, abf, P.wait_ns) && ok;
-#pragma unroll
-        for (int e = 0; e < 3; ++e) {
-          if constexpr (kEights == 1) {
-            store(0, e);
-          } else if constexpr (kEights == 3) {   // (the second warpgroup starts in the middle of 16 bytes)
-            if (w == 0) {
-              store2(0, e);
-              store(2, e);
-            } else {
-              store(0, e);
-              store2(1, e);
+            for (int k = 0; k < 4; ++k) {
+              const int e = 4 * c + k;
+              ph[k] = 0;
+              if (e >= NC / 2) continue;
+              const float2 p = make_float2(ex2f(y[h][e].x), ex2f(y[h][e].y));
+              l2[e] = __ffma2_rn(p, vi2, l2[e]);
+              ph[k] = pack2<true>(p.x, p.y);
             }
-          } else {
+            cut_weights(ph[0], ph[1], w0);
+            if (NC - 8 * c >= 8) cut_weights(ph[2], ph[3], w1);   // (what the columns of padding hold does not matter)
 #pragma unroll
-            for (int c = 0; c < kEights; c += 2) store2(c, e);
+            for (int e = 0; e < 3; ++e) piece[c][e] = make_uint2(w0[e], w1[e]);
           }
-        }
+          auto store = [&](int c, int e) {
+            const uint32_t col = e * N + c_first + 8 * c;
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(dst + (col >> 5) * Cfg::kAtom + ((col & 24) ^ swap)), "r"(piece[c][e].x),
+                         "r"(piece[c][e].y)
+                         : "memory");
+          };
+          auto store2 = [&](int c, int e) {   // (where 16 bytes begin)
+            const uint32_t col = e * N + c_first + 8 * c;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (col >> 5) * Cfg::kAtom + ((col & 16) ^ swap)), "r"(piece[c][e].x),
+                         "r"(piece[c][e].y), "r"(piece[c + 1][e].x), "r"(piece[c + 1][e].y)
+                         : "memory");
+          };
+#pragma unroll
+          for (int e = 0; e < 3; ++e) {
+            if constexpr (kEights == 1) {
+              store(0, e);
+            } else if constexpr (kEights == 3) {   // (the second warpgroup starts in the middle of 16 bytes)
+              if (w == 0) {
+                store2(0, e);
+                store(2, e);
+              } else {
+                store(0, e);
+                store2(1, e);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < kEights; c += 2) store2(c, e);
+            }
+          }
+        };
+        weights(0);
+        if (T > 1 && nt > 1) weights(T - 1);
         fence_proxy_async_shared();
         t5_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&p_full[x]);
-          if (u % kChunk >= kChunk - 2) mbar_arrive(&page_empty[u / kChunk % kChunks]);
-        }
-        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[pb]);
+        __syncwarp();   // (what follows takes whole warps)
+        pages_done(u);
+        if (nt > 1) pages_done(u + 1);
+        ti += nt;
+        u += nt;
         if (done.pending) finish();
       }
       if (gone) break;
-      if (done.pending) finish();   // (an item without a tile of this pipeline)
-      // ---- this pipeline's sums over the keys --------------------------------
+      // ---- epilogue, first part: sums over the keys -------------------------
       {
         float v[NC];
 #pragma unroll
         for (int k = 0; k < NC; ++k) v[k] = k & 1 ? l2[k / 2].y : l2[k / 2].x;
-        int at = 0, cnt = 0;
-        warp_sums<NC>(v, lane, at, cnt);
+        int at = 0, n = 0;
+        warp_sums<NC>(v, lane, at, n);
 #pragma unroll
         for (int k = 0; k < 5; ++k)   // (lanes with the same sums write the same words)
-          if (k < cnt) s_max[warp][at + k] = v[k];
+          if (k < n) s_red[warp][at + k] = v[k];
       }
-      gone = bar_or(bar, 128, !ok);
+      named_bar_sync(bar, 128);
+      const int64_t ent = 2 * (int64_t)blockIdx.x + (it.w & kOpening ? 0 : 1);
       if (t < live) {
-        const float(*sum)[NC] = s_max + (warp & ~3);
-        s_ml[i & 1][x][c_first + t] = make_float2(unset ? -kUnset : -nbs[t], (sum[0][t] + sum[1][t]) + (sum[2][t] + sum[3][t]));
+        float l = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) l += s_red[4 * w + k][t];
+        // (a row of NaN stays NaN; l is 0 only for a row without keys, which a query that sees itself never is)
+        s_fin[i & 1][c_first + t] = it.w & kWhole ? 1.f / l : 1.f;
+        if (!(it.w & kWhole)) {
+          const int64_t e = ent * P.Rg + w * live0 + t;
+          P.ws_ml[2 * e] = unset ? -kUnset : -s_nb[c_first + t];
+          P.ws_ml[2 * e + 1] = l;
+        }
       }
-      if ((warp & 3) == 0) {   // (at most 32 live rows: the first warp's)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ml_full[i & 1]);
-      }
-      __syncwarp();
-      if (x == (i & 1))
-        done = {true, (it.w & kWhole) != 0, ntiles > 1, u0 & 1, i, 2 * (int64_t)blockIdx.x + (it.w & kOpening ? 0 : 1)};
-      u0 += ntiles;
+      done = {true, (it.w & kWhole) != 0, step - 1, i, ent};
+      ++i;
     }
-    if (!gone && done.pending) finish();
+    named_bar_sync(bar, 128);
+    if (done.pending) finish();
   }
   __syncthreads();
   if (tid == 0 && *abf) atomic_or_status(P.status, SV_DEV_TIMEOUT);
