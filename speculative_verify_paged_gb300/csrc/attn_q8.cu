@@ -176,9 +176,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
       mbar_init(&q_full[k], 1);
       mbar_init(&q_empty[k], 1);
       mbar_init(&o_free[k], softmax_warps);
-      // Q K^T of the step (its commit, and the issuing lane itself, which has seen
-      // the scales), and P V of the step before the last
-      mbar_init(&s_full[k], 3);
+      mbar_init(&s_full[k], 2);   // Q K^T of the step, and P V of the step before the last
       mbar_init(&p_full[k], softmax_warps);
       mbar_init(&pv_done[k], 1);
     }
@@ -394,7 +392,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
           ok = kl_wait(&q_full[items & 1], (items >> 1) & 1, abf, P.wait_ns) && ok;
           ++items;
         }
-        if (u % kChunk == 0) ok = kl_wait(&scale_full[u / kChunk % kChunks], (u / (kChunk * kChunks)) & 1, abf, P.wait_ns) && ok;
         // the softmax of the step before the last has read the S buffers
         // (before there is one, the phase that counts as done)
         if (!(flag & kSecond)) ok = kl_wait2(&k_full[s], round & 1, &p_full[pb], ((step >> 1) & 1) ^ 1, abf, P.wait_ns) && ok;
@@ -411,7 +408,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
           t5_commit(&k_empty[s]);
           if (flag & kEnd) {
             t5_commit(&s_full[pb]);
-            mbar_arrive(&s_full[pb]);
           }
           if (flag & kLast) t5_commit(&q_empty[(items - 1) & 1]);
         }
@@ -551,18 +547,19 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
       bool gone = bar_or(bar, 128, !ok);
       for (int ti = 0; ti < ntiles && !gone; ++step) {
         const int nt = min(ntiles - ti, T);
-        // S of this step, and with it the scales and P' buffers that P V two
-        // steps ago has read
+        // S of this step, and with it the P' buffers that P V two steps ago has read
         const int pb = step & 1;
-        ok = kl_wait(&s_full[pb], (step >> 1) & 1, abf, P.wait_ns) && ok;
         float ka[T], vc[T], vi[T];
 #pragma unroll
         for (int h = 0; h < T; ++h) {   // this thread's keys
+          if (h < nt && (u + h) % kChunk == 0)
+            ok = kl_wait(&scale_full[(u + h) / kChunk % kChunks], ((u + h) / (kChunk * kChunks)) & 1, abf, P.wait_ns) && ok;
           const float4 s = s_scale[(u + h) % (kChunk * kChunks) * kTP + (t >> 4)];   // (of an absent tile: any)
           ka[h] = s.x * fabsf(fold);
           vc[h] = s.y;
           vi[h] = s.z;
         }
+        ok = kl_wait(&s_full[pb], (step >> 1) & 1, abf, P.wait_ns) && ok;
         const uint32_t s_col = lanes + Cfg::kSCol + T * pb * Cfg::kSCols + c_first;
         // A step that ends past the oldest query or holds keys that a window has
         // left: position j sees a key iff 0 <= j - j0 < reach.
@@ -641,18 +638,23 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
 #pragma unroll
           for (int k = 0; k < NC / 2; ++k) top = fmaxf(fmaxf(top, y[1][k].x), y[1][k].y);
         }
+        bool moved = false;
         if (bar_or(bar, 128, open || top > kMove || !ok)) {
           if (bar_or(bar, 128, !ok)) {
             gone = true;
             break;
           }
-          float mine = -INFINITY;   // each column's largest weight
+          {   // each column's largest weight
+            float v[NC];
 #pragma unroll
-          for (int k = 0; k < NC; ++k) {
-            const float m = warp_top(k & 1 ? fmaxf(y[0][k / 2].y, y[T - 1][k / 2].y) : fmaxf(y[0][k / 2].x, y[T - 1][k / 2].x));
-            if (lane == k) mine = m;
+            for (int k = 0; k < NC; ++k)
+              v[k] = k & 1 ? fmaxf(y[0][k / 2].y, y[T - 1][k / 2].y) : fmaxf(y[0][k / 2].x, y[T - 1][k / 2].x);
+            int at = 0, n = 0;
+            warp_joined<NC, true>(v, lane, at, n);
+#pragma unroll
+            for (int k = 0; k < 5; ++k)   // (lanes with the same maxima write the same words)
+              if (k < n) s_max[warp][at + k] = v[k];
           }
-          if (lane < NC) s_max[warp][lane] = mine;
           named_bar_sync(bar, 128);
           if (t < NC) {
             float a = 1.f, by = 0.f;
@@ -681,27 +683,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
             l2[k / 2] = __fmul2_rn(l2[k / 2], make_float2(a.x, a.y));
             l2[k / 2 + 1] = __fmul2_rn(l2[k / 2 + 1], make_float2(a.z, a.w));
           }
-          if (ti > 0) {   // O too, once the previous P V has landed
-            ok = __all_sync(0xffffffffu, kl_wait(&pv_done[pb ^ 1], ((step - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
-            t5_fence_after();
-#pragma unroll 1
-            for (int e = 0; e < 3; ++e) {
-              float o[NC];
-              t5_ldn(o_col + e * N, reinterpret_cast<uint32_t(&)[NC]>(o));
-              t5_wait_ld();
-              keep_after<NC>(o);
-#pragma unroll
-              for (int k = 0; k < NC; k += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(&s_a[c_first + k]);
-                o[k] *= a.x;
-                o[k + 1] *= a.y;
-                o[k + 2] *= a.z;
-                o[k + 3] *= a.w;
-              }
-              t5_stn(o_col + e * N, reinterpret_cast<const uint32_t(&)[NC]>(o));
-            }
-            t5_wait_st();
-          }
+          moved = ti > 0;
         }
         auto weights = [&](int h) {
           const float2 vi2 = make_float2(vi[h], vi[h]);
@@ -757,6 +739,28 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
         };
         weights(0);
         if (T > 1 && nt > 1) weights(T - 1);
+        if (moved) {   // O too, once the previous P V has landed (its wait lies behind the weights)
+          ok = __all_sync(0xffffffffu, kl_wait(&pv_done[pb ^ 1], ((step - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
+          t5_fence_after();
+          float o[3][NC];
+#pragma unroll
+          for (int e = 0; e < 3; ++e) t5_ldn(o_col + e * N, reinterpret_cast<uint32_t(&)[NC]>(o[e]));
+          t5_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 3; ++e) {
+            keep_after<NC>(o[e]);
+#pragma unroll
+            for (int k = 0; k < NC; k += 4) {
+              const float4 a = *reinterpret_cast<const float4 *>(&s_a[c_first + k]);
+              o[e][k] *= a.x;
+              o[e][k + 1] *= a.y;
+              o[e][k + 2] *= a.z;
+              o[e][k + 3] *= a.w;
+            }
+            t5_stn(o_col + e * N, reinterpret_cast<const uint32_t(&)[NC]>(o[e]));
+          }
+          t5_wait_st();
+        }
         fence_proxy_async_shared();
         t5_fence_before();
         __syncwarp();
@@ -775,7 +779,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
 #pragma unroll
         for (int k = 0; k < NC; ++k) v[k] = k & 1 ? l2[k / 2].y : l2[k / 2].x;
         int at = 0, n = 0;
-        warp_sums<NC>(v, lane, at, n);
+        warp_joined<NC, false>(v, lane, at, n);
 #pragma unroll
         for (int k = 0; k < 5; ++k)   // (lanes with the same sums write the same words)
           if (k < n) s_red[warp][at + k] = v[k];

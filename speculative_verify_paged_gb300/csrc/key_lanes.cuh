@@ -371,11 +371,12 @@ __device__ __forceinline__ void t5_mma_ts_f8(uint32_t d, uint32_t a, uint64_t b,
                "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 
-// Sums of v[0..NV) over the warp's lanes. While their number is even, each step
-// exchanges the half of the values that the other lane keeps; lane l is left
-// with the sums of n values from `at` on.
-template <int NV, int O = 16>
-__device__ __forceinline__ void warp_sums(float *v, int lane, int &at, int &n) {
+// Sums, or maxima (NaN left out), of v[0..NV) over the warp's lanes. While their
+// number is even, each step exchanges the half of the values that the other lane
+// keeps; lane l is left with those of n values from `at` on.
+template <int NV, bool MAX, int O = 16>
+__device__ __forceinline__ void warp_joined(float *v, int lane, int &at, int &n) {
+  auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
   if constexpr (O == 0) {
     n = NV;
   } else if constexpr (NV % 2 == 0) {
@@ -384,16 +385,18 @@ __device__ __forceinline__ void warp_sums(float *v, int lane, int &at, int &n) {
 #pragma unroll
     for (int k = 0; k < H; ++k) {
       const float send = up ? v[k] : v[k + H], keep = up ? v[k + H] : v[k];
-      v[k] = keep + __shfl_xor_sync(0xffffffffu, send, O);
+      v[k] = join(keep, __shfl_xor_sync(0xffffffffu, send, O));
     }
     if (up) at += H;
-    warp_sums<H, O / 2>(v, lane, at, n);
+    warp_joined<H, MAX, O / 2>(v, lane, at, n);
   } else {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], O);
-    warp_sums<NV, O / 2>(v, lane, at, n);
+    for (int k = 0; k < NV; ++k) v[k] = join(v[k], __shfl_xor_sync(0xffffffffu, v[k], O));
+    warp_joined<NV, MAX, O / 2>(v, lane, at, n);
   }
 }
+template <int NV>
+__device__ __forceinline__ void warp_sums(float *v, int lane, int &at, int &n) { warp_joined<NV, false>(v, lane, at, n); }
 
 // Largest of the warp's values (NaN left out)
 __device__ __forceinline__ float warp_top(float x) {
