@@ -833,7 +833,7 @@ sv_status launch_q4(const KlParams &P, int C, cudaStream_t st) {
   });
   if (err != cudaSuccess) return fail(SV_ERR_CUDA, "spec_verify_attn_q4: cudaFuncSetAttribute: %s", cudaGetErrorString(err));
   const int64_t prep = (P.NR + kPrepWarps - 1) / kPrepWarps + (int64_t)P.B * P.H_kv * P.RG;
-  launch_k(kl_prep_kernel<NC, true>, dim3((unsigned)prep), dim3(32 * kPrepWarps), 0, st, 1, P);
+  launch_k(kl_prep_kernel<NC, 2, true>, dim3((unsigned)prep), dim3(32 * kPrepWarps), 0, st, 1, P);
   launch_k(attn_q4_kernel<NC>, dim3(C), dim3(32 * kWarps), Q4Cfg<NC>::kSmem, st, 1, P);
   return check_launch("spec_verify_attn_q4 launch");
 }

@@ -36,19 +36,20 @@ namespace sv {
 namespace {
 
 constexpr int kTile = kTK * kD;            // bytes of a tile of K or V
-constexpr int kWarps = 16;
-constexpr int kPageWarp = 8, kKWarp = 9, kVWarp = 10, kQkWarp = 11, kPvWarp = 12, kQWarp = 13, kScaleWarp = 14;
-// Registers a thread: the softmax warps take what the others leave.
-constexpr int kRegs = 128, kRegsSoftmax = 192, kRegsOther = 64;
-static_assert(256 * kRegsSoftmax + 32 * (kWarps - 8) * kRegsOther <= 32 * kWarps * kRegs, "registers");
 // A row's reference puts its largest weight at 2^kTop and moves once one exceeds
 // 2^kMove (f16 ends at 65504, which e5m2 takes for 57344 and two smaller terms).
 constexpr float kTop = 5.f, kMove = 15.9f;
 
-template <int NC> struct Q8Cfg : KlCfg<NC> {
-  using KlCfg<NC>::kN;
-  using KlCfg<NC>::kQ;
-  using KlCfg<NC>::kT;
+template <int NC, int W> struct Q8Cfg : KlCfg<NC, W> {
+  using KlCfg<NC, W>::kN;
+  using KlCfg<NC, W>::kQ;
+  using KlCfg<NC, W>::kT;
+  // Registers a thread: at the launch, of the softmax warps, which take what the
+  // others leave, and of those.
+  static constexpr int kWarps = 4 * W + 8;
+  static constexpr int kRegs = W == 2 ? 128 : W == 3 ? 96 : 80;
+  static constexpr int kRegsSoftmax = W == 2 ? 192 : W == 3 ? 128 : 96, kRegsOther = W == 2 ? 64 : 48;
+  static_assert(4 * W * kRegsSoftmax + 8 * kRegsOther <= kWarps * kRegs, "registers");
   // The terms of P', and where tensor memory has room those of Q, side by side are
   // the columns of one product with several sums: what an MMA of few columns costs
   // is its other operand (16 or 32 columns 41 cycles, 48 45, 96 57, 144 72), 4 KB
@@ -106,14 +107,16 @@ __device__ __forceinline__ void cut_weights(uint32_t h0, uint32_t h1, uint32_t (
   w[2] = __byte_perm(last(rest(h0)), last(rest(h1)), 0x7531);
 }
 
-// Warps 0-3 and 4-7: softmax (a key per thread and tile; each warpgroup half of
+// W warpgroups: softmax (a key per thread and tile; each warpgroup its share of
 // the query rows, or the first all of up to 8), later the epilogue (a head dim
 // per thread). 8: block numbers and flags of the tiles ahead. 9, 10: copy the K
 // and V codes. 11: issues Q K^T, owns the 512 TMEM columns. 12: issues P V. 13: Q
 // of the next sequence. 14: the blocks' scales.
-template <int NC>
-__global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_constant__ KlParams P, const __grid_constant__ Q8Maps M) {
-  using Cfg = Q8Cfg<NC>;
+template <int NC, int W>
+__global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(const __grid_constant__ KlParams P, const __grid_constant__ Q8Maps M) {
+  using Cfg = Q8Cfg<NC, W>;
+  constexpr int kPageWarp = 4 * W, kKWarp = kPageWarp + 1, kVWarp = kPageWarp + 2, kQkWarp = kPageWarp + 3, kPvWarp = kPageWarp + 4,
+                kQWarp = kPageWarp + 5, kScaleWarp = kPageWarp + 6;
   constexpr int N = Cfg::kN, CP = Cfg::kCols, T = Cfg::kT, KS = Cfg::kKS, VS = Cfg::kVS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t page_full[kChunks], page_empty[kChunks], scale_full[kChunks];
@@ -135,15 +138,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
   __shared__ float s_fold[3];
   __shared__ __align__(16) int4 s_item[3];   // first tile, tiles, length in span coordinates, kWhole | kOpening
   __shared__ __align__(16) float s_nb[N], s_by[N], s_a[N];   // minus the reference; what it last moved by, as a power and a factor
-  __shared__ float s_max[8][NC], s_red[8][NC], s_fin[2][N];
+  __shared__ float s_max[4 * W][NC], s_red[4 * W][NC], s_fin[2][N];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Hp = P.H_kv * P.RG;
   const int range = blockIdx.x / Hp, gp = blockIdx.x % Hp;
   const int g = gp / P.RG, row0 = (gp % P.RG) * P.Rg;
   const int rows = min(P.Rg, P.R - row0);       // live rows of this CTA
-  const int live0 = kl_first(rows);             // of the first softmax warpgroup
-  const int softmax_warps = live0 < rows ? 8 : 4;
+  const int live0 = kl_first(rows, W);          // of a softmax warpgroup, but the last
+  const int softmax_warps = 4 * ((rows + live0 - 1) / live0);
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t q_smem = smem_u32(smem);
   const uint32_t k_ring = q_smem + 2 * Cfg::kQ, v_ring = k_ring + KS * kTile;
@@ -208,7 +211,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
     }
   };
 
-  if (warp >= kPageWarp) regs_dec<kRegsOther>();
+  if (warp >= kPageWarp) regs_dec<Cfg::kRegsOther>();
   if (warp != kPageWarp) pdl_wait();
   pdl_trigger();
   if (warp == kPageWarp) {
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
       const float fold = qs[N];
       for (int col = lane; col < N; col += 32) {
         const int w = col / CP, c = col - w * CP;
-        const int r = row0 + (c < (w ? rows - live0 : live0) ? w * live0 + c : 0);   // (padding: any)
+        const int r = row0 + (c < min(rows - w * live0, live0) ? w * live0 + c : 0);   // (padding: any)
         const int j = r / P.G;
         s_pos[row][col] = j;
         s_row[row][col] = (it.b * P.n_new + j) * P.H_q + g * P.G + (r - j * P.G);
@@ -487,10 +490,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
     }
   } else if (warp < softmax_warps) {
     // ------------------------------------------------------------- softmax --
-    regs_inc<kRegsSoftmax>();
+    regs_inc<Cfg::kRegsSoftmax>();
     const int w = warp >> 2, t = tid & 127;
     const int c_first = w * CP;                 // this warpgroup's columns
-    const int live = w ? rows - live0 : live0;
+    const int live = min(rows - w * live0, live0);
     const int bar = 1 + w;
     const uint32_t lanes = tb + ((uint32_t)((warp & 3) * 32) << 16);
     // this key's row of P', and what its two 16-byte pieces are exchanged by
@@ -723,8 +726,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
           for (int e = 0; e < 3; ++e) {
             if constexpr (kEights == 1) {
               store(0, e);
-            } else if constexpr (kEights == 3) {   // (the second warpgroup starts in the middle of 16 bytes)
-              if (w == 0) {
+            } else if constexpr (kEights == 3) {   // (odd warpgroups start in the middle of 16 bytes)
+              if (w % 2 == 0) {
                 store2(0, e);
                 store(2, e);
               } else {
@@ -811,18 +814,21 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_q8_kernel(const __grid_co
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tb), "r"(512));
 }
 
-template <int NC>
+template <int NC, int W>
 sv_status launch_q8(const KlParams &P, const Q8Maps &M, int C, cudaStream_t st) {
   static DeviceOnce once;
   const cudaError_t err = once_per_device(once, [] {
-    return cudaFuncSetAttribute(attn_q8_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q8Cfg<NC>::kSmem);
+    return cudaFuncSetAttribute(attn_q8_kernel<NC, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q8Cfg<NC, W>::kSmem);
   });
   if (err != cudaSuccess) return fail(SV_ERR_CUDA, "spec_verify_attn_q8: cudaFuncSetAttribute: %s", cudaGetErrorString(err));
   const int64_t prep = (P.NR + kPrepWarps - 1) / kPrepWarps + (int64_t)P.B * P.H_kv * P.RG;
-  launch_k(kl_prep_kernel<NC, false>, dim3((unsigned)prep), dim3(32 * kPrepWarps), 0, st, 1, P);
-  launch_k(attn_q8_kernel<NC>, dim3(C), dim3(32 * kWarps), Q8Cfg<NC>::kSmem, st, 1, P, M);
+  launch_k(kl_prep_kernel<NC, W, false>, dim3((unsigned)prep), dim3(32 * kPrepWarps), 0, st, 1, P);
+  launch_k(attn_q8_kernel<NC, W>, dim3(C), dim3(32 * Q8Cfg<NC, W>::kWarps), Q8Cfg<NC, W>::kSmem, st, 1, P, M);
   return check_launch("spec_verify_attn_q8 launch");
 }
+
+// Softmax warpgroups: as many as keep 16 rows or fewer each.
+int q8_groups(int rows) { return rows <= 32 ? 2 : rows <= 48 ? 3 : 4; }
 
 // Query rows of a kv head on the tensor cores: 64 share a pass over the cache.
 constexpr int64_t kMaxRows = 1 << 14;
@@ -840,7 +846,7 @@ extern "C" size_t spec_verify_attn_q8_workspace_size(int B, int n_new, int H_q, 
   if ((int64_t)window >= (int64_t)max_blocks_per_seq * block_size) window = sinks = 0;
   const KlPlan p = kl_plan(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size, SV_BF16, window, sinks, kMaxRows);
   // (queries in f32 run on the CUDA-core kernel whatever the shape)
-  return p.tc ? std::max(other, kl_ws_bytes(p, B, H_kv)) : other;
+  return p.tc ? std::max(other, kl_ws_bytes(p, B, H_kv, q8_groups(p.Rg))) : other;
 }
 
 extern "C" sv_status spec_verify_attn_q8(const void *q, sv_dtype q_dtype, const void *k_cache, const void *v_cache,
@@ -870,7 +876,8 @@ extern "C" sv_status spec_verify_attn_q8(const void *q, sv_dtype q_dtype, const 
   memset(&P, 0, sizeof(P));
   const sv_status rc = q8_check("spec_verify_attn_q8", k_cache, v_cache, layout, H_kv, d_head, block_size, &P.block_stride);
   if (rc != SV_OK) return rc;
-  const size_t need = kl_ws_bytes(p, B, H_kv);
+  const int W = q8_groups(p.Rg);
+  const size_t need = kl_ws_bytes(p, B, H_kv, W);
   if (!workspace || workspace_bytes < need)
     return fail(SV_ERR_WORKSPACE, "spec_verify_attn_q8: workspace needs %zu bytes", need);
   if (!aligned(workspace, 256)) return fail(SV_ERR_WORKSPACE, "spec_verify_attn_q8: workspace not 256-byte aligned");
@@ -899,7 +906,7 @@ extern "C" sv_status spec_verify_attn_q8(const void *q, sv_dtype q_dtype, const 
   P.ws_split = reinterpret_cast<int4 *>(at);
   at += align_up((size_t)p.NR * sizeof(int4), 256);
   P.ws_q = at;
-  at += align_up((size_t)B * H_kv * p.RG * kl_cols(p) * 256, 256);
+  at += align_up((size_t)B * H_kv * p.RG * kl_cols(p, W) * 256, 256);
   P.ws_qs = reinterpret_cast<float *>(at);
   P.status = dev_status;
   P.B = B; P.n_new = n_new; P.H_q = H_q; P.H_kv = H_kv; P.G = H_q / H_kv; P.R = p.R; P.Rg = p.Rg; P.RG = p.RG;
@@ -908,14 +915,13 @@ extern "C" sv_status spec_verify_attn_q8(const void *q, sv_dtype q_dtype, const 
   P.wait_ns = wait_limit_ns();
   P.withhold = test_withhold();
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int half = kl_first(p.Rg);   // rows of a softmax warpgroup
-  const sv_status r2 = half <= 4    ? launch_q8<4>(P, M, p.C, st)
-                       : half <= 8  ? launch_q8<8>(P, M, p.C, st)
-                       : half <= 12 ? launch_q8<12>(P, M, p.C, st)
-                       : half <= 16 ? launch_q8<16>(P, M, p.C, st)
-                       : half <= 20 ? launch_q8<20>(P, M, p.C, st)
-                       : half <= 24 ? launch_q8<24>(P, M, p.C, st)
-                                    : launch_q8<32>(P, M, p.C, st);
+  const int each = kl_first(p.Rg, W);   // rows of a softmax warpgroup
+  const sv_status r2 = W == 3       ? launch_q8<16, 3>(P, M, p.C, st)
+                       : W == 4     ? launch_q8<16, 4>(P, M, p.C, st)
+                       : each <= 4  ? launch_q8<4, 2>(P, M, p.C, st)
+                       : each <= 8  ? launch_q8<8, 2>(P, M, p.C, st)
+                       : each <= 12 ? launch_q8<12, 2>(P, M, p.C, st)
+                                    : launch_q8<16, 2>(P, M, p.C, st);
   if (r2 != SV_OK || p.NR == 1) return r2;
   launch_k(kl_merge_kernel, dim3((p.NR - 1) * H_kv * p.RG, (p.Rg + kMergeWarps - 1) / kMergeWarps),
            dim3(32 * kMergeWarps), 0, st, 1, P);

@@ -33,7 +33,8 @@ constexpr float kUnset = 1e30f;            // minus the reference of a row that 
 // captured: 4 rows 90.3 against 97.4 us, 8 rows 96.4 against 97.4; up to 16 it
 // would be 106.7 against 104.6 with 16 rows, 105.6 against 104.6 with 12).
 constexpr int kAlone = 8;
-__host__ __device__ inline int kl_first(int rows) { return rows <= kAlone ? rows : (rows + 1) / 2; }
+// (of W warpgroups; row w * kl_first + c is row c of warpgroup w)
+__host__ __device__ inline int kl_first(int rows, int W = 2) { return rows <= kAlone ? rows : (rows + W - 1) / W; }
 
 struct KlParams {
   const void *q;
@@ -57,9 +58,9 @@ struct KlParams {
   unsigned withhold;
 };
 
-template <int NC> struct KlCfg {   // NC query rows per softmax warpgroup
-  static constexpr int kCols = (NC + 7) / 8 * 8, kN = 2 * kCols;   // columns of S and O
-  static constexpr int kT = NC > 24 ? 1 : 2;   // tiles of a softmax step (their scores stay in registers)
+template <int NC, int W = 2> struct KlCfg {   // NC query rows per softmax warpgroup, W of these
+  static constexpr int kCols = (NC + 7) / 8 * 8, kN = W * kCols;   // columns of S and O
+  static constexpr int kT = W * NC > 48 ? 1 : 2;   // tiles of a softmax step (their scores stay in registers)
   static constexpr int kQ = kN * 256;   // the two e4m3 terms of a row, 128 bytes each
 };
 
@@ -193,9 +194,9 @@ constexpr int kPrepWarps = 4;
 constexpr int kNear = 6;
 // NIB (4-bit codes): the dims in the order in which codes are spread, with the
 // rows' sums; otherwise in their own order.
-template <int NC, bool NIB>
+template <int NC, int W, bool NIB>
 __global__ void __launch_bounds__(32 * kPrepWarps) kl_prep_kernel(const __grid_constant__ KlParams P) {
-  using Cfg = KlCfg<NC>;
+  using Cfg = KlCfg<NC, W>;
   constexpr int N = Cfg::kN, CP = Cfg::kCols;
   constexpr int kPass = N / (2 * kPrepWarps);   // half a warp a row and pass
   __shared__ uint32_t s_top[kPrepWarps], s_low[kPrepWarps];
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps) kl_prep_kernel(const __grid_c
   const int Hp = P.H_kv * P.RG;
   const int gp = (int)(ent % Hp), b = (int)(ent / Hp);
   const int g = gp / P.RG, row0 = (gp % P.RG) * P.Rg;
-  const int rows = min(P.Rg, P.R - row0), live0 = kl_first(rows);
+  const int rows = min(P.Rg, P.R - row0), live0 = kl_first(rows, W);
   const int c8 = lane & 15;
   uint4 v[kPass];
   // largest finite elements (their bits): of each row, of the entry, and of its smallest row but those of zeros
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps) kl_prep_kernel(const __grid_c
     const int col = (k * kPrepWarps + warp) * 2 + (lane >> 4);
     const int w = col / CP, c = col - w * CP;
     v[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (c < (w ? rows - live0 : live0)) {
+    if (c < min(rows - w * live0, live0)) {
       const int r = row0 + w * live0 + c, j = r / P.G;
       const int64_t at = ((int64_t)b * P.n_new + j) * P.H_q + g * P.G + (r - j * P.G);
       v[k] = static_cast<const uint4 *>(P.q)[at * 16 + c8];
@@ -581,10 +582,10 @@ inline KlPlan kl_plan(int B, int n_new, int H_q, int H_kv, int d, int max_blocks
 }
 
 // Columns of S and O, a softmax warpgroup's rows in steps of 4 (of 8 for the layout)
-inline int kl_cols(const KlPlan &p) { return 2 * ((kl_first(p.Rg) + 7) / 8 * 8); }
+inline int kl_cols(const KlPlan &p, int W = 2) { return W * ((kl_first(p.Rg, W) + 7) / 8 * 8); }
 
-inline size_t kl_ws_bytes(const KlPlan &p, int B, int H_kv) {
-  const size_t ent = (size_t)2 * p.C * p.Rg, qent = (size_t)B * H_kv * p.RG, n = kl_cols(p);
+inline size_t kl_ws_bytes(const KlPlan &p, int B, int H_kv, int W = 2) {
+  const size_t ent = (size_t)2 * p.C * p.Rg, qent = (size_t)B * H_kv * p.RG, n = kl_cols(p, W);
   return align_up(ent * kD * sizeof(float), 256) + align_up(ent * 2 * sizeof(float), 256) +
          align_up((size_t)p.NR * sizeof(int4), 256) + align_up(qent * n * 256, 256) +
          align_up(qent * (2 * n + 4) * sizeof(float), 256);
