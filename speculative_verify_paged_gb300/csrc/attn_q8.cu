@@ -47,8 +47,8 @@ template <int NC, int W> struct Q8Cfg : KlCfg<NC, W> {
   // Registers a thread: at the launch, of the softmax warps, which take what the
   // others leave, and of those.
   static constexpr int kWarps = 4 * W + 8;
-  static constexpr int kRegs = W == 2 ? 128 : W == 3 ? 96 : 80;
-  static constexpr int kRegsSoftmax = W == 2 ? 192 : W == 3 ? 128 : 96, kRegsOther = W == 2 ? 64 : 48;
+  static constexpr int kRegs = W == 2 ? 128 : W == 4 ? 80 : 64;
+  static constexpr int kRegsSoftmax = W == 2 ? 192 : W == 4 ? 96 : 72, kRegsOther = W == 2 ? 64 : W == 4 ? 48 : 40;
   static_assert(4 * W * kRegsSoftmax + 8 * kRegsOther <= kWarps * kRegs, "registers");
   // The terms of P', and where tensor memory has room those of Q, side by side are
   // the columns of one product with several sums: what an MMA of few columns costs
@@ -827,8 +827,12 @@ sv_status launch_q8(const KlParams &P, const Q8Maps &M, int C, cudaStream_t st) 
   return check_launch("spec_verify_attn_q8 launch");
 }
 
-// Softmax warpgroups: as many as keep 16 rows or fewer each.
-int q8_groups(int rows) { return rows <= 32 ? 2 : rows <= 48 ? 3 : 4; }
+// Softmax warpgroups: 8 rows each as far as threads go, then 16. A step is a chain
+// of waits that more warpgroups with shorter columns overlap better. 64 sequences of
+// 4750 keys, 8 kv heads, 32 rows: four of 8 rows 116.2 us, two of 16 126.1; 40 rows:
+// six of 8 144.7 us, three of 16 148.0 (1024..8192 keys: 152.7, 160.9). A window of
+// 4096 keys of 16 sequences loses by it, 54.4 against 53.4.
+int q8_groups(int rows) { return rows <= 16 ? 2 : rows <= 32 ? 4 : rows <= 48 ? 6 : 4; }
 
 // Query rows of a kv head on the tensor cores: 64 share a pass over the cache.
 constexpr int64_t kMaxRows = 1 << 14;
@@ -916,12 +920,10 @@ extern "C" sv_status spec_verify_attn_q8(const void *q, sv_dtype q_dtype, const 
   P.withhold = test_withhold();
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int each = kl_first(p.Rg, W);   // rows of a softmax warpgroup
-  const sv_status r2 = W == 3       ? launch_q8<16, 3>(P, M, p.C, st)
-                       : W == 4     ? launch_q8<16, 4>(P, M, p.C, st)
-                       : each <= 4  ? launch_q8<4, 2>(P, M, p.C, st)
-                       : each <= 8  ? launch_q8<8, 2>(P, M, p.C, st)
-                       : each <= 12 ? launch_q8<12, 2>(P, M, p.C, st)
-                                    : launch_q8<16, 2>(P, M, p.C, st);
+  const sv_status r2 = W == 6     ? launch_q8<8, 6>(P, M, p.C, st)
+                       : W == 2   ? (each <= 4 ? launch_q8<4, 2>(P, M, p.C, st) : launch_q8<8, 2>(P, M, p.C, st))
+                       : each <= 8 ? launch_q8<8, 4>(P, M, p.C, st)
+                                   : launch_q8<16, 4>(P, M, p.C, st);
   if (r2 != SV_OK || p.NR == 1) return r2;
   launch_k(kl_merge_kernel, dim3((p.NR - 1) * H_kv * p.RG, (p.Rg + kMergeWarps - 1) / kMergeWarps),
            dim3(32 * kMergeWarps), 0, st, 1, P);
