@@ -26,7 +26,7 @@ struct RopeArgs {
   const int32_t *positions, *seq_lens;
   int n_new, d, r, offset;
   int units, rotated;      // pieces of work of a head, the first `rotated` of them pairs
-  unsigned magic;          // floor(x / units) = x magic >> 32 (0: units is 1)
+  int lanes, side;         // threads of a head, heads side by side
   int heads;               // of a CTA
   bool copy[2];            // the dims that stay are copied
   float m;
@@ -50,32 +50,81 @@ __device__ __forceinline__ void store_v(T *p, const T (&x)[V]) {
   else p[0] = x[0];
 }
 
-// A CTA takes `heads` heads (queries first, then keys) of one row: the cosines
-// and sines of the row once, a thread a pair, then pieces of V pairs (two
-// 16-byte vectors, or two elements where something is not aligned to 16 bytes)
-// and of V dims that stay.
-constexpr int kRopeThreads = 256;
+// A CTA takes `heads` heads (queries first, then keys) of one row, in pieces: V
+// pairs, or two vectors of V dims that stay (V: a 16-byte vector, or one element
+// where something is not aligned to 16 bytes). A thread takes the same piece of
+// every side-th head, kRopeBatch heads at a time: what a piece needs besides its
+// data is worked out once (with places worked out per piece the kernel was short of
+// instructions, not of bandwidth). The first batch is read before the row's cosines
+// and sines are made, a thread a pair.
+// Bound by memory: 32752 rows of 72 heads of 128 bf16, 64 dims rotated, 1.21 GB
+// read and written, take 171 us (282 with places per piece; batches of 2 heads 188,
+// of 4 181); 160 rows of 129 heads of 576, 48 MB, 13.4 us with the launch (23.7).
+constexpr int kRopeThreads = 256, kRopeBatch = 3;
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ __align__(16) float s_cos[SV_ROPE_MAX_DIM / 2], s_sin[SV_ROPE_MAX_DIM / 2];
   pdl_trigger();
-  const int64_t rowi = blockIdx.x;
-  const int b = (int)(rowi / a.n_new), j = (int)(rowi % a.n_new);
+  const unsigned rowi = blockIdx.x;
+  const int b = (int)(rowi / (unsigned)a.n_new), j = (int)(rowi % (unsigned)a.n_new);
+  const int hh = (int)(threadIdx.x / (unsigned)a.lanes);
+  int u = (int)threadIdx.x - hh * a.lanes;
+  const int H_q = a.H[0], h0 = blockIdx.y * a.heads + hh, h1 = min((blockIdx.y + 1) * a.heads, H_q + a.H[1]);
+  const T *src[2];
+  T *dst[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {   // (of head 0, counted over both)
+    src[w] = static_cast<const T *>(a.src[w]) + b * a.seq[w] + j * a.row[w] - (w ? H_q * a.head[1] : 0);
+    dst[w] = static_cast<T *>(a.dst[w]) + b * a.seq[2 + w] + j * a.row[2 + w] - (w ? H_q * a.head[3] : 0);
+  }
+  // (positions may be what the kernel before writes; the lengths never are)
   int pos = 0;
   bool ok = true;
-  // (positions may be what the kernel before writes; the lengths never are)
   if (!a.positions) {
     const int L = a.seq_lens[b];
     ok = L >= a.n_new;
     pos = L - a.n_new + j;
   }
   pdl_wait();
-  if (a.positions) pos = a.positions[rowi];
   if (!ok) {
     if (threadIdx.x == 0 && blockIdx.y == 0) atomic_or_status(a.status, SV_DEV_BAD_SEQ_LEN);
     return;
   }
-  for (int i = threadIdx.x; i < a.r / 2; i += kRopeThreads) {
+  if (a.positions) pos = a.positions[rowi];
+  const int stay = a.d - a.r;
+  auto dim = [&](int k) { return k < a.offset ? k : k + a.r; };   // of the k-th that stays
+  alignas(16) T lo[kRopeBatch][V], hi[kRopeBatch][V];
+  int at0 = 0, at1 = 0, h = h0;
+  bool two = true;
+  auto place = [&] {   // where a piece's two vectors are in its head
+    if (u < a.rotated) {
+      at0 = a.offset + u * (INTER ? 2 * V : V);
+      at1 = at0 + (INTER ? V : a.r / 2);
+    } else {
+      const int c = (u - a.rotated) * V, c1 = c + (a.units - a.rotated) * V;
+      at0 = dim(c);
+      at1 = dim(c1);
+      two = c1 < stay;
+    }
+  };
+  auto fetch = [&] {
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k) {
+      const int head = h + k * a.side;
+      if (head >= h1) break;
+      const bool key = head >= H_q;
+      if (u >= a.rotated && !a.copy[key]) continue;
+      const T *p = (key ? src[1] : src[0]) + head * (key ? a.head[1] : a.head[0]);
+      load_v<T, V>(p + at0, lo[k]);
+      if (two) load_v<T, V>(p + at1, hi[k]);
+    }
+  };
+  bool live = hh < a.side && u < a.units && h < h1;
+  if (live) {
+    place();
+    fetch();
+  }
+  for (int i = threadIdx.x; i < a.r / 2; i += blockDim.x) {
     const unsigned long long turn = (unsigned long long)(long long)pos * a.turns[i];
     float s, c;
     sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &c);
@@ -83,37 +132,50 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     s_sin[i] = s * a.m;
   }
   __syncthreads();
-  const int h0 = blockIdx.y * a.heads, n = min(a.heads, a.H[0] + a.H[1] - h0) * a.units;
-  for (int x = threadIdx.x; x < n; x += kRopeThreads) {
-    const int hh = a.magic ? (int)__umulhi((unsigned)x, a.magic) : x, u = x - hh * a.units;
-    int h = h0 + hh;
-    const int w = h >= a.H[0] ? 1 : 0;
-    if (w) h -= a.H[0];
-    const T *src = static_cast<const T *>(a.src[w]) + b * a.seq[w] + j * a.row[w] + h * a.head[w];
-    T *dst = static_cast<T *>(a.dst[w]) + b * a.seq[2 + w] + j * a.row[2 + w] + h * a.head[2 + w];
-    alignas(16) T lo[V], hi[V];
+  while (live) {
+    float c[V], s[V];
     if (u < a.rotated) {
-      const int i = u * V;   // first pair
-      const int at = a.offset + (INTER ? 2 * i : i), step = INTER ? V : a.r / 2;
-      load_v<T, V>(src + at, lo);
-      load_v<T, V>(src + at + step, hi);
+      if constexpr (V > 1) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        // pair k: interleaved, elements 2k and 2k + 1 of the 2 V in a row
-        T &ta = !INTER ? lo[k] : 2 * k < V ? lo[2 * k] : hi[2 * k - V];
-        T &tb = !INTER ? hi[k] : 2 * k + 1 < V ? lo[2 * k + 1] : hi[2 * k + 1 - V];
-        const float xa = to_f32(ta), xb = to_f32(tb), c = s_cos[i + k], s = s_sin[i + k];
-        ta = from_f32<T>(xa * c - xb * s);
-        tb = from_f32<T>(xb * c + xa * s);
+        for (int e = 0; e < V; e += 4) {
+          *reinterpret_cast<float4 *>(c + e) = *reinterpret_cast<const float4 *>(&s_cos[u * V + e]);
+          *reinterpret_cast<float4 *>(s + e) = *reinterpret_cast<const float4 *>(&s_sin[u * V + e]);
+        }
+      } else {
+        c[0] = s_cos[u];
+        s[0] = s_sin[u];
       }
-      store_v<T, V>(dst + at, lo);
-      store_v<T, V>(dst + at + step, hi);
-    } else if (a.copy[w]) {
-      int at = (u - a.rotated) * V;
-      if (at >= a.offset) at += a.r;
-      load_v<T, V>(src + at, lo);
-      store_v<T, V>(dst + at, lo);
     }
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k) {
+      const int head = h + k * a.side;
+      if (head >= h1) break;
+      const bool key = head >= H_q;
+      if (u < a.rotated) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          // pair e: interleaved, elements 2e and 2e + 1 of the 2 V in a row
+          T &ta = !INTER ? lo[k][e] : 2 * e < V ? lo[k][2 * e] : hi[k][2 * e - V];
+          T &tb = !INTER ? hi[k][e] : 2 * e + 1 < V ? lo[k][2 * e + 1] : hi[k][2 * e + 1 - V];
+          const float xa = to_f32(ta), xb = to_f32(tb);
+          ta = from_f32<T>(xa * c[e] - xb * s[e]);
+          tb = from_f32<T>(xb * c[e] + xa * s[e]);
+        }
+      } else if (!a.copy[key]) {
+        continue;
+      }
+      T *p = (key ? dst[1] : dst[0]) + head * (key ? a.head[3] : a.head[2]);
+      store_v<T, V>(p + at0, lo[k]);
+      if (two) store_v<T, V>(p + at1, hi[k]);
+    }
+    h += kRopeBatch * a.side;
+    if (h >= h1) {
+      h = h0;
+      u += a.lanes;
+      live = u < a.units;
+      if (live) place();
+    }
+    if (live) fetch();
   }
 }
 
@@ -122,21 +184,25 @@ sv_status launch_rope(RopeArgs &a, int B, bool inter, bool vec, cudaStream_t s) 
   constexpr int V = 16 / (int)sizeof(T);
   const int v = vec ? V : 1;
   a.rotated = a.r / 2 / v;
-  a.units = a.rotated + (a.copy[0] || a.copy[1] ? (a.d - a.r) / v : 0);
-  a.magic = a.units > 1 ? (unsigned)(0x100000000ull / (unsigned)a.units + 1) : 0;
+  a.units = a.rotated + (a.copy[0] || a.copy[1] ? ((a.d - a.r) / v + 1) / 2 : 0);
   const int H = a.H[0] + a.H[1];
   const int64_t rows = (int64_t)B * a.n_new;
-  // Many rows: a CTA takes all heads of a row (up to 2^14 pieces). Few: a piece
-  // or two a thread, so that one token's heads spread over the SMs.
-  int64_t per = rows >= 1024 ? (1 << 14) : 2 * kRopeThreads;
-  a.heads = (int)std::max<int64_t>(1, std::min<int64_t>(H, per / a.units));
+  a.lanes = std::min(a.units, kRopeThreads);
+  // Heads side by side as threads go, and batches in turn: all of a row's, if
+  // that leaves four CTAs an SM; else as many as leave that, and a batch at most.
+  const int side = kRopeThreads / a.lanes;
+  const int64_t want = (rows * H + 607) / 608;   // heads of a CTA when there are four an SM
+  a.heads = rows >= 608 ? H : (int)std::min<int64_t>(std::min<int64_t>(H, want), (int64_t)side * kRopeBatch);
+  const int turns = (a.heads + side - 1) / side;
+  a.side = (a.heads + turns - 1) / turns;
+  const int threads = (a.side * a.lanes + 31) / 32 * 32;
   const dim3 grid((unsigned)rows, (unsigned)((H + a.heads - 1) / a.heads));
   if (inter) {
-    if (vec) launch_k(rope_kernel<T, V, true>, grid, dim3(kRopeThreads), 0, s, 1, a);
-    else launch_k(rope_kernel<T, 1, true>, grid, dim3(kRopeThreads), 0, s, 1, a);
+    if (vec) launch_k(rope_kernel<T, V, true>, grid, dim3(threads), 0, s, 1, a);
+    else launch_k(rope_kernel<T, 1, true>, grid, dim3(threads), 0, s, 1, a);
   } else {
-    if (vec) launch_k(rope_kernel<T, V, false>, grid, dim3(kRopeThreads), 0, s, 1, a);
-    else launch_k(rope_kernel<T, 1, false>, grid, dim3(kRopeThreads), 0, s, 1, a);
+    if (vec) launch_k(rope_kernel<T, V, false>, grid, dim3(threads), 0, s, 1, a);
+    else launch_k(rope_kernel<T, 1, false>, grid, dim3(threads), 0, s, 1, a);
   }
   return check_launch("spec_rope launch");
 }
