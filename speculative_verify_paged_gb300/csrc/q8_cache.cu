@@ -29,10 +29,18 @@ struct Q8AppendArgs {
 constexpr int kEaWarps = 8;
 constexpr int kEaBatch = 4;   // pieces of 16 elements that a lane holds
 
-// Sixteen consecutive elements of a row; `vec`: 16-byte aligned.
+// Sixteen consecutive elements of a row, aligned to `to` bytes (32, 16, or less).
 template <typename T>
-__device__ __forceinline__ void load16(const T *p, bool vec, T (&x)[16]) {
-  if (vec) {
+__device__ __forceinline__ void load16(const T *p, int to, T (&x)[16]) {
+  uint32_t *w = reinterpret_cast<uint32_t *>(x);
+  if (to == 32) {
+#pragma unroll
+    for (int k = 0; k < 4 * (int)sizeof(T); k += 8)
+      asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                   : "=r"(w[k]), "=r"(w[k + 1]), "=r"(w[k + 2]), "=r"(w[k + 3]), "=r"(w[k + 4]), "=r"(w[k + 5]),
+                     "=r"(w[k + 6]), "=r"(w[k + 7])
+                   : "l"(reinterpret_cast<const uint32_t *>(p) + k));
+  } else if (to == 16) {
 #pragma unroll
     for (int k = 0; k < (int)sizeof(T); ++k) reinterpret_cast<uint4 *>(x)[k] = reinterpret_cast<const uint4 *>(p)[k];
   } else {
@@ -40,13 +48,52 @@ __device__ __forceinline__ void load16(const T *p, bool vec, T (&x)[16]) {
     for (int k = 0; k < 16; ++k) x[k] = p[k];
   }
 }
-
-// The largest magnitude of x and m, NaN left out.
 template <typename T>
-__device__ __forceinline__ float amax16(const T (&x)[16], float m) {
+__device__ __forceinline__ void store16(T *p, int to, const T (&x)[16]) {
+  const uint32_t *w = reinterpret_cast<const uint32_t *>(x);
+  if (to == 32) {
 #pragma unroll
-  for (int k = 0; k < 16; ++k) m = fmaxf(m, fabsf(to_f32(x[k])));
+    for (int k = 0; k < 4 * (int)sizeof(T); k += 8)
+      asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(w[k]), "r"(w[k + 1]), "r"(w[k + 2]),
+                   "r"(w[k + 3]), "r"(w[k + 4]), "r"(w[k + 5]), "r"(w[k + 6]), "r"(w[k + 7]),
+                   "l"(reinterpret_cast<uint32_t *>(p) + k)
+                   : "memory");
+  } else if (to == 16) {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T); ++k) reinterpret_cast<uint4 *>(p)[k] = reinterpret_cast<const uint4 *>(x)[k];
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) p[k] = x[k];
+  }
+}
+
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The largest magnitude of x and m; a NaN among them stays.
+__device__ __forceinline__ float amax16(const __nv_bfloat16 (&x)[16], float m) {
+  __nv_bfloat162 t = __habs2(reinterpret_cast<const __nv_bfloat162 *>(x)[0]);
+#pragma unroll
+  for (int k = 1; k < 8; ++k) t = __hmax2_nan(t, __habs2(reinterpret_cast<const __nv_bfloat162 *>(x)[k]));
+  return fmax_nan(fmax_nan(__low2float(t), __high2float(t)), m);
+}
+__device__ __forceinline__ float amax16(const float (&x)[16], float m) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) m = fmax_nan(m, fabsf(x[k]));
   return m;
+}
+
+// NaN as 0.
+template <typename T>
+__device__ __forceinline__ void drop_nan(T (&x)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float v = to_f32(x[k]);
+    if (v != v) x[k] = T(0.f);
+  }
 }
 
 // The smallest e with a <= 448 * 2^e (448 = 1.75 * 2^8), within +-32.
@@ -56,9 +103,9 @@ __device__ __forceinline__ int q8_exponent(float a) {
   return min(max(e, -kQ8MaxExp), kQ8MaxExp);
 }
 
-// Codes of sixteen elements, x / s (inv = 1 / s where s is a power of two, else 0).
-template <typename T>
-__device__ __forceinline__ uint4 codes16(const T (&x)[16], float s, float inv) {
+// Codes of sixteen elements: x by `by`, or (DIV) over it.
+template <bool DIV, typename T>
+__device__ __forceinline__ uint4 codes16(const T (&x)[16], float by) {
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -66,7 +113,7 @@ __device__ __forceinline__ uint4 codes16(const T (&x)[16], float s, float inv) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float v = to_f32(x[4 * k + e]);
-      y[e] = v == v ? (inv != 0.f ? v * inv : __fdiv_rn(v, s)) : 0.f;
+      y[e] = DIV ? __fdiv_rn(v, by) : v * by;
     }
     w[k] = f32x2_to_e4m3x2(y[0], y[1]) | (f32x2_to_e4m3x2(y[2], y[3]) << 16);
   }
@@ -78,14 +125,19 @@ __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t codes) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// A warp takes the new rows of one (block written, kv head) of K or of V.
+// A warp takes the new rows of one (block written, kv head) of K or of V: largest
+// magnitude and codes from one read, the rows in registers between.
+// Bound by memory, with the instructions not far behind: 16 prompts of 2047 rows, 8
+// kv heads of 128, 134 MB read and 67 MB written, take 36 us (52 with a division
+// chosen per element; 16-byte reads, which fetch each sector twice, and NaN looked
+// for per element cost another 10).
 template <typename T>
-__global__ void __launch_bounds__(32 * kEaWarps) q8_append_kernel(const __grid_constant__ Q8AppendArgs a, bool vec) {
+__global__ void __launch_bounds__(32 * kEaWarps, 4) q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int to) {
   pdl_trigger();
   const int lane = threadIdx.x & 31, b = blockIdx.y;
-  const int64_t unit = (int64_t)blockIdx.x * kEaWarps + (threadIdx.x >> 5);
-  const int kv = (int)(unit & 1), g = (int)((unit >> 1) % a.H_kv);
-  const int64_t p = (unit >> 1) / a.H_kv;
+  const unsigned unit = blockIdx.x * kEaWarps + (threadIdx.x >> 5);
+  const int kv = (int)(unit & 1), g = (int)((unit >> 1) % (unsigned)a.H_kv);
+  const int64_t p = (unit >> 1) / (unsigned)a.H_kv;
   const int bs = a.bs, d = a.d, L = a.seq_lens[b];
   const bool len_ok = L >= a.n_new && L <= a.max_blocks * bs;
   const int first = L - a.n_new;
@@ -98,33 +150,46 @@ __global__ void __launch_bounds__(32 * kEaWarps) q8_append_kernel(const __grid_c
   pdl_wait();
   if (!len_ok && lane == 0 && unit == 0) atomic_or_status(a.status, SV_DEV_BAD_SEQ_LEN);
   if (!mine) return;
-  if (phys < 0 || phys >= a.num_blocks) {
-    if (lane == 0) atomic_or_status(a.status, SV_DEV_BAD_BLOCK);
-    return;
-  }
   const int C = d / 16, n = (s1 - s0) * C;   // pieces of 16 elements in a row, and in all
   const int64_t row_stride = (int64_t)a.H_kv * d;
   const T *src = static_cast<const T *>(a.src[kv]) + (((int64_t)b * a.n_new + (page * bs + s0 - first)) * a.H_kv + g) * d;
-  uint8_t *pg = a.cache[kv] + (int64_t)phys * a.block_stride;
-  uint8_t *codes = pg + (int64_t)g * bs * d;
-  float *scale_at = reinterpret_cast<float *>(pg + q8_scale_offset(a.H_kv, d, bs)) + g;
   alignas(16) T x[kEaBatch][16];
   auto fetch = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < kEaBatch; ++k) {
       const int i = i0 + 32 * k + lane;
-      if (i < n) load16(src + (int64_t)(i / C) * row_stride + (i % C) * 16, vec, x[k]);
+      if (i < n) load16(src + (int64_t)(i / C) * row_stride + (i % C) * 16, to, x[k]);
     }
   };
   const bool once = n <= 32 * kEaBatch;   // the rows stay in registers
-  float top = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32 * kEaBatch) {
-    fetch(i0);
-#pragma unroll
-    for (int k = 0; k < kEaBatch; ++k)
-      if (i0 + 32 * k + lane < n) top = amax16(x[k], top);
+  fetch(0);
+  if (phys < 0 || phys >= a.num_blocks) {
+    if (lane == 0) atomic_or_status(a.status, SV_DEV_BAD_BLOCK);
+    return;
   }
-  top = warp_max(top);
+  uint8_t *pg = a.cache[kv] + (int64_t)phys * a.block_stride;
+  uint8_t *codes = pg + (int64_t)g * bs * d;
+  float *scale_at = reinterpret_cast<float *>(pg + q8_scale_offset(a.H_kv, d, bs)) + g;
+  auto drop = [&] {
+#pragma unroll
+    for (int k = 0; k < kEaBatch; ++k) drop_nan(x[k]);
+  };
+  auto largest = [&](bool nan) {
+    float top = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32 * kEaBatch) {
+      if (i0 > 0 || (nan && !once)) fetch(i0);
+      if (nan) drop();
+#pragma unroll
+      for (int k = 0; k < kEaBatch; ++k)
+        if (i0 + 32 * k + lane < n) top = amax16(x[k], top);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    return top;
+  };
+  float top = largest(false);
+  const bool nan = top != top;   // rare: once more without it
+  if (nan) top = largest(true);
   const float fresh = __uint_as_float((uint32_t)(127 + q8_exponent(top)) << 23);
   float s = fresh;
   if (s0 > 0) {
@@ -153,11 +218,17 @@ __global__ void __launch_bounds__(32 * kEaWarps) q8_append_kernel(const __grid_c
   const uint32_t bits = __float_as_uint(s);
   const float inv = (bits & 0x7fffffu) == 0 ? __uint_as_float((254u << 23) - bits) : 0.f;
   for (int i0 = 0; i0 < n; i0 += 32 * kEaBatch) {
-    if (!once) fetch(i0);
+    if (!once) {
+      fetch(i0);
+      if (nan) drop();
+    }
 #pragma unroll
     for (int k = 0; k < kEaBatch; ++k) {
       const int i = i0 + 32 * k + lane;
-      if (i < n) reinterpret_cast<uint4 *>(codes)[s0 * C + i] = codes16(x[k], s, inv);
+      if (i >= n) continue;
+      uint4 *at = reinterpret_cast<uint4 *>(codes) + s0 * C + i;
+      if (inv != 0.f) *at = codes16<false>(x[k], inv);
+      else *at = codes16<true>(x[k], s);
     }
   }
 }
@@ -173,7 +244,7 @@ struct Q8GatherArgs {
 
 // Sixteen codes times s to sixteen consecutive elements of a row.
 template <typename T>
-__device__ __forceinline__ void write16(T *dst, bool vec, uint4 codes, float s) {
+__device__ __forceinline__ void write16(T *dst, int to, uint4 codes, float s) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
   alignas(16) T v[16];
 #pragma unroll
@@ -186,45 +257,39 @@ __device__ __forceinline__ void write16(T *dst, bool vec, uint4 codes, float s) 
       reinterpret_cast<__nv_bfloat162 *>(v)[k] = __floats2bfloat162_rn(f.x * s, f.y * s);
     }
   }
-  if (vec) {
-#pragma unroll
-    for (int k = 0; k < (int)sizeof(T); ++k) reinterpret_cast<uint4 *>(dst)[k] = reinterpret_cast<const uint4 *>(v)[k];
-  } else {
-#pragma unroll
-    for (int k = 0; k < 16; ++k) dst[k] = v[k];
-  }
+  store16(dst, to, v);
 }
 
 // A warp takes one block of one kv head, of K or of V. Rows outside the
 // sequence, and those of a block with a number out of range, are written as
 // zeros.
+// Bound by memory: 16 prefixes of 4096 .. 8192 rows, 8 kv heads of 128, 739 MB read
+// and written, take 114 us (144 with 16-byte stores, which write each sector in two
+// pieces; two blocks a warp 116, four 118).
 constexpr int kEgWarps = 8;
-constexpr int kEgBatch = 4;
+constexpr int kEgBatch = 4;   // pieces of 16 codes that a lane holds
 template <typename T>
-__global__ void __launch_bounds__(32 * kEgWarps) q8_gather_kernel(const __grid_constant__ Q8GatherArgs a, bool vec) {
+__global__ void __launch_bounds__(32 * kEgWarps, 5) q8_gather_kernel(const __grid_constant__ Q8GatherArgs a, int to) {
   pdl_trigger();
   const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * kEgWarps + (threadIdx.x >> 5);
-  const int kv = (int)(unit & 1), g = (int)((unit >> 1) % a.H_kv);
-  const int64_t p = (unit >> 1) / a.H_kv;
+  const unsigned unit = blockIdx.x * kEgWarps + (threadIdx.x >> 5);
+  const int kv = (int)(unit & 1), g = (int)((unit >> 1) % (unsigned)a.H_kv);
+  const int p = (int)((unit >> 1) / (unsigned)a.H_kv);
   const int bs = a.bs, d = a.d;
   const int L = a.seq_lens[b], start = a.start[b];
-  pdl_wait();
-  if (p >= a.pages) return;
   const bool len_ok = L >= 0 && L <= a.max_blocks * bs;
-  if (!len_ok && lane == 0 && unit == 0) atomic_or_status(a.status, SV_DEV_BAD_SEQ_LEN);
   const int64_t page = (start >= 0 ? start / bs : -((bs - 1 - (int64_t)start) / bs)) + p;
   const int64_t i0 = page * bs - start;   // output row of slot 0
   const int r0 = (int)max((int64_t)0, -i0), r1 = (int)min((int64_t)bs, a.n_rows - i0);   // slots to write
-  if (r0 >= r1) return;
-  int held = len_ok && page >= 0 ? (int)min((int64_t)bs, max((int64_t)0, L - page * bs)) : 0;   // slots that hold rows
-  int phys = 0;
-  if (held > 0) {
-    phys = a.block_table[(int64_t)b * a.max_blocks + page];
-    if (phys < 0 || phys >= a.num_blocks) {
-      if (lane == 0) atomic_or_status(a.status, SV_DEV_BAD_BLOCK);
-      phys = held = 0;
-    }
+  const bool mine = p < a.pages && r0 < r1;
+  int held = mine && len_ok && page >= 0 ? (int)min((int64_t)bs, max((int64_t)0, L - page * bs)) : 0;   // slots that hold rows
+  int phys = held > 0 ? a.block_table[(int64_t)b * a.max_blocks + page] : 0;
+  pdl_wait();
+  if (!len_ok && lane == 0 && unit == 0) atomic_or_status(a.status, SV_DEV_BAD_SEQ_LEN);
+  if (!mine) return;
+  if (phys < 0 || phys >= a.num_blocks) {
+    if (lane == 0) atomic_or_status(a.status, SV_DEV_BAD_BLOCK);
+    phys = held = 0;
   }
   const uint8_t *pg = a.cache[kv] + (int64_t)phys * a.block_stride;
   const uint4 *codes = reinterpret_cast<const uint4 *>(pg + (int64_t)g * bs * d);
@@ -243,7 +308,7 @@ __global__ void __launch_bounds__(32 * kEgWarps) q8_gather_kernel(const __grid_c
 #pragma unroll
     for (int k = 0; k < kEgBatch; ++k) {
       const int i = k0 + 32 * k + lane;
-      if (i < r1 * C) write16(out + (i / C) * stride + (i % C) * 16, vec, w[k], s);
+      if (i < r1 * C) write16(out + (i / C) * stride + (i % C) * 16, to, w[k], s);
     }
   }
 }
@@ -298,13 +363,13 @@ extern "C" sv_status kv_block_append_q8(const void *k_new, const void *v_new, sv
   a.block_table = block_table; a.seq_lens = seq_lens; a.max_blocks = max_blocks_per_seq; a.n_new = n_new;
   a.H_kv = H_kv; a.d = d_head; a.bs = block_size; a.num_blocks = num_blocks; a.status = dev_status;
   a.pages = (int)std::min<int64_t>(((int64_t)n_new + block_size - 2) / block_size + 1, max_blocks_per_seq);
-  const int64_t ctas = ((int64_t)a.pages * H_kv * 2 + kEaWarps - 1) / kEaWarps;
-  if (ctas >= (1ll << 31)) return fail(SV_ERR_UNSUPPORTED, "kv_block_append_q8: too many rows");
-  const bool vec = aligned(k_new, 16) && aligned(v_new, 16);
+  const int64_t units = (int64_t)a.pages * H_kv * 2, ctas = (units + kEaWarps - 1) / kEaWarps;
+  if (units >= (1ll << 31)) return fail(SV_ERR_UNSUPPORTED, "kv_block_append_q8: too many rows");
+  const int to = aligned(k_new, 32) && aligned(v_new, 32) ? 32 : aligned(k_new, 16) && aligned(v_new, 16) ? 16 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid((unsigned)ctas, B), block(32 * kEaWarps);
-  if (new_dtype == SV_F32) launch_k(q8_append_kernel<float>, grid, block, 0, s, 1, a, vec);
-  else launch_k(q8_append_kernel<__nv_bfloat16>, grid, block, 0, s, 1, a, vec);
+  if (new_dtype == SV_F32) launch_k(q8_append_kernel<float>, grid, block, 0, s, 1, a, to);
+  else launch_k(q8_append_kernel<__nv_bfloat16>, grid, block, 0, s, 1, a, to);
   return check_launch("kv_block_append_q8 launch");
 }
 
@@ -332,12 +397,12 @@ extern "C" sv_status kv_block_gather_q8(const void *k_cache, const void *v_cache
   a.max_blocks = max_blocks_per_seq; a.n_rows = n_rows; a.H_kv = H_kv; a.d = d_head; a.bs = block_size;
   a.num_blocks = num_blocks; a.status = dev_status;
   a.pages = (int)(((int64_t)n_rows + block_size - 2) / block_size + 1);
-  const int64_t ctas = ((int64_t)a.pages * H_kv * 2 + kEgWarps - 1) / kEgWarps;
-  if (ctas >= (1ll << 31)) return fail(SV_ERR_UNSUPPORTED, "kv_block_gather_q8: too many rows");
-  const bool vec = aligned(k_out, 16) && aligned(v_out, 16);
+  const int64_t units = (int64_t)a.pages * H_kv * 2, ctas = (units + kEgWarps - 1) / kEgWarps;
+  if (units >= (1ll << 31)) return fail(SV_ERR_UNSUPPORTED, "kv_block_gather_q8: too many rows");
+  const int to = aligned(k_out, 32) && aligned(v_out, 32) ? 32 : aligned(k_out, 16) && aligned(v_out, 16) ? 16 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid((unsigned)ctas, B), block(32 * kEgWarps);
-  if (out_dtype == SV_F32) launch_k(q8_gather_kernel<float>, grid, block, 0, s, 1, a, vec);
-  else launch_k(q8_gather_kernel<__nv_bfloat16>, grid, block, 0, s, 1, a, vec);
+  if (out_dtype == SV_F32) launch_k(q8_gather_kernel<float>, grid, block, 0, s, 1, a, to);
+  else launch_k(q8_gather_kernel<__nv_bfloat16>, grid, block, 0, s, 1, a, to);
   return check_launch("kv_block_gather_q8 launch");
 }
