@@ -36,6 +36,7 @@ namespace sv {
 namespace {
 
 constexpr int kTile = kTK * kD;            // bytes of a tile of K or V
+constexpr int kEdge = 16;                  // of a tile: some query does not see all its keys
 // A row's reference puts its largest weight at 2^kTop and moves once one exceeds
 // 2^kMove (f16 ends at 65504, which e5m2 takes for 57344 and two smaller terms).
 constexpr float kTop = 5.f, kMove = 15.9f;
@@ -121,8 +122,8 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t page_full[kChunks], page_empty[kChunks], scale_full[kChunks];
   __shared__ int s_phys[kChunks * kChunk * kTP];   // blocks of the tiles ahead
-  __shared__ __align__(16) float4 s_scale[kChunks * kChunk * kTP];   // their scales: of K, log2 of V's, 1 / V's
-  __shared__ int s_flag[kChunks * kChunk];   // kFirst, kLast, kEnd, kSecond, blocks of the tile << 8
+  __shared__ __align__(16) float4 s_scale[kChunks * kChunk * kTP];   // their scales: of K, log2 of V's, 1 / V's; not 0 in an edge tile
+  __shared__ int s_flag[kChunks * kChunk];   // kFirst, kLast, kEnd, kSecond, kEdge, blocks of the tile << 8
   // rows of V that no query sees: [z0, z1) and from z2 on, z0 | z1 << 8 | z2 << 16
   __shared__ int s_zero[kChunks * kChunk];
   __shared__ __align__(8) uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS];
@@ -251,14 +252,15 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
         if (lane < n) {
           const int tt = ti + lane, at = c % kChunks * kChunk + filled + lane;
           const int key0 = (it.tile0 + tt) * kTK, nv = min(kTP, it.span.nblk - (it.tile0 + tt) * kTP);
-          s_flag[at] = (tt == 0 ? kFirst : 0) | (tt == it.ntiles - 1 ? kLast | kEnd : 0) | (tt % T == T - 1 ? kEnd : 0) |
-                       (tt % T ? kSecond : 0) | nv << 8;
           int z0 = 0, z1 = 0;
+          const bool edge = key0 + kTK - 1 > it.span.L - P.n_new || (P.window > 0 && key0 < it.span.L - P.window);
           if (P.window > 0) {   // between the sinks and the oldest query's window
             z0 = min(max(P.sinks - key0, 0), kTK);
             z1 = min(max(it.span.L - P.n_new - P.window + 1 - key0, 0), kTK);
             if (z0 >= z1) z0 = z1 = 0;
           }
+          s_flag[at] = (tt == 0 ? kFirst : 0) | (tt == it.ntiles - 1 ? kLast | kEnd : 0) | (tt % T == T - 1 ? kEnd : 0) |
+                       (tt % T ? kSecond : 0) | (edge ? kEdge : 0) | nv << 8;
           s_zero[at] = z0 | z1 << 8 | min(it.span.L - key0, kTK) << 16;
         }
         filled += n;
@@ -295,7 +297,8 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
 #pragma unroll
       for (int k = 0; k < kE; ++k) {
         const float v = q8_scale(vs[k]);
-        if (lane + 32 * k < n) s_scale[at + lane + 32 * k] = make_float4(q8_scale(ks[k]), lg2f(v), rcpf(v), 0.f);
+        if (lane + 32 * k < n)
+          s_scale[at + lane + 32 * k] = make_float4(q8_scale(ks[k]), lg2f(v), rcpf(v), s_flag[(at + lane + 32 * k) / kTP] & kEdge ? 1.f : 0.f);
       }
       __syncwarp();
       if (lane == 0) {
@@ -506,14 +509,16 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
     // The epilogue's second part, a head dim per thread: O of an item, once its
     // last P V is done; it is taken after the next item's first step, which hides
     // that P V.
-    struct { bool pending, whole; uint32_t step; int i; int64_t ent; } done = {false, false, 0, 0, 0};
+    bool pending = false;   // (of item i - 1, whose last step was step - 1)
     auto finish = [&] {
-      done.pending = false;
-      ok = __all_sync(0xffffffffu, kl_wait(&pv_done[done.step & 1], (done.step >> 1) & 1, abf, P.wait_ns)) && ok;
+      pending = false;
+      const int buf = (i - 1) & 1, row = (i - 1) % 3, kind = s_item[row].w;
+      const int64_t ent = 2 * (int64_t)blockIdx.x + (kind & kOpening ? 0 : 1);
+      ok = __all_sync(0xffffffffu, kl_wait(&pv_done[(step - 1) & 1], ((step - 1) >> 1) & 1, abf, P.wait_ns)) && ok;
       if (!ok) return;
       t5_fence_after();
       float o[NC], o1[NC], o2[NC];
-      const uint32_t at = lanes + Cfg::kOCol + (done.i & 1) * Cfg::kOCols + c_first;
+      const uint32_t at = lanes + Cfg::kOCol + buf * Cfg::kOCols + c_first;
       t5_ldn(at, reinterpret_cast<uint32_t(&)[NC]>(o));
       t5_ldn(at + N, reinterpret_cast<uint32_t(&)[NC]>(o1));
       t5_ldn(at + 2 * N, reinterpret_cast<uint32_t(&)[NC]>(o2));
@@ -524,24 +529,22 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
         if (k >= live) break;
-        const float x = fmaf(o2[k], kCut, o[k] + o1[k]) * s_fin[done.i & 1][c_first + k];
-        if (done.whole)
-          static_cast<__nv_bfloat16 *>(P.out)[(int64_t)s_row[done.i % 3][c_first + k] * kD + t] = __float2bfloat16_rn(x);
+        const float x = fmaf(o2[k], kCut, o[k] + o1[k]) * s_fin[buf][c_first + k];
+        if (kind & kWhole)
+          static_cast<__nv_bfloat16 *>(P.out)[(int64_t)s_row[row][c_first + k] * kD + t] = __float2bfloat16_rn(x);
         else
-          P.ws_acc[(done.ent * P.Rg + w * live0 + k) * kD + t] = x;
+          P.ws_acc[(ent * P.Rg + w * live0 + k) * kD + t] = x;
       }
       t5_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&o_free[done.i & 1]);
+      if (lane == 0) mbar_arrive(&o_free[buf]);
     };
-    while (u < total) {
+    while (u < s_work.z) {
       const int buf = i % 3;
       const uint32_t o_col = lanes + Cfg::kOCol + (i & 1) * Cfg::kOCols + c_first;
       ok = __all_sync(0xffffffffu, kl_wait(&q_full[i & 1], (i >> 1) & 1, abf, P.wait_ns)) && ok;
       const float fold = P.scale_log2 * s_fold[buf];
-      const int4 it = s_item[buf];
-      const int tile0 = it.x, ntiles = it.y, L = it.z;
-      const int edge0 = fold < 0.f ? INT_MIN : L - P.n_new - T * kTK + 2, edge1 = P.window > 0 ? L - P.window : 0;
+      const int ntiles = s_item[buf].y;
       if (t < NC) s_nb[c_first + t] = t < live ? 0.f : -kUnset;   // (padding has no weight)
       bool open = true, unset = t < live;   // rows that have met no key; this thread's row among them
       float2 l2[NC / 2];
@@ -553,6 +556,7 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
         // S of this step, and with it the P' buffers that P V two steps ago has read
         const int pb = step & 1;
         float ka[T], vc[T], vi[T];
+        bool edge[T];
 #pragma unroll
         for (int h = 0; h < T; ++h) {   // this thread's keys
           if (h < nt && (u + h) % kChunk == 0)
@@ -561,27 +565,12 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
           ka[h] = s.x * fabsf(fold);
           vc[h] = s.y;
           vi[h] = s.z;
+          edge[h] = s.w != 0.f;
         }
         ok = kl_wait(&s_full[pb], (step >> 1) & 1, abf, P.wait_ns) && ok;
         const uint32_t s_col = lanes + Cfg::kSCol + T * pb * Cfg::kSCols + c_first;
-        // A step that ends past the oldest query or holds keys that a window has
-        // left: position j sees a key iff 0 <= j - j0 < reach.
-        const int key0 = (tile0 + ti) * kTK;
-        const bool edge = key0 >= edge0 || key0 < edge1;
-        int j0[T] = {};
-        uint32_t reach[T] = {};
-        if (edge) {
-#pragma unroll
-          for (int h = 0; h < T; ++h) {
-            const int key = key0 + h * kTK + t;
-            j0[h] = key - (L - P.n_new);
-            reach[h] = P.window > 0 && key >= P.sinks ? (uint32_t)P.window : 0x80000000u;
-          }
-          // Rows with powers of their own: every step of such an item counts as an edge.
-          ok = __all_sync(0xffffffffu, ok);
-          if (fold < 0.f && ok) kl_scale_rows<NC, N>(s_col, nt * Cfg::kSSums, &s_qf[buf][c_first]);
-        }
         ok = __all_sync(0xffffffffu, ok);
+        if (fold < 0.f && ok) kl_scale_rows_in<NC, N>(s_col, nt * Cfg::kSSums, &s_qf[buf][c_first]);   // rows with powers of their own
         t5_fence_after();
         float2 y[T][NC / 2];   // log2 weights, minus the reference
         {
@@ -610,16 +599,6 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
               if constexpr (Cfg::kSSums > 1) q = __fadd2_rn(q, make_float2(__uint_as_float(v[h][1][2 * k]), __uint_as_float(v[h][1][2 * k + 1])));
               y[h][k] = __ffma2_rn(q, ka2, __fadd2_rn(vc2, nb[k]));
             }
-            if (edge) {
-#pragma unroll
-              for (int k = 0; k < NC; k += 4) {
-                const int4 j = *reinterpret_cast<const int4 *>(&s_pos[buf][c_first + k]);
-                if ((uint32_t)(j.x - j0[h]) >= reach[h]) y[h][k / 2].x = -INFINITY;
-                if ((uint32_t)(j.y - j0[h]) >= reach[h]) y[h][k / 2].y = -INFINITY;
-                if ((uint32_t)(j.z - j0[h]) >= reach[h]) y[h][k / 2 + 1].x = -INFINITY;
-                if ((uint32_t)(j.w - j0[h]) >= reach[h]) y[h][k / 2 + 1].y = -INFINITY;
-              }
-            }
           };
           scores(0);
           if constexpr (T > 1) {
@@ -631,6 +610,23 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
             }
           }
         }
+        // A tile that ends past the oldest query or holds keys that a window has
+        // left: position j sees a key iff 0 <= j - j0 < reach.
+#pragma unroll
+        for (int h = 0; h < T; ++h)
+          if (edge[h]) {
+            const int4 at = s_item[buf];
+            const int key = (at.x + ti + h) * kTK + t, j0 = key - (at.z - P.n_new);
+            const uint32_t reach = P.window > 0 && key >= P.sinks ? (uint32_t)P.window : 0x80000000u;
+#pragma unroll
+            for (int k = 0; k < NC; k += 4) {
+              const int4 j = *reinterpret_cast<const int4 *>(&s_pos[buf][c_first + k]);
+              if ((uint32_t)(j.x - j0) >= reach) y[h][k / 2].x = -INFINITY;
+              if ((uint32_t)(j.y - j0) >= reach) y[h][k / 2].y = -INFINITY;
+              if ((uint32_t)(j.z - j0) >= reach) y[h][k / 2 + 1].x = -INFINITY;
+              if ((uint32_t)(j.w - j0) >= reach) y[h][k / 2 + 1].y = -INFINITY;
+            }
+          }
         // Steps set the references of rows that have met no key yet (they are 0 so
         // far), and move those of rows with a weight above 2^kMove. All four warps
         // decide together, as they share O.
@@ -773,7 +769,7 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
         if (nt > 1) pages_done(u + 1);
         ti += nt;
         u += nt;
-        if (done.pending) finish();
+        if (pending) finish();
       }
       if (gone) break;
       // ---- epilogue, first part: sums over the keys -------------------------
@@ -788,24 +784,25 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
           if (k < n) s_red[warp][at + k] = v[k];
       }
       named_bar_sync(bar, 128);
-      const int64_t ent = 2 * (int64_t)blockIdx.x + (it.w & kOpening ? 0 : 1);
+      const int kind = s_item[buf].w;
+      const int64_t ent = 2 * (int64_t)blockIdx.x + (kind & kOpening ? 0 : 1);
       if (t < live) {
         float l = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) l += s_red[4 * w + k][t];
         // (a row of NaN stays NaN; l is 0 only for a row without keys, which a query that sees itself never is)
-        s_fin[i & 1][c_first + t] = it.w & kWhole ? 1.f / l : 1.f;
-        if (!(it.w & kWhole)) {
+        s_fin[i & 1][c_first + t] = kind & kWhole ? 1.f / l : 1.f;
+        if (!(kind & kWhole)) {
           const int64_t e = ent * P.Rg + w * live0 + t;
           P.ws_ml[2 * e] = unset ? -kUnset : -s_nb[c_first + t];
           P.ws_ml[2 * e + 1] = l;
         }
       }
-      done = {true, (it.w & kWhole) != 0, step - 1, i, ent};
+      pending = true;
       ++i;
     }
     named_bar_sync(bar, 128);
-    if (done.pending) finish();
+    if (pending) finish();
   }
   __syncthreads();
   if (tid == 0 && *abf) atomic_or_status(P.status, SV_DEV_TIMEOUT);

@@ -453,7 +453,7 @@ __device__ __forceinline__ void t5_stn(uint32_t taddr, const uint32_t (&r)[N]) {
 
 // Columns of S times their rows' powers of two, where they lie (nt tiles)
 template <int NC, int N>
-__device__ __noinline__ void kl_scale_rows(uint32_t s_col, int nt, const float *qf) {
+__device__ __forceinline__ void kl_scale_rows_in(uint32_t s_col, int nt, const float *qf) {
   t5_fence_after();
 #pragma unroll 1
   for (int h = 0; h < nt; ++h)
@@ -469,6 +469,8 @@ __device__ __noinline__ void kl_scale_rows(uint32_t s_col, int nt, const float *
     }
   t5_wait_st();
 }
+template <int NC, int N>
+__device__ __noinline__ void kl_scale_rows(uint32_t s_col, int nt, const float *qf) { kl_scale_rows_in<NC, N>(s_col, nt, qf); }
 
 // Merge of the sequences that more than one range holds: CTA (range r, kv head
 // and row group, eight rows) leaves at once unless r's start is the first cut
