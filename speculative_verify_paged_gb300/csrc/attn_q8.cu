@@ -48,8 +48,8 @@ template <int NC, int W> struct Q8Cfg : KlCfg<NC, W> {
   // Registers a thread: at the launch, of the softmax warps, which take what the
   // others leave, and of those.
   static constexpr int kWarps = 4 * W + 8;
-  static constexpr int kRegs = W == 2 ? 128 : W == 4 ? 80 : 64;
-  static constexpr int kRegsSoftmax = W == 2 ? 192 : W == 4 ? 96 : 72, kRegsOther = W == 2 ? 64 : W == 4 ? 48 : 40;
+  static constexpr int kRegs = W == 2 ? 128 : W == 4 ? 80 : W == 5 ? 72 : 64;
+  static constexpr int kRegsSoftmax = W == 2 ? 192 : W == 4 ? 96 : W == 5 ? 80 : 72, kRegsOther = W == 2 ? 64 : W <= 5 ? 48 : 40;
   static_assert(4 * W * kRegsSoftmax + 8 * kRegsOther <= kWarps * kRegs, "registers");
   // The terms of P', and where tensor memory has room those of Q, side by side are
   // the columns of one product with several sums: what an MMA of few columns costs
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
         ok = kl_wait(&s_full[pb], (step >> 1) & 1, abf, P.wait_ns) && ok;
         const uint32_t s_col = lanes + Cfg::kSCol + T * pb * Cfg::kSCols + c_first;
         ok = __all_sync(0xffffffffu, ok);
-        if (fold < 0.f && ok) kl_scale_rows_in<NC, N>(s_col, nt * Cfg::kSSums, &s_qf[buf][c_first]);   // rows with powers of their own
+        if (fold < 0.f && ok) kl_scale_rows<NC, N>(s_col, nt * Cfg::kSSums, &s_qf[buf][c_first]);   // rows with powers of their own
         t5_fence_after();
         float2 y[T][NC / 2];   // log2 weights, minus the reference
         {
@@ -829,7 +829,7 @@ sv_status launch_q8(const KlParams &P, const Q8Maps &M, int C, cudaStream_t st) 
 // 4750 keys, 8 kv heads, 32 rows: four of 8 rows 116.2 us, two of 16 126.1; 40 rows:
 // six of 8 144.7 us, three of 16 148.0 (1024..8192 keys: 152.7, 160.9). A window of
 // 4096 keys of 16 sequences loses by it, 54.4 against 53.4.
-int q8_groups(int rows) { return rows <= 16 ? 2 : rows <= 32 ? 4 : rows <= 48 ? 6 : 4; }
+int q8_groups(int rows) { return rows <= 16 ? 2 : rows <= 32 ? 4 : rows <= 40 ? 5 : rows <= 48 ? 6 : 4; }
 
 // Query rows of a kv head on the tensor cores: 64 share a pass over the cache.
 constexpr int64_t kMaxRows = 1 << 14;
@@ -918,6 +918,7 @@ extern "C" sv_status spec_verify_attn_q8(const void *q, sv_dtype q_dtype, const 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int each = kl_first(p.Rg, W);   // rows of a softmax warpgroup
   const sv_status r2 = W == 6     ? launch_q8<8, 6>(P, M, p.C, st)
+                       : W == 5   ? launch_q8<8, 5>(P, M, p.C, st)
                        : W == 2   ? (each <= 4 ? launch_q8<4, 2>(P, M, p.C, st) : launch_q8<8, 2>(P, M, p.C, st))
                        : each <= 8 ? launch_q8<8, 4>(P, M, p.C, st)
                                    : launch_q8<16, 4>(P, M, p.C, st);

@@ -59,7 +59,7 @@ struct KlParams {
 };
 
 template <int NC, int W = 2> struct KlCfg {   // NC query rows per softmax warpgroup, W of these
-  static constexpr int kCols = (NC + 7) / 8 * 8, kN = W * kCols;   // columns of S and O
+  static constexpr int kCols = (NC + 7) / 8 * 8, kN = (W * kCols + 15) / 16 * 16;   // columns of S and O
   static constexpr int kT = W * NC > 48 ? 1 : 2;   // tiles of a softmax step (their scores stay in registers)
   static constexpr int kQ = kN * 256;   // the two e4m3 terms of a row, 128 bytes each
 };
@@ -453,7 +453,7 @@ __device__ __forceinline__ void t5_stn(uint32_t taddr, const uint32_t (&r)[N]) {
 
 // Columns of S times their rows' powers of two, where they lie (nt tiles)
 template <int NC, int N>
-__device__ __forceinline__ void kl_scale_rows_in(uint32_t s_col, int nt, const float *qf) {
+__device__ __noinline__ void kl_scale_rows(uint32_t s_col, int nt, const float *qf) {
   t5_fence_after();
 #pragma unroll 1
   for (int h = 0; h < nt; ++h)
@@ -469,8 +469,6 @@ __device__ __forceinline__ void kl_scale_rows_in(uint32_t s_col, int nt, const f
     }
   t5_wait_st();
 }
-template <int NC, int N>
-__device__ __noinline__ void kl_scale_rows(uint32_t s_col, int nt, const float *qf) { kl_scale_rows_in<NC, N>(s_col, nt, qf); }
 
 // Merge of the sequences that more than one range holds: CTA (range r, kv head
 // and row group, eight rows) leaves at once unless r's start is the first cut
@@ -584,7 +582,7 @@ inline KlPlan kl_plan(int B, int n_new, int H_q, int H_kv, int d, int max_blocks
 }
 
 // Columns of S and O, a softmax warpgroup's rows in steps of 4 (of 8 for the layout)
-inline int kl_cols(const KlPlan &p, int W = 2) { return W * ((kl_first(p.Rg, W) + 7) / 8 * 8); }
+inline int kl_cols(const KlPlan &p, int W = 2) { return (W * ((kl_first(p.Rg, W) + 7) / 8 * 8) + 15) / 16 * 16; }
 
 inline size_t kl_ws_bytes(const KlPlan &p, int B, int H_kv, int W = 2) {
   const size_t ent = (size_t)2 * p.C * p.Rg, qent = (size_t)B * H_kv * p.RG, n = kl_cols(p, W);
