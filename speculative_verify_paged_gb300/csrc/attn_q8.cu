@@ -17,12 +17,27 @@
 // would not do: the sum over a long row needs the small weights as well. A weight
 // is rounded to f16 and cut into three e5m2 terms, which is a matter of bytes: the
 // upper byte of an f16 is an e5m2 number, what is left after taking it off is
-// exact in f16 again, and so on; the third is rounded. So weights keep 2^-10
-// relative (f16's 2^-11 first) down to 2^-6 (2^-16 of the largest), and an
-// absolute 2^-17 below: kind::f8f6f4 takes e4m3 and e5m2 side by side.
+// exact in f16 again, and so on; the third is taken 32 times and rounded. A row's
+// largest weight lies around 2^kTop, so weights keep 2^-10 relative (f16's 2^-11
+// first) and an absolute 2^-22, 2^-27 of the largest. kind::f8f6f4 takes e4m3 and
+// e5m2 side by side.
 // Keys on the lanes: S^T = C Q^T, O^T = C'^T P'^T (key_lanes.cuh). C is K-major as
 // it lies, C'^T is read across its rows (head dims contiguous), P' is written by
 // the key's thread as a row of its columns.
+//
+// What bounds it. Up to 16 query rows a kv head, memory: 64 sequences of 8192 keys,
+// 1.07 GB, 174 us with 4 to 16 rows. Above, the chain of a softmax step (scores from
+// tensor memory, the vote on the references, powers, terms, their way to shared
+// memory), which W warpgroups take side by side: at 64 sequences of 4750 keys and 40
+// rows a tile costs 1710 cycles, 1290 of them what its bytes take; the schedulers
+// issue in two thirds, and with nearly no products it would be a tenth faster. What
+// got it there, at 64 sequences of 1024 .. 8192 keys, 40 rows, 616 MB: references
+// moved in registers instead of from tensor memory 319 -> 177 us; the terms as columns
+// of one wide product, the scales by a warp of their own 161; eight rows a warpgroup
+// 153; edge flags with the scales and little else carried along 144; five warpgroups
+// with 80 registers instead of six with 72 134; fixed addresses of the terms 132. Some
+// 15 us of it, and all of a short single call's 17, are the three launches and the way
+// from a page's number to its first score.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -53,8 +68,8 @@ template <int NC, int W> struct Q8Cfg : KlCfg<NC, W> {
   static_assert(4 * W * kRegsSoftmax + 8 * kRegsOther <= kWarps * kRegs, "registers");
   // The terms of P', and where tensor memory has room those of Q, side by side are
   // the columns of one product with several sums: what an MMA of few columns costs
-  // is its other operand (16 or 32 columns 41 cycles, 48 45, 96 57, 144 72), 4 KB
-  // from shared memory, whose bandwidth the kernel is short of.
+  // is its other operand, 4 KB from shared memory (16 or 32 columns 41 cycles, 48 45,
+  // 96 57, 144 72).
   static constexpr int kSSums = kN <= 32 ? 2 : 1, kSCols = kSSums * kN, kOCols = 3 * kN;
   // P' lies in atoms of 32 columns, 32 bytes a key.
   static constexpr int kAtom = kTK * 32, kPBytes = (kOCols + 31) / 32 * kAtom;
@@ -110,9 +125,9 @@ __device__ __forceinline__ void cut_weights(uint32_t h0, uint32_t h1, uint32_t (
 
 // W warpgroups: softmax (a key per thread and tile; each warpgroup its share of
 // the query rows, or the first all of up to 8), later the epilogue (a head dim
-// per thread). 8: block numbers and flags of the tiles ahead. 9, 10: copy the K
-// and V codes. 11: issues Q K^T, owns the 512 TMEM columns. 12: issues P V. 13: Q
-// of the next sequence. 14: the blocks' scales.
+// per thread). Then eight warps: block numbers and flags of the tiles ahead; copies
+// of the K codes; of the V codes; Q K^T, which owns the 512 TMEM columns; P V; Q of
+// the next sequence; the blocks' scales; one idle.
 template <int NC, int W>
 __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(const __grid_constant__ KlParams P, const __grid_constant__ Q8Maps M) {
   using Cfg = Q8Cfg<NC, W>;
@@ -499,8 +514,15 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
     const int live = min(rows - w * live0, live0);
     const int bar = 1 + w;
     const uint32_t lanes = tb + ((uint32_t)((warp & 3) * 32) << 16);
-    // this key's row of P', and what its two 16-byte pieces are exchanged by
-    const uint32_t p_row = p_smem + t * 32, swap = (t << 2) & 16;
+    // where this warpgroup's columns of each term begin in this key's row of P' (its two 16-byte
+    // pieces are exchanged in every other four rows)
+    uint32_t p_row[3];
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+      const uint32_t col = e * N + c_first;
+      p_row[e] = p_smem + t * 32 + (col >> 5) * Cfg::kAtom + ((col & 24) ^ ((t << 2) & 16));
+      if constexpr (W < 6) asm volatile("" : "+r"(p_row[e]));   // (kept, not worked out for every store, where registers allow)
+    }
     int u = 0, i = 0;            // tiles and items done
     uint32_t step = 0;
     // A wait that gave up (ok false) only shows at the warpgroup's next vote, so
@@ -686,8 +708,9 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
         }
         auto weights = [&](int h) {
           const float2 vi2 = make_float2(vi[h], vi[h]);
-          const uint32_t dst = p_row + (T * pb + h) * Cfg::kPBytes;
-          constexpr int kEights = (NC + 7) / 8;   // pieces of eight columns, a half of 16 bytes
+          const uint32_t at = (T * pb + h) * Cfg::kPBytes;
+          constexpr int kEights = (NC + 7) / 8;   // pieces of eight columns: 8 or 16 bytes
+          static_assert(kEights <= 2);
           uint2 piece[kEights][3];
 #pragma unroll
           for (int c = 0; c < kEights; ++c) {
@@ -706,34 +729,14 @@ __global__ void __launch_bounds__(32 * Q8Cfg<NC, W>::kWarps, 1) attn_q8_kernel(c
 #pragma unroll
             for (int e = 0; e < 3; ++e) piece[c][e] = make_uint2(w0[e], w1[e]);
           }
-          auto store = [&](int c, int e) {
-            const uint32_t col = e * N + c_first + 8 * c;
-            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(dst + (col >> 5) * Cfg::kAtom + ((col & 24) ^ swap)), "r"(piece[c][e].x),
-                         "r"(piece[c][e].y)
-                         : "memory");
-          };
-          auto store2 = [&](int c, int e) {   // (where 16 bytes begin)
-            const uint32_t col = e * N + c_first + 8 * c;
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (col >> 5) * Cfg::kAtom + ((col & 16) ^ swap)), "r"(piece[c][e].x),
-                         "r"(piece[c][e].y), "r"(piece[c + 1][e].x), "r"(piece[c + 1][e].y)
-                         : "memory");
-          };
 #pragma unroll
           for (int e = 0; e < 3; ++e) {
-            if constexpr (kEights == 1) {
-              store(0, e);
-            } else if constexpr (kEights == 3) {   // (odd warpgroups start in the middle of 16 bytes)
-              if (w % 2 == 0) {
-                store2(0, e);
-                store(2, e);
-              } else {
-                store(0, e);
-                store2(1, e);
-              }
-            } else {
-#pragma unroll
-              for (int c = 0; c < kEights; c += 2) store2(c, e);
-            }
+            if constexpr (kEights == 1)
+              asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(p_row[e] + at), "r"(piece[0][e].x), "r"(piece[0][e].y) : "memory");
+            else
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p_row[e] + at), "r"(piece[0][e].x), "r"(piece[0][e].y),
+                           "r"(piece[1][e].x), "r"(piece[1][e].y)
+                           : "memory");
           }
         };
         weights(0);
@@ -825,10 +828,10 @@ sv_status launch_q8(const KlParams &P, const Q8Maps &M, int C, cudaStream_t st) 
 }
 
 // Softmax warpgroups: 8 rows each as far as threads go, then 16. A step is a chain
-// of waits that more warpgroups with shorter columns overlap better. 64 sequences of
-// 4750 keys, 8 kv heads, 32 rows: four of 8 rows 116.2 us, two of 16 126.1; 40 rows:
-// six of 8 144.7 us, three of 16 148.0 (1024..8192 keys: 152.7, 160.9). A window of
-// 4096 keys of 16 sequences loses by it, 54.4 against 53.4.
+// of waits that more warpgroups with shorter columns overlap better, as long as the
+// registers suffice. 64 sequences of 4750 keys, 8 kv heads: 32 rows, four of 8 116 us,
+// two of 16 126; 40 rows, five of 8 121, six 130, three of 16 148; 48 rows, six of 8
+// 132, four of 16 160.
 int q8_groups(int rows) { return rows <= 16 ? 2 : rows <= 32 ? 4 : rows <= 40 ? 5 : rows <= 48 ? 6 : 4; }
 
 // Query rows of a kv head on the tensor cores: 64 share a pass over the cache.
