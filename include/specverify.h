@@ -448,6 +448,16 @@ sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const void *k_cac
  *   256-byte aligned; its contents need no initialisation. It holds what one
  *   call computes on the way: calls that may run at the same time need one
  *   each.
+ *   bf16 queries and outputs, d_head 128, blocks of 16 and up to 2^14 query
+ *   rows n_new * H_q / H_kv a kv head run on the tensor cores (64 rows share a
+ *   pass over the cache); q and out are then 16-byte aligned
+ *   (SV_ERR_INVALID_ARG otherwise). The scores multiply the codes by the query
+ *   as two e4m3 terms, as in spec_verify_attn_q4; the weights, times their
+ *   values' scale, keep 2^-10 relative, and 2^-27 of the row's largest
+ *   absolutely; sums are f32.
+ *   Everything else runs on the CUDA cores in f32, far slower, with at most as
+ *   many query rows a kv head as their shared memory takes (147 at d_head 128;
+ *   SV_ERR_UNSUPPORTED beyond).
  * ------------------------------------------------------------------------ */
 size_t sv_q8_page_bytes(int H_kv, int d_head, int block_size);
 
@@ -516,7 +526,8 @@ sv_status spec_verify_attn_q8(const void *q, sv_dtype q_dtype, const void *k_cac
  *   rows unwritten).
  *   The rows of each tensor are packed [B][n_new][heads][d], or lie at the
  *   strides (elements, not negative) of its sv_rope_rows, e.g. heads of a
- *   packed projection. The angle is exact to 2^-31 turns at every 32-bit
+ *   packed projection; rows that are written must not overlap
+ *   (SV_ERR_INVALID_ARG). The angle is exact to 2^-31 turns at every 32-bit
  *   position. rope is read before the call returns (a captured call keeps
  *   it). rotary_dim <= SV_ROPE_MAX_DIM.
  * ------------------------------------------------------------------------ */

@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <utility>
 
 #include "sv_common.cuh"
 
@@ -305,9 +306,19 @@ extern "C" sv_status spec_rope(const void *q, void *q_out, const void *k, void *
     a.head[t] = rows[t] ? rows[t]->head_stride : d;
     a.row[t] = rows[t] ? rows[t]->row_stride : (int64_t)H * d;
     a.seq[t] = rows[t] ? rows[t]->seq_stride : (int64_t)n_new * H * d;
-    // rows that are written must not overlap
-    if (t >= 2 && ((H > 1 && a.head[t] < d) || (n_new > 1 && a.row[t] < d) || (B > 1 && a.seq[t] < d)))
-      return fail(SV_ERR_INVALID_ARG, "spec_rope: output strides smaller than d");
+    // rows that are written must not overlap: by ascending stride, each beyond what those before it span
+    if (t >= 2) {
+      std::pair<int64_t, int64_t> by[3] = {{a.head[t], H}, {a.row[t], n_new}, {a.seq[t], B}};   // stride, count
+      std::sort(by, by + 3);
+      int64_t span = d;
+      for (const auto &[stride, count] : by) {
+        if (count < 2) continue;
+        if (stride < span) return fail(SV_ERR_INVALID_ARG, "spec_rope: output rows overlap (strides %lld, %lld, %lld)",
+                                       (long long)a.seq[t], (long long)a.row[t], (long long)a.head[t]);
+        if (stride > (INT64_MAX - span) / (count - 1)) return fail(SV_ERR_INVALID_ARG, "spec_rope: output strides too large");
+        span += (count - 1) * stride;
+      }
+    }
     vec = vec && a.head[t] % V == 0 && a.row[t] % V == 0 && a.seq[t] % V == 0 && aligned(t < 2 ? a.src[t] : a.dst[t - 2], 16);
   }
   for (int w = 0; w < 2; ++w) {
