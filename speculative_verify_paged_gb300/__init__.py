@@ -859,18 +859,50 @@ def spec_rope(q, k, rope, seq_lens=None, positions=None, q_out=None, k_out=None,
     may be k; other overlaps are not allowed. Positions: seq_lens - n_new + j (those the append writes), or
     positions [B, n_new] (the nodes of a tree)."""
     what = "spec_rope"
+    x = q if q is not None else k
+    if not _rope_plain(q, k, rope, seq_lens, positions, q_out, k_out, status):
+        _check_rope(what, x, q, k, rope, seq_lens, positions, q_out, k_out, status)
+    B, n_new, H, d = x.shape
+    if q is not None and q_out is None:
+        q_out = torch.empty((B, n_new, H, d), dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    if x.numel():
+        _check(load_library().spec_rope(
+            _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), _dtype_code(x), _rope_rows(what, "q", q),
+            _rope_rows(what, "q_out", q_out), _rope_rows(what, "k", k), _rope_rows(what, "k_out", k_out), rope._ref,
+            _ptr(positions), _ptr(seq_lens), B, n_new, 0 if q is None else H, 0 if k is None else k.shape[2], d,
+            _ptr(status), _stream()))
+    return q_out, k_out
+
+
+def _rope_plain(q, k, rope, seq_lens, positions, q_out, k_out, status):
+    """True for the usual call (queries and keys on the current device, rotated to their lengths' positions, out of place
+    or in it) that is right in everything _check_rope looks at: a small call's time is these checks."""
+    if q is None or k is None or seq_lens is None or positions is not None or status is not None or type(rope) is not Rope:
+        return False
+    s, t, dtype, dev = q.shape, k.shape, q.dtype, q.get_device()
+    return ((q_out is None or q_out is q) and (k_out is None or k_out is k) and len(s) == 4 and len(t) == 4 and
+            s[0] == t[0] and s[1] == t[1] and s[3] == t[3] and dtype == k.dtype and dtype in _ROPE_DTYPES and
+            dev >= 0 and k.get_device() == dev and seq_lens.get_device() == dev and seq_lens.dtype == torch.int32 and
+            seq_lens.shape == s[:1] and seq_lens.is_contiguous() and torch.cuda.current_device() == dev)
+
+
+_ROPE_DTYPES = (torch.bfloat16, torch.float32, torch.float16)
+
+
+def _check_rope(what, x, q, k, rope, seq_lens, positions, q_out, k_out, status):
     if not isinstance(rope, Rope):
         raise TypeError("%s: rope must be a Rope" % what)
     if seq_lens is None and positions is None:
         raise ValueError("%s: seq_lens or positions is needed" % what)
     _int32(seq_lens=seq_lens, positions=positions)
-    x = q if q is not None else k
     if x is None or any(t is not None and (t.dim() != 4 or t.shape[:2] != x.shape[:2] or t.shape[3] != x.shape[3] or
                                            t.dtype != x.dtype) for t in (q, k)):
         raise ValueError("%s: q and k must be [B, n_new, heads, d] of one dtype" % what)
-    if x.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+    if x.dtype not in _ROPE_DTYPES:
         raise ValueError("%s: rows must be f32, bf16 or f16, not %s" % (what, x.dtype))
-    B, n_new, _, d = x.shape
+    B, n_new = x.shape[:2]
     if seq_lens is not None:
         _check_like(what, "seq_lens", seq_lens, (B,), torch.int32)
     if positions is not None:
@@ -885,17 +917,6 @@ def spec_rope(q, k, rope, seq_lens=None, positions=None, q_out=None, k_out=None,
     if not x.is_cuda:
         raise ValueError("tensor arguments must live on a CUDA device")
     _on_current_device(what, x, q, k, q_out, k_out, seq_lens, positions, status)
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    if x.numel():
-        _check(load_library().spec_rope(
-            _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), _dtype_code(x), _rope_rows(what, "q", q),
-            _rope_rows(what, "q_out", q_out), _rope_rows(what, "k", k), _rope_rows(what, "k_out", k_out), rope._ref,
-            _ptr(positions), _ptr(seq_lens), B, n_new, 0 if q is None else q.shape[2], 0 if k is None else k.shape[2], d,
-            _ptr(status), _stream()))
-    return q_out, k_out
 
 
 def _append_any(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, block_size, status):
