@@ -867,7 +867,7 @@ def spec_rope(q, k, rope, seq_lens=None, positions=None, q_out=None, k_out=None,
         q_out = torch.empty((B, n_new, H, d), dtype=q.dtype, device=q.device)
     if k is not None and k_out is None:
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    if x.numel():
+    if x.numel() or (k is not None and k.numel()):   # (queries of no heads beside keys)
         _check(load_library().spec_rope(
             _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), _dtype_code(x), _rope_rows(what, "q", q),
             _rope_rows(what, "q_out", q_out), _rope_rows(what, "k", k), _rope_rows(what, "k_out", k_out), rope._ref,

@@ -129,3 +129,16 @@ def test_rope_outputs_side_by_side(lib):
     want, _ = lib.spec_rope(q, None, rope, seq_lens=lens)
     got, _ = lib.spec_rope(q, None, rope, seq_lens=lens, q_out=out)
     assert got is out and torch.equal(out, want)
+
+
+def test_rope_of_no_heads(lib):
+    rope, lens = lib.Rope(64), i32([9, 300])
+    k = torch.randn((2, 3, 4, 64), device=DEV).bfloat16()
+    want = lib.spec_rope(None, k, rope, seq_lens=lens)[1]
+    none = k[:, :, :0].contiguous()
+    q, got = lib.spec_rope(none, k, rope, seq_lens=lens)
+    assert q.shape == none.shape and torch.equal(got, want)
+    got, q = lib.spec_rope(k, none, rope, seq_lens=lens)
+    assert q.shape == none.shape and torch.equal(got, want)
+    q, got = lib.spec_rope(none, none, rope, seq_lens=lens)
+    assert q.shape == none.shape == got.shape
