@@ -581,7 +581,7 @@ inline KlPlan kl_plan(int B, int n_new, int H_q, int H_kv, int d, int max_blocks
   return p;
 }
 
-// Columns of S and O, a softmax warpgroup's rows in steps of 4 (of 8 for the layout)
+// Columns of S and O: a softmax warpgroup's rows in steps of 8, all together in steps of 16
 inline int kl_cols(const KlPlan &p, int W = 2) { return (W * ((kl_first(p.Rg, W) + 7) / 8 * 8) + 15) / 16 * 16; }
 
 inline size_t kl_ws_bytes(const KlPlan &p, int B, int H_kv, int W = 2) {
