@@ -193,7 +193,9 @@ __device__ int64_t kl_all_tiles(const KlParams &P, bool &bad) {
 constexpr int kPrepWarps = 4;
 constexpr int kNear = 6;
 // NIB (4-bit codes): the dims in the order in which codes are spread, with the
-// rows' sums; otherwise in their own order.
+// rows' sums; otherwise in their own order. An infinite element would saturate to
+// a finite term: it becomes NaN, so that its row's scores and output are NaN (with
+// NIB the row's sum carries it).
 template <int NC, int W, bool NIB>
 __global__ void __launch_bounds__(32 * kPrepWarps) kl_prep_kernel(const __grid_constant__ KlParams P) {
   using Cfg = KlCfg<NC, W>;
@@ -296,7 +298,11 @@ __global__ void __launch_bounds__(32 * kPrepWarps) kl_prep_kernel(const __grid_c
       hi[e] = lo[e] = 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float y0 = x[NIB ? 4 * h + e : 4 * e + 2 * h] * up, y1 = x[NIB ? 4 * h + 2 + e : 4 * e + 2 * h + 1] * up;
+        float y0 = x[NIB ? 4 * h + e : 4 * e + 2 * h] * up, y1 = x[NIB ? 4 * h + 2 + e : 4 * e + 2 * h + 1] * up;
+        if constexpr (!NIB) {   // (what is finite is below 2^8)
+          y0 += y0 - y0;
+          y1 += y1 - y1;
+        }
         const uint32_t c = f32x2_to_e4m3x2(y0, y1);
         const uint32_t f = e4m3x2_to_f16x2((uint16_t)c);
         const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&f));
