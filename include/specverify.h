@@ -453,8 +453,9 @@ sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const void *k_cac
  *   pass over the cache); q and out are then 16-byte aligned
  *   (SV_ERR_INVALID_ARG otherwise). The scores multiply the codes by the query
  *   as two e4m3 terms, as in spec_verify_attn_q4; the weights, times their
- *   values' scale, keep 2^-10 relative, and 2^-27 of the row's largest
- *   absolutely; sums are f32. A query row that holds a NaN or an infinity comes
+ *   values' scale, are rounded to f16 (2^-11 relative) down to 2^-15 of the
+ *   row's largest, and below that they are off by at most 2^-25 of it; sums
+ *   are f32. A query row that holds a NaN or an infinity comes
  *   out as NaN, and no other row is touched by it.
  *   Everything else runs on the CUDA cores in f32, far slower, with at most as
  *   many query rows a kv head as their shared memory takes (147 at d_head 128;

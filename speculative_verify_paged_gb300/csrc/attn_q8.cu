@@ -16,11 +16,12 @@
 // P V has e4m3 codes on one side, so the weights have to be 8-bit too, and e4m3
 // would not do: the sum over a long row needs the small weights as well. A weight
 // is rounded to f16 and cut into three e5m2 terms, which is a matter of bytes: the
-// upper byte of an f16 is an e5m2 number, what is left after taking it off is
-// exact in f16 again, and so on; the third is taken 32 times and rounded. A row's
-// largest weight lies around 2^kTop, so weights keep 2^-10 relative (f16's 2^-11
-// first) and an absolute 2^-22, 2^-27 of the largest. kind::f8f6f4 takes e4m3 and
-// e5m2 side by side.
+// upper byte of an f16 is an e5m2 number, what is left after taking the nearest off is
+// exact in f16 again, and so on; the third is taken 32 times (cut_weights). From 2^-10
+// on the terms hold the f16 exactly, so such weights keep f16's 2^-11; below, they are
+// off by at most 2^-21, and f16's subnormals by 2^-25. A row's largest weight is at
+// least 2^kTop: 2^-11 relative down to 2^-15 of the largest, and 2^-25 of it below.
+// kind::f8f6f4 takes e4m3 and e5m2 side by side.
 // Keys on the lanes: S^T = C Q^T, O^T = C'^T P'^T (key_lanes.cuh). C is K-major as
 // it lies, C'^T is read across its rows (head dims contiguous), P' is written by
 // the key's thread as a row of its columns.
@@ -53,7 +54,7 @@ namespace {
 constexpr int kTile = kTK * kD;            // bytes of a tile of K or V
 constexpr int kEdge = 16;                  // of a tile: some query does not see all its keys
 // A row's reference puts its largest weight at 2^kTop and moves once one exceeds
-// 2^kMove (f16 ends at 65504, which e5m2 takes for 57344 and two smaller terms).
+// 2^kMove (rounded to f16 that is 61152, the nearest e5m2 to which is its largest, 57344).
 constexpr float kTop = 5.f, kMove = 15.9f;
 
 template <int NC, int W> struct Q8Cfg : KlCfg<NC, W> {
@@ -102,25 +103,33 @@ __device__ __forceinline__ uint64_t t5_desc32(uint32_t saddr, uint32_t lbo, uint
   return d;
 }
 
-// Four weights (two f16 pairs) as three words of e5m2: the upper bytes, those of
-// what they leave, and 32 times what is left then, rounded. (With a weight below
-// 2^16 the first leaves less than 2^13, the second less than 2^10.)
+// Four weights (two f16 pairs) as three words of e5m2, each term the nearest to what
+// is left: half a step added to the bits moves a magnitude to the nearest upper byte
+// (below 2^16 none becomes an infinity), and what it then exceeds or leaves, of
+// either sign, is exact in f16. Of an f16's ten bits after the first the first term
+// leaves at most the lower seven, the second the lower three, which the third, 32 times,
+// holds. (Terms cut off instead of rounded would leave up to 2^-9, and on average more
+// than nothing.) NaN becomes zeros: the row's sum carries it.
 constexpr float kCut = 0.03125f;
 __device__ __forceinline__ void cut_weights(uint32_t h0, uint32_t h1, uint32_t (&w)[3]) {
-  auto rest = [](uint32_t h) {   // minus its upper byte's value
-    const uint32_t u = h & 0xFF00FF00u;
+  auto near = [](uint32_t h) { return h + 0x00800080u; };   // (no NaN but 0x7fff: no carry into the other half)
+  auto rest = [](uint32_t h, uint32_t n) {   // minus the term's value
+    const uint32_t u = n & 0xFF00FF00u;
     const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&u));
     return *reinterpret_cast<const uint32_t *>(&r);
   };
   auto last = [](uint32_t h) {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&h), __float2half2_rn(32.f));
-    return *reinterpret_cast<const uint32_t *>(&r) + 0x00800080u;   // (to nearest; far from carrying into the other half)
+    return *reinterpret_cast<const uint32_t *>(&r) + 0x00800080u;
   };
-  w[0] = __byte_perm(h0, h1, 0x7531);
-  h0 = rest(h0);
-  h1 = rest(h1);
-  w[1] = __byte_perm(h0, h1, 0x7531);
-  w[2] = __byte_perm(last(rest(h0)), last(rest(h1)), 0x7531);
+  uint32_t n0 = near(h0), n1 = near(h1);
+  w[0] = __byte_perm(n0, n1, 0x7531);
+  h0 = rest(h0, n0);
+  h1 = rest(h1, n1);
+  n0 = near(h0);
+  n1 = near(h1);
+  w[1] = __byte_perm(n0, n1, 0x7531);
+  w[2] = __byte_perm(last(rest(h0, n0)), last(rest(h1, n1)), 0x7531);
 }
 
 // W warpgroups: softmax (a key per thread and tile; each warpgroup its share of
