@@ -447,7 +447,7 @@ sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const void *k_cac
  *   SV_F32. The workspace is spec_verify_attn_q8_workspace_size(...) bytes,
  *   256-byte aligned; its contents need no initialisation. It holds what one
  *   call computes on the way: calls that may run at the same time need one
- *   each.
+ *   each. (The size is 0 for arguments that every call refuses.)
  *   bf16 queries and outputs, d_head 128, blocks of 16 and up to 2^14 query
  *   rows n_new * H_q / H_kv a kv head run on the tensor cores (64 rows share a
  *   pass over the cache); q and out are then 16-byte aligned

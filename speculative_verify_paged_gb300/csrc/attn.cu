@@ -2277,10 +2277,15 @@ sv_status launch_tc5(const TcParams &P0, cudaStream_t st) {
   return check_launch("spec_verify_attn tcgen05 launch");
 }
 
+// Shared memory of the CUDA-core kernel for R query rows a kv head, and the most it takes.
+constexpr size_t kGenSmem = 200 * 1024;
+size_t gen_smem(int64_t R, int d) { return sizeof(float) * ((size_t)2 * R * d + 2 * kGenKeys * d + (size_t)R * kGenKeys + 3 * R); }
+sv_status gen_too_large() { return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: (K+1)*G*d_head too large for the fp32 path"); }
+
 template <typename TKV, typename TQ>
 sv_status launch_gen(const GenParams &P, cudaStream_t st) {
-  const size_t smem = sizeof(float) * ((size_t)2 * P.R * P.d + 2 * kGenKeys * P.d + (size_t)P.R * kGenKeys + 3 * P.R);
-  if (smem > 200 * 1024) return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: (K+1)*G*d_head too large for the fp32 path");
+  const size_t smem = gen_smem(P.R, P.d);
+  if (smem > kGenSmem) return gen_too_large();
   cudaError_t e = cudaFuncSetAttribute(attn_generic_kernel<TKV, TQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return fail(SV_ERR_CUDA, "spec_verify_attn: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
@@ -2338,6 +2343,8 @@ static sv_status attn_impl(const void *q, sv_dtype q_dtype, const void *k_cache,
   const Plan plan =
       make_plan(B, n_new, H_q, H_kv, d_head, span_blocks, block_size, kv_dtype, q_dtype, layout, bps_req);
   if (plan.R > 65535) return fail(SV_ERR_UNSUPPORTED, "spec_verify_attn: too many query rows per kv head");
+  // (before the workspace: its size counts no path that cannot run)
+  if (kv_dtype == kQ8 && gen_smem(plan.R, d_head) > kGenSmem) return gen_too_large();
   const size_t base_need = ws_bytes(plan, B, H_kv);
   const size_t need = base_need + (tree_parent ? align_up((size_t)B * n_new * sizeof(uint64_t), 256) : 0);
   if (!workspace || workspace_bytes < need)
@@ -2598,6 +2605,8 @@ sv_status attn_cuda_core_q4(const void *q, sv_dtype q_dtype, const void *k_cache
                    seq_lens, B, n_new, H_q, H_kv, d_head, block_size, num_blocks, softmax_scale, out, out_dtype,
                    workspace, workspace_bytes, dev_status, 0, nullptr, window, sinks, stream);
 }
+
+bool attn_cuda_core_fits(int64_t R, int d_head) { return gen_smem(R, d_head) <= kGenSmem; }
 
 sv_status attn_cuda_core_q8(const void *q, sv_dtype q_dtype, const void *k_cache, const void *v_cache,
                             const sv_kv_layout *layout, const int32_t *block_table, int max_blocks_per_seq,

@@ -853,12 +853,14 @@ using namespace sv;
 
 extern "C" size_t spec_verify_attn_q8_workspace_size(int B, int n_new, int H_q, int H_kv, int d_head,
                                                      int max_blocks_per_seq, int block_size, int window, int sinks) {
-  const size_t other = spec_verify_attn_window_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq,
-                                                              block_size, window, sinks);
+  size_t other = spec_verify_attn_window_workspace_size(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq,
+                                                        block_size, window, sinks);
   if (other == 0) return 0;
+  // (queries in f32 run on the CUDA-core kernel whatever the shape, as far as it takes their rows:
+  // its partials of 2^14 rows would be gigabytes that no call can use)
+  if (!attn_cuda_core_fits((int64_t)n_new * (H_q / H_kv), d_head)) other = 0;
   if ((int64_t)window >= (int64_t)max_blocks_per_seq * block_size) window = sinks = 0;
   const KlPlan p = kl_plan(B, n_new, H_q, H_kv, d_head, max_blocks_per_seq, block_size, SV_BF16, window, sinks, kMaxRows);
-  // (queries in f32 run on the CUDA-core kernel whatever the shape)
   return p.tc ? std::max(other, kl_ws_bytes(p, B, H_kv, q8_groups(p.Rg))) : other;
 }
 

@@ -35,8 +35,11 @@ constexpr sv_dtype kQ8 = static_cast<sv_dtype>(5);
 sv_status q8_check(const char *what, const void *k_cache, const void *v_cache, const sv_kv_layout *layout, int H_kv,
                    int d_head, int block_size, int64_t *block_stride);
 
-// spec_verify_attn_q8 on the CUDA-core kernel (attn.cu), for every shape and
-// type, with all its argument checks.
+// Whether the CUDA-core kernel (attn.cu) takes R query rows a kv head.
+bool attn_cuda_core_fits(int64_t R, int d_head);
+
+// spec_verify_attn_q8 on the CUDA-core kernel, for every shape and type, with
+// all its argument checks.
 sv_status attn_cuda_core_q8(const void *q, sv_dtype q_dtype, const void *k_cache, const void *v_cache,
                             const sv_kv_layout *layout, const int32_t *block_table, int max_blocks_per_seq,
                             const int32_t *seq_lens, int B, int n_new, int H_q, int H_kv, int d_head, int block_size,
