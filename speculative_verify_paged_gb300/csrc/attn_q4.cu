@@ -884,7 +884,7 @@ extern "C" sv_status spec_verify_attn_q4(const void *q, sv_dtype q_dtype, const 
   const sv_status rc = q4_check("spec_verify_attn_q4", k_cache, v_cache, layout, H_kv, d_head, block_size,
                                 &P.block_stride, &P.head_stride);
   if (rc != SV_OK) return rc;
-  const size_t need = kl_ws_bytes(p, B, H_kv);
+  const size_t need = B > 0 ? kl_ws_bytes(p, B, H_kv) : 0;
   if (!workspace || workspace_bytes < need)
     return fail(SV_ERR_WORKSPACE, "spec_verify_attn_q4: workspace needs %zu bytes", need);
   if (!aligned(workspace, 256)) return fail(SV_ERR_WORKSPACE, "spec_verify_attn_q4: workspace not 256-byte aligned");

@@ -892,7 +892,7 @@ extern "C" sv_status spec_verify_attn_q8(const void *q, sv_dtype q_dtype, const 
   const sv_status rc = q8_check("spec_verify_attn_q8", k_cache, v_cache, layout, H_kv, d_head, block_size, &P.block_stride);
   if (rc != SV_OK) return rc;
   const int W = q8_groups(p.Rg);
-  const size_t need = kl_ws_bytes(p, B, H_kv, W);
+  const size_t need = B > 0 ? kl_ws_bytes(p, B, H_kv, W) : 0;
   if (!workspace || workspace_bytes < need)
     return fail(SV_ERR_WORKSPACE, "spec_verify_attn_q8: workspace needs %zu bytes", need);
   if (!aligned(workspace, 256)) return fail(SV_ERR_WORKSPACE, "spec_verify_attn_q8: workspace not 256-byte aligned");
