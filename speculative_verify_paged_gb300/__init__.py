@@ -1312,7 +1312,8 @@ class MultiLayerVerify:
     A layer's pools may be 4-bit or 8-bit block-scaled ones (alloc_q4_pools,
     alloc_q8_pools), a layer with "window" (and "sinks") attends through a
     sliding window, and one with "rope" (a Rope) rotates its q and k_new first,
-    into buffers of the round's own.
+    into buffers of the round's own (they may be strided then). Layers may differ
+    in their heads and types.
     Inputs and outputs stay in these static buffers, so the round can be
     captured once as a CUDA graph (capture()) and replayed (replay()); run()
     launches it directly. Attention outputs: self.outs[layer]; sampling:
@@ -1330,7 +1331,7 @@ class MultiLayerVerify:
         B, n_new, H_q, d = q0.shape
         H_kv = layers[0]["k_new"].shape[2]
         dev = q0.device
-        self.outs = [torch.empty_like(l["q"]) for l in layers]
+        self.outs = [torch.empty(l["q"].shape, dtype=l["q"].dtype, device=dev) for l in layers]
         shape = (B, n_new, H_q, H_kv, d, block_table.shape[1], block_size)
         need = 0
         for l in layers:
@@ -1338,10 +1339,25 @@ class MultiLayerVerify:
             need = max(need, attn_q8_workspace_size(*shape, *span) if _is_q8(l["k_cache"])
                        else attn_q4_workspace_size(*shape, *span) if _is_q4(l["k_cache"])
                        else attn_window_workspace_size(*shape, *span) if span[0] else attn_workspace_size(*shape))
-        # (layers run one after the other: one pair of buffers serves all that rotate)
-        self.turned = None
-        if any(l.get("rope") is not None for l in layers):
-            self.turned = torch.empty_like(q0), torch.empty_like(layers[0]["k_new"])
+        # (layers run one after the other: a pair of buffers serves all that rotate rows of its shape and type)
+        pairs = {}
+        self.turned = []
+        for i, l in enumerate(layers):
+            rope, q, k = l.get("rope"), l["q"], l["k_new"]
+            if rope is None:
+                self.turned.append(None)
+                continue
+            if not isinstance(rope, Rope):
+                raise TypeError("MultiLayerVerify: the rope of layer %d must be a Rope" % i)
+            if (q.dim() != 4 or k.dim() != 4 or q.shape[:2] != (B, n_new) or k.shape[:2] != (B, n_new) or
+                    q.shape[3] != k.shape[3] or q.dtype != k.dtype or rope.offset + rope.rotary_dim > q.shape[3]):
+                raise ValueError("MultiLayerVerify: layer %d rotates dims %d .. %d of q and k_new [%d, %d, heads, d] of one "
+                                 "dtype, got %s %s and %s %s" % (i, rope.offset, rope.offset + rope.rotary_dim - 1, B, n_new,
+                                                                 tuple(q.shape), q.dtype, tuple(k.shape), k.dtype))
+            key = tuple(q.shape), tuple(k.shape), q.dtype
+            if key not in pairs:
+                pairs[key] = tuple(torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (q, k))   # (packed, as the append takes them)
+            self.turned.append(pairs[key])
         self.attn_ws = alloc_workspace(need, dev)
         Bs, K1, V = target_logits.shape
         self.samp_ws = alloc_workspace(sample_workspace_size(Bs, K1 - 1, V), dev)
@@ -1351,11 +1367,11 @@ class MultiLayerVerify:
         self.graph = None
 
     def run(self):
-        for l, out in zip(self.layers, self.outs):
+        for l, out, turned in zip(self.layers, self.outs, self.turned):
             q, k_new = l["q"], l["k_new"]
             if l.get("rope") is not None:
-                q, k_new = spec_rope(q, k_new, l["rope"], seq_lens=self.seq_lens, q_out=self.turned[0],
-                                     k_out=self.turned[1], status=self.status)
+                q, k_new = spec_rope(q, k_new, l["rope"], seq_lens=self.seq_lens, q_out=turned[0], k_out=turned[1],
+                                     status=self.status)
             _append_any(k_new, l["v_new"], l["k_cache"], l["v_cache"], self.block_table, self.seq_lens,
                         l.get("k_scale"), l.get("v_scale"), self.block_size, self.status)
             _attn_any(q, l["k_cache"], l["v_cache"], self.block_table, self.seq_lens, None, l.get("k_scale"),
