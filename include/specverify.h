@@ -530,9 +530,11 @@ sv_status spec_verify_attn_q8(const void *q, sv_dtype q_dtype, const void *k_cac
  *   The rows of each tensor are packed [B][n_new][heads][d], or lie at the
  *   strides (elements, not negative) of its sv_rope_rows, e.g. heads of a
  *   packed projection; rows that are written must not overlap
- *   (SV_ERR_INVALID_ARG). The angle is exact to 2^-31 turns at every 32-bit
- *   position. rope is read before the call returns (a captured call keeps
- *   it). rotary_dim <= SV_ROPE_MAX_DIM.
+ *   (SV_ERR_INVALID_ARG). The angle, taken modulo a turn, is right to 2^-25.9
+ *   turns (its rounding to f32) at every 32-bit position for frequencies up
+ *   to 2^40 radians a position; larger ones lose bits at far positions. rope
+ *   is read before the call returns (a captured call keeps it). rotary_dim <=
+ *   SV_ROPE_MAX_DIM.
  * ------------------------------------------------------------------------ */
 #define SV_ROPE_MAX_DIM 256
 

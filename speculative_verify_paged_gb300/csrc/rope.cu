@@ -5,8 +5,11 @@
 //   (a, b) -> m (a cos - b sin, b cos + a sin).
 // The angle is taken in turns: w_i / (2 pi) as a 64-bit fixed-point fraction,
 // times p modulo 2^64, is the fraction of a turn to 2^-33 at any 32-bit
-// position, from one integer product; its upper 32 bits go to sincospif. (In
-// f32 the angle of position 131071 is off by up to 2^-8 for w_0 = 1.)
+// position, from one integer product; its upper 32 bits, as half turns in f32
+// (rounded to 2^-26 turns), go to sincospif. The fraction needs more than a
+// double holds (2^-56 of a turn a position would be 2^-25 at position 2^31): it
+// is made from w_i / (2 pi) in two doubles. (In f32 the angle of position 131071
+// is off by up to 2^-8 for w_0 = 1.)
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -18,6 +21,7 @@ namespace sv {
 namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr double kTurn = 0.15915494309189535, kTurnLow = -9.839338337591243e-18;   // 1 / (2 pi) to 2^-110
 
 struct RopeArgs {
   const void *src[2];      // queries, keys
@@ -208,6 +212,20 @@ sv_status launch_rope(RopeArgs &a, int B, bool inter, bool vec, cudaStream_t s) 
   return check_launch("spec_rope launch");
 }
 
+// The fraction of w / (2 pi) as a 64-bit one, to half a step of it for |w| up to 2^40.
+unsigned long long turns_of(double w) {
+  const double x = std::fabs(w), hi = x * kTurn;
+  double low = std::fma(x, kTurn, -hi) + x * kTurnLow;   // hi + low = |w| / (2 pi)
+  low -= std::rint(low);
+  double whole;
+  const double f = std::modf(hi, &whole) * 0x1p64;   // (modf: a difference with the product could be contracted)
+  const unsigned long long steps = (unsigned long long)f;
+  low = low * 0x1p64 + (f - (double)steps);
+  const unsigned long long more = (unsigned long long)std::rint(std::fabs(low));   // at most 2^63
+  const unsigned long long t = low < 0 ? steps - more : steps + more;
+  return w < 0 ? 0 - t : t;
+}
+
 bool rope_ok(const sv_rope *r) { return r && r->rotary_dim >= 2 && r->rotary_dim % 2 == 0 && r->rotary_dim <= SV_ROPE_MAX_DIM; }
 
 }  // namespace
@@ -330,10 +348,8 @@ extern "C" sv_status spec_rope(const void *q, void *q_out, const void *k, void *
   a.positions = positions; a.seq_lens = seq_lens; a.n_new = n_new;
   a.d = d; a.r = rope->rotary_dim; a.offset = rope->offset; a.m = rope->scale; a.status = dev_status;
   for (int i = 0; i < a.r / 2; ++i) {
-    double f = rope->inv_freq[i] / kTwoPi;   // turns a position
-    if (!std::isfinite(f)) return fail(SV_ERR_INVALID_ARG, "spec_rope: inv_freq[%d] is not finite", i);
-    f = (f - std::floor(f)) * 0x1p64;
-    a.turns[i] = f < 0x1p64 ? (unsigned long long)f : 0;
+    if (!std::isfinite(rope->inv_freq[i])) return fail(SV_ERR_INVALID_ARG, "spec_rope: inv_freq[%d] is not finite", i);
+    a.turns[i] = turns_of(rope->inv_freq[i]);
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == SV_F32) return launch_rope<float>(a, B, inter, vec, s);
