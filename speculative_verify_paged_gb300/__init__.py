@@ -1328,13 +1328,12 @@ class MultiLayerVerify:
         self.draft_tokens, self.uniforms = draft_tokens, uniforms
         self.draft_is_probs, self.temperature, self.block_size = draft_is_probs, temperature, block_size
         q0 = layers[0]["q"]
-        B, n_new, H_q, d = q0.shape
-        H_kv = layers[0]["k_new"].shape[2]
+        B, n_new = q0.shape[:2]
         dev = q0.device
         self.outs = [torch.empty(l["q"].shape, dtype=l["q"].dtype, device=dev) for l in layers]
-        shape = (B, n_new, H_q, H_kv, d, block_table.shape[1], block_size)
         need = 0
         for l in layers:
+            shape = (B, n_new, l["q"].shape[2], l["k_new"].shape[2], l["q"].shape[3], block_table.shape[1], block_size)
             span = (l.get("window", 0), l.get("sinks", 0))
             need = max(need, attn_q8_workspace_size(*shape, *span) if _is_q8(l["k_cache"])
                        else attn_q4_workspace_size(*shape, *span) if _is_q4(l["k_cache"])
