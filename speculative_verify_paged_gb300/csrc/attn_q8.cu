@@ -27,7 +27,7 @@
 // the key's thread as a row of its columns.
 //
 // What bounds it. Up to 16 query rows a kv head, memory: 64 sequences of 8192 keys,
-// 1.07 GB, 174 us with 4 to 16 rows. Above, the chain of a softmax step (scores from
+// 1.07 GB, 174 to 177 us with 4 to 16 rows. Above, the chain of a softmax step (scores from
 // tensor memory, the vote on the references, powers, terms, their way to shared
 // memory), which W warpgroups take side by side: at 64 sequences of 4750 keys and 40
 // rows a tile costs 1710 cycles, 1290 of them what its bytes take; the schedulers
@@ -36,9 +36,10 @@
 // moved in registers instead of from tensor memory 319 -> 177 us; the terms as columns
 // of one wide product, the scales by a warp of their own 161; eight rows a warpgroup
 // 153; edge flags with the scales and little else carried along 144; five warpgroups
-// with 80 registers instead of six with 72 134; fixed addresses of the terms 132. Some
-// 15 us of it, and all of a short single call's 17, are the three launches and the way
-// from a page's number to its first score.
+// with 80 registers instead of six with 72 134; fixed addresses of the terms 132; and
+// the terms rounded instead of cut off cost 2. Some 15 us of it, and all of a short
+// single call's 17, are the three launches and the way from a page's number to its
+// first score.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -838,9 +839,9 @@ sv_status launch_q8(const KlParams &P, const Q8Maps &M, int C, cudaStream_t st) 
 
 // Softmax warpgroups: 8 rows each as far as threads go, then 16. A step is a chain
 // of waits that more warpgroups with shorter columns overlap better, as long as the
-// registers suffice. 64 sequences of 4750 keys, 8 kv heads: 32 rows, four of 8 116 us,
-// two of 16 126; 40 rows, five of 8 121, six 130, three of 16 148; 48 rows, six of 8
-// 132, four of 16 160.
+// registers suffice. 64 sequences of 4750 keys, 8 kv heads, captured: 32 rows, four of
+// 8 120 us, two of 16 128; 40 rows, five of 8 132, six 143; 48 rows, six of 8 142, four
+// of 16 168.
 int q8_groups(int rows) { return rows <= 16 ? 2 : rows <= 32 ? 4 : rows <= 40 ? 5 : rows <= 48 ? 6 : 4; }
 
 // Query rows of a kv head on the tensor cores: 64 share a pass over the cache.
